@@ -545,6 +545,184 @@ rlscan_status rlscan_linear_scan(const float *alpha, const float *beta, const fl
                                  int64_t row_stride, float *out, void *ws, size_t ws_bytes,
                                  rlscan_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The state-space layer.
+ *
+ * The same first-order recurrence, with coefficients a model computes from
+ * its tokens: h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t for every channel and
+ * state (the selective scan), the short causal convolution in front of it
+ * and the root-mean-square norm in front of the layer, each over prompts
+ * (`rlscan_x`), in training (`rlscan_x_backward`) and, scan and convolution,
+ * for single tokens (`rlscan_x_step`).
+ *
+ * Conventions of these entry points
+ *  - Arrays over tokens are token-major, [N, T, width] with element stride 1
+ *    and strides of their own in elements (rlscan_array3; a stride of 0
+ *    repeats a row or a token), so that a slice of a projection's output is
+ *    taken as it is.  Any alignment is accepted; arrays whose address and
+ *    strides are multiples of 16 bytes take wide copies, with the same
+ *    results.  Outputs are dense.  Offsets are 64-bit.
+ *  - `dtype` (RLSCAN_F32 or RLSCAN_BF16) is the type of every activation and
+ *    of its gradient; parameters, recurrent states of the scan and their
+ *    gradients are float32, and so is the arithmetic: states, sums and norms
+ *    stay in 32 bits and an output is rounded once.
+ *  - resets [N,T] uint8, nullable: a non-zero flag at t says that a new
+ *    episode starts at t (RLSCAN_STARTS_AT): nothing from before t reaches
+ *    t or what follows it, whatever its value.
+ *  - lengths [N] int32, nullable: row n holds lengths[n] tokens (clamped to
+ *    0..T), the rest is padding, which is not read: outputs and gradients
+ *    there are 0 and the final state is the one after the last token.
+ *  - Results are the same bits on every call (no atomics).
+ *  - All memory is device (or page-locked host) memory, owned by the caller.
+ *    A workspace is scratch for one call: 16-byte aligned, it needs no
+ *    initialisation.  An output must not overlap an input.
+ * ------------------------------------------------------------------------- */
+
+/* [N, T, width] array (or [N, width]: token_stride unused), strides in elements. */
+typedef struct rlscan_array3 {
+    const void *data;
+    int64_t row_stride, token_stride;
+} rlscan_array3;
+
+/* What the forms of the selective scan share.
+ *   dt_t = softplus(delta_t + delta_bias)  (without softplus: delta_t + delta_bias)
+ *   h_t  = exp(dt_t A) h_{t-1} + dt_t x_t B_t            [N,D,S], h_{-1} = initial_state
+ *   y_t  = (sum_s C_t h_t + skip x_t) * z_t sigmoid(z_t)
+ * (Gu and Dao, "Mamba: Linear-Time Sequence Modeling with Selective State
+ * Spaces", 2023, Eq. 2a and Algorithm 2; the step of B is dt B.) */
+typedef struct rlscan_selective_scan_args {
+    int64_t N, T, D, S;           /* rows, tokens, channels, states (1..128) */
+    int64_t dtype;                /* RLSCAN_F32 or RLSCAN_BF16 */
+    int64_t delta_softplus;       /* 0 or 1 */
+    rlscan_array3 x, delta;       /* [N,T,D] */
+    rlscan_array3 z;              /* [N,T,D], data nullable: no gate */
+    rlscan_array3 B, C;           /* [N,T,S] */
+    const float *A;               /* [D,S] */
+    const float *skip;            /* [D], nullable: 0 */
+    const float *delta_bias;      /* [D], nullable: 0 */
+    const float *initial_state;   /* [N,D,S], nullable: 0 */
+    const uint8_t *resets;        /* [N,T], nullable */
+    const int32_t *lengths;       /* [N], nullable */
+} rlscan_selective_scan_args;
+
+/* Tokens between two checkpoints: checkpoints [N, ceil(T / 16), D, S] hold
+ * the state before tokens 0, 16, 32, ... */
+#define RLSCAN_SELECTIVE_SCAN_CHECKPOINT 16
+
+/* Scratch of a forward call (0: none). */
+size_t rlscan_selective_scan_workspace_bytes(const rlscan_selective_scan_args *args);
+
+/* Forward.  Outputs: y [N,T,D]; final_state [N,D,S] nullable; checkpoints
+ * nullable (what the backward pass needs).
+ * Errors: RLSCAN_ERR_NULL, RLSCAN_ERR_SHAPE (a negative size),
+ * RLSCAN_ERR_ARG_VALUE (S outside 1..128, unknown dtype),
+ * RLSCAN_ERR_ARG_CONFLICT (an output that is an input),
+ * RLSCAN_ERR_WORKSPACE, RLSCAN_ERR_MEMORY, RLSCAN_ERR_CUDA. */
+rlscan_status rlscan_selective_scan(const rlscan_selective_scan_args *args, void *y, float *final_state,
+                                    float *checkpoints, void *ws, size_t ws_bytes, rlscan_stream_t stream);
+
+/* Gradients, with G_t = dL/dh_t = C_t g_t + exp(dt_{t+1} A) G_{t+1}, where g
+ * is the gradient of sum_s C h (no carry over a reset; past the last token
+ * grad_final_state):
+ *   dC = sum_d g h;  dB = sum_d G dt x;  dA = sum_{n,t} G exp(dt A) h_{t-1} dt
+ *   ddt = sum_s G exp(dt A) h_{t-1} A + x sum_s G B;  ddelta = ddt softplus'
+ *   dx = dt sum_s G B + g skip;  dz = dL/dy (y before the gate) silu'(z)
+ * Every gradient but x's is nullable (not computed); z needs args->z,
+ * skip needs args->skip, delta_bias needs args->delta_bias. */
+typedef struct rlscan_selective_scan_grads {
+    void *x, *delta;              /* [N,T,D] */
+    void *z;                      /* [N,T,D] */
+    void *B, *C;                  /* [N,T,S] */
+    float *A;                     /* [D,S] */
+    float *skip, *delta_bias;     /* [D] */
+    float *initial_state;         /* [N,D,S] */
+} rlscan_selective_scan_grads;
+
+size_t rlscan_selective_scan_backward_workspace_bytes(const rlscan_selective_scan_args *args);
+
+rlscan_status rlscan_selective_scan_backward(const rlscan_selective_scan_args *args,
+                                             const rlscan_array3 *grad_y, const float *grad_final_state,
+                                             const float *checkpoints, const rlscan_selective_scan_grads *grads,
+                                             void *ws, size_t ws_bytes, rlscan_stream_t stream);
+
+/* One token of each of N sequences (T = 1; the arrays' token strides,
+ * initial_state, resets and lengths are not used).  state [P,D,S] is updated
+ * in place: sequence n has slot slots[n] (slots NULL: slot n, P >= N).  A
+ * slot outside 0..P-1 (-1, say) marks an idle sequence: its y is 0 and no
+ * state changes.  The slots of one call are distinct. */
+rlscan_status rlscan_selective_scan_step(const rlscan_selective_scan_args *args, float *state, int64_t P,
+                                         const int32_t *slots, void *y, rlscan_stream_t stream);
+
+/* The causal convolution of each channel with its own K taps (1..8):
+ *   pre_t = bias + sum_k weight[k] x_{t-K+1+k},   y = silu(pre) or pre
+ * Tokens before the first are initial_state's [N,K-1,D] (oldest first, 0 when
+ * NULL); taps that lie before the token's episode count 0. */
+typedef struct rlscan_causal_conv_args {
+    int64_t N, T, D, K;
+    int64_t dtype;                /* RLSCAN_F32 or RLSCAN_BF16 */
+    int64_t silu;                 /* 0 or 1 */
+    rlscan_array3 x;              /* [N,T,D] */
+    const float *weight;          /* [D,K] */
+    const float *bias;            /* [D], nullable: 0 */
+    const void *initial_state;    /* [N,K-1,D], nullable: 0 */
+    const uint8_t *resets;        /* [N,T], nullable */
+    const int32_t *lengths;       /* [N], nullable */
+} rlscan_causal_conv_args;
+
+/* Forward.  Outputs: y [N,T,D]; final_state [N,K-1,D] nullable: the last K-1
+ * inputs of the row (0 where they lie before its last episode). */
+rlscan_status rlscan_causal_conv(const rlscan_causal_conv_args *args, void *y, void *final_state,
+                                 rlscan_stream_t stream);
+
+/* Gradients with g = dL/dy silu'(pre): dx_t = sum_j weight[K-1-j] g_{t+j}
+ * within the episode, dweight[k] = sum g_t x_{t-K+1+k}, dbias = sum g.
+ * grad_final_state [N,K-1,D], grad_weight [D,K], grad_bias [D] and
+ * grad_initial_state [N,K-1,D] are nullable. */
+size_t rlscan_causal_conv_backward_workspace_bytes(const rlscan_causal_conv_args *args);
+
+rlscan_status rlscan_causal_conv_backward(const rlscan_causal_conv_args *args, const rlscan_array3 *grad_y,
+                                          const void *grad_final_state, void *grad_x, float *grad_weight,
+                                          float *grad_bias, void *grad_initial_state, void *ws,
+                                          size_t ws_bytes, rlscan_stream_t stream);
+
+/* One token of each of N sequences: state [P,K-1,D] (slots as in
+ * rlscan_selective_scan_step) is shifted by one and takes the token. */
+rlscan_status rlscan_causal_conv_step(const rlscan_causal_conv_args *args, void *state, int64_t P,
+                                      const int32_t *slots, void *y, rlscan_stream_t stream);
+
+/* Root-mean-square norm with the residual's addition (Zhang and Sennrich,
+ * "Root Mean Square Layer Normalization", 2019):
+ *   h = x + residual,  y = h / sqrt(mean(h^2) + eps) * weight
+ * over rows of D elements.  Inputs: x [M,D] of `dtype`; residual [M,D]
+ * nullable, of residual_dtype (RLSCAN_F32 or `dtype`); row strides in
+ * elements.  Outputs: residual_out [M,D] of residual_dtype, h rounded
+ * (required with residual, unused without); y [M,D]: with scales NULL of
+ * `dtype`, else in 8 bits (e4m3) with scales [M, ceil(D/128)] float32, one
+ * for each 128 columns: scale = max(max|y|, 2^-100) / 448, stored y / scale
+ * to nearest even, saturated.  A block with a NaN or infinite y has a NaN
+ * scale.  y is made from h before h is rounded. */
+rlscan_status rlscan_add_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                                  const float *weight, int64_t M, int64_t D, float eps, rlscan_dtype dtype,
+                                  rlscan_dtype residual_dtype, void *y, float *scales, void *residual_out,
+                                  rlscan_stream_t stream);
+
+/* Gradients from the stored sum h (residual_out, or x where there was no
+ * residual), r = 1 / sqrt(mean(h^2) + eps), n = h r, gn = grad_y weight:
+ *   dh = r (gn - n mean(gn n)) + grad_residual      (x's and residual's)
+ *   dweight = sum over rows of grad_y n
+ * grad_residual is the gradient of residual_out (nullable, of h's type);
+ * grad_y and grad_x have `dtype`; grad_h [M,D] of h_dtype is written beside
+ * grad_x where it is given (the residual's gradient where its type differs);
+ * grad_weight [D] float32 nullable. */
+size_t rlscan_add_rms_norm_backward_workspace_bytes(int64_t M, int64_t D);
+
+rlscan_status rlscan_add_rms_norm_backward(const void *grad_y, int64_t grad_y_stride, const void *h,
+                                           int64_t h_stride, const void *grad_residual,
+                                           int64_t grad_residual_stride, const float *weight, int64_t M,
+                                           int64_t D, float eps, rlscan_dtype dtype, rlscan_dtype h_dtype,
+                                           void *grad_x, void *grad_h, float *grad_weight, void *ws,
+                                           size_t ws_bytes, rlscan_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

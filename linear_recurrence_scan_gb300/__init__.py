@@ -2,7 +2,8 @@
 
 The compute path is the CUDA library ``librlscan.so`` (hand-written sm_103a
 kernels behind the C ABI in ``include/rlscan.h``); ``api`` binds it for
-PyTorch tensors.  ``synthetic`` draws seeded rollout buffers.  Importing the
+PyTorch tensors, and ``state_space`` the state-space layer's operators.
+``synthetic`` draws seeded rollout buffers.  Importing the
 package does not load the library; the first estimator call does (and raises
 if it has not been built).
 """
@@ -15,6 +16,11 @@ _API = {
     "compute_discounted_returns", "compute_eligibility_traces", "compute_episodic_prefix_sum",
     "linear_scan", "workspace_status",
 }
+_STATE_SPACE = {
+    "selective_scan", "selective_scan_backward", "selective_scan_step", "SelectiveScanGrads",
+    "causal_conv", "causal_conv_backward", "causal_conv_step", "CausalConvGrads",
+    "add_rms_norm", "add_rms_norm_backward", "RmsNorm", "RmsNormGrads",
+}
 
 
 def __getattr__(name):
@@ -23,8 +29,13 @@ def __getattr__(name):
         value = getattr(api, name)
         globals()[name] = value  # later lookups skip this hook
         return value
+    if name in _STATE_SPACE:
+        from . import state_space
+        value = getattr(state_space, name)
+        globals()[name] = value
+        return value
     raise AttributeError(name)
 
 
 def __dir__():
-    return sorted(set(globals()) | _API)
+    return sorted(set(globals()) | _API | _STATE_SPACE)

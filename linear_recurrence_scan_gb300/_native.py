@@ -66,6 +66,19 @@ SIGNATURES = {
     "rlscan_eligibility_traces": ([_P] * 3 + [_I64] * 3 + [_F, _F, _P, _P, _SZ, _P], _I),
     "rlscan_episodic_prefix_sum": ([_P] * 3 + [_I] + [_I64] * 3 + [_P, _P, _SZ, _P], _I),
     "rlscan_linear_scan": ([_P] * 3 + [_I] + [_I64] * 3 + [_P, _P, _SZ, _P], _I),
+    # the state-space layer (argument structs are passed packed, as bytes)
+    "rlscan_selective_scan_workspace_bytes": ([_P], _SZ),
+    "rlscan_selective_scan": ([_P] * 5 + [_SZ, _P], _I),
+    "rlscan_selective_scan_backward_workspace_bytes": ([_P], _SZ),
+    "rlscan_selective_scan_backward": ([_P] * 6 + [_SZ, _P], _I),
+    "rlscan_selective_scan_step": ([_P, _P, _I64] + [_P] * 3, _I),
+    "rlscan_causal_conv": ([_P] * 4, _I),
+    "rlscan_causal_conv_backward_workspace_bytes": ([_P], _SZ),
+    "rlscan_causal_conv_backward": ([_P] * 8 + [_SZ, _P], _I),
+    "rlscan_causal_conv_step": ([_P, _P, _I64] + [_P] * 3, _I),
+    "rlscan_add_rms_norm": ([_P, _I64, _P, _I64, _P, _I64, _I64, _F, _I, _I] + [_P] * 4, _I),
+    "rlscan_add_rms_norm_backward_workspace_bytes": ([_I64, _I64], _SZ),
+    "rlscan_add_rms_norm_backward": ([_P, _I64] * 3 + [_P, _I64, _I64, _F, _I, _I] + [_P] * 4 + [_SZ, _P], _I),
 }
 
 _lib = None
