@@ -2,8 +2,12 @@
 //
 //   h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t,   y_t = (C_t h_t + skip x_t) silu(z_t)
 //
-// A lane holds four states of one channel in registers and walks the tokens
-// in order; the lanes of a channel add their parts of C h with shuffles.
+// Prompts.  A lane holds SPT states of one channel in registers and walks the
+// tokens in order; LANES lanes share a channel.  Tiles of 16 tokens come into
+// shared memory by asynchronous copies, two tiles ahead.  A tile's tokens are
+// shared out over a channel's lanes: each prepares its own (softplus, dt x,
+// the gate), hands dt and dt x to the others with shuffles, and gets its
+// tokens' sums over the states back.
 #include "sequence.cuh"
 
 namespace rlscan {
@@ -11,152 +15,544 @@ namespace seq {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kTile = kCheckpoint;
 
 struct ScanOut {
     void *y;
     float *final_state, *checkpoints;
+    // rows in `chunks` chunks of `chunk` tokens
+    int64_t chunk, chunks;
+    int unit;        // bytes of the copies into shared memory: 16, 4 or 0 (single values)
+    bool vec;        // states in whole 16-byte units
+    float *states;   // [N][chunks][D][S]: a chunk's own end state, then the state in front of it
+    float *spans;    // [N][chunks][D]: the chunk's sum of dt
+    uint8_t *cuts;   // [N][chunks]: an episode starts in the chunk
 };
+
+template <class T, int SPT, int LANES>
+struct Shape {
+    static constexpr int CH = kThreads / LANES;     // channels of a block
+    static constexpr int SP = SPT * LANES;          // states, padded
+    static constexpr int PER = kTile / LANES;       // tokens of a tile that a lane prepares: sl, sl + LANES, ...
+    // rows of the lanes that share a channel lie in different banks
+    static constexpr int ROWB = 32 / LANES * static_cast<int>(sizeof(T));
+    static constexpr int PITCH = CH * static_cast<int>(sizeof(T)) + (ROWB > 16 ? ROWB : 16);
+    static constexpr int BW = SP * sizeof(T) < 16 ? 16 / static_cast<int>(sizeof(T)) : SP;  // whole 16-byte units
+    static constexpr int BPITCH = BW * static_cast<int>(sizeof(T));
+    static constexpr int ACT = kTile * PITCH, BC = kTile * BPITCH;
+    static constexpr int STAGE = 3 * ACT + 2 * BC;
+    static constexpr int STAGES = 3;
+    static constexpr bool CONVERT = sizeof(T) == 2;
+    static constexpr int WIDE = CONVERT ? 2 * kTile * SP * 4 : 0;  // B and C in float32
+    static constexpr size_t SMEM = STAGES * STAGE + 2 * WIDE;
+    static constexpr int BLOCKS = SPT == 16 ? 2 : 3;  // registers for 16 tokens' work at once
+    static_assert(ACT % 16 == 0 && BC % 16 == 0);
+};
+
+// Sums over a channel's LANES lanes of v[0..LANES): lane l gets that of v[l].
+template <int LANES>
+__device__ __forceinline__ float scatter_sum(float *v, int sl)
+{
+    if constexpr (LANES == 1) {
+        return v[0];
+    } else {
+        constexpr int HALF = LANES / 2;
+        const bool upper = (sl & HALF) != 0;
+#pragma unroll
+        for (int i = 0; i < HALF; ++i) {
+            const float give = upper ? v[i] : v[i + HALF];
+            const float keep = upper ? v[i + HALF] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, HALF);
+        }
+        return scatter_sum<HALF>(v, sl);
+    }
+}
+
+template <class T, int SPT>
+__device__ __forceinline__ void load_states(f2 *h, const float *p, int s0, int S, bool on)
+{
+#pragma unroll
+    for (int i = 0; i < SPT / 2; ++i) {
+        const int s = s0 + 2 * i;
+        h[i] = pair(on && s < S ? p[s] : 0.f, on && s + 1 < S ? p[s + 1] : 0.f);
+    }
+}
+
+template <int SPT>
+__device__ __forceinline__ void store_states(float *p, const f2 *h, int s0, int S, bool vec)
+{
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < SPT / 4; ++i) {
+            const float2 a = halves(h[2 * i]), b = halves(h[2 * i + 1]);
+            if (s0 + 4 * i < S) *reinterpret_cast<float4 *>(p + s0 + 4 * i) = make_float4(a.x, a.y, b.x, b.y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < SPT / 2; ++i) {
+            const float2 a = halves(h[i]);
+            if (s0 + 2 * i < S) p[s0 + 2 * i] = a.x;
+            if (s0 + 2 * i + 1 < S) p[s0 + 2 * i + 1] = a.y;
+        }
+    }
+}
+
+// FULL: outputs; otherwise only a chunk's end state and sum of dt, from 0.
+template <class T, int SPT, int LANES, bool FULL>
+__global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
+    scan_kernel(const __grid_constant__ rlscan_selective_scan_args a, const __grid_constant__ ScanOut o)
+{
+    using P = Shape<T, SPT, LANES>;
+    extern __shared__ __align__(16) char smem[];
+    float *wide = reinterpret_cast<float *>(smem + P::STAGES * P::STAGE);
+    ptx::pdl_trigger_dependents();
+    ptx::pdl_wait_prerequisites();
+    const int lane = threadIdx.x & 31, sl = lane % LANES, ch = threadIdx.x / LANES;
+    const int64_t blocks = (a.D + P::CH - 1) / P::CH;
+    const int64_t c0 = blockIdx.x % blocks * P::CH, chunk = blockIdx.x / blocks % o.chunks,
+                  n = blockIdx.x / blocks / o.chunks;
+    const int64_t d = c0 + ch;
+    const bool live = d < a.D;
+    const int64_t dd = live ? d : a.D - 1;
+    const int s0 = SPT * sl, S = static_cast<int>(a.S);
+    const int width = static_cast<int>(a.D - c0 < P::CH ? a.D - c0 : P::CH);
+    const bool gated = FULL && a.z.data != nullptr;
+    const uint32_t gate = gated ? ~0u : 0u, soft = a.delta_softplus ? ~0u : 0u;
+    const int64_t first = chunk * o.chunk, last = first + o.chunk < a.T ? first + o.chunk : a.T;
+    const int64_t len = row_length(a.lengths, n, a.T);
+    const int64_t stop = len < last ? len : last;  // tokens first <= t < stop are scanned
+
+    const T *x = static_cast<const T *>(a.x.data) + n * a.x.row_stride + first * a.x.token_stride + c0;
+    const T *delta = static_cast<const T *>(a.delta.data) + n * a.delta.row_stride + first * a.delta.token_stride + c0;
+    const T *z = static_cast<const T *>(a.z.data) + n * a.z.row_stride + first * a.z.token_stride + c0;
+    const T *B = static_cast<const T *>(a.B.data) + n * a.B.row_stride + first * a.B.token_stride;
+    const T *C = static_cast<const T *>(a.C.data) + n * a.C.row_stride + first * a.C.token_stride;
+    const uint8_t *resets = a.resets != nullptr ? a.resets + n * a.T + first : nullptr;
+
+    auto copy_tile = [&](auto unit, int64_t tile) {
+        constexpr int CHUNK = decltype(unit)::value;
+        const int64_t t = tile * kTile, left = stop - first - t;
+        char *st = smem + tile % P::STAGES * P::STAGE;
+        const int rows = left < kTile ? static_cast<int>(left) : kTile;
+        load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kThreads>(st, x + t * a.x.token_stride, a.x.token_stride, rows, width);
+        load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kThreads>(st + P::ACT, delta + t * a.delta.token_stride,
+                                                              a.delta.token_stride, rows, width);
+        load_tile<T, kTile, P::BW, P::BPITCH, CHUNK, kThreads>(st + 3 * P::ACT, B + t * a.B.token_stride,
+                                                               a.B.token_stride, rows, S);
+        if (FULL) {
+            if (gated)
+                load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kThreads>(st + 2 * P::ACT, z + t * a.z.token_stride,
+                                                                      a.z.token_stride, rows, width);
+            load_tile<T, kTile, P::BW, P::BPITCH, CHUNK, kThreads>(st + 3 * P::ACT + P::BC, C + t * a.C.token_stride,
+                                                                   a.C.token_stride, rows, S);
+        }
+    };
+    auto issue = [&](int64_t tile) {
+        if (stop - first > tile * kTile) {
+            if (o.unit == 16)
+                copy_tile(std::integral_constant<int, 16>(), tile);
+            else if (o.unit == 4)
+                copy_tile(std::integral_constant<int, 4>(), tile);
+            else
+                copy_tile(std::integral_constant<int, 0>(), tile);
+        }
+        copies_commit();
+    };
+    issue(0);
+    issue(1);
+
+    f2 A2[SPT / 2], h[SPT / 2];
+    load_states<T, SPT>(A2, a.A + dd * S, s0, S, true);
+#pragma unroll
+    for (int i = 0; i < SPT / 2; ++i) A2[i] = mul2(A2[i], both(kLog2e));
+    if (FULL && o.chunks > 1)
+        load_states<T, SPT>(h, o.states + ((n * o.chunks + chunk) * a.D + dd) * S, s0, S, true);
+    else
+        load_states<T, SPT>(h, a.initial_state + (n * a.D + dd) * S, s0, S, FULL && a.initial_state != nullptr);
+    const float bias = a.delta_bias != nullptr ? a.delta_bias[dd] : 0.f;
+    const float skip = FULL && a.skip != nullptr ? a.skip[dd] : 0.f;
+    const int64_t marks = (a.T + kTile - 1) / kTile;
+    T *y = static_cast<T *>(o.y) + (n * a.T + first) * a.D + dd;
+    float *mark = o.checkpoints != nullptr ? o.checkpoints + ((n * marks + first / kTile) * a.D + dd) * S : nullptr;
+    float span = 0.f;
+    uint32_t cut = 0;
+
+    const int64_t count = stop - first, tiles = count > 0 ? (count + kTile - 1) / kTile : 0;
+    uint32_t flag = resets != nullptr && lane < kTile && lane < count ? resets[lane] : 0u;  // one tile ahead
+    for (int64_t tile = 0; tile < tiles; ++tile) {
+        const int64_t t0 = tile * kTile;
+        copies_wait<1>();
+        __syncthreads();  // the tile is here, and its predecessor's buffer is free
+        issue(tile + 2);
+        const char *st = smem + tile % P::STAGES * P::STAGE;
+        const float *Bw, *Cw;
+        if constexpr (P::CONVERT) {
+            float *w = wide + (tile & 1) * (2 * kTile * P::SP);
+            constexpr int QUADS = kTile * P::SP / 4;
+#pragma unroll
+            for (int i = threadIdx.x; i < (FULL ? 2 : 1) * QUADS; i += kThreads) {
+                const int k = i / QUADS, r = i / (P::SP / 4) % kTile, c = i % (P::SP / 4);
+                const uint2 v = *reinterpret_cast<const uint2 *>(st + 3 * P::ACT + k * P::BC + r * P::BPITCH + c * 8);
+                *reinterpret_cast<float4 *>(w + 4 * i) =
+                    make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                                __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+            }
+            __syncthreads();
+            Bw = w + s0;
+            Cw = w + kTile * P::SP + s0;
+        } else {
+            Bw = reinterpret_cast<const float *>(st + 3 * P::ACT) + s0;
+            Cw = Bw + P::BC / 4;
+        }
+        const uint32_t starts = resets != nullptr ? __ballot_sync(0xffffffffu, flag != 0) : 0u;
+        if (resets != nullptr) flag = lane < kTile && t0 + kTile + lane < count ? resets[t0 + kTile + lane] : 0u;
+        cut |= starts;
+        if (FULL && mark != nullptr && live) store_states<SPT>(mark + tile * a.D * S, h, s0, S, o.vec);
+        const int left = count - t0 < kTile ? static_cast<int>(count - t0) : kTile;
+        const T *xs = reinterpret_cast<const T *>(st) + ch, *ds = reinterpret_cast<const T *>(st + P::ACT) + ch,
+                *zs = reinterpret_cast<const T *>(st + 2 * P::ACT) + ch;
+        constexpr int ROW = P::PITCH / static_cast<int>(sizeof(T));
+        constexpr int BROW = P::CONVERT ? P::SP : P::BPITCH / 4;
+        T *yt = y + t0 * a.D;
+        // FAST: 16 tokens of one episode, without a branch, so that the tokens' work overlaps
+        auto walk = [&](auto fast) {
+            constexpr bool FAST = decltype(fast)::value;
+            float xv[P::PER], dt[P::PER], dtx[P::PER], part[kTile];
+#pragma unroll
+            for (int p = 0; p < P::PER; ++p) {
+                xv[p] = to_f(xs[(p * LANES + sl) * ROW]);
+                dt[p] = to_f(ds[(p * LANES + sl) * ROW]) + bias;
+            }
+            if constexpr (P::PER == 1) {
+                dt[0] = choose(soft, softplus(dt[0]), dt[0]);
+            } else {
+#pragma unroll
+                for (int p = 0; p < P::PER; p += 2) {
+                    const float2 v = halves(softplus(pair(dt[p], dt[p + 1])));
+                    dt[p] = choose(soft, v.x, dt[p]);
+                    dt[p + 1] = choose(soft, v.y, dt[p + 1]);
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < P::PER; ++p) {
+                if (!FAST) dt[p] = p * LANES + sl < left ? dt[p] : 0.f;  // past the last token the state stays
+                dtx[p] = dt[p] * xv[p];
+                if (!FULL) span += dt[p];
+            }
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) {
+                float dj = dt[k / LANES], xj = dtx[k / LANES];
+                if constexpr (LANES > 1) {
+                    dj = __shfl_sync(0xffffffffu, dj, k % LANES, LANES);
+                    xj = __shfl_sync(0xffffffffu, xj, k % LANES, LANES);
+                }
+                if (!FAST && (starts >> k & 1u) != 0) {
+#pragma unroll
+                    for (int i = 0; i < SPT / 2; ++i) h[i] = 0ull;
+                }
+                const f2 dp = both(dj), xp = both(xj);
+                f2 acc[2] = {0ull, 0ull};
+#pragma unroll
+                for (int i = 0; i < SPT / 4; ++i) {
+                    const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(Bw + k * BROW + 4 * i);
+                    h[2 * i] = fma2(exp2_fast(mul2(dp, A2[2 * i])), h[2 * i], mul2(xp, b.x));
+                    h[2 * i + 1] = fma2(exp2_fast(mul2(dp, A2[2 * i + 1])), h[2 * i + 1], mul2(xp, b.y));
+                    if (FULL) {
+                        const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(Cw + k * BROW + 4 * i);
+                        acc[0] = i == 0 ? mul2(c.x, h[0]) : fma2(c.x, h[2 * i], acc[0]);
+                        acc[1] = i == 0 ? mul2(c.y, h[1]) : fma2(c.y, h[2 * i + 1], acc[1]);
+                    }
+                }
+                if (FULL) {
+                    const float2 v = halves(add2(acc[0], acc[1]));
+                    part[k] = v.x + v.y;
+                }
+            }
+            if constexpr (FULL) {
+#pragma unroll
+                for (int p = 0; p < P::PER; ++p) {
+                    const int k = p * LANES + sl;
+                    float v = fmaf(skip, xv[p], scatter_sum<LANES>(part + p * LANES, sl));
+                    const float zv = to_f(zs[k * ROW]);
+                    v *= choose(gate, zv * sigmoid(zv), 1.f);
+                    if (FAST) {
+                        if (live) yt[k * a.D] = from_f<T>(v);
+                    } else if (live && t0 + k < last - first) {
+                        yt[k * a.D] = from_f<T>(k < left ? v : 0.f);
+                    }
+                }
+            }
+        };
+        if (starts == 0 && left == kTile)
+            walk(std::true_type());
+        else
+            walk(std::false_type());
+    }
+    if (!FULL) {
+        if constexpr (LANES > 1) {
+#pragma unroll
+            for (int m = LANES / 2; m > 0; m /= 2) span += __shfl_xor_sync(0xffffffffu, span, m);
+        }
+        if (live) {
+            const int64_t at = (n * o.chunks + chunk) * a.D + d;
+            store_states<SPT>(o.states + at * S, h, s0, S, o.vec);
+            if (sl == 0) o.spans[at] = span;
+        }
+        if (c0 == 0 && threadIdx.x == 0) o.cuts[n * o.chunks + chunk] = cut != 0;
+        return;
+    }
+    if (!live) return;
+    // padding behind the last tile; checkpoints there hold the final state
+    for (int64_t t = tiles * kTile + sl; t < last - first; t += LANES) y[t * a.D] = from_f<T>(0.f);
+    if (mark != nullptr)
+        for (int64_t m = tiles; m * kTile < last - first; ++m) store_states<SPT>(mark + m * a.D * S, h, s0, S, o.vec);
+    // the chunk with the row's last token (the first chunk of an empty row)
+    if (o.final_state != nullptr && (len > first ? len <= last : len == 0 && chunk == 0))
+        store_states<SPT>(o.final_state + (n * a.D + d) * S, h, s0, S, o.vec);
+}
+
+// The state in front of each chunk: carry = exp(A span) carry + the chunk's
+// own end state, or that alone where an episode starts in the chunk.
+__global__ void __launch_bounds__(256)
+    chunk_kernel(const __grid_constant__ rlscan_selective_scan_args a, const __grid_constant__ ScanOut o)
+{
+    ptx::pdl_trigger_dependents();
+    ptx::pdl_wait_prerequisites();
+    const int64_t i = blockIdx.x * 256ll + threadIdx.x, DS = a.D * a.S;
+    if (i >= a.N * DS) return;
+    const int64_t n = i / DS, e = i % DS, d = e / a.S;
+    const float A2 = a.A[e] * kLog2e;
+    float carry = a.initial_state != nullptr ? a.initial_state[i] : 0.f;
+    float *st = o.states + n * o.chunks * DS + e;
+    const float *sp = o.spans + n * o.chunks * a.D + d;
+#pragma unroll 4
+    for (int64_t c = 0; c < o.chunks; ++c) {
+        const float own = st[c * DS], span = sp[c * a.D];
+        const bool cut = o.cuts[n * o.chunks + c] != 0;
+        st[c * DS] = carry;
+        carry = cut ? own : fmaf(exp2_fast(A2 * span), carry, own);
+    }
+}
+
+template <class T, int SPT, int LANES>
+rlscan_status launch_shape(const rlscan_selective_scan_args &a, const ScanOut &o, cudaStream_t s)
+{
+    using P = Shape<T, SPT, LANES>;
+    const int64_t grid = a.N * ceil_div(a.D, P::CH) * o.chunks;
+    auto full = scan_kernel<T, SPT, LANES, true>;
+    auto part = scan_kernel<T, SPT, LANES, false>;
+    static const bool sized =
+        cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess &&
+        cudaFuncSetAttribute(part, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
+    if (!sized) return RLSCAN_ERR_CUDA;
+    if (o.chunks > 1) {
+        rlscan_status st = launch_overlapped(part, grid, kThreads, P::SMEM, s, a, o);
+        if (st == RLSCAN_OK) st = launch_overlapped(chunk_kernel, ceil_div(a.N * a.D * a.S, 256), 256, 0, s, a, o);
+        if (st != RLSCAN_OK) return st;
+    }
+    return launch_overlapped(full, grid, kThreads, P::SMEM, s, a, o);
+}
+
+// How a call is laid out: states per lane, and chunks of each row.
+struct Plan {
+    int spt, lanes;
+    int64_t chunk, chunks;
+};
+
+// Sixteen states a lane need the fewest instructions a state, eight give
+// twice the warps; chunks give as many warps as a row has tokens for, but
+// compute every state twice.  Measured (D 2048, S 16, bf16, microseconds):
+//   one row    T 512: 60 unsplit (8 states), 34 in chunks of 64;
+//              T 2048: 213, 68 (128);  T 8192: 829, 185 (16 states, 512)
+//   four rows  T 512: 60, 65;  T 2048: 214, 175 (16, 128);  T 8192: 830, 563 (16, 512)
+//   eight rows T 2048: 267 (8) and 279 (16), 301 (16, 256);  T 8192: 1037 (8), 1081 (16, 512)
+// so rows are split while the unsplit call has less than 1.5 blocks an SM.
+Plan plan(const rlscan_selective_scan_args &a)
+{
+    const int64_t sms = sm_count() > 0 ? sm_count() : 152;
+    auto lanes_of = [&](int spt) {
+        int lanes = 1;
+        while (spt * lanes < a.S) lanes *= 2;
+        return lanes;
+    };
+    auto blocks_of = [&](int spt) { return a.N * ceil_div(a.D * lanes_of(spt), kThreads); };
+    Plan p;
+    const int64_t narrow = blocks_of(8);
+    const bool split = a.T > 256 && 2 * narrow < 3 * sms && !(4 * narrow >= 3 * sms && a.T <= 1024);
+    p.spt = a.S > 8 && (split ? a.T >= 1024 : narrow >= 3 * sms) ? 16 : 8;
+    p.chunk = ceil_div(a.T > 0 ? a.T : 1, kTile) * kTile;
+    if (split) {
+        p.chunk = a.T < 1024 ? 64 : 256;
+        while (p.chunk > 64 && blocks_of(p.spt) * ceil_div(a.T, p.chunk) < sms) p.chunk /= 2;
+    }
+    p.lanes = lanes_of(p.spt);
+    p.chunks = ceil_div(a.T > 0 ? a.T : 1, p.chunk);
+    return p;
+}
+
+template <class T, int SPT>
+rlscan_status by_lanes(int lanes, const rlscan_selective_scan_args &a, const ScanOut &o, cudaStream_t s)
+{
+    switch (lanes) {
+    case 1: return launch_shape<T, SPT, 1>(a, o, s);
+    case 2: return launch_shape<T, SPT, 2>(a, o, s);
+    case 4: return launch_shape<T, SPT, 4>(a, o, s);
+    case 8: return launch_shape<T, SPT, 8>(a, o, s);
+    default: return launch_shape<T, SPT, 16>(a, o, s);
+    }
+}
+
+template <class T>
+rlscan_status launch_typed(const Plan &p, const rlscan_selective_scan_args &a, ScanOut o, cudaStream_t s)
+{
+    Chunk c;
+    for (const rlscan_array3 *v : {&a.x, &a.delta, &a.B, &a.C}) c.add(v->data, v->row_stride, v->token_stride, sizeof(T));
+    if (a.z.data != nullptr) c.add(a.z.data, a.z.row_stride, a.z.token_stride, sizeof(T));
+    o.unit = c.size();
+    o.vec = a.S % 4 == 0 &&
+            ((reinterpret_cast<uintptr_t>(o.final_state) | reinterpret_cast<uintptr_t>(o.checkpoints)) & 15u) == 0;
+    if (p.spt == 16) return by_lanes<T, 16>(p.lanes, a, o, s);
+    return by_lanes<T, 8>(p.lanes, a, o, s);
+}
+
+// One token: a lane has four states of one channel, of kStepRows sequences
+// in turn, whose loads are in flight together and share its row of A.
+constexpr int kStepRows = 2;
 
 template <class T, int LANES>
 __global__ void __launch_bounds__(kThreads)
-    scan_kernel(const __grid_constant__ rlscan_selective_scan_args a, const __grid_constant__ ScanOut o)
+    step_kernel(const __grid_constant__ rlscan_selective_scan_args a, float *state, int64_t P, const int32_t *slots, T *y,
+                bool vec)
 {
-    constexpr int CH = 32 / LANES;  // channels of a warp
-    const int lane = threadIdx.x & 31, sl = lane % LANES;
-    const int64_t blocks = (a.D + CH - 1) / CH;
-    const int64_t warp = blockIdx.x * static_cast<int64_t>(kThreads / 32) + threadIdx.x / 32;
-    if (warp >= a.N * blocks) return;
-    const int64_t n = warp / blocks, d = (warp % blocks) * CH + lane / LANES;
+    constexpr int CH = kThreads / LANES;
+    ptx::pdl_trigger_dependents();
+    ptx::pdl_wait_prerequisites();
+    const int sl = threadIdx.x % LANES, s0 = 4 * sl, S = static_cast<int>(a.S);
+    const int64_t blocks = (a.D + CH - 1) / CH, d = blockIdx.x % blocks * CH + threadIdx.x / LANES;
+    const int64_t n0 = blockIdx.x / blocks * kStepRows;
     const bool live = d < a.D;
     const int64_t dd = live ? d : a.D - 1;
-    const int s0 = 4 * sl, S = static_cast<int>(a.S);
-    float A2[4], h[4];
+    const bool mine = live && s0 < S;
+    float4 h[kStepRows], B[kStepRows], C[kStepRows];
+    float xv[kStepRows], dt[kStepRows], zv[kStepRows];
+    int64_t at[kStepRows];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        A2[i] = s0 + i < S ? a.A[dd * S + s0 + i] * kLog2e : 0.f;
-        h[i] = s0 + i < S && a.initial_state != nullptr ? a.initial_state[(n * a.D + dd) * S + s0 + i] : 0.f;
+    for (int r = 0; r < kStepRows; ++r) {
+        const int64_t n = n0 + r;
+        const int64_t slot = n < a.N ? (slots != nullptr ? slots[n] : n) : -1;
+        at[r] = slot >= 0 && slot < P ? (slot * a.D + dd) * S + s0 : -1;
     }
-    const float bias = a.delta_bias != nullptr ? a.delta_bias[dd] : 0.f;
-    const float skip = a.skip != nullptr ? a.skip[dd] : 0.f;
-    const T *x = static_cast<const T *>(a.x.data) + n * a.x.row_stride + dd;
-    const T *delta = static_cast<const T *>(a.delta.data) + n * a.delta.row_stride + dd;
-    const T *z = a.z.data != nullptr ? static_cast<const T *>(a.z.data) + n * a.z.row_stride + dd : nullptr;
-    const T *B = static_cast<const T *>(a.B.data) + n * a.B.row_stride;
-    const T *C = static_cast<const T *>(a.C.data) + n * a.C.row_stride;
-    T *y = static_cast<T *>(o.y) + n * a.T * a.D + dd;
-    const int64_t len = row_length(a.lengths, n, a.T);
-    const int64_t marks = (a.T + kCheckpoint - 1) / kCheckpoint;
-    for (int64_t t = 0; t < len; ++t) {
-        if (o.checkpoints != nullptr && t % kCheckpoint == 0 && live)
-            for (int i = 0; i < 4; ++i)
-                if (s0 + i < S) o.checkpoints[((n * marks + t / kCheckpoint) * a.D + d) * S + s0 + i] = h[i];
-        if (a.resets != nullptr && a.resets[n * a.T + t] != 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = 0.f;
+    auto four = [&](const auto *p, bool on, bool wide) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        using E = std::remove_cv_t<std::remove_reference_t<decltype(*p)>>;
+        if (wide && sizeof(E) == 4) {
+            if (on) v = *reinterpret_cast<const float4 *>(p);
+        } else {
+            if (on && s0 < S) v.x = to_f(p[0]);
+            if (on && s0 + 1 < S) v.y = to_f(p[1]);
+            if (on && s0 + 2 < S) v.z = to_f(p[2]);
+            if (on && s0 + 3 < S) v.w = to_f(p[3]);
         }
-        const float xv = to_f(x[t * a.x.token_stride]);
-        float dt = to_f(delta[t * a.delta.token_stride]) + bias;
-        if (a.delta_softplus) dt = softplus(dt);
-        const float dtx = dt * xv;
-        float acc = 0.f;
+        return v;
+    };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (s0 + i < S) {
-                h[i] = fmaf(exp2_fast(dt * A2[i]), h[i], dtx * to_f(B[t * a.B.token_stride + s0 + i]));
-                acc = fmaf(to_f(C[t * a.C.token_stride + s0 + i]), h[i], acc);
+    for (int r = 0; r < kStepRows; ++r) {
+        const int64_t n = n0 + r < a.N ? n0 + r : a.N - 1;
+        h[r] = four(state + (at[r] >= 0 ? at[r] : 0), mine && at[r] >= 0, vec);
+        B[r] = four(static_cast<const T *>(a.B.data) + n * a.B.row_stride + s0, true, false);
+        C[r] = four(static_cast<const T *>(a.C.data) + n * a.C.row_stride + s0, true, false);
+        xv[r] = to_f(static_cast<const T *>(a.x.data)[n * a.x.row_stride + dd]);
+        dt[r] = to_f(static_cast<const T *>(a.delta.data)[n * a.delta.row_stride + dd]);
+        zv[r] = a.z.data != nullptr ? to_f(static_cast<const T *>(a.z.data)[n * a.z.row_stride + dd]) : 0.f;
+    }
+    float4 A = four(a.A + dd * S + s0, true, vec && s0 < S);
+    A.x *= kLog2e;
+    A.y *= kLog2e;
+    A.z *= kLog2e;
+    A.w *= kLog2e;
+    const float bias = a.delta_bias != nullptr ? a.delta_bias[dd] : 0.f, skip = a.skip != nullptr ? a.skip[dd] : 0.f;
+#pragma unroll
+    for (int r = 0; r < kStepRows; ++r) {
+        float t = dt[r] + bias;
+        if (a.delta_softplus) t = softplus(t);
+        const float tx = t * xv[r];
+        h[r].x = fmaf(exp2_fast(t * A.x), h[r].x, tx * B[r].x);
+        h[r].y = fmaf(exp2_fast(t * A.y), h[r].y, tx * B[r].y);
+        h[r].z = fmaf(exp2_fast(t * A.z), h[r].z, tx * B[r].z);
+        h[r].w = fmaf(exp2_fast(t * A.w), h[r].w, tx * B[r].w);
+        float v = fmaf(C[r].x, h[r].x, C[r].y * h[r].y) + fmaf(C[r].z, h[r].z, C[r].w * h[r].w);
+#pragma unroll
+        for (int m = LANES / 2; m > 0; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
+        if (at[r] >= 0 && mine) {
+            float *p = state + at[r];
+            if (vec) {
+                *reinterpret_cast<float4 *>(p) = h[r];
+            } else {
+                p[0] = h[r].x;
+                if (s0 + 1 < S) p[1] = h[r].y;
+                if (s0 + 2 < S) p[2] = h[r].z;
+                if (s0 + 3 < S) p[3] = h[r].w;
             }
         }
-#pragma unroll
-        for (int m = LANES / 2; m > 0; m /= 2) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-        acc = fmaf(skip, xv, acc);
-        if (z != nullptr) {
-            const float zv = to_f(z[t * a.z.token_stride]);
-            acc *= zv * sigmoid(zv);
-        }
-        if (live && sl == 0) y[t * a.D] = from_f<T>(acc);
+        v = fmaf(skip, xv[r], v);
+        if (a.z.data != nullptr) v *= zv[r] * sigmoid(zv[r]);
+        if (live && sl == 0 && n0 + r < a.N) y[(n0 + r) * a.D + d] = from_f<T>(at[r] >= 0 ? v : 0.f);
     }
-    if (live && sl == 0)
-        for (int64_t t = len; t < a.T; ++t) y[t * a.D] = from_f<T>(0.f);
-    if (live)
-        for (int i = 0; i < 4; ++i) {
-            if (s0 + i >= S) break;
-            // checkpoints past the last token: the final state
-            if (o.checkpoints != nullptr)
-                for (int64_t m = (len + kCheckpoint - 1) / kCheckpoint; m < marks; ++m)
-                    o.checkpoints[((n * marks + m) * a.D + d) * S + s0 + i] = h[i];
-            if (o.final_state != nullptr) o.final_state[(n * a.D + d) * S + s0 + i] = h[i];
-        }
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads)
-    step_kernel(const __grid_constant__ rlscan_selective_scan_args a, float *state, int64_t P, const int32_t *slots, T *y)
+rlscan_status step_typed(const rlscan_selective_scan_args &a, float *state, int64_t P, const int32_t *slots, void *y,
+                         cudaStream_t s)
 {
-    const int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
-    if (i >= a.N * a.D) return;
-    const int64_t n = i / a.D, d = i % a.D, slot = slots != nullptr ? slots[n] : n;
-    if (slot < 0 || slot >= P) {
-        y[i] = from_f<T>(0.f);
-        return;
+    const bool vec =
+        a.S % 4 == 0 && ((reinterpret_cast<uintptr_t>(state) | reinterpret_cast<uintptr_t>(a.A)) & 15u) == 0;
+    auto go = [&](auto lanes) {
+        constexpr int LANES = decltype(lanes)::value;
+        return launch_overlapped(step_kernel<T, LANES>, ceil_div(a.N, kStepRows) * ceil_div(a.D, kThreads / LANES), kThreads, 0,
+                                 s, a, state, P, slots, static_cast<T *>(y), vec);
+    };
+    switch (state_lanes(a.S)) {
+    case 1: return go(std::integral_constant<int, 1>());
+    case 2: return go(std::integral_constant<int, 2>());
+    case 4: return go(std::integral_constant<int, 4>());
+    case 8: return go(std::integral_constant<int, 8>());
+    case 16: return go(std::integral_constant<int, 16>());
+    default: return go(std::integral_constant<int, 32>());
     }
-    const int S = static_cast<int>(a.S);
-    const float xv = to_f(static_cast<const T *>(a.x.data)[n * a.x.row_stride + d]);
-    float dt = to_f(static_cast<const T *>(a.delta.data)[n * a.delta.row_stride + d]);
-    if (a.delta_bias != nullptr) dt += a.delta_bias[d];
-    if (a.delta_softplus) dt = softplus(dt);
-    const T *B = static_cast<const T *>(a.B.data) + n * a.B.row_stride;
-    const T *C = static_cast<const T *>(a.C.data) + n * a.C.row_stride;
-    float *h = state + (slot * a.D + d) * S;
-    float acc = a.skip != nullptr ? a.skip[d] * xv : 0.f;
-    for (int s = 0; s < S; ++s) {
-        const float v = fmaf(exp2_fast(dt * (a.A[d * S + s] * kLog2e)), h[s], dt * xv * to_f(B[s]));
-        h[s] = v;
-        acc = fmaf(to_f(C[s]), v, acc);
-    }
-    if (a.z.data != nullptr) {
-        const float zv = to_f(static_cast<const T *>(a.z.data)[n * a.z.row_stride + d]);
-        acc *= zv * sigmoid(zv);
-    }
-    y[i] = from_f<T>(acc);
 }
 
-template <class T>
-rlscan_status launch_typed(const rlscan_selective_scan_args &a, const ScanOut &o, cudaStream_t s)
-{
-    const int lanes = state_lanes(a.S);
-    const int64_t warps = a.N * ceil_div(a.D, 32 / lanes);
-    const unsigned grid = static_cast<unsigned>(ceil_div(warps, kThreads / 32));
-    switch (lanes) {
-    case 1: scan_kernel<T, 1><<<grid, kThreads, 0, s>>>(a, o); break;
-    case 2: scan_kernel<T, 2><<<grid, kThreads, 0, s>>>(a, o); break;
-    case 4: scan_kernel<T, 4><<<grid, kThreads, 0, s>>>(a, o); break;
-    case 8: scan_kernel<T, 8><<<grid, kThreads, 0, s>>>(a, o); break;
-    case 16: scan_kernel<T, 16><<<grid, kThreads, 0, s>>>(a, o); break;
-    default: scan_kernel<T, 32><<<grid, kThreads, 0, s>>>(a, o); break;
-    }
-    return launched();
-}
+size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
-size_t selective_scan_workspace(const rlscan_selective_scan_args &) { return 0; }
+size_t selective_scan_workspace(const rlscan_selective_scan_args &a)
+{
+    const Plan p = plan(a);
+    if (p.chunks <= 1) return 0;
+    const size_t each = static_cast<size_t>(a.N) * p.chunks;
+    return up(each * a.D * a.S * 4) + up(each * a.D * 4) + up(each);
+}
 
 rlscan_status launch_selective_scan(const rlscan_selective_scan_args &a, void *y, float *final_state,
-                                    float *checkpoints, void *, cudaStream_t s)
+                                    float *checkpoints, void *ws, cudaStream_t s)
 {
-    const ScanOut o{y, final_state, checkpoints};
-    return a.dtype == RLSCAN_BF16 ? launch_typed<bf16>(a, o, s) : launch_typed<float>(a, o, s);
+    const Plan p = plan(a);
+    ScanOut o{y, final_state, checkpoints, p.chunk, p.chunks, 0, false, nullptr, nullptr, nullptr};
+    if (p.chunks > 1) {
+        const size_t each = static_cast<size_t>(a.N) * p.chunks;
+        char *w = static_cast<char *>(ws);
+        o.states = reinterpret_cast<float *>(w);
+        o.spans = reinterpret_cast<float *>(w + up(each * a.D * a.S * 4));
+        o.cuts = reinterpret_cast<uint8_t *>(w + up(each * a.D * a.S * 4) + up(each * a.D * 4));
+    }
+    return a.dtype == RLSCAN_BF16 ? launch_typed<bf16>(p, a, o, s) : launch_typed<float>(p, a, o, s);
 }
 
 rlscan_status launch_selective_scan_step(const rlscan_selective_scan_args &a, float *state, int64_t P,
                                          const int32_t *slots, void *y, cudaStream_t s)
 {
-    const unsigned grid = static_cast<unsigned>(ceil_div(a.N * a.D, kThreads));
-    if (a.dtype == RLSCAN_BF16)
-        step_kernel<bf16><<<grid, kThreads, 0, s>>>(a, state, P, slots, static_cast<bf16 *>(y));
-    else
-        step_kernel<float><<<grid, kThreads, 0, s>>>(a, state, P, slots, static_cast<float *>(y));
-    return launched();
+    return a.dtype == RLSCAN_BF16 ? step_typed<bf16>(a, state, P, slots, y, s)
+                                  : step_typed<float>(a, state, P, slots, y, s);
 }
 
 }  // namespace seq

@@ -1,18 +1,25 @@
 // k_selective_scan_backward.cu -- gradients of the selective scan.
 //
 // With g the gradient of sum_s C h and G_t = C_t g_t + exp(dt_{t+1} A) G_{t+1}
-// the gradient of h_t, segments of kCheckpoint tokens are taken from the last
-// to the first: the states are made again from the segment's checkpoint and
-// kept in registers, then G runs back over them.  exp(dt A) h_{t-1} is
-// h_t - dt x B, so that the previous state is not needed.
+// the gradient of h_t, tiles of 16 tokens are taken from the last to the
+// first.  exp(dt A) h_{t-1} is h_t - dt x B, so that the states alone are
+// needed: they are made again from the tile's checkpoint, 8 tokens at a time,
+// and stay in registers while G runs back over them.
+//
+// A lane holds four channels x four states, in pairs of channels: the sums
+// over channels (dB, dC) start in its registers, which leaves an eighth of
+// the shuffles that one channel a lane would need.  What each channel and
+// token needs once (softplus, the gate, the outputs) is shared out over the
+// lanes through shared memory.
 #include "sequence.cuh"
 
 namespace rlscan {
 namespace seq {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int L = kCheckpoint;
+constexpr int kTile = kCheckpoint;
+constexpr int kHalf = kTile / 2;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct GradArgs {
     rlscan_array3 grad_y;
@@ -20,173 +27,434 @@ struct GradArgs {
     void *x, *delta, *z;
     float *initial_state;
     float *part_B, *part_C;  // [channel blocks][N T S]
-    float *part_A;           // [N][D S]
-    float *part_d;           // [N][2][D]: skip, delta_bias
+    float *part_A;           // [N chunks][D S]
+    float *part_d;           // [N chunks][2][D]: skip, delta_bias
+    int unit;                // bytes of the copies into shared memory: 16, 4 or 0 (single values)
+    bool vec;                // checkpoints in whole 16-byte units
 };
 
 template <class T, int LANES>
-__global__ void __launch_bounds__(kThreads)
-    grad_kernel(const __grid_constant__ rlscan_selective_scan_args a, const __grid_constant__ GradArgs g)
-{
-    constexpr int CH = 32 / LANES;
-    const int lane = threadIdx.x & 31, sl = lane % LANES;
-    const int64_t blocks = (a.D + CH - 1) / CH;
-    const int64_t warp = blockIdx.x * static_cast<int64_t>(kThreads / 32) + threadIdx.x / 32;
-    if (warp >= a.N * blocks) return;
-    const int64_t n = warp / blocks, block = warp % blocks, d = block * CH + lane / LANES;
-    const bool live = d < a.D;
-    const int64_t dd = live ? d : a.D - 1;
-    const int s0 = 4 * sl, S = static_cast<int>(a.S);
-    const int64_t marks = (a.T + L - 1) / L;
-    float A1[4], G[4], dA[4] = {};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        A1[i] = s0 + i < S ? a.A[dd * S + s0 + i] : 0.f;
-        G[i] = live && s0 + i < S && g.grad_final != nullptr ? g.grad_final[(n * a.D + dd) * S + s0 + i] : 0.f;
-    }
-    const float bias = a.delta_bias != nullptr ? a.delta_bias[dd] : 0.f;
-    const float skip = a.skip != nullptr ? a.skip[dd] : 0.f;
-    const T *x = static_cast<const T *>(a.x.data) + n * a.x.row_stride + dd;
-    const T *delta = static_cast<const T *>(a.delta.data) + n * a.delta.row_stride + dd;
-    const T *z = a.z.data != nullptr ? static_cast<const T *>(a.z.data) + n * a.z.row_stride + dd : nullptr;
-    const T *gy = static_cast<const T *>(g.grad_y.data) + n * g.grad_y.row_stride + dd;
-    const T *B = static_cast<const T *>(a.B.data) + n * a.B.row_stride;
-    const T *C = static_cast<const T *>(a.C.data) + n * a.C.row_stride;
-    T *gx = static_cast<T *>(g.x), *gdelta = static_cast<T *>(g.delta), *gz = static_cast<T *>(g.z);
-    const int64_t len = row_length(a.lengths, n, a.T);
-    float dskip = 0.f, dbias = 0.f;
+struct Shape {
+    static constexpr int WARPS = LANES == 2 ? 2 : 4, THREADS = 32 * WARPS;
+    static constexpr int GROUPS = 32 / LANES;
+    static constexpr int CW = 4 * GROUPS, CH = WARPS * CW;  // channels of a warp, of a block
+    static constexpr int SP = 4 * LANES;                    // states, padded
+    static constexpr int CPL = CW > 32 ? CW / 32 : 1;       // channels a lane prepares
+    static constexpr int ITEMS = CW * kTile / 32;           // (channel, token) pairs a lane prepares
+    static constexpr int PITCH = CH * static_cast<int>(sizeof(T));
+    static constexpr int BPITCH = SP * static_cast<int>(sizeof(T));
+    static constexpr int ACT = kTile * PITCH, BC = kTile * BPITCH, MARK = THREADS * 64;
+    static constexpr int STAGE = 4 * ACT + 2 * BC + MARK, STAGES = 2;
+    static constexpr int F = kTile * CW;                    // floats of one array of a warp
+    static constexpr int WIDE = 2 * kTile * SP * 8;         // B and C, each value twice
+    static constexpr int RED = WARPS * kTile * 2 * SP * 4;
+    static constexpr size_t SMEM = STAGES * STAGE + WARPS * 4 * F * 4 + WIDE + RED;
+    static_assert(ACT % 16 == 0 && BC % 16 == 0 && BPITCH % 16 == 0 && PITCH % 16 == 0);
+};
 
-    for (int64_t t = a.T - 1; t >= len; --t) {
-        const int64_t e = (n * a.T + t) * a.D + dd;
-        if (live && sl == 0) {
-            gx[e] = from_f<T>(0.f);
-            if (gdelta != nullptr) gdelta[e] = from_f<T>(0.f);
-            if (gz != nullptr) gz[e] = from_f<T>(0.f);
+// Sums of v[0..N) over the lanes that differ in the bits HI .. LO of their
+// number, shared out: while values are left, each bit halves them (a lane
+// keeps one half), after that lanes hold the same sums.  Returns the index of
+// the first value kept.
+template <int N, int HI, int LO>
+__device__ __forceinline__ int scatter_sums(float *v, int lane)
+{
+    if constexpr (HI < LO || HI == 0) {
+        return 0;
+    } else if constexpr (N == 1) {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], HI);
+        return scatter_sums<1, HI / 2, LO>(v, lane);
+    } else {
+        constexpr int H = N / 2;
+        const bool upper = (lane & HI) != 0;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float give = upper ? v[i] : v[i + H], keep = upper ? v[i + H] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, HI);
         }
-        if (lane < LANES)
-            for (int i = 0; i < 4; ++i)
-                if (s0 + i < S) {
-                    const int64_t p = (block * a.N * a.T + n * a.T + t) * S + s0 + i;
-                    if (g.part_B != nullptr) g.part_B[p] = 0.f;
-                    if (g.part_C != nullptr) g.part_C[p] = 0.f;
-                }
-    }
-    for (int64_t m = (len + L - 1) / L - 1; m >= 0; --m) {
-        const int64_t t0 = m * L;
-        const int count = static_cast<int>(len - t0 < L ? len - t0 : L);
-        float h[L][4];
-        float start[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            start[i] = s0 + i < S ? g.checkpoints[((n * marks + m) * a.D + dd) * S + s0 + i] : 0.f;
-#pragma unroll
-        for (int k = 0; k < L; ++k) {
-            const int64_t t = t0 + k;
-            if (k < count) {
-                const bool reset = a.resets != nullptr && a.resets[n * a.T + t] != 0;
-                const float xv = to_f(x[t * a.x.token_stride]);
-                float dt = to_f(delta[t * a.delta.token_stride]) + bias;
-                if (a.delta_softplus) dt = softplus(dt);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float b = s0 + i < S ? to_f(B[t * a.B.token_stride + s0 + i]) : 0.f;
-                    const float before = reset ? 0.f : (k > 0 ? h[k > 0 ? k - 1 : 0][i] : start[i]);
-                    h[k][i] = fmaf(exp2_fast(dt * (A1[i] * kLog2e)), before, dt * xv * b);
-                }
-            }
-        }
-#pragma unroll
-        for (int k = L - 1; k >= 0; --k) {
-            const int64_t t = t0 + k;
-            if (k >= count) continue;
-            const bool reset = a.resets != nullptr && a.resets[n * a.T + t] != 0;
-            const float xv = to_f(x[t * a.x.token_stride]);
-            const float pre = to_f(delta[t * a.delta.token_stride]) + bias;
-            const float dt = a.delta_softplus ? softplus(pre) : pre;
-            const float dtx = dt * xv;
-            float gv = live ? to_f(gy[t * g.grad_y.token_stride]) : 0.f;
-            float zv = 0.f, sg = 0.f, out = gv;
-            if (z != nullptr) {
-                zv = to_f(z[t * a.z.token_stride]);
-                sg = sigmoid(zv);
-                gv = out * (zv * sg);
-            }
-            float u = 0.f, w = 0.f, yv = 0.f, gB[4], gC[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float b = s0 + i < S ? to_f(B[t * a.B.token_stride + s0 + i]) : 0.f;
-                const float c = s0 + i < S ? to_f(C[t * a.C.token_stride + s0 + i]) : 0.f;
-                G[i] = fmaf(c, gv, G[i]);
-                yv = fmaf(c, h[k][i], yv);
-                gC[i] = gv * h[k][i];
-                gB[i] = G[i] * dtx;
-                u = fmaf(G[i], b, u);
-                const float q = reset ? 0.f : G[i] * fmaf(-dtx, b, h[k][i]);
-                w = fmaf(q, A1[i], w);
-                dA[i] = fmaf(q, dt, dA[i]);
-                G[i] = reset ? 0.f : G[i] * exp2_fast(dt * (A1[i] * kLog2e));
-            }
-#pragma unroll
-            for (int s = LANES / 2; s > 0; s /= 2) {
-                u += __shfl_xor_sync(0xffffffffu, u, s);
-                w += __shfl_xor_sync(0xffffffffu, w, s);
-                yv += __shfl_xor_sync(0xffffffffu, yv, s);
-            }
-            // over the warp's channels
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                gB[i] = live ? gB[i] : 0.f;
-                gC[i] = live ? gC[i] : 0.f;
-            }
-#pragma unroll
-            for (int s = 16; s >= LANES; s /= 2)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    gB[i] += __shfl_xor_sync(0xffffffffu, gB[i], s);
-                    gC[i] += __shfl_xor_sync(0xffffffffu, gC[i], s);
-                }
-            if (lane < LANES)
-                for (int i = 0; i < 4; ++i)
-                    if (s0 + i < S) {
-                        const int64_t p = (block * a.N * a.T + n * a.T + t) * S + s0 + i;
-                        if (g.part_B != nullptr) g.part_B[p] = gB[i];
-                        if (g.part_C != nullptr) g.part_C[p] = gC[i];
-                    }
-            float gd = fmaf(u, xv, w);
-            if (a.delta_softplus) gd *= sigmoid(pre);
-            dskip = fmaf(gv, xv, dskip);
-            dbias += gd;
-            if (live && sl == 0) {
-                const int64_t e = (n * a.T + t) * a.D + d;
-                gx[e] = from_f<T>(fmaf(u, dt, gv * skip));
-                if (gdelta != nullptr) gdelta[e] = from_f<T>(gd);
-                if (gz != nullptr)
-                    gz[e] = from_f<T>(out * fmaf(skip, xv, yv) * sg * fmaf(zv, 1.f - sg, 1.f));
-            }
-        }
-    }
-    if (!live) return;
-    for (int i = 0; i < 4; ++i) {
-        if (s0 + i >= S) break;
-        if (g.initial_state != nullptr) g.initial_state[(n * a.D + d) * S + s0 + i] = G[i];
-        if (g.part_A != nullptr) g.part_A[(n * a.D + d) * S + s0 + i] = dA[i];
-    }
-    if (g.part_d != nullptr && sl == 0) {
-        g.part_d[(n * 2 + 0) * a.D + d] = dskip;
-        g.part_d[(n * 2 + 1) * a.D + d] = dbias;
+        return scatter_sums<H, HI / 2, LO>(v, lane) + (upper ? H : 0);
     }
 }
 
-__global__ void sum_parts_kernel(const float *part, int64_t parts, int64_t pitch, int64_t m, void *out, int bf16_out)
+template <class T, int LANES>
+__global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
+    grad_kernel(const __grid_constant__ rlscan_selective_scan_args a, const __grid_constant__ GradArgs g)
 {
-    const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-    if (i >= m) return;
+    using P = Shape<T, LANES>;
+    extern __shared__ __align__(16) char smem[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, sl = lane % LANES, group = lane / LANES;
+    float *F0 = reinterpret_cast<float *>(smem + P::STAGES * P::STAGE) + warp * 4 * P::F;  // dt
+    float *F1 = F0 + P::F, *F2 = F1 + P::F, *F3 = F2 + P::F;  // dt x then sum G B; g then sum q A2; sum C h
+    char *wide = smem + P::STAGES * P::STAGE + P::WARPS * 4 * P::F * 4;
+    float *red = reinterpret_cast<float *>(wide + P::WIDE);
+    ptx::pdl_trigger_dependents();
+    ptx::pdl_wait_prerequisites();
+    const int64_t blocks = (a.D + P::CH - 1) / P::CH, block = blockIdx.x % blocks, n = blockIdx.x / blocks;
+    const int64_t c0 = block * P::CH;
+    const int S = static_cast<int>(a.S), s0 = 4 * sl;
+    const int width = static_cast<int>(a.D - c0 < P::CH ? a.D - c0 : P::CH);
+    const int cw = warp * P::CW, c4 = cw + 4 * group;  // the warp's and the lane's first channel in the block
+    const int64_t marks = (a.T + kTile - 1) / kTile;
+    const int64_t len = row_length(a.lengths, n, a.T), tiles = (len + kTile - 1) / kTile;
+    const bool gated = a.z.data != nullptr;
+    const uint32_t gate = gated ? ~0u : 0u, soft = a.delta_softplus ? ~0u : 0u;
+
+    const T *x = static_cast<const T *>(a.x.data) + n * a.x.row_stride + c0;
+    const T *delta = static_cast<const T *>(a.delta.data) + n * a.delta.row_stride + c0;
+    const T *z = static_cast<const T *>(a.z.data) + n * a.z.row_stride + c0;
+    const T *gy = static_cast<const T *>(g.grad_y.data) + n * g.grad_y.row_stride + c0;
+    const T *B = static_cast<const T *>(a.B.data) + n * a.B.row_stride;
+    const T *C = static_cast<const T *>(a.C.data) + n * a.C.row_stride;
+    const uint8_t *resets = a.resets != nullptr ? a.resets + n * a.T : nullptr;
+    const float *mark = g.checkpoints + (n * marks * a.D + c0 + c4) * S + s0;
+
+    auto copy_tile = [&](auto unit, char *st, int64_t t, int rows) {
+        constexpr int CHUNK = decltype(unit)::value;
+        load_tile<T, kTile, P::CH, P::PITCH, CHUNK, P::THREADS>(st, x + t * a.x.token_stride, a.x.token_stride, rows, width);
+        load_tile<T, kTile, P::CH, P::PITCH, CHUNK, P::THREADS>(st + P::ACT, delta + t * a.delta.token_stride,
+                                                                a.delta.token_stride, rows, width);
+        if (gated)
+            load_tile<T, kTile, P::CH, P::PITCH, CHUNK, P::THREADS>(st + 2 * P::ACT, z + t * a.z.token_stride,
+                                                                    a.z.token_stride, rows, width);
+        load_tile<T, kTile, P::CH, P::PITCH, CHUNK, P::THREADS>(st + 3 * P::ACT, gy + t * g.grad_y.token_stride,
+                                                                g.grad_y.token_stride, rows, width);
+        load_tile<T, kTile, P::SP, P::BPITCH, CHUNK, P::THREADS>(st + 4 * P::ACT, B + t * a.B.token_stride,
+                                                                 a.B.token_stride, rows, S);
+        load_tile<T, kTile, P::SP, P::BPITCH, CHUNK, P::THREADS>(st + 4 * P::ACT + P::BC, C + t * a.C.token_stride,
+                                                                 a.C.token_stride, rows, S);
+    };
+    auto issue = [&](int64_t tile) {  // tiles go down
+        if (tile >= 0) {
+            char *st = smem + tile % P::STAGES * P::STAGE;
+            const int64_t t = tile * kTile, left = len - t;
+            const int rows = left < kTile ? static_cast<int>(left) : kTile;
+            if (g.unit == 16)
+                copy_tile(std::integral_constant<int, 16>(), st, t, rows);
+            else if (g.unit == 4)
+                copy_tile(std::integral_constant<int, 4>(), st, t, rows);
+            else
+                copy_tile(std::integral_constant<int, 0>(), st, t, rows);
+            // the lane's own states, four of each of its channels
+            char *own = st + 4 * P::ACT + 2 * P::BC + threadIdx.x * 16;
+            const float *m = mark + tile * a.D * S;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const bool on = c4 + c < width;
+                if (g.vec) {
+                    const bool have = on && s0 < S;
+                    copy16(own + c * P::THREADS * 16, have ? m + c * S : g.checkpoints, have ? 16 : 0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool have = on && s0 + i < S;
+                        copy4(own + c * P::THREADS * 16 + 4 * i, have ? m + c * S + i : g.checkpoints, have ? 4 : 0);
+                    }
+                }
+            }
+        }
+        copies_commit();
+    };
+
+    // padding: zeros
+    for (int64_t t = tiles * kTile; t < a.T; ++t) {
+        const int64_t row = n * a.T + t;
+        for (int c = threadIdx.x; c < width; c += P::THREADS) {
+            static_cast<T *>(g.x)[row * a.D + c0 + c] = from_f<T>(0.f);
+            if (g.delta != nullptr) static_cast<T *>(g.delta)[row * a.D + c0 + c] = from_f<T>(0.f);
+            if (g.z != nullptr) static_cast<T *>(g.z)[row * a.D + c0 + c] = from_f<T>(0.f);
+        }
+        for (int s = threadIdx.x; s < S; s += P::THREADS) {
+            if (g.part_B != nullptr) g.part_B[(block * a.N * a.T + row) * S + s] = 0.f;
+            if (g.part_C != nullptr) g.part_C[(block * a.N * a.T + row) * S + s] = 0.f;
+        }
+    }
+    issue(tiles - 1);
+
+    // [pair of channels][state]
+    f2 A2[2][4], G[2][4], dA[2][4];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float v[2], f[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int c = c4 + 2 * p + q;
+                const bool on = c < width && s0 + i < S;
+                v[q] = on ? a.A[(c0 + c) * S + s0 + i] * kLog2e : 0.f;
+                f[q] = on && g.grad_final != nullptr ? g.grad_final[(n * a.D + c0 + c) * S + s0 + i] : 0.f;
+            }
+            A2[p][i] = pair(v[0], v[1]);
+            G[p][i] = pair(f[0], f[1]);
+            dA[p][i] = 0ull;
+        }
+    float bias[P::CPL], skip[P::CPL], dskip[P::CPL], dbias[P::CPL];
+#pragma unroll
+    for (int j = 0; j < P::CPL; ++j) {
+        const int c = cw + (lane + 32 * j) % P::CW;
+        bias[j] = a.delta_bias != nullptr && c < width ? a.delta_bias[c0 + c] : 0.f;
+        skip[j] = a.skip != nullptr && c < width ? a.skip[c0 + c] : 0.f;
+        dskip[j] = dbias[j] = 0.f;
+    }
+
+    for (int64_t tile = tiles - 1; tile >= 0; --tile) {
+        const int64_t t0 = tile * kTile;
+        const int left = len - t0 < kTile ? static_cast<int>(len - t0) : kTile;
+        copies_wait<0>();
+        __syncthreads();  // the tile is here, and the buffer of the one before is free
+        issue(tile - 1);
+        const char *st = smem + tile % P::STAGES * P::STAGE;
+        const uint32_t starts =
+            resets != nullptr ? __ballot_sync(0xffffffffu, lane < left && resets[t0 + lane] != 0) : 0u;
+        for (int i = threadIdx.x; i < 2 * kTile * P::SP; i += P::THREADS) {
+            const float v = to_f(reinterpret_cast<const T *>(st + 4 * P::ACT)[i]);  // C lies behind B
+            reinterpret_cast<float2 *>(wide)[i] = make_float2(v, v);
+        }
+        const T *xs = reinterpret_cast<const T *>(st) + cw, *ds = reinterpret_cast<const T *>(st + P::ACT) + cw,
+                *zs = reinterpret_cast<const T *>(st + 2 * P::ACT) + cw, *ys = reinterpret_cast<const T *>(st + 3 * P::ACT) + cw;
+#pragma unroll
+        for (int j = 0; j < P::ITEMS; ++j) {
+            const int item = lane + 32 * j, c = item % P::CW, k = item / P::CW;
+            const float xv = to_f(xs[k * P::CH + c]), zv = to_f(zs[k * P::CH + c]);
+            const float pre = to_f(ds[k * P::CH + c]) + bias[j % P::CPL];
+            const float dt = k < left ? choose(soft, softplus(pre), pre) : 0.f;
+            F0[item] = dt;
+            F1[item] = dt * xv;
+            F2[item] = to_f(ys[k * P::CH + c]) * choose(gate, zv * sigmoid(zv), 1.f);
+        }
+        __syncthreads();
+
+        const ulonglong2 *Bd = reinterpret_cast<const ulonglong2 *>(wide) + 2 * sl;
+        const ulonglong2 *Cd = Bd + kTile * P::SP / 2;
+        const char *own = st + 4 * P::ACT + 2 * P::BC + threadIdx.x * 16;
+        auto row = [&](const float *f, int k, f2 *v) {  // four channels of a token
+            const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(f + k * P::CW + 4 * group);
+            v[0] = r.x;
+            v[1] = r.y;
+        };
+        auto states = [&](const ulonglong2 *w, int k, f2 *v) {  // four states of a token, each twice
+            const ulonglong2 lo = w[k * (P::SP / 2)], hi = w[k * (P::SP / 2) + 1];
+            v[0] = lo.x;
+            v[1] = lo.y;
+            v[2] = hi.x;
+            v[3] = hi.y;
+        };
+        auto begin = [&](f2 (*h)[4]) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const float4 u = *reinterpret_cast<const float4 *>(own + 2 * p * P::THREADS * 16);
+                const float4 v = *reinterpret_cast<const float4 *>(own + (2 * p + 1) * P::THREADS * 16);
+                h[p][0] = pair(u.x, v.x);
+                h[p][1] = pair(u.y, v.y);
+                h[p][2] = pair(u.z, v.z);
+                h[p][3] = pair(u.w, v.w);
+            }
+        };
+        auto walk = [&](auto fast) {
+            constexpr bool FAST = decltype(fast)::value;
+            auto step = [&](int k, const f2 (*from)[4], f2 (*to)[4]) {
+                f2 d[2], dx[2], b[4];
+                row(F0, k, d);
+                row(F1, k, dx);
+                states(Bd, k, b);
+                const bool cut = !FAST && (starts >> k & 1u) != 0;
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const f2 before = cut ? 0ull : from[p][i];
+                        to[p][i] = fma2(exp2_fast(mul2(d[p], A2[p][i])), before, mul2(dx[p], b[i]));
+                    }
+            };
+#pragma unroll 1
+            for (int half = 1; half >= 0; --half) {
+                f2 h[kHalf][2][4], h0[2][4];
+                begin(h0);
+                if (half == 1) {
+#pragma unroll
+                    for (int k = 0; k < kHalf; ++k) step(k, h0, h0);
+                }
+                const int k0 = half * kHalf;
+#pragma unroll
+                for (int k = 0; k < kHalf; ++k) step(k0 + k, k > 0 ? h[k > 0 ? k - 1 : 0] : h0, h[k]);
+#pragma unroll
+                for (int j = kHalf - 1; j >= 0; --j) {
+                    const int k = k0 + j;
+                    f2 d[2], dx[2], gv[2], b[4], c[4], u[2], w[2], y[2], gB[4], gC[4];
+                    row(F0, k, d);
+                    row(F1, k, dx);
+                    row(F2, k, gv);
+                    states(Bd, k, b);
+                    states(Cd, k, c);
+                    const bool cut = !FAST && (starts >> k & 1u) != 0;
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const f2 ndx = mul2(dx[p], both(-1.f));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const f2 hv = h[j][p][i];
+                            const f2 Gt = fma2(c[i], gv[p], G[p][i]);
+                            y[p] = i == 0 ? mul2(hv, c[i]) : fma2(hv, c[i], y[p]);
+                            gC[i] = p == 0 ? mul2(hv, gv[p]) : fma2(hv, gv[p], gC[i]);
+                            gB[i] = p == 0 ? mul2(Gt, dx[p]) : fma2(Gt, dx[p], gB[i]);
+                            u[p] = i == 0 ? mul2(Gt, b[i]) : fma2(Gt, b[i], u[p]);
+                            f2 q = mul2(Gt, fma2(ndx, b[i], hv));  // G exp(dt A) h_{t-1}
+                            if (!FAST) q = cut ? 0ull : q;
+                            w[p] = i == 0 ? mul2(q, A2[p][i]) : fma2(q, A2[p][i], w[p]);
+                            dA[p][i] = fma2(q, d[p], dA[p][i]);
+                            G[p][i] = mul2(Gt, exp2_fast(mul2(d[p], A2[p][i])));
+                            if (!FAST) G[p][i] = cut ? 0ull : G[p][i];
+                        }
+                    }
+                    float bc[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 vb = halves(gB[i]), vc = halves(gC[i]);
+                        bc[i] = vb.x + vb.y;
+                        bc[4 + i] = vc.x + vc.y;
+                    }
+                    const int kept = scatter_sums<8, 16, LANES>(bc, lane);
+                    constexpr int KEEP = P::GROUPS >= 8 ? 1 : 8 / P::GROUPS;
+#pragma unroll
+                    for (int i = 0; i < KEEP; ++i) {
+                        const int v = kept + i;
+                        red[((warp * kTile + k) * 2 + v / 4) * P::SP + s0 + v % 4] = bc[i];
+                    }
+                    float uv[4], wv[4], yv[4];
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const float2 a0 = halves(u[p]), a1 = halves(w[p]), a2 = halves(y[p]);
+                        uv[2 * p] = a0.x;
+                        uv[2 * p + 1] = a0.y;
+                        wv[2 * p] = a1.x;
+                        wv[2 * p + 1] = a1.y;
+                        yv[2 * p] = a2.x;
+                        yv[2 * p + 1] = a2.y;
+                    }
+                    const int ch = scatter_sums<4, LANES / 2, 1>(uv, lane);
+                    scatter_sums<4, LANES / 2, 1>(wv, lane);
+                    scatter_sums<4, LANES / 2, 1>(yv, lane);
+                    // every lane of the warp has read this token's F1 and F2: the shuffles came after
+                    constexpr int MINE = LANES >= 4 ? 1 : 4 / LANES;
+#pragma unroll
+                    for (int i = 0; i < MINE; ++i) {
+                        const int at = k * P::CW + 4 * group + ch + i;
+                        F1[at] = uv[i];
+                        F2[at] = wv[i];
+                        F3[at] = yv[i];
+                    }
+                }
+            }
+        };
+        if (starts == 0)
+            walk(std::true_type());
+        else
+            walk(std::false_type());
+        __syncthreads();
+
+        float sk[P::CPL], sb[P::CPL];
+#pragma unroll
+        for (int j = 0; j < P::CPL; ++j) sk[j] = sb[j] = 0.f;
+#pragma unroll
+        for (int j = 0; j < P::ITEMS; ++j) {
+            const int item = lane + 32 * j, c = item % P::CW, k = item / P::CW, m = j % P::CPL;
+            const float xv = to_f(xs[k * P::CH + c]), zv = to_f(zs[k * P::CH + c]), yv = to_f(ys[k * P::CH + c]);
+            const float pre = to_f(ds[k * P::CH + c]) + bias[m];
+            const float dt = F0[item], u = F1[item], w = F2[item] * kLn2, sum = F3[item];
+            const float sg = sigmoid(zv), gv = yv * choose(gate, zv * sg, 1.f);
+            const bool on = k < left;
+            float gd = fmaf(u, xv, w);
+            gd = on ? choose(soft, gd * sigmoid(pre), gd) : 0.f;
+            const float gx = on ? fmaf(u, dt, gv * skip[m]) : 0.f;
+            const float gz = on ? yv * fmaf(skip[m], xv, sum) * sg * fmaf(zv, 1.f - sg, 1.f) : 0.f;
+            sk[m] = fmaf(gv, xv, sk[m]);
+            sb[m] += gd;
+            if (cw + c < width && t0 + k < a.T) {
+                const int64_t e = (n * a.T + t0 + k) * a.D + c0 + cw + c;
+                static_cast<T *>(g.x)[e] = from_f<T>(gx);
+                if (g.delta != nullptr) static_cast<T *>(g.delta)[e] = from_f<T>(gd);
+                if (g.z != nullptr) static_cast<T *>(g.z)[e] = from_f<T>(gz);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < P::CPL; ++j) {
+            dskip[j] += sk[j];
+            dbias[j] += sb[j];
+        }
+        // the block's sums over its channels
+        for (int i = threadIdx.x; i < 2 * kTile * P::SP; i += P::THREADS) {
+            const int k = i / (2 * P::SP), which = i / P::SP % 2, s = i % P::SP;
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < P::WARPS; ++w) v += red[w * kTile * 2 * P::SP + i];
+            float *part = which == 0 ? g.part_B : g.part_C;
+            if (part != nullptr && s < S && t0 + k < a.T)
+                part[((block * a.N + n) * a.T + t0 + k) * S + s] = k < left ? v : 0.f;
+        }
+    }
+
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 gi = halves(G[p][i]), ga = halves(dA[p][i]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int c = c4 + 2 * p + q;
+                if (c >= width || s0 + i >= S) continue;
+                const int64_t e = (n * a.D + c0 + c) * S + s0 + i;
+                if (g.initial_state != nullptr) g.initial_state[e] = q == 0 ? gi.x : gi.y;
+                if (g.part_A != nullptr) g.part_A[e] = q == 0 ? ga.x : ga.y;
+            }
+        }
+    if (g.part_d != nullptr) {
+#pragma unroll
+        for (int j = 0; j < P::CPL; ++j) {
+#pragma unroll
+            for (int m = 16; m >= P::CW; m /= 2) {  // lanes that share a channel
+                dskip[j] += __shfl_xor_sync(0xffffffffu, dskip[j], m);
+                dbias[j] += __shfl_xor_sync(0xffffffffu, dbias[j], m);
+            }
+            const int c = cw + (lane + 32 * j) % P::CW;
+            if (c < width && lane < P::CW) {
+                g.part_d[(n * 2 + 0) * a.D + c0 + c] = dskip[j];
+                g.part_d[(n * 2 + 1) * a.D + c0 + c] = dbias[j];
+            }
+        }
+    }
+}
+
+// 32 columns x 8 slices of the parts a block; a slice adds its parts in
+// order, then the slices are added in order.
+constexpr int kSlices = 8;
+
+__global__ void __launch_bounds__(32 * kSlices) sums_kernel(const __grid_constant__ SumJobs jobs)
+{
+    __shared__ float scratch[kSlices][32];
+    ptx::pdl_trigger_dependents();
+    ptx::pdl_wait_prerequisites();
+    int which = 0;
+#pragma unroll
+    for (int j = 1; j < SumJobs::kMost; ++j)
+        if (j < jobs.count && blockIdx.x >= jobs.job[j].first) which = j;
+    const SumJobs::Job &job = jobs.job[which];
+    const int slice = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int64_t i = (blockIdx.x - job.first) * 32 + lane;
     float acc = 0.f;
-    for (int64_t w = 0; w < parts; ++w) acc += part[w * pitch + i];
-    if (bf16_out)
-        static_cast<bf16 *>(out)[i] = from_f<bf16>(acc);
+    if (i < job.m) {
+        const float *p = job.part + i;
+#pragma unroll 4
+        for (int64_t w = slice; w < job.parts; w += kSlices) acc += p[w * job.pitch];
+    }
+    scratch[slice][lane] = acc;
+    __syncthreads();
+    if (slice != 0 || i >= job.m) return;
+#pragma unroll
+    for (int s = 1; s < kSlices; ++s) acc += scratch[s][lane];
+    if (job.bf16_out)
+        static_cast<bf16 *>(job.out)[i] = from_f<bf16>(acc);
     else
-        static_cast<float *>(out)[i] = acc;
+        static_cast<float *>(job.out)[i] = acc;
 }
 
 struct Layout {
@@ -194,10 +462,17 @@ struct Layout {
     size_t B, C, A, d, bytes;
 };
 
+int grad_lanes(int64_t S)
+{
+    const int lanes = state_lanes(S);
+    return lanes < 2 ? 2 : lanes;
+}
+
 Layout layout(const rlscan_selective_scan_args &a)
 {
     Layout l;
-    l.blocks = ceil_div(a.D, 32 / state_lanes(a.S));
+    const int lanes = grad_lanes(a.S);
+    l.blocks = ceil_div(a.D, (lanes == 2 ? 2 : 4) * 4 * (32 / lanes));
     const size_t bc = sizeof(float) * static_cast<size_t>(l.blocks) * a.N * a.T * a.S;
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     l.B = 0;
@@ -208,30 +483,41 @@ Layout layout(const rlscan_selective_scan_args &a)
     return l;
 }
 
-template <class T>
-rlscan_status launch_typed(const rlscan_selective_scan_args &a, const GradArgs &g, cudaStream_t s)
+template <class T, int LANES>
+rlscan_status launch_shape(const rlscan_selective_scan_args &a, const GradArgs &g, cudaStream_t s)
 {
-    const int lanes = state_lanes(a.S);
-    const unsigned grid = static_cast<unsigned>(ceil_div(a.N * ceil_div(a.D, 32 / lanes), kThreads / 32));
-    switch (lanes) {
-    case 1: grad_kernel<T, 1><<<grid, kThreads, 0, s>>>(a, g); break;
-    case 2: grad_kernel<T, 2><<<grid, kThreads, 0, s>>>(a, g); break;
-    case 4: grad_kernel<T, 4><<<grid, kThreads, 0, s>>>(a, g); break;
-    case 8: grad_kernel<T, 8><<<grid, kThreads, 0, s>>>(a, g); break;
-    case 16: grad_kernel<T, 16><<<grid, kThreads, 0, s>>>(a, g); break;
-    default: grad_kernel<T, 32><<<grid, kThreads, 0, s>>>(a, g); break;
+    using P = Shape<T, LANES>;
+    auto kernel = grad_kernel<T, LANES>;
+    static const bool sized =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
+    if (!sized) return RLSCAN_ERR_CUDA;
+    return launch_overlapped(kernel, a.N * ceil_div(a.D, P::CH), P::THREADS, P::SMEM, s, a, g);
+}
+
+template <class T>
+rlscan_status launch_typed(const rlscan_selective_scan_args &a, GradArgs g, cudaStream_t s)
+{
+    Chunk c;
+    for (const rlscan_array3 *v : {&a.x, &a.delta, &a.B, &a.C, static_cast<const rlscan_array3 *>(&g.grad_y)})
+        c.add(v->data, v->row_stride, v->token_stride, sizeof(T));
+    if (a.z.data != nullptr) c.add(a.z.data, a.z.row_stride, a.z.token_stride, sizeof(T));
+    g.unit = c.size();
+    g.vec = a.S % 4 == 0 && (reinterpret_cast<uintptr_t>(g.checkpoints) & 15u) == 0;
+    switch (grad_lanes(a.S)) {
+    case 2: return launch_shape<T, 2>(a, g, s);
+    case 4: return launch_shape<T, 4>(a, g, s);
+    case 8: return launch_shape<T, 8>(a, g, s);
+    case 16: return launch_shape<T, 16>(a, g, s);
+    default: return launch_shape<T, 32>(a, g, s);
     }
-    return launched();
 }
 
 }  // namespace
 
-rlscan_status launch_sum_parts(const float *part, int64_t parts, int64_t pitch, int64_t m, void *out, bool bf16_out,
-                               cudaStream_t s)
+rlscan_status launch_sums(const SumJobs &jobs, cudaStream_t s)
 {
-    if (m == 0) return RLSCAN_OK;
-    sum_parts_kernel<<<static_cast<unsigned>(ceil_div(m, 256)), 256, 0, s>>>(part, parts, pitch, m, out, bf16_out);
-    return launched();
+    if (jobs.blocks == 0) return RLSCAN_OK;
+    return launch_overlapped(sums_kernel, jobs.blocks, 32 * kSlices, 0, s, jobs);
 }
 
 size_t selective_scan_backward_workspace(const rlscan_selective_scan_args &a) { return layout(a).bytes; }
@@ -260,14 +546,13 @@ rlscan_status launch_selective_scan_backward(const rlscan_selective_scan_args &a
         if (st != RLSCAN_OK) return st;
     }
     const int64_t bc = a.N * a.T * a.S;
-    rlscan_status st = RLSCAN_OK;
-    if (g.B != nullptr) st = launch_sum_parts(k.part_B, l.blocks, bc, bc, g.B, b16, s);
-    if (st == RLSCAN_OK && g.C != nullptr) st = launch_sum_parts(k.part_C, l.blocks, bc, bc, g.C, b16, s);
-    if (st == RLSCAN_OK && g.A != nullptr) st = launch_sum_parts(k.part_A, a.N, a.D * a.S, a.D * a.S, g.A, false, s);
-    if (st == RLSCAN_OK && g.skip != nullptr) st = launch_sum_parts(k.part_d, a.N, 2 * a.D, a.D, g.skip, false, s);
-    if (st == RLSCAN_OK && g.delta_bias != nullptr)
-        st = launch_sum_parts(k.part_d + a.D, a.N, 2 * a.D, a.D, g.delta_bias, false, s);
-    return st;
+    SumJobs jobs;
+    if (g.B != nullptr) jobs.add(k.part_B, l.blocks, bc, bc, g.B, b16);
+    if (g.C != nullptr) jobs.add(k.part_C, l.blocks, bc, bc, g.C, b16);
+    if (g.A != nullptr) jobs.add(k.part_A, a.N, a.D * a.S, a.D * a.S, g.A, false);
+    if (g.skip != nullptr) jobs.add(k.part_d, a.N, 2 * a.D, a.D, g.skip, false);
+    if (g.delta_bias != nullptr) jobs.add(k.part_d + a.D, a.N, 2 * a.D, a.D, g.delta_bias, false);
+    return launch_sums(jobs, s);
 }
 
 }  // namespace seq

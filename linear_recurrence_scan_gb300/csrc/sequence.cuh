@@ -6,9 +6,14 @@
 #include <cstddef>
 #include <cstdint>
 
+#include <initializer_list>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "params.cuh"
+#include "ptx.cuh"
 #include "rlscan.h"
 
 namespace rlscan {
@@ -69,12 +74,201 @@ __device__ __forceinline__ float softplus(float v)
     return fmaf(2.f * s, p, fmaxf(v, 0.f));
 }
 
+// `a` where the mask is all ones, `b` where it is 0.  Bit by bit: a ternary
+// around an expensive `a` becomes a branch, which would keep the work of
+// neighbouring tokens from overlapping.
+__device__ __forceinline__ float choose(uint32_t mask, float a, float b)
+{
+    return __uint_as_float((__float_as_uint(a) & mask) | (__float_as_uint(b) & ~mask));
+}
+
 // tokens of row n, clamped to the array
 __device__ __forceinline__ int64_t row_length(const int32_t *lengths, int64_t n, int64_t T)
 {
     if (lengths == nullptr) return T;
     const int64_t len = lengths[n];
     return len < 0 ? 0 : (len < T ? len : T);
+}
+
+// ---- pairs of float32 in one register pair (PTX f32x2) -----------------------
+// The pipe runs 128 float32 lanes a clock and SM either way; a pair halves the
+// instructions, which these kernels run out of first (measured: an
+// exponential with four multiply-adds a value, 31.5 values/clk/SM in pairs,
+// 24.7 one by one).
+using f2 = unsigned long long;
+
+__device__ __forceinline__ f2 pair(float lo, float hi)
+{
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 halves(f2 v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
+{
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b)
+{
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 both(float v) { return pair(v, v); }
+__device__ __forceinline__ f2 exp2_fast(f2 v)
+{
+    const float2 h = halves(v);
+    return pair(exp2_fast(h.x), exp2_fast(h.y));
+}
+__device__ __forceinline__ f2 rcp_fast(f2 v)
+{
+    const float2 h = halves(v);
+    return pair(rcp_fast(h.x), rcp_fast(h.y));
+}
+__device__ __forceinline__ f2 sigmoid(f2 v) { return rcp_fast(add2(both(1.f), exp2_fast(mul2(v, both(-kLog2e))))); }
+
+// softplus of both halves, as softplus(float)
+__device__ __forceinline__ f2 softplus(f2 v)
+{
+    const float2 h = halves(v);
+    const f2 e = exp2_fast(mul2(pair(fabsf(h.x), fabsf(h.y)), both(-kLog2e)));
+    const f2 s = mul2(e, rcp_fast(add2(both(2.f), e)));
+    const f2 q = mul2(s, s);
+    f2 p = both(1.f / 13.f);
+    p = fma2(p, q, both(1.f / 11.f));
+    p = fma2(p, q, both(1.f / 9.f));
+    p = fma2(p, q, both(1.f / 7.f));
+    p = fma2(p, q, both(1.f / 5.f));
+    p = fma2(p, q, both(1.f / 3.f));
+    p = fma2(p, q, both(1.f));
+    return fma2(add2(s, s), p, pair(fmaxf(h.x, 0.f), fmaxf(h.y, 0.f)));
+}
+
+// ---- asynchronous copies into shared memory ---------------------------------
+// `bytes` (0..16, rest zero-filled) of a 16-byte chunk, or 4 bytes
+__device__ __forceinline__ void copy16(void *dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(void *dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// A tile of ROWS tokens x WIDTH values in shared memory (rows PITCH bytes
+// apart) from rows `row_bytes` apart at `src`: `rows` of them hold tokens and
+// `width` values of each are inside the array; the rest of the tile becomes
+// 0.  CHUNK is the unit of the copies: 16 or 4 bytes, asynchronous, where
+// addresses and strides are multiples of it, or 0 for single values.
+template <class T, int ROWS, int WIDTH, int PITCH, int CHUNK, int THREADS>
+__device__ __forceinline__ void load_tile(char *dst, const T *src, int64_t stride, int rows, int width)
+{
+    if constexpr (CHUNK == 0) {
+        constexpr int N = ROWS * WIDTH;
+#pragma unroll 8
+        for (int i = threadIdx.x; i < N; i += THREADS) {
+            const int r = i / WIDTH, c = i % WIDTH;
+            T v = from_f<T>(0.f);
+            if (r < rows && c < width) v = src[r * stride + c];
+            *reinterpret_cast<T *>(dst + r * PITCH + c * sizeof(T)) = v;
+        }
+    } else {
+        constexpr int PER = CHUNK / static_cast<int>(sizeof(T)), CPR = WIDTH / PER, N = ROWS * CPR;
+        static_assert(WIDTH % PER == 0 && PITCH % CHUNK == 0 && (THREADS % CPR == 0 || CPR % THREADS == 0));
+        // a thread keeps its column and steps over rows (or, of wide rows, over columns)
+        constexpr int STEP = THREADS >= CPR ? THREADS / CPR : 1, ACROSS = THREADS >= CPR ? 1 : CPR / THREADS;
+        const int r0 = threadIdx.x / CPR, c0 = threadIdx.x % CPR * PER;
+        if (N < THREADS && threadIdx.x >= N) return;
+        const T *from = src + r0 * stride + c0;
+        char *to = dst + r0 * PITCH + c0 * static_cast<int>(sizeof(T));
+#pragma unroll
+        for (int r = 0; r < ROWS; r += STEP) {
+#pragma unroll
+            for (int x = 0; x < ACROSS; ++x) {
+                const int have = (width - c0 - x * THREADS * PER) * static_cast<int>(sizeof(T));
+                const int bytes = r0 + r < rows && have > 0 ? (have < CHUNK ? have : CHUNK) : 0;
+                const T *at = bytes > 0 ? from + x * THREADS * PER : src;
+                char *into = to + r * PITCH + x * THREADS * PER * static_cast<int>(sizeof(T));
+                if constexpr (CHUNK == 16)
+                    copy16(into, at, bytes);
+                else
+                    copy4(into, at, bytes);
+            }
+            from += STEP * stride;
+        }
+    }
+}
+
+// The chunk that fits a set of arrays: `add` each one's address and strides.
+struct Chunk {
+    uint64_t bits = 0;
+    void add(const void *p, int64_t row_stride, int64_t token_stride, int size)
+    {
+        bits |= reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(row_stride) * size |
+                static_cast<uint64_t>(token_stride) * size;
+    }
+    int size() const { return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 0; }
+};
+
+// Launch that lets the kernel's start overlap the end of the kernel before
+// it; every such kernel begins with ptx::pdl_wait_prerequisites().
+template <class K, class... Args>
+inline rlscan_status launch_overlapped(K kernel, int64_t grid, int threads, size_t smem, cudaStream_t stream,
+                                       Args... args)
+{
+    if (grid > 0x7fffffff) return RLSCAN_ERR_SHAPE;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return RLSCAN_ERR_CUDA;
+    }
+    return RLSCAN_OK;
+}
+
+// The device's SM count (0 on an error).
+inline int sm_count()
+{
+    static int counts[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (counts[dev] == 0 &&
+        cudaDeviceGetAttribute(&counts[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return counts[dev];
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -113,6 +307,7 @@ struct NormArgs {
     void *y;
     float *scales;
     void *residual_out;
+    bool vec = false;  // set by the launcher
 };
 rlscan_status launch_add_rms_norm(const NormArgs &a, bool bf16_io, bool bf16_residual, cudaStream_t s);
 
@@ -124,13 +319,32 @@ struct NormGradArgs {
     float eps;
     void *grad_x, *grad_h;
     float *grad_weight;
+    bool vec = false;  // set by the launcher
 };
 rlscan_status launch_add_rms_norm_backward(const NormGradArgs &a, bool bf16_io, bool bf16_h, void *ws, cudaStream_t s);
 size_t add_rms_norm_backward_workspace(int64_t M, int64_t D);
 
-// out[i] = sum over w in order of part[w * pitch + i], i < m, rounded to `bf16_out`'s type
-rlscan_status launch_sum_parts(const float *part, int64_t parts, int64_t pitch, int64_t m, void *out, bool bf16_out,
-                               cudaStream_t s);
+// Sums over parts, several in one launch:
+// out[i] = sum over w < parts of part[w * pitch + i], i < m, in a fixed order.
+struct SumJobs {
+    static constexpr int kMost = 5;
+    struct Job {
+        const float *part;
+        int64_t parts, pitch, m;
+        void *out;
+        int bf16_out;
+        int64_t first;  // its first block
+    } job[kMost];
+    int count = 0;
+    int64_t blocks = 0;
+    void add(const float *part, int64_t parts, int64_t pitch, int64_t m, void *out, bool bf16_out)
+    {
+        if (m == 0) return;
+        job[count++] = Job{part, parts, pitch, m, out, bf16_out ? 1 : 0, blocks};
+        blocks += (m + 31) / 32;
+    }
+};
+rlscan_status launch_sums(const SumJobs &jobs, cudaStream_t s);
 
 inline rlscan_status launched()
 {
