@@ -1,8 +1,9 @@
 // k_rms_norm.cu -- root-mean-square norm with the residual's addition, its
 // 8-bit output with a scale for each 128 columns, and its gradients.
 //
-// One pass: TPR threads take a row and keep it in registers (two chunks of
-// 16 bytes of x each) between the sum of squares and the outputs.
+// One pass: a warp or a block takes a row and keeps it in registers (two
+// chunks of 16 bytes of x a thread) between the sum of squares and the
+// outputs.
 #include <cuda_fp8.h>
 
 #include "sequence.cuh"
@@ -11,176 +12,169 @@ namespace rlscan {
 namespace seq {
 namespace {
 
+// Registers of a thread.  Measured (bf16): forward 32768 x 4096 to 8 bits
+// with 64: 154 us, 80: 152, 104: 175; gradients 16384 x 2560 with the
+// forward pass with 80: 176 us, 104: 136, 128: 133.
+constexpr int kNormRegisters = 80, kGradRegisters = 128;
 constexpr int kChunks = 2;  // chunks of a thread
+constexpr int kMostThreads = 512;
+constexpr int kRowWarps = 4;  // rows of a block whose rows take a warp each
 
 template <class T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));
 
-// the smallest power of two of threads that holds a row, 0 if 1024 do not
+// Threads of a row: whole warps, two chunks a thread; 0 if the row is too long.
 template <class T>
 int row_threads(int64_t D)
 {
-    for (int t = 32; t <= 1024; t *= 2)
-        if (D <= static_cast<int64_t>(t) * kChunks * kVec<T>) return t;
-    return 0;
+    const int64_t t = (D + kChunks * kVec<T> * 32 - 1) / (kChunks * kVec<T> * 32) * 32;
+    return t <= kMostThreads ? static_cast<int>(t) : 0;
 }
 
-// a chunk of V values of type R, wide where `vec`, else those inside the row (the others 0)
-template <class R, int V>
-__device__ __forceinline__ void load_chunk(float *v, const R *p, int64_t c, int64_t D, bool vec)
+// values c .. c+V-1 of a row of D, wide where `vec`; those past the row are 0
+template <class E, int V>
+__device__ __forceinline__ void load_raw(Words<E, V> &r, const E *p, int c, int D, bool vec)
 {
-    if (vec) {
-        constexpr int B = V * static_cast<int>(sizeof(R));
-        alignas(16) R raw[V];
-        if (c < D) {
-            if constexpr (B >= 16) {
-#pragma unroll
-                for (int i = 0; i < B / 16; ++i)
-                    reinterpret_cast<uint4 *>(raw)[i] = __ldg(reinterpret_cast<const uint4 *>(p + c) + i);
-            } else {
-                *reinterpret_cast<uint2 *>(raw) = __ldg(reinterpret_cast<const uint2 *>(p + c));
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = c < D ? to_f(raw[i]) : 0.f;
+    if (vec && c < D) {
+        r.load(p + c);
     } else {
+        r.zero();
+        if (!vec)
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = c + i < D ? to_f(p[c + i]) : 0.f;
+            for (int i = 0; i < V; i += 2)
+                r.set(i / 2, c + i < D ? to_f(p[c + i]) : 0.f, c + i + 1 < D ? to_f(p[c + i + 1]) : 0.f);
     }
 }
 
-template <class R, int V>
-__device__ __forceinline__ void store_chunk(R *p, const float *v, int64_t c, int64_t D, bool vec)
+template <class E, int V>
+__device__ __forceinline__ void store_chunk(E *p, const float *v, int c, int D, bool vec)
 {
     if (vec) {
-        constexpr int B = V * static_cast<int>(sizeof(R));
-        alignas(16) R raw[V];
+        Words<E, V> r;
 #pragma unroll
-        for (int i = 0; i < V; ++i) raw[i] = from_f<R>(v[i]);
-        if (c < D) {
-            if constexpr (B >= 16) {
-#pragma unroll
-                for (int i = 0; i < B / 16; ++i) reinterpret_cast<uint4 *>(p + c)[i] = reinterpret_cast<uint4 *>(raw)[i];
-            } else {
-                *reinterpret_cast<uint2 *>(p + c) = *reinterpret_cast<uint2 *>(raw);
-            }
-        }
+        for (int i = 0; i < V; i += 2) r.set(i / 2, v[i], v[i + 1]);
+        if (c < D) r.store(p + c);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (c + i < D) p[c + i] = from_f<R>(v[i]);
+            if (c + i < D) p[c + i] = from_f<E>(v[i]);
     }
 }
 
-// Sums of v[0..N) over a row's TPR threads, the same bits in each.
-template <int TPR, int N>
-__device__ __forceinline__ void row_sums(float *v, float (*scratch)[N])
+// Sums of v[0..N) over the threads of a row (WARP: a warp's, else the
+// block's), the same bits in each.  `flip` alternates, so that one barrier
+// suffices: a half is written again only after the next call's barrier.
+template <bool WARP, int N>
+__device__ __forceinline__ void row_sums(float *v, float (*scratch)[32][N], int flip)
 {
 #pragma unroll
     for (int m = 16; m > 0; m /= 2)
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
-    if constexpr (TPR > 32) {
-        const int warp = threadIdx.x / 32;
-        __syncthreads();  // scratch is free again
+    if constexpr (!WARP) {
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
-            for (int i = 0; i < N; ++i) scratch[warp][i] = v[i];
+            for (int i = 0; i < N; ++i) scratch[flip][threadIdx.x / 32][i] = v[i];
         __syncthreads();
-        const int first = warp / (TPR / 32) * (TPR / 32);
+        const int warps = blockDim.x / 32;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            v[i] = 0.f;
+        for (int i = 0; i < N; ++i) v[i] = 0.f;
+        for (int w = 0; w < warps; ++w)
 #pragma unroll
-            for (int w = 0; w < TPR / 32; ++w) v[i] += scratch[first + w][i];
-        }
+            for (int i = 0; i < N; ++i) v[i] += scratch[flip][w][i];
     }
 }
 
-template <int TPR>
-constexpr int kBlock = TPR > 128 ? TPR : 128;
-
-template <class T, class R, int TPR>
-__global__ void __launch_bounds__(kBlock<TPR>) norm_kernel(const __grid_constant__ NormArgs a)
+// A block walks rows in strides of the grid: the next row's loads are in
+// flight while this row's sum and outputs are made.
+template <class T, class R, bool WARP>
+__global__ void __maxnreg__(kNormRegisters) norm_kernel(const __grid_constant__ NormArgs a)
 {
-    constexpr int V = kVec<T>, ROWS = kBlock<TPR> / TPR;
-    __shared__ float scratch[kBlock<TPR> / 32][1];
+    constexpr int V = kVec<T>;
+    __shared__ float scratch[2][32][1];
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
-    const int64_t row = blockIdx.x * static_cast<int64_t>(ROWS) + threadIdx.x / TPR;
-    const bool on = row < a.M;
-    const int64_t D = on ? a.D : 0;
-    const int64_t rr = on ? row : 0;
-    const int tid = threadIdx.x % TPR;
-    const T *x = static_cast<const T *>(a.x) + rr * a.x_stride;
-    const R *r = static_cast<const R *>(a.residual) + (a.residual != nullptr ? rr * a.residual_stride : 0);
-    float h[kChunks][V];
-#pragma unroll
-    for (int j = 0; j < kChunks; ++j) load_chunk<T, V>(h[j], x, (j * TPR + tid) * V, D, a.vec);
-    if (a.residual != nullptr) {
-        float q[kChunks][V];
-#pragma unroll
-        for (int j = 0; j < kChunks; ++j) load_chunk<R, V>(q[j], r, (j * TPR + tid) * V, D, a.vec);
+    const int threads = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x, D = static_cast<int>(a.D);
+    const int64_t rows = WARP ? kRowWarps : 1, step = gridDim.x * rows;
+    int64_t row = blockIdx.x * rows + (WARP ? threadIdx.x / 32 : 0);
+    const int c0 = tid * V, c1 = c0 + threads * V;
+    const bool summed = a.residual != nullptr;
+    Words<T, V> x[kChunks];
+    Words<R, V> r[kChunks];
+    auto load = [&](int64_t at) {
+        const T *xp = static_cast<const T *>(a.x) + at * a.x_stride;
+        load_raw<T, V>(x[0], xp, c0, D, a.vec);
+        load_raw<T, V>(x[1], xp, c1, D, a.vec);
+        if (summed) {
+            const R *rp = static_cast<const R *>(a.residual) + at * a.residual_stride;
+            load_raw<R, V>(r[0], rp, c0, D, a.vec);
+            load_raw<R, V>(r[1], rp, c1, D, a.vec);
+        }
+    };
+    Words<float, V> w[kChunks];
+    if (row < a.M) load(row);
+    load_raw<float, V>(w[0], a.weight, c0, D, a.vec);
+    load_raw<float, V>(w[1], a.weight, c1, D, a.vec);
+    const float over = 1.f / static_cast<float>(D);
+    for (int flip = 0; row < a.M; row += step, flip ^= 1) {
+        float h[kChunks][V], ss[1] = {0.f};
 #pragma unroll
         for (int j = 0; j < kChunks; ++j) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) h[j][i] += q[j][i];
-            store_chunk<R, V>(static_cast<R *>(a.residual_out) + rr * a.D, h[j], (j * TPR + tid) * V, D, a.vec);
-        }
-    }
-    float ss[1] = {0.f};
-#pragma unroll
-    for (int j = 0; j < kChunks; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) ss[0] = fmaf(h[j][i], h[j][i], ss[0]);
-    row_sums<TPR, 1>(ss, scratch);
-    const float inv = rsqrtf(ss[0] / static_cast<float>(a.D) + a.eps);
-#pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-        const int64_t c = (j * TPR + tid) * V;
-        if (TPR * V * j >= a.D) break;
-        float w[V];
-        load_chunk<float, V>(w, a.weight, c, D, a.vec);
-#pragma unroll
-        for (int i = 0; i < V; ++i) h[j][i] = h[j][i] * inv * w[i];
-        if (a.scales == nullptr) {
-            store_chunk<T, V>(static_cast<T *>(a.y) + rr * a.D, h[j], c, D, a.vec);
-            continue;
-        }
-        // kScaleBlock / V neighbouring lanes hold a block of columns
-        float top = 0.f;
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            top = fmaxf(top, fabsf(h[j][i]));
-            bad = bad || !(fabsf(h[j][i]) <= 3.402823466e38f);
-        }
-        top = bad ? __int_as_float(0x7f800000) : top;
-#pragma unroll
-        for (int m = kScaleBlock / V / 2; m > 0; m /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        const float scale = top <= 3.402823466e38f ? fmaxf(top, kScaleFloor) / kE4m3Max : __int_as_float(0x7fffffff);
-        uint32_t q[V / 4];
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(h[j][i] / scale, h[j][i + 1] / scale),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(h[j][i + 2] / scale, h[j][i + 3] / scale),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            q[i / 4] = lo | hi << 16;
-        }
-        uint8_t *y = static_cast<uint8_t *>(a.y) + rr * a.D;
-        if (a.vec) {
-            if (c < D) {
-#pragma unroll
-                for (int i = 0; i < V / 4; ++i) reinterpret_cast<uint32_t *>(y + c)[i] = q[i];
+            for (int i = 0; i < V; ++i) {
+                h[j][i] = x[j][i];
+                if (summed) h[j][i] += r[j][i];
+                ss[0] = fmaf(h[j][i], h[j][i], ss[0]);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (c + i < D) y[c + i] = static_cast<uint8_t>(q[i / 4] >> (i % 4 * 8));
+            if (summed) store_chunk<R, V>(static_cast<R *>(a.residual_out) + row * a.D, h[j], j == 0 ? c0 : c1, D, a.vec);
         }
-        if (c < D && c % kScaleBlock == 0)
-            a.scales[rr * ((a.D + kScaleBlock - 1) / kScaleBlock) + c / kScaleBlock] = scale;
+        if (row + step < a.M) load(row + step);
+        row_sums<WARP, 1>(ss, scratch, flip);
+        const float inv = rsqrtf(fmaf(ss[0], over, a.eps));
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+            const int c = j == 0 ? c0 : c1;
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[j][i] = h[j][i] * inv * w[j][i];
+            if (a.scales == nullptr) {
+                store_chunk<T, V>(static_cast<T *>(a.y) + row * a.D, h[j], c, D, a.vec);
+                continue;
+            }
+            // kScaleBlock / V neighbouring lanes hold a block of columns; the
+            // bits of |v| order like |v|, with infinities and NaN on top
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(h[j][i]) & 0x7fffffffu);
+#pragma unroll
+            for (int m = kScaleBlock / V / 2; m > 0; m /= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+            const float scale =
+                top < 0x7f800000u ? fmaxf(__uint_as_float(top), kScaleFloor) / kE4m3Max : __int_as_float(0x7fffffff);
+            const float back = 1.f / scale;
+            uint32_t q[V / 4];
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const uint32_t lo =
+                    __nv_cvt_float2_to_fp8x2(make_float2(h[j][i] * back, h[j][i + 1] * back), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(h[j][i + 2] * back, h[j][i + 3] * back),
+                                                             __NV_SATFINITE, __NV_E4M3);
+                q[i / 4] = lo | hi << 16;
+            }
+            uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.D;
+            if (a.vec) {
+                if (c < D) {
+                    if constexpr (V == 8)
+                        *reinterpret_cast<uint2 *>(y + c) = make_uint2(q[0], q[1]);
+                    else
+                        *reinterpret_cast<uint32_t *>(y + c) = q[0];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (c + i < D) y[c + i] = static_cast<uint8_t>(q[i / 4] >> (i % 4 * 8));
+            }
+            if (c < D && c % kScaleBlock == 0)
+                a.scales[row * ((a.D + kScaleBlock - 1) / kScaleBlock) + c / kScaleBlock] = scale;
+        }
     }
 }
 
@@ -190,7 +184,7 @@ constexpr int kLongThreads = 1024;
 template <class T, class R>
 __global__ void __launch_bounds__(kLongThreads) long_norm_kernel(const __grid_constant__ NormArgs a)
 {
-    __shared__ float scratch[kLongThreads / 32][1];
+    __shared__ float scratch[2][32][1];
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
     const int64_t row = blockIdx.x;
@@ -203,7 +197,7 @@ __global__ void __launch_bounds__(kLongThreads) long_norm_kernel(const __grid_co
         ss[0] = fmaf(h, h, ss[0]);
         if (r != nullptr) static_cast<R *>(a.residual_out)[row * a.D + c] = from_f<R>(h);
     }
-    row_sums<kLongThreads, 1>(ss, scratch);
+    row_sums<false, 1>(ss, scratch, 0);
     const float inv = rsqrtf(ss[0] / static_cast<float>(a.D) + a.eps);
     if (a.scales == nullptr) {
         for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads)
@@ -237,85 +231,94 @@ __global__ void __launch_bounds__(kLongThreads) long_norm_kernel(const __grid_co
     }
 }
 
-// Gradients: dh = r (gn - n mean(gn n)) + grad_residual.  A block takes rows
-// in strides of the grid, the next row's loads ahead of this row's sums, and
-// keeps its sums of dy n in registers: one row of `part` for each row it
-// works on at a time.
-template <class T, class R, int TPR>
-__global__ void __launch_bounds__(kBlock<TPR>)
+// Gradients: dh = r (gn - n mean(gn n)) + grad_residual.  Rows as above; a
+// row's threads keep their sums of dy n in registers and write them as one
+// row of `part` at the end.
+template <class T, class R, bool WARP>
+__global__ void __maxnreg__(kGradRegisters)
     norm_grad_kernel(const __grid_constant__ NormGradArgs a, float *part)
 {
-    constexpr int V = kVec<T>, ROWS = kBlock<TPR> / TPR;
-    __shared__ float scratch[kBlock<TPR> / 32][2];
+    constexpr int V = kVec<T>;
+    __shared__ float scratch[2][32][2];
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
-    const int tid = threadIdx.x % TPR;
-    const int64_t slot = blockIdx.x * static_cast<int64_t>(ROWS) + threadIdx.x / TPR;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
-    float w[kChunks][V], dw[kChunks][V];
+    const int threads = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x, D = static_cast<int>(a.D);
+    const int64_t rows = WARP ? kRowWarps : 1, step = gridDim.x * rows;
+    const int64_t slot = blockIdx.x * rows + (WARP ? threadIdx.x / 32 : 0);
+    int64_t row = slot;
+    const int c0 = tid * V, c1 = c0 + threads * V;
+    Words<T, V> gy[kChunks];
+    Words<R, V> hr[kChunks], gr[kChunks];
 #pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-        load_chunk<float, V>(w[j], a.weight, (j * TPR + tid) * V, a.D, a.vec);
+    for (int j = 0; j < kChunks; ++j) gr[j].zero();
+    auto load = [&](int64_t at) {
+        const T *gp = static_cast<const T *>(a.grad_y) + at * a.grad_y_stride;
+        const R *hp = static_cast<const R *>(a.h) + at * a.h_stride;
+        load_raw<R, V>(hr[0], hp, c0, D, a.vec);
+        load_raw<R, V>(hr[1], hp, c1, D, a.vec);
+        load_raw<T, V>(gy[0], gp, c0, D, a.vec);
+        load_raw<T, V>(gy[1], gp, c1, D, a.vec);
+        if (a.grad_residual != nullptr) {
+            const R *rp = static_cast<const R *>(a.grad_residual) + at * a.grad_residual_stride;
+            load_raw<R, V>(gr[0], rp, c0, D, a.vec);
+            load_raw<R, V>(gr[1], rp, c1, D, a.vec);
+        }
+    };
+    if (row < a.M) load(row);
+    Words<float, V> w[kChunks];
+    load_raw<float, V>(w[0], a.weight, c0, D, a.vec);
+    load_raw<float, V>(w[1], a.weight, c1, D, a.vec);
+    float dw[kChunks][V];
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) dw[j][i] = 0.f;
-    }
-    const float over = 1.f / static_cast<float>(a.D);
-    for (int64_t base = blockIdx.x * static_cast<int64_t>(ROWS); base < a.M; base += step) {
-        const int64_t row = base + threadIdx.x / TPR;
-        const bool on = row < a.M;
-        const int64_t rr = on ? row : 0, D = on ? a.D : 0;
-        const T *gy = static_cast<const T *>(a.grad_y) + rr * a.grad_y_stride;
-        const R *h = static_cast<const R *>(a.h) + rr * a.h_stride;
-        float hv[kChunks][V], gv[kChunks][V], gr[kChunks][V];
-#pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            load_chunk<R, V>(hv[j], h, (j * TPR + tid) * V, D, a.vec);
-            load_chunk<T, V>(gv[j], gy, (j * TPR + tid) * V, D, a.vec);
-            if (a.grad_residual != nullptr) {
-                load_chunk<R, V>(gr[j], static_cast<const R *>(a.grad_residual) + rr * a.grad_residual_stride,
-                                 (j * TPR + tid) * V, D, a.vec);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) gr[j][i] = 0.f;
-            }
-        }
+    const float over = 1.f / static_cast<float>(D);
+    for (int flip = 0; row < a.M; row += step, flip ^= 1) {
+        Words<T, V> g0[kChunks];
+        Words<R, V> h0[kChunks], r0[kChunks];
         float s[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j)
+        for (int j = 0; j < kChunks; ++j) {
+            g0[j] = gy[j];
+            h0[j] = hr[j];
+            r0[j] = gr[j];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                s[0] = fmaf(hv[j][i], hv[j][i], s[0]);
-                s[1] = fmaf(gv[j][i] * w[j][i], hv[j][i], s[1]);
+                s[0] = fmaf(h0[j][i], h0[j][i], s[0]);
+                s[1] = fmaf(g0[j][i] * w[j][i], h0[j][i], s[1]);
             }
-        row_sums<TPR, 2>(s, scratch);
+        }
+        if (row + step < a.M) load(row + step);
+        row_sums<WARP, 2>(s, scratch, flip);
         const float inv = rsqrtf(fmaf(s[0], over, a.eps)), mean = s[1] * inv * over;
 #pragma unroll
         for (int j = 0; j < kChunks; ++j) {
-            const int64_t c = (j * TPR + tid) * V;
+            const int c = j == 0 ? c0 : c1;
+            float v[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float nv = hv[j][i] * inv;
-                dw[j][i] = fmaf(gv[j][i], nv, dw[j][i]);
-                gr[j][i] = fmaf(inv, fmaf(-nv, mean, gv[j][i] * w[j][i]), gr[j][i]);
+                const float nv = h0[j][i] * inv, gv = g0[j][i];
+                dw[j][i] = fmaf(gv, nv, dw[j][i]);
+                v[i] = fmaf(inv, fmaf(-nv, mean, gv * w[j][i]), r0[j][i]);
             }
-            store_chunk<T, V>(static_cast<T *>(a.grad_x) + rr * a.D, gr[j], c, D, a.vec);
-            if (a.grad_h != nullptr) store_chunk<R, V>(static_cast<R *>(a.grad_h) + rr * a.D, gr[j], c, D, a.vec);
+            store_chunk<T, V>(static_cast<T *>(a.grad_x) + row * a.D, v, c, D, a.vec);
+            if (a.grad_h != nullptr) store_chunk<R, V>(static_cast<R *>(a.grad_h) + row * a.D, v, c, D, a.vec);
         }
     }
     if (part != nullptr) {
-#pragma unroll
-        for (int j = 0; j < kChunks; ++j)
-            store_chunk<float, V>(part + slot * a.D, dw[j], (j * TPR + tid) * V, a.D, a.vec);
+        store_chunk<float, V>(part + slot * a.D, dw[0], c0, D, a.vec);
+        store_chunk<float, V>(part + slot * a.D, dw[1], c1, D, a.vec);
     }
 }
 
 template <class T, class R>
 __global__ void __launch_bounds__(kLongThreads) long_norm_grad_kernel(const __grid_constant__ NormGradArgs a, float *part)
 {
-    __shared__ float scratch[kLongThreads / 32][2];
+    __shared__ float scratch[2][32][2];
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
-    for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
+    for (int64_t row = blockIdx.x, flip = 0; row < a.M; row += gridDim.x, flip ^= 1) {
         const T *gy = static_cast<const T *>(a.grad_y) + row * a.grad_y_stride;
         const R *h = static_cast<const R *>(a.h) + row * a.h_stride;
         const R *gr = a.grad_residual != nullptr ? static_cast<const R *>(a.grad_residual) + row * a.grad_residual_stride
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(kLongThreads) long_norm_grad_kernel(const __gr
             s[0] = fmaf(hv, hv, s[0]);
             s[1] = fmaf(to_f(gy[c]) * a.weight[c], hv, s[1]);
         }
-        row_sums<kLongThreads, 2>(s, scratch);
+        row_sums<false, 2>(s, scratch, static_cast<int>(flip));
         const float inv = rsqrtf(s[0] / static_cast<float>(a.D) + a.eps), mean = s[1] * inv / static_cast<float>(a.D);
         for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads) {
             const float nv = to_f(h[c]) * inv, gv = to_f(gy[c]);
@@ -341,62 +344,77 @@ __global__ void __launch_bounds__(kLongThreads) long_norm_grad_kernel(const __gr
     }
 }
 
+// Blocks of a call: a wave of resident ones, at most what kWaveThreads allows
+// (the workspace's bound, from sizes alone).
+constexpr int kWaveThreads = 1536;
+
+int64_t row_blocks(int64_t M, int threads) { return threads == 32 ? ceil_div(M, kRowWarps) : M; }
+int block_threads(int threads) { return threads == 32 ? 32 * kRowWarps : threads; }
+
+int64_t most_blocks(int threads)
+{
+    const int64_t sms = sm_count() > 0 ? sm_count() : 152;
+    const int per_sm = kWaveThreads / block_threads(threads);
+    return sms * (per_sm > 0 ? per_sm : 1);
+}
+
+// resident blocks of `kernel` on the device; asked once for each block size
+template <class K>
+int64_t resident(K kernel, int threads)
+{
+    static int known[kLongThreads / 32 + 1] = {};
+    int &n = known[threads / 32];
+    if (n == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1)) {
+        cudaGetLastError();
+        n = 1;
+    }
+    return static_cast<int64_t>(n) * (sm_count() > 0 ? sm_count() : 1);
+}
+
+template <class K>
+int64_t wave(K kernel, int64_t M, int threads)
+{
+    int64_t grid = row_blocks(M, threads);
+    for (int64_t most : {most_blocks(threads), resident(kernel, block_threads(threads))})
+        if (grid > most) grid = most;
+    return grid;
+}
+
 template <class T, class R>
 rlscan_status forward(const NormArgs &a, cudaStream_t s)
 {
-    auto go = [&](auto tpr) {
-        constexpr int TPR = decltype(tpr)::value;
-        return launch_overlapped(norm_kernel<T, R, TPR>, ceil_div(a.M, kBlock<TPR> / TPR), kBlock<TPR>, 0, s, a);
-    };
-    switch (row_threads<T>(a.D)) {
-    case 32: return go(std::integral_constant<int, 32>());
-    case 64: return go(std::integral_constant<int, 64>());
-    case 128: return go(std::integral_constant<int, 128>());
-    case 256: return go(std::integral_constant<int, 256>());
-    case 512: return go(std::integral_constant<int, 512>());
-    case 1024: return go(std::integral_constant<int, 1024>());
-    default: return launch_overlapped(long_norm_kernel<T, R>, a.M, kLongThreads, 0, s, a);
-    }
+    const int t = row_threads<T>(a.D);
+    if (t == 0) return launch_overlapped(long_norm_kernel<T, R>, a.M, kLongThreads, 0, s, a);
+    if (t == 32)
+        return launch_overlapped(norm_kernel<T, R, true>, wave(norm_kernel<T, R, true>, a.M, t), block_threads(t), 0, s, a);
+    return launch_overlapped(norm_kernel<T, R, false>, wave(norm_kernel<T, R, false>, a.M, t), t, 0, s, a);
 }
 
-// Rows of partial sums of the weight's gradient: a wave of blocks' worth.
-constexpr int64_t kParts = 152 * 8;
-
+// most rows of `part` that a call fills
 template <class T>
-int64_t grad_grid(int64_t M, int64_t D)
+int64_t most_parts(int64_t M, int64_t D)
 {
-    const int tpr = row_threads<T>(D);
-    const int64_t rows = tpr > 0 && tpr < 128 ? 128 / tpr : 1;   // a block works on at a time
-    const int64_t most = tpr > 256 || tpr == 0 ? kParts / 4 : kParts / rows;
-    const int64_t need = ceil_div(M, rows);
-    return need < most ? need : most;
+    const int t = row_threads<T>(D);
+    const int64_t need = row_blocks(M, t), most = most_blocks(t == 0 ? kLongThreads : t);
+    return (need < most ? need : most) * (t == 32 ? kRowWarps : 1);
 }
 
+// launches, and says how many rows of `part` it fills
 template <class T, class R>
-rlscan_status backward(const NormGradArgs &a, float *part, cudaStream_t s)
+rlscan_status backward(const NormGradArgs &a, float *part, int64_t &parts, cudaStream_t s)
 {
-    const int64_t grid = grad_grid<T>(a.M, a.D);
-    auto go = [&](auto tpr) {
-        constexpr int TPR = decltype(tpr)::value;
-        return launch_overlapped(norm_grad_kernel<T, R, TPR>, grid, kBlock<TPR>, 0, s, a, part);
-    };
-    switch (row_threads<T>(a.D)) {
-    case 32: return go(std::integral_constant<int, 32>());
-    case 64: return go(std::integral_constant<int, 64>());
-    case 128: return go(std::integral_constant<int, 128>());
-    case 256: return go(std::integral_constant<int, 256>());
-    case 512: return go(std::integral_constant<int, 512>());
-    case 1024: return go(std::integral_constant<int, 1024>());
-    default: return launch_overlapped(long_norm_grad_kernel<T, R>, grid, kLongThreads, 0, s, a, part);
+    const int t = row_threads<T>(a.D);
+    if (t == 0) {
+        parts = wave(long_norm_grad_kernel<T, R>, a.M, kLongThreads);
+        return launch_overlapped(long_norm_grad_kernel<T, R>, parts, kLongThreads, 0, s, a, part);
     }
-}
-
-// rows of `part` that a call fills
-template <class T>
-int64_t parts_of(int64_t M, int64_t D)
-{
-    const int tpr = row_threads<T>(D);
-    return grad_grid<T>(M, D) * (tpr > 0 && tpr < 128 ? 128 / tpr : 1);
+    if (t == 32) {
+        const int64_t grid = wave(norm_grad_kernel<T, R, true>, a.M, t);
+        parts = grid * kRowWarps;
+        return launch_overlapped(norm_grad_kernel<T, R, true>, grid, block_threads(t), 0, s, a, part);
+    }
+    parts = wave(norm_grad_kernel<T, R, false>, a.M, t);
+    return launch_overlapped(norm_grad_kernel<T, R, false>, parts, t, 0, s, a, part);
 }
 
 uint64_t low_bits(const void *p) { return reinterpret_cast<uintptr_t>(p); }
@@ -417,7 +435,7 @@ rlscan_status launch_add_rms_norm(const NormArgs &args, bool bf16_io, bool bf16_
 
 size_t add_rms_norm_backward_workspace(int64_t M, int64_t D)
 {
-    const int64_t f = parts_of<float>(M, D), b = parts_of<bf16>(M, D);
+    const int64_t f = most_parts<float>(M, D), b = most_parts<bf16>(M, D);
     return sizeof(float) * static_cast<size_t>(f > b ? f : b) * D;
 }
 
@@ -430,13 +448,14 @@ rlscan_status launch_add_rms_norm_backward(const NormGradArgs &args, bool bf16_i
     if (a.grad_residual != nullptr) bits |= low_bits(a.grad_residual) | a.grad_residual_stride * hs;
     a.vec = bits % 16 == 0;
     float *part = a.grad_weight != nullptr ? static_cast<float *>(ws) : nullptr;
+    int64_t parts = 0;
     if (a.M > 0) {
-        const rlscan_status st = !bf16_io ? backward<float, float>(a, part, s)
-                                          : (bf16_h ? backward<bf16, bf16>(a, part, s) : backward<bf16, float>(a, part, s));
+        const rlscan_status st = !bf16_io ? backward<float, float>(a, part, parts, s)
+                                 : bf16_h ? backward<bf16, bf16>(a, part, parts, s)
+                                          : backward<bf16, float>(a, part, parts, s);
         if (st != RLSCAN_OK) return st;
     }
     if (a.grad_weight == nullptr) return RLSCAN_OK;
-    const int64_t parts = a.M == 0 ? 0 : (bf16_io ? parts_of<bf16>(a.M, a.D) : parts_of<float>(a.M, a.D));
     SumJobs jobs;
     jobs.add(part, parts, a.D, a.D, a.grad_weight, false);
     return launch_sums(jobs, s);

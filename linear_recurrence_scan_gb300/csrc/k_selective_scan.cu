@@ -27,6 +27,7 @@ struct ScanOut {
     float *states;   // [N][chunks][D][S]: a chunk's own end state, then the state in front of it
     float *spans;    // [N][chunks][D]: the chunk's sum of dt
     uint8_t *cuts;   // [N][chunks]: an episode starts in the chunk
+    rlscan_array3 grad_y;  // BACK
 };
 
 template <class T, int SPT, int LANES>
@@ -97,12 +98,18 @@ __device__ __forceinline__ void store_states(float *p, const f2 *h, int s0, int 
     }
 }
 
-// FULL: outputs; otherwise only a chunk's end state and sum of dt, from 0.
-template <class T, int SPT, int LANES, bool FULL>
+// FULL: outputs.  PART: a chunk's end state from 0 and its sum of dt.  BACK:
+// the same for the gradient of the states, from the chunk's last token to
+// its first: E_t = exp(dt_t A) (E_{t+1} + C_t g_t), with grad_y in x's place
+// and C in B's.
+enum Mode { FULL_SCAN, PART, BACK };
+
+template <class T, int SPT, int LANES, int MODE>
 __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
     scan_kernel(const __grid_constant__ rlscan_selective_scan_args a, const __grid_constant__ ScanOut o)
 {
     using P = Shape<T, SPT, LANES>;
+    constexpr bool FULL = MODE == FULL_SCAN;
     extern __shared__ __align__(16) char smem[];
     float *wide = reinterpret_cast<float *>(smem + P::STAGES * P::STAGE);
     ptx::pdl_trigger_dependents();
@@ -116,39 +123,41 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
     const int64_t dd = live ? d : a.D - 1;
     const int s0 = SPT * sl, S = static_cast<int>(a.S);
     const int width = static_cast<int>(a.D - c0 < P::CH ? a.D - c0 : P::CH);
-    const bool gated = FULL && a.z.data != nullptr;
+    const bool gated = MODE != PART && a.z.data != nullptr;
     const uint32_t gate = gated ? ~0u : 0u, soft = a.delta_softplus ? ~0u : 0u;
     const int64_t first = chunk * o.chunk, last = first + o.chunk < a.T ? first + o.chunk : a.T;
     const int64_t len = row_length(a.lengths, n, a.T);
     const int64_t stop = len < last ? len : last;  // tokens first <= t < stop are scanned
 
-    const T *x = static_cast<const T *>(a.x.data) + n * a.x.row_stride + first * a.x.token_stride + c0;
+    const rlscan_array3 &in = MODE == BACK ? o.grad_y : a.x, &drive = MODE == BACK ? a.C : a.B;
+    const T *x = static_cast<const T *>(in.data) + n * in.row_stride + first * in.token_stride + c0;
     const T *delta = static_cast<const T *>(a.delta.data) + n * a.delta.row_stride + first * a.delta.token_stride + c0;
     const T *z = static_cast<const T *>(a.z.data) + n * a.z.row_stride + first * a.z.token_stride + c0;
-    const T *B = static_cast<const T *>(a.B.data) + n * a.B.row_stride + first * a.B.token_stride;
+    const T *B = static_cast<const T *>(drive.data) + n * drive.row_stride + first * drive.token_stride;
     const T *C = static_cast<const T *>(a.C.data) + n * a.C.row_stride + first * a.C.token_stride;
     const uint8_t *resets = a.resets != nullptr ? a.resets + n * a.T + first : nullptr;
 
+    const int64_t count = stop - first, tiles = count > 0 ? (count + kTile - 1) / kTile : 0;
     auto copy_tile = [&](auto unit, int64_t tile) {
         constexpr int CHUNK = decltype(unit)::value;
-        const int64_t t = tile * kTile, left = stop - first - t;
+        const int64_t t = (MODE == BACK ? tiles - 1 - tile : tile) * kTile, left = count - t;
         char *st = smem + tile % P::STAGES * P::STAGE;
         const int rows = left < kTile ? static_cast<int>(left) : kTile;
-        load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kThreads>(st, x + t * a.x.token_stride, a.x.token_stride, rows, width);
+        load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kThreads>(st, x + t * in.token_stride, in.token_stride, rows, width);
         load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kThreads>(st + P::ACT, delta + t * a.delta.token_stride,
                                                               a.delta.token_stride, rows, width);
-        load_tile<T, kTile, P::BW, P::BPITCH, CHUNK, kThreads>(st + 3 * P::ACT, B + t * a.B.token_stride,
-                                                               a.B.token_stride, rows, S);
+        load_tile<T, kTile, P::BW, P::BPITCH, CHUNK, kThreads>(st + 3 * P::ACT, B + t * drive.token_stride,
+                                                               drive.token_stride, rows, S);
+        if (gated)
+            load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kThreads>(st + 2 * P::ACT, z + t * a.z.token_stride,
+                                                                  a.z.token_stride, rows, width);
         if (FULL) {
-            if (gated)
-                load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kThreads>(st + 2 * P::ACT, z + t * a.z.token_stride,
-                                                                      a.z.token_stride, rows, width);
             load_tile<T, kTile, P::BW, P::BPITCH, CHUNK, kThreads>(st + 3 * P::ACT + P::BC, C + t * a.C.token_stride,
                                                                    a.C.token_stride, rows, S);
         }
     };
     auto issue = [&](int64_t tile) {
-        if (stop - first > tile * kTile) {
+        if (tile < tiles) {
             if (o.unit == 16)
                 copy_tile(std::integral_constant<int, 16>(), tile);
             else if (o.unit == 4)
@@ -177,10 +186,13 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
     float span = 0.f;
     uint32_t cut = 0;
 
-    const int64_t count = stop - first, tiles = count > 0 ? (count + kTile - 1) / kTile : 0;
-    uint32_t flag = resets != nullptr && lane < kTile && lane < count ? resets[lane] : 0u;  // one tile ahead
+    auto flag_at = [&](int64_t tile) {
+        const int64_t t = (MODE == BACK ? tiles - 1 - tile : tile) * kTile + lane;
+        return resets != nullptr && lane < kTile && t >= 0 && t < count ? static_cast<uint32_t>(resets[t]) : 0u;
+    };
+    uint32_t flag = flag_at(0);  // one tile ahead
     for (int64_t tile = 0; tile < tiles; ++tile) {
-        const int64_t t0 = tile * kTile;
+        const int64_t t0 = (MODE == BACK ? tiles - 1 - tile : tile) * kTile;
         copies_wait<1>();
         __syncthreads();  // the tile is here, and its predecessor's buffer is free
         issue(tile + 2);
@@ -205,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
             Cw = Bw + P::BC / 4;
         }
         const uint32_t starts = resets != nullptr ? __ballot_sync(0xffffffffu, flag != 0) : 0u;
-        if (resets != nullptr) flag = lane < kTile && t0 + kTile + lane < count ? resets[t0 + kTile + lane] : 0u;
+        if (resets != nullptr) flag = tile + 1 < tiles ? flag_at(tile + 1) : 0u;
         cut |= starts;
         if (FULL && mark != nullptr && live) store_states<SPT>(mark + tile * a.D * S, h, s0, S, o.vec);
         const int left = count - t0 < kTile ? static_cast<int>(count - t0) : kTile;
@@ -236,17 +248,23 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
 #pragma unroll
             for (int p = 0; p < P::PER; ++p) {
                 if (!FAST) dt[p] = p * LANES + sl < left ? dt[p] : 0.f;  // past the last token the state stays
-                dtx[p] = dt[p] * xv[p];
+                if constexpr (MODE == BACK) {
+                    const float zv = to_f(zs[(p * LANES + sl) * ROW]);
+                    dtx[p] = xv[p] * choose(gate, zv * sigmoid(zv), 1.f);
+                } else {
+                    dtx[p] = dt[p] * xv[p];
+                }
                 if (!FULL) span += dt[p];
             }
 #pragma unroll
-            for (int k = 0; k < kTile; ++k) {
+            for (int kk = 0; kk < kTile; ++kk) {
+                const int k = MODE == BACK ? kTile - 1 - kk : kk;
                 float dj = dt[k / LANES], xj = dtx[k / LANES];
                 if constexpr (LANES > 1) {
                     dj = __shfl_sync(0xffffffffu, dj, k % LANES, LANES);
                     xj = __shfl_sync(0xffffffffu, xj, k % LANES, LANES);
                 }
-                if (!FAST && (starts >> k & 1u) != 0) {
+                if (!FAST && MODE != BACK && (starts >> k & 1u) != 0) {
 #pragma unroll
                     for (int i = 0; i < SPT / 2; ++i) h[i] = 0ull;
                 }
@@ -255,13 +273,23 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
 #pragma unroll
                 for (int i = 0; i < SPT / 4; ++i) {
                     const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(Bw + k * BROW + 4 * i);
-                    h[2 * i] = fma2(exp2_fast(mul2(dp, A2[2 * i])), h[2 * i], mul2(xp, b.x));
-                    h[2 * i + 1] = fma2(exp2_fast(mul2(dp, A2[2 * i + 1])), h[2 * i + 1], mul2(xp, b.y));
+                    const f2 e0 = exp2_fast(mul2(dp, A2[2 * i])), e1 = exp2_fast(mul2(dp, A2[2 * i + 1]));
+                    if constexpr (MODE == BACK) {
+                        h[2 * i] = mul2(e0, fma2(xp, b.x, h[2 * i]));
+                        h[2 * i + 1] = mul2(e1, fma2(xp, b.y, h[2 * i + 1]));
+                    } else {
+                        h[2 * i] = fma2(e0, h[2 * i], mul2(xp, b.x));
+                        h[2 * i + 1] = fma2(e1, h[2 * i + 1], mul2(xp, b.y));
+                    }
                     if (FULL) {
                         const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(Cw + k * BROW + 4 * i);
                         acc[0] = i == 0 ? mul2(c.x, h[0]) : fma2(c.x, h[2 * i], acc[0]);
                         acc[1] = i == 0 ? mul2(c.y, h[1]) : fma2(c.y, h[2 * i + 1], acc[1]);
                     }
+                }
+                if (!FAST && MODE == BACK && (starts >> k & 1u) != 0) {
+#pragma unroll
+                    for (int i = 0; i < SPT / 2; ++i) h[i] = 0ull;
                 }
                 if (FULL) {
                     const float2 v = halves(add2(acc[0], acc[1]));
@@ -312,25 +340,42 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
 }
 
 // The state in front of each chunk: carry = exp(A span) carry + the chunk's
-// own end state, or that alone where an episode starts in the chunk.
-__global__ void __launch_bounds__(256)
-    chunk_kernel(const __grid_constant__ rlscan_selective_scan_args a, const __grid_constant__ ScanOut o)
+// own end state, or that alone where an episode starts in the chunk.  BACK:
+// the gradient's message behind each chunk, from the last to the first.
+// Eight chunks' loads are in flight before their states are replaced.
+template <bool REVERSE>
+__global__ void __launch_bounds__(256) chunk_kernel(const __grid_constant__ rlscan_selective_scan_args a,
+                                                    const __grid_constant__ ScanOut o, const float *start)
 {
+    constexpr int AHEAD = 8;
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
     const int64_t i = blockIdx.x * 256ll + threadIdx.x, DS = a.D * a.S;
     if (i >= a.N * DS) return;
     const int64_t n = i / DS, e = i % DS, d = e / a.S;
     const float A2 = a.A[e] * kLog2e;
-    float carry = a.initial_state != nullptr ? a.initial_state[i] : 0.f;
+    float carry = start != nullptr ? start[i] : 0.f;
     float *st = o.states + n * o.chunks * DS + e;
     const float *sp = o.spans + n * o.chunks * a.D + d;
-#pragma unroll 4
-    for (int64_t c = 0; c < o.chunks; ++c) {
-        const float own = st[c * DS], span = sp[c * a.D];
-        const bool cut = o.cuts[n * o.chunks + c] != 0;
-        st[c * DS] = carry;
-        carry = cut ? own : fmaf(exp2_fast(A2 * span), carry, own);
+    const uint8_t *cut = o.cuts + n * o.chunks;
+    for (int64_t base = 0; base < o.chunks; base += AHEAD) {
+        float own[AHEAD], span[AHEAD];
+        uint8_t cuts[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            if (base + u >= o.chunks) break;
+            const int64_t c = REVERSE ? o.chunks - 1 - base - u : base + u;
+            own[u] = st[c * DS];
+            span[u] = sp[c * a.D];
+            cuts[u] = cut[c];
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            if (base + u >= o.chunks) break;
+            const int64_t c = REVERSE ? o.chunks - 1 - base - u : base + u;
+            st[c * DS] = carry;
+            carry = cuts[u] != 0 ? own[u] : fmaf(exp2_fast(A2 * span[u]), carry, own[u]);
+        }
     }
 }
 
@@ -339,15 +384,16 @@ rlscan_status launch_shape(const rlscan_selective_scan_args &a, const ScanOut &o
 {
     using P = Shape<T, SPT, LANES>;
     const int64_t grid = a.N * ceil_div(a.D, P::CH) * o.chunks;
-    auto full = scan_kernel<T, SPT, LANES, true>;
-    auto part = scan_kernel<T, SPT, LANES, false>;
+    auto full = scan_kernel<T, SPT, LANES, FULL_SCAN>;
+    auto part = scan_kernel<T, SPT, LANES, PART>;
     static const bool sized =
         cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess &&
         cudaFuncSetAttribute(part, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
     if (!sized) return RLSCAN_ERR_CUDA;
     if (o.chunks > 1) {
         rlscan_status st = launch_overlapped(part, grid, kThreads, P::SMEM, s, a, o);
-        if (st == RLSCAN_OK) st = launch_overlapped(chunk_kernel, ceil_div(a.N * a.D * a.S, 256), 256, 0, s, a, o);
+        if (st == RLSCAN_OK)
+            st = launch_overlapped(chunk_kernel<false>, ceil_div(a.N * a.D * a.S, 256), 256, 0, s, a, o, a.initial_state);
         if (st != RLSCAN_OK) return st;
     }
     return launch_overlapped(full, grid, kThreads, P::SMEM, s, a, o);
@@ -413,6 +459,37 @@ rlscan_status launch_typed(const Plan &p, const rlscan_selective_scan_args &a, S
             ((reinterpret_cast<uintptr_t>(o.final_state) | reinterpret_cast<uintptr_t>(o.checkpoints)) & 15u) == 0;
     if (p.spt == 16) return by_lanes<T, 16>(p.lanes, a, o, s);
     return by_lanes<T, 8>(p.lanes, a, o, s);
+}
+
+// The gradient's messages, for the backward pass: its own shape of lanes.
+template <class T, int SPT, int LANES>
+rlscan_status launch_back(const rlscan_selective_scan_args &a, const ScanOut &o, const float *grad_final, cudaStream_t s)
+{
+    using P = Shape<T, SPT, LANES>;
+    auto back = scan_kernel<T, SPT, LANES, BACK>;
+    static const bool sized =
+        cudaFuncSetAttribute(back, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
+    if (!sized) return RLSCAN_ERR_CUDA;
+    const rlscan_status st =
+        launch_overlapped(back, a.N * ceil_div(a.D, P::CH) * o.chunks, kThreads, P::SMEM, s, a, o);
+    if (st != RLSCAN_OK) return st;
+    return launch_overlapped(chunk_kernel<true>, ceil_div(a.N * a.D * a.S, 256), 256, 0, s, a, o, grad_final);
+}
+
+template <class T>
+rlscan_status back_typed(const rlscan_selective_scan_args &a, ScanOut o, const float *grad_final, cudaStream_t s)
+{
+    Chunk c;
+    for (const rlscan_array3 *v : {static_cast<const rlscan_array3 *>(&o.grad_y), &a.delta, &a.C})
+        c.add(v->data, v->row_stride, v->token_stride, sizeof(T));
+    if (a.z.data != nullptr) c.add(a.z.data, a.z.row_stride, a.z.token_stride, sizeof(T));
+    o.unit = c.size();
+    o.vec = a.S % 4 == 0;
+    if (a.S <= 8) return launch_back<T, 8, 1>(a, o, grad_final, s);
+    if (a.S <= 16) return launch_back<T, 8, 2>(a, o, grad_final, s);
+    if (a.S <= 32) return launch_back<T, 8, 4>(a, o, grad_final, s);
+    if (a.S <= 64) return launch_back<T, 8, 8>(a, o, grad_final, s);
+    return launch_back<T, 8, 16>(a, o, grad_final, s);
 }
 
 // One token: a lane has four states of one channel, of kStepRows sequences
@@ -537,7 +614,7 @@ rlscan_status launch_selective_scan(const rlscan_selective_scan_args &a, void *y
                                     float *checkpoints, void *ws, cudaStream_t s)
 {
     const Plan p = plan(a);
-    ScanOut o{y, final_state, checkpoints, p.chunk, p.chunks, 0, false, nullptr, nullptr, nullptr};
+    ScanOut o{y, final_state, checkpoints, p.chunk, p.chunks, 0, false, nullptr, nullptr, nullptr, {}};
     if (p.chunks > 1) {
         const size_t each = static_cast<size_t>(a.N) * p.chunks;
         char *w = static_cast<char *>(ws);
@@ -546,6 +623,14 @@ rlscan_status launch_selective_scan(const rlscan_selective_scan_args &a, void *y
         o.cuts = reinterpret_cast<uint8_t *>(w + up(each * a.D * a.S * 4) + up(each * a.D * 4));
     }
     return a.dtype == RLSCAN_BF16 ? launch_typed<bf16>(p, a, o, s) : launch_typed<float>(p, a, o, s);
+}
+
+rlscan_status launch_back_states(const rlscan_selective_scan_args &a, const rlscan_array3 &grad_y, const float *grad_final,
+                                 int64_t chunk, int64_t chunks, float *states, float *spans, uint8_t *cuts,
+                                 cudaStream_t s)
+{
+    const ScanOut o{nullptr, nullptr, nullptr, chunk, chunks, 0, false, states, spans, cuts, grad_y};
+    return a.dtype == RLSCAN_BF16 ? back_typed<bf16>(a, o, grad_final, s) : back_typed<float>(a, o, grad_final, s);
 }
 
 rlscan_status launch_selective_scan_step(const rlscan_selective_scan_args &a, float *state, int64_t P,

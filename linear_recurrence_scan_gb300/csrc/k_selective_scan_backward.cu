@@ -18,12 +18,17 @@ namespace seq {
 namespace {
 
 constexpr int kTile = kCheckpoint;
-constexpr int kHalf = kTile / 2;
+// Tokens whose states are in registers.  Eight need fewer steps made again,
+// but their code no longer fits the instruction cache (measured, 8 x 2048 x
+// 4096 bf16 with the forward pass: 8: 2992 us, 4: 2294 us).
+constexpr int kSub = 4;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct GradArgs {
     rlscan_array3 grad_y;
-    const float *grad_final, *checkpoints;
+    const float *grad_final;  // of the final state; with chunks the messages behind them [N][chunks][D][S]
+    const float *checkpoints;
+    int64_t chunk, chunks;    // rows in chunks of tokens
     void *x, *delta, *z;
     float *initial_state;
     float *part_B, *part_C;  // [channel blocks][N T S]
@@ -46,9 +51,10 @@ struct Shape {
     static constexpr int ACT = kTile * PITCH, BC = kTile * BPITCH, MARK = THREADS * 64;
     static constexpr int STAGE = 4 * ACT + 2 * BC + MARK, STAGES = 2;
     static constexpr int F = kTile * CW;                    // floats of one array of a warp
+    static constexpr int MINE = LANES >= 4 ? 1 : 4 / LANES;  // channels whose sums a lane ends up with
     static constexpr int WIDE = 2 * kTile * SP * 8;         // B and C, each value twice
     static constexpr int RED = WARPS * kTile * 2 * SP * 4;
-    static constexpr size_t SMEM = STAGES * STAGE + WARPS * 4 * F * 4 + WIDE + RED;
+    static constexpr size_t SMEM = STAGES * STAGE + WARPS * 3 * F * 4 + WIDE + RED;
     static_assert(ACT % 16 == 0 && BC % 16 == 0 && BPITCH % 16 == 0 && PITCH % 16 == 0);
 };
 
@@ -83,19 +89,22 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
     using P = Shape<T, LANES>;
     extern __shared__ __align__(16) char smem[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, sl = lane % LANES, group = lane / LANES;
-    float *F0 = reinterpret_cast<float *>(smem + P::STAGES * P::STAGE) + warp * 4 * P::F;  // dt
-    float *F1 = F0 + P::F, *F2 = F1 + P::F, *F3 = F2 + P::F;  // dt x then sum G B; g then sum q A2; sum C h
-    char *wide = smem + P::STAGES * P::STAGE + P::WARPS * 4 * P::F * 4;
+    float *F0 = reinterpret_cast<float *>(smem + P::STAGES * P::STAGE) + warp * 3 * P::F;  // dt
+    float *F1 = F0 + P::F, *F2 = F1 + P::F;                                               // dt x, g
+    char *wide = smem + P::STAGES * P::STAGE + P::WARPS * 3 * P::F * 4;
     float *red = reinterpret_cast<float *>(wide + P::WIDE);
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
-    const int64_t blocks = (a.D + P::CH - 1) / P::CH, block = blockIdx.x % blocks, n = blockIdx.x / blocks;
+    const int64_t blocks = (a.D + P::CH - 1) / P::CH, block = blockIdx.x % blocks;
+    const int64_t chunk = blockIdx.x / blocks % g.chunks, n = blockIdx.x / blocks / g.chunks;
+    const int64_t first = chunk * g.chunk, last = first + g.chunk < a.T ? first + g.chunk : a.T;
     const int64_t c0 = block * P::CH;
     const int S = static_cast<int>(a.S), s0 = 4 * sl;
     const int width = static_cast<int>(a.D - c0 < P::CH ? a.D - c0 : P::CH);
     const int cw = warp * P::CW, c4 = cw + 4 * group;  // the warp's and the lane's first channel in the block
     const int64_t marks = (a.T + kTile - 1) / kTile;
-    const int64_t len = row_length(a.lengths, n, a.T), tiles = (len + kTile - 1) / kTile;
+    const int64_t all = row_length(a.lengths, n, a.T), len = all < last ? all : last;  // tokens first <= t < len
+    const int64_t low = first / kTile, tiles = len > first ? (len + kTile - 1) / kTile : low;  // tiles low .. tiles-1
     const bool gated = a.z.data != nullptr;
     const uint32_t gate = gated ? ~0u : 0u, soft = a.delta_softplus ? ~0u : 0u;
 
@@ -124,7 +133,7 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
                                                                  a.C.token_stride, rows, S);
     };
     auto issue = [&](int64_t tile) {  // tiles go down
-        if (tile >= 0) {
+        if (tile >= low) {
             char *st = smem + tile % P::STAGES * P::STAGE;
             const int64_t t = tile * kTile, left = len - t;
             const int rows = left < kTile ? static_cast<int>(left) : kTile;
@@ -156,7 +165,7 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
     };
 
     // padding: zeros
-    for (int64_t t = tiles * kTile; t < a.T; ++t) {
+    for (int64_t t = tiles * kTile; t < last; ++t) {
         const int64_t row = n * a.T + t;
         for (int c = threadIdx.x; c < width; c += P::THREADS) {
             static_cast<T *>(g.x)[row * a.D + c0 + c] = from_f<T>(0.f);
@@ -182,22 +191,31 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
                 const int c = c4 + 2 * p + q;
                 const bool on = c < width && s0 + i < S;
                 v[q] = on ? a.A[(c0 + c) * S + s0 + i] * kLog2e : 0.f;
-                f[q] = on && g.grad_final != nullptr ? g.grad_final[(n * a.D + c0 + c) * S + s0 + i] : 0.f;
+                f[q] = on && g.grad_final != nullptr ? g.grad_final[((n * g.chunks + chunk) * a.D + c0 + c) * S + s0 + i] : 0.f;
             }
             A2[p][i] = pair(v[0], v[1]);
             G[p][i] = pair(f[0], f[1]);
             dA[p][i] = 0ull;
         }
-    float bias[P::CPL], skip[P::CPL], dskip[P::CPL], dbias[P::CPL];
+    float bias[P::CPL];  // of the channels the lane prepares
 #pragma unroll
     for (int j = 0; j < P::CPL; ++j) {
         const int c = cw + (lane + 32 * j) % P::CW;
         bias[j] = a.delta_bias != nullptr && c < width ? a.delta_bias[c0 + c] : 0.f;
-        skip[j] = a.skip != nullptr && c < width ? a.skip[c0 + c] : 0.f;
-        dskip[j] = dbias[j] = 0.f;
+    }
+    // the channels whose outputs the lane writes: those that scatter_sums leaves it
+    const int mine = 4 * group + (LANES >= 4 ? sl / (LANES / 4) : sl * P::MINE);
+    const bool writes = LANES <= 4 || sl % (LANES / 4) == 0;
+    float obias[P::MINE], skip[P::MINE], dskip[P::MINE], dbias[P::MINE];
+#pragma unroll
+    for (int i = 0; i < P::MINE; ++i) {
+        const int c = cw + mine + i;
+        obias[i] = a.delta_bias != nullptr && c < width ? a.delta_bias[c0 + c] : 0.f;
+        skip[i] = a.skip != nullptr && c < width ? a.skip[c0 + c] : 0.f;
+        dskip[i] = dbias[i] = 0.f;
     }
 
-    for (int64_t tile = tiles - 1; tile >= 0; --tile) {
+    for (int64_t tile = tiles - 1; tile >= low; --tile) {
         const int64_t t0 = tile * kTile;
         const int left = len - t0 < kTile ? static_cast<int>(len - t0) : kTile;
         copies_wait<0>();
@@ -213,16 +231,30 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
         const T *xs = reinterpret_cast<const T *>(st) + cw, *ds = reinterpret_cast<const T *>(st + P::ACT) + cw,
                 *zs = reinterpret_cast<const T *>(st + 2 * P::ACT) + cw, *ys = reinterpret_cast<const T *>(st + 3 * P::ACT) + cw;
 #pragma unroll
-        for (int j = 0; j < P::ITEMS; ++j) {
-            const int item = lane + 32 * j, c = item % P::CW, k = item / P::CW;
-            const float xv = to_f(xs[k * P::CH + c]), zv = to_f(zs[k * P::CH + c]);
-            const float pre = to_f(ds[k * P::CH + c]) + bias[j % P::CPL];
-            const float dt = k < left ? choose(soft, softplus(pre), pre) : 0.f;
-            F0[item] = dt;
-            F1[item] = dt * xv;
-            F2[item] = to_f(ys[k * P::CH + c]) * choose(gate, zv * sigmoid(zv), 1.f);
+        for (int j = 0; j < P::ITEMS; j += 2) {  // two (channel, token) pairs at once
+            float xv[2], pre[2], zv[2], gv[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int item = lane + 32 * (j + q), at = item / P::CW * P::CH + item % P::CW;
+                xv[q] = to_f(xs[at]);
+                zv[q] = to_f(zs[at]);
+                gv[q] = to_f(ys[at]);
+                pre[q] = to_f(ds[at]) + bias[(j + q) % P::CPL];
+            }
+            const float2 sp = halves(softplus(pair(pre[0], pre[1]))), sg = halves(sigmoid(pair(zv[0], zv[1])));
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int item = lane + 32 * (j + q);
+                const float dt = item / P::CW < left ? choose(soft, q == 0 ? sp.x : sp.y, pre[q]) : 0.f;
+                F0[item] = dt;
+                F1[item] = dt * xv[q];
+                F2[item] = gv[q] * choose(gate, zv[q] * (q == 0 ? sg.x : sg.y), 1.f);
+            }
         }
         __syncthreads();
+        float sk[P::MINE], sb[P::MINE];  // the tile's share of dskip, dbias: short sums
+#pragma unroll
+        for (int i = 0; i < P::MINE; ++i) sk[i] = sb[i] = 0.f;
 
         const ulonglong2 *Bd = reinterpret_cast<const ulonglong2 *>(wide) + 2 * sl;
         const ulonglong2 *Cd = Bd + kTile * P::SP / 2;
@@ -250,6 +282,7 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
                 h[p][3] = pair(u.w, v.w);
             }
         };
+        const int64_t out = (n * a.T + t0) * a.D + c0 + cw + mine;
         auto walk = [&](auto fast) {
             constexpr bool FAST = decltype(fast)::value;
             auto step = [&](int k, const f2 (*from)[4], f2 (*to)[4]) {
@@ -267,18 +300,18 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
                     }
             };
 #pragma unroll 1
-            for (int half = 1; half >= 0; --half) {
-                f2 h[kHalf][2][4], h0[2][4];
+            for (int k0 = kTile - kSub; k0 >= 0; k0 -= kSub) {
+                f2 h[kSub][2][4], h0[2][4];
                 begin(h0);
-                if (half == 1) {
+#pragma unroll 1
+                for (int k = 0; k < k0; k += kSub) {
 #pragma unroll
-                    for (int k = 0; k < kHalf; ++k) step(k, h0, h0);
+                    for (int u = 0; u < kSub; ++u) step(k + u, h0, h0);
                 }
-                const int k0 = half * kHalf;
 #pragma unroll
-                for (int k = 0; k < kHalf; ++k) step(k0 + k, k > 0 ? h[k > 0 ? k - 1 : 0] : h0, h[k]);
+                for (int k = 0; k < kSub; ++k) step(k0 + k, k > 0 ? h[k > 0 ? k - 1 : 0] : h0, h[k]);
 #pragma unroll
-                for (int j = kHalf - 1; j >= 0; --j) {
+                for (int j = kSub - 1; j >= 0; --j) {
                     const int k = k0 + j;
                     f2 d[2], dx[2], gv[2], b[4], c[4], u[2], w[2], y[2], gB[4], gC[4];
                     row(F0, k, d);
@@ -331,17 +364,30 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
                         yv[2 * p] = a2.x;
                         yv[2 * p + 1] = a2.y;
                     }
-                    const int ch = scatter_sums<4, LANES / 2, 1>(uv, lane);
+                    scatter_sums<4, LANES / 2, 1>(uv, lane);
                     scatter_sums<4, LANES / 2, 1>(wv, lane);
                     scatter_sums<4, LANES / 2, 1>(yv, lane);
-                    // every lane of the warp has read this token's F1 and F2: the shuffles came after
-                    constexpr int MINE = LANES >= 4 ? 1 : 4 / LANES;
+                    const bool on = k < left;
 #pragma unroll
-                    for (int i = 0; i < MINE; ++i) {
-                        const int at = k * P::CW + 4 * group + ch + i;
-                        F1[at] = uv[i];
-                        F2[at] = wv[i];
-                        F3[at] = yv[i];
+                    for (int m = 0; m < P::MINE; ++m) {
+                        const int at = k * P::CH + mine + m;
+                        const float xv = to_f(xs[at]), zv = to_f(zs[at]), go = to_f(ys[at]), pre = to_f(ds[at]) + obias[m];
+                        const float dt = F0[k * P::CW + mine + m], sg = sigmoid(zv);
+                        const float gm = go * choose(gate, zv * sg, 1.f);
+                        float gd = fmaf(uv[m], xv, wv[m] * kLn2);
+                        gd = on ? gd * choose(soft, sigmoid(pre), 1.f) : 0.f;
+                        const float gx = on ? fmaf(uv[m], dt, gm * skip[m]) : 0.f;
+                        sk[m] = fmaf(gm, xv, sk[m]);
+                        sb[m] += gd;
+                        if (writes && cw + mine + m < width && t0 + k < last) {
+                            const int64_t e = out + k * a.D + m;
+                            static_cast<T *>(g.x)[e] = from_f<T>(gx);
+                            if (g.delta != nullptr) static_cast<T *>(g.delta)[e] = from_f<T>(gd);
+                            if (g.z != nullptr) {
+                                const float gz = go * fmaf(skip[m], xv, yv[m]) * sg * fmaf(zv, 1.f - sg, 1.f);
+                                static_cast<T *>(g.z)[e] = from_f<T>(on ? gz : 0.f);
+                            }
+                        }
                     }
                 }
             }
@@ -351,35 +397,10 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
         else
             walk(std::false_type());
         __syncthreads();
-
-        float sk[P::CPL], sb[P::CPL];
 #pragma unroll
-        for (int j = 0; j < P::CPL; ++j) sk[j] = sb[j] = 0.f;
-#pragma unroll
-        for (int j = 0; j < P::ITEMS; ++j) {
-            const int item = lane + 32 * j, c = item % P::CW, k = item / P::CW, m = j % P::CPL;
-            const float xv = to_f(xs[k * P::CH + c]), zv = to_f(zs[k * P::CH + c]), yv = to_f(ys[k * P::CH + c]);
-            const float pre = to_f(ds[k * P::CH + c]) + bias[m];
-            const float dt = F0[item], u = F1[item], w = F2[item] * kLn2, sum = F3[item];
-            const float sg = sigmoid(zv), gv = yv * choose(gate, zv * sg, 1.f);
-            const bool on = k < left;
-            float gd = fmaf(u, xv, w);
-            gd = on ? choose(soft, gd * sigmoid(pre), gd) : 0.f;
-            const float gx = on ? fmaf(u, dt, gv * skip[m]) : 0.f;
-            const float gz = on ? yv * fmaf(skip[m], xv, sum) * sg * fmaf(zv, 1.f - sg, 1.f) : 0.f;
-            sk[m] = fmaf(gv, xv, sk[m]);
-            sb[m] += gd;
-            if (cw + c < width && t0 + k < a.T) {
-                const int64_t e = (n * a.T + t0 + k) * a.D + c0 + cw + c;
-                static_cast<T *>(g.x)[e] = from_f<T>(gx);
-                if (g.delta != nullptr) static_cast<T *>(g.delta)[e] = from_f<T>(gd);
-                if (g.z != nullptr) static_cast<T *>(g.z)[e] = from_f<T>(gz);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < P::CPL; ++j) {
-            dskip[j] += sk[j];
-            dbias[j] += sb[j];
+        for (int m = 0; m < P::MINE; ++m) {
+            dskip[m] += sk[m];
+            dbias[m] += sb[m];
         }
         // the block's sums over its channels
         for (int i = threadIdx.x; i < 2 * kTile * P::SP; i += P::THREADS) {
@@ -402,24 +423,19 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
             for (int q = 0; q < 2; ++q) {
                 const int c = c4 + 2 * p + q;
                 if (c >= width || s0 + i >= S) continue;
-                const int64_t e = (n * a.D + c0 + c) * S + s0 + i;
-                if (g.initial_state != nullptr) g.initial_state[e] = q == 0 ? gi.x : gi.y;
-                if (g.part_A != nullptr) g.part_A[e] = q == 0 ? ga.x : ga.y;
+                const int64_t e = (c0 + c) * S + s0 + i;
+                if (g.initial_state != nullptr && chunk == 0) g.initial_state[n * a.D * S + e] = q == 0 ? gi.x : gi.y;
+                if (g.part_A != nullptr) g.part_A[(n * g.chunks + chunk) * a.D * S + e] = q == 0 ? ga.x : ga.y;
             }
         }
-    if (g.part_d != nullptr) {
+    if (g.part_d != nullptr && writes) {
 #pragma unroll
-        for (int j = 0; j < P::CPL; ++j) {
-#pragma unroll
-            for (int m = 16; m >= P::CW; m /= 2) {  // lanes that share a channel
-                dskip[j] += __shfl_xor_sync(0xffffffffu, dskip[j], m);
-                dbias[j] += __shfl_xor_sync(0xffffffffu, dbias[j], m);
-            }
-            const int c = cw + (lane + 32 * j) % P::CW;
-            if (c < width && lane < P::CW) {
-                g.part_d[(n * 2 + 0) * a.D + c0 + c] = dskip[j];
-                g.part_d[(n * 2 + 1) * a.D + c0 + c] = dbias[j];
-            }
+        for (int m = 0; m < P::MINE; ++m) {
+            const int c = cw + mine + m;
+            if (c >= width) break;
+            float *part = g.part_d + (n * g.chunks + chunk) * 2 * a.D + c0 + c;
+            part[0] = dskip[m];
+            part[a.D] = dbias[m];
         }
     }
 }
@@ -457,29 +473,49 @@ __global__ void __launch_bounds__(32 * kSlices) sums_kernel(const __grid_constan
         static_cast<float *>(job.out)[i] = acc;
 }
 
-struct Layout {
-    int64_t blocks;
-    size_t B, C, A, d, bytes;
-};
-
 int grad_lanes(int64_t S)
 {
     const int lanes = state_lanes(S);
     return lanes < 2 ? 2 : lanes;
 }
 
+// How a call is laid out, and its workspace.  Rows are split into chunks of
+// tokens, whose messages take a pass of their own (about a quarter of the
+// work), while there are less than 1.5 blocks an SM without.
+struct Layout {
+    int64_t blocks, chunk, chunks;
+    size_t B, C, A, d, states, spans, cuts, bytes;
+};
+
 Layout layout(const rlscan_selective_scan_args &a)
 {
     Layout l;
     const int lanes = grad_lanes(a.S);
+    const int64_t sms = sm_count() > 0 ? sm_count() : 152;
     l.blocks = ceil_div(a.D, (lanes == 2 ? 2 : 4) * 4 * (32 / lanes));
-    const size_t bc = sizeof(float) * static_cast<size_t>(l.blocks) * a.N * a.T * a.S;
-    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    l.B = 0;
-    l.C = up(bc);
-    l.A = l.C + up(bc);
-    l.d = l.A + up(sizeof(float) * static_cast<size_t>(a.N) * a.D * a.S);
-    l.bytes = l.d + up(sizeof(float) * 2 * static_cast<size_t>(a.N) * a.D);
+    l.chunk = ceil_div(a.T > 0 ? a.T : 1, kTile) * kTile;
+    if (a.N > 0 && a.T > 128 && 2 * a.N * l.blocks < 3 * sms) {
+        const int64_t want = ceil_div(4 * sms, a.N * l.blocks);
+        const int64_t chunk = ceil_div(ceil_div(a.T, want), kTile) * kTile;
+        l.chunk = chunk < 64 ? 64 : chunk;
+    }
+    l.chunks = ceil_div(a.T > 0 ? a.T : 1, l.chunk);
+    const size_t each = static_cast<size_t>(a.N) * l.chunks, F = sizeof(float);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    l.B = take(F * l.blocks * a.N * a.T * a.S);
+    l.C = take(F * l.blocks * a.N * a.T * a.S);
+    l.A = take(F * each * a.D * a.S);
+    l.d = take(F * each * 2 * a.D);
+    const bool split = l.chunks > 1;
+    l.states = take(split ? F * each * a.D * a.S : 0);
+    l.spans = take(split ? F * each * a.D : 0);
+    l.cuts = take(split ? each : 0);
+    l.bytes = at;
     return l;
 }
 
@@ -491,7 +527,7 @@ rlscan_status launch_shape(const rlscan_selective_scan_args &a, const GradArgs &
     static const bool sized =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
     if (!sized) return RLSCAN_ERR_CUDA;
-    return launch_overlapped(kernel, a.N * ceil_div(a.D, P::CH), P::THREADS, P::SMEM, s, a, g);
+    return launch_overlapped(kernel, a.N * ceil_div(a.D, P::CH) * g.chunks, P::THREADS, P::SMEM, s, a, g);
 }
 
 template <class T>
@@ -541,7 +577,17 @@ rlscan_status launch_selective_scan_backward(const rlscan_selective_scan_args &a
     k.part_A = g.A != nullptr ? reinterpret_cast<float *>(w + l.A) : nullptr;
     k.part_d = g.skip != nullptr || g.delta_bias != nullptr ? reinterpret_cast<float *>(w + l.d) : nullptr;
     const bool b16 = a.dtype == RLSCAN_BF16;
+    k.chunk = l.chunk;
+    k.chunks = l.chunks;
     if (a.N > 0) {
+        if (l.chunks > 1) {
+            float *states = reinterpret_cast<float *>(w + l.states);
+            const rlscan_status st =
+                launch_back_states(a, grad_y, grad_final_state, l.chunk, l.chunks, states,
+                                   reinterpret_cast<float *>(w + l.spans), reinterpret_cast<uint8_t *>(w + l.cuts), s);
+            if (st != RLSCAN_OK) return st;
+            k.grad_final = states;
+        }
         const rlscan_status st = b16 ? launch_typed<bf16>(a, k, s) : launch_typed<float>(a, k, s);
         if (st != RLSCAN_OK) return st;
     }
@@ -549,9 +595,9 @@ rlscan_status launch_selective_scan_backward(const rlscan_selective_scan_args &a
     SumJobs jobs;
     if (g.B != nullptr) jobs.add(k.part_B, l.blocks, bc, bc, g.B, b16);
     if (g.C != nullptr) jobs.add(k.part_C, l.blocks, bc, bc, g.C, b16);
-    if (g.A != nullptr) jobs.add(k.part_A, a.N, a.D * a.S, a.D * a.S, g.A, false);
-    if (g.skip != nullptr) jobs.add(k.part_d, a.N, 2 * a.D, a.D, g.skip, false);
-    if (g.delta_bias != nullptr) jobs.add(k.part_d + a.D, a.N, 2 * a.D, a.D, g.delta_bias, false);
+    if (g.A != nullptr) jobs.add(k.part_A, a.N * l.chunks, a.D * a.S, a.D * a.S, g.A, false);
+    if (g.skip != nullptr) jobs.add(k.part_d, a.N * l.chunks, 2 * a.D, a.D, g.skip, false);
+    if (g.delta_bias != nullptr) jobs.add(k.part_d + a.D, a.N * l.chunks, 2 * a.D, a.D, g.delta_bias, false);
     return launch_sums(jobs, s);
 }
 

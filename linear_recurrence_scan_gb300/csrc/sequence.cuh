@@ -74,6 +74,79 @@ __device__ __forceinline__ float softplus(float v)
     return fmaf(2.f * s, p, fmaxf(v, 0.f));
 }
 
+// V neighbouring values as they are stored, in whole registers: a load into
+// them can stay in flight until a value is looked at.
+template <class T, int V>
+struct Words {
+    static constexpr int BYTES = V * static_cast<int>(sizeof(T)), N = (BYTES + 3) / 4;
+    uint32_t w[N];
+    __device__ __forceinline__ float operator[](int i) const
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        return __uint_as_float(i % 2 == 0 ? w[i / 2] << 16 : w[i / 2] & 0xffff0000u);
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ void load(const T *p)  // aligned to BYTES (or 16)
+    {
+        if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const uint4 q = reinterpret_cast<const uint4 *>(p)[i / 4];
+                w[i] = q.x;
+                w[i + 1] = q.y;
+                w[i + 2] = q.z;
+                w[i + 3] = q.w;
+            }
+        } else if constexpr (BYTES == 8) {
+            const uint2 q = *reinterpret_cast<const uint2 *>(p);
+            w[0] = q.x;
+            w[1] = q.y;
+        } else if constexpr (BYTES == 4) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            static_assert(BYTES == 2);
+            asm volatile("ld.u16 %0, [%1];" : "=r"(w[0]) : "l"(p) : "memory");
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const
+    {
+        if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+                reinterpret_cast<uint4 *>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        } else if constexpr (BYTES == 8) {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        } else if constexpr (BYTES == 4) {
+            *reinterpret_cast<uint32_t *>(p) = w[0];
+        } else {
+            *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(w[0]);
+        }
+    }
+    // rounds values 2 i and 2 i + 1 (one value: 2 i alone) into their words
+    __device__ __forceinline__ void set(int i, float lo, float hi)
+    {
+        if constexpr (sizeof(T) == 4) {
+            w[2 * i] = __float_as_uint(lo);
+            if (2 * i + 1 < V) w[2 * i + 1 < N ? 2 * i + 1 : 0] = __float_as_uint(hi);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+};
+
+// a byte in a whole register
+__device__ __forceinline__ uint32_t load_byte(const uint8_t *p)
+{
+    uint32_t v;
+    asm volatile("ld.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // `a` where the mask is all ones, `b` where it is 0.  Bit by bit: a ternary
 // around an expensive `a` becomes a branch, which would keep the work of
 // neighbouring tokens from overlapping.
@@ -284,6 +357,11 @@ inline int state_lanes(int64_t S)
 rlscan_status launch_selective_scan(const rlscan_selective_scan_args &a, void *y, float *final_state,
                                     float *checkpoints, void *ws, cudaStream_t s);
 size_t selective_scan_workspace(const rlscan_selective_scan_args &a);
+// The gradient's message behind each chunk of tokens (states [N][chunks][D][S]);
+// spans [N][chunks][D] and cuts [N][chunks] are scratch.
+rlscan_status launch_back_states(const rlscan_selective_scan_args &a, const rlscan_array3 &grad_y, const float *grad_final,
+                                 int64_t chunk, int64_t chunks, float *states, float *spans, uint8_t *cuts,
+                                 cudaStream_t s);
 rlscan_status launch_selective_scan_step(const rlscan_selective_scan_args &a, float *state, int64_t P,
                                          const int32_t *slots, void *y, cudaStream_t s);
 rlscan_status launch_selective_scan_backward(const rlscan_selective_scan_args &a, const rlscan_array3 &grad_y,
