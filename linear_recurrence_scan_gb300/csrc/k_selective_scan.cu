@@ -30,11 +30,16 @@ struct ScanOut {
     rlscan_array3 grad_y;  // BACK
 };
 
-template <class T, int SPT, int LANES>
+template <class T, int SPT, int LANES, bool SPLIT>
 struct Shape {
     static constexpr int CH = kThreads / LANES;     // channels of a block
     static constexpr int SP = SPT * LANES;          // states, padded
-    static constexpr int PER = kTile / LANES;       // tokens of a tile that a lane prepares: sl, sl + LANES, ...
+    // Tokens taken at once, and registers: calls whose rows are whole have few
+    // warps and live on the overlap of 16 tokens; those in chunks have many
+    // (measured, unsplit 8 x 4096 x 4096 ragged: 16 tokens 652 us, 8: 695;
+    // in chunks, 2 x 16384 x 2048: 16 tokens 570 us, 8 with four blocks 525).
+    static constexpr int MOST = SPLIT ? 8 : 16, WALK = LANES > MOST ? LANES : MOST;
+    static constexpr int PER = WALK / LANES;              // of them a lane prepares sl, sl + LANES, ...
     // rows of the lanes that share a channel lie in different banks
     static constexpr int ROWB = 32 / LANES * static_cast<int>(sizeof(T));
     static constexpr int PITCH = CH * static_cast<int>(sizeof(T)) + (ROWB > 16 ? ROWB : 16);
@@ -46,7 +51,7 @@ struct Shape {
     static constexpr bool CONVERT = sizeof(T) == 2;
     static constexpr int WIDE = CONVERT ? 2 * kTile * SP * 4 : 0;  // B and C in float32
     static constexpr size_t SMEM = STAGES * STAGE + 2 * WIDE;
-    static constexpr int BLOCKS = SPT == 16 ? 2 : 3;  // registers for 16 tokens' work at once
+    static constexpr int BLOCKS = SPLIT ? (SPT == 16 ? 4 : 4) : (SPT == 16 ? 2 : 3);
     static_assert(ACT % 16 == 0 && BC % 16 == 0);
 };
 
@@ -104,11 +109,11 @@ __device__ __forceinline__ void store_states(float *p, const f2 *h, int s0, int 
 // and C in B's.
 enum Mode { FULL_SCAN, PART, BACK };
 
-template <class T, int SPT, int LANES, int MODE>
-__global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
+template <class T, int SPT, int LANES, int MODE, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES, SPLIT>::BLOCKS)
     scan_kernel(const __grid_constant__ rlscan_selective_scan_args a, const __grid_constant__ ScanOut o)
 {
-    using P = Shape<T, SPT, LANES>;
+    using P = Shape<T, SPT, LANES, SPLIT>;
     constexpr bool FULL = MODE == FULL_SCAN;
     extern __shared__ __align__(16) char smem[];
     float *wide = reinterpret_cast<float *>(smem + P::STAGES * P::STAGE);
@@ -227,13 +232,13 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
         constexpr int BROW = P::CONVERT ? P::SP : P::BPITCH / 4;
         T *yt = y + t0 * a.D;
         // FAST: 16 tokens of one episode, without a branch, so that the tokens' work overlaps
-        auto walk = [&](auto fast) {
+        auto walk = [&](auto fast, int w0) {
             constexpr bool FAST = decltype(fast)::value;
-            float xv[P::PER], dt[P::PER], dtx[P::PER], part[kTile];
+            float xv[P::PER], dt[P::PER], dtx[P::PER], part[P::WALK];
 #pragma unroll
             for (int p = 0; p < P::PER; ++p) {
-                xv[p] = to_f(xs[(p * LANES + sl) * ROW]);
-                dt[p] = to_f(ds[(p * LANES + sl) * ROW]) + bias;
+                xv[p] = to_f(xs[(w0 + p * LANES + sl) * ROW]);
+                dt[p] = to_f(ds[(w0 + p * LANES + sl) * ROW]) + bias;
             }
             if constexpr (P::PER == 1) {
                 dt[0] = choose(soft, softplus(dt[0]), dt[0]);
@@ -247,9 +252,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
             }
 #pragma unroll
             for (int p = 0; p < P::PER; ++p) {
-                if (!FAST) dt[p] = p * LANES + sl < left ? dt[p] : 0.f;  // past the last token the state stays
+                if (!FAST) dt[p] = w0 + p * LANES + sl < left ? dt[p] : 0.f;  // past the last token the state stays
                 if constexpr (MODE == BACK) {
-                    const float zv = to_f(zs[(p * LANES + sl) * ROW]);
+                    const float zv = to_f(zs[(w0 + p * LANES + sl) * ROW]);
                     dtx[p] = xv[p] * choose(gate, zv * sigmoid(zv), 1.f);
                 } else {
                     dtx[p] = dt[p] * xv[p];
@@ -257,12 +262,12 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
                 if (!FULL) span += dt[p];
             }
 #pragma unroll
-            for (int kk = 0; kk < kTile; ++kk) {
-                const int k = MODE == BACK ? kTile - 1 - kk : kk;
-                float dj = dt[k / LANES], xj = dtx[k / LANES];
+            for (int kk = 0; kk < P::WALK; ++kk) {
+                const int j = MODE == BACK ? P::WALK - 1 - kk : kk, k = w0 + j;
+                float dj = dt[j / LANES], xj = dtx[j / LANES];
                 if constexpr (LANES > 1) {
-                    dj = __shfl_sync(0xffffffffu, dj, k % LANES, LANES);
-                    xj = __shfl_sync(0xffffffffu, xj, k % LANES, LANES);
+                    dj = __shfl_sync(0xffffffffu, dj, j % LANES, LANES);
+                    xj = __shfl_sync(0xffffffffu, xj, j % LANES, LANES);
                 }
                 if (!FAST && MODE != BACK && (starts >> k & 1u) != 0) {
 #pragma unroll
@@ -278,8 +283,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
                         h[2 * i] = mul2(e0, fma2(xp, b.x, h[2 * i]));
                         h[2 * i + 1] = mul2(e1, fma2(xp, b.y, h[2 * i + 1]));
                     } else {
-                        h[2 * i] = fma2(e0, h[2 * i], mul2(xp, b.x));
-                        h[2 * i + 1] = fma2(e1, h[2 * i + 1], mul2(xp, b.y));
+                        // xp is the same register for all states: one new operand less than e h + (x B)
+                        h[2 * i] = fma2(xp, b.x, mul2(e0, h[2 * i]));
+                        h[2 * i + 1] = fma2(xp, b.y, mul2(e1, h[2 * i + 1]));
                     }
                     if (FULL) {
                         const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(Cw + k * BROW + 4 * i);
@@ -293,13 +299,13 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
                 }
                 if (FULL) {
                     const float2 v = halves(add2(acc[0], acc[1]));
-                    part[k] = v.x + v.y;
+                    part[j] = v.x + v.y;
                 }
             }
             if constexpr (FULL) {
 #pragma unroll
                 for (int p = 0; p < P::PER; ++p) {
-                    const int k = p * LANES + sl;
+                    const int k = w0 + p * LANES + sl;
                     float v = fmaf(skip, xv[p], scatter_sum<LANES>(part + p * LANES, sl));
                     const float zv = to_f(zs[k * ROW]);
                     v *= choose(gate, zv * sigmoid(zv), 1.f);
@@ -311,10 +317,14 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES>::BLOCKS)
                 }
             }
         };
-        if (starts == 0 && left == kTile)
-            walk(std::true_type());
-        else
-            walk(std::false_type());
+#pragma unroll 1
+        for (int w = 0; w < kTile; w += P::WALK) {
+            const int w0 = MODE == BACK ? kTile - P::WALK - w : w;
+            if (starts == 0 && left == kTile)
+                walk(std::true_type(), w0);
+            else
+                walk(std::false_type(), w0);
+        }
     }
     if (!FULL) {
         if constexpr (LANES > 1) {
@@ -379,24 +389,26 @@ __global__ void __launch_bounds__(256) chunk_kernel(const __grid_constant__ rlsc
     }
 }
 
+template <class T, int SPT, int LANES, int MODE, bool SPLIT>
+rlscan_status launch_mode(const rlscan_selective_scan_args &a, const ScanOut &o, cudaStream_t s)
+{
+    using P = Shape<T, SPT, LANES, SPLIT>;
+    auto kernel = scan_kernel<T, SPT, LANES, MODE, SPLIT>;
+    static const bool sized =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
+    if (!sized) return RLSCAN_ERR_CUDA;
+    return launch_overlapped(kernel, a.N * ceil_div(a.D, P::CH) * o.chunks, kThreads, P::SMEM, s, a, o);
+}
+
 template <class T, int SPT, int LANES>
 rlscan_status launch_shape(const rlscan_selective_scan_args &a, const ScanOut &o, cudaStream_t s)
 {
-    using P = Shape<T, SPT, LANES>;
-    const int64_t grid = a.N * ceil_div(a.D, P::CH) * o.chunks;
-    auto full = scan_kernel<T, SPT, LANES, FULL_SCAN>;
-    auto part = scan_kernel<T, SPT, LANES, PART>;
-    static const bool sized =
-        cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess &&
-        cudaFuncSetAttribute(part, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
-    if (!sized) return RLSCAN_ERR_CUDA;
-    if (o.chunks > 1) {
-        rlscan_status st = launch_overlapped(part, grid, kThreads, P::SMEM, s, a, o);
-        if (st == RLSCAN_OK)
-            st = launch_overlapped(chunk_kernel<false>, ceil_div(a.N * a.D * a.S, 256), 256, 0, s, a, o, a.initial_state);
-        if (st != RLSCAN_OK) return st;
-    }
-    return launch_overlapped(full, grid, kThreads, P::SMEM, s, a, o);
+    if (o.chunks == 1) return launch_mode<T, SPT, LANES, FULL_SCAN, false>(a, o, s);
+    rlscan_status st = launch_mode<T, SPT, LANES, PART, true>(a, o, s);
+    if (st == RLSCAN_OK)
+        st = launch_overlapped(chunk_kernel<false>, ceil_div(a.N * a.D * a.S, 256), 256, 0, s, a, o, a.initial_state);
+    if (st != RLSCAN_OK) return st;
+    return launch_mode<T, SPT, LANES, FULL_SCAN, true>(a, o, s);
 }
 
 // How a call is laid out: states per lane, and chunks of each row.
@@ -465,13 +477,7 @@ rlscan_status launch_typed(const Plan &p, const rlscan_selective_scan_args &a, S
 template <class T, int SPT, int LANES>
 rlscan_status launch_back(const rlscan_selective_scan_args &a, const ScanOut &o, const float *grad_final, cudaStream_t s)
 {
-    using P = Shape<T, SPT, LANES>;
-    auto back = scan_kernel<T, SPT, LANES, BACK>;
-    static const bool sized =
-        cudaFuncSetAttribute(back, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
-    if (!sized) return RLSCAN_ERR_CUDA;
-    const rlscan_status st =
-        launch_overlapped(back, a.N * ceil_div(a.D, P::CH) * o.chunks, kThreads, P::SMEM, s, a, o);
+    const rlscan_status st = launch_mode<T, SPT, LANES, BACK, true>(a, o, s);
     if (st != RLSCAN_OK) return st;
     return launch_overlapped(chunk_kernel<true>, ceil_div(a.N * a.D * a.S, 256), 256, 0, s, a, o, grad_final);
 }

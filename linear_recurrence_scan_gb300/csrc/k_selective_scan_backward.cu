@@ -54,7 +54,8 @@ struct Shape {
     static constexpr int MINE = LANES >= 4 ? 1 : 4 / LANES;  // channels whose sums a lane ends up with
     static constexpr int WIDE = 2 * kTile * SP * 8;         // B and C, each value twice
     static constexpr int RED = WARPS * kTile * 2 * SP * 4;
-    static constexpr size_t SMEM = STAGES * STAGE + WARPS * 3 * F * 4 + WIDE + RED;
+    static constexpr int KEEP = (kTile / kSub - 2) * MARK;   // states between the sub-tiles
+    static constexpr size_t SMEM = STAGES * STAGE + WARPS * 3 * F * 4 + WIDE + RED + KEEP + MARK;
     static_assert(ACT % 16 == 0 && BC % 16 == 0 && BPITCH % 16 == 0 && PITCH % 16 == 0);
 };
 
@@ -93,6 +94,8 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
     float *F1 = F0 + P::F, *F2 = F1 + P::F;                                               // dt x, g
     char *wide = smem + P::STAGES * P::STAGE + P::WARPS * 3 * P::F * 4;
     float *red = reinterpret_cast<float *>(wide + P::WIDE);
+    char *keep = wide + P::WIDE + P::RED + threadIdx.x * 16;  // the lane's own, as the checkpoint's
+    char *sumA = keep + P::KEEP;  // dA: a tile's sum is in registers, the sum over tiles here (two short sums, not one long)
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
     const int64_t blocks = (a.D + P::CH - 1) / P::CH, block = blockIdx.x % blocks;
@@ -197,6 +200,19 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
             G[p][i] = pair(f[0], f[1]);
             dA[p][i] = 0ull;
         }
+    auto add_dA = [&](bool first_tile) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ulonglong2 *at = reinterpret_cast<ulonglong2 *>(sumA + (2 * p + h) * P::THREADS * 16);
+                ulonglong2 v = make_ulonglong2(dA[p][2 * h], dA[p][2 * h + 1]);
+                if (!first_tile) v = make_ulonglong2(add2(v.x, at->x), add2(v.y, at->y));
+                *at = v;
+                dA[p][2 * h] = dA[p][2 * h + 1] = 0ull;
+            }
+    };
+    add_dA(true);
     float bias[P::CPL];  // of the channels the lane prepares
 #pragma unroll
     for (int j = 0; j < P::CPL; ++j) {
@@ -256,69 +272,82 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
 #pragma unroll
         for (int i = 0; i < P::MINE; ++i) sk[i] = sb[i] = 0.f;
 
-        const ulonglong2 *Bd = reinterpret_cast<const ulonglong2 *>(wide) + 2 * sl;
-        const ulonglong2 *Cd = Bd + kTile * P::SP / 2;
+        auto off = [&](const void *p) { return static_cast<uint32_t>(static_cast<const char *>(p) - smem); };
+        const uint32_t oB = off(wide) + 32 * sl, oC = oB + kTile * P::SP * 8;
+        const uint32_t o0 = off(F0) + 16 * group, o1 = o0 + P::F * 4, o2 = o1 + P::F * 4;
         const char *own = st + 4 * P::ACT + 2 * P::BC + threadIdx.x * 16;
-        auto row = [&](const float *f, int k, f2 *v) {  // four channels of a token
-            const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(f + k * P::CW + 4 * group);
-            v[0] = r.x;
-            v[1] = r.y;
+        auto row = [&](uint32_t f, int k, f2 *v) { load_pairs(v[0], v[1], f + k * (P::CW * 4)); };  // a token's four channels
+        auto states = [&](uint32_t w, int k, f2 *v) {  // a token's four states, each twice
+            load_pairs(v[0], v[1], w + k * (P::SP * 8));
+            load_pairs(v[2], v[3], w + k * (P::SP * 8) + 16);
         };
-        auto states = [&](const ulonglong2 *w, int k, f2 *v) {  // four states of a token, each twice
-            const ulonglong2 lo = w[k * (P::SP / 2)], hi = w[k * (P::SP / 2) + 1];
-            v[0] = lo.x;
-            v[1] = lo.y;
-            v[2] = hi.x;
-            v[3] = hi.y;
-        };
-        auto begin = [&](f2 (*h)[4]) {
+        auto begin = [&](f2 (*h)[4], const char *from) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const float4 u = *reinterpret_cast<const float4 *>(own + 2 * p * P::THREADS * 16);
-                const float4 v = *reinterpret_cast<const float4 *>(own + (2 * p + 1) * P::THREADS * 16);
+                const float4 u = *reinterpret_cast<const float4 *>(from + 2 * p * P::THREADS * 16);
+                const float4 v = *reinterpret_cast<const float4 *>(from + (2 * p + 1) * P::THREADS * 16);
                 h[p][0] = pair(u.x, v.x);
                 h[p][1] = pair(u.y, v.y);
                 h[p][2] = pair(u.z, v.z);
                 h[p][3] = pair(u.w, v.w);
             }
         };
+        auto save = [&](const f2 (*h)[4], char *to) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const float2 a0 = halves(h[p][0]), a1 = halves(h[p][1]), a2 = halves(h[p][2]), a3 = halves(h[p][3]);
+                *reinterpret_cast<float4 *>(to + 2 * p * P::THREADS * 16) = make_float4(a0.x, a1.x, a2.x, a3.x);
+                *reinterpret_cast<float4 *>(to + (2 * p + 1) * P::THREADS * 16) = make_float4(a0.y, a1.y, a2.y, a3.y);
+            }
+        };
+        const uint32_t oX = off(xs) + mine * static_cast<uint32_t>(sizeof(T));  // the lane's channel in the raw rows
         const int64_t out = (n * a.T + t0) * a.D + c0 + cw + mine;
         auto walk = [&](auto fast) {
             constexpr bool FAST = decltype(fast)::value;
-            auto step = [&](int k, const f2 (*from)[4], f2 (*to)[4]) {
+            auto step = [&](uint32_t base, int k, const f2 (*from)[4], f2 (*to)[4]) {
                 f2 d[2], dx[2], b[4];
-                row(F0, k, d);
-                row(F1, k, dx);
-                states(Bd, k, b);
+                row(base + o0, k, d);
+                row(base + o1, k, dx);
+                states(base + oB, k, b);
                 const bool cut = !FAST && (starts >> k & 1u) != 0;
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const f2 before = cut ? 0ull : from[p][i];
-                        to[p][i] = fma2(exp2_fast(mul2(d[p], A2[p][i])), before, mul2(dx[p], b[i]));
+                        to[p][i] = fma2(dx[p], b[i], mul2(exp2_fast(mul2(d[p], A2[p][i])), before));
                     }
             };
+            // the states at each sub-tile's start: the first is the checkpoint,
+            // the last stays in registers, those between go to the lane's own place
+            f2 h0[2][4];
+            begin(h0, own);
+#pragma unroll 1
+            for (int k = 0; k < kTile - kSub; k += kSub) {
+                if (k > 0) save(h0, keep + (k / kSub - 1) * P::MARK);
+                const uint32_t base = anchor(smem);
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) step(base, k + u, h0, h0);
+            }
 #pragma unroll 1
             for (int k0 = kTile - kSub; k0 >= 0; k0 -= kSub) {
-                f2 h[kSub][2][4], h0[2][4];
-                begin(h0);
-#pragma unroll 1
-                for (int k = 0; k < k0; k += kSub) {
+                f2 h[kSub][2][4];
+                if (k0 < kTile - kSub) begin(h0, k0 > 0 ? keep + (k0 / kSub - 1) * P::MARK : own);
+                uint32_t base = anchor(smem);
 #pragma unroll
-                    for (int u = 0; u < kSub; ++u) step(k + u, h0, h0);
-                }
-#pragma unroll
-                for (int k = 0; k < kSub; ++k) step(k0 + k, k > 0 ? h[k > 0 ? k - 1 : 0] : h0, h[k]);
+                for (int k = 0; k < kSub; ++k) step(base, k0 + k, k > 0 ? h[k > 0 ? k - 1 : 0] : h0, h[k]);
+                // a new anchor for each part: its loads are its own, not registers held since the part before
+                base = anchor(smem);
+                constexpr int KEPT = P::GROUPS >= 8 ? 1 : 8 / P::GROUPS;
 #pragma unroll
                 for (int j = kSub - 1; j >= 0; --j) {
                     const int k = k0 + j;
                     f2 d[2], dx[2], gv[2], b[4], c[4], u[2], w[2], y[2], gB[4], gC[4];
-                    row(F0, k, d);
-                    row(F1, k, dx);
-                    row(F2, k, gv);
-                    states(Bd, k, b);
-                    states(Cd, k, c);
+                    row(base + o0, k, d);
+                    row(base + o1, k, dx);
+                    row(base + o2, k, gv);
+                    states(base + oB, k, b);
+                    states(base + oC, k, c);
                     const bool cut = !FAST && (starts >> k & 1u) != 0;
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
@@ -346,10 +375,10 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
                         bc[i] = vb.x + vb.y;
                         bc[4 + i] = vc.x + vc.y;
                     }
+                    base = anchor(smem);  // the next token's loads may start here, no sooner
                     const int kept = scatter_sums<8, 16, LANES>(bc, lane);
-                    constexpr int KEEP = P::GROUPS >= 8 ? 1 : 8 / P::GROUPS;
 #pragma unroll
-                    for (int i = 0; i < KEEP; ++i) {
+                    for (int i = 0; i < KEPT; ++i) {
                         const int v = kept + i;
                         red[((warp * kTile + k) * 2 + v / 4) * P::SP + s0 + v % 4] = bc[i];
                     }
@@ -367,36 +396,35 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
                     scatter_sums<4, LANES / 2, 1>(uv, lane);
                     scatter_sums<4, LANES / 2, 1>(wv, lane);
                     scatter_sums<4, LANES / 2, 1>(yv, lane);
-                    const bool on = k < left;
+                    const bool on = FAST || k < left;
 #pragma unroll
                     for (int m = 0; m < P::MINE; ++m) {
-                        const int at = k * P::CH + mine + m;
-                        const float xv = to_f(xs[at]), zv = to_f(zs[at]), go = to_f(ys[at]), pre = to_f(ds[at]) + obias[m];
-                        const float dt = F0[k * P::CW + mine + m], sg = sigmoid(zv);
+                        const uint32_t raw = base + oX + (k * P::CH + m) * static_cast<uint32_t>(sizeof(T));
+                        const float xv = load_value(raw, T()), pre = load_value(raw + P::ACT, T()) + obias[m];
+                        const float zv = load_value(raw + 2 * P::ACT, T()), go = load_value(raw + 3 * P::ACT, T());
+                        const float dt = load_value(base + off(F0) + (k * P::CW + mine + m) * 4, 0.f), sg = sigmoid(zv);
                         const float gm = go * choose(gate, zv * sg, 1.f);
                         float gd = fmaf(uv[m], xv, wv[m] * kLn2);
                         gd = on ? gd * choose(soft, sigmoid(pre), 1.f) : 0.f;
                         const float gx = on ? fmaf(uv[m], dt, gm * skip[m]) : 0.f;
+                        const float gz = on ? go * fmaf(skip[m], xv, yv[m]) * sg * fmaf(zv, 1.f - sg, 1.f) : 0.f;
                         sk[m] = fmaf(gm, xv, sk[m]);
                         sb[m] += gd;
-                        if (writes && cw + mine + m < width && t0 + k < last) {
-                            const int64_t e = out + k * a.D + m;
-                            static_cast<T *>(g.x)[e] = from_f<T>(gx);
-                            if (g.delta != nullptr) static_cast<T *>(g.delta)[e] = from_f<T>(gd);
-                            if (g.z != nullptr) {
-                                const float gz = go * fmaf(skip[m], xv, yv[m]) * sg * fmaf(zv, 1.f - sg, 1.f);
-                                static_cast<T *>(g.z)[e] = from_f<T>(on ? gz : 0.f);
-                            }
-                        }
+                        const bool st = writes && cw + mine + m < width && (FAST || t0 + k < last);
+                        const int64_t e = out + k * a.D + m;
+                        if (st) static_cast<T *>(g.x)[e] = from_f<T>(gx);
+                        if (st && g.delta != nullptr) static_cast<T *>(g.delta)[e] = from_f<T>(gd);
+                        if (st && g.z != nullptr) static_cast<T *>(g.z)[e] = from_f<T>(gz);
                     }
                 }
             }
         };
-        if (starts == 0)
+        if (starts == 0 && left == kTile)
             walk(std::true_type());
         else
             walk(std::false_type());
         __syncthreads();
+        add_dA(false);
 #pragma unroll
         for (int m = 0; m < P::MINE; ++m) {
             dskip[m] += sk[m];
@@ -418,7 +446,8 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
     for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 gi = halves(G[p][i]), ga = halves(dA[p][i]);
+            const float2 gi = halves(G[p][i]);
+            const float2 ga = halves(reinterpret_cast<const f2 *>(sumA + (2 * p + i / 2) * P::THREADS * 16)[i % 2]);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int c = c4 + 2 * p + q;

@@ -230,6 +230,34 @@ __device__ __forceinline__ f2 softplus(f2 v)
     return fma2(add2(s, s), p, pair(fmaxf(h.x, 0.f), fmaxf(h.y, 0.f)));
 }
 
+// ---- loads from shared memory that stores do not hold up --------------------
+// To the compiler these depend on their address alone, so it may move them
+// over stores, which plain loads of possibly the same memory have to wait
+// for.  `anchor` gives an address that it takes for new: loads through it
+// stay behind the anchor, and it stays behind the barrier in front of it.
+__device__ __forceinline__ uint32_t anchor(const void *p)
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %1;" : "=r"(r) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))) : "memory");
+    return r;
+}
+__device__ __forceinline__ void load_pairs(f2 &a, f2 &b, uint32_t at)
+{
+    asm("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(at));
+}
+__device__ __forceinline__ float load_value(uint32_t at, float)
+{
+    float v;
+    asm("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ float load_value(uint32_t at, bf16)
+{
+    uint32_t v;
+    asm("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(at));
+    return __uint_as_float(v << 16);
+}
+
 // ---- asynchronous copies into shared memory ---------------------------------
 // `bytes` (0..16, rest zero-filled) of a 16-byte chunk, or 4 bytes
 __device__ __forceinline__ void copy16(void *dst, const void *src, int bytes)
