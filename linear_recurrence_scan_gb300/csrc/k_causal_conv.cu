@@ -136,8 +136,9 @@ __global__ void __launch_bounds__(kThreads)
 {
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
-    const int64_t vecs = a.D / V, i0 = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
-    const int64_t d = i0 % vecs * V, run = i0 / vecs % o.runs, n = i0 / vecs / o.runs;
+    const Division at = divide(blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x, a.D / V);
+    const Division at_row = divide(at.q, o.runs);
+    const int64_t d = at.r * V, run = at_row.r, n = at_row.q;
     if (n >= a.N) return;
     const T *x = static_cast<const T *>(a.x.data) + n * a.x.row_stride + d;
     T *y = static_cast<T *>(o.y) + n * a.T * a.D + d;
@@ -213,8 +214,8 @@ __global__ void __launch_bounds__(kThreads)
 {
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
-    const int64_t vecs = a.D / V, i0 = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
-    const int64_t n = i0 / vecs, d = i0 % vecs * V;
+    const Division at = divide(blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x, a.D / V);
+    const int64_t n = at.q, d = at.r * V;
     if (n >= a.N) return;
     const int64_t slot = slots != nullptr ? slots[n] : n;
     Words<T, V> xv;
@@ -263,8 +264,9 @@ __global__ void __launch_bounds__(kThreads)
     constexpr int H = kPairs<V>;
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
-    const int64_t vecs = a.D / V, i0 = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
-    const int64_t d = i0 % vecs * V, run = i0 / vecs % g.runs, n = i0 / vecs / g.runs;
+    const Division at = divide(blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x, a.D / V);
+    const Division at_row = divide(at.q, g.runs);
+    const int64_t d = at.r * V, run = at_row.r, n = at_row.q;
     if (n >= a.N) return;
     const T *x = static_cast<const T *>(a.x.data) + n * a.x.row_stride + d;
     const T *gy = static_cast<const T *>(g.grad_y.data) + n * g.grad_y.row_stride + d;

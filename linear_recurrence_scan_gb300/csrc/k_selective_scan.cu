@@ -1,8 +1,8 @@
-// k_selective_scan.cu -- the selective scan over prompts and for one token.
+// k_selective_scan.cu -- the selective scan over prompts.
 //
 //   h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t,   y_t = (C_t h_t + skip x_t) silu(z_t)
 //
-// Prompts.  A lane holds SPT states of one channel in registers and walks the
+// A lane holds SPT states of one channel in registers and walks the
 // tokens in order; LANES lanes share a channel.  Tiles of 16 tokens come into
 // shared memory by asynchronous copies, two tiles ahead.  A tile's tokens are
 // shared out over a channel's lanes: each prepares its own (softplus, dt x,
@@ -55,25 +55,6 @@ struct Shape {
     static_assert(ACT % 16 == 0 && BC % 16 == 0);
 };
 
-// Sums over a channel's LANES lanes of v[0..LANES): lane l gets that of v[l].
-template <int LANES>
-__device__ __forceinline__ float scatter_sum(float *v, int sl)
-{
-    if constexpr (LANES == 1) {
-        return v[0];
-    } else {
-        constexpr int HALF = LANES / 2;
-        const bool upper = (sl & HALF) != 0;
-#pragma unroll
-        for (int i = 0; i < HALF; ++i) {
-            const float give = upper ? v[i] : v[i + HALF];
-            const float keep = upper ? v[i + HALF] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, HALF);
-        }
-        return scatter_sum<HALF>(v, sl);
-    }
-}
-
 template <class T, int SPT>
 __device__ __forceinline__ void load_states(f2 *h, const float *p, int s0, int S, bool on)
 {
@@ -121,8 +102,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES, SPLIT>::BLOCKS)
     ptx::pdl_wait_prerequisites();
     const int lane = threadIdx.x & 31, sl = lane % LANES, ch = threadIdx.x / LANES;
     const int64_t blocks = (a.D + P::CH - 1) / P::CH;
-    const int64_t c0 = blockIdx.x % blocks * P::CH, chunk = blockIdx.x / blocks % o.chunks,
-                  n = blockIdx.x / blocks / o.chunks;
+    const Division at_block = divide(blockIdx.x, blocks), at_row = divide(at_block.q, o.chunks);
+    const int64_t c0 = at_block.r * P::CH, chunk = at_row.r, n = at_row.q;
     const int64_t d = c0 + ch;
     const bool live = d < a.D;
     const int64_t dd = live ? d : a.D - 1;
@@ -306,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES, SPLIT>::BLOCKS)
 #pragma unroll
                 for (int p = 0; p < P::PER; ++p) {
                     const int k = w0 + p * LANES + sl;
-                    float v = fmaf(skip, xv[p], scatter_sum<LANES>(part + p * LANES, sl));
+                    scatter_sums<LANES, LANES / 2, 1>(part + p * LANES, lane);  // leaves lane sl the sum of its token
+                    float v = fmaf(skip, xv[p], part[p * LANES]);
                     const float zv = to_f(zs[k * ROW]);
                     v *= choose(gate, zv * sigmoid(zv), 1.f);
                     if (FAST) {
@@ -362,7 +344,8 @@ __global__ void __launch_bounds__(256) chunk_kernel(const __grid_constant__ rlsc
     ptx::pdl_wait_prerequisites();
     const int64_t i = blockIdx.x * 256ll + threadIdx.x, DS = a.D * a.S;
     if (i >= a.N * DS) return;
-    const int64_t n = i / DS, e = i % DS, d = e / a.S;
+    const Division at = divide(i, DS);
+    const int64_t n = at.q, e = at.r, d = divide(e, a.S).q;
     const float A2 = a.A[e] * kLog2e;
     float carry = start != nullptr ? start[i] : 0.f;
     float *st = o.states + n * o.chunks * DS + e;
@@ -498,112 +481,6 @@ rlscan_status back_typed(const rlscan_selective_scan_args &a, ScanOut o, const f
     return launch_back<T, 8, 16>(a, o, grad_final, s);
 }
 
-// One token: a lane has four states of one channel, of kStepRows sequences
-// in turn, whose loads are in flight together and share its row of A.
-constexpr int kStepRows = 2;
-
-template <class T, int LANES>
-__global__ void __launch_bounds__(kThreads)
-    step_kernel(const __grid_constant__ rlscan_selective_scan_args a, float *state, int64_t P, const int32_t *slots, T *y,
-                bool vec)
-{
-    constexpr int CH = kThreads / LANES;
-    ptx::pdl_trigger_dependents();
-    ptx::pdl_wait_prerequisites();
-    const int sl = threadIdx.x % LANES, s0 = 4 * sl, S = static_cast<int>(a.S);
-    const int64_t blocks = (a.D + CH - 1) / CH, d = blockIdx.x % blocks * CH + threadIdx.x / LANES;
-    const int64_t n0 = blockIdx.x / blocks * kStepRows;
-    const bool live = d < a.D;
-    const int64_t dd = live ? d : a.D - 1;
-    const bool mine = live && s0 < S;
-    float4 h[kStepRows], B[kStepRows], C[kStepRows];
-    float xv[kStepRows], dt[kStepRows], zv[kStepRows];
-    int64_t at[kStepRows];
-#pragma unroll
-    for (int r = 0; r < kStepRows; ++r) {
-        const int64_t n = n0 + r;
-        const int64_t slot = n < a.N ? (slots != nullptr ? slots[n] : n) : -1;
-        at[r] = slot >= 0 && slot < P ? (slot * a.D + dd) * S + s0 : -1;
-    }
-    auto four = [&](const auto *p, bool on, bool wide) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        using E = std::remove_cv_t<std::remove_reference_t<decltype(*p)>>;
-        if (wide && sizeof(E) == 4) {
-            if (on) v = *reinterpret_cast<const float4 *>(p);
-        } else {
-            if (on && s0 < S) v.x = to_f(p[0]);
-            if (on && s0 + 1 < S) v.y = to_f(p[1]);
-            if (on && s0 + 2 < S) v.z = to_f(p[2]);
-            if (on && s0 + 3 < S) v.w = to_f(p[3]);
-        }
-        return v;
-    };
-#pragma unroll
-    for (int r = 0; r < kStepRows; ++r) {
-        const int64_t n = n0 + r < a.N ? n0 + r : a.N - 1;
-        h[r] = four(state + (at[r] >= 0 ? at[r] : 0), mine && at[r] >= 0, vec);
-        B[r] = four(static_cast<const T *>(a.B.data) + n * a.B.row_stride + s0, true, false);
-        C[r] = four(static_cast<const T *>(a.C.data) + n * a.C.row_stride + s0, true, false);
-        xv[r] = to_f(static_cast<const T *>(a.x.data)[n * a.x.row_stride + dd]);
-        dt[r] = to_f(static_cast<const T *>(a.delta.data)[n * a.delta.row_stride + dd]);
-        zv[r] = a.z.data != nullptr ? to_f(static_cast<const T *>(a.z.data)[n * a.z.row_stride + dd]) : 0.f;
-    }
-    float4 A = four(a.A + dd * S + s0, true, vec && s0 < S);
-    A.x *= kLog2e;
-    A.y *= kLog2e;
-    A.z *= kLog2e;
-    A.w *= kLog2e;
-    const float bias = a.delta_bias != nullptr ? a.delta_bias[dd] : 0.f, skip = a.skip != nullptr ? a.skip[dd] : 0.f;
-#pragma unroll
-    for (int r = 0; r < kStepRows; ++r) {
-        float t = dt[r] + bias;
-        if (a.delta_softplus) t = softplus(t);
-        const float tx = t * xv[r];
-        h[r].x = fmaf(exp2_fast(t * A.x), h[r].x, tx * B[r].x);
-        h[r].y = fmaf(exp2_fast(t * A.y), h[r].y, tx * B[r].y);
-        h[r].z = fmaf(exp2_fast(t * A.z), h[r].z, tx * B[r].z);
-        h[r].w = fmaf(exp2_fast(t * A.w), h[r].w, tx * B[r].w);
-        float v = fmaf(C[r].x, h[r].x, C[r].y * h[r].y) + fmaf(C[r].z, h[r].z, C[r].w * h[r].w);
-#pragma unroll
-        for (int m = LANES / 2; m > 0; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
-        if (at[r] >= 0 && mine) {
-            float *p = state + at[r];
-            if (vec) {
-                *reinterpret_cast<float4 *>(p) = h[r];
-            } else {
-                p[0] = h[r].x;
-                if (s0 + 1 < S) p[1] = h[r].y;
-                if (s0 + 2 < S) p[2] = h[r].z;
-                if (s0 + 3 < S) p[3] = h[r].w;
-            }
-        }
-        v = fmaf(skip, xv[r], v);
-        if (a.z.data != nullptr) v *= zv[r] * sigmoid(zv[r]);
-        if (live && sl == 0 && n0 + r < a.N) y[(n0 + r) * a.D + d] = from_f<T>(at[r] >= 0 ? v : 0.f);
-    }
-}
-
-template <class T>
-rlscan_status step_typed(const rlscan_selective_scan_args &a, float *state, int64_t P, const int32_t *slots, void *y,
-                         cudaStream_t s)
-{
-    const bool vec =
-        a.S % 4 == 0 && ((reinterpret_cast<uintptr_t>(state) | reinterpret_cast<uintptr_t>(a.A)) & 15u) == 0;
-    auto go = [&](auto lanes) {
-        constexpr int LANES = decltype(lanes)::value;
-        return launch_overlapped(step_kernel<T, LANES>, ceil_div(a.N, kStepRows) * ceil_div(a.D, kThreads / LANES), kThreads, 0,
-                                 s, a, state, P, slots, static_cast<T *>(y), vec);
-    };
-    switch (state_lanes(a.S)) {
-    case 1: return go(std::integral_constant<int, 1>());
-    case 2: return go(std::integral_constant<int, 2>());
-    case 4: return go(std::integral_constant<int, 4>());
-    case 8: return go(std::integral_constant<int, 8>());
-    case 16: return go(std::integral_constant<int, 16>());
-    default: return go(std::integral_constant<int, 32>());
-    }
-}
-
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
@@ -637,13 +514,6 @@ rlscan_status launch_back_states(const rlscan_selective_scan_args &a, const rlsc
 {
     const ScanOut o{nullptr, nullptr, nullptr, chunk, chunks, 0, false, states, spans, cuts, grad_y};
     return a.dtype == RLSCAN_BF16 ? back_typed<bf16>(a, o, grad_final, s) : back_typed<float>(a, o, grad_final, s);
-}
-
-rlscan_status launch_selective_scan_step(const rlscan_selective_scan_args &a, float *state, int64_t P,
-                                         const int32_t *slots, void *y, cudaStream_t s)
-{
-    return a.dtype == RLSCAN_BF16 ? step_typed<bf16>(a, state, P, slots, y, s)
-                                  : step_typed<float>(a, state, P, slots, y, s);
 }
 
 }  // namespace seq

@@ -59,30 +59,6 @@ struct Shape {
     static_assert(ACT % 16 == 0 && BC % 16 == 0 && BPITCH % 16 == 0 && PITCH % 16 == 0);
 };
 
-// Sums of v[0..N) over the lanes that differ in the bits HI .. LO of their
-// number, shared out: while values are left, each bit halves them (a lane
-// keeps one half), after that lanes hold the same sums.  Returns the index of
-// the first value kept.
-template <int N, int HI, int LO>
-__device__ __forceinline__ int scatter_sums(float *v, int lane)
-{
-    if constexpr (HI < LO || HI == 0) {
-        return 0;
-    } else if constexpr (N == 1) {
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], HI);
-        return scatter_sums<1, HI / 2, LO>(v, lane);
-    } else {
-        constexpr int H = N / 2;
-        const bool upper = (lane & HI) != 0;
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-            const float give = upper ? v[i] : v[i + H], keep = upper ? v[i + H] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, HI);
-        }
-        return scatter_sums<H, HI / 2, LO>(v, lane) + (upper ? H : 0);
-    }
-}
-
 template <class T, int LANES>
 __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
     grad_kernel(const __grid_constant__ rlscan_selective_scan_args a, const __grid_constant__ GradArgs g)
@@ -98,8 +74,9 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
     char *sumA = keep + P::KEEP;  // dA: a tile's sum is in registers, the sum over tiles here (two short sums, not one long)
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
-    const int64_t blocks = (a.D + P::CH - 1) / P::CH, block = blockIdx.x % blocks;
-    const int64_t chunk = blockIdx.x / blocks % g.chunks, n = blockIdx.x / blocks / g.chunks;
+    const int64_t blocks = (a.D + P::CH - 1) / P::CH, block = divide(blockIdx.x, blocks).r;
+    const Division at_row = divide(divide(blockIdx.x, blocks).q, g.chunks);
+    const int64_t chunk = at_row.r, n = at_row.q;
     const int64_t first = chunk * g.chunk, last = first + g.chunk < a.T ? first + g.chunk : a.T;
     const int64_t c0 = block * P::CH;
     const int S = static_cast<int>(a.S), s0 = 4 * sl;

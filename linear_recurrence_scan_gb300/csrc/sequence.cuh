@@ -155,6 +155,44 @@ __device__ __forceinline__ float choose(uint32_t mask, float a, float b)
     return __uint_as_float((__float_as_uint(a) & mask) | (__float_as_uint(b) & ~mask));
 }
 
+// Sums of v[0..N) over the lanes that differ in the bits HI .. LO of their
+// number, shared out: while values are left, each bit halves them (a lane
+// keeps one half), after that lanes hold the same sums.  Returns the index of
+// the first value kept.
+template <int N, int HI, int LO>
+__device__ __forceinline__ int scatter_sums(float *v, int lane)
+{
+    if constexpr (HI < LO || HI == 0) {
+        return 0;
+    } else if constexpr (N == 1) {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], HI);
+        return scatter_sums<1, HI / 2, LO>(v, lane);
+    } else {
+        constexpr int H = N / 2;
+        const bool upper = (lane & HI) != 0;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float give = upper ? v[i] : v[i + H], keep = upper ? v[i + H] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, HI);
+        }
+        return scatter_sums<H, HI / 2, LO>(v, lane) + (upper ? H : 0);
+    }
+}
+
+// quotient and remainder; in 32 bits where the numbers fit (a 64-bit division
+// is over a hundred instructions, more than all else a token's call needs)
+struct Division {
+    int64_t q, r;
+};
+__device__ __forceinline__ Division divide(int64_t i, int64_t n)
+{
+    if ((static_cast<uint64_t>(i) | static_cast<uint64_t>(n)) >> 32 == 0) {
+        const uint32_t q = static_cast<uint32_t>(i) / static_cast<uint32_t>(n);
+        return {q, static_cast<uint32_t>(i) - q * static_cast<uint32_t>(n)};
+    }
+    return {i / n, i % n};
+}
+
 // tokens of row n, clamped to the array
 __device__ __forceinline__ int64_t row_length(const int32_t *lengths, int64_t n, int64_t T)
 {
