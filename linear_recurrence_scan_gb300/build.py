@@ -1,6 +1,6 @@
 """Build ``librlscan.so`` (the CUDA library behind the C ABI) in-tree.
 
-Each translation unit in ``csrc/`` is compiled in parallel with nvcc for
+Each translation unit in ``csrc/`` and ``csrc_sequence/`` is compiled in parallel with nvcc for
 sm_103a only, then linked into ``linear_recurrence_scan_gb300/_build/
 librlscan.so``.  Run ``python -m linear_recurrence_scan_gb300.build``.
 """
@@ -14,14 +14,15 @@ import subprocess
 import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-CSRC = os.path.join(HERE, "csrc")
+CSRC = os.path.join(HERE, "csrc")                    # the estimators' scan kernels
+CSRC_SEQUENCE = os.path.join(HERE, "csrc_sequence")  # the state-space layer
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "librlscan.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
-              "-Xcompiler", "-fvisibility=hidden", "-I", CSRC, "-I", INCLUDE]
+              "-Xcompiler", "-fvisibility=hidden", "-I", CSRC, "-I", CSRC_SEQUENCE, "-I", INCLUDE]
 
 
 def _nvcc() -> str:
@@ -32,11 +33,11 @@ def _nvcc() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return [f for d in (CSRC, CSRC_SEQUENCE) for f in sorted(glob.glob(os.path.join(d, "*.cu")))]
 
 
 def _headers():
-    return (sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) +
+    return ([f for d in (CSRC, CSRC_SEQUENCE) for f in sorted(glob.glob(os.path.join(d, "*.cuh")))] +
             [os.path.join(INCLUDE, "rlscan.h")])
 
 

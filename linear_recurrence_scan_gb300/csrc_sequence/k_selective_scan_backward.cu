@@ -44,6 +44,7 @@ struct Shape {
     static constexpr int GROUPS = 32 / LANES;
     static constexpr int CW = 4 * GROUPS, CH = WARPS * CW;  // channels of a warp, of a block
     static constexpr int SP = 4 * LANES;                    // states, padded
+    static constexpr int SHARE = LANES >= 4 ? LANES / 4 : 1;  // lanes that end up with the same sums
     static constexpr int CPL = CW > 32 ? CW / 32 : 1;       // channels a lane prepares
     static constexpr int ITEMS = CW * kTile / 32;           // (channel, token) pairs a lane prepares
     static constexpr int PITCH = CH * static_cast<int>(sizeof(T));
@@ -197,8 +198,8 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
         bias[j] = a.delta_bias != nullptr && c < width ? a.delta_bias[c0 + c] : 0.f;
     }
     // the channels whose outputs the lane writes: those that scatter_sums leaves it
-    const int mine = 4 * group + (LANES >= 4 ? sl / (LANES / 4) : sl * P::MINE);
-    const bool writes = LANES <= 4 || sl % (LANES / 4) == 0;
+    const int mine = 4 * group + (LANES >= 4 ? sl / P::SHARE : sl * P::MINE);
+    const bool writes = sl % P::SHARE == 0;
     float obias[P::MINE], skip[P::MINE], dskip[P::MINE], dbias[P::MINE];
 #pragma unroll
     for (int i = 0; i < P::MINE; ++i) {
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const f2 before = cut ? 0ull : from[p][i];
-                        to[p][i] = fma2(dx[p], b[i], mul2(exp2_fast(mul2(d[p], A2[p][i])), before));
+                        to[p][i] = fma2(dx[p], b[i], mul2(decay(d[p], A2[p][i]), before));
                     }
             };
             // the states at each sub-tile's start: the first is the checkpoint,
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
                             if (!FAST) q = cut ? 0ull : q;
                             w[p] = i == 0 ? mul2(q, A2[p][i]) : fma2(q, A2[p][i], w[p]);
                             dA[p][i] = fma2(q, d[p], dA[p][i]);
-                            G[p][i] = mul2(Gt, exp2_fast(mul2(d[p], A2[p][i])));
+                            G[p][i] = mul2(Gt, decay(d[p], A2[p][i]));
                             if (!FAST) G[p][i] = cut ? 0ull : G[p][i];
                         }
                     }

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads)
         sum[r] = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[i] = fmaf(exp2_fast(t * A2[i]), h[r][i], tx * B[r][i]);
+            v[i] = fmaf(decay(t, A2[i]), h[r][i], tx * B[r][i]);
             sum[r] = fmaf(C[r][i], v[i], sum[r]);
         }
         if (mine && state[r] != nullptr) {

@@ -1,0 +1,37 @@
+// scan_plan.cuh -- how a call of the selective scan is laid out, and what its
+// kernels write.
+#pragma once
+
+#include "sequence.cuh"
+
+namespace rlscan {
+namespace seq {
+
+constexpr int kScanThreads = 128;
+
+struct ScanOut {
+    void *y;
+    float *final_state, *checkpoints;
+    // rows in `chunks` chunks of `chunk` tokens
+    int64_t chunk, chunks;
+    int unit;        // bytes of the copies into shared memory: 16, 4 or 0 (single values)
+    bool vec;        // states in whole 16-byte units
+    float *states;   // [N][chunks][D][S]: a chunk's own end state, then the state in front of it
+    float *spans;    // [N][chunks][D]: the chunk's sum of dt
+    uint8_t *cuts;   // [N][chunks]: an episode starts in the chunk
+    rlscan_array3 grad_y;  // BACK
+};
+
+// How a call is laid out: states per lane, and chunks of each row.
+struct Plan {
+    int spt, lanes;
+    int64_t chunk, chunks;
+};
+
+template <class T>
+rlscan_status scan_typed(const Plan &p, const rlscan_selective_scan_args &a, ScanOut o, cudaStream_t s);
+template <class T>
+rlscan_status back_states_typed(const rlscan_selective_scan_args &a, ScanOut o, const float *grad_final, cudaStream_t s);
+
+}  // namespace seq
+}  // namespace rlscan

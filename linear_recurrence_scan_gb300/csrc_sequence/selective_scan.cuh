@@ -1,4 +1,6 @@
-// k_selective_scan.cu -- the selective scan over prompts.
+// selective_scan.cuh -- the selective scan over prompts, for one activation
+// type: the kernels, and the launches that k_selective_scan_*.cu instantiate
+// (a translation unit for each type, which halves the build).
 //
 //   h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t,   y_t = (C_t h_t + skip x_t) silu(z_t)
 //
@@ -8,31 +10,19 @@
 // shared out over a channel's lanes: each prepares its own (softplus, dt x,
 // the gate), hands dt and dt x to the others with shuffles, and gets its
 // tokens' sums over the states back.
-#include "sequence.cuh"
+#pragma once
+
+#include "scan_plan.cuh"
 
 namespace rlscan {
 namespace seq {
 namespace {
 
-constexpr int kThreads = 128;
 constexpr int kTile = kCheckpoint;
-
-struct ScanOut {
-    void *y;
-    float *final_state, *checkpoints;
-    // rows in `chunks` chunks of `chunk` tokens
-    int64_t chunk, chunks;
-    int unit;        // bytes of the copies into shared memory: 16, 4 or 0 (single values)
-    bool vec;        // states in whole 16-byte units
-    float *states;   // [N][chunks][D][S]: a chunk's own end state, then the state in front of it
-    float *spans;    // [N][chunks][D]: the chunk's sum of dt
-    uint8_t *cuts;   // [N][chunks]: an episode starts in the chunk
-    rlscan_array3 grad_y;  // BACK
-};
 
 template <class T, int SPT, int LANES, bool SPLIT>
 struct Shape {
-    static constexpr int CH = kThreads / LANES;     // channels of a block
+    static constexpr int CH = kScanThreads / LANES;     // channels of a block
     static constexpr int SP = SPT * LANES;          // states, padded
     // Tokens taken at once, and registers: calls whose rows are whole have few
     // warps and live on the overlap of 16 tokens; those in chunks have many
@@ -91,7 +81,7 @@ __device__ __forceinline__ void store_states(float *p, const f2 *h, int s0, int 
 enum Mode { FULL_SCAN, PART, BACK };
 
 template <class T, int SPT, int LANES, int MODE, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES, SPLIT>::BLOCKS)
+__global__ void __launch_bounds__(kScanThreads, Shape<T, SPT, LANES, SPLIT>::BLOCKS)
     scan_kernel(const __grid_constant__ rlscan_selective_scan_args a, const __grid_constant__ ScanOut o)
 {
     using P = Shape<T, SPT, LANES, SPLIT>;
@@ -129,16 +119,16 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES, SPLIT>::BLOCKS)
         const int64_t t = (MODE == BACK ? tiles - 1 - tile : tile) * kTile, left = count - t;
         char *st = smem + tile % P::STAGES * P::STAGE;
         const int rows = left < kTile ? static_cast<int>(left) : kTile;
-        load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kThreads>(st, x + t * in.token_stride, in.token_stride, rows, width);
-        load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kThreads>(st + P::ACT, delta + t * a.delta.token_stride,
+        load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kScanThreads>(st, x + t * in.token_stride, in.token_stride, rows, width);
+        load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kScanThreads>(st + P::ACT, delta + t * a.delta.token_stride,
                                                               a.delta.token_stride, rows, width);
-        load_tile<T, kTile, P::BW, P::BPITCH, CHUNK, kThreads>(st + 3 * P::ACT, B + t * drive.token_stride,
+        load_tile<T, kTile, P::BW, P::BPITCH, CHUNK, kScanThreads>(st + 3 * P::ACT, B + t * drive.token_stride,
                                                                drive.token_stride, rows, S);
         if (gated)
-            load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kThreads>(st + 2 * P::ACT, z + t * a.z.token_stride,
+            load_tile<T, kTile, P::CH, P::PITCH, CHUNK, kScanThreads>(st + 2 * P::ACT, z + t * a.z.token_stride,
                                                                   a.z.token_stride, rows, width);
         if (FULL) {
-            load_tile<T, kTile, P::BW, P::BPITCH, CHUNK, kThreads>(st + 3 * P::ACT + P::BC, C + t * a.C.token_stride,
+            load_tile<T, kTile, P::BW, P::BPITCH, CHUNK, kScanThreads>(st + 3 * P::ACT + P::BC, C + t * a.C.token_stride,
                                                                    a.C.token_stride, rows, S);
         }
     };
@@ -188,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES, SPLIT>::BLOCKS)
             float *w = wide + (tile & 1) * (2 * kTile * P::SP);
             constexpr int QUADS = kTile * P::SP / 4;
 #pragma unroll
-            for (int i = threadIdx.x; i < (FULL ? 2 : 1) * QUADS; i += kThreads) {
+            for (int i = threadIdx.x; i < (FULL ? 2 : 1) * QUADS; i += kScanThreads) {
                 const int k = i / QUADS, r = i / (P::SP / 4) % kTile, c = i % (P::SP / 4);
                 const uint2 v = *reinterpret_cast<const uint2 *>(st + 3 * P::ACT + k * P::BC + r * P::BPITCH + c * 8);
                 *reinterpret_cast<float4 *>(w + 4 * i) =
@@ -259,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, SPT, LANES, SPLIT>::BLOCKS)
 #pragma unroll
                 for (int i = 0; i < SPT / 4; ++i) {
                     const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(Bw + k * BROW + 4 * i);
-                    const f2 e0 = exp2_fast(mul2(dp, A2[2 * i])), e1 = exp2_fast(mul2(dp, A2[2 * i + 1]));
+                    const f2 e0 = decay(dp, A2[2 * i]), e1 = decay(dp, A2[2 * i + 1]);
                     if constexpr (MODE == BACK) {
                         h[2 * i] = mul2(e0, fma2(xp, b.x, h[2 * i]));
                         h[2 * i + 1] = mul2(e1, fma2(xp, b.y, h[2 * i + 1]));
@@ -380,7 +370,7 @@ rlscan_status launch_mode(const rlscan_selective_scan_args &a, const ScanOut &o,
     static const bool sized =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
     if (!sized) return RLSCAN_ERR_CUDA;
-    return launch_overlapped(kernel, a.N * ceil_div(a.D, P::CH) * o.chunks, kThreads, P::SMEM, s, a, o);
+    return launch_overlapped(kernel, a.N * ceil_div(a.D, P::CH) * o.chunks, kScanThreads, P::SMEM, s, a, o);
 }
 
 template <class T, int SPT, int LANES>
@@ -392,43 +382,6 @@ rlscan_status launch_shape(const rlscan_selective_scan_args &a, const ScanOut &o
         st = launch_overlapped(chunk_kernel<false>, ceil_div(a.N * a.D * a.S, 256), 256, 0, s, a, o, a.initial_state);
     if (st != RLSCAN_OK) return st;
     return launch_mode<T, SPT, LANES, FULL_SCAN, true>(a, o, s);
-}
-
-// How a call is laid out: states per lane, and chunks of each row.
-struct Plan {
-    int spt, lanes;
-    int64_t chunk, chunks;
-};
-
-// Sixteen states a lane need the fewest instructions a state, eight give
-// twice the warps; chunks give as many warps as a row has tokens for, but
-// compute every state twice.  Measured (D 2048, S 16, bf16, microseconds):
-//   one row    T 512: 60 unsplit (8 states), 34 in chunks of 64;
-//              T 2048: 213, 68 (128);  T 8192: 829, 185 (16 states, 512)
-//   four rows  T 512: 60, 65;  T 2048: 214, 175 (16, 128);  T 8192: 830, 563 (16, 512)
-//   eight rows T 2048: 267 (8) and 279 (16), 301 (16, 256);  T 8192: 1037 (8), 1081 (16, 512)
-// so rows are split while the unsplit call has less than 1.5 blocks an SM.
-Plan plan(const rlscan_selective_scan_args &a)
-{
-    const int64_t sms = sm_count() > 0 ? sm_count() : 152;
-    auto lanes_of = [&](int spt) {
-        int lanes = 1;
-        while (spt * lanes < a.S) lanes *= 2;
-        return lanes;
-    };
-    auto blocks_of = [&](int spt) { return a.N * ceil_div(a.D * lanes_of(spt), kThreads); };
-    Plan p;
-    const int64_t narrow = blocks_of(8);
-    const bool split = a.T > 256 && 2 * narrow < 3 * sms && !(4 * narrow >= 3 * sms && a.T <= 1024);
-    p.spt = a.S > 8 && (split ? a.T >= 1024 : narrow >= 3 * sms) ? 16 : 8;
-    p.chunk = ceil_div(a.T > 0 ? a.T : 1, kTile) * kTile;
-    if (split) {
-        p.chunk = a.T < 1024 ? 64 : 256;
-        while (p.chunk > 64 && blocks_of(p.spt) * ceil_div(a.T, p.chunk) < sms) p.chunk /= 2;
-    }
-    p.lanes = lanes_of(p.spt);
-    p.chunks = ceil_div(a.T > 0 ? a.T : 1, p.chunk);
-    return p;
 }
 
 template <class T, int SPT>
@@ -443,8 +396,19 @@ rlscan_status by_lanes(int lanes, const rlscan_selective_scan_args &a, const Sca
     }
 }
 
+// The gradient's messages, for the backward pass: its own shape of lanes.
+template <class T, int SPT, int LANES>
+rlscan_status launch_back(const rlscan_selective_scan_args &a, const ScanOut &o, const float *grad_final, cudaStream_t s)
+{
+    const rlscan_status st = launch_mode<T, SPT, LANES, BACK, true>(a, o, s);
+    if (st != RLSCAN_OK) return st;
+    return launch_overlapped(chunk_kernel<true>, ceil_div(a.N * a.D * a.S, 256), 256, 0, s, a, o, grad_final);
+}
+
+}  // namespace
+
 template <class T>
-rlscan_status launch_typed(const Plan &p, const rlscan_selective_scan_args &a, ScanOut o, cudaStream_t s)
+rlscan_status scan_typed(const Plan &p, const rlscan_selective_scan_args &a, ScanOut o, cudaStream_t s)
 {
     Chunk c;
     for (const rlscan_array3 *v : {&a.x, &a.delta, &a.B, &a.C}) c.add(v->data, v->row_stride, v->token_stride, sizeof(T));
@@ -456,17 +420,8 @@ rlscan_status launch_typed(const Plan &p, const rlscan_selective_scan_args &a, S
     return by_lanes<T, 8>(p.lanes, a, o, s);
 }
 
-// The gradient's messages, for the backward pass: its own shape of lanes.
-template <class T, int SPT, int LANES>
-rlscan_status launch_back(const rlscan_selective_scan_args &a, const ScanOut &o, const float *grad_final, cudaStream_t s)
-{
-    const rlscan_status st = launch_mode<T, SPT, LANES, BACK, true>(a, o, s);
-    if (st != RLSCAN_OK) return st;
-    return launch_overlapped(chunk_kernel<true>, ceil_div(a.N * a.D * a.S, 256), 256, 0, s, a, o, grad_final);
-}
-
 template <class T>
-rlscan_status back_typed(const rlscan_selective_scan_args &a, ScanOut o, const float *grad_final, cudaStream_t s)
+rlscan_status back_states_typed(const rlscan_selective_scan_args &a, ScanOut o, const float *grad_final, cudaStream_t s)
 {
     Chunk c;
     for (const rlscan_array3 *v : {static_cast<const rlscan_array3 *>(&o.grad_y), &a.delta, &a.C})
@@ -479,41 +434,6 @@ rlscan_status back_typed(const rlscan_selective_scan_args &a, ScanOut o, const f
     if (a.S <= 32) return launch_back<T, 8, 4>(a, o, grad_final, s);
     if (a.S <= 64) return launch_back<T, 8, 8>(a, o, grad_final, s);
     return launch_back<T, 8, 16>(a, o, grad_final, s);
-}
-
-size_t up(size_t v) { return (v + 255) / 256 * 256; }
-
-}  // namespace
-
-size_t selective_scan_workspace(const rlscan_selective_scan_args &a)
-{
-    const Plan p = plan(a);
-    if (p.chunks <= 1) return 0;
-    const size_t each = static_cast<size_t>(a.N) * p.chunks;
-    return up(each * a.D * a.S * 4) + up(each * a.D * 4) + up(each);
-}
-
-rlscan_status launch_selective_scan(const rlscan_selective_scan_args &a, void *y, float *final_state,
-                                    float *checkpoints, void *ws, cudaStream_t s)
-{
-    const Plan p = plan(a);
-    ScanOut o{y, final_state, checkpoints, p.chunk, p.chunks, 0, false, nullptr, nullptr, nullptr, {}};
-    if (p.chunks > 1) {
-        const size_t each = static_cast<size_t>(a.N) * p.chunks;
-        char *w = static_cast<char *>(ws);
-        o.states = reinterpret_cast<float *>(w);
-        o.spans = reinterpret_cast<float *>(w + up(each * a.D * a.S * 4));
-        o.cuts = reinterpret_cast<uint8_t *>(w + up(each * a.D * a.S * 4) + up(each * a.D * 4));
-    }
-    return a.dtype == RLSCAN_BF16 ? launch_typed<bf16>(p, a, o, s) : launch_typed<float>(p, a, o, s);
-}
-
-rlscan_status launch_back_states(const rlscan_selective_scan_args &a, const rlscan_array3 &grad_y, const float *grad_final,
-                                 int64_t chunk, int64_t chunks, float *states, float *spans, uint8_t *cuts,
-                                 cudaStream_t s)
-{
-    const ScanOut o{nullptr, nullptr, nullptr, chunk, chunks, 0, false, states, spans, cuts, grad_y};
-    return a.dtype == RLSCAN_BF16 ? back_typed<bf16>(a, o, grad_final, s) : back_typed<float>(a, o, grad_final, s);
 }
 
 }  // namespace seq

@@ -51,6 +51,13 @@ __device__ __forceinline__ float rcp_fast(float v)
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// exp(dt A) from A log2 e.  A state multiplies thousands of these, so their mean
+// error counts more than a single one's: ex2.approx lies 0.1 to 0.44 units of
+// 2^-24 below the exact value on average for dt A in (-1, 0) (measured against
+// 64 bits), which the small constant in the exponent takes back: the gradient
+// of A over 8 x 2048 tokens is 0.7e-6 off with it, 1.6e-6 without.
+constexpr float kDecayShift = 2.5e-8f;
+
 // 1 / (1 + exp(-v)); 2^x is infinite below v = -88, whose reciprocal is 0
 __device__ __forceinline__ float sigmoid(float v) { return rcp_fast(1.f + exp2_fast(-kLog2e * v)); }
 
@@ -244,6 +251,8 @@ __device__ __forceinline__ f2 exp2_fast(f2 v)
     const float2 h = halves(v);
     return pair(exp2_fast(h.x), exp2_fast(h.y));
 }
+__device__ __forceinline__ float decay(float dt, float A2) { return exp2_fast(fmaf(dt, A2, kDecayShift)); }
+__device__ __forceinline__ f2 decay(f2 dt, f2 A2) { return exp2_fast(fma2(dt, A2, both(kDecayShift))); }
 __device__ __forceinline__ f2 rcp_fast(f2 v)
 {
     const float2 h = halves(v);

@@ -185,7 +185,7 @@ class _SelectiveScan(torch.autograd.Function):
     def forward(ctx, x, delta, A, B, C, D, z, delta_bias, delta_softplus, initial_state, resets, lengths):
         y, final, marks = _scan_forward(True, x, delta, A, B, C, D, z, delta_bias, delta_softplus, initial_state,
                                         resets, lengths)
-        ctx.delta_softplus = delta_softplus
+        ctx.delta_softplus, ctx.started = delta_softplus, initial_state is not None
         ctx.save_for_backward(x, delta, A, B, C, D, z, delta_bias, resets, lengths, marks)
         ctx.set_materialize_grads(False)
         return y, final
@@ -200,7 +200,8 @@ class _SelectiveScan(torch.autograd.Function):
             grad_y = torch.zeros_like(x)
         g = selective_scan_backward(grad_y, x, delta, A, B, C, marks, D, z, delta_bias, ctx.delta_softplus, resets,
                                     lengths, grad_final)
-        return g.x, g.delta, g.A, g.B, g.C, g.D, g.z, g.delta_bias, None, g.initial_state, None, None
+        return (g.x, g.delta, g.A, g.B, g.C, g.D, g.z, g.delta_bias, None,
+                g.initial_state if ctx.started else None, None, None)
 
 
 def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_softplus=True, initial_state=None,

@@ -203,6 +203,18 @@ def test_scan_masked_places_may_hold_anything(dtype):
     close(final, np64(final2), np.abs(np64(final2)) + 1, scan_factor(T), "final state after the reset")
 
 
+@pytest.mark.parametrize("T,n", [(20, 17), (64, 33), (250, 1)])
+def test_scan_padding_leaves_the_state(T, n):
+    """A padded row's states and outputs are the shorter call's, bit for bit."""
+    a, init, _, _, _ = scan_inputs(1, T, 48, 16, F32, 22)
+    dev = {k: v.to(DEV) for k, v in a.items()}
+    lengths = torch.tensor([n], dtype=torch.int32).to(DEV)
+    y, final = L().selective_scan(**dev, initial_state=to_dev(init), lengths=lengths)
+    head = {k: (t[:, :n] if k in ("x", "delta", "z", "B", "C") else t) for k, t in dev.items()}
+    y2, final2 = L().selective_scan(**head, initial_state=to_dev(init))
+    assert torch.equal(y[:, :n], y2) and torch.equal(final, final2) and not y[:, n:].any()
+
+
 def test_scan_no_tokens_and_no_rows():
     a, init, _, _, _ = scan_inputs(2, 1, 8, 4, F32, 9)
     none = {k: (v[:, :0] if k in ("x", "delta", "z", "B", "C") else v).to(DEV) for k, v in a.items()}
