@@ -31,33 +31,52 @@ int row_threads(int64_t D)
     return t <= kMostThreads ? static_cast<int>(t) : 0;
 }
 
-// values c .. c+V-1 of a row of D, wide where `vec`; those past the row are 0
-template <class E, int V>
-__device__ __forceinline__ void load_raw(Words<E, V> &r, const E *p, int c, int D, bool vec)
+// Where a thread's values lie in its row.  VEC: V neighbours, chunk j at
+// column (j threads + tid) V.  Otherwise single values, neighbouring lanes
+// side by side: value i of chunk j at column (j V + i) threads + tid.
+template <bool VEC, int V>
+struct Columns {
+    int tid, threads, D;
+    __device__ __forceinline__ int first(int j) const { return VEC ? (j * threads + tid) * V : j * V * threads + tid; }
+    __device__ __forceinline__ int at(int j, int i) const { return VEC ? first(j) + i : first(j) + i * threads; }
+};
+
+// chunk j of a row, 0 past its end
+template <bool VEC, class E, int V>
+__device__ __forceinline__ void load_chunk(Words<E, V> &r, const E *p, const Columns<VEC, V> &c, int j)
 {
-    if (vec && c < D) {
-        r.load(p + c);
-    } else {
-        r.zero();
-        if (!vec)
+    r.zero();
+    if constexpr (VEC) {
+        if (c.first(j) < c.D) r.load(p + c.first(j));
+    } else if constexpr (sizeof(E) == 4) {
 #pragma unroll
-            for (int i = 0; i < V; i += 2)
-                r.set(i / 2, c + i < D ? to_f(p[c + i]) : 0.f, c + i + 1 < D ? to_f(p[c + i + 1]) : 0.f);
+        for (int i = 0; i < V; ++i)
+            if (c.at(j, i) < c.D) r.w[i] = *reinterpret_cast<const uint32_t *>(p + c.at(j, i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            Words<E, 1> lo, hi;
+            lo.zero();
+            hi.zero();
+            if (c.at(j, i) < c.D) lo.load(p + c.at(j, i));
+            if (c.at(j, i + 1) < c.D) hi.load(p + c.at(j, i + 1));
+            r.w[i / 2] = lo.w[0] | hi.w[0] << 16;
+        }
     }
 }
 
-template <class E, int V>
-__device__ __forceinline__ void store_chunk(E *p, const float *v, int c, int D, bool vec)
+template <bool VEC, class E, int V>
+__device__ __forceinline__ void store_chunk(E *p, const float *v, const Columns<VEC, V> &c, int j)
 {
-    if (vec) {
+    if constexpr (VEC) {
         Words<E, V> r;
 #pragma unroll
         for (int i = 0; i < V; i += 2) r.set(i / 2, v[i], v[i + 1]);
-        if (c < D) r.store(p + c);
+        if (c.first(j) < c.D) r.store(p + c.first(j));
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (c + i < D) p[c + i] = from_f<E>(v[i]);
+            if (c.at(j, i) < c.D) p[c.at(j, i)] = from_f<E>(v[i]);
     }
 }
 
@@ -87,35 +106,37 @@ __device__ __forceinline__ void row_sums(float *v, float (*scratch)[32][N], int 
 
 // A block walks rows in strides of the grid: the next row's loads are in
 // flight while this row's sum and outputs are made.
-template <class T, class R, bool WARP>
+template <class T, class R, bool WARP, bool VEC>
 __global__ void __maxnreg__(kNormRegisters) norm_kernel(const __grid_constant__ NormArgs a)
 {
     constexpr int V = kVec<T>;
     __shared__ float scratch[2][32][1];
+    __shared__ uint32_t tops[WARP ? kRowWarps : 1][VEC ? 1 : kMostThreads * kChunks * V / kScaleBlock];
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
     const int threads = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x, D = static_cast<int>(a.D);
     const int64_t rows = WARP ? kRowWarps : 1, step = gridDim.x * rows;
     int64_t row = blockIdx.x * rows + (WARP ? threadIdx.x / 32 : 0);
-    const int c0 = tid * V, c1 = c0 + threads * V;
+    const Columns<VEC, V> col{tid, threads, D};
     const bool summed = a.residual != nullptr;
     Words<T, V> x[kChunks];
     Words<R, V> r[kChunks];
     auto load = [&](int64_t at) {
         const T *xp = static_cast<const T *>(a.x) + at * a.x_stride;
-        load_raw<T, V>(x[0], xp, c0, D, a.vec);
-        load_raw<T, V>(x[1], xp, c1, D, a.vec);
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) load_chunk<VEC>(x[j], xp, col, j);
         if (summed) {
             const R *rp = static_cast<const R *>(a.residual) + at * a.residual_stride;
-            load_raw<R, V>(r[0], rp, c0, D, a.vec);
-            load_raw<R, V>(r[1], rp, c1, D, a.vec);
+#pragma unroll
+            for (int j = 0; j < kChunks; ++j) load_chunk<VEC>(r[j], rp, col, j);
         }
     };
     Words<float, V> w[kChunks];
     if (row < a.M) load(row);
-    load_raw<float, V>(w[0], a.weight, c0, D, a.vec);
-    load_raw<float, V>(w[1], a.weight, c1, D, a.vec);
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) load_chunk<VEC>(w[j], a.weight, col, j);
     const float over = 1.f / static_cast<float>(D);
+    const int blocks = (D + kScaleBlock - 1) / kScaleBlock;
     for (int flip = 0; row < a.M; row += step, flip ^= 1) {
         float h[kChunks][V], ss[1] = {0.f};
 #pragma unroll
@@ -126,54 +147,87 @@ __global__ void __maxnreg__(kNormRegisters) norm_kernel(const __grid_constant__ 
                 if (summed) h[j][i] += r[j][i];
                 ss[0] = fmaf(h[j][i], h[j][i], ss[0]);
             }
-            if (summed) store_chunk<R, V>(static_cast<R *>(a.residual_out) + row * a.D, h[j], j == 0 ? c0 : c1, D, a.vec);
+            if (summed) store_chunk<VEC>(static_cast<R *>(a.residual_out) + row * a.D, h[j], col, j);
         }
         if (row + step < a.M) load(row + step);
         row_sums<WARP, 1>(ss, scratch, flip);
         const float inv = rsqrtf(fmaf(ss[0], over, a.eps));
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            const int c = j == 0 ? c0 : c1;
+        for (int j = 0; j < kChunks; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) h[j][i] = h[j][i] * inv * w[j][i];
-            if (a.scales == nullptr) {
-                store_chunk<T, V>(static_cast<T *>(a.y) + row * a.D, h[j], c, D, a.vec);
-                continue;
-            }
-            // kScaleBlock / V neighbouring lanes hold a block of columns; the
-            // bits of |v| order like |v|, with infinities and NaN on top
-            uint32_t top = 0;
+        if (a.scales == nullptr) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(h[j][i]) & 0x7fffffffu);
+            for (int j = 0; j < kChunks; ++j) store_chunk<VEC>(static_cast<T *>(a.y) + row * a.D, h[j], col, j);
+            continue;
+        }
+        uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.D;
+        float *scales = a.scales + row * blocks;
+        // the bits of |v| order like |v|, with infinities and NaN on top
+        auto scale_of = [](uint32_t top) {
+            return top < 0x7f800000u ? fmaxf(__uint_as_float(top), kScaleFloor) / kE4m3Max : __int_as_float(0x7fffffff);
+        };
+        if constexpr (VEC) {
+            // kScaleBlock / V neighbouring lanes hold a block of columns
 #pragma unroll
-            for (int m = kScaleBlock / V / 2; m > 0; m /= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-            const float scale =
-                top < 0x7f800000u ? fmaxf(__uint_as_float(top), kScaleFloor) / kE4m3Max : __int_as_float(0x7fffffff);
-            const float back = 1.f / scale;
-            uint32_t q[V / 4];
+            for (int j = 0; j < kChunks; ++j) {
+                const int c = col.first(j);
+                uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < V; i += 4) {
-                const uint32_t lo =
-                    __nv_cvt_float2_to_fp8x2(make_float2(h[j][i] * back, h[j][i + 1] * back), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(h[j][i + 2] * back, h[j][i + 3] * back),
-                                                             __NV_SATFINITE, __NV_E4M3);
-                q[i / 4] = lo | hi << 16;
-            }
-            uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.D;
-            if (a.vec) {
+                for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(h[j][i]) & 0x7fffffffu);
+#pragma unroll
+                for (int m = kScaleBlock / V / 2; m > 0; m /= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+                const float scale = scale_of(top), back = 1.f / scale;
+                uint32_t q[V / 4];
+#pragma unroll
+                for (int i = 0; i < V; i += 4) {
+                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(h[j][i] * back, h[j][i + 1] * back),
+                                                                 __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(h[j][i + 2] * back, h[j][i + 3] * back),
+                                                                 __NV_SATFINITE, __NV_E4M3);
+                    q[i / 4] = lo | hi << 16;
+                }
                 if (c < D) {
                     if constexpr (V == 8)
                         *reinterpret_cast<uint2 *>(y + c) = make_uint2(q[0], q[1]);
                     else
                         *reinterpret_cast<uint32_t *>(y + c) = q[0];
+                    if (c % kScaleBlock == 0) scales[c / kScaleBlock] = scale;
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (c + i < D) y[c + i] = static_cast<uint8_t>(q[i / 4] >> (i % 4 * 8));
             }
-            if (c < D && c % kScaleBlock == 0)
-                a.scales[row * ((a.D + kScaleBlock - 1) / kScaleBlock) + c / kScaleBlock] = scale;
+        } else {
+            // a warp's value lies in one block of columns (threads are whole
+            // warps, 32 divides 128); the block's largest is kept in shared
+            // memory (a maximum does not depend on the order)
+            uint32_t *top = tops[WARP ? threadIdx.x / 32 : 0];
+            auto rows_barrier = [] {
+                if constexpr (WARP)
+                    __syncwarp();
+                else
+                    __syncthreads();
+            };
+            rows_barrier();  // the row before has been read
+            for (int b = tid; b < blocks; b += threads) top[b] = 0u;
+            rows_barrier();
+#pragma unroll
+            for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int c = col.at(j, i), b = (c - (tid & 31)) / kScaleBlock;
+                    const uint32_t v = __reduce_max_sync(0xffffffffu, c < D ? __float_as_uint(h[j][i]) & 0x7fffffffu : 0u);
+                    if ((tid & 31) == 0 && b < blocks) atomicMax(&top[b], v);
+                }
+            rows_barrier();
+            for (int b = tid; b < blocks; b += threads) scales[b] = scale_of(top[b]);
+#pragma unroll
+            for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int c = col.at(j, i);
+                    if (c < D)
+                        y[c] = __nv_cvt_float_to_fp8(h[j][i] * (1.f / scale_of(top[c / kScaleBlock])), __NV_SATFINITE,
+                                                     __NV_E4M3);
+                }
         }
     }
 }
@@ -234,7 +288,7 @@ __global__ void __launch_bounds__(kLongThreads) long_norm_kernel(const __grid_co
 // Gradients: dh = r (gn - n mean(gn n)) + grad_residual.  Rows as above; a
 // row's threads keep their sums of dy n in registers and write them as one
 // row of `part` at the end.
-template <class T, class R, bool WARP>
+template <class T, class R, bool WARP, bool VEC>
 __global__ void __maxnreg__(kGradRegisters)
     norm_grad_kernel(const __grid_constant__ NormGradArgs a, float *part)
 {
@@ -246,7 +300,7 @@ __global__ void __maxnreg__(kGradRegisters)
     const int64_t rows = WARP ? kRowWarps : 1, step = gridDim.x * rows;
     const int64_t slot = blockIdx.x * rows + (WARP ? threadIdx.x / 32 : 0);
     int64_t row = slot;
-    const int c0 = tid * V, c1 = c0 + threads * V;
+    const Columns<VEC, V> col{tid, threads, D};
     Words<T, V> gy[kChunks];
     Words<R, V> hr[kChunks], gr[kChunks];
 #pragma unroll
@@ -254,20 +308,21 @@ __global__ void __maxnreg__(kGradRegisters)
     auto load = [&](int64_t at) {
         const T *gp = static_cast<const T *>(a.grad_y) + at * a.grad_y_stride;
         const R *hp = static_cast<const R *>(a.h) + at * a.h_stride;
-        load_raw<R, V>(hr[0], hp, c0, D, a.vec);
-        load_raw<R, V>(hr[1], hp, c1, D, a.vec);
-        load_raw<T, V>(gy[0], gp, c0, D, a.vec);
-        load_raw<T, V>(gy[1], gp, c1, D, a.vec);
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+            load_chunk<VEC>(hr[j], hp, col, j);
+            load_chunk<VEC>(gy[j], gp, col, j);
+        }
         if (a.grad_residual != nullptr) {
             const R *rp = static_cast<const R *>(a.grad_residual) + at * a.grad_residual_stride;
-            load_raw<R, V>(gr[0], rp, c0, D, a.vec);
-            load_raw<R, V>(gr[1], rp, c1, D, a.vec);
+#pragma unroll
+            for (int j = 0; j < kChunks; ++j) load_chunk<VEC>(gr[j], rp, col, j);
         }
     };
     if (row < a.M) load(row);
     Words<float, V> w[kChunks];
-    load_raw<float, V>(w[0], a.weight, c0, D, a.vec);
-    load_raw<float, V>(w[1], a.weight, c1, D, a.vec);
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) load_chunk<VEC>(w[j], a.weight, col, j);
     float dw[kChunks][V];
 #pragma unroll
     for (int j = 0; j < kChunks; ++j)
@@ -294,7 +349,6 @@ __global__ void __maxnreg__(kGradRegisters)
         const float inv = rsqrtf(fmaf(s[0], over, a.eps)), mean = s[1] * inv * over;
 #pragma unroll
         for (int j = 0; j < kChunks; ++j) {
-            const int c = j == 0 ? c0 : c1;
             float v[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -302,13 +356,13 @@ __global__ void __maxnreg__(kGradRegisters)
                 dw[j][i] = fmaf(gv, nv, dw[j][i]);
                 v[i] = fmaf(inv, fmaf(-nv, mean, gv * w[j][i]), r0[j][i]);
             }
-            store_chunk<T, V>(static_cast<T *>(a.grad_x) + row * a.D, v, c, D, a.vec);
-            if (a.grad_h != nullptr) store_chunk<R, V>(static_cast<R *>(a.grad_h) + row * a.D, v, c, D, a.vec);
+            store_chunk<VEC>(static_cast<T *>(a.grad_x) + row * a.D, v, col, j);
+            if (a.grad_h != nullptr) store_chunk<VEC>(static_cast<R *>(a.grad_h) + row * a.D, v, col, j);
         }
     }
     if (part != nullptr) {
-        store_chunk<float, V>(part + slot * a.D, dw[0], c0, D, a.vec);
-        store_chunk<float, V>(part + slot * a.D, dw[1], c1, D, a.vec);
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) store_chunk<VEC>(part + slot * a.D, dw[j], col, j);
     }
 }
 
@@ -358,12 +412,16 @@ int64_t most_blocks(int threads)
     return sms * (per_sm > 0 ? per_sm : 1);
 }
 
-// resident blocks of `kernel` on the device; asked once for each block size
+// Resident blocks of a kernel on the device, asked once for each kernel and
+// block size (`slot` tells apart the kernels of one type).
+constexpr int kSlots = 4;
+int slot_of(int threads, bool vec) { return (threads == 32 ? 2 : 0) + (vec ? 1 : 0); }
+
 template <class K>
-int64_t resident(K kernel, int threads)
+int64_t resident(K kernel, int threads, int slot)
 {
-    static int known[kLongThreads / 32 + 1] = {};
-    int &n = known[threads / 32];
+    static int known[kSlots][kMostThreads / 32 + 1] = {};
+    int &n = known[slot][threads / 32];
     if (n == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1)) {
         cudaGetLastError();
         n = 1;
@@ -372,10 +430,10 @@ int64_t resident(K kernel, int threads)
 }
 
 template <class K>
-int64_t wave(K kernel, int64_t M, int threads)
+int64_t wave(K kernel, int64_t M, int threads, int slot)
 {
     int64_t grid = row_blocks(M, threads);
-    for (int64_t most : {most_blocks(threads), resident(kernel, block_threads(threads))})
+    for (int64_t most : {most_blocks(threads), resident(kernel, block_threads(threads), slot)})
         if (grid > most) grid = most;
     return grid;
 }
@@ -385,9 +443,11 @@ rlscan_status forward(const NormArgs &a, cudaStream_t s)
 {
     const int t = row_threads<T>(a.D);
     if (t == 0) return launch_overlapped(long_norm_kernel<T, R>, a.M, kLongThreads, 0, s, a);
-    if (t == 32)
-        return launch_overlapped(norm_kernel<T, R, true>, wave(norm_kernel<T, R, true>, a.M, t), block_threads(t), 0, s, a);
-    return launch_overlapped(norm_kernel<T, R, false>, wave(norm_kernel<T, R, false>, a.M, t), t, 0, s, a);
+    auto go = [&](auto kernel) {
+        return launch_overlapped(kernel, wave(kernel, a.M, t, slot_of(t, a.vec)), block_threads(t), 0, s, a);
+    };
+    if (t == 32) return a.vec ? go(norm_kernel<T, R, true, true>) : go(norm_kernel<T, R, true, false>);
+    return a.vec ? go(norm_kernel<T, R, false, true>) : go(norm_kernel<T, R, false, false>);
 }
 
 // most rows of `part` that a call fills
@@ -405,16 +465,17 @@ rlscan_status backward(const NormGradArgs &a, float *part, int64_t &parts, cudaS
 {
     const int t = row_threads<T>(a.D);
     if (t == 0) {
-        parts = wave(long_norm_grad_kernel<T, R>, a.M, kLongThreads);
+        const int64_t most = most_blocks(kLongThreads);
+        parts = a.M < most ? a.M : most;
         return launch_overlapped(long_norm_grad_kernel<T, R>, parts, kLongThreads, 0, s, a, part);
     }
-    if (t == 32) {
-        const int64_t grid = wave(norm_grad_kernel<T, R, true>, a.M, t);
-        parts = grid * kRowWarps;
-        return launch_overlapped(norm_grad_kernel<T, R, true>, grid, block_threads(t), 0, s, a, part);
-    }
-    parts = wave(norm_grad_kernel<T, R, false>, a.M, t);
-    return launch_overlapped(norm_grad_kernel<T, R, false>, parts, t, 0, s, a, part);
+    auto go = [&](auto kernel) {
+        const int64_t grid = wave(kernel, a.M, t, slot_of(t, a.vec));
+        parts = grid * (t == 32 ? kRowWarps : 1);
+        return launch_overlapped(kernel, grid, block_threads(t), 0, s, a, part);
+    };
+    if (t == 32) return a.vec ? go(norm_grad_kernel<T, R, true, true>) : go(norm_grad_kernel<T, R, true, false>);
+    return a.vec ? go(norm_grad_kernel<T, R, false, true>) : go(norm_grad_kernel<T, R, false, false>);
 }
 
 uint64_t low_bits(const void *p) { return reinterpret_cast<uintptr_t>(p); }

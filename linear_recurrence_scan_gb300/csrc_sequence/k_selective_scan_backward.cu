@@ -50,7 +50,8 @@ struct Shape {
     static constexpr int PITCH = CH * static_cast<int>(sizeof(T));
     static constexpr int BPITCH = SP * static_cast<int>(sizeof(T));
     static constexpr int ACT = kTile * PITCH, BC = kTile * BPITCH, MARK = THREADS * 64;
-    static constexpr int STAGE = 4 * ACT + 2 * BC + MARK, STAGES = 2;
+    // two stages, or one where two would leave a single block an SM (float32)
+    static constexpr int STAGE = 4 * ACT + 2 * BC + MARK, STAGES = sizeof(T) == 4 ? 1 : 2;
     static constexpr int F = kTile * CW;                    // floats of one array of a warp
     static constexpr int MINE = LANES >= 4 ? 1 : 4 / LANES;  // channels whose sums a lane ends up with
     static constexpr int WIDE = 2 * kTile * SP * 8;         // B and C, each value twice
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
         const int left = len - t0 < kTile ? static_cast<int>(len - t0) : kTile;
         copies_wait<0>();
         __syncthreads();  // the tile is here, and the buffer of the one before is free
-        issue(tile - 1);
+        if (P::STAGES > 1) issue(tile - 1);
         const char *st = smem + tile % P::STAGES * P::STAGE;
         const uint32_t starts =
             resets != nullptr ? __ballot_sync(0xffffffffu, lane < left && resets[t0 + lane] != 0) : 0u;
@@ -402,6 +403,7 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
         else
             walk(std::false_type());
         __syncthreads();
+        if (P::STAGES == 1) issue(tile - 1);
         add_dA(false);
 #pragma unroll
         for (int m = 0; m < P::MINE; ++m) {

@@ -74,16 +74,36 @@ def _lead(name, t, dims):
     return t.get_device()
 
 
+# The checks of every call cost as much as a small kernel, so the usual case
+# asks a tensor for no more than what decides: its type, shape and device (-1
+# for a CPU tensor).  Whatever is out of order goes through _check, which
+# says what.
+
 def _act(name, t, shape, dtype, device):
-    """An activation: any strides over rows and tokens, element stride 1."""
-    _check(name, t, shape, dtype, device)
-    return t if t.stride(-1) == 1 or shape[-1] <= 1 else t.contiguous()
+    """(address, row stride, token stride, tensor) of an activation: any strides
+    over rows and tokens, element stride 1."""
+    try:
+        fits = t.dtype is dtype and t.shape == shape and t.get_device() == device
+    except AttributeError:
+        fits = False
+    if not fits:
+        _check(name, t, shape, dtype, device)
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
+        t = t.contiguous()
+        strides = t.stride()
+    return t.data_ptr(), strides[0], (strides[1] if len(strides) == 3 else 0), t
 
 
 def _dense(name, t, shape, dtype, device):
     """A dense array or None."""
     if t is None:
         return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t
+    except AttributeError:
+        pass
     _check(name, t, shape, dtype, device)
     return t if t.is_contiguous() else t.contiguous()
 
@@ -100,18 +120,15 @@ def _at(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _strides(t):
-    """(address, row stride, token stride) of an activation."""
-    if t is None:
-        return 0, 0, 0
-    if t.dim() == 2:
-        return t.data_ptr(), t.stride(0), 0
-    return t.data_ptr(), t.stride(0), t.stride(1)
+_NONE = (0, 0, 0, None)
 
 
 def _wants_grad(*ts):
-    return torch.is_grad_enabled() and any(t is not None and isinstance(t, torch.Tensor) and t.requires_grad
-                                           for t in ts)
+    if torch.is_grad_enabled():
+        for t in ts:
+            if t is not None and getattr(t, "requires_grad", False):
+                return True
+    return False
 
 
 def _scratch(nbytes, device):
@@ -147,21 +164,23 @@ def _scan_args(step, x, delta, A, B, C, D, z, delta_bias, delta_softplus, initia
     f32 = torch.float32
     A = _dense("A", A, (width, S), f32, dev)
     bc = (N, S) if step else (N, T, S)
-    x = _act("x", x, shape, dtype, dev)
-    delta = _act("delta", delta, shape, dtype, dev)
-    B = _act("B", B, bc, dtype, dev)
-    C = _act("C", C, bc, dtype, dev)
-    if z is not None:
-        z = _act("z", z, shape, dtype, dev)
+    xp, xr, xt, x = _act("x", x, shape, dtype, dev)
+    dp, dr, dt, delta = _act("delta", delta, shape, dtype, dev)
+    Bp, Br, Bt, B = _act("B", B, bc, dtype, dev)
+    Cp, Cr, Ct, C = _act("C", C, bc, dtype, dev)
+    zp, zr, zt, z = _NONE if z is None else _act("z", z, shape, dtype, dev)
     D = _dense("D", D, (width,), f32, dev)
     delta_bias = _dense("delta_bias", delta_bias, (width,), f32, dev)
-    initial_state = _dense("initial_state", initial_state, (N, width, S), f32, dev)
-    resets = _flags(resets, (N, T), dev)
-    lengths = _dense("lengths", lengths, (N,), torch.int32, dev)
+    if initial_state is not None:
+        initial_state = _dense("initial_state", initial_state, (N, width, S), f32, dev)
+    if resets is not None:
+        resets = _flags(resets, (N, T), dev)
+    if lengths is not None:
+        lengths = _dense("lengths", lengths, (N,), torch.int32, dev)
     kept = (x, delta, z, B, C, A, D, delta_bias, initial_state, resets, lengths)
-    packed = _SCAN_ARGS.pack(
-        N, T, width, S, _TYPES[dtype], 1 if delta_softplus else 0, *_strides(x), *_strides(delta), *_strides(z),
-        *_strides(B), *_strides(C), _at(A), _at(D), _at(delta_bias), _at(initial_state), _at(resets), _at(lengths))
+    packed = _SCAN_ARGS.pack(N, T, width, S, _TYPES[dtype], 1 if delta_softplus else 0, xp, xr, xt, dp, dr, dt, zp, zr,
+                             zt, Bp, Br, Bt, Cp, Cr, Ct, A.data_ptr(), _at(D), _at(delta_bias), _at(initial_state),
+                             _at(resets), _at(lengths))
     return dev, (N, T, width, S), packed, kept
 
 
@@ -238,7 +257,7 @@ def selective_scan_backward(grad_y, x, delta, A, B, C, checkpoints, D=None, z=No
                                                      None, resets, lengths)
     x = kept[0]
     dtype, f32 = x.dtype, torch.float32
-    grad_y = _act("grad_y", grad_y, x.shape, dtype, dev)
+    gp, gr, gt, grad_y = _act("grad_y", grad_y, x.shape, dtype, dev)
     marks = _dense("checkpoints", checkpoints, (N, -(-T // CHECKPOINT), width, S), f32, dev)
     if marks is None:
         raise ValueError("checkpoints is required (selective_scan(..., return_checkpoints=True))")
@@ -255,7 +274,7 @@ def selective_scan_backward(grad_y, x, delta, A, B, C, checkpoints, D=None, z=No
     lib = _native.lib()
     ws = _scratch(lib.rlscan_selective_scan_backward_workspace_bytes(packed), x.device)
     _native.check(lib.rlscan_selective_scan_backward(
-        packed, _ARRAY3.pack(*_strides(grad_y)), _at(gfinal), marks.data_ptr(),
+        packed, _ARRAY3.pack(gp, gr, gt), _at(gfinal), marks.data_ptr(),
         _SCAN_GRADS.pack(_at(g.x), _at(g.delta), _at(g.z), _at(g.B), _at(g.C), _at(g.A), _at(g.D),
                          _at(g.delta_bias), _at(g.initial_state)),
         _at(ws), 0 if ws is None else ws.numel(), _stream_handle(x.device)), "rlscan_selective_scan_backward")
@@ -284,10 +303,12 @@ def _slot_pool(state, shape, dtype, device):
     """The number of slots of a state that is updated in place."""
     if not isinstance(state, torch.Tensor) or state.dim() != 3:
         raise ValueError("state must be a [slots, ...] tensor of 3 dimensions")
-    _check("state", state, (state.shape[0], *shape), dtype, device)
+    whole = state.shape
+    if state.dtype is not dtype or whole[1:] != shape or state.get_device() != device:
+        _check("state", state, (whole[0], *shape), dtype, device)
     if not state.is_contiguous():
         raise ValueError("state must be contiguous: it is updated in place")
-    return state.shape[0]
+    return whole[0]
 
 
 # ---------------------------------------------------------------------------
@@ -314,11 +335,14 @@ def _conv_args(step, x, weight, bias, activation, initial_state, resets, lengths
         raise ValueError(f"weight has {K} taps: 1 to {MAX_TAPS} are supported")
     weight = _dense("weight", weight, (width, K), torch.float32, dev)
     bias = _dense("bias", bias, (width,), torch.float32, dev)
-    x = _act("x", x, shape, dtype, dev)
-    initial_state = _dense("initial_state", initial_state, (N, K - 1, width), dtype, dev)
-    resets = _flags(resets, (N, T), dev)
-    lengths = _dense("lengths", lengths, (N,), torch.int32, dev)
-    packed = _CONV_ARGS.pack(N, T, width, K, _TYPES[dtype], 1 if activation else 0, *_strides(x), _at(weight),
+    xp, xr, xt, x = _act("x", x, shape, dtype, dev)
+    if initial_state is not None:
+        initial_state = _dense("initial_state", initial_state, (N, K - 1, width), dtype, dev)
+    if resets is not None:
+        resets = _flags(resets, (N, T), dev)
+    if lengths is not None:
+        lengths = _dense("lengths", lengths, (N,), torch.int32, dev)
+    packed = _CONV_ARGS.pack(N, T, width, K, _TYPES[dtype], 1 if activation else 0, xp, xr, xt, weight.data_ptr(),
                              _at(bias), _at(initial_state), _at(resets), _at(lengths))
     return dev, (N, T, width, K), packed, (x, weight, bias, initial_state, resets, lengths)
 
@@ -375,7 +399,7 @@ def causal_conv_backward(grad_y, x, weight, bias=None, activation="silu", initia
     type or None).  Returns CausalConvGrads."""
     dev, (N, T, width, K), packed, kept = _conv_args(False, x, weight, bias, activation, initial_state, resets, lengths)
     x = kept[0]
-    grad_y = _act("grad_y", grad_y, x.shape, x.dtype, dev)
+    gp, gr, gt, grad_y = _act("grad_y", grad_y, x.shape, x.dtype, dev)
     gfinal = _dense("grad_final_state", grad_final_state, (N, K - 1, width), x.dtype, dev)
     f32 = dict(dtype=torch.float32, device=x.device)
     g = CausalConvGrads(
@@ -385,7 +409,7 @@ def causal_conv_backward(grad_y, x, weight, bias=None, activation="silu", initia
     lib = _native.lib()
     ws = _scratch(lib.rlscan_causal_conv_backward_workspace_bytes(packed), x.device)
     _native.check(lib.rlscan_causal_conv_backward(
-        packed, _ARRAY3.pack(*_strides(grad_y)), _at(gfinal), g.x.data_ptr(), g.weight.data_ptr(), _at(g.bias),
+        packed, _ARRAY3.pack(gp, gr, gt), _at(gfinal), g.x.data_ptr(), g.weight.data_ptr(), _at(g.bias),
         g.initial_state.data_ptr(), _at(ws), 0 if ws is None else ws.numel(), _stream_handle(x.device)),
         "rlscan_causal_conv_backward")
     return g
@@ -426,22 +450,32 @@ class RmsNormGrads(NamedTuple):
 
 def _rows(name, t, shape, dtype, device):
     """(tensor, address, row stride) of [..., D] as rows of D elements."""
-    _check(name, t, shape, dtype, device)
-    if t.dim() != 2:
+    try:
+        fits = t.dtype is dtype and t.shape == shape and t.get_device() == device
+    except AttributeError:
+        fits = False
+    if not fits:
+        _check(name, t, shape, dtype, device)
+    if len(shape) != 2:
         t = t.reshape(-1, shape[-1])
-    if t.stride(1) != 1 and shape[-1] > 1:
+    strides = t.stride()
+    if strides[1] != 1 and shape[-1] > 1:
         t = t.contiguous()
-    return t, t.data_ptr(), t.stride(0)
+        strides = t.stride()
+    return t, t.data_ptr(), strides[0]
 
 
 def _norm_lead(name, x, weight, eps):
     if not isinstance(x, torch.Tensor) or x.dim() < 2:
         raise ValueError(f"{name} must be a [..., channels] tensor of at least 2 dimensions")
-    dev = _lead(name, x, x.dim())
+    dev = x.get_device()
+    if dev < 0 or x.dtype not in _TYPES:
+        _lead(name, x, x.dim())
     if not float(eps) >= 0:
         raise ValueError("eps must not be negative")
-    width = x.shape[-1]
-    M = x.numel() // width if width else 0
+    shape = x.shape
+    width = shape[-1]
+    M = shape[0] if len(shape) == 2 else (x.numel() // width if width else 0)
     return dev, M, width, _dense("weight", weight, (width,), torch.float32, dev)
 
 
