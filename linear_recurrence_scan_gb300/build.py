@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")                    # the estimators' scan kernels
@@ -49,6 +50,26 @@ def _stale(target, deps):
 
 
 CHECKED_DIR = os.path.join(OUT_DIR, "checked")
+FASTCALL = os.path.join(OUT_DIR, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
+def build_fastcall(force: bool = False):
+    """Compile the latency-bound calls' argument handling (fastcall.c, plain
+    Python C API) in-tree; returns its path, or None where this Python has no
+    headers (the calls then handle their arguments in Python)."""
+    src, include = os.path.join(CSRC_SEQUENCE, "fastcall.c"), sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    if not force and not _stale(FASTCALL, [src, os.path.join(INCLUDE, "rlscan.h")]):
+        return FASTCALL
+    os.makedirs(OUT_DIR, exist_ok=True)
+    tmp = FASTCALL + ".tmp%d" % os.getpid()
+    cmd = ["gcc", "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", include, "-I", INCLUDE, src, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on fastcall.c:\n{r.stderr}")
+    os.replace(tmp, FASTCALL)
+    return FASTCALL
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), out_dir: str = OUT_DIR) -> str:
@@ -56,6 +77,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), out_dir: s
     Rebuilds only when a source or header is newer than the library (or
     ``force``)."""
     lib_path = os.path.join(out_dir, "librlscan.so")
+    if out_dir == OUT_DIR:
+        build_fastcall(force)
     srcs = _sources()
     deps = srcs + _headers() + [os.path.abspath(__file__)]
     if not force and not _stale(lib_path, deps):

@@ -15,13 +15,17 @@ the ``*_backward`` functions are the same gradients as plain calls.
 """
 from __future__ import annotations
 
+import ctypes
+import importlib.machinery
+import importlib.util
+import os
 import struct
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _native
-from .api import _stream_handle
+from .api import _raw_stream, _stream_handle
 
 __all__ = [
     "selective_scan", "selective_scan_backward", "selective_scan_step", "SelectiveScanGrads",
@@ -39,6 +43,42 @@ _SCAN_ARGS = struct.Struct("=27q")
 _SCAN_GRADS = struct.Struct("=9q")
 _CONV_ARGS = struct.Struct("=14q")
 _ARRAY3 = struct.Struct("=3q")
+
+
+# ---------------------------------------------------------------------------
+# calls in the usual form (csrc_sequence/fastcall.c), where it has been built
+
+class _NoFastCall:
+    """Leaves every call to the Python way."""
+
+    @staticmethod
+    def _none(*args):
+        return None
+
+    selective_scan = selective_scan_step = causal_conv = causal_conv_step = add_rms_norm = _none
+
+
+_fast = None
+
+
+def _load_fast():
+    """The native call layer, or one that leaves all to Python."""
+    global _fast
+    if _fast is None:
+        path = os.path.join(_native.HERE, "_build", "_fastcall" + importlib.machinery.EXTENSION_SUFFIXES[0])
+        if not os.path.exists(path) or _raw_stream is None:
+            _fast = _NoFastCall
+        else:
+            lib = _native.lib()
+            spec = importlib.util.spec_from_file_location("_fastcall", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.setup(torch, RmsNorm, _raw_stream, *(
+                ctypes.cast(getattr(lib, "rlscan_" + name), ctypes.c_void_p).value for name in (
+                    "selective_scan_workspace_bytes", "selective_scan", "selective_scan_step", "causal_conv",
+                    "causal_conv_step", "add_rms_norm")))
+            _fast = module
+    return _fast
 
 
 # ---------------------------------------------------------------------------
@@ -240,6 +280,11 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_sof
     states [N,channels,S] float32 after each row's last token.  With
     ``return_checkpoints`` a third value, what selective_scan_backward
     needs: the states before every 16th token."""
+    if not return_checkpoints:
+        out = (_fast or _load_fast()).selective_scan(x, delta, A, B, C, D, z, delta_bias, delta_softplus,
+                                                     initial_state, resets, lengths)
+        if out is not None:
+            return out
     if not return_checkpoints and _wants_grad(x, delta, A, B, C, D, z, delta_bias, initial_state):
         return _SelectiveScan.apply(x, delta, A, B, C, D, z, delta_bias, delta_softplus, initial_state, resets,
                                     lengths)
@@ -287,6 +332,9 @@ def selective_scan_step(state, x, delta, A, B, C, D=None, z=None, delta_bias=Non
     has the state of slot ``slots[n]`` (int32; None: slot n); a slot outside
     0..P-1 marks an idle sequence, whose y is 0.  The slots of a call are
     distinct.  Returns y [N,channels].  Not differentiable."""
+    y = (_fast or _load_fast()).selective_scan_step(state, x, delta, A, B, C, D, z, delta_bias, delta_softplus, slots)
+    if y is not None:
+        return y
     dev, (N, _, width, S), packed, kept = _scan_args(True, x, delta, A, B, C, D, z, delta_bias, delta_softplus, None,
                                                      None, None)
     P = _slot_pool(state, (width, S), torch.float32, dev)
@@ -388,6 +436,9 @@ def causal_conv(x, weight, bias=None, activation="silu", initial_state=None, res
     and ``lengths`` as in selective_scan: taps stay inside their token's
     episode.  Returns (y, final_state): the last K-1 inputs of each row, zero
     where they lie before its last episode."""
+    out = (_fast or _load_fast()).causal_conv(x, weight, bias, activation, initial_state, resets, lengths)
+    if out is not None:
+        return out
     if _wants_grad(x, weight, bias, initial_state):
         return _CausalConv.apply(x, weight, bias, activation, initial_state, resets, lengths)
     return _conv_forward(x, weight, bias, activation, initial_state, resets, lengths)
@@ -420,6 +471,9 @@ def causal_conv_step(state, x, weight, bias=None, activation="silu", slots=None)
     [P,K-1,channels] of x's type (dense) is shifted by one token in place.
     ``slots`` as in selective_scan_step.  Returns y [N,channels].  Not
     differentiable."""
+    y = (_fast or _load_fast()).causal_conv_step(state, x, weight, bias, activation, slots)
+    if y is not None:
+        return y
     dev, (N, _, width, K), packed, kept = _conv_args(True, x, weight, bias, activation, None, None, None)
     P = _slot_pool(state, (K - 1, width), x.dtype, dev)
     slots = _dense("slots", slots, (N,), torch.int32, dev)
@@ -534,6 +588,9 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None):
     ``out_dtype=torch.float8_e4m3fn`` gives y in 8 bits with a float32 scale
     for each 128 columns of a row (y stands for y.float() * its scale); that
     form is not differentiable."""
+    out = (_fast or _load_fast()).add_rms_norm(x, weight, residual, eps, out_dtype)
+    if out is not None:
+        return out
     if out_dtype != torch.float8_e4m3fn and _wants_grad(x, weight, residual):
         if out_dtype not in (None, x.dtype):
             raise ValueError("out_dtype must be x's type or torch.float8_e4m3fn")

@@ -653,3 +653,44 @@ def test_refusals():
         L().add_rms_norm(x, nw, x.bfloat16())
     with pytest.raises(ValueError):
         L().add_rms_norm(x, nw[:-1])
+
+
+def test_the_native_call_layer_is_the_python_way(monkeypatch):
+    """Calls in the usual form go through the native layer; the Python way gives the same bits."""
+    from linear_recurrence_scan_gb300 import state_space as ss
+    fast = ss._load_fast()
+    assert fast is not ss._NoFastCall
+    N, T, D, S, K = 2, 40, 32, 16, 4
+    a, init, resets, _, _ = scan_inputs(N, T, D, S, BF16, 23, "packed")
+    dev = {k: v.to(DEV) for k, v in a.items()}
+    step = {k: (v[:, 0] if k in ("x", "delta", "z", "B", "C") else v) for k, v in dev.items()}
+    w, nw = torch.randn(D, K, device=DEV), torch.randn(D, device=DEV)
+    lengths = torch.tensor([T, 7], dtype=torch.int32, device=DEV)
+    slots = torch.tensor([1, 0], dtype=torch.int32, device=DEV)
+    rows = dev["x"].view(-1, D)
+    window = torch.randn(N, K - 1, D, device=DEV).to(BF16)
+
+    def calls():
+        state, win = init.to(DEV), window.clone()
+        n = L().add_rms_norm(rows, nw, rows)
+        q = L().add_rms_norm(rows, nw, rows.float(), out_dtype=torch.float8_e4m3fn)
+        return [*L().selective_scan(**dev), *L().selective_scan(**dev, initial_state=init.to(DEV),
+                                                                resets=to_dev(resets), lengths=lengths),
+                L().selective_scan_step(state, **step, slots=slots), state,
+                *L().causal_conv(dev["x"], w, nw, None, window, to_dev(resets).bool(), lengths),
+                L().causal_conv_step(win, step["x"], w, nw, slots=slots), win, n.y, n.residual, q.y.view(torch.uint8),
+                q.scales, q.residual]
+
+    got = calls()
+    assert fast.selective_scan_step(init.to(DEV), *(step[k] for k in ("x", "delta", "A", "B", "C", "D", "z",
+                                                                      "delta_bias")), True, None) is not None
+    assert fast.add_rms_norm(rows, nw, None, 1e-6, None) is not None
+    # what is not in the usual form is left to Python
+    assert fast.add_rms_norm(rows, nw.bfloat16(), None, 1e-6, None) is None
+    assert fast.add_rms_norm(rows, nw.clone().requires_grad_(), None, 1e-6, None) is None
+    assert fast.causal_conv(dev["x"].cpu(), w, None, "silu", None, None, None) is None
+    with torch.no_grad():
+        assert fast.add_rms_norm(rows, torch.nn.Parameter(nw), None, 1e-6, None) is not None
+    monkeypatch.setattr(ss, "_fast", ss._NoFastCall)
+    for p, q in zip(got, calls()):
+        assert torch.equal(p, q)
