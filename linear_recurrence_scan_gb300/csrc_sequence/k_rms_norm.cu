@@ -41,28 +41,31 @@ struct Columns {
     __device__ __forceinline__ int at(int j, int i) const { return VEC ? first(j) + i : first(j) + i * threads; }
 };
 
+// The values of a chunk as loaded: V side by side, or a register each (put
+// together at once they would wait for their loads at once).
+template <bool VEC, class E, int V>
+struct Held {
+    Words<E, VEC ? V : 1> v[VEC ? 1 : V];
+    __device__ __forceinline__ float operator[](int i) const
+    {
+        if constexpr (VEC) return v[0][i];
+        return v[VEC ? 0 : i][0];
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < (VEC ? 1 : V); ++i) v[i].zero();
+    }
+};
+
 // chunk j of a row, 0 past its end
 template <bool VEC, class E, int V>
-__device__ __forceinline__ void load_chunk(Words<E, V> &r, const E *p, const Columns<VEC, V> &c, int j)
+__device__ __forceinline__ void load_chunk(Held<VEC, E, V> &r, const E *p, const Columns<VEC, V> &c, int j)
 {
     r.zero();
-    if constexpr (VEC) {
-        if (c.first(j) < c.D) r.load(p + c.first(j));
-    } else if constexpr (sizeof(E) == 4) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (c.at(j, i) < c.D) r.w[i] = *reinterpret_cast<const uint32_t *>(p + c.at(j, i));
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; i += 2) {
-            Words<E, 1> lo, hi;
-            lo.zero();
-            hi.zero();
-            if (c.at(j, i) < c.D) lo.load(p + c.at(j, i));
-            if (c.at(j, i + 1) < c.D) hi.load(p + c.at(j, i + 1));
-            r.w[i / 2] = lo.w[0] | hi.w[0] << 16;
-        }
-    }
+    for (int i = 0; i < (VEC ? 1 : V); ++i)
+        if (c.at(j, i) < c.D) r.v[i].load(p + c.at(j, i));
 }
 
 template <bool VEC, class E, int V>
@@ -107,7 +110,7 @@ __device__ __forceinline__ void row_sums(float *v, float (*scratch)[32][N], int 
 // A block walks rows in strides of the grid: the next row's loads are in
 // flight while this row's sum and outputs are made.
 template <class T, class R, bool WARP, bool VEC>
-__global__ void __maxnreg__(kNormRegisters) norm_kernel(const __grid_constant__ NormArgs a)
+__global__ void __maxnreg__(VEC ? kNormRegisters : 128) norm_kernel(const __grid_constant__ NormArgs a)
 {
     constexpr int V = kVec<T>;
     __shared__ float scratch[2][32][1];
@@ -119,8 +122,8 @@ __global__ void __maxnreg__(kNormRegisters) norm_kernel(const __grid_constant__ 
     int64_t row = blockIdx.x * rows + (WARP ? threadIdx.x / 32 : 0);
     const Columns<VEC, V> col{tid, threads, D};
     const bool summed = a.residual != nullptr;
-    Words<T, V> x[kChunks];
-    Words<R, V> r[kChunks];
+    Held<VEC, T, V> x[kChunks];
+    Held<VEC, R, V> r[kChunks];
     auto load = [&](int64_t at) {
         const T *xp = static_cast<const T *>(a.x) + at * a.x_stride;
 #pragma unroll
@@ -131,7 +134,7 @@ __global__ void __maxnreg__(kNormRegisters) norm_kernel(const __grid_constant__ 
             for (int j = 0; j < kChunks; ++j) load_chunk<VEC>(r[j], rp, col, j);
         }
     };
-    Words<float, V> w[kChunks];
+    Held<VEC, float, V> w[kChunks];
     if (row < a.M) load(row);
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) load_chunk<VEC>(w[j], a.weight, col, j);
@@ -218,14 +221,19 @@ __global__ void __maxnreg__(kNormRegisters) norm_kernel(const __grid_constant__ 
                     if ((tid & 31) == 0 && b < blocks) atomicMax(&top[b], v);
                 }
             rows_barrier();
-            for (int b = tid; b < blocks; b += threads) scales[b] = scale_of(top[b]);
+            for (int b = tid; b < blocks; b += threads) {
+                const float scale = scale_of(top[b]);
+                scales[b] = scale;
+                top[b] = __float_as_uint(1.f / scale);
+            }
+            rows_barrier();
 #pragma unroll
             for (int j = 0; j < kChunks; ++j)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int c = col.at(j, i);
                     if (c < D)
-                        y[c] = __nv_cvt_float_to_fp8(h[j][i] * (1.f / scale_of(top[c / kScaleBlock])), __NV_SATFINITE,
+                        y[c] = __nv_cvt_float_to_fp8(h[j][i] * __uint_as_float(top[c / kScaleBlock]), __NV_SATFINITE,
                                                      __NV_E4M3);
                 }
         }
@@ -301,8 +309,8 @@ __global__ void __maxnreg__(kGradRegisters)
     const int64_t slot = blockIdx.x * rows + (WARP ? threadIdx.x / 32 : 0);
     int64_t row = slot;
     const Columns<VEC, V> col{tid, threads, D};
-    Words<T, V> gy[kChunks];
-    Words<R, V> hr[kChunks], gr[kChunks];
+    Held<VEC, T, V> gy[kChunks];
+    Held<VEC, R, V> hr[kChunks], gr[kChunks];
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) gr[j].zero();
     auto load = [&](int64_t at) {
@@ -320,7 +328,7 @@ __global__ void __maxnreg__(kGradRegisters)
         }
     };
     if (row < a.M) load(row);
-    Words<float, V> w[kChunks];
+    Held<VEC, float, V> w[kChunks];
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) load_chunk<VEC>(w[j], a.weight, col, j);
     float dw[kChunks][V];
@@ -330,8 +338,8 @@ __global__ void __maxnreg__(kGradRegisters)
         for (int i = 0; i < V; ++i) dw[j][i] = 0.f;
     const float over = 1.f / static_cast<float>(D);
     for (int flip = 0; row < a.M; row += step, flip ^= 1) {
-        Words<T, V> g0[kChunks];
-        Words<R, V> h0[kChunks], r0[kChunks];
+        Held<VEC, T, V> g0[kChunks];
+        Held<VEC, R, V> h0[kChunks], r0[kChunks];
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < kChunks; ++j) {

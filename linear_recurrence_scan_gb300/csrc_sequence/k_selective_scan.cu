@@ -42,20 +42,120 @@ Plan plan(const rlscan_selective_scan_args &a)
 
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
-}  // namespace
-
-size_t selective_scan_workspace(const rlscan_selective_scan_args &a)
+size_t chunk_workspace(const rlscan_selective_scan_args &a, const Plan &p)
 {
-    const Plan p = plan(a);
     if (p.chunks <= 1) return 0;
     const size_t each = static_cast<size_t>(a.N) * p.chunks;
     return up(each * a.D * a.S * 4) + up(each * a.D * 4) + up(each);
 }
 
-rlscan_status launch_selective_scan(const rlscan_selective_scan_args &a, void *y, float *final_state,
+// ---- rows of 2-byte alignment -----------------------------------------------
+
+constexpr int kRealigned = 6;  // x, delta, z, grad_y, B, C
+
+struct RealignJobs {
+    struct Job {
+        rlscan_array3 from;
+        uint32_t *to;        // rows of `words` pairs of values
+        int64_t T, width, words, rows;
+    } job[kRealigned];
+    int jobs;
+};
+
+int64_t padded(int64_t width) { return (width + 7) / 8 * 8; }
+
+// A warp copies a row, neighbouring lanes neighbouring pairs of values.
+__global__ void __launch_bounds__(256) realign_kernel(const __grid_constant__ RealignJobs r)
+{
+    ptx::pdl_trigger_dependents();
+    ptx::pdl_wait_prerequisites();
+    const RealignJobs::Job &job = r.job[blockIdx.y];
+    const int lane = threadIdx.x & 31, width = static_cast<int>(job.width), words = static_cast<int>(job.words);
+    for (int64_t row = blockIdx.x * 8ll + threadIdx.x / 32; row < job.rows; row += gridDim.x * 8ll) {
+        const Division at = divide(row, job.T);
+        const uint16_t *p =
+            static_cast<const uint16_t *>(job.from.data) + at.q * job.from.row_stride + at.r * job.from.token_stride;
+        uint32_t *to = job.to + row * words;
+#pragma unroll 8
+        for (int i = lane; i < words; i += 32) {
+            const uint32_t lo = 2 * i < width ? p[2 * i] : 0u, hi = 2 * i + 1 < width ? p[2 * i + 1] : 0u;
+            to[i] = lo | hi << 16;
+        }
+    }
+}
+
+bool odd_rows(const rlscan_selective_scan_args &a)
+{
+    Chunk c;
+    for (const rlscan_array3 *v : {&a.x, &a.delta, &a.B, &a.C}) c.add(v->data, v->row_stride, v->token_stride, 2);
+    if (a.z.data != nullptr) c.add(a.z.data, a.z.row_stride, a.z.token_stride, 2);
+    return c.size() == 0;
+}
+
+}  // namespace
+
+size_t realign_workspace(const rlscan_selective_scan_args &a, bool backward)
+{
+    if (a.dtype != RLSCAN_BF16 || a.N * a.T * a.D < (1 << 18) || !odd_rows(a)) return 0;
+    const size_t rows = 2 * static_cast<size_t>(a.N) * a.T;
+    return up(rows * padded(a.D)) * (backward ? 4 : 3) + up(rows * padded(a.S)) * 2;
+}
+
+rlscan_status realign(rlscan_selective_scan_args &a, rlscan_array3 *grad_y, char *ws, cudaStream_t s)
+{
+    RealignJobs r;
+    r.jobs = 0;
+    auto take = [&](rlscan_array3 &v, int64_t width) {
+        if (v.data == nullptr) return;
+        RealignJobs::Job &j = r.job[r.jobs++];
+        j.from = v;
+        j.to = reinterpret_cast<uint32_t *>(ws);
+        j.T = a.T;
+        j.width = width;
+        j.words = padded(width) / 2;
+        j.rows = a.N * a.T;
+        v.data = ws;
+        v.token_stride = padded(width);
+        v.row_stride = a.T * v.token_stride;
+        ws += up(2 * static_cast<size_t>(a.N) * a.T * padded(width));
+    };
+    take(a.x, a.D);
+    take(a.delta, a.D);
+    take(a.z, a.D);
+    take(a.B, a.S);
+    take(a.C, a.S);
+    if (grad_y != nullptr) take(*grad_y, a.D);
+    const int64_t sms = sm_count() > 0 ? sm_count() : 152, need = ceil_div(a.N * a.T, 8);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(need < 8 * sms ? need : 8 * sms), static_cast<unsigned>(r.jobs));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, realign_kernel, r) != cudaSuccess) {
+        cudaGetLastError();
+        return RLSCAN_ERR_CUDA;
+    }
+    return RLSCAN_OK;
+}
+
+size_t selective_scan_workspace(const rlscan_selective_scan_args &a)
+{
+    return chunk_workspace(a, plan(a)) + realign_workspace(a, false);
+}
+
+rlscan_status launch_selective_scan(const rlscan_selective_scan_args &args, void *y, float *final_state,
                                     float *checkpoints, void *ws, cudaStream_t s)
 {
+    rlscan_selective_scan_args a = args;
     const Plan p = plan(a);
+    if (realign_workspace(a, false) > 0) {
+        const rlscan_status st = realign(a, nullptr, static_cast<char *>(ws) + chunk_workspace(a, p), s);
+        if (st != RLSCAN_OK) return st;
+    }
     ScanOut o{y, final_state, checkpoints, p.chunk, p.chunks, 0, false, nullptr, nullptr, nullptr, {}};
     if (p.chunks > 1) {
         const size_t each = static_cast<size_t>(a.N) * p.chunks;

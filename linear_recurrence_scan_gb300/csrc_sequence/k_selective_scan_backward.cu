@@ -11,7 +11,7 @@
 // the shuffles that one channel a lane would need.  What each channel and
 // token needs once (softplus, the gate, the outputs) is shared out over the
 // lanes through shared memory.
-#include "sequence.cuh"
+#include "scan_plan.cuh"
 
 namespace rlscan {
 namespace seq {
@@ -493,7 +493,7 @@ int grad_lanes(int64_t S)
 // work), while there are less than 1.5 blocks an SM without.
 struct Layout {
     int64_t blocks, chunk, chunks;
-    size_t B, C, A, d, states, spans, cuts, bytes;
+    size_t B, C, A, d, states, spans, cuts, realigned, bytes;
 };
 
 Layout layout(const rlscan_selective_scan_args &a)
@@ -524,6 +524,7 @@ Layout layout(const rlscan_selective_scan_args &a)
     l.states = take(split ? F * each * a.D * a.S : 0);
     l.spans = take(split ? F * each * a.D : 0);
     l.cuts = take(split ? each : 0);
+    l.realigned = take(realign_workspace(a, true));
     l.bytes = at;
     return l;
 }
@@ -567,12 +568,18 @@ rlscan_status launch_sums(const SumJobs &jobs, cudaStream_t s)
 
 size_t selective_scan_backward_workspace(const rlscan_selective_scan_args &a) { return layout(a).bytes; }
 
-rlscan_status launch_selective_scan_backward(const rlscan_selective_scan_args &a, const rlscan_array3 &grad_y,
+rlscan_status launch_selective_scan_backward(const rlscan_selective_scan_args &args, const rlscan_array3 &grad,
                                              const float *grad_final_state, const float *checkpoints,
                                              const rlscan_selective_scan_grads &g, void *ws, cudaStream_t s)
 {
+    rlscan_selective_scan_args a = args;
+    rlscan_array3 grad_y = grad;
     const Layout l = layout(a);
     char *w = static_cast<char *>(ws);
+    if (realign_workspace(a, true) > 0) {
+        const rlscan_status st = realign(a, &grad_y, w + l.realigned, s);
+        if (st != RLSCAN_OK) return st;
+    }
     GradArgs k;
     k.grad_y = grad_y;
     k.grad_final = grad_final_state;

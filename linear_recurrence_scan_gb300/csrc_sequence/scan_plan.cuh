@@ -28,6 +28,14 @@ struct Plan {
     int64_t chunk, chunks;
 };
 
+// Arrays whose rows are aligned to 2 bytes alone would come into shared memory
+// value by value (measured, 8 x 2048 x 2049 x 16 bf16: 765 us, with aligned
+// rows 236); a call that is large enough for another launch copies them into
+// aligned rows first.  Whether it does, and the copies' bytes; then the
+// copies, which replace the arrays in `a` (and *grad_y, where given).
+size_t realign_workspace(const rlscan_selective_scan_args &a, bool backward);
+rlscan_status realign(rlscan_selective_scan_args &a, rlscan_array3 *grad_y, char *ws, cudaStream_t s);
+
 template <class T>
 rlscan_status scan_typed(const Plan &p, const rlscan_selective_scan_args &a, ScanOut o, cudaStream_t s);
 template <class T>

@@ -694,3 +694,23 @@ def test_the_native_call_layer_is_the_python_way(monkeypatch):
     monkeypatch.setattr(ss, "_fast", ss._NoFastCall)
     for p, q in zip(got, calls()):
         assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("gap", [0, 3])
+def test_scan_rows_of_two_byte_alignment(gap):
+    """Odd rows of bfloat16, large enough to be copied into aligned rows first, against the same values in aligned ones."""
+    N, T, D, S = 2, 333, 601, 12
+    a, init, resets, _, rng = scan_inputs(N, T, D, S, BF16, 24, "packed")
+    gy = torch.from_numpy(rng.standard_normal((N, T, D)).astype(np.float32)).to(BF16)
+    even = {k: (strided(v, 8 - v.shape[-1] % 8) if k in ("x", "delta", "z", "B", "C") else v.to(DEV))
+            for k, v in a.items()}
+    odd = {k: (strided(v, gap) if gap and k in ("x", "delta", "z", "B", "C") else v.to(DEV)) for k, v in a.items()}
+    outs = []
+    for d, g in ((even, strided(gy, 8 - D % 8)), (odd, gy.to(DEV))):
+        y, final, marks = L().selective_scan(**d, initial_state=to_dev(init), resets=to_dev(resets),
+                                             return_checkpoints=True)
+        grads = L().selective_scan_backward(g, d["x"], d["delta"], d["A"], d["B"], d["C"], marks, d["D"], d["z"],
+                                            d["delta_bias"], resets=to_dev(resets))
+        outs.append((y, final, *grads))
+    for p, q in zip(*outs):
+        assert torch.equal(p, q)
