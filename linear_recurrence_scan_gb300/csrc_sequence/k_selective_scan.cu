@@ -11,12 +11,16 @@ constexpr int kTile = kCheckpoint;
 
 // Sixteen states a lane need the fewest instructions a state, eight give
 // twice the warps; chunks give as many warps as a row has tokens for, but
-// compute every state twice.  Measured (D 2048, S 16, bf16, microseconds):
-//   one row    T 512: 60 unsplit (8 states), 34 in chunks of 64;
-//              T 2048: 213, 68 (128);  T 8192: 829, 185 (16 states, 512)
-//   four rows  T 512: 60, 65;  T 2048: 214, 175 (16, 128);  T 8192: 830, 563 (16, 512)
-//   eight rows T 2048: 267 (8) and 279 (16), 301 (16, 256);  T 8192: 1037 (8), 1081 (16, 512)
-// so rows are split while the unsplit call has less than 1.5 blocks an SM.
+// compute every state twice.  Measured (D 2048, S 16, bf16, microseconds; the
+// states a lane and the chunk in parentheses):
+//   one row    T 256: 27 unsplit;  T 512: 48 unsplit, 28 (8, 64);  T 1024: 91, 40 (8, 64);
+//              T 2048: 173, 61 (16, 128);  T 8192: 668, 151 (16, 128)
+//   four rows  T 512: 50, 56 (8, 64);  T 1024: 91, 93 (16, 128);  T 2048: 174, 148 (16, 128);
+//              T 8192: 666, 500 (16, 128)
+//   eight rows T 512: 62 unsplit with 16, 66 with 8;  T 2048: 222 and 236, 268 (16, 256);
+//              T 8192: 861 and 914, 944 (16, 256)
+// so rows are split while the unsplit call with eight states a lane has less
+// than 1.5 blocks an SM (up to 1024 tokens: less than 0.75).
 Plan plan(const rlscan_selective_scan_args &a)
 {
     const int64_t sms = sm_count() > 0 ? sm_count() : 152;
@@ -29,12 +33,9 @@ Plan plan(const rlscan_selective_scan_args &a)
     Plan p;
     const int64_t narrow = blocks_of(8);
     const bool split = a.T > 256 && 2 * narrow < 3 * sms && !(4 * narrow >= 3 * sms && a.T <= 1024);
-    p.spt = a.S > 8 && (split ? a.T >= 1024 : narrow >= 3 * sms) ? 16 : 8;
+    p.spt = a.S > 8 && (split ? a.T >= 2048 : 2 * narrow >= 3 * sms) ? 16 : 8;
     p.chunk = ceil_div(a.T > 0 ? a.T : 1, kTile) * kTile;
-    if (split) {
-        p.chunk = a.T < 1024 ? 64 : 256;
-        while (p.chunk > 64 && blocks_of(p.spt) * ceil_div(a.T, p.chunk) < sms) p.chunk /= 2;
-    }
+    if (split) p.chunk = p.spt == 8 ? 64 : 128;
     p.lanes = lanes_of(p.spt);
     p.chunks = ceil_div(a.T > 0 ? a.T : 1, p.chunk);
     return p;

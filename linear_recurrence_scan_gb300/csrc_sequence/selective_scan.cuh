@@ -206,32 +206,40 @@ __global__ void __launch_bounds__(kScanThreads, Shape<T, SPT, LANES, SPLIT>::BLO
         auto walk = [&](auto fast, int w0) {
             constexpr bool FAST = decltype(fast)::value;
             float xv[P::PER], dt[P::PER], dtx[P::PER], part[P::WALK];
-#pragma unroll
-            for (int p = 0; p < P::PER; ++p) {
-                xv[p] = to_f(xs[(w0 + p * LANES + sl) * ROW]);
-                dt[p] = to_f(ds[(w0 + p * LANES + sl) * ROW]) + bias;
-            }
-            if constexpr (P::PER == 1) {
-                dt[0] = choose(soft, softplus(dt[0]), dt[0]);
-            } else {
-#pragma unroll
-                for (int p = 0; p < P::PER; p += 2) {
-                    const float2 v = halves(softplus(pair(dt[p], dt[p + 1])));
-                    dt[p] = choose(soft, v.x, dt[p]);
-                    dt[p + 1] = choose(soft, v.y, dt[p + 1]);
-                }
-            }
-#pragma unroll
-            for (int p = 0; p < P::PER; ++p) {
-                if (!FAST) dt[p] = w0 + p * LANES + sl < left ? dt[p] : 0.f;  // past the last token the state stays
-                if constexpr (MODE == BACK) {
-                    const float zv = to_f(zs[(w0 + p * LANES + sl) * ROW]);
-                    dtx[p] = xv[p] * choose(gate, zv * sigmoid(zv), 1.f);
+            // f(first, how many) for the lane's tokens, two at once where it has two
+            auto by_pairs = [](auto f) {
+                if constexpr (P::PER == 1) {
+                    f(0, std::integral_constant<int, 1>());
                 } else {
-                    dtx[p] = dt[p] * xv[p];
+#pragma unroll
+                    for (int p = 0; p < P::PER; p += 2) f(p, std::integral_constant<int, 2>());
                 }
-                if (!FULL) span += dt[p];
-            }
+            };
+            auto gate_of = [&](int p) {  // of tokens p and p + 1
+                const float z0 = to_f(zs[(w0 + p * LANES + sl) * ROW]);
+                const float z1 = P::PER > 1 ? to_f(zs[(w0 + (p + 1) * LANES + sl) * ROW]) : 0.f;
+                const f2 z = pair(z0, z1);
+                const float2 v = halves(mul2(z, sigmoid(z)));
+                return pair(choose(gate, v.x, 1.f), choose(gate, v.y, 1.f));
+            };
+            by_pairs([&](int p, auto two) {
+                constexpr int Q = decltype(two)::value - 1;
+                xv[p] = to_f(xs[(w0 + p * LANES + sl) * ROW]);
+                xv[p + Q] = to_f(xs[(w0 + (p + Q) * LANES + sl) * ROW]);
+                const f2 pre = add2(pair(to_f(ds[(w0 + p * LANES + sl) * ROW]), to_f(ds[(w0 + (p + Q) * LANES + sl) * ROW])),
+                                    both(bias));
+                const float2 s = halves(softplus(pre)), r = halves(pre);
+                dt[p] = choose(soft, s.x, r.x);
+                dt[p + Q] = choose(soft, Q == 0 ? s.x : s.y, Q == 0 ? r.x : r.y);
+                if (!FAST) {  // past the last token the state stays
+                    dt[p] = w0 + p * LANES + sl < left ? dt[p] : 0.f;
+                    dt[p + Q] = w0 + (p + Q) * LANES + sl < left ? dt[p + Q] : 0.f;
+                }
+                const float2 v = halves(mul2(pair(xv[p], xv[p + Q]), MODE == BACK ? gate_of(p) : pair(dt[p], dt[p + Q])));
+                dtx[p] = v.x;
+                dtx[p + Q] = Q == 0 ? v.x : v.y;
+                if (!FULL) span += Q == 0 ? dt[p] : dt[p] + dt[p + Q];
+            });
 #pragma unroll
             for (int kk = 0; kk < P::WALK; ++kk) {
                 const int j = MODE == BACK ? P::WALK - 1 - kk : kk, k = w0 + j;
@@ -274,19 +282,24 @@ __global__ void __launch_bounds__(kScanThreads, Shape<T, SPT, LANES, SPLIT>::BLO
                 }
             }
             if constexpr (FULL) {
+                by_pairs([&](int p, auto two) {
+                    constexpr int Q = decltype(two)::value - 1;
+                    // leaves lane sl the sums of its tokens
+                    scatter_sums<LANES, LANES / 2, 1>(part + p * LANES, lane);
+                    if (Q > 0) scatter_sums<LANES, LANES / 2, 1>(part + (p + Q) * LANES, lane);
+                    const float2 v = halves(mul2(
+                        fma2(both(skip), pair(xv[p], xv[p + Q]), pair(part[p * LANES], part[(p + Q) * LANES])), gate_of(p)));
 #pragma unroll
-                for (int p = 0; p < P::PER; ++p) {
-                    const int k = w0 + p * LANES + sl;
-                    scatter_sums<LANES, LANES / 2, 1>(part + p * LANES, lane);  // leaves lane sl the sum of its token
-                    float v = fmaf(skip, xv[p], part[p * LANES]);
-                    const float zv = to_f(zs[k * ROW]);
-                    v *= choose(gate, zv * sigmoid(zv), 1.f);
-                    if (FAST) {
-                        if (live) yt[k * a.D] = from_f<T>(v);
-                    } else if (live && t0 + k < last - first) {
-                        yt[k * a.D] = from_f<T>(k < left ? v : 0.f);
+                    for (int q = 0; q <= Q; ++q) {
+                        const int k = w0 + (p + q) * LANES + sl;
+                        const float out = q == 0 ? v.x : v.y;
+                        if (FAST) {
+                            if (live) yt[k * a.D] = from_f<T>(out);
+                        } else if (live && t0 + k < last - first) {
+                            yt[k * a.D] = from_f<T>(k < left ? out : 0.f);
+                        }
                     }
-                }
+                });
             }
         };
 #pragma unroll 1
