@@ -12,7 +12,11 @@ namespace seq {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 4;  // tokens whose loads are in flight together
+constexpr int kAhead = 4;   // tokens of a block
+// Blocks on their way to a thread.  Measured (8 x 4096 x 4096 bf16, forward
+// and with gradients): in registers, one block ahead, 121 and 327 us; through
+// shared memory with 3, 4, 6, 8 blocks 99, 97, 97, 101 and 303, 296, 303, 315.
+constexpr int kBlocks = 4;
 
 struct ConvOut {
     void *y, *final_state;
@@ -113,6 +117,65 @@ struct Window {
     }
 };
 
+// A thread's next values of ARRAYS arrays, kBlocks blocks of kAhead tokens on
+// their way: through its own place in shared memory by asynchronous copies,
+// which hold no registers while in flight, or, for single 16-bit values,
+// which these cannot copy, in registers and one block ahead.
+template <class T, int V, int ARRAYS>
+struct Feed {
+    static constexpr int BYTES = V * static_cast<int>(sizeof(T));
+    static constexpr bool RING = BYTES >= 4;
+    static constexpr int DEPTH = RING ? kBlocks : 2;
+    static constexpr size_t SMEM = RING ? static_cast<size_t>(DEPTH) * kAhead * ARRAYS * kThreads * BYTES : 0;
+    char *ring;
+    Words<T, V> next[RING ? 1 : ARRAYS][RING ? 1 : kAhead], held[RING ? 1 : ARRAYS][RING ? 1 : kAhead];
+    uint32_t next_flag[kAhead], flag[kAhead];
+
+    __device__ __forceinline__ char *place(int block, int u, int array)
+    {
+        return ring + (((block % DEPTH) * kAhead + u) * ARRAYS + array) * (kThreads * BYTES) + threadIdx.x * BYTES;
+    }
+    // token u of block `block`, `from` its address, if it is there
+    __device__ __forceinline__ void take(int block, int u, int array, const T *from, const T *safe, bool there)
+    {
+        if constexpr (RING) {
+            void *to = place(block, u, array);
+            const T *at = there ? from : safe;
+            const int bytes = there ? BYTES : 0;
+            if constexpr (BYTES == 16)
+                copy16(to, at, bytes);
+            else if constexpr (BYTES == 8)
+                copy8(to, at, bytes);
+            else
+                copy4(to, at, bytes);
+        } else if (there) {
+            next[array][u].load(from);
+        }
+    }
+    // block `block`'s turn: its values are here
+    __device__ __forceinline__ void turn()
+    {
+        if constexpr (RING) {
+            copies_wait<DEPTH - 1>();
+        } else {
+#pragma unroll
+            for (int i = 0; i < ARRAYS; ++i)
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) held[i][u] = next[i][u];
+        }
+    }
+    __device__ __forceinline__ Words<T, V> get(int block, int u, int array)
+    {
+        if constexpr (RING) {
+            Words<T, V> r;
+            r.load(reinterpret_cast<const T *>(place(block, u, array)));
+            return r;
+        } else {
+            return held[array][u];
+        }
+    }
+};
+
 // a bit for each token that starts an episode
 __device__ __forceinline__ uint32_t bits(const uint32_t (&flag)[kAhead])
 {
@@ -150,38 +213,49 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t silu = a.silu ? ~0u : 0u;
     Window<T, K, V> win;
     win.fill(a, x, n, d, t0 < len ? t0 : len);
-    // blocks of kAhead tokens, the next one's loads in front of this one's work
-    struct Block {
-        Words<T, V> r[kAhead];
-        uint32_t flag[kAhead];  // looked at only when the block's turn comes
-    };
-    const int count = static_cast<int>(stop - t0);
+    using F = Feed<T, V, 1>;
+    extern __shared__ __align__(16) char ring[];
+    F feed;
+    feed.ring = ring;
+    const int count = static_cast<int>(stop > t0 ? stop - t0 : 0), blocks = (count + kAhead - 1) / kAhead;
     const T *xt = x + t0 * a.x.token_stride;
     const uint8_t *resets = a.resets != nullptr ? a.resets + n * a.T + t0 : nullptr;
     T *yt = y + t0 * a.D;
-    auto load = [&](Block &b, int t) {
+    auto issue = [&](int block) {
+        if (block * kAhead < count)
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int t = block * kAhead + u;
+                feed.take(block, u, 0, xt + t * a.x.token_stride, x, t < count);
+            }
+        copies_commit();
+    };
+    auto flags_of = [&](int block) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            b.flag[u] = 0;
-            if (t + u < count) {
-                b.r[u].load(xt + (t + u) * a.x.token_stride);
-                if (resets != nullptr) b.flag[u] = load_byte(resets + t + u);
-            }
+            const int t = block * kAhead + u;
+            feed.next_flag[u] = resets != nullptr && t < count ? load_byte(resets + t) : 0u;
         }
     };
-    Block cur;
-    load(cur, 0);
-    for (int t = 0; t < count; t += kAhead) {
-        Block next;
-        load(next, t + kAhead);
-        const uint32_t starts = bits(cur.flag);
+#pragma unroll
+    for (int b = 0; b < F::DEPTH - 1; ++b) issue(b);
+    flags_of(0);
+    for (int b = 0; b < blocks; ++b) {
+        if (F::RING) issue(b + F::DEPTH - 1);
+        feed.turn();
+        if (!F::RING) issue(b + 1);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) feed.flag[u] = feed.next_flag[u];
+        flags_of(b + 1);
+        const uint32_t starts = bits(feed.flag);
+        const int t = b * kAhead;
         auto walk = [&](auto fast) {
             constexpr bool FAST = decltype(fast)::value;
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (!FAST && t + u >= count) break;
                 if (!FAST && (starts >> u & 1u) != 0) win.clear();
-                win.push(cur.r[u]);
+                win.push(feed.get(b, u, 0));
                 f2 acc[kPairs<V>];
                 win.dot(acc, w, bias);
 #pragma unroll
@@ -196,8 +270,8 @@ __global__ void __launch_bounds__(kThreads)
             walk(std::true_type());
         else
             walk(std::false_type());
-        cur = next;
     }
+    copies_wait<0>();
     const f2 zero[kPairs<V>] = {};
     for (int64_t t = stop > t0 ? stop : t0; t < t1; ++t) store<T, V>(y + t * a.D, zero);
     // the run that holds the last token writes the final state (run 0 of an empty row)
@@ -286,10 +360,6 @@ __global__ void __launch_bounds__(kThreads)
     Window<T, K, V> win;
     win.fill(a, x, n, d, t0 < len ? t0 : len);
     int since = K;  // tokens of the episode in front of t, as far as a tap of this run's tokens can see
-    struct Block {
-        Words<T, V> x[kAhead], g[kAhead];
-        uint32_t flag[kAhead];  // looked at only when the block's turn comes
-    };
     // in tokens behind t0: the run's own, those with a dL/dy, all it walks
     const int own = static_cast<int>(t1 - t0), all = static_cast<int>(stop - t0);
     const int64_t rest = len - t0;
@@ -298,15 +368,25 @@ __global__ void __launch_bounds__(kThreads)
     const uint8_t *resets = a.resets != nullptr ? a.resets + n * a.T + t0 : nullptr;
     T *dx = static_cast<T *>(g.grad_x) + (n * a.T + t0) * a.D + d;
     const uint32_t silu = a.silu ? ~0u : 0u;
-    auto load = [&](Block &b, int t) {
+    using F = Feed<T, V, 2>;
+    extern __shared__ __align__(16) char ring[];
+    F feed;
+    feed.ring = ring;
+    auto issue = [&](int block) {
+        if (block * kAhead < live)
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int t = block * kAhead + u;
+                feed.take(block, u, 0, xt + t * a.x.token_stride, x, t < live);
+                feed.take(block, u, 1, gt + t * g.grad_y.token_stride, gy, t < live);
+            }
+        copies_commit();
+    };
+    auto flags_of = [&](int block) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            b.flag[u] = 0;
-            if (t + u < live) {
-                b.x[u].load(xt + (t + u) * a.x.token_stride);
-                b.g[u].load(gt + (t + u) * g.grad_y.token_stride);
-                if (resets != nullptr) b.flag[u] = load_byte(resets + t + u);
-            }
+            const int t = block * kAhead + u;
+            feed.next_flag[u] = resets != nullptr && t < live ? load_byte(resets + t) : 0u;
         }
     };
     auto slope = [&](f2 *gv) {  // dL/dpre from dL/dy: silu' = s (1 + v (1 - s))
@@ -336,21 +416,27 @@ __global__ void __launch_bounds__(kThreads)
             for (int k = 0; k < K; ++k) dw[k][i] = fma2(gv[i], win.v[k][i], dw[k][i]);
         }
     };
-    Block cur;
-    load(cur, 0);
-    for (int t = 0; t < all; t += kAhead) {
-        Block next;
-        load(next, t + kAhead);
-        const uint32_t starts = bits(cur.flag);
+#pragma unroll
+    for (int b = 0; b < F::DEPTH - 1; ++b) issue(b);
+    flags_of(0);
+    for (int b = 0; b * kAhead < all; ++b) {
+        if (F::RING) issue(b + F::DEPTH - 1);
+        feed.turn();
+        if (!F::RING) issue(b + 1);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) feed.flag[u] = feed.next_flag[u];
+        flags_of(b + 1);
+        const uint32_t starts = bits(feed.flag);
+        const int t = b * kAhead;
         const int safe = g.grad_final == nullptr ? live : live - (K - 1);
         if (starts == 0 && since >= K - 1 && t >= K - 1 && t + kAhead <= own && t + kAhead <= safe) {
             // tokens of one episode inside the run, without a branch
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 shift();
-                win.push(cur.x[u]);
+                win.push(feed.get(b, u, 0));
                 f2 gv[H];
-                widen<T, V>(gv, cur.g[u]);
+                widen<T, V>(gv, feed.get(b, u, 1));
                 slope(gv);
 #pragma unroll
                 for (int k = 0; k < K; ++k)
@@ -370,9 +456,9 @@ __global__ void __launch_bounds__(kThreads)
                         win.clear();
                         since = 0;
                     }
-                    win.push(cur.x[u]);
+                    win.push(feed.get(b, u, 0));
                     f2 gv[H];
-                    widen<T, V>(gv, cur.g[u]);
+                    widen<T, V>(gv, feed.get(b, u, 1));
                     slope(gv);
 #pragma unroll
                     for (int k = 0; k < K; ++k)
@@ -406,8 +492,8 @@ __global__ void __launch_bounds__(kThreads)
                     store<T, V>(static_cast<T *>(g.grad_initial) + (n * (K - 1) + to + K - 1) * a.D + d, v);
             }
         }
-        cur = next;
     }
+    copies_wait<0>();
     if (g.part != nullptr) {
         float *p = g.part + (n * g.runs + run) * (K + 1) * a.D;
         float flat[V * K];
@@ -435,7 +521,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Channels of a thread: four (measured, 8 x 4096 x 4096 bf16 forward and
-// backward: 328 us, with two 398 us, with eight 336 us), two where four do
+// backward, next block in registers: 328 us, with two 398, with eight 336), two where four do
 // not fit the rows or leave too few threads even in runs of 8 tokens
 // (1 x 509 x 1536 forward: 8.8 us with two, 10.9 us with four), else one.
 constexpr int64_t kFullThreads = 768;  // threads an SM that keep enough loads in flight
@@ -481,8 +567,13 @@ rlscan_status forward(const rlscan_causal_conv_args &a, ConvOut o, cudaStream_t 
     o.run = run_length(a, V, kMostRun);
     o.runs = a.T > 0 ? ceil_div(a.T, o.run) : 1;
     return by_taps(a.K, [&](auto k) {
-        return launch_overlapped(conv_kernel<T, decltype(k)::value, V>, ceil_div(a.N * o.runs * (a.D / V), kThreads), kThreads,
-                                 0, s, a, o);
+        auto kernel = conv_kernel<T, decltype(k)::value, V>;
+        constexpr size_t SMEM = Feed<T, V, 1>::SMEM;
+        static const bool sized =
+            SMEM <= 48 * 1024 ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) == cudaSuccess;
+        if (!sized) return RLSCAN_ERR_CUDA;
+        return launch_overlapped(kernel, ceil_div(a.N * o.runs * (a.D / V), kThreads), kThreads, SMEM, s, a, o);
     });
 }
 
@@ -500,8 +591,13 @@ template <class T, int V>
 rlscan_status backward(const rlscan_causal_conv_args &a, const ConvGrad &g, cudaStream_t s)
 {
     return by_taps(a.K, [&](auto k) {
-        return launch_overlapped(conv_grad_kernel<T, decltype(k)::value, V>, ceil_div(a.N * g.runs * (a.D / V), kThreads),
-                                 kThreads, 0, s, a, g);
+        auto kernel = conv_grad_kernel<T, decltype(k)::value, V>;
+        constexpr size_t SMEM = Feed<T, V, 2>::SMEM;
+        static const bool sized =
+            SMEM <= 48 * 1024 ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) == cudaSuccess;
+        if (!sized) return RLSCAN_ERR_CUDA;
+        return launch_overlapped(kernel, ceil_div(a.N * g.runs * (a.D / V), kThreads), kThreads, SMEM, s, a, g);
     });
 }
 

@@ -449,13 +449,13 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
     }
 }
 
-// 32 columns x 8 slices of the parts a block; a slice adds its parts in
-// order, then the slices are added in order.
-constexpr int kSlices = 8;
+// A block takes 32 columns: 8 threads of four columns x 32 slices of the
+// parts.  A slice adds its parts in order, then the slices are added in order.
+constexpr int kSlices = 32, kColumns = SumJobs::kColumns;
 
-__global__ void __launch_bounds__(32 * kSlices) sums_kernel(const __grid_constant__ SumJobs jobs)
+__global__ void __launch_bounds__(8 * kSlices) sums_kernel(const __grid_constant__ SumJobs jobs)
 {
-    __shared__ float scratch[kSlices][32];
+    __shared__ float scratch[kSlices][kColumns + 4];
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
     int which = 0;
@@ -463,23 +463,39 @@ __global__ void __launch_bounds__(32 * kSlices) sums_kernel(const __grid_constan
     for (int j = 1; j < SumJobs::kMost; ++j)
         if (j < jobs.count && blockIdx.x >= jobs.job[j].first) which = j;
     const SumJobs::Job &job = jobs.job[which];
-    const int slice = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int64_t i = (blockIdx.x - job.first) * 32 + lane;
-    float acc = 0.f;
-    if (i < job.m) {
-        const float *p = job.part + i;
+    const int slice = threadIdx.x / 8, quad = threadIdx.x % 8;
+    const int64_t c0 = (blockIdx.x - job.first) * kColumns, c = c0 + 4 * quad;
+    const float *p = job.part + c;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (job.vec) {
+        if (c < job.m) {
 #pragma unroll 4
-        for (int64_t w = slice; w < job.parts; w += kSlices) acc += p[w * job.pitch];
-    }
-    scratch[slice][lane] = acc;
-    __syncthreads();
-    if (slice != 0 || i >= job.m) return;
+            for (int64_t w = slice; w < job.parts; w += kSlices) {
+                const float4 v = *reinterpret_cast<const float4 *>(p + w * job.pitch);
+                acc[0] += v.x;
+                acc[1] += v.y;
+                acc[2] += v.z;
+                acc[3] += v.w;
+            }
+        }
+    } else {
+        for (int64_t w = slice; w < job.parts; w += kSlices)
 #pragma unroll
-    for (int s = 1; s < kSlices; ++s) acc += scratch[s][lane];
+            for (int i = 0; i < 4; ++i)
+                if (c + i < job.m) acc[i] += p[w * job.pitch + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) scratch[slice][4 * quad + i] = acc[i];
+    __syncthreads();
+    const int64_t out = c0 + threadIdx.x;
+    if (threadIdx.x >= kColumns || out >= job.m) return;
+    float sum = scratch[0][threadIdx.x];
+#pragma unroll
+    for (int s = 1; s < kSlices; ++s) sum += scratch[s][threadIdx.x];
     if (job.bf16_out)
-        static_cast<bf16 *>(job.out)[i] = from_f<bf16>(acc);
+        static_cast<bf16 *>(job.out)[out] = from_f<bf16>(sum);
     else
-        static_cast<float *>(job.out)[i] = acc;
+        static_cast<float *>(job.out)[out] = sum;
 }
 
 int grad_lanes(int64_t S)
@@ -563,7 +579,7 @@ rlscan_status launch_typed(const rlscan_selective_scan_args &a, GradArgs g, cuda
 rlscan_status launch_sums(const SumJobs &jobs, cudaStream_t s)
 {
     if (jobs.blocks == 0) return RLSCAN_OK;
-    return launch_overlapped(sums_kernel, jobs.blocks, 32 * kSlices, 0, s, jobs);
+    return launch_overlapped(sums_kernel, jobs.blocks, 8 * kSlices, 0, s, jobs);
 }
 
 size_t selective_scan_backward_workspace(const rlscan_selective_scan_args &a) { return layout(a).bytes; }

@@ -321,6 +321,13 @@ __device__ __forceinline__ void copy4(void *dst, const void *src, int bytes)
                  "l"(src), "r"(bytes)
                  : "memory");
 }
+__device__ __forceinline__ void copy8(void *dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
 __device__ __forceinline__ void copies_wait()
@@ -480,21 +487,22 @@ size_t add_rms_norm_backward_workspace(int64_t M, int64_t D);
 // Sums over parts, several in one launch:
 // out[i] = sum over w < parts of part[w * pitch + i], i < m, in a fixed order.
 struct SumJobs {
-    static constexpr int kMost = 5;
+    static constexpr int kMost = 5, kColumns = 32;  // columns of a block
     struct Job {
         const float *part;
         int64_t parts, pitch, m;
         void *out;
-        int bf16_out;
-        int64_t first;  // its first block
+        bool bf16_out, vec;  // vec: columns in whole, aligned units of four
+        int64_t first;       // its first block
     } job[kMost];
     int count = 0;
     int64_t blocks = 0;
     void add(const float *part, int64_t parts, int64_t pitch, int64_t m, void *out, bool bf16_out)
     {
         if (m == 0) return;
-        job[count++] = Job{part, parts, pitch, m, out, bf16_out ? 1 : 0, blocks};
-        blocks += (m + 31) / 32;
+        const bool vec = m % 4 == 0 && pitch % 4 == 0 && (reinterpret_cast<uintptr_t>(part) & 15u) == 0;
+        job[count++] = Job{part, parts, pitch, m, out, bf16_out, vec, blocks};
+        blocks += (m + kColumns - 1) / kColumns;
     }
 };
 rlscan_status launch_sums(const SumJobs &jobs, cudaStream_t s);
