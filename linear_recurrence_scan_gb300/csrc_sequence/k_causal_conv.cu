@@ -5,6 +5,8 @@
 // inputs before the token in registers, in pairs of channels.  A reset clears
 // that window, so that taps never reach into the episode before; a run starts
 // by reading the K-1 tokens in front of it (or the initial state).
+// Bytes bound it: 8 x 4096 x 4096 bf16 97 us forward (5.5 TB/s), 289 us with
+// gradients (4.6 TB/s, 60 % of the issue slots).
 #include "sequence.cuh"
 
 namespace rlscan {

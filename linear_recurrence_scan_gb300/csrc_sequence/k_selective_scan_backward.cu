@@ -3,7 +3,7 @@
 // With g the gradient of sum_s C h and G_t = C_t g_t + exp(dt_{t+1} A) G_{t+1}
 // the gradient of h_t, tiles of 16 tokens are taken from the last to the
 // first.  exp(dt A) h_{t-1} is h_t - dt x B, so that the states alone are
-// needed: they are made again from the tile's checkpoint, 8 tokens at a time,
+// needed: they are made again from the tile's checkpoint, 4 tokens at a time,
 // and stay in registers while G runs back over them.
 //
 // A lane holds four channels x four states, in pairs of channels: the sums
@@ -11,6 +11,12 @@
 // the shuffles that one channel a lane would need.  What each channel and
 // token needs once (softplus, the gate, the outputs) is shared out over the
 // lanes through shared memory.
+//
+// Instructions bound it, 421 for a warp (32 channels x 16 states) and token,
+// at the two warps a scheduler that 255 registers leave.  Measured, 8 x 512 x
+// 4096 x 16 bf16: 389 us, 60 % of the issue slots where an SM has two blocks;
+// 8 x 2048 x 4096 with the forward pass 1994 us, with three blocks an SM
+// (168 registers, spills) 3088, with two channels a lane and four blocks 2234.
 #include "scan_plan.cuh"
 
 namespace rlscan {

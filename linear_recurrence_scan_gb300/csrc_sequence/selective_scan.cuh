@@ -10,6 +10,13 @@
 // shared out over a channel's lanes: each prepares its own (softplus, dt x,
 // the gate), hands dt and dt x to the others with shuffles, and gets its
 // tokens' sums over the states back.
+//
+// An exponential and four multiply-adds a state value bound it: in pairs they
+// run at 31.5 values a clock and SM.
+// Measured, S 16 bf16: 8 x 4096 x 4096 ragged 640 us, 3.4e12 values/s, 63 % of
+// the issue slots where an SM has two blocks; whole rows of 8 x 1024 x 4096
+// 183 us.  1 x 4096 x 2048 in chunks: 35 us for the chunks' states (69 % of
+// the exponential units), 8 for joining them, 54 for the outputs.
 #pragma once
 
 #include "scan_plan.cuh"
@@ -41,7 +48,7 @@ struct Shape {
     static constexpr bool CONVERT = sizeof(T) == 2;
     static constexpr int WIDE = CONVERT ? 2 * kTile * SP * 4 : 0;  // B and C in float32
     static constexpr size_t SMEM = STAGES * STAGE + 2 * WIDE;
-    static constexpr int BLOCKS = SPLIT ? (SPT == 16 ? 4 : 4) : (SPT == 16 ? 2 : 3);
+    static constexpr int BLOCKS = SPLIT ? 4 : (SPT == 16 ? 2 : 3);
     static_assert(ACT % 16 == 0 && BC % 16 == 0);
 };
 
