@@ -42,6 +42,7 @@ struct GradArgs {
     float *part_d;           // [N chunks][2][D]: skip, delta_bias
     int unit;                // bytes of the copies into shared memory: 16, 4 or 0 (single values)
     bool vec;                // checkpoints in whole 16-byte units
+    int64_t sms;             // as ScanOut's
 };
 
 template <class T, int LANES>
@@ -82,8 +83,11 @@ __global__ void __launch_bounds__(Shape<T, LANES>::THREADS)
     char *sumA = keep + P::KEEP;  // dA: a tile's sum is in registers, the sum over tiles here (two short sums, not one long)
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
-    const int64_t blocks = (a.D + P::CH - 1) / P::CH, block = divide(blockIdx.x, blocks).r;
-    const Division at_row = divide(divide(blockIdx.x, blocks).q, g.chunks);
+    const int64_t blocks = (a.D + P::CH - 1) / P::CH;
+    const int64_t place =
+        g.sms > 0 ? by_length(a.lengths, static_cast<int>(a.N), blocks, g.sms, reinterpret_cast<int *>(smem)) : blockIdx.x;
+    const Division at_block = divide(place, blocks), at_row = divide(at_block.q, g.chunks);
+    const int64_t block = at_block.r;
     const int64_t chunk = at_row.r, n = at_row.q;
     const int64_t first = chunk * g.chunk, last = first + g.chunk < a.T ? first + g.chunk : a.T;
     const int64_t c0 = block * P::CH;
@@ -559,7 +563,8 @@ rlscan_status launch_shape(const rlscan_selective_scan_args &a, const GradArgs &
     static const bool sized =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
     if (!sized) return RLSCAN_ERR_CUDA;
-    return launch_overlapped(kernel, a.N * ceil_div(a.D, P::CH) * g.chunks, P::THREADS, P::SMEM, s, a, g);
+    const int64_t grid = a.N * ceil_div(a.D, P::CH) * g.chunks;
+    return launch(!spread_out(grid, g.sms), kernel, grid, P::THREADS, P::SMEM, s, a, g);
 }
 
 template <class T>
@@ -617,6 +622,7 @@ rlscan_status launch_selective_scan_backward(const rlscan_selective_scan_args &a
     const bool b16 = a.dtype == RLSCAN_BF16;
     k.chunk = l.chunk;
     k.chunks = l.chunks;
+    k.sms = order_sms(a.lengths, a.N, l.blocks, l.chunks);
     if (a.N > 0) {
         if (l.chunks > 1) {
             float *states = reinterpret_cast<float *>(w + l.states);

@@ -20,6 +20,7 @@ struct ScanOut {
     float *spans;    // [N][chunks][D]: the chunk's sum of dt
     uint8_t *cuts;   // [N][chunks]: an episode starts in the chunk
     rlscan_array3 grad_y;  // BACK
+    int64_t sms;           // rows in the order of their lengths, for so many SMs; 0: as they are
 };
 
 // How a call is laid out: states per lane, and chunks of each row.

@@ -99,7 +99,10 @@ __global__ void __launch_bounds__(kScanThreads, Shape<T, SPT, LANES, SPLIT>::BLO
     ptx::pdl_wait_prerequisites();
     const int lane = threadIdx.x & 31, sl = lane % LANES, ch = threadIdx.x / LANES;
     const int64_t blocks = (a.D + P::CH - 1) / P::CH;
-    const Division at_block = divide(blockIdx.x, blocks), at_row = divide(at_block.q, o.chunks);
+    const int64_t place = FULL && !SPLIT && o.sms > 0
+                              ? by_length(a.lengths, static_cast<int>(a.N), blocks, o.sms, reinterpret_cast<int *>(smem))
+                              : blockIdx.x;
+    const Division at_block = divide(place, blocks), at_row = divide(at_block.q, o.chunks);
     const int64_t c0 = at_block.r * P::CH, chunk = at_row.r, n = at_row.q;
     const int64_t d = c0 + ch;
     const bool live = d < a.D;
@@ -383,14 +386,16 @@ __global__ void __launch_bounds__(256) chunk_kernel(const __grid_constant__ rlsc
 }
 
 template <class T, int SPT, int LANES, int MODE, bool SPLIT>
-rlscan_status launch_mode(const rlscan_selective_scan_args &a, const ScanOut &o, cudaStream_t s)
+rlscan_status launch_mode(const rlscan_selective_scan_args &a, ScanOut o, cudaStream_t s)
 {
     using P = Shape<T, SPT, LANES, SPLIT>;
+    o.sms = order_sms(a.lengths, a.N, ceil_div(a.D, P::CH), o.chunks);
     auto kernel = scan_kernel<T, SPT, LANES, MODE, SPLIT>;
     static const bool sized =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
     if (!sized) return RLSCAN_ERR_CUDA;
-    return launch_overlapped(kernel, a.N * ceil_div(a.D, P::CH) * o.chunks, kScanThreads, P::SMEM, s, a, o);
+    const int64_t grid = a.N * ceil_div(a.D, P::CH) * o.chunks;
+    return launch(!spread_out(grid, o.sms), kernel, grid, kScanThreads, P::SMEM, s, a, o);
 }
 
 template <class T, int SPT, int LANES>

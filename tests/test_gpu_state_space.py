@@ -64,6 +64,13 @@ def test_scan_forward_and_gradients(N, T, D, S, dtype, kind):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("N,T,D,S", [(40, 21, 520, 16), (64, 18, 700, 16), (33, 9, 1300, 8), (65, 7, 400, 16)])
+def test_scan_rows_in_the_order_of_their_lengths(N, T, D, S, dtype):
+    """More blocks than SMs, up to and over two an SM: rows change places, equal and empty ones too."""
+    test_scan_forward_and_gradients(N, T, D, S, dtype, "ragged")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("T,D", [(700, 64), (2100, 24), (1030, 7)])
 def test_scan_long_rows(T, D, dtype):
     """Few channels and many tokens: rows that are split along the tokens."""
