@@ -20,7 +20,12 @@ constexpr int kTile = kCheckpoint;
 //   eight rows T 512: 62 unsplit with 16, 66 with 8;  T 2048: 222 and 236, 268 (16, 256);
 //              T 8192: 861 and 914, 944 (16, 256)
 // so rows are split while the unsplit call with eight states a lane has less
-// than 1.5 blocks an SM (up to 1024 tokens: less than 0.75).
+// than 1.5 blocks an SM (up to 1024 tokens: less than 0.75).  The chunks fill
+// the four blocks an SM: against those of 64 or 128 tokens,
+//   1 x 509 x 1536 31 us, 26 (chunks of 32);  2 x 700 x 2048 49, 45 (80);  1 x 2048 x 4096 93, 87 (112);
+//   3 x 2048 x 2048 129, 120 (176);  2 x 16384 x 2048 509, 508 (224), ragged 421, 400
+// Rows too long for that in eight half waves take chunks of 128 (2 x 16384 x
+// 2048: 64: 556 us, 128: 509, 288: 488, 864: 498; ragged 461, 421, 415, 494).
 Plan plan(const rlscan_selective_scan_args &a)
 {
     const int64_t sms = sm_count() > 0 ? sm_count() : 152;
@@ -35,8 +40,11 @@ Plan plan(const rlscan_selective_scan_args &a)
     const bool split = a.T > 256 && 2 * narrow < 3 * sms && !(4 * narrow >= 3 * sms && a.T <= 1024);
     p.spt = a.S > 8 && (split ? a.T >= 2048 : 2 * narrow >= 3 * sms) ? 16 : 8;
     p.chunk = ceil_div(a.T > 0 ? a.T : 1, kTile) * kTile;
-    if (split) p.chunk = p.spt == 8 ? 64 : 128;
     p.lanes = lanes_of(p.spt);
+    if (split) {
+        const int64_t chunk = wave_chunk(a.T, blocks_of(p.spt), 4 * sms, 8, 256);
+        p.chunk = chunk > 0 ? chunk : 128;
+    }
     p.chunks = ceil_div(a.T > 0 ? a.T : 1, p.chunk);
     return p;
 }

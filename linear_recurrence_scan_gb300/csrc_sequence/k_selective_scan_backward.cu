@@ -516,7 +516,15 @@ int grad_lanes(int64_t S)
 
 // How a call is laid out, and its workspace.  Rows are split into chunks of
 // tokens, whose messages take a pass of their own (about a quarter of the
-// work), while there are less than 1.5 blocks an SM without.
+// work), while there are less than 1.5 blocks an SM without; the chunks fill
+// whole waves of two blocks an SM.  Measured with the forward pass, against
+// chunks for two waves, whole or not, of 64 tokens or more (us): 1 x 509 x
+// 1536 126, 96 (chunks of 32);  2 x 300 x 768 113, 88 (32);  2 x 8192 x 1024
+// 601, 581;  8 x 500 x 3000 480, 461.  Of rows with lengths nobody knows here
+// how many blocks have tokens: chunks for three waves, short enough that the
+// last one costs little (ragged 3 x 1500 x 3000: 128: 454, as if all rows were
+// full, 384: 488;  4 x 1024 x 2048: 80: 332, 256: 363;  3 x 1001 x 1111 float32:
+// 48: 188, 64: 200, 96: 194).
 struct Layout {
     int64_t blocks, chunk, chunks;
     size_t B, C, A, d, states, spans, cuts, realigned, bytes;
@@ -530,9 +538,11 @@ Layout layout(const rlscan_selective_scan_args &a)
     l.blocks = ceil_div(a.D, (lanes == 2 ? 2 : 4) * 4 * (32 / lanes));
     l.chunk = ceil_div(a.T > 0 ? a.T : 1, kTile) * kTile;
     if (a.N > 0 && a.T > 128 && 2 * a.N * l.blocks < 3 * sms) {
-        const int64_t want = ceil_div(4 * sms, a.N * l.blocks);
-        const int64_t chunk = ceil_div(ceil_div(a.T, want), kTile) * kTile;
-        l.chunk = chunk < 64 ? 64 : chunk;
+        const int64_t want = ceil_div(6 * sms, a.N * l.blocks), even = ceil_div(ceil_div(a.T, want), kTile) * kTile;
+        if (a.lengths != nullptr)
+            l.chunk = even < 48 ? 48 : even;
+        else
+            l.chunk = wave_chunk(a.T, a.N * l.blocks, 2 * sms, 4, a.T + kTile);
     }
     l.chunks = ceil_div(a.T > 0 ? a.T : 1, l.chunk);
     const size_t each = static_cast<size_t>(a.N) * l.chunks, F = sizeof(float);

@@ -29,6 +29,30 @@ struct Plan {
     int64_t chunk, chunks;
 };
 
+// Tokens of a chunk where a chunk of every row takes `each` blocks and `slots`
+// blocks run at once: chunks that fill whole waves, or half of the last one
+// (whose blocks have an SM to fewer and take about 0.8 of the time).  A
+// block's time is that of its tokens and of about eight more.  Of up to
+// `halves` half waves the least time; 0 if all have more than `most` tokens.
+inline int64_t wave_chunk(int64_t T, int64_t each, int64_t slots, int halves, int64_t most)
+{
+    int64_t best = 0, least = 0;
+    for (int k = 1; k <= halves; ++k) {
+        const int64_t count = k * slots / 2 / each;
+        if (count < 1) continue;
+        int64_t chunk = ceil_div(ceil_div(T, count), kCheckpoint) * kCheckpoint;
+        chunk = chunk < 32 ? 32 : chunk;
+        if (chunk > most) continue;
+        const int64_t blocks = ceil_div(T, chunk) * each, rest = blocks % slots;
+        const int64_t cost = (blocks / slots * 10 + (rest == 0 ? 0 : 2 * rest <= slots ? 8 : 10)) * (chunk + 8);
+        if (best == 0 || cost < least) {
+            best = chunk;
+            least = cost;
+        }
+    }
+    return best;
+}
+
 // Arrays whose rows are aligned to 2 bytes alone would come into shared memory
 // value by value (measured, 8 x 2048 x 2049 x 16 bf16: 765 us, with aligned
 // rows 236); a call that is large enough for another launch copies them into
