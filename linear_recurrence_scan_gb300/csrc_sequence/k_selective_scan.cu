@@ -36,8 +36,8 @@ Plan plan(const rlscan_selective_scan_args &a)
     };
     auto blocks_of = [&](int spt) { return a.N * ceil_div(a.D * lanes_of(spt), kScanThreads); };
     Plan p;
-    const int64_t narrow = blocks_of(8);
-    const bool split = a.T > 256 && 2 * narrow < 3 * sms && !(4 * narrow >= 3 * sms && a.T <= 1024);
+    const int64_t narrow = blocks_of(8);  // 0 without rows or channels
+    const bool split = narrow > 0 && a.T > 256 && 2 * narrow < 3 * sms && !(4 * narrow >= 3 * sms && a.T <= 1024);
     p.spt = a.S > 8 && (split ? a.T >= 2048 : 2 * narrow >= 3 * sms) ? 16 : 8;
     p.chunk = ceil_div(a.T > 0 ? a.T : 1, kTile) * kTile;
     p.lanes = lanes_of(p.spt);

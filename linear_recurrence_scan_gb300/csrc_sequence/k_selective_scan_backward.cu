@@ -552,7 +552,7 @@ Layout layout(const rlscan_selective_scan_args &a)
     const int64_t sms = sm_count() > 0 ? sm_count() : 152;
     l.blocks = ceil_div(a.D, (lanes == 2 ? 2 : 4) * 4 * (32 / lanes));
     l.chunk = ceil_div(a.T > 0 ? a.T : 1, kTile) * kTile;
-    if (a.N > 0 && a.T > 128 && 2 * a.N * l.blocks < 3 * sms) {
+    if (a.N * l.blocks > 0 && a.T > 128 && 2 * a.N * l.blocks < 3 * sms) {
         const int64_t want = ceil_div(6 * sms, a.N * l.blocks), even = ceil_div(ceil_div(a.T, want), kTile) * kTile;
         if (a.lengths != nullptr)
             l.chunk = even < 48 ? 48 : even;
