@@ -648,7 +648,7 @@ rlscan_status launch_selective_scan_backward(const rlscan_selective_scan_args &a
     k.chunk = l.chunk;
     k.chunks = l.chunks;
     k.sms = order_sms(a.lengths, a.N, l.blocks, l.chunks);
-    if (a.N > 0) {
+    if (a.N > 0 && a.D > 0) {
         if (l.chunks > 1) {
             float *states = reinterpret_cast<float *>(w + l.states);
             const rlscan_status st =

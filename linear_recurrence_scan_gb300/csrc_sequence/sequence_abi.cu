@@ -142,8 +142,7 @@ RLSCAN_API rlscan_status rlscan_selective_scan_backward(const rlscan_selective_s
     if (grad_y == nullptr || grads == nullptr) return RLSCAN_ERR_NULL;
     const rlscan_selective_scan_args &a = *args;
     const rlscan_selective_scan_grads &g = *grads;
-    if (a.D == 0) return RLSCAN_OK;
-    if (a.N > 0) {
+    if (a.N > 0 && a.D > 0) {  // without channels the gradients of B and C are zeros, and read nothing
         RLSCAN_TRY(check_scan_inputs(a));
         if (a.T > 0 && (!grad_y->data || !checkpoints || !g.x)) return RLSCAN_ERR_NULL;
     }

@@ -1,0 +1,48 @@
+"""The state-space layer's calls as torch sees them: empty arrays."""
+import pytest
+import torch
+
+from state_space_cases import DEV
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from linear_recurrence_scan_gb300 import build
+    build.build()
+
+
+def L():
+    import linear_recurrence_scan_gb300 as lib
+    return lib
+
+
+@pytest.fixture(params=["native", "python"])
+def layer(request, monkeypatch):
+    """The calls through the native call layer and the Python way."""
+    from linear_recurrence_scan_gb300 import state_space as ss
+    ss._load_fast()
+    if request.param == "python":
+        monkeypatch.setattr(ss, "_fast", ss._NoFastCall)
+    return request.param
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_scan_without_channels_or_rows(layer, dtype):
+    """Nothing to scan over many tokens: empty results, and gradients of B and C that are zeros, not left as they were."""
+    T, S = 600, 16
+    for N, D in ((2, 0), (0, 64), (0, 0)):
+        x, bc = torch.zeros(N, T, D, dtype=dtype, device=DEV), torch.randn(N, T, S, device=DEV).to(dtype)
+        A, D1 = -torch.ones(D, S, device=DEV), torch.ones(D, device=DEV)
+        y, final = L().selective_scan(x, x, A, bc, bc, D1, x, D1)
+        assert y.shape == (N, T, D) and final.shape == (N, D, S)
+        _, _, marks = L().selective_scan(x, x, A, bc, bc, D1, x, D1, return_checkpoints=True)
+        for _ in range(2):   # what the allocator hands out next is not zero
+            junk = [torch.full((N, T, S), 7.0, dtype=dtype, device=DEV) for _ in range(8)]
+            del junk
+            g = L().selective_scan_backward(x, x, x, A, bc, bc, marks, D1, x, D1)
+            assert g.B.shape == g.C.shape == (N, T, S) and not g.B.any() and not g.C.any()
+            assert g.x.shape == x.shape and g.A.shape == (D, S) and not g.A.any() and not g.D.any()
