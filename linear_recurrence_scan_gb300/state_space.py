@@ -246,12 +246,13 @@ class _SelectiveScan(torch.autograd.Function):
                                         resets, lengths)
         ctx.delta_softplus, ctx.started = delta_softplus, initial_state is not None
         ctx.save_for_backward(x, delta, A, B, C, D, z, delta_bias, resets, lengths, marks)
+        ctx.mark_non_differentiable(marks)
         ctx.set_materialize_grads(False)
-        return y, final
+        return y, final, marks
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, grad_y, grad_final):
+    def backward(ctx, grad_y, grad_final, _):
         x, delta, A, B, C, D, z, delta_bias, resets, lengths, marks = ctx.saved_tensors
         if grad_y is None:
             if grad_final is None:
@@ -279,17 +280,15 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_sof
     padding (not read, y = 0).  Returns (y, final_state): y like x, the
     states [N,channels,S] float32 after each row's last token.  With
     ``return_checkpoints`` a third value, what selective_scan_backward
-    needs: the states before every 16th token."""
+    needs: the states before every 16th token (these carry no gradient)."""
     if not return_checkpoints:
         out = (_fast or _load_fast()).selective_scan(x, delta, A, B, C, D, z, delta_bias, delta_softplus,
                                                      initial_state, resets, lengths)
         if out is not None:
             return out
-    if not return_checkpoints and _wants_grad(x, delta, A, B, C, D, z, delta_bias, initial_state):
-        return _SelectiveScan.apply(x, delta, A, B, C, D, z, delta_bias, delta_softplus, initial_state, resets,
-                                    lengths)
-    out = _scan_forward(return_checkpoints, x, delta, A, B, C, D, z, delta_bias, delta_softplus, initial_state,
-                        resets, lengths)
+    args = (x, delta, A, B, C, D, z, delta_bias, delta_softplus, initial_state, resets, lengths)
+    out = (_SelectiveScan.apply(*args) if _wants_grad(x, delta, A, B, C, D, z, delta_bias, initial_state)
+           else _scan_forward(return_checkpoints, *args))
     return out if return_checkpoints else out[:2]
 
 

@@ -1,8 +1,9 @@
-"""The state-space layer's calls as torch sees them: empty arrays."""
+"""The state-space layer's calls as torch sees them: what autograd follows,
+refuses and notices, the device a call runs on, empty arrays."""
 import pytest
 import torch
 
-from state_space_cases import DEV
+from state_space_cases import DEV, scan_inputs, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +47,23 @@ def test_scan_without_channels_or_rows(layer, dtype):
             g = L().selective_scan_backward(x, x, x, A, bc, bc, marks, D1, x, D1)
             assert g.B.shape == g.C.shape == (N, T, S) and not g.B.any() and not g.C.any()
             assert g.x.shape == x.shape and g.A.shape == (D, S) and not g.A.any() and not g.D.any()
+
+
+def test_checkpoints_do_not_detach(layer):
+    """return_checkpoints with inputs that want a gradient: the same gradients as without."""
+    N, T, D, S = 2, 40, 32, 16
+    a, init, resets, _, _ = scan_inputs(N, T, D, S, F32, 41, "packed")
+    grads = []
+    for more in (False, True):
+        leaves = {k: v.to(DEV).requires_grad_() for k, v in {**a, "initial_state": init}.items()}
+        out = L().selective_scan(**leaves, resets=to_dev(resets), return_checkpoints=more)
+        assert out[0].requires_grad and out[1].requires_grad and len(out) == 2 + more
+        if more:
+            assert not out[2].requires_grad
+            plain = L().selective_scan(**{k: v.detach() for k, v in leaves.items()}, resets=to_dev(resets),
+                                       return_checkpoints=True)
+            assert all(torch.equal(p, q) for p, q in zip(out, plain))
+        (out[0].square().sum() + out[1].sum()).backward()
+        grads.append([v.grad for v in leaves.values()])
+    for p, q in zip(*grads):
+        assert torch.equal(p, q)
