@@ -5,8 +5,9 @@
  * their type, shape, strides and address from Python takes longer.  Each
  * function here does what its namesake in state_space.py does for arguments
  * in the usual form (plain CUDA tensors of the right type and shape, element
- * stride 1, no gradient wanted) and returns None for any others, which then
- * take the Python way and its error messages.  It needs Python.h alone; the
+ * stride 1, no gradient wanted, outside forward-mode differentiation) and
+ * returns None for any others, which then take the Python way and its error
+ * messages.  It needs Python.h alone; the
  * entry points' addresses come from the loaded library.
  */
 #define PY_SSIZE_T_CLEAN
@@ -23,8 +24,8 @@ typedef struct Tensor {
 } Tensor;
 
 static PyObject *g_tensor, *g_parameter, *g_f32, *g_bf16, *g_i32, *g_u8, *g_bool, *g_fp8, *g_empty,
-    *g_raw_stream, *g_grad_enabled, *g_norm_result;
-static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_requires_grad, *s_device, *kw_empty;
+    *g_raw_stream, *g_grad_enabled, *g_norm_result, *g_forward_ad;
+static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_requires_grad, *s_device, *s_level, *kw_empty;
 
 static size_t (*f_scan_ws)(const rlscan_selective_scan_args *);
 static rlscan_status (*f_scan)(const rlscan_selective_scan_args *, void *, float *, float *, void *, size_t,
@@ -174,6 +175,16 @@ static int stream_of(int64_t device, rlscan_stream_t *s)
     return !PyErr_Occurred();
 }
 
+/* whether tensors may carry tangents: inside a dual level (-1: none) */
+static int dual_level(void)
+{
+    PyObject *v = PyObject_GetAttr(g_forward_ad, s_level);
+    if (v == NULL) return 1;
+    const long level = PyLong_AsLong(v);
+    Py_DECREF(v);
+    return level >= 0 || PyErr_Occurred() != NULL;
+}
+
 /* "not in the usual form": the Python way takes over, and says what is wrong */
 static PyObject *other_way(void)
 {
@@ -237,7 +248,7 @@ static PyObject *selective_scan(PyObject *self, PyObject *const *args, Py_ssize_
     int64_t device = -1;
     const void *init, *resets, *lengths;
     rlscan_stream_t s;
-    if (n != 12 || !scan_args(args, &a, &dtype, &device, 0) ||
+    if (n != 12 || dual_level() || !scan_args(args, &a, &dtype, &device, 0) ||
         !array(args[9], &init, g_f32, &device, 0, 3, a.N, a.D, a.S) || !flags(args[10], &resets, &device, a.N, a.T) ||
         !array(args[11], &lengths, g_i32, &device, 0, 1, a.N, 0, 0) || !stream_of(device, &s))
         return other_way();
@@ -268,7 +279,7 @@ static PyObject *selective_scan_step(PyObject *self, PyObject *const *args, Py_s
     Tensor state;
     const void *slots;
     rlscan_stream_t s;
-    if (n != 11 || !scan_args(args + 1, &a, &dtype, &device, 1) || !look(args[0], &state, g_f32, &device) ||
+    if (n != 11 || dual_level() || !scan_args(args + 1, &a, &dtype, &device, 1) || !look(args[0], &state, g_f32, &device) ||
         !sized(&state, 3, state.size[0], a.D, a.S) || !dense(&state) ||
         !array(args[10], &slots, g_i32, &device, 0, 1, a.N, 0, 0) || !stream_of(device, &s))
         return other_way();
@@ -317,7 +328,7 @@ static PyObject *causal_conv(PyObject *self, PyObject *const *args, Py_ssize_t n
     int64_t device = -1;
     const void *resets, *lengths;
     rlscan_stream_t s;
-    if (n != 7 || !conv_args(args, &a, &dtype, &device, 0) || a.K < 2 ||
+    if (n != 7 || dual_level() || !conv_args(args, &a, &dtype, &device, 0) || a.K < 2 ||
         !array(args[4], &a.initial_state, dtype, &device, 0, 3, a.N, a.K - 1, a.D) ||
         !flags(args[5], &resets, &device, a.N, a.T) || !array(args[6], &lengths, g_i32, &device, 0, 1, a.N, 0, 0) ||
         !stream_of(device, &s))
@@ -343,7 +354,8 @@ static PyObject *causal_conv_step(PyObject *self, PyObject *const *args, Py_ssiz
     Tensor state;
     const void *slots;
     rlscan_stream_t s;
-    if (n != 6 || !conv_args(args + 1, &a, &dtype, &device, 1) || a.K < 2 || !look(args[0], &state, dtype, &device) ||
+    if (n != 6 || dual_level() || !conv_args(args + 1, &a, &dtype, &device, 1) || a.K < 2 ||
+        !look(args[0], &state, dtype, &device) ||
         !sized(&state, 3, state.size[0], a.K - 1, a.D) || !dense(&state) ||
         !array(args[5], &slots, g_i32, &device, 0, 1, a.N, 0, 0) || !stream_of(device, &s))
         return other_way();
@@ -363,7 +375,7 @@ static PyObject *add_rms_norm(PyObject *self, PyObject *const *args, Py_ssize_t 
     int64_t device = -1, code, rcode = RLSCAN_F32;
     const void *w;
     rlscan_stream_t s;
-    if (n != 5 || !io_type(args[0], &dtype, &code) || !look(args[0], &x, dtype, &device) || x.dims != 2 ||
+    if (n != 5 || dual_level() || !io_type(args[0], &dtype, &code) || !look(args[0], &x, dtype, &device) || x.dims != 2 ||
         x.stride[1] != 1 || !array(args[1], &w, g_f32, &device, 1, 1, x.size[1], 0, 0) || !PyFloat_Check(args[3]))
         return other_way();
     const int eight = args[4] == g_fp8, summed = args[2] != Py_None;
@@ -391,12 +403,13 @@ static PyObject *add_rms_norm(PyObject *self, PyObject *const *args, Py_ssize_t 
     return result != NULL ? result : other_way();
 }
 
-/* setup(torch, RmsNorm, raw stream function, addresses of the six entry points) */
+/* setup(torch, RmsNorm, raw stream function, torch.autograd.forward_ad, addresses of the six entry points) */
 static PyObject *setup(PyObject *self, PyObject *args)
 {
-    PyObject *torch, *result, *stream;
+    PyObject *torch, *result, *stream, *forward_ad;
     unsigned long long f[6];
-    if (!PyArg_ParseTuple(args, "OOOKKKKKK", &torch, &result, &stream, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5]))
+    if (!PyArg_ParseTuple(args, "OOOOKKKKKK", &torch, &result, &stream, &forward_ad, &f[0], &f[1], &f[2], &f[3], &f[4],
+                          &f[5]))
         return NULL;
     const struct {
         PyObject **to;
@@ -414,6 +427,8 @@ static PyObject *setup(PyObject *self, PyObject *args)
     g_norm_result = result;
     Py_INCREF(stream);
     g_raw_stream = stream;
+    Py_INCREF(forward_ad);
+    g_forward_ad = forward_ad;
     s_dtype = PyUnicode_InternFromString("dtype");
     s_shape = PyUnicode_InternFromString("shape");
     s_stride = PyUnicode_InternFromString("stride");
@@ -421,8 +436,10 @@ static PyObject *setup(PyObject *self, PyObject *args)
     s_get_device = PyUnicode_InternFromString("get_device");
     s_requires_grad = PyUnicode_InternFromString("requires_grad");
     s_device = PyUnicode_InternFromString("device");
+    s_level = PyUnicode_InternFromString("_current_level");
     kw_empty = Py_BuildValue("(ss)", "dtype", "device");
-    if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_get_device || !s_requires_grad || !s_device || !kw_empty)
+    if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_get_device || !s_requires_grad || !s_device || !s_level ||
+        !kw_empty)
         return NULL;
     f_scan_ws = (size_t (*)(const rlscan_selective_scan_args *))(uintptr_t)f[0];
     f_scan = (rlscan_status (*)(const rlscan_selective_scan_args *, void *, float *, float *, void *, size_t,

@@ -11,7 +11,8 @@ of the scan are float32.
 
 ``selective_scan``, ``causal_conv`` and ``add_rms_norm`` are differentiable
 when an input requires a gradient (once; the gradients themselves are not);
-the ``*_backward`` functions are the same gradients as plain calls.
+the ``*_backward`` functions are the same gradients as plain calls.  Nothing
+here has a forward-mode derivative: dual tensors are refused.
 """
 from __future__ import annotations
 
@@ -23,6 +24,7 @@ import struct
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from . import _native
 from .api import _raw_stream, _stream_handle
@@ -73,7 +75,7 @@ def _load_fast():
             spec = importlib.util.spec_from_file_location("_fastcall", path)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
-            module.setup(torch, RmsNorm, _raw_stream, *(
+            module.setup(torch, RmsNorm, _raw_stream, _forward_ad, *(
                 ctypes.cast(getattr(lib, "rlscan_" + name), ctypes.c_void_p).value for name in (
                     "selective_scan_workspace_bytes", "selective_scan", "selective_scan_step", "causal_conv",
                     "causal_conv_step", "add_rms_norm")))
@@ -169,6 +171,15 @@ def _wants_grad(*ts):
             if t is not None and getattr(t, "requires_grad", False):
                 return True
     return False
+
+
+def _refuse_tangents(*ts):
+    """These functions have no forward-mode derivative: dual tensors, which
+    live inside a dual level only, would lose their tangents."""
+    if _forward_ad._current_level >= 0:
+        for t in ts:
+            if isinstance(t, torch.Tensor) and _forward_ad.unpack_dual(t).tangent is not None:
+                raise RuntimeError("the state-space layer's functions have no forward-mode derivative")
 
 
 def _scratch(nbytes, device):
@@ -286,6 +297,7 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_sof
                                                      initial_state, resets, lengths)
         if out is not None:
             return out
+    _refuse_tangents(x, delta, A, B, C, D, z, delta_bias, initial_state)
     args = (x, delta, A, B, C, D, z, delta_bias, delta_softplus, initial_state, resets, lengths)
     out = (_SelectiveScan.apply(*args) if _wants_grad(x, delta, A, B, C, D, z, delta_bias, initial_state)
            else _scan_forward(return_checkpoints, *args))
@@ -297,6 +309,7 @@ def selective_scan_backward(grad_y, x, delta, A, B, C, checkpoints, D=None, z=No
     """Gradients of selective_scan: ``grad_y`` like x, ``checkpoints`` from the
     forward call on the same inputs, ``grad_final_state`` [N,channels,S]
     float32 or None.  Returns SelectiveScanGrads."""
+    _refuse_tangents(grad_y, x, delta, A, B, C, checkpoints, D, z, delta_bias, grad_final_state)
     dev, (N, T, width, S), packed, kept = _scan_args(False, x, delta, A, B, C, D, z, delta_bias, delta_softplus,
                                                      None, resets, lengths)
     x = kept[0]
@@ -334,6 +347,7 @@ def selective_scan_step(state, x, delta, A, B, C, D=None, z=None, delta_bias=Non
     y = (_fast or _load_fast()).selective_scan_step(state, x, delta, A, B, C, D, z, delta_bias, delta_softplus, slots)
     if y is not None:
         return y
+    _refuse_tangents(state, x, delta, A, B, C, D, z, delta_bias)
     dev, (N, _, width, S), packed, kept = _scan_args(True, x, delta, A, B, C, D, z, delta_bias, delta_softplus, None,
                                                      None, None)
     P = _slot_pool(state, (width, S), torch.float32, dev)
@@ -438,6 +452,7 @@ def causal_conv(x, weight, bias=None, activation="silu", initial_state=None, res
     out = (_fast or _load_fast()).causal_conv(x, weight, bias, activation, initial_state, resets, lengths)
     if out is not None:
         return out
+    _refuse_tangents(x, weight, bias, initial_state)
     if _wants_grad(x, weight, bias, initial_state):
         return _CausalConv.apply(x, weight, bias, activation, initial_state, resets, lengths)
     return _conv_forward(x, weight, bias, activation, initial_state, resets, lengths)
@@ -447,6 +462,7 @@ def causal_conv_backward(grad_y, x, weight, bias=None, activation="silu", initia
                          lengths=None, grad_final_state=None):
     """Gradients of causal_conv (``grad_final_state`` [N,K-1,channels] of x's
     type or None).  Returns CausalConvGrads."""
+    _refuse_tangents(grad_y, x, weight, bias, initial_state, grad_final_state)
     dev, (N, T, width, K), packed, kept = _conv_args(False, x, weight, bias, activation, initial_state, resets, lengths)
     x = kept[0]
     gp, gr, gt, grad_y = _act("grad_y", grad_y, x.shape, x.dtype, dev)
@@ -473,6 +489,7 @@ def causal_conv_step(state, x, weight, bias=None, activation="silu", slots=None)
     y = (_fast or _load_fast()).causal_conv_step(state, x, weight, bias, activation, slots)
     if y is not None:
         return y
+    _refuse_tangents(state, x, weight, bias)
     dev, (N, _, width, K), packed, kept = _conv_args(True, x, weight, bias, activation, None, None, None)
     P = _slot_pool(state, (K - 1, width), x.dtype, dev)
     slots = _dense("slots", slots, (N,), torch.int32, dev)
@@ -590,6 +607,7 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None):
     out = (_fast or _load_fast()).add_rms_norm(x, weight, residual, eps, out_dtype)
     if out is not None:
         return out
+    _refuse_tangents(x, weight, residual)
     if out_dtype != torch.float8_e4m3fn and _wants_grad(x, weight, residual):
         if out_dtype not in (None, x.dtype):
             raise ValueError("out_dtype must be x's type or torch.float8_e4m3fn")
@@ -603,6 +621,7 @@ def add_rms_norm_backward(grad_y, h, weight, grad_residual=None, eps=1e-6):
     (x itself where there was none): ``grad_y`` float32 or bfloat16, h of its
     type or float32, ``grad_residual`` the gradient of the returned sum (h's
     type) or None.  Returns RmsNormGrads."""
+    _refuse_tangents(grad_y, h, weight, grad_residual)
     dev, M, width, weight = _norm_lead("grad_y", grad_y, weight, eps)
     shape = grad_y.shape
     if not isinstance(h, torch.Tensor) or h.dtype not in (grad_y.dtype, torch.float32):

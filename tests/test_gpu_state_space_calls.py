@@ -67,3 +67,39 @@ def test_checkpoints_do_not_detach(layer):
         grads.append([v.grad for v in leaves.values()])
     for p, q in zip(*grads):
         assert torch.equal(p, q)
+
+
+def test_forward_mode_is_refused(layer):
+    """A tangent would be lost without a word: dual tensors are refused, others pass inside a dual level."""
+    import torch.autograd.forward_ad as fwd
+    N, T, D, S, K = 2, 20, 16, 4, 4
+    a, init, _, _, _ = scan_inputs(N, T, D, S, F32, 42)
+    dev = {k: v.to(DEV) for k, v in a.items()}
+    step = {k: (v[:, 0].contiguous() if k in ("x", "delta", "z", "B", "C") else v) for k, v in dev.items()}
+    x, w, nw = dev["x"], torch.randn(D, K, device=DEV), torch.ones(D, device=DEV)
+    _, _, marks = L().selective_scan(**dev, return_checkpoints=True)
+    scan = ("x", "delta", "A", "B", "C", "D", "z", "delta_bias")
+    calls = [(lambda f, k=k: L().selective_scan(**{**dev, k: f(dev[k])})) for k in scan]
+    calls += [(lambda f, k=k: L().selective_scan_step(init.to(DEV), **{**step, k: f(step[k])})) for k in scan]
+    calls += [
+        lambda f: L().selective_scan(**dev, initial_state=f(init.to(DEV))),
+        lambda f: L().selective_scan(**{**dev, "x": f(x)}, return_checkpoints=True),
+        lambda f: L().selective_scan_step(f(init.to(DEV)), **step),
+        lambda f: L().selective_scan_backward(f(x), x, dev["delta"], dev["A"], dev["B"], dev["C"], marks),
+        lambda f: L().selective_scan_backward(x, x, f(dev["delta"]), dev["A"], dev["B"], dev["C"], marks),
+        lambda f: L().causal_conv(f(x), w), lambda f: L().causal_conv(x, f(w)), lambda f: L().causal_conv(x, w, f(nw)),
+        lambda f: L().causal_conv(x, w, initial_state=f(torch.zeros(N, K - 1, D, device=DEV))),
+        lambda f: L().causal_conv_step(torch.zeros(N, K - 1, D, device=DEV), f(step["x"]), w),
+        lambda f: L().causal_conv_backward(f(x), x, w), lambda f: L().causal_conv_backward(x, x, f(w)),
+        lambda f: L().add_rms_norm(f(step["x"]), nw), lambda f: L().add_rms_norm(step["x"], f(nw)),
+        lambda f: L().add_rms_norm(step["x"], nw, f(step["x"])),
+        lambda f: L().add_rms_norm(f(step["x"]), nw, out_dtype=torch.float8_e4m3fn),
+        lambda f: L().add_rms_norm_backward(f(step["x"]), step["x"], nw),
+        lambda f: L().add_rms_norm_backward(step["x"], f(step["x"]), nw)]
+    with fwd.dual_level():
+        for call in calls:
+            call(lambda t: t)
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                call(lambda t: fwd.make_dual(t, torch.ones_like(t)))
+            with pytest.raises(RuntimeError, match="forward-mode"), torch.no_grad():
+                call(lambda t: fwd.make_dual(t, torch.ones_like(t)))

@@ -1,5 +1,5 @@
 """The state-space layer's host side without a GPU: workspace queries of
-empty calls."""
+empty calls, refusals."""
 import os
 import subprocess
 import sys
@@ -34,3 +34,25 @@ def test_empty_calls_need_no_workspace(lib):
     """No rows or no channels: the queries answer 0 (in a child: an integer division by zero ends the process)."""
     r = subprocess.run([sys.executable, "-c", EMPTY], capture_output=True, text=True, cwd=ROOT, timeout=300)
     assert r.returncode == 0 and "done" in r.stdout, (r.returncode, r.stderr[-2000:])
+
+
+def test_forward_mode_is_refused():
+    """Dual tensors are refused before anything else is looked at; others pass inside a dual level."""
+    import torch
+    import torch.autograd.forward_ad as fwd
+    import linear_recurrence_scan_gb300 as rl
+    x, bc, A, w = torch.zeros(2, 4, 8), torch.zeros(2, 4, 3), torch.zeros(8, 3), torch.zeros(8, 4)
+    state, marks = torch.zeros(2, 8, 3), torch.zeros(2, 1, 8, 3)
+    calls = [lambda f: rl.selective_scan(f(x), x, A, bc, bc), lambda f: rl.selective_scan(x, x, A, f(bc), bc),
+             lambda f: rl.selective_scan(x, x, A, bc, bc, initial_state=f(state)),
+             lambda f: rl.selective_scan_backward(x, x, x, f(A), bc, bc, marks),
+             lambda f: rl.selective_scan_step(state, x[:, 0], f(x[:, 0]), A, bc[:, 0], bc[:, 0]),
+             lambda f: rl.causal_conv(x, f(w)), lambda f: rl.causal_conv_backward(f(x), x, w),
+             lambda f: rl.causal_conv_step(torch.zeros(2, 3, 8), f(x[:, 0]), w),
+             lambda f: rl.add_rms_norm(f(x), A[:, 0]), lambda f: rl.add_rms_norm_backward(x, f(x), A[:, 0])]
+    with fwd.dual_level():
+        for call in calls:
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                call(lambda t: fwd.make_dual(t, torch.ones_like(t)))
+            with pytest.raises(ValueError, match="CUDA"):
+                call(lambda t: t)
