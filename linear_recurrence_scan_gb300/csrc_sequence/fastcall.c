@@ -24,7 +24,7 @@ typedef struct Tensor {
 } Tensor;
 
 static PyObject *g_tensor, *g_parameter, *g_f32, *g_bf16, *g_i32, *g_u8, *g_bool, *g_fp8, *g_empty,
-    *g_raw_stream, *g_grad_enabled, *g_norm_result, *g_forward_ad;
+    *g_raw_stream, *g_grad_enabled, *g_norm_result, *g_forward_ad, *g_changed;
 static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_requires_grad, *s_device, *s_level, *kw_empty;
 
 static size_t (*f_scan_ws)(const rlscan_selective_scan_args *);
@@ -270,6 +270,15 @@ static PyObject *selective_scan(PyObject *self, PyObject *const *args, Py_ssize_
     return r != NULL ? r : other_way();
 }
 
+/* y of a call that has updated its state, which autograd is told */
+static PyObject *updated(PyObject *state, PyObject *y)
+{
+    PyObject *r = PyObject_CallOneArg(g_changed, state);
+    if (r == NULL) Py_CLEAR(y);
+    Py_XDECREF(r);
+    return y;
+}
+
 /* selective_scan_step(state, x, delta, A, B, C, D, z, delta_bias, delta_softplus, slots) */
 static PyObject *selective_scan_step(PyObject *self, PyObject *const *args, Py_ssize_t n)
 {
@@ -287,7 +296,7 @@ static PyObject *selective_scan_step(PyObject *self, PyObject *const *args, Py_s
     PyObject *y = new_tensor(args[1], 2, a.N, a.D, 0, dtype, &yp);
     if (y != NULL &&
         f_scan_step(&a, (float *)state.data, state.size[0], (const int32_t *)slots, yp, s) == RLSCAN_OK)
-        return y;
+        return updated(args[0], y);
     Py_XDECREF(y);
     return other_way();
 }
@@ -362,7 +371,7 @@ static PyObject *causal_conv_step(PyObject *self, PyObject *const *args, Py_ssiz
     void *yp;
     PyObject *y = new_tensor(args[1], 2, a.N, a.D, 0, dtype, &yp);
     if (y != NULL && f_conv_step(&a, (void *)state.data, state.size[0], (const int32_t *)slots, yp, s) == RLSCAN_OK)
-        return y;
+        return updated(args[0], y);
     Py_XDECREF(y);
     return other_way();
 }
@@ -403,13 +412,14 @@ static PyObject *add_rms_norm(PyObject *self, PyObject *const *args, Py_ssize_t 
     return result != NULL ? result : other_way();
 }
 
-/* setup(torch, RmsNorm, raw stream function, torch.autograd.forward_ad, addresses of the six entry points) */
+/* setup(torch, RmsNorm, raw stream function, torch.autograd.forward_ad, increment_version, addresses of the six
+ * entry points) */
 static PyObject *setup(PyObject *self, PyObject *args)
 {
-    PyObject *torch, *result, *stream, *forward_ad;
+    PyObject *torch, *result, *stream, *forward_ad, *changed;
     unsigned long long f[6];
-    if (!PyArg_ParseTuple(args, "OOOOKKKKKK", &torch, &result, &stream, &forward_ad, &f[0], &f[1], &f[2], &f[3], &f[4],
-                          &f[5]))
+    if (!PyArg_ParseTuple(args, "OOOOOKKKKKK", &torch, &result, &stream, &forward_ad, &changed, &f[0], &f[1], &f[2],
+                          &f[3], &f[4], &f[5]))
         return NULL;
     const struct {
         PyObject **to;
@@ -429,6 +439,8 @@ static PyObject *setup(PyObject *self, PyObject *args)
     g_raw_stream = stream;
     Py_INCREF(forward_ad);
     g_forward_ad = forward_ad;
+    Py_INCREF(changed);
+    g_changed = changed;
     s_dtype = PyUnicode_InternFromString("dtype");
     s_shape = PyUnicode_InternFromString("shape");
     s_stride = PyUnicode_InternFromString("stride");

@@ -40,6 +40,7 @@ MAX_STATES = 128
 MAX_TAPS = 8
 SCALE_BLOCK = 128  # columns that share one scale of an 8-bit output
 
+_changed = torch.autograd.graph.increment_version   # what a graph saved of a state is then known to be stale
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 _SCAN_ARGS = struct.Struct("=27q")
 _SCAN_GRADS = struct.Struct("=9q")
@@ -75,7 +76,7 @@ def _load_fast():
             spec = importlib.util.spec_from_file_location("_fastcall", path)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
-            module.setup(torch, RmsNorm, _raw_stream, _forward_ad, *(
+            module.setup(torch, RmsNorm, _raw_stream, _forward_ad, _changed, *(
                 ctypes.cast(getattr(lib, "rlscan_" + name), ctypes.c_void_p).value for name in (
                     "selective_scan_workspace_bytes", "selective_scan", "selective_scan_step", "causal_conv",
                     "causal_conv_step", "add_rms_norm")))
@@ -357,6 +358,7 @@ def selective_scan_step(state, x, delta, A, B, C, D=None, z=None, delta_bias=Non
     y = torch.empty((N, width), dtype=x.dtype, device=x.device)
     _native.check(_native.lib().rlscan_selective_scan_step(packed, state.data_ptr(), P, _at(slots), y.data_ptr(),
                                                            _stream_handle(x.device)), "rlscan_selective_scan_step")
+    _changed(state)
     return y
 
 
@@ -498,6 +500,7 @@ def causal_conv_step(state, x, weight, bias=None, activation="silu", slots=None)
     y = torch.empty((N, width), dtype=x.dtype, device=x.device)
     _native.check(_native.lib().rlscan_causal_conv_step(packed, state.data_ptr(), P, _at(slots), y.data_ptr(),
                                                         _stream_handle(x.device)), "rlscan_causal_conv_step")
+    _changed(state)
     return y
 
 

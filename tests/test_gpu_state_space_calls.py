@@ -103,3 +103,26 @@ def test_forward_mode_is_refused(layer):
                 call(lambda t: fwd.make_dual(t, torch.ones_like(t)))
             with pytest.raises(RuntimeError, match="forward-mode"), torch.no_grad():
                 call(lambda t: fwd.make_dual(t, torch.ones_like(t)))
+
+
+def test_states_updated_in_place_are_seen_by_autograd(layer):
+    """A step changes its state: a graph that saved the state refuses to go back with the changed one."""
+    N, T, D, S, K = 2, 12, 16, 4, 4
+    a, init, _, _, _ = scan_inputs(N, T, D, S, F32, 43)
+    dev = {k: v.to(DEV) for k, v in a.items()}
+    step = {k: (v[:, 0].contiguous() if k in ("x", "delta", "z", "B", "C") else v) for k, v in dev.items()}
+    state, window, w = init.to(DEV), torch.randn(N, K - 1, D, device=DEV), torch.randn(D, K, device=DEV)
+    scale = torch.ones(1, device=DEV, requires_grad=True)
+    kept, before = scale * state, (state._version, window._version)
+    y, _ = L().causal_conv(dev["x"], w.clone().requires_grad_(), initial_state=window)
+    with torch.no_grad():
+        L().selective_scan_step(state, **step)
+        L().causal_conv_step(window, step["x"], w)
+    assert state._version > before[0] and window._version > before[1]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        kept.sum().backward()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    with torch.inference_mode():   # tensors without a version counter
+        L().selective_scan_step(init.to(DEV), **step)
+        L().causal_conv_step(torch.zeros(N, K - 1, D, device=DEV), step["x"], w)
