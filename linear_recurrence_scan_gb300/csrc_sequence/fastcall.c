@@ -5,9 +5,9 @@
  * their type, shape, strides and address from Python takes longer.  Each
  * function here does what its namesake in state_space.py does for arguments
  * in the usual form (plain CUDA tensors of the right type and shape, element
- * stride 1, no gradient wanted, outside forward-mode differentiation) and
- * returns None for any others, which then take the Python way and its error
- * messages.  It needs Python.h alone; the
+ * stride 1, no gradient wanted, outside forward-mode differentiation, on the
+ * current device) and returns None for any others, which then take the
+ * Python way and its error messages.  It needs Python.h alone; the
  * entry points' addresses come from the loaded library.
  */
 #define PY_SSIZE_T_CLEAN
@@ -24,7 +24,8 @@ typedef struct Tensor {
 } Tensor;
 
 static PyObject *g_tensor, *g_parameter, *g_f32, *g_bf16, *g_i32, *g_u8, *g_bool, *g_fp8, *g_empty,
-    *g_raw_stream, *g_grad_enabled, *g_norm_result, *g_forward_ad, *g_changed;
+    *g_raw_stream, *g_grad_enabled, *g_norm_result, *g_current_device, *g_forward_ad,
+    *g_changed;
 static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_requires_grad, *s_device, *s_level, *kw_empty;
 
 static size_t (*f_scan_ws)(const rlscan_selective_scan_args *);
@@ -163,10 +164,15 @@ static PyObject *new_tensor(PyObject *like, int dims, int64_t a, int64_t b, int6
     return r;
 }
 
+/* the current stream of `device`, which has to be the current device */
 static int stream_of(int64_t device, rlscan_stream_t *s)
 {
-    PyObject *d = PyLong_FromLongLong(device);
+    PyObject *d = PyObject_CallNoArgs(g_current_device);
     if (d == NULL) return 0;
+    if (PyLong_AsLongLong(d) != device) {
+        Py_DECREF(d);
+        return 0;
+    }
     PyObject *r = PyObject_CallOneArg(g_raw_stream, d);
     Py_DECREF(d);
     if (r == NULL) return 0;
@@ -412,14 +418,14 @@ static PyObject *add_rms_norm(PyObject *self, PyObject *const *args, Py_ssize_t 
     return result != NULL ? result : other_way();
 }
 
-/* setup(torch, RmsNorm, raw stream function, torch.autograd.forward_ad, increment_version, addresses of the six
- * entry points) */
+/* setup(torch, RmsNorm, raw stream function, current device function, torch.autograd.forward_ad, increment_version,
+ * addresses of the six entry points) */
 static PyObject *setup(PyObject *self, PyObject *args)
 {
-    PyObject *torch, *result, *stream, *forward_ad, *changed;
+    PyObject *torch, *result, *stream, *device, *forward_ad, *changed;
     unsigned long long f[6];
-    if (!PyArg_ParseTuple(args, "OOOOOKKKKKK", &torch, &result, &stream, &forward_ad, &changed, &f[0], &f[1], &f[2],
-                          &f[3], &f[4], &f[5]))
+    if (!PyArg_ParseTuple(args, "OOOOOOKKKKKK", &torch, &result, &stream, &device, &forward_ad, &changed, &f[0], &f[1],
+                          &f[2], &f[3], &f[4], &f[5]))
         return NULL;
     const struct {
         PyObject **to;
@@ -437,6 +443,8 @@ static PyObject *setup(PyObject *self, PyObject *args)
     g_norm_result = result;
     Py_INCREF(stream);
     g_raw_stream = stream;
+    Py_INCREF(device);
+    g_current_device = device;
     Py_INCREF(forward_ad);
     g_forward_ad = forward_ad;
     Py_INCREF(changed);

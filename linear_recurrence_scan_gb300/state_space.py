@@ -3,8 +3,8 @@ causal convolution in front of it and the root-mean-square norm in front of
 the layer, over prompts, in training and for single tokens.
 
 Like the estimators, each function checks its arguments, allocates the
-outputs with torch and makes one librlscan call on the current CUDA stream,
-without synchronising; there is no CPU path.  Unlike the estimators, tensors
+outputs with torch and makes one librlscan call on the current CUDA stream
+of the tensors' device, without synchronising; there is no CPU path.  Unlike the estimators, tensors
 live on the GPU, activations are token-major ([N, T, width], any strides over
 rows and tokens) and float32 or bfloat16, and parameters and recurrent states
 of the scan are float32.
@@ -16,6 +16,7 @@ here has a forward-mode derivative: dual tensors are refused.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -41,6 +42,8 @@ MAX_TAPS = 8
 SCALE_BLOCK = 128  # columns that share one scale of an 8-bit output
 
 _changed = torch.autograd.graph.increment_version   # what a graph saved of a state is then known to be stale
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_HERE = contextlib.nullcontext()
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 _SCAN_ARGS = struct.Struct("=27q")
 _SCAN_GRADS = struct.Struct("=9q")
@@ -72,16 +75,19 @@ def _load_fast():
         if not os.path.exists(path) or _raw_stream is None:
             _fast = _NoFastCall
         else:
-            lib = _native.lib()
             spec = importlib.util.spec_from_file_location("_fastcall", path)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
-            module.setup(torch, RmsNorm, _raw_stream, _forward_ad, _changed, *(
-                ctypes.cast(getattr(lib, "rlscan_" + name), ctypes.c_void_p).value for name in (
-                    "selective_scan_workspace_bytes", "selective_scan", "selective_scan_step", "causal_conv",
-                    "causal_conv_step", "add_rms_norm")))
+            _setup(module)
             _fast = module
     return _fast
+
+
+def _setup(module):
+    module.setup(torch, RmsNorm, _raw_stream, _current_device, _forward_ad, _changed, *(
+        ctypes.cast(getattr(_native.lib(), "rlscan_" + name), ctypes.c_void_p).value for name in (
+            "selective_scan_workspace_bytes", "selective_scan", "selective_scan_step", "causal_conv",
+            "causal_conv_step", "add_rms_norm")))
 
 
 # ---------------------------------------------------------------------------
@@ -183,6 +189,11 @@ def _refuse_tangents(*ts):
                 raise RuntimeError("the state-space layer's functions have no forward-mode derivative")
 
 
+def _on(device):
+    """Plans, workspace sizes and launches are the current device's: makes it the tensors' own."""
+    return _HERE if _current_device() == device else torch.cuda.device(device)
+
+
 def _scratch(nbytes, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
@@ -244,10 +255,11 @@ def _scan_forward(want_checkpoints, *args):
     final = torch.empty((N, width, S), **f32)
     marks = torch.empty((N, -(-T // CHECKPOINT), width, S), **f32) if want_checkpoints else None
     lib = _native.lib()
-    ws = _scratch(lib.rlscan_selective_scan_workspace_bytes(packed), x.device)
-    _native.check(lib.rlscan_selective_scan(packed, y.data_ptr(), final.data_ptr(), _at(marks), _at(ws),
-                                            0 if ws is None else ws.numel(), _stream_handle(x.device)),
-                  "rlscan_selective_scan")
+    with _on(dev):
+        ws = _scratch(lib.rlscan_selective_scan_workspace_bytes(packed), x.device)
+        _native.check(lib.rlscan_selective_scan(packed, y.data_ptr(), final.data_ptr(), _at(marks), _at(ws),
+                                                0 if ws is None else ws.numel(), _stream_handle(x.device)),
+                      "rlscan_selective_scan")
     return y, final, marks
 
 
@@ -330,12 +342,13 @@ def selective_scan_backward(grad_y, x, delta, A, B, C, checkpoints, D=None, z=No
         C=like((N, T, S), dtype), D=like((width,), when=D is not None), z=like(acts, dtype, z is not None),
         delta_bias=like((width,), when=delta_bias is not None), initial_state=like((N, width, S)))
     lib = _native.lib()
-    ws = _scratch(lib.rlscan_selective_scan_backward_workspace_bytes(packed), x.device)
-    _native.check(lib.rlscan_selective_scan_backward(
-        packed, _ARRAY3.pack(gp, gr, gt), _at(gfinal), marks.data_ptr(),
-        _SCAN_GRADS.pack(_at(g.x), _at(g.delta), _at(g.z), _at(g.B), _at(g.C), _at(g.A), _at(g.D),
-                         _at(g.delta_bias), _at(g.initial_state)),
-        _at(ws), 0 if ws is None else ws.numel(), _stream_handle(x.device)), "rlscan_selective_scan_backward")
+    with _on(dev):
+        ws = _scratch(lib.rlscan_selective_scan_backward_workspace_bytes(packed), x.device)
+        _native.check(lib.rlscan_selective_scan_backward(
+            packed, _ARRAY3.pack(gp, gr, gt), _at(gfinal), marks.data_ptr(),
+            _SCAN_GRADS.pack(_at(g.x), _at(g.delta), _at(g.z), _at(g.B), _at(g.C), _at(g.A), _at(g.D),
+                             _at(g.delta_bias), _at(g.initial_state)),
+            _at(ws), 0 if ws is None else ws.numel(), _stream_handle(x.device)), "rlscan_selective_scan_backward")
     return g
 
 
@@ -356,8 +369,9 @@ def selective_scan_step(state, x, delta, A, B, C, D=None, z=None, delta_bias=Non
     if slots is None and P < N:
         raise ValueError(f"state holds {P} slots for {N} sequences")
     y = torch.empty((N, width), dtype=x.dtype, device=x.device)
-    _native.check(_native.lib().rlscan_selective_scan_step(packed, state.data_ptr(), P, _at(slots), y.data_ptr(),
-                                                           _stream_handle(x.device)), "rlscan_selective_scan_step")
+    with _on(dev):
+        _native.check(_native.lib().rlscan_selective_scan_step(packed, state.data_ptr(), P, _at(slots), y.data_ptr(),
+                                                               _stream_handle(x.device)), "rlscan_selective_scan_step")
     _changed(state)
     return y
 
@@ -415,8 +429,9 @@ def _conv_forward(x, weight, bias, activation, initial_state, resets, lengths):
     x = kept[0]
     y = torch.empty((N, T, width), dtype=x.dtype, device=x.device)
     final = torch.empty((N, K - 1, width), dtype=x.dtype, device=x.device)
-    _native.check(_native.lib().rlscan_causal_conv(packed, y.data_ptr(), final.data_ptr(), _stream_handle(x.device)),
-                  "rlscan_causal_conv")
+    with _on(dev):
+        _native.check(_native.lib().rlscan_causal_conv(packed, y.data_ptr(), final.data_ptr(),
+                                                       _stream_handle(x.device)), "rlscan_causal_conv")
     return y, final
 
 
@@ -475,11 +490,12 @@ def causal_conv_backward(grad_y, x, weight, bias=None, activation="silu", initia
         bias=torch.empty((width,), **f32) if bias is not None else None,
         initial_state=torch.empty((N, K - 1, width), dtype=x.dtype, device=x.device))
     lib = _native.lib()
-    ws = _scratch(lib.rlscan_causal_conv_backward_workspace_bytes(packed), x.device)
-    _native.check(lib.rlscan_causal_conv_backward(
-        packed, _ARRAY3.pack(gp, gr, gt), _at(gfinal), g.x.data_ptr(), g.weight.data_ptr(), _at(g.bias),
-        g.initial_state.data_ptr(), _at(ws), 0 if ws is None else ws.numel(), _stream_handle(x.device)),
-        "rlscan_causal_conv_backward")
+    with _on(dev):
+        ws = _scratch(lib.rlscan_causal_conv_backward_workspace_bytes(packed), x.device)
+        _native.check(lib.rlscan_causal_conv_backward(
+            packed, _ARRAY3.pack(gp, gr, gt), _at(gfinal), g.x.data_ptr(), g.weight.data_ptr(), _at(g.bias),
+            g.initial_state.data_ptr(), _at(ws), 0 if ws is None else ws.numel(), _stream_handle(x.device)),
+            "rlscan_causal_conv_backward")
     return g
 
 
@@ -498,8 +514,9 @@ def causal_conv_step(state, x, weight, bias=None, activation="silu", slots=None)
     if slots is None and P < N:
         raise ValueError(f"state holds {P} slots for {N} sequences")
     y = torch.empty((N, width), dtype=x.dtype, device=x.device)
-    _native.check(_native.lib().rlscan_causal_conv_step(packed, state.data_ptr(), P, _at(slots), y.data_ptr(),
-                                                        _stream_handle(x.device)), "rlscan_causal_conv_step")
+    with _on(dev):
+        _native.check(_native.lib().rlscan_causal_conv_step(packed, state.data_ptr(), P, _at(slots), y.data_ptr(),
+                                                            _stream_handle(x.device)), "rlscan_causal_conv_step")
     _changed(state)
     return y
 
@@ -571,9 +588,10 @@ def _norm_forward(x, weight, residual, eps, out_dtype):
     scales = None
     if eight:
         scales = torch.empty((*shape[:-1], -(-width // SCALE_BLOCK)), dtype=torch.float32, device=x.device)
-    _native.check(_native.lib().rlscan_add_rms_norm(
-        xp, xs, rp, rs, weight.data_ptr(), M, width, eps, _TYPES[x.dtype], rtype, y.data_ptr(), _at(scales),
-        _at(summed), _stream_handle(x.device)), "rlscan_add_rms_norm")
+    with _on(dev):
+        _native.check(_native.lib().rlscan_add_rms_norm(
+            xp, xs, rp, rs, weight.data_ptr(), M, width, eps, _TYPES[x.dtype], rtype, y.data_ptr(), _at(scales),
+            _at(summed), _stream_handle(x.device)), "rlscan_add_rms_norm")
     return RmsNorm(y, summed, scales)
 
 
@@ -638,9 +656,10 @@ def add_rms_norm_backward(grad_y, h, weight, grad_residual=None, eps=1e-6):
     gh = gx if h.dtype == grad_y.dtype else torch.empty(shape, dtype=h.dtype, device=h.device)
     gw = torch.empty((width,), dtype=torch.float32, device=grad_y.device)
     lib = _native.lib()
-    ws = _scratch(lib.rlscan_add_rms_norm_backward_workspace_bytes(M, width), grad_y.device)
-    _native.check(lib.rlscan_add_rms_norm_backward(
-        yp, ys, hp, hs, gp, gs, weight.data_ptr(), M, width, eps, _TYPES[grad_y.dtype], _TYPES[h.dtype],
-        gx.data_ptr(), 0 if gh is gx else gh.data_ptr(), gw.data_ptr(), _at(ws), 0 if ws is None else ws.numel(),
-        _stream_handle(grad_y.device)), "rlscan_add_rms_norm_backward")
+    with _on(dev):
+        ws = _scratch(lib.rlscan_add_rms_norm_backward_workspace_bytes(M, width), grad_y.device)
+        _native.check(lib.rlscan_add_rms_norm_backward(
+            yp, ys, hp, hs, gp, gs, weight.data_ptr(), M, width, eps, _TYPES[grad_y.dtype], _TYPES[h.dtype],
+            gx.data_ptr(), 0 if gh is gx else gh.data_ptr(), gw.data_ptr(), _at(ws), 0 if ws is None else ws.numel(),
+            _stream_handle(grad_y.device)), "rlscan_add_rms_norm_backward")
     return RmsNormGrads(gx, gw, gh)

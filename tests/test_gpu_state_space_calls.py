@@ -126,3 +126,66 @@ def test_states_updated_in_place_are_seen_by_autograd(layer):
     with torch.inference_mode():   # tensors without a version counter
         L().selective_scan_step(init.to(DEV), **step)
         L().causal_conv_step(torch.zeros(N, K - 1, D, device=DEV), step["x"], w)
+
+
+def test_a_call_runs_on_its_tensors_device(monkeypatch):
+    """Another device is current (as far as the calls can tell): each makes its tensors' own current while it plans
+    and launches, and the native call layer leaves the call to Python."""
+    from linear_recurrence_scan_gb300 import state_space as ss
+    N, T, D, S, K = 2, 20, 16, 4, 4
+    a, init, _, _, _ = scan_inputs(N, T, D, S, F32, 44)
+    dev = {k: v.to(DEV) for k, v in a.items()}
+    step = {k: (v[:, 0].contiguous() if k in ("x", "delta", "z", "B", "C") else v) for k, v in dev.items()}
+    x, w, nw = dev["x"], torch.randn(D, K, device=DEV), torch.ones(D, device=DEV)
+    y, _, marks = L().selective_scan(**dev, return_checkpoints=True)
+    rows = step["x"]
+
+    def calls():
+        state, window = init.to(DEV), torch.ones(N, K - 1, D, device=DEV)
+        yield L().selective_scan(**dev)
+        yield L().selective_scan_backward(y, x, dev["delta"], dev["A"], dev["B"], dev["C"], marks)
+        yield L().selective_scan_step(state, **step), state
+        yield L().causal_conv(x, w)
+        yield L().causal_conv_backward(y, x, w)
+        yield L().causal_conv_step(window, rows, w), window
+        yield L().add_rms_norm(rows, nw, rows)
+        yield L().add_rms_norm_backward(rows, rows, nw, rows)
+
+    want = list(calls())
+    entered, now = [], [7]
+
+    class Device(torch.cuda.device):
+        def __enter__(self):
+            entered.append(self.idx)
+            now[0] = self.idx
+            super().__enter__()
+
+        def __exit__(self, *args):
+            now[0] = 7
+            return super().__exit__(*args)
+
+    lib = ss._native.lib()
+
+    class Watched:
+        """the library, used on the tensors' device alone"""
+        def __getattr__(self, name):
+            assert now[0] == 0, name
+            return getattr(lib, name)
+
+    fast = ss._load_fast()
+    monkeypatch.setattr(ss, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    try:
+        ss._setup(fast)
+        assert fast.add_rms_norm(rows, nw, None, 1e-6, None) is None and fast.causal_conv(x, w, None, "silu", None, None,
+                                                                                          None) is None
+        monkeypatch.setattr(ss._native, "lib", Watched)
+        got = list(calls())
+        assert entered == [0] * len(want) and now == [7]
+    finally:
+        monkeypatch.undo()
+        ss._setup(fast)
+    assert fast is ss._NoFastCall or fast.add_rms_norm(rows, nw, None, 1e-6, None) is not None
+    for p, q in zip(want, got):
+        for u, v in zip(p, q):
+            assert (u is None and v is None) or torch.equal(u, v)
