@@ -571,10 +571,8 @@ rlscan_status forward(const rlscan_causal_conv_args &a, ConvOut o, cudaStream_t 
     return by_taps(a.K, [&](auto k) {
         auto kernel = conv_kernel<T, decltype(k)::value, V>;
         constexpr size_t SMEM = Feed<T, V, 1>::SMEM;
-        static const bool sized =
-            SMEM <= 48 * 1024 ||
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) == cudaSuccess;
-        if (!sized) return RLSCAN_ERR_CUDA;
+        static PerDevice raised;
+        if (!raise_smem(raised, kernel, SMEM)) return RLSCAN_ERR_CUDA;
         return launch_overlapped(kernel, ceil_div(a.N * o.runs * (a.D / V), kThreads), kThreads, SMEM, s, a, o);
     });
 }
@@ -595,10 +593,8 @@ rlscan_status backward(const rlscan_causal_conv_args &a, const ConvGrad &g, cuda
     return by_taps(a.K, [&](auto k) {
         auto kernel = conv_grad_kernel<T, decltype(k)::value, V>;
         constexpr size_t SMEM = Feed<T, V, 2>::SMEM;
-        static const bool sized =
-            SMEM <= 48 * 1024 ||
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) == cudaSuccess;
-        if (!sized) return RLSCAN_ERR_CUDA;
+        static PerDevice raised;
+        if (!raise_smem(raised, kernel, SMEM)) return RLSCAN_ERR_CUDA;
         return launch_overlapped(kernel, ceil_div(a.N * g.runs * (a.D / V), kThreads), kThreads, SMEM, s, a, g);
     });
 }

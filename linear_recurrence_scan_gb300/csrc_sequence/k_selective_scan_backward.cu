@@ -585,9 +585,8 @@ rlscan_status launch_shape(const rlscan_selective_scan_args &a, const GradArgs &
 {
     using P = Shape<T, LANES>;
     auto kernel = grad_kernel<T, LANES>;
-    static const bool sized =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
-    if (!sized) return RLSCAN_ERR_CUDA;
+    static PerDevice raised;
+    if (!raise_smem(raised, kernel, P::SMEM)) return RLSCAN_ERR_CUDA;
     const int64_t grid = a.N * ceil_div(a.D, P::CH) * g.chunks;
     return launch(!spread_out(grid, g.sms), kernel, grid, P::THREADS, P::SMEM, s, a, g);
 }

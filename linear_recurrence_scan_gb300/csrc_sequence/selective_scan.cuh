@@ -391,9 +391,8 @@ rlscan_status launch_mode(const rlscan_selective_scan_args &a, ScanOut o, cudaSt
     using P = Shape<T, SPT, LANES, SPLIT>;
     o.sms = order_sms(a.lengths, a.N, ceil_div(a.D, P::CH), o.chunks);
     auto kernel = scan_kernel<T, SPT, LANES, MODE, SPLIT>;
-    static const bool sized =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM) == cudaSuccess;
-    if (!sized) return RLSCAN_ERR_CUDA;
+    static PerDevice raised;
+    if (!raise_smem(raised, kernel, P::SMEM)) return RLSCAN_ERR_CUDA;
     const int64_t grid = a.N * ceil_div(a.D, P::CH) * o.chunks;
     return launch(!spread_out(grid, o.sms), kernel, grid, kScanThreads, P::SMEM, s, a, o);
 }

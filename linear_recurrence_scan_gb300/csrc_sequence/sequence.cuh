@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "params.cuh"
+#include "per_device.cuh"
 #include "ptx.cuh"
 #include "rlscan.h"
 
@@ -453,16 +454,40 @@ inline rlscan_status launch_overlapped(K kernel, int64_t grid, int threads, size
     return launch(true, kernel, grid, threads, smem, stream, args...);
 }
 
+inline bool ok(cudaError_t e)
+{
+    if (e != cudaSuccess) cudaGetLastError();
+    return e == cudaSuccess;
+}
+
+// The current device (-1 on an error).
+inline int current_device()
+{
+    int dev = 0;
+    return ok(cudaGetDevice(&dev)) ? dev : -1;
+}
+
 // The device's SM count (0 on an error).
 inline int sm_count()
 {
-    static int counts[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (counts[dev] == 0 &&
-        cudaDeviceGetAttribute(&counts[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return counts[dev];
+    static PerDevice counts;
+    const int dev = current_device();
+    if (dev < 0) return 0;
+    return counts.get(dev, [&] {
+        int n = 0;
+        return ok(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) ? n : 0;
+    });
+}
+
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device;
+// `raised` is the kernel's own.
+template <class K>
+inline bool raise_smem(PerDevice &raised, K kernel, size_t bytes)
+{
+    if (bytes <= 48 * 1024) return true;
+    return raised.get(current_device(), [&] {
+        return ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes))) ? 1 : 0;
+    }) > 0;
 }
 
 // SMs for by_length, or 0 where the order of the rows is left alone

@@ -56,3 +56,38 @@ def test_forward_mode_is_refused():
                 call(lambda t: fwd.make_dual(t, torch.ones_like(t)))
             with pytest.raises(ValueError, match="CUDA"):
                 call(lambda t: t)
+
+
+PER_DEVICE = """
+#include <cstdio>
+#include "per_device.cuh"
+using rlscan::seq::PerDevice;
+int main()
+{
+    static PerDevice limits;
+    int asked[3] = {0, 0, 0}, current = 0, answer = 0;
+    auto find = [&] { ++asked[current]; return answer; };
+    if (limits.get(0, find) != 0 || limits.get(0, find) != 0 || asked[0] != 2) return 1;   // a failure is not kept
+    answer = 100;
+    if (limits.get(0, find) != 100 || limits.get(0, find) != 100 || asked[0] != 3) return 2;
+    current = 1;
+    answer = 200;   // another device is asked itself, and the first keeps its own
+    if (limits.get(1, find) != 200 || asked[1] != 1 || limits.get(0, find) != 100 || asked[0] != 3) return 3;
+    current = 2;    // devices that are not numbered here are asked every time
+    const int others[3] = {-1, PerDevice::kDevices, PerDevice::kDevices};
+    for (int d : others)
+        if (limits.get(d, find) != 200) return 4;
+    if (asked[2] != 3) return 5;
+    std::puts("done");
+}
+"""
+
+
+def test_limits_are_kept_for_each_device(tmp_path):
+    """What a launch finds out once (shared memory raised, SMs, resident blocks) it finds out on each device."""
+    src, exe = tmp_path / "per_device.cpp", tmp_path / "per_device"
+    src.write_text(PER_DEVICE)
+    include = os.path.join(ROOT, "linear_recurrence_scan_gb300", "csrc_sequence")
+    subprocess.run(["g++", "-std=c++17", "-I", include, str(src), "-o", str(exe)], check=True, timeout=300)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and "done" in r.stdout, r.returncode
