@@ -421,30 +421,41 @@ int64_t most_blocks(int threads)
     return sms * (per_sm > 0 ? per_sm : 1);
 }
 
-// Resident blocks of a kernel on the device, asked once for each kernel and
-// block size (`slot` tells apart the kernels of one type).
-constexpr int kSlots = 4;
-int slot_of(int threads, bool vec) { return (threads == 32 ? 2 : 0) + (vec ? 1 : 0); }
-
-template <class K>
-int64_t resident(K kernel, int threads, int slot)
+// Resident blocks of a kernel on the device, asked once for each kernel (the
+// kernel itself, not its type: the types' kernels share one and differ in
+// registers), block size and device.
+template <auto KERNEL>
+int64_t resident(int threads)
 {
-    static int known[kSlots][kMostThreads / 32 + 1] = {};
-    int &n = known[slot][threads / 32];
-    if (n == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1)) {
-        cudaGetLastError();
-        n = 1;
-    }
-    return static_cast<int64_t>(n) * (sm_count() > 0 ? sm_count() : 1);
+    static PerDevice known[kMostThreads / 32 + 1];
+    const int n = known[threads / 32].get(current_device(), [&] {
+        int blocks = 0;
+        return ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, KERNEL, threads, 0)) ? blocks : 0;
+    });
+    return static_cast<int64_t>(n > 0 ? n : 1) * (sm_count() > 0 ? sm_count() : 1);
 }
 
-template <class K>
-int64_t wave(K kernel, int64_t M, int threads, int slot)
+template <auto KERNEL>
+int64_t wave(int64_t M, int threads)
 {
     int64_t grid = row_blocks(M, threads);
-    for (int64_t most : {most_blocks(threads), resident(kernel, block_threads(threads), slot)})
+    for (int64_t most : {most_blocks(threads), resident<KERNEL>(block_threads(threads))})
         if (grid > most) grid = most;
     return grid;
+}
+
+template <auto KERNEL>
+rlscan_status forward_rows(const NormArgs &a, int threads, cudaStream_t s)
+{
+    return launch_overlapped(KERNEL, wave<KERNEL>(a.M, threads), block_threads(threads), 0, s, a);
+}
+
+template <auto KERNEL>
+rlscan_status backward_rows(const NormGradArgs &a, int threads, float *part, int64_t &parts, cudaStream_t s)
+{
+    const int64_t grid = wave<KERNEL>(a.M, threads);
+    parts = grid * (threads == 32 ? kRowWarps : 1);
+    return launch_overlapped(KERNEL, grid, block_threads(threads), 0, s, a, part);
 }
 
 template <class T, class R>
@@ -452,11 +463,11 @@ rlscan_status forward(const NormArgs &a, cudaStream_t s)
 {
     const int t = row_threads<T>(a.D);
     if (t == 0) return launch_overlapped(long_norm_kernel<T, R>, a.M, kLongThreads, 0, s, a);
-    auto go = [&](auto kernel) {
-        return launch_overlapped(kernel, wave(kernel, a.M, t, slot_of(t, a.vec)), block_threads(t), 0, s, a);
-    };
-    if (t == 32) return a.vec ? go(norm_kernel<T, R, true, true>) : go(norm_kernel<T, R, true, false>);
-    return a.vec ? go(norm_kernel<T, R, false, true>) : go(norm_kernel<T, R, false, false>);
+    if (t == 32)
+        return a.vec ? forward_rows<norm_kernel<T, R, true, true>>(a, t, s)
+                     : forward_rows<norm_kernel<T, R, true, false>>(a, t, s);
+    return a.vec ? forward_rows<norm_kernel<T, R, false, true>>(a, t, s)
+                 : forward_rows<norm_kernel<T, R, false, false>>(a, t, s);
 }
 
 // most rows of `part` that a call fills
@@ -478,13 +489,11 @@ rlscan_status backward(const NormGradArgs &a, float *part, int64_t &parts, cudaS
         parts = a.M < most ? a.M : most;
         return launch_overlapped(long_norm_grad_kernel<T, R>, parts, kLongThreads, 0, s, a, part);
     }
-    auto go = [&](auto kernel) {
-        const int64_t grid = wave(kernel, a.M, t, slot_of(t, a.vec));
-        parts = grid * (t == 32 ? kRowWarps : 1);
-        return launch_overlapped(kernel, grid, block_threads(t), 0, s, a, part);
-    };
-    if (t == 32) return a.vec ? go(norm_grad_kernel<T, R, true, true>) : go(norm_grad_kernel<T, R, true, false>);
-    return a.vec ? go(norm_grad_kernel<T, R, false, true>) : go(norm_grad_kernel<T, R, false, false>);
+    if (t == 32)
+        return a.vec ? backward_rows<norm_grad_kernel<T, R, true, true>>(a, t, part, parts, s)
+                     : backward_rows<norm_grad_kernel<T, R, true, false>>(a, t, part, parts, s);
+    return a.vec ? backward_rows<norm_grad_kernel<T, R, false, true>>(a, t, part, parts, s)
+                 : backward_rows<norm_grad_kernel<T, R, false, false>>(a, t, part, parts, s);
 }
 
 uint64_t low_bits(const void *p) { return reinterpret_cast<uintptr_t>(p); }

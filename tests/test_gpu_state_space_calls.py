@@ -189,3 +189,55 @@ def test_a_call_runs_on_its_tensors_device(monkeypatch):
     for p, q in zip(want, got):
         for u, v in zip(p, q):
             assert (u is None and v is None) or torch.equal(u, v)
+
+
+ORDER = """
+import ctypes, sys, torch
+import linear_recurrence_scan_gb300 as rl
+
+class KernelNode(ctypes.Structure):   # CUDA_KERNEL_NODE_PARAMS
+    _fields_ = ([("func", ctypes.c_void_p)] + [(n, ctypes.c_uint) for n in "gx gy gz bx by bz smem".split()] +
+                [(n, ctypes.c_void_p) for n in "params extra kern ctx".split()])
+
+def grids(graph):
+    cuda, g, n = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t()
+    assert cuda.cuGraphGetNodes(g, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert cuda.cuGraphGetNodes(g, nodes, ctypes.byref(n)) == 0
+    out = []
+    for node in nodes:
+        kind, p = ctypes.c_int(), KernelNode()
+        assert cuda.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        if kind.value == 0:
+            assert cuda.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+            out.append((p.gx, p.bx))
+    return sorted(out)
+
+def call(dtype):   # 14 warps a row in either type
+    D = 3584 if dtype is torch.float32 else 7168
+    x, r = (torch.randn(4001, D, device="cuda").to(dtype) for _ in range(2))
+    w = torch.ones(D, device="cuda")
+    rl.add_rms_norm(x, w, r), rl.add_rms_norm_backward(x, r, w, x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        rl.add_rms_norm(x, w, r), rl.add_rms_norm_backward(x, r, w, x)
+    return grids(graph)
+
+found = {name: call(getattr(torch, name)) for name in sys.argv[1].split(",")}
+print(sorted(found.items()))
+"""
+
+
+def test_the_first_type_of_a_process_does_not_shape_the_others():
+    """The norm's grids are those of the call's own kernel, whichever type ran first."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    grids = []
+    for order in ("float32,bfloat16", "bfloat16,float32"):
+        r = subprocess.run([sys.executable, "-c", ORDER, order], capture_output=True, text=True, cwd=root, timeout=600)
+        assert r.returncode == 0, r.stderr[-2000:]
+        grids.append(r.stdout.splitlines()[-1])
+    assert grids[0].count("(") >= 2 * 3 and grids[0] == grids[1]
