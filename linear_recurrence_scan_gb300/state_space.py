@@ -547,7 +547,7 @@ def _rows(name, t, shape, dtype, device):
     if not fits:
         _check(name, t, shape, dtype, device)
     if len(shape) != 2:
-        t = t.reshape(-1, shape[-1])
+        t = t.reshape(t.numel() // max(shape[-1], 1), shape[-1])
     strides = t.stride()
     if strides[1] != 1 and shape[-1] > 1:
         t = t.contiguous()
@@ -561,6 +561,8 @@ def _norm_lead(name, x, weight, eps):
     dev = x.get_device()
     if dev < 0 or x.dtype not in _TYPES:
         _lead(name, x, x.dim())
+    if weight is None:
+        raise TypeError("weight must be a torch.Tensor")
     if not float(eps) >= 0:
         raise ValueError("eps must not be negative")
     shape = x.shape

@@ -241,3 +241,18 @@ def test_the_first_type_of_a_process_does_not_shape_the_others():
         assert r.returncode == 0, r.stderr[-2000:]
         grids.append(r.stdout.splitlines()[-1])
     assert grids[0].count("(") >= 2 * 3 and grids[0] == grids[1]
+
+
+def test_norm_without_channels_or_weight(layer):
+    for shape in ((2, 3, 0), (3, 0), (0, 3, 5), (2, 0, 5)):
+        x, w = torch.zeros(shape, device=DEV), torch.ones(shape[-1], device=DEV)
+        n = L().add_rms_norm(x, w, x)
+        assert n.y.shape == n.residual.shape == shape
+        q = L().add_rms_norm(x, w, x, out_dtype=torch.float8_e4m3fn)
+        assert q.y.shape == shape and q.scales.shape == (*shape[:-1], -(-shape[-1] // 128))
+        g = L().add_rms_norm_backward(x, x, w, x)
+        assert g.x.shape == shape and g.weight.shape == w.shape and not g.weight.any()
+    with pytest.raises(TypeError, match="weight"):
+        L().add_rms_norm(torch.zeros(2, 8, device=DEV), None)
+    with pytest.raises(TypeError, match="weight"):
+        L().add_rms_norm_backward(torch.zeros(2, 8, device=DEV), torch.zeros(2, 8, device=DEV), None)
