@@ -256,3 +256,47 @@ def test_norm_without_channels_or_weight(layer):
         L().add_rms_norm(torch.zeros(2, 8, device=DEV), None)
     with pytest.raises(TypeError, match="weight"):
         L().add_rms_norm_backward(torch.zeros(2, 8, device=DEV), torch.zeros(2, 8, device=DEV), None)
+
+
+def test_a_float32_residual_through_autograd():
+    M, D = 37, 200
+    x, nw = torch.randn(M, D, device=DEV).to(BF16), torch.rand(D, device=DEV) + 0.5
+    r, gy, gr = torch.randn(M, D, device=DEV), torch.randn(M, D, device=DEV).to(BF16), torch.randn(M, D, device=DEV)
+    leaves = [t.clone().requires_grad_() for t in (x, nw, r)]
+    n = L().add_rms_norm(*leaves, eps=1e-5)
+    assert n.y.dtype == BF16 and n.residual.dtype == F32
+    torch.autograd.backward([n.y, n.residual], [gy, gr])
+    g = L().add_rms_norm_backward(gy, n.residual.detach(), nw, gr, eps=1e-5)
+    assert torch.equal(leaves[0].grad, g.x) and torch.equal(leaves[1].grad, g.weight)
+    assert leaves[2].grad.dtype == F32 and torch.equal(leaves[2].grad, g.residual)
+
+
+def test_captured_steps(layer):
+    """A token of a layer in a graph: norm, convolution and scan steps, replayed on new inputs and moving states."""
+    N, D, S, K = 5, 64, 16, 4
+    a, init, _, _, _ = scan_inputs(N, 1, D, S, BF16, 45, step=True)
+    dev = {k: v.to(DEV) for k, v in a.items()}
+    w, nw = torch.randn(D, K, device=DEV), torch.ones(D, device=DEV)
+    slots = torch.tensor([4, 0, -1, 2, 1], dtype=torch.int32, device=DEV)
+    residual = torch.randn(N, D, device=DEV)
+
+    def token(state, window):
+        n = L().add_rms_norm(dev["x"], nw, residual)
+        x = L().causal_conv_step(window, n.y, w, slots=slots)
+        return L().selective_scan_step(state, **{**dev, "x": x}, slots=slots), n.residual
+
+    states = [(init.to(DEV), torch.zeros(N, K - 1, D, device=DEV).to(BF16)) for _ in range(2)]
+    for s in states:
+        token(*s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = token(*states[0])
+    for seed in (46, 47):
+        b, _, _, _, _ = scan_inputs(N, 1, D, S, BF16, seed, step=True)
+        for k in ("x", "delta", "z", "B", "C"):
+            dev[k].copy_(b[k])
+        graph.replay()
+        want = token(*states[1])
+        for p, q in zip((*out, *states[0]), (*want, *states[1])):
+            assert torch.equal(p, q)
