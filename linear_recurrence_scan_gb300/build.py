@@ -109,8 +109,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), out_dir: s
 
 def build_checked(force: bool = False) -> str:
     """The bounds-checked build (RLSCAN_CHECK_BOUNDS=1: every global access
-    and bulk copy of the scan kernels is tested against its argument's
-    extent, violations are counted and skipped), in its own directory."""
+    and bulk copy of the estimators' scan kernels, csrc/, is tested against
+    its argument's extent, violations are counted and skipped), in its own
+    directory.  The state-space layer, csrc_sequence/, is compiled along
+    without such tests."""
     return build(force, extra_flags=("-DRLSCAN_CHECK_BOUNDS=1",), out_dir=CHECKED_DIR)
 
 

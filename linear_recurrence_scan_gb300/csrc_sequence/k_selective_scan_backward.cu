@@ -16,11 +16,12 @@
 // token needs once (softplus, the gate, the outputs) is shared out over the
 // lanes through shared memory.
 //
-// Instructions bound it, 421 for a warp (32 channels x 16 states) and token,
+// Instructions bound it, 408 for a warp (32 channels x 16 states) and token,
 // at the two warps a scheduler that 255 registers leave.  Measured, 8 x 512 x
-// 4096 x 16 bf16: 389 us, 60 % of the issue slots where an SM has two blocks;
-// 8 x 2048 x 4096 with the forward pass 1994 us, with three blocks an SM
-// (168 registers, spills) 3088, with two channels a lane and four blocks 2234.
+// 4096 x 16 bf16: 379 us, 59 % of the issue slots where an SM has two blocks;
+// 8 x 2048 x 4096 with the forward pass 1989 us.  (Tried when that was 1994:
+// three blocks an SM at 168 registers, with spills, 3088; two channels a lane
+// and four blocks 2234.)
 #include "scan_plan.cuh"
 
 namespace rlscan {

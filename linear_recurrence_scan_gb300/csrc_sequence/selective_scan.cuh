@@ -15,7 +15,7 @@
 // run at 31.5 values a clock and SM.
 // Measured, S 16 bf16: 8 x 4096 x 4096 675 us, 3.2e12 values/s, 63 % of the
 // issue slots where an SM has two blocks; with ragged rows (62 % of the
-// tokens) 503 us back to back.  1 x 4096 x 2048 in chunks of 128: 35 us for the chunks' states (69 % of
+// tokens) 500 to 530 us back to back.  1 x 4096 x 2048 in chunks of 128: 35 us for the chunks' states (69 % of
 // the exponential units), 8 for joining them, 54 for the outputs.
 #pragma once
 
