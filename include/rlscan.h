@@ -699,8 +699,8 @@ rlscan_status rlscan_causal_conv_step(const rlscan_causal_conv_args *args, void 
  * (required with residual, unused without); y [M,D]: with scales NULL of
  * `dtype`, else in 8 bits (e4m3) with scales [M, ceil(D/128)] float32, one
  * for each 128 columns: scale = max(max|y|, 2^-100) / 448, stored y / scale
- * to nearest even, saturated.  A block with a NaN or infinite y has a NaN
- * scale.  y is made from h before h is rounded. */
+ * (right to two float32 roundings) to nearest even, saturated.  A block with
+ * a NaN or infinite y has a NaN scale.  y is made from h before h is rounded. */
 rlscan_status rlscan_add_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
                                   const float *weight, int64_t M, int64_t D, float eps, rlscan_dtype dtype,
                                   rlscan_dtype residual_dtype, void *y, float *scales, void *residual_out,
