@@ -723,6 +723,69 @@ rlscan_status rlscan_add_rms_norm_backward(const void *grad_y, int64_t grad_y_st
                                            void *grad_x, void *grad_h, float *grad_weight, void *ws,
                                            size_t ws_bytes, rlscan_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The gated recurrence: one state a channel, its decay and its input gated
+ * token by token.  Conventions as for the state-space layer (token-major
+ * arrays with strides of their own, resets, lengths, slots, one rounding,
+ * the same bits on every call, scratch workspaces).
+ * ------------------------------------------------------------------------- */
+
+/* What its forms share, with r = sigmoid(gate) and i = sigmoid(input_gate):
+ *   a_t = exp(log_decay r_t)
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t        [N,D], h_{-1} = initial_state
+ *   y_t = h_t
+ * (the linear recurrence with the gates of De et al., "Mixing Gated Linear
+ * Recurrences with Local Attention for Efficient Language Models", 2024,
+ * Sec. 2.4; log_decay is its -c softplus(Lambda)).  At a reset h_{t-1} counts
+ * 0, the input keeps its root.  log_decay is below 0 in use; at 0 and above,
+ * and where a gate closes so far that a_t is 1, 1 - a_t^2 counts 2^-100. */
+typedef struct rlscan_gated_scan_args {
+    int64_t N, T, D;              /* rows, tokens, channels */
+    int64_t dtype;                /* RLSCAN_F32 or RLSCAN_BF16 */
+    rlscan_array3 x, gate, input_gate; /* [N,T,D] */
+    const float *log_decay;       /* [D] */
+    const float *initial_state;   /* [N,D], nullable: 0 */
+    const uint8_t *resets;        /* [N,T], nullable */
+    const int32_t *lengths;       /* [N], nullable */
+} rlscan_gated_scan_args;
+
+/* Tokens between two checkpoints: checkpoints [N, ceil(T / 64), D] hold the
+ * state before tokens 0, 64, 128, ... */
+#define RLSCAN_GATED_SCAN_CHECKPOINT 64
+
+/* Forward.  Outputs: y [N,T,D]; final_state [N,D] nullable: the state after
+ * each row's last token; checkpoints nullable (what the backward pass needs).
+ * Errors: RLSCAN_ERR_NULL, RLSCAN_ERR_SHAPE, RLSCAN_ERR_ARG_VALUE (unknown
+ * dtype), RLSCAN_ERR_ARG_CONFLICT (an output that is an input),
+ * RLSCAN_ERR_MEMORY, RLSCAN_ERR_CUDA. */
+rlscan_status rlscan_gated_scan(const rlscan_gated_scan_args *args, void *y, float *final_state, float *checkpoints,
+                                rlscan_stream_t stream);
+
+/* Gradients, with G_t = dL/dh_t = grad_y_t + a_{t+1} G_{t+1} (no carry over a
+ * reset; past the last token grad_final_state):
+ *   dx = G root i;  dinput_gate = G root x i (1 - i),  root = sqrt(1 - a^2)
+ *   dL = G (a h_{t-1} - i x a^2 / root);  dgate = dL log_decay r (1 - r)
+ *   dlog_decay = sum_{n,t} dL r;  dinitial_state = a_0 G_0 (0 behind a reset)
+ * args->initial_state is not read (the checkpoints hold it).  x, gate and
+ * input_gate are required, the others nullable (not computed). */
+typedef struct rlscan_gated_scan_grads {
+    void *x, *gate, *input_gate;  /* [N,T,D] */
+    float *log_decay;             /* [D] */
+    float *initial_state;         /* [N,D] */
+} rlscan_gated_scan_grads;
+
+size_t rlscan_gated_scan_backward_workspace_bytes(const rlscan_gated_scan_args *args);
+
+rlscan_status rlscan_gated_scan_backward(const rlscan_gated_scan_args *args, const rlscan_array3 *grad_y,
+                                         const float *grad_final_state, const float *checkpoints,
+                                         const rlscan_gated_scan_grads *grads, void *ws, size_t ws_bytes,
+                                         rlscan_stream_t stream);
+
+/* One token of each of N sequences (T = 1): state [P,D] is updated in place,
+ * slots as in rlscan_selective_scan_step. */
+rlscan_status rlscan_gated_scan_step(const rlscan_gated_scan_args *args, float *state, int64_t P,
+                                     const int32_t *slots, void *y, rlscan_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

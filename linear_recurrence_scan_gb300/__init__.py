@@ -2,7 +2,8 @@
 
 The compute path is the CUDA library ``librlscan.so`` (hand-written sm_103a
 kernels behind the C ABI in ``include/rlscan.h``); ``api`` binds it for
-PyTorch tensors, and ``state_space`` the state-space layer's operators.
+PyTorch tensors, ``state_space`` the state-space layer's operators and
+``token_policy`` the gated recurrence of such policies.
 ``synthetic`` draws seeded rollout buffers.  Importing the
 package does not load the library; the first estimator call does (and raises
 if it has not been built).
@@ -22,6 +23,10 @@ _STATE_SPACE = {
     "add_rms_norm", "add_rms_norm_backward", "RmsNorm", "RmsNormGrads",
 }
 
+_TOKEN_POLICY = {
+    "gated_scan", "gated_scan_backward", "gated_scan_step", "GatedScanGrads",
+}
+
 
 def __getattr__(name):
     if name in _API:
@@ -34,8 +39,13 @@ def __getattr__(name):
         value = getattr(state_space, name)
         globals()[name] = value
         return value
+    if name in _TOKEN_POLICY:
+        from . import token_policy
+        value = getattr(token_policy, name)
+        globals()[name] = value
+        return value
     raise AttributeError(name)
 
 
 def __dir__():
-    return sorted(set(globals()) | _API | _STATE_SPACE)
+    return sorted(set(globals()) | _API | _STATE_SPACE | _TOKEN_POLICY)

@@ -79,6 +79,11 @@ SIGNATURES = {
     "rlscan_add_rms_norm": ([_P, _I64, _P, _I64, _P, _I64, _I64, _F, _I, _I] + [_P] * 4, _I),
     "rlscan_add_rms_norm_backward_workspace_bytes": ([_I64, _I64], _SZ),
     "rlscan_add_rms_norm_backward": ([_P, _I64] * 3 + [_P, _I64, _I64, _F, _I, _I] + [_P] * 4 + [_SZ, _P], _I),
+    # the gated recurrence
+    "rlscan_gated_scan": ([_P] * 5, _I),
+    "rlscan_gated_scan_backward_workspace_bytes": ([_P], _SZ),
+    "rlscan_gated_scan_backward": ([_P] * 6 + [_SZ, _P], _I),
+    "rlscan_gated_scan_step": ([_P, _P, _I64] + [_P] * 3, _I),
 }
 
 _lib = None

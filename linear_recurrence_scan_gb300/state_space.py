@@ -186,7 +186,7 @@ def _refuse_tangents(*ts):
     if _forward_ad._current_level >= 0:
         for t in ts:
             if isinstance(t, torch.Tensor) and _forward_ad.unpack_dual(t).tangent is not None:
-                raise RuntimeError("the state-space layer's functions have no forward-mode derivative")
+                raise RuntimeError("these functions have no forward-mode derivative")
 
 
 def _on(device):

@@ -1,0 +1,168 @@
+"""A recurrent token policy's other operators for PyTorch tensors: the gated
+recurrence (one state a channel), the gated feed-forward block's projections,
+and the loss that distils a teacher's top logits into the policy.
+
+They follow the state-space layer's functions (``state_space.py``): arguments
+are checked, outputs allocated with torch, one librlscan call is made on the
+current CUDA stream of the tensors' device, without synchronising; there is no
+CPU path.  What has gradients has them once, in reverse mode; the
+``*_backward`` functions are the same gradients as plain calls; dual tensors
+are refused.
+"""
+from __future__ import annotations
+
+import struct
+from typing import NamedTuple
+
+import torch
+
+from . import _native
+from .api import _stream_handle
+from .state_space import (_ARRAY3, _TYPES, _act, _at, _changed, _check, _dense, _flags, _lead, _on,
+                          _refuse_tangents, _scratch, _wants_grad)
+
+__all__ = ["gated_scan", "gated_scan_backward", "gated_scan_step", "GatedScanGrads"]
+
+GATED_CHECKPOINT = 64   # tokens between two checkpoints of the gated scan (RLSCAN_GATED_SCAN_CHECKPOINT)
+
+_GATED_ARGS = struct.Struct("=17q")
+_GATED_GRADS = struct.Struct("=5q")
+
+
+# ---------------------------------------------------------------------------
+# gated scan
+
+class GatedScanGrads(NamedTuple):
+    """Gradients of gated_scan's inputs."""
+    x: torch.Tensor
+    gate: torch.Tensor
+    input_gate: torch.Tensor
+    log_decay: torch.Tensor
+    initial_state: torch.Tensor
+
+
+def _gated_args(step, x, gate, input_gate, log_decay, initial_state, resets, lengths):
+    """Checks; (device, (N, T, channels), the packed arguments, the tensors they point at)."""
+    dev = _lead("x", x, 2 if step else 3)
+    dtype, shape = x.dtype, x.shape
+    N, T, width = (shape[0], 1, shape[1]) if step else shape
+    xp, xr, xt, x = _act("x", x, shape, dtype, dev)
+    gp, gr, gt, gate = _act("gate", gate, shape, dtype, dev)
+    ip, ir, it, input_gate = _act("input_gate", input_gate, shape, dtype, dev)
+    if log_decay is None:
+        raise TypeError("log_decay must be a torch.Tensor")
+    log_decay = _dense("log_decay", log_decay, (width,), torch.float32, dev)
+    initial_state = _dense("initial_state", initial_state, (N, width), torch.float32, dev)
+    resets = _flags(resets, (N, T), dev)
+    lengths = _dense("lengths", lengths, (N,), torch.int32, dev)
+    packed = _GATED_ARGS.pack(N, T, width, _TYPES[dtype], xp, xr, xt, gp, gr, gt, ip, ir, it, log_decay.data_ptr(),
+                              _at(initial_state), _at(resets), _at(lengths))
+    return dev, (N, T, width), packed, (x, gate, input_gate, log_decay, initial_state, resets, lengths)
+
+
+def _gated_forward(want_checkpoints, *args):
+    dev, (N, T, width), packed, kept = _gated_args(False, *args)
+    x = kept[0]
+    f32 = dict(dtype=torch.float32, device=x.device)
+    y = torch.empty((N, T, width), dtype=x.dtype, device=x.device)
+    final = torch.empty((N, width), **f32)
+    marks = torch.empty((N, -(-T // GATED_CHECKPOINT), width), **f32) if want_checkpoints else None
+    with _on(dev):
+        _native.check(_native.lib().rlscan_gated_scan(packed, y.data_ptr(), final.data_ptr(), _at(marks),
+                                                      _stream_handle(x.device)), "rlscan_gated_scan")
+    return y, final, marks
+
+
+class _GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gate, input_gate, log_decay, initial_state, resets, lengths):
+        y, final, marks = _gated_forward(True, x, gate, input_gate, log_decay, initial_state, resets, lengths)
+        ctx.started = initial_state is not None
+        ctx.save_for_backward(x, gate, input_gate, log_decay, resets, lengths, marks)
+        ctx.mark_non_differentiable(marks)
+        ctx.set_materialize_grads(False)
+        return y, final, marks
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_y, grad_final, _):
+        x, gate, input_gate, log_decay, resets, lengths, marks = ctx.saved_tensors
+        if grad_y is None:
+            if grad_final is None:
+                return (None,) * 7
+            grad_y = torch.zeros_like(x)
+        g = gated_scan_backward(grad_y, x, gate, input_gate, log_decay, marks, resets, lengths, grad_final)
+        return g.x, g.gate, g.input_gate, g.log_decay, g.initial_state if ctx.started else None, None, None
+
+
+def gated_scan(x, gate, input_gate, log_decay, initial_state=None, resets=None, lengths=None,
+               return_checkpoints=False):
+    """The gated linear recurrence over prompts, for every channel
+
+        r_t = sigmoid(gate_t),  i_t = sigmoid(input_gate_t),  a_t = exp(log_decay r_t)
+        y_t = h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t,    h_{-1} = initial_state
+
+    x, gate and input_gate [N,T,channels] are float32 or bfloat16 (one type,
+    any strides over rows and tokens); log_decay [channels], below 0, and
+    initial_state [N,channels] float32.  ``resets`` and ``lengths`` as in
+    selective_scan (at a reset h_{t-1} counts 0, the input keeps its root).
+    Returns (y, final_state): y like x, the states [N,channels] float32 after
+    each row's last token.  With ``return_checkpoints`` a third value, what
+    gated_scan_backward needs: the states before every 64th token (these
+    carry no gradient)."""
+    args = (x, gate, input_gate, log_decay, initial_state, resets, lengths)
+    _refuse_tangents(*args[:5])
+    out = _GatedScan.apply(*args) if _wants_grad(*args[:5]) else _gated_forward(return_checkpoints, *args)
+    return out if return_checkpoints else out[:2]
+
+
+def gated_scan_backward(grad_y, x, gate, input_gate, log_decay, checkpoints, resets=None, lengths=None,
+                        grad_final_state=None):
+    """Gradients of gated_scan: ``grad_y`` like x, ``checkpoints`` from the
+    forward call on the same inputs, ``grad_final_state`` [N,channels] float32
+    or None.  Returns GatedScanGrads."""
+    _refuse_tangents(grad_y, x, gate, input_gate, log_decay, checkpoints, grad_final_state)
+    dev, (N, T, width), packed, kept = _gated_args(False, x, gate, input_gate, log_decay, None, resets, lengths)
+    x = kept[0]
+    gp, gr, gt, grad_y = _act("grad_y", grad_y, x.shape, x.dtype, dev)
+    if checkpoints is None:
+        raise ValueError("checkpoints is required (gated_scan(..., return_checkpoints=True))")
+    marks = _dense("checkpoints", checkpoints, (N, -(-T // GATED_CHECKPOINT), width), torch.float32, dev)
+    gfinal = _dense("grad_final_state", grad_final_state, (N, width), torch.float32, dev)
+    acts, f32 = dict(dtype=x.dtype, device=x.device), dict(dtype=torch.float32, device=x.device)
+    g = GatedScanGrads(x=torch.empty((N, T, width), **acts), gate=torch.empty((N, T, width), **acts),
+                       input_gate=torch.empty((N, T, width), **acts), log_decay=torch.empty((width,), **f32),
+                       initial_state=torch.empty((N, width), **f32))
+    lib = _native.lib()
+    with _on(dev):
+        ws = _scratch(lib.rlscan_gated_scan_backward_workspace_bytes(packed), x.device)
+        _native.check(lib.rlscan_gated_scan_backward(
+            packed, _ARRAY3.pack(gp, gr, gt), _at(gfinal), marks.data_ptr(),
+            _GATED_GRADS.pack(g.x.data_ptr(), g.gate.data_ptr(), g.input_gate.data_ptr(), g.log_decay.data_ptr(),
+                              g.initial_state.data_ptr()),
+            _at(ws), 0 if ws is None else ws.numel(), _stream_handle(x.device)), "rlscan_gated_scan_backward")
+    return g
+
+
+def gated_scan_step(state, x, gate, input_gate, log_decay, slots=None):
+    """One token of each of N sequences: x, gate, input_gate [N,channels];
+    ``state`` [P,channels] float32 (dense) is updated in place, with ``slots``
+    as in selective_scan_step.  Returns y [N,channels].  Not differentiable."""
+    _refuse_tangents(state, x, gate, input_gate, log_decay)
+    dev, (N, _, width), packed, kept = _gated_args(True, x, gate, input_gate, log_decay, None, None, None)
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+        raise ValueError("state must be a [slots, channels] tensor")
+    P = state.shape[0]
+    _check("state", state, (P, width), torch.float32, dev)
+    if not state.is_contiguous():
+        raise ValueError("state must be contiguous: it is updated in place")
+    slots = _dense("slots", slots, (N,), torch.int32, dev)
+    if slots is None and P < N:
+        raise ValueError(f"state holds {P} slots for {N} sequences")
+    x = kept[0]
+    y = torch.empty((N, width), dtype=x.dtype, device=x.device)
+    with _on(dev):
+        _native.check(_native.lib().rlscan_gated_scan_step(packed, state.data_ptr(), P, _at(slots), y.data_ptr(),
+                                                           _stream_handle(x.device)), "rlscan_gated_scan_step")
+    _changed(state)
+    return y

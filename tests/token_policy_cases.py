@@ -1,0 +1,46 @@
+"""Inputs and error bounds the tests of the token policy's operators share.
+
+u = 2^-24 is the float32 rounding unit; every bound is a factor times the
+formula on absolute values (``bound=True`` of the oracle).
+
+* gated scan, gate values within 4 of 0.  exp(-v) is right to (|v| + 2) u, so
+  a sigmoid to (|v| + 2) u e / (1 + e) + 2 u <= 14 u, the exponent L =
+  log_decay r to 15 u and a = exp(L) to (15 |L| + 5) u.  1 - a^2 is its series
+  to 25 u, or beyond |2 L| = 1/4, where a^2 <= 0.78, to 2 (15 |L| + 5) u a^2 /
+  (1 - a^2) <= 55 u; its root to 30 u, and root i x to 50 u.  A contribution
+  that has decayed by exp(-X) over n steps is right to (15 X + 6 n) u of
+  itself, and past X = 25 it no longer counts: gated(T) = (430 + 6 T) u.
+  A gradient multiplies two such sums; a^2 / root adds 2 (15 |L| + 5) + 32 u
+  (|L| <= 5 here: 192 u), 1 - r, whose r is right to 3 u where it is near 1,
+  another 3 u / (1 - r) <= 165 u and its factors 20 u; a sum over `terms`
+  tokens in float32 adds as many u: (2 (430 + 6 T) + 400 + terms) u.
+* an output in bfloat16 is rounded by at most 2^-9 of itself (2^-8 where the
+  two sides lie on different sides of a binade).
+"""
+import numpy as np
+import torch
+
+from state_space_cases import U, flags
+
+
+def gated_factor(T):
+    return (430 + 6 * T) * U
+
+
+def gated_grad_factor(T, terms=0):
+    return (2 * (430 + 6 * T) + 400 + terms) * U
+
+
+def gated_inputs(N, T, D, dtype, seed, kind="none", step=False, strongest=5.0):
+    """x, both gates, log_decay between -strongest and -1e-4; initial state, resets, lengths, the generator"""
+    rng = np.random.default_rng(seed)
+    lead = (N,) if step else (N, T)
+
+    def normal(*shape, scale=1.0, to=dtype):
+        return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(to)
+
+    a = dict(x=normal(*lead, D), gate=normal(*lead, D, scale=1.3).clamp(-4, 4),
+             input_gate=normal(*lead, D, scale=1.3).clamp(-4, 4),
+             log_decay=-torch.from_numpy(np.exp(rng.uniform(np.log(1e-4), np.log(strongest), D)).astype(np.float32)))
+    resets, lengths = flags(kind, N, T, rng)
+    return a, normal(N, D, to=torch.float32), resets, lengths, rng
