@@ -786,6 +786,59 @@ rlscan_status rlscan_gated_scan_backward(const rlscan_gated_scan_args *args, con
 rlscan_status rlscan_gated_scan_step(const rlscan_gated_scan_args *args, float *state, int64_t P,
                                      const int32_t *slots, void *y, rlscan_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Distillation from a teacher's top logits.  For each token, with the
+ * teacher's logits over K tokens of the vocabulary and the student's over all:
+ *   q = softmax(teacher / temperature) over the K,
+ *   p = softmax(logits / temperature) over the V,
+ *   loss = sum_k q_k (log q_k - log p_k)
+ *   dloss/dlogits = (p - q) / temperature       (q at the K tokens, else 0)
+ * (Hinton, Vinyals and Dean, "Distilling the Knowledge in a Neural Network",
+ * 2015, Sec. 2, with the teacher cut to its K tokens and renormalised; the
+ * factor temperature^2 is left to the caller).
+ *  - A teacher token outside 0..V-1 (-1, say) is an empty place; a token that
+ *    comes twice counts twice; a teacher logit of -infinity counts q = 0.  A
+ *    row with nothing left has loss 0 and gradient 0.
+ *  - mask [N,T] uint8, nullable: tokens where it is 0 have loss and gradient 0;
+ *    their logits and teacher are not read.
+ *  - A logit of -infinity has p = 0; a NaN or +infinity makes its row's loss
+ *    and gradient NaN.
+ *  - Conventions as for the state-space layer: logits token-major with strides
+ *    of their own, outputs dense, float32 arithmetic, one rounding, the same
+ *    bits on every call.
+ * ------------------------------------------------------------------------- */
+#define RLSCAN_DISTILL_MOST 256   /* K at most */
+
+typedef struct rlscan_distill_args {
+    int64_t N, T, V, K;           /* rows, tokens, vocabulary (below 2^31), the teacher's tokens (1..256) */
+    int64_t dtype;                /* of logits and their gradient: RLSCAN_F32 or RLSCAN_BF16 */
+    int64_t teacher_dtype;        /* of teacher_logits: RLSCAN_F32 or RLSCAN_BF16 */
+    int64_t token_bytes;          /* of teacher_tokens: 4 or 8 */
+    rlscan_array3 logits;         /* [N,T,V] */
+    const void *teacher_logits;   /* [N,T,K] */
+    const void *teacher_tokens;   /* [N,T,K] int32 or int64 */
+    const uint8_t *mask;          /* [N,T], nullable */
+    double temperature;           /* above 0 */
+} rlscan_distill_args;
+
+/* loss [N,T] float32; normalizers [N,T,2] float32, nullable: the row's largest
+ * logit m and sum exp((logit - m) / temperature), which the gradient needs.
+ * Errors: RLSCAN_ERR_NULL, RLSCAN_ERR_SHAPE, RLSCAN_ERR_ARG_VALUE (K, a type or
+ * the temperature out of range), RLSCAN_ERR_ARG_CONFLICT, RLSCAN_ERR_MEMORY,
+ * RLSCAN_ERR_CUDA. */
+rlscan_status rlscan_distill_loss(const rlscan_distill_args *args, float *loss, float *normalizers,
+                                  rlscan_stream_t stream);
+
+/* grad_logits [N,T,V] of `dtype` = grad_loss [N,T] float32 times the gradient,
+ * from the normalizers of the forward call on the same inputs. */
+rlscan_status rlscan_distill_loss_backward(const rlscan_distill_args *args, const float *grad_loss,
+                                           const float *normalizers, void *grad_logits, rlscan_stream_t stream);
+
+/* Both, for a caller who knows grad_loss beforehand: the logits are read once
+ * (while a row of V logits has at most 512 KB; longer rows are read twice). */
+rlscan_status rlscan_distill_loss_and_grad(const rlscan_distill_args *args, const float *grad_loss, float *loss,
+                                           float *normalizers, void *grad_logits, rlscan_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,6 +25,7 @@ _STATE_SPACE = {
 
 _TOKEN_POLICY = {
     "gated_scan", "gated_scan_backward", "gated_scan_step", "GatedScanGrads",
+    "distill_loss", "distill_loss_backward", "distill_loss_and_grad",
 }
 
 

@@ -84,6 +84,10 @@ SIGNATURES = {
     "rlscan_gated_scan_backward_workspace_bytes": ([_P], _SZ),
     "rlscan_gated_scan_backward": ([_P] * 6 + [_SZ, _P], _I),
     "rlscan_gated_scan_step": ([_P, _P, _I64] + [_P] * 3, _I),
+    # the distillation loss
+    "rlscan_distill_loss": ([_P] * 4, _I),
+    "rlscan_distill_loss_backward": ([_P] * 5, _I),
+    "rlscan_distill_loss_and_grad": ([_P] * 6, _I),
 }
 
 _lib = None

@@ -21,12 +21,18 @@ from .api import _stream_handle
 from .state_space import (_ARRAY3, _TYPES, _act, _at, _changed, _check, _dense, _flags, _lead, _on,
                           _refuse_tangents, _scratch, _wants_grad)
 
-__all__ = ["gated_scan", "gated_scan_backward", "gated_scan_step", "GatedScanGrads"]
+__all__ = [
+    "gated_scan", "gated_scan_backward", "gated_scan_step", "GatedScanGrads",
+    "distill_loss", "distill_loss_backward", "distill_loss_and_grad",
+]
 
 GATED_CHECKPOINT = 64   # tokens between two checkpoints of the gated scan (RLSCAN_GATED_SCAN_CHECKPOINT)
 
 _GATED_ARGS = struct.Struct("=17q")
 _GATED_GRADS = struct.Struct("=5q")
+_DISTILL_ARGS = struct.Struct("=13qd")
+
+MAX_TEACHER_TOKENS = 256   # RLSCAN_DISTILL_MOST
 
 
 # ---------------------------------------------------------------------------
@@ -166,3 +172,135 @@ def gated_scan_step(state, x, gate, input_gate, log_decay, slots=None):
                                                            _stream_handle(x.device)), "rlscan_gated_scan_step")
     _changed(state)
     return y
+
+
+# ---------------------------------------------------------------------------
+# distillation from a teacher's top logits
+
+def _distill_args(logits, teacher_logits, teacher_tokens, temperature, mask):
+    """Checks; (device, the packed arguments, the tensors they point at)."""
+    dev = _lead("logits", logits, 3)
+    N, T, V = logits.shape
+    if V == 0:
+        raise ValueError("logits must have a vocabulary")
+    if not isinstance(teacher_logits, torch.Tensor) or teacher_logits.dim() != 3:
+        raise ValueError("teacher_logits must be a [N, T, K] tensor")
+    K = teacher_logits.shape[2]
+    if not 1 <= K <= MAX_TEACHER_TOKENS:
+        raise ValueError(f"teacher_logits has {K} tokens: 1 to {MAX_TEACHER_TOKENS} are supported")
+    if teacher_logits.dtype not in _TYPES:
+        raise TypeError(f"teacher_logits: expected torch.float32 or torch.bfloat16, got {teacher_logits.dtype}")
+    if not isinstance(teacher_tokens, torch.Tensor) or teacher_tokens.dtype not in (torch.int32, torch.int64):
+        raise TypeError("teacher_tokens must be an int32 or int64 tensor")
+    if not 1e-6 <= temperature <= 1e6:
+        raise ValueError("temperature must be between 1e-6 and 1e6")
+    lp, lr, lt, logits = _act("logits", logits, logits.shape, logits.dtype, dev)
+    teacher_logits = _dense("teacher_logits", teacher_logits, (N, T, K), teacher_logits.dtype, dev)
+    teacher_tokens = _dense("teacher_tokens", teacher_tokens, (N, T, K), teacher_tokens.dtype, dev)
+    if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
+        mask = mask.view(torch.uint8)
+    mask = _dense("mask", mask, (N, T), torch.uint8, dev)
+    packed = _DISTILL_ARGS.pack(N, T, V, K, _TYPES[logits.dtype], _TYPES[teacher_logits.dtype],
+                                teacher_tokens.element_size(), lp, lr, lt, teacher_logits.data_ptr(),
+                                teacher_tokens.data_ptr(), _at(mask), temperature)
+    return dev, packed, (logits, teacher_logits, teacher_tokens, mask)
+
+
+def _distill_forward(want_normalizers, *args):
+    dev, packed, kept = _distill_args(*args)
+    logits = kept[0]
+    loss = torch.empty(logits.shape[:2], dtype=torch.float32, device=logits.device)
+    norm = torch.empty((*logits.shape[:2], 2), dtype=torch.float32, device=logits.device) if want_normalizers else None
+    with _on(dev):
+        _native.check(_native.lib().rlscan_distill_loss(packed, loss.data_ptr(), _at(norm),
+                                                        _stream_handle(logits.device)), "rlscan_distill_loss")
+    return loss, norm
+
+
+class _DistillLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, teacher_logits, teacher_tokens, temperature, mask):
+        loss, norm = _distill_forward(True, logits, teacher_logits, teacher_tokens, temperature, mask)
+        ctx.temperature = temperature
+        ctx.save_for_backward(logits, teacher_logits, teacher_tokens, mask, norm)
+        ctx.mark_non_differentiable(norm)
+        ctx.set_materialize_grads(False)
+        return loss, norm
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss, _):
+        if grad_loss is None:
+            return (None,) * 5
+        logits, teacher_logits, teacher_tokens, mask, norm = ctx.saved_tensors
+        return (distill_loss_backward(grad_loss, logits, teacher_logits, teacher_tokens, norm, ctx.temperature, mask),
+                None, None, None, None)
+
+
+def distill_loss(logits, teacher_logits, teacher_tokens, temperature=1.0, mask=None, return_normalizers=False):
+    """The divergence of a student's tokens from a teacher's top logits:
+
+        q = softmax(teacher_logits / temperature) over the teacher's K tokens
+        p = softmax(logits / temperature) over the vocabulary
+        loss = sum_k q_k (log q_k - log p_k)
+
+    logits [N,T,vocabulary] float32 or bfloat16 (any strides over rows and
+    tokens); teacher_logits [N,T,K] float32 or bfloat16 and teacher_tokens
+    [N,T,K] int32 or int64, K up to 256 (a token outside the vocabulary, -1
+    say, is an empty place; one that comes twice counts twice); ``mask`` [N,T]
+    (uint8 or bool) is 0 where a token has no loss, and its logits are not
+    read.  Returns the loss [N,T] float32, 0 where nothing is left to learn
+    from; with ``return_normalizers`` also what distill_loss_backward needs,
+    [N,T,2] float32.  Differentiable in the logits; the teacher has no
+    gradient (one that requires it is refused).  The factor temperature^2
+    that some recipes have is left to the caller."""
+    _refuse_tangents(logits, teacher_logits)
+    args = (logits, teacher_logits, teacher_tokens, temperature, mask)
+    if _wants_grad(teacher_logits):
+        raise ValueError("teacher_logits must not require a gradient: detach the teacher")
+    out = _DistillLoss.apply(*args) if _wants_grad(logits) else _distill_forward(return_normalizers, *args)
+    return out if return_normalizers else out[0]
+
+
+def _grad_loss(grad_loss, logits, device):
+    if grad_loss is None:
+        raise TypeError("grad_loss must be a torch.Tensor")
+    return _dense("grad_loss", grad_loss, logits.shape[:2], torch.float32, device)
+
+
+def distill_loss_backward(grad_loss, logits, teacher_logits, teacher_tokens, normalizers, temperature=1.0, mask=None):
+    """The gradient of distill_loss in the logits (dense, of their type):
+    ``grad_loss`` [N,T] float32, ``normalizers`` from the forward call on the
+    same inputs."""
+    _refuse_tangents(grad_loss, logits, teacher_logits)
+    dev, packed, kept = _distill_args(logits, teacher_logits, teacher_tokens, temperature, mask)
+    logits = kept[0]
+    grad_loss = _grad_loss(grad_loss, logits, dev)
+    if normalizers is None:
+        raise ValueError("normalizers is required (distill_loss(..., return_normalizers=True))")
+    norm = _dense("normalizers", normalizers, (*logits.shape[:2], 2), torch.float32, dev)
+    grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    with _on(dev):
+        _native.check(_native.lib().rlscan_distill_loss_backward(
+            packed, grad_loss.data_ptr(), norm.data_ptr(), grad.data_ptr(), _stream_handle(logits.device)),
+            "rlscan_distill_loss_backward")
+    return grad
+
+
+def distill_loss_and_grad(grad_loss, logits, teacher_logits, teacher_tokens, temperature=1.0, mask=None):
+    """(loss, gradient in the logits) in one call, for a training step that
+    knows each token's weight ``grad_loss`` [N,T] float32 before its loss (a
+    mask over the number of tokens, say): the logits are read once.  Not
+    followed by autograd."""
+    _refuse_tangents(grad_loss, logits, teacher_logits)
+    dev, packed, kept = _distill_args(logits, teacher_logits, teacher_tokens, temperature, mask)
+    logits = kept[0]
+    grad_loss = _grad_loss(grad_loss, logits, dev)
+    f32 = dict(dtype=torch.float32, device=logits.device)
+    loss, norm = torch.empty(logits.shape[:2], **f32), torch.empty((*logits.shape[:2], 2), **f32)
+    grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    with _on(dev):
+        _native.check(_native.lib().rlscan_distill_loss_and_grad(
+            packed, grad_loss.data_ptr(), loss.data_ptr(), norm.data_ptr(), grad.data_ptr(),
+            _stream_handle(logits.device)), "rlscan_distill_loss_and_grad")
+    return loss, grad

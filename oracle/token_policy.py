@@ -60,3 +60,42 @@ def gated_scan_backward(gy, x, gate, input_gate, log_decay, initial_state=None, 
         G = np.where(on, np.where(cut, 0.0, a[:, t] * total), G)
     out["initial_state"] = G
     return out
+
+
+def distill_loss(logits, teacher_logits, teacher_tokens, temperature=1.0, mask=None, grad_loss=None):
+    """(loss [N,T], gradient [N,T,V] or None, the terms' magnitude for each of both)"""
+    logits, teacher = _f64(logits, teacher_logits)
+    N, T, V = logits.shape
+    K = teacher.shape[2]
+    loss, mag = np.zeros((N, T)), np.zeros((N, T))
+    grad = gmag = None
+    if grad_loss is not None:
+        grad, gmag = np.zeros((N, T, V)), np.zeros((N, T, V))
+    for n in range(N):
+        for t in range(T):
+            if mask is not None and not mask[n, t]:
+                continue
+            ok = (teacher_tokens[n, t] >= 0) & (teacher_tokens[n, t] < V)
+            with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
+                th = np.where(ok, teacher[n, t], -np.inf) / temperature
+                if (th == -np.inf).all():
+                    continue
+                lq = th - th.max()
+                lq = lq - np.log(np.exp(lq).sum())
+                q = np.exp(lq)
+                z = (logits[n, t] - logits[n, t].max()) / temperature
+                e = np.exp(z)
+                p = e / e.sum()
+                for k in range(K):
+                    if q[k] != 0:
+                        zk = z[teacher_tokens[n, t, k]]
+                        loss[n, t] += q[k] * (lq[k] - zk + np.log(e.sum()))
+                        mag[n, t] += q[k] * (abs(lq[k]) + abs(zk) + np.log(e.sum()) + 1)
+                if grad is not None:
+                    w = grad_loss[n, t] / temperature
+                    grad[n, t], gmag[n, t] = p * w, p * abs(w)
+                    for k in range(K):
+                        if ok[k]:
+                            grad[n, t, teacher_tokens[n, t, k]] -= q[k] * w
+                            gmag[n, t, teacher_tokens[n, t, k]] += q[k] * abs(w)
+    return loss, grad, mag, gmag

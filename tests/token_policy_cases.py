@@ -14,6 +14,12 @@ formula on absolute values (``bound=True`` of the oracle).
   (|L| <= 5 here: 192 u), 1 - r, whose r is right to 3 u where it is near 1,
   another 3 u / (1 - r) <= 165 u and its factors 20 u; a sum over `terms`
   tokens in float32 adds as many u: (2 (430 + 6 T) + 400 + terms) u.
+* distillation.  With X the largest difference of two logits (the student's
+  or the teacher's) over the temperature, an exponent is right to 2 X u and an
+  exponential to (2 X + 4) u, a softmax to twice that and its sum's rounding:
+  a thread adds at most V / 32 values one after the other, in four sums at
+  once, lanes and warps another 60.  Products and logarithms add 20 u, sums
+  over the K tokens K u: (4 X + 100 + V / 32 + K) u of the terms' magnitude.
 * an output in bfloat16 is rounded by at most 2^-9 of itself (2^-8 where the
   two sides lie on different sides of a binade).
 """
@@ -44,3 +50,21 @@ def gated_inputs(N, T, D, dtype, seed, kind="none", step=False, strongest=5.0):
              log_decay=-torch.from_numpy(np.exp(rng.uniform(np.log(1e-4), np.log(strongest), D)).astype(np.float32)))
     resets, lengths = flags(kind, N, T, rng)
     return a, normal(N, D, to=torch.float32), resets, lengths, rng
+
+
+def distill_factor(V, K, spread):
+    return (4 * spread + 100 + V / 32 + K) * U
+
+
+def distill_inputs(N, T, V, K, dtype, seed, teacher_dtype=torch.float32, token_dtype=torch.int64):
+    """logits, the teacher's logits and tokens (some empty, some twice), a mask, grad_loss, the generator"""
+    rng = np.random.default_rng(seed)
+    tokens = rng.integers(0, V, (N, T, K))
+    tokens[rng.random((N, T, K)) < 0.1] = -1
+    tokens[rng.random((N, T, K)) < 0.03] = V
+    tokens[..., 0] = rng.integers(0, V, (N, T))
+    logits = torch.from_numpy((2 * rng.standard_normal((N, T, V))).astype(np.float32)).to(dtype)
+    teacher = torch.from_numpy((2 * rng.standard_normal((N, T, K))).astype(np.float32)).to(teacher_dtype)
+    mask = torch.from_numpy((rng.random((N, T)) < 0.8).astype(np.uint8))
+    grad = torch.from_numpy(rng.standard_normal((N, T)).astype(np.float32))
+    return logits, teacher, torch.from_numpy(tokens).to(token_dtype), mask, grad, rng
