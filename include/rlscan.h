@@ -787,6 +787,54 @@ rlscan_status rlscan_gated_scan_step(const rlscan_gated_scan_args *args, float *
                                      const int32_t *slots, void *y, rlscan_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * The gated feed-forward block: both projections, the activation and the
+ * product (Shazeer, "GLU Variants Improve Transformer", 2020, Eq. 5):
+ *   z = x Wg^T,  u = x Wu^T,  h = act(z) u                       [M,F]
+ * in bfloat16 with float32 sums; z and u stay in 32 bits and h is rounded
+ * once.  Rows have strides of their own; any alignment is accepted, arrays
+ * whose address and row stride are no multiples of 16 bytes are copied first
+ * (in the workspace).  Outputs are dense; results are the same bits on every
+ * call.  M, D and F are below 2^31 - 256.
+ * ------------------------------------------------------------------------- */
+#define RLSCAN_SILU 0   /* z sigmoid(z) */
+#define RLSCAN_GELU 1   /* z times the normal distribution up to z */
+
+typedef struct rlscan_gated_projection_args {
+    int64_t M, D, F;              /* rows, their values, the projections' */
+    int64_t activation;           /* RLSCAN_SILU or RLSCAN_GELU */
+    const void *x;                /* [M,D] */
+    int64_t x_stride;             /* values from row to row */
+    const void *gate_weight;      /* [F,D]: Wg */
+    int64_t gate_stride;
+    const void *up_weight;        /* [F,D]: Wu */
+    int64_t up_stride;
+} rlscan_gated_projection_args;
+
+size_t rlscan_gated_projection_workspace_bytes(const rlscan_gated_projection_args *args);
+
+/* h [M,F].  Errors: RLSCAN_ERR_NULL, RLSCAN_ERR_SHAPE, RLSCAN_ERR_ARG_VALUE
+ * (unknown activation), RLSCAN_ERR_ARG_CONFLICT (h is an input),
+ * RLSCAN_ERR_WORKSPACE, RLSCAN_ERR_MEMORY (inputs and h are device memory),
+ * RLSCAN_ERR_CUDA. */
+rlscan_status rlscan_gated_projection(const rlscan_gated_projection_args *args, void *h, void *ws, size_t ws_bytes,
+                                      rlscan_stream_t stream);
+
+/* Gradients, with z and u made again (32 bits of both are 8 M F bytes to keep):
+ *   gz = grad_h u act'(z),  gu = grad_h act(z)       (rounded to bfloat16)
+ *   grad_x = gz Wg + gu Wu [M,D];  grad_gate = gz^T x,  grad_up = gu^T x [F,D]
+ * grad_x is nullable, grad_gate and grad_up are nullable together. */
+size_t rlscan_gated_projection_backward_workspace_bytes(const rlscan_gated_projection_args *args);
+
+rlscan_status rlscan_gated_projection_backward(const rlscan_gated_projection_args *args, const void *grad_h,
+                                               int64_t grad_h_stride, void *grad_x, void *grad_gate, void *grad_up,
+                                               void *ws, size_t ws_bytes, rlscan_stream_t stream);
+
+/* Synchronises the stream; RLSCAN_ERR_TIMEOUT once after a wait inside a
+ * projection on the current device ran out (4 s; what that call wrote is
+ * incomplete). */
+rlscan_status rlscan_gated_projection_status(rlscan_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Distillation from a teacher's top logits.  For each token, with the
  * teacher's logits over K tokens of the vocabulary and the student's over all:
  *   q = softmax(teacher / temperature) over the K,

@@ -3,7 +3,8 @@
 The compute path is the CUDA library ``librlscan.so`` (hand-written sm_103a
 kernels behind the C ABI in ``include/rlscan.h``); ``api`` binds it for
 PyTorch tensors, ``state_space`` the state-space layer's operators and
-``token_policy`` the gated recurrence of such policies.
+``token_policy`` the gated recurrence and feed-forward block of such policies
+and the loss that distils a teacher into them.
 ``synthetic`` draws seeded rollout buffers.  Importing the
 package does not load the library; the first estimator call does (and raises
 if it has not been built).
@@ -25,6 +26,7 @@ _STATE_SPACE = {
 
 _TOKEN_POLICY = {
     "gated_scan", "gated_scan_backward", "gated_scan_step", "GatedScanGrads",
+    "gated_projection", "gated_projection_backward", "GatedProjectionGrads",
     "distill_loss", "distill_loss_backward", "distill_loss_and_grad",
 }
 

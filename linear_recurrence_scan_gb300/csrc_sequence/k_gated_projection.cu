@@ -1,0 +1,458 @@
+// k_gated_projection.cu -- the gated feed-forward block's two projections with
+// the activation and the product, and its gradients:
+//   z = x Wg^T,  u = x Wu^T,  h = act(z) u
+//   gz = grad_h u act'(z),  gu = grad_h act(z)
+//   dx = gz Wg + gu Wu,  dWg = gz^T x,  dWu = gu^T x
+// Four products on the tensor cores; the first two share their main loop.
+#include "gated_projection.cuh"
+#include "gated_scan.cuh"
+#include "umma.cuh"
+
+namespace rlscan {
+namespace seq {
+namespace {
+
+__device__ unsigned int g_timed_out;  // a wait ran out on this device
+
+// Forward: z and u, then h.  Gates: z and u, then gz and gu.  Input: dx, the
+// sum over both gates' columns.  Weights: dWg and dWu.
+enum class Job { Forward, Gates, Input, Weights };
+
+struct Maps {
+    CUtensorMap a[2], b[2];
+};
+
+struct Work {
+    int64_t M, D, F;
+    int64_t tiles_m, tiles_n, steps;  // steps: blocks of 64 values of K
+    int act;
+    const bf16 *grad_h;
+    int64_t grad_h_stride;
+    bool grad_h_vec, out_vec;
+    bf16 *out[2];
+    int64_t out_stride;
+};
+
+constexpr int kBlockK = 64;  // values of K in a stage: a row of 128 bytes
+constexpr int kStages = 6, kThreads = 256;
+constexpr uint32_t kTileBytes = 128 * kBlockK * 2, kStageBytes = 2 * kTileBytes;
+constexpr size_t kSmem = kStages * kStageBytes + 1024;
+
+__device__ __forceinline__ float2 act_slope(float z, int act)
+{
+    if (act == RLSCAN_SILU) {
+        const float g = sigmoid(z), a = z * g;
+        return make_float2(a, fmaf(a, 1.f - g, g));
+    }
+    const float half = 0.5f * erfcf(-0.70710678118654752f * z);  // the normal distribution up to z
+    return make_float2(z * half, fmaf(z * 0.3989422804014327f, exp2_fast(-0.5f * kLog2e * z * z), half));
+}
+
+// 32 neighbouring values of a row, from column `c`, of which `n` are the row's
+__device__ __forceinline__ void store_row(bf16 *p, const float (&v)[32], int64_t n, bool vec)
+{
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+        if (vec && i + 8 <= n) {
+            Words<bf16, 8> w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w.set(j, v[i + 2 * j], v[i + 2 * j + 1]);
+            w.store(p + i);
+        } else {
+#pragma unroll
+            for (int j = i; j < i + 8; ++j)
+                if (j < n) p[j] = from_f<bf16>(v[j]);
+        }
+    }
+}
+__device__ __forceinline__ void load_row(Words<bf16, 8> (&w)[4], const bf16 *p, int64_t n, bool vec)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i].zero();
+        if (vec && 8 * i + 8 <= n) {
+            w[i].load(p + 8 * i);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = 8 * i + 2 * j;
+                w[i].set(j, at < n ? to_f(p[at]) : 0.f, at + 1 < n ? to_f(p[at + 1]) : 0.f);
+            }
+        }
+    }
+}
+
+// A pair of blocks, one on each of two SMs, makes tiles of 256 x 256: each
+// block has 128 rows of A and half the columns of B in its shared memory, and
+// one thread of the pair's first block multiplies for both.  For z and u the
+// halves are 128 columns of z and the same 128 of u, so that the epilogue
+// finds both of a value in its own tensor memory.  Warps: 0 copies, 1
+// multiplies (the first block's), 2 holds the tensor memory, 4 to 7 take the
+// sums out while the next tile's are made in the other half of the 512 columns.
+template <Job JOB>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    projection_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Work k)
+{
+    constexpr bool kGates = JOB == Job::Forward || JOB == Job::Gates;
+    constexpr bool kAMn = JOB == Job::Weights, kBMn = !kGates;
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t full[kStages], empty[kStages], sums_full[2], sums_empty[2];
+    __shared__ uint32_t tmem_at;
+    __shared__ int gave_up;
+    ptx::pdl_trigger_dependents();
+    const uint32_t smem = (ptx::smem_u32(raw) + 1023u) & ~1023u, rank = umma::cluster_rank();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        for (int i = 0; i < kStages; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sums_full[i], 1);
+            ptx::mbar_init(&sums_empty[i], 8);  // a warp's arrival each, of both blocks
+        }
+        ptx::fence_mbar_init();
+    }
+    if (warp == 2) umma::tmem_alloc(ptx::smem_u32(&tmem_at), 512);
+    umma::fence_before();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    umma::fence_after();
+    const uint32_t tmem = tmem_at;
+    ptx::pdl_wait_prerequisites();
+    const int64_t tiles = k.tiles_m * k.tiles_n, pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    // Tiles in bands of eight rows of tiles, column after column: the pairs at
+    // work share rows of A and columns of B in L2.
+    auto place = [&](int64_t tile, int64_t &m, int64_t &n) {
+        constexpr int64_t kBand = 8;
+        const int64_t band = tile / (kBand * k.tiles_n), in = tile - band * kBand * k.tiles_n;
+        const int64_t high = k.tiles_m - band * kBand < kBand ? k.tiles_m - band * kBand : kBand;
+        m = band * kBand + in % high;
+        n = in / high;
+    };
+    if (warp == 0 && lane == 0) {  // copies
+        uint32_t stage = 0, phase = 1;  // the first wait on an empty stage passes
+        int64_t issued = 0;
+        const int64_t half = kGates ? 0 : JOB == Job::Input ? k.steps / 2 : k.tiles_m / 2;
+        for (int64_t tile = pair; tile < tiles && !*const_cast<volatile int *>(&gave_up); tile += pairs) {
+            int64_t tm, tn;
+            place(tile, tm, tn);
+            for (int64_t s = 0; s < k.steps; ++s) {
+                if (!umma::wait(ptx::smem_u32(&empty[stage]), phase, &gave_up)) break;
+                const uint32_t bar = umma::of_rank(ptx::smem_u32(&full[stage]), 0);
+                const uint32_t a = smem + stage * kStageBytes, b = a + kTileBytes;
+                if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+                if constexpr (kGates) {
+                    const int k0 = static_cast<int>(s) * kBlockK;
+                    umma::load_box(a, &maps.a[0], k0, static_cast<int>(tm * 256 + rank * 128), bar);
+                    umma::load_box(b, &maps.b[rank], k0, static_cast<int>(tn * 128), bar);
+                } else if constexpr (JOB == Job::Input) {
+                    const int part = s >= half ? 1 : 0, k0 = static_cast<int>(s - part * half) * kBlockK;
+                    umma::load_box(a, &maps.a[part], k0, static_cast<int>(tm * 256 + rank * 128), bar);
+                    for (int i = 0; i < 2; ++i)
+                        umma::load_box(b + i * (kTileBytes / 2), &maps.b[part], static_cast<int>(tn * 256 + rank * 128 + 64 * i), k0, bar);
+                } else {
+                    const int part = tm >= half ? 1 : 0, k0 = static_cast<int>(s) * kBlockK;
+                    const int f0 = static_cast<int>((tm - part * half) * 256 + rank * 128);
+                    for (int i = 0; i < 2; ++i) {
+                        umma::load_box(a + i * (kTileBytes / 2), &maps.a[part], f0 + 64 * i, k0, bar);
+                        umma::load_box(b + i * (kTileBytes / 2), &maps.b[0], static_cast<int>(tn * 256 + rank * 128 + 64 * i), k0, bar);
+                    }
+                }
+                ++issued;
+                if (++stage == kStages) stage = 0, phase ^= 1;
+            }
+        }
+        // The block stays until the products have taken its last copies.
+        for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+            if (!umma::wait(ptx::smem_u32(&empty[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u, &gave_up)) break;
+    } else if (warp == 1 && lane == 0 && rank == 0) {  // products
+        constexpr uint32_t kInstruction = umma::instruction(kAMn, kBMn, 256, 256);
+        uint32_t stage = 0, phase = 0, buffer = 0, buffer_phase = 1;
+        for (int64_t tile = pair; tile < tiles; tile += pairs) {
+            if (!umma::wait(ptx::smem_u32(&sums_empty[buffer]), buffer_phase, &gave_up)) break;
+            umma::fence_after();
+            bool fine = true;
+            for (int64_t s = 0; s < k.steps && fine; ++s) {
+                fine = umma::wait(ptx::smem_u32(&full[stage]), phase, &gave_up);
+                if (!fine) break;
+                umma::fence_after();
+                const uint32_t a = smem + stage * kStageBytes, b = a + kTileBytes;
+#pragma unroll
+                for (int j = 0; j < kBlockK / 16; ++j)
+                    umma::multiply(tmem + buffer * 256, umma::descriptor(a + j * (kAMn ? 2048 : 32), kTileBytes / 2),
+                                   umma::descriptor(b + j * (kBMn ? 2048 : 32), kTileBytes / 2), kInstruction, s > 0 || j > 0);
+                umma::commit(ptx::smem_u32(&empty[stage]));
+                if (++stage == kStages) stage = 0, phase ^= 1;
+            }
+            if (!fine) break;
+            umma::commit(ptx::smem_u32(&sums_full[buffer]));
+            buffer ^= 1;
+            if (buffer == 0) buffer_phase ^= 1;
+        }
+    } else if (warp >= 4) {  // sums
+        uint32_t buffer = 0, phase = 0;
+        const int part = warp % 4;
+        for (int64_t tile = pair; tile < tiles; tile += pairs) {
+            int64_t tm, tn;
+            place(tile, tm, tn);
+            const int64_t half = k.tiles_m / 2;
+            const int which = JOB == Job::Weights && tm >= half ? 1 : 0;
+            const int64_t row = (tm - which * half) * 256 + rank * 128 + part * 32 + lane;
+            const int64_t rows = JOB == Job::Weights ? k.F : k.M;
+            if (!umma::wait(ptx::smem_u32(&sums_full[buffer]), phase, &gave_up)) break;
+            umma::fence_after();
+            const uint32_t at = tmem + buffer * 256 + (static_cast<uint32_t>(part * 32) << 16);
+            if constexpr (kGates) {
+                const int64_t f0 = tn * 128;
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    const int64_t n = row < rows ? k.F - f0 - c : 0;
+                    uint32_t z[32], u[32];
+                    Words<bf16, 8> gh[4];
+                    if constexpr (JOB == Job::Gates) load_row(gh, k.grad_h + row * k.grad_h_stride + f0 + c, n, k.grad_h_vec);
+                    umma::tmem_load(z, at + c);
+                    umma::tmem_load(u, at + 128 + c);
+                    umma::tmem_loaded();
+                    float v[32], w[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float uu = __uint_as_float(u[i]);
+                        const float2 as = act_slope(__uint_as_float(z[i]), k.act);
+                        if constexpr (JOB == Job::Forward) {
+                            v[i] = as.x * uu;
+                        } else {
+                            const float g = gh[i / 8][i % 8];
+                            v[i] = g * uu * as.y;
+                            w[i] = g * as.x;
+                        }
+                    }
+                    store_row(k.out[0] + row * k.out_stride + f0 + c, v, n, k.out_vec);
+                    if constexpr (JOB == Job::Gates) store_row(k.out[1] + row * k.out_stride + f0 + c, w, n, k.out_vec);
+                }
+            } else {
+                const int64_t d0 = tn * 256;
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 32) {
+                    uint32_t v[32];
+                    umma::tmem_load(v, at + c);
+                    umma::tmem_loaded();
+                    float f[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+                    store_row(k.out[which] + row * k.out_stride + d0 + c, f, row < rows ? k.D - d0 - c : 0, k.out_vec);
+                }
+            }
+            umma::fence_before();
+            __syncwarp();
+            if (lane == 0) umma::arrive_cluster(umma::of_rank(ptx::smem_u32(&sums_empty[buffer]), 0));
+            buffer ^= 1;
+            if (buffer == 0) phase ^= 1;
+        }
+    }
+    __syncwarp();
+    umma::fence_before();
+    __syncthreads();
+    if (gave_up != 0) {  // copies and products in flight take microseconds: they end before the block does
+        if (threadIdx.x == 0) atomicExch(&g_timed_out, 1u);
+        const uint64_t start = ptx::globaltimer_ns();
+        while (ptx::globaltimer_ns() - start < 1'000'000) {
+        }
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();  // neither block leaves while the other may still reach it
+    umma::fence_after();
+    if (warp == 2) umma::tmem_free(tmem, 512);
+}
+
+// Rows of `columns` values into rows `pitch` values apart
+__global__ void __launch_bounds__(256) pack_kernel(const bf16 *from, int64_t stride, bf16 *to, int64_t pitch, int64_t rows, int64_t columns)
+{
+    ptx::pdl_trigger_dependents();
+    ptx::pdl_wait_prerequisites();
+    const int64_t all = rows * columns, step = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += step) {
+        const Division at = divide(i, columns);
+        to[at.q * pitch + at.r] = from[at.q * stride + at.r];
+    }
+}
+
+int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+
+// Tensor maps take arrays whose address and row stride are multiples of 16
+// bytes; others are copied first.
+bool fits_map(const void *p, int64_t rows, int64_t columns, int64_t stride)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || (stride % 8 == 0 && stride >= columns && stride < (int64_t{1} << 38)));
+}
+
+struct Operand {
+    const void *p;
+    int64_t rows, columns, pitch;
+    bool packed;
+};
+
+Operand operand(const void *p, int64_t rows, int64_t columns, int64_t stride)
+{
+    const bool fits = fits_map(p, rows, columns, stride);
+    return {p, rows, columns, fits && rows > 1 ? stride : up8(columns), !fits};
+}
+
+size_t bytes_of(const Operand &o) { return o.packed ? static_cast<size_t>(o.rows) * o.pitch * 2 : 0; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct Layout {
+    Operand x, gate, up;
+    size_t at_x, at_gate, at_up, bytes;
+};
+
+Layout layout(const rlscan_gated_projection_args &a)
+{
+    Layout l;
+    l.x = operand(a.x, a.M, a.D, a.x_stride);
+    l.gate = operand(a.gate_weight, a.F, a.D, a.gate_stride);
+    l.up = operand(a.up_weight, a.F, a.D, a.up_stride);
+    l.at_x = 0;
+    l.at_gate = l.at_x + up256(bytes_of(l.x));
+    l.at_up = l.at_gate + up256(bytes_of(l.gate));
+    l.bytes = l.at_up + up256(bytes_of(l.up));
+    return l;
+}
+
+rlscan_status pack(Operand &o, int64_t stride, void *to, cudaStream_t s)
+{
+    if (!o.packed) return RLSCAN_OK;
+    const int64_t blocks = ceil_div(o.rows * o.columns, 256), most = 16 * (sm_count() > 0 ? sm_count() : 152);
+    const rlscan_status st = launch_overlapped(pack_kernel, blocks < most ? blocks : most, 256, 0, s, static_cast<const bf16 *>(o.p),
+                                               stride, static_cast<bf16 *>(to), o.pitch, o.rows, o.columns);
+    o.p = to;
+    return st;
+}
+
+rlscan_status pack_all(const rlscan_gated_projection_args &a, Layout &l, char *ws, cudaStream_t s)
+{
+    rlscan_status st = pack(l.x, a.x_stride, ws + l.at_x, s);
+    if (st == RLSCAN_OK) st = pack(l.gate, a.gate_stride, ws + l.at_gate, s);
+    if (st == RLSCAN_OK) st = pack(l.up, a.up_stride, ws + l.at_up, s);
+    return st;
+}
+
+bool map_of(CUtensorMap *m, const Operand &o, uint32_t box) { return umma::encode(m, o.p, o.rows, o.columns, o.pitch, box); }
+
+template <Job JOB>
+rlscan_status launch_job(const Maps &maps, Work &w, cudaStream_t s)
+{
+    static PerDevice raised, pairs_of;
+    if (!raise_smem(raised, projection_kernel<JOB>, kSmem)) return RLSCAN_ERR_CUDA;
+    const int most = pairs_of.get(current_device(), [] {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        return ok(cudaOccupancyMaxActiveClusters(&n, projection_kernel<JOB>, &cfg)) ? n : 0;
+    });
+    const int64_t tiles = w.tiles_m * w.tiles_n, pairs = most > 0 ? most : 1;
+    if (w.M > 0x7fffffff - 256 || w.F > 0x7fffffff - 256 || w.D > 0x7fffffff - 256) return RLSCAN_ERR_SHAPE;
+    return launch(true, projection_kernel<JOB>, 2 * (tiles < pairs ? tiles : pairs), kThreads, kSmem, s, maps, w);
+}
+
+bool vec_rows(const void *p, int64_t stride) { return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(stride * 2)) & 15u) == 0; }
+
+}  // namespace
+
+size_t gated_projection_workspace(const rlscan_gated_projection_args &a)
+{
+    return a.M == 0 || a.F == 0 || a.D == 0 ? 0 : layout(a).bytes;
+}
+
+rlscan_status launch_gated_projection(const rlscan_gated_projection_args &a, void *h, void *ws, cudaStream_t s)
+{
+    if (a.D == 0) return ok(cudaMemsetAsync(h, 0, static_cast<size_t>(a.M) * a.F * 2, s)) ? RLSCAN_OK : RLSCAN_ERR_CUDA;
+    Layout l = layout(a);
+    rlscan_status st = pack_all(a, l, static_cast<char *>(ws), s);
+    if (st != RLSCAN_OK) return st;
+    Maps m = {};
+    if (!map_of(&m.a[0], l.x, 128) || !map_of(&m.b[0], l.gate, 128) || !map_of(&m.b[1], l.up, 128)) return RLSCAN_ERR_CUDA;
+    Work w = {};
+    w.M = a.M, w.D = a.D, w.F = a.F, w.act = static_cast<int>(a.activation);
+    w.tiles_m = ceil_div(a.M, 256), w.tiles_n = ceil_div(a.F, 128), w.steps = ceil_div(a.D, kBlockK);
+    w.out[0] = static_cast<bf16 *>(h), w.out_stride = a.F, w.out_vec = vec_rows(h, a.F);
+    return launch_job<Job::Forward>(m, w, s);
+}
+
+size_t gated_projection_backward_workspace(const rlscan_gated_projection_args &a)
+{
+    if (a.M == 0 || a.F == 0 || a.D == 0) return 0;
+    return layout(a).bytes + static_cast<size_t>(a.M) * 2 * up8(a.F) * 2;
+}
+
+rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_args &a, const void *grad_h,
+                                               int64_t grad_h_stride, void *grad_x, void *grad_gate, void *grad_up,
+                                               void *ws, cudaStream_t s)
+{
+    if (a.M == 0 || a.F == 0 || a.D == 0) {  // sums of nothing
+        const size_t w = static_cast<size_t>(a.F) * a.D * 2, x = static_cast<size_t>(a.M) * a.D * 2;
+        for (void *p : {grad_gate, grad_up})
+            if (p != nullptr && w > 0 && !ok(cudaMemsetAsync(p, 0, w, s))) return RLSCAN_ERR_CUDA;
+        if (grad_x != nullptr && x > 0 && !ok(cudaMemsetAsync(grad_x, 0, x, s))) return RLSCAN_ERR_CUDA;
+        return RLSCAN_OK;
+    }
+    Layout l = layout(a);
+    rlscan_status st = pack_all(a, l, static_cast<char *>(ws), s);
+    if (st != RLSCAN_OK) return st;
+    const int64_t pitch = up8(a.F);
+    bf16 *g = reinterpret_cast<bf16 *>(static_cast<char *>(ws) + l.bytes);  // [M, 2 pitch]: gz, gu
+    Maps m = {};
+    if (!map_of(&m.a[0], l.x, 128) || !map_of(&m.b[0], l.gate, 128) || !map_of(&m.b[1], l.up, 128)) return RLSCAN_ERR_CUDA;
+    Work w = {};
+    w.M = a.M, w.D = a.D, w.F = a.F, w.act = static_cast<int>(a.activation);
+    w.tiles_m = ceil_div(a.M, 256), w.tiles_n = ceil_div(a.F, 128), w.steps = ceil_div(a.D, kBlockK);
+    w.grad_h = static_cast<const bf16 *>(grad_h), w.grad_h_stride = grad_h_stride, w.grad_h_vec = vec_rows(grad_h, grad_h_stride);
+    w.out[0] = g, w.out[1] = g + pitch, w.out_stride = 2 * pitch, w.out_vec = true;
+    st = launch_job<Job::Gates>(m, w, s);
+    if (st != RLSCAN_OK) return st;
+    const Operand gz{g, a.M, a.F, 2 * pitch, false}, gu{g + pitch, a.M, a.F, 2 * pitch, false};
+    if (grad_x != nullptr) {
+        Maps mx = {};
+        if (!map_of(&mx.a[0], gz, 128) || !map_of(&mx.a[1], gu, 128) || !map_of(&mx.b[0], l.gate, 64) || !map_of(&mx.b[1], l.up, 64))
+            return RLSCAN_ERR_CUDA;
+        w.tiles_n = ceil_div(a.D, 256), w.steps = 2 * ceil_div(a.F, kBlockK);
+        w.out[0] = static_cast<bf16 *>(grad_x), w.out_stride = a.D, w.out_vec = vec_rows(grad_x, a.D);
+        st = launch_job<Job::Input>(mx, w, s);
+        if (st != RLSCAN_OK) return st;
+    }
+    if (grad_gate != nullptr) {
+        Maps mw = {};
+        if (!map_of(&mw.a[0], gz, 64) || !map_of(&mw.a[1], gu, 64) || !map_of(&mw.b[0], l.x, 64)) return RLSCAN_ERR_CUDA;
+        w.tiles_m = 2 * ceil_div(a.F, 256), w.tiles_n = ceil_div(a.D, 256), w.steps = ceil_div(a.M, kBlockK);
+        w.out[0] = static_cast<bf16 *>(grad_gate), w.out[1] = static_cast<bf16 *>(grad_up), w.out_stride = a.D;
+        w.out_vec = vec_rows(grad_gate, a.D) && vec_rows(grad_up, a.D);
+        st = launch_job<Job::Weights>(mw, w, s);
+    }
+    return st;
+}
+
+rlscan_status gated_projection_status(cudaStream_t s)
+{
+    unsigned int seen = 0;
+    if (!ok(cudaMemcpyFromSymbolAsync(&seen, g_timed_out, sizeof seen, 0, cudaMemcpyDeviceToHost, s)) || !ok(cudaStreamSynchronize(s)))
+        return RLSCAN_ERR_CUDA;
+    if (seen == 0) return RLSCAN_OK;
+    const unsigned int none = 0;
+    if (!ok(cudaMemcpyToSymbolAsync(g_timed_out, &none, sizeof none, 0, cudaMemcpyHostToDevice, s)) || !ok(cudaStreamSynchronize(s)))
+        return RLSCAN_ERR_CUDA;
+    return RLSCAN_ERR_TIMEOUT;
+}
+
+}  // namespace seq
+}  // namespace rlscan

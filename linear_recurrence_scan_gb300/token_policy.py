@@ -23,6 +23,7 @@ from .state_space import (_ARRAY3, _TYPES, _act, _at, _changed, _check, _dense, 
 
 __all__ = [
     "gated_scan", "gated_scan_backward", "gated_scan_step", "GatedScanGrads",
+    "gated_projection", "gated_projection_backward", "GatedProjectionGrads",
     "distill_loss", "distill_loss_backward", "distill_loss_and_grad",
 ]
 
@@ -30,6 +31,8 @@ GATED_CHECKPOINT = 64   # tokens between two checkpoints of the gated scan (RLSC
 
 _GATED_ARGS = struct.Struct("=17q")
 _GATED_GRADS = struct.Struct("=5q")
+_PROJECTION_ARGS = struct.Struct("=10q")
+_ACTIVATIONS = {"silu": 0, "gelu": 1}
 _DISTILL_ARGS = struct.Struct("=13qd")
 
 MAX_TEACHER_TOKENS = 256   # RLSCAN_DISTILL_MOST
@@ -172,6 +175,118 @@ def gated_scan_step(state, x, gate, input_gate, log_decay, slots=None):
                                                            _stream_handle(x.device)), "rlscan_gated_scan_step")
     _changed(state)
     return y
+
+
+# ---------------------------------------------------------------------------
+# gated feed-forward block
+
+class GatedProjectionGrads(NamedTuple):
+    """Gradients of gated_projection's inputs."""
+    x: torch.Tensor
+    gate_weight: torch.Tensor
+    up_weight: torch.Tensor
+
+
+def _matrix(name, t, shape, device):
+    """(tensor, address, row stride) of a bfloat16 [..., columns] array as rows."""
+    _check(name, t, shape, torch.bfloat16, device)
+    if len(shape) != 2:
+        t = t.reshape(t.numel() // max(shape[-1], 1), shape[-1])
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        t = t.contiguous()
+    return t, t.data_ptr(), t.stride(0)
+
+
+def _projection_args(x, gate_weight, up_weight, activation):
+    """Checks; (device, the packed arguments, (x, both weights) as rows)."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 2:
+        raise ValueError("x must be a [..., values] tensor of at least 2 dimensions")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be 'silu' or 'gelu', got {activation!r}")
+    dev = _lead("x", x, x.dim())
+    D = x.shape[-1]
+    if not isinstance(gate_weight, torch.Tensor) or gate_weight.dim() != 2:
+        raise ValueError("gate_weight must be a [features, values] tensor")
+    F = gate_weight.shape[0]
+    if D == 0:
+        raise ValueError("x must have values")
+    x, xp, xs = _matrix("x", x, x.shape, dev)
+    gate_weight, gp, gs = _matrix("gate_weight", gate_weight, (F, D), dev)
+    up_weight, up, us = _matrix("up_weight", up_weight, (F, D), dev)
+    packed = _PROJECTION_ARGS.pack(x.shape[0], D, F, _ACTIVATIONS[activation], xp, xs, gp, gs, up, us)
+    return dev, packed, (x, gate_weight, up_weight)
+
+
+def _projection_forward(x, gate_weight, up_weight, activation):
+    dev, packed, (rows, gate, up) = _projection_args(x, gate_weight, up_weight, activation)
+    h = torch.empty((*x.shape[:-1], gate.shape[0]), dtype=x.dtype, device=x.device)
+    lib = _native.lib()
+    with _on(dev):
+        ws = _scratch(lib.rlscan_gated_projection_workspace_bytes(packed), x.device)
+        _native.check(lib.rlscan_gated_projection(packed, h.data_ptr(), _at(ws), 0 if ws is None else ws.numel(),
+                                                  _stream_handle(x.device)), "rlscan_gated_projection")
+    return h
+
+
+class _GatedProjection(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gate_weight, up_weight, activation):
+        ctx.activation = activation
+        ctx.save_for_backward(x, gate_weight, up_weight)
+        ctx.set_materialize_grads(False)
+        return _projection_forward(x, gate_weight, up_weight, activation)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_h):
+        if grad_h is None:
+            return None, None, None, None
+        x, gate_weight, up_weight = ctx.saved_tensors
+        g = _projection_backward(grad_h, x, gate_weight, up_weight, ctx.activation, ctx.needs_input_grad[0],
+                                 ctx.needs_input_grad[1] or ctx.needs_input_grad[2])
+        return (*g, None)
+
+
+def gated_projection(x, gate_weight, up_weight, activation="silu"):
+    """The gated feed-forward block's projections, activation and product:
+
+        z = x gate_weight^T,  u = x up_weight^T,  h = act(z) * u
+
+    x [..., D] and both weights [F, D] are bfloat16 (rows of any stride:
+    halves of one [2F, D] weight are taken as they are); the sums, z and u are
+    float32, h [..., F] is rounded once.  ``activation`` is "silu" or "gelu"
+    (z times the normal distribution up to z).  float32 is refused: the tensor
+    cores would round its factors to 11 bits."""
+    _refuse_tangents(x, gate_weight, up_weight)
+    if _wants_grad(x, gate_weight, up_weight):
+        return _GatedProjection.apply(x, gate_weight, up_weight, activation)
+    return _projection_forward(x, gate_weight, up_weight, activation)
+
+
+def _projection_backward(grad_h, x, gate_weight, up_weight, activation, want_x, want_weights):
+    shape = x.shape
+    dev, packed, (rows, gate, up) = _projection_args(x, gate_weight, up_weight, activation)
+    grad_h, ghp, ghs = _matrix("grad_h", grad_h, (*shape[:-1], gate.shape[0]), dev)
+
+    def like(size, wanted):
+        return torch.empty(size, dtype=x.dtype, device=x.device) if wanted else None
+
+    g = GatedProjectionGrads(like(shape, want_x), like(gate.shape, want_weights), like(gate.shape, want_weights))
+    lib = _native.lib()
+    with _on(dev):
+        ws = _scratch(lib.rlscan_gated_projection_backward_workspace_bytes(packed), x.device)
+        _native.check(lib.rlscan_gated_projection_backward(
+            packed, ghp, ghs, _at(g.x), _at(g.gate_weight), _at(g.up_weight), _at(ws),
+            0 if ws is None else ws.numel(), _stream_handle(x.device)), "rlscan_gated_projection_backward")
+    return g
+
+
+def gated_projection_backward(grad_h, x, gate_weight, up_weight, activation="silu"):
+    """Gradients of gated_projection: ``grad_h`` [..., F] bfloat16.  z and u
+    are made again from x, in 32 bits; the gradients at z and u are rounded to
+    bfloat16 for the products that follow.  Returns GatedProjectionGrads."""
+    _refuse_tangents(grad_h, x, gate_weight, up_weight)
+    return _projection_backward(grad_h, x, gate_weight, up_weight, activation, True, True)
 
 
 # ---------------------------------------------------------------------------

@@ -68,3 +68,46 @@ def distill_inputs(N, T, V, K, dtype, seed, teacher_dtype=torch.float32, token_d
     mask = torch.from_numpy((rng.random((N, T)) < 0.8).astype(np.uint8))
     grad = torch.from_numpy(rng.standard_normal((N, T)).astype(np.float32))
     return logits, teacher, torch.from_numpy(tokens).to(token_dtype), mask, grad, rng
+
+
+def projection_inputs(M, D, F, seed, scale=1.0):
+    """x, both weights, grad_h in bfloat16, the generator"""
+    rng = np.random.default_rng(seed)
+
+    def normal(*shape, s=1.0):
+        return torch.from_numpy((rng.standard_normal(shape) * s).astype(np.float32)).to(torch.bfloat16)
+
+    return normal(M, D, s=scale), normal(F, D, s=D ** -0.5), normal(F, D, s=D ** -0.5), normal(M, F), rng
+
+
+def projection_oracle(x, wg, wu, gh, act):
+    """name -> (value, bound in front of the last rounding), float64.
+
+    A sum of n products in the tensor cores is right to 2 n u of its terms'
+    magnitude (each of n additions is off by less than a step, 2 u); an
+    activation and its slope move by at most 1.13 and 0.8 of z's error and are
+    right to 40 u of themselves (a sigmoid to (2 |z| + 6) u, |z| <= 17); gz and
+    gu are rounded by 2^-8 of themselves for the products that follow."""
+    x, wg, wu, gh = (np.asarray(t.float().numpy(), np.float64) for t in (x, wg, wu, gh))
+    n = lambda k: 2 * (k + 8) * U  # noqa: E731
+    z, u = x @ wg.T, x @ wu.T
+    ez, eu = (n(x.shape[1]) * (np.abs(x) @ np.abs(w).T) for w in (wg, wu))
+    if act == "silu":
+        g = 1 / (1 + np.exp(-z))
+        a, s = z * g, g * (1 + z * (1 - g))
+    else:
+        from scipy.special import ndtr
+        g = ndtr(z)
+        a, s = z * g, g + z * np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
+    ea = 1.13 * ez + 40 * U * np.abs(a)
+    es = 0.8 * ez + 40 * U * (1 + np.abs(z) * 0)
+    h, gz, gu = a * u, gh * u * s, gh * a
+    r = 2.0 ** -8
+    egz = np.abs(gh) * (np.abs(s) * eu + np.abs(u) * es) + r * np.abs(gz) + 1e-30
+    egu = np.abs(gh) * ea + r * np.abs(gu) + 1e-30
+    F, M = wg.shape[0], x.shape[0]
+    return dict(
+        h=(h, np.abs(u) * ea + np.abs(a) * eu + 4 * U * np.abs(h)),
+        x=(gz @ wg + gu @ wu, egz @ np.abs(wg) + egu @ np.abs(wu) + n(2 * F) * (np.abs(gz) @ np.abs(wg) + np.abs(gu) @ np.abs(wu))),
+        gate_weight=(gz.T @ x, egz.T @ np.abs(x) + n(M) * (np.abs(gz).T @ np.abs(x))),
+        up_weight=(gu.T @ x, egu.T @ np.abs(x) + n(M) * (np.abs(gu).T @ np.abs(x))))
