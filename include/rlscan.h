@@ -749,9 +749,9 @@ typedef struct rlscan_gated_scan_args {
     const int32_t *lengths;       /* [N], nullable */
 } rlscan_gated_scan_args;
 
-/* Tokens between two checkpoints: checkpoints [N, ceil(T / 64), D] hold the
- * state before tokens 0, 64, 128, ... */
-#define RLSCAN_GATED_SCAN_CHECKPOINT 64
+/* Tokens between two checkpoints: checkpoints [N, ceil(T / 32), D] hold the
+ * state before tokens 0, 32, 64, ... */
+#define RLSCAN_GATED_SCAN_CHECKPOINT 32
 
 /* Forward.  Outputs: y [N,T,D]; final_state [N,D] nullable: the state after
  * each row's last token; checkpoints nullable (what the backward pass needs).

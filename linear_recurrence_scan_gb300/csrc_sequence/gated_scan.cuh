@@ -8,9 +8,10 @@
 namespace rlscan {
 namespace seq {
 
-constexpr int kGatedTile = RLSCAN_GATED_SCAN_CHECKPOINT;  // tokens of a block's step
-constexpr int kGatedWidth = 64;                           // channels of a block: two a lane
-constexpr int kGatedCluster = 8;                          // blocks that share a row, at most
+constexpr int kGatedTile = 64;     // tokens of a block's step
+constexpr int kGatedWarps = 8;     // of a block
+constexpr int kGatedWidth = 64;    // channels of a block: two a lane
+constexpr int kGatedCluster = 8;   // blocks that share a row, at most
 constexpr float kSquareFloor = 0x1p-100f;
 
 // NaN stays NaN
@@ -28,7 +29,9 @@ __device__ __forceinline__ float rsqrt_fast(float v)
 }
 
 // Two channels of one token as they are stored.  VEC: neighbours, one aligned
-// load; otherwise 32 channels apart, so that a warp still reads whole sectors.
+// load; otherwise `apart` values apart (32, less at the array's edge), so that
+// a warp still reads whole sectors.  A load stays in flight until its value is
+// looked at.
 template <class T, bool VEC>
 struct Two {
     static constexpr int N = VEC && sizeof(T) == 2 ? 1 : 2;
@@ -38,24 +41,19 @@ struct Two {
         w[0] = 0u;
         if constexpr (N == 2) w[1] = 0u;
     }
-    // on0, on1: whether the channels are the array's (VEC: both or none)
-    __device__ __forceinline__ void load(const T *p, bool on0, bool on1)
+    __device__ __forceinline__ void load(const T *p, int apart)
     {
-        zero();
         if constexpr (VEC) {
-            if (on0) {
-                if constexpr (N == 1) {
-                    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
-                } else {
-                    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-                }
-            }
+            if constexpr (N == 1)
+                asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+            else
+                asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
         } else if constexpr (sizeof(T) == 2) {
-            if (on0) asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(w[0]) : "l"(p));
-            if (on1) asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(w[1]) : "l"(p + 32));
+            asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(w[0]) : "l"(p));
+            asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(w[1]) : "l"(p + apart));
         } else {
-            if (on0) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
-            if (on1) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(w[1]) : "l"(p + 32));
+            asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+            asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(w[1]) : "l"(p + apart));
         }
     }
     __device__ __forceinline__ f2 get() const
@@ -69,6 +67,52 @@ struct Two {
         }
     }
 };
+
+// A lane's two channels: the first one, whether both are the array's, and the
+// ones it reads (a lane past the last channel reads the last ones, and writes
+// nothing).
+template <bool VEC>
+struct Lane {
+    int64_t d, from;
+    bool on0, on1;
+    int apart;
+    __device__ __forceinline__ Lane(int64_t block, int lane, int64_t D)
+    {
+        d = block * kGatedWidth + (VEC ? 2 * lane : lane);
+        on0 = d < D;
+        on1 = VEC ? on0 : d + 32 < D;
+        from = on0 ? d : D - (VEC ? 2 : 1);
+        apart = on1 ? 32 : 0;
+    }
+};
+
+// TOK tokens from t0 on of one array; past `len` (the row's tokens) zeros
+template <class T, bool VEC, int TOK>
+__device__ __forceinline__ void fetch_tokens(Two<T, VEC> (&v)[TOK], const rlscan_array3 &a, int64_t n, int64_t t0, int64_t len, const Lane<VEC> &l)
+{
+    const T *p = static_cast<const T *>(a.data) + n * a.row_stride + t0 * a.token_stride + l.from;
+    const int64_t step = a.token_stride;
+    if (t0 + TOK <= len) {
+#pragma unroll
+        for (int k = 0; k < TOK; ++k, p += step) v[k].load(p, l.apart);
+    } else {
+#pragma unroll
+        for (int k = 0; k < TOK; ++k) {
+            v[k].zero();
+            if (t0 + k < len) v[k].load(p + k * step, l.apart);
+        }
+    }
+}
+
+// bit k: a new episode starts at token t0 + k
+template <int TOK>
+__device__ __forceinline__ uint32_t fetch_resets(const uint8_t *resets, int64_t row, int64_t t0, int64_t len, int lane)
+{
+    if (resets == nullptr) return 0u;
+    uint32_t flag = 0;
+    if (lane < TOK && t0 + lane < len) flag = resets[row + t0 + lane];
+    return __ballot_sync(0xffffffffu, flag != 0);
+}
 
 template <class T, bool VEC>
 __device__ __forceinline__ void store_two(T *p, f2 v, bool on0, bool on1)
@@ -141,14 +185,39 @@ __device__ __forceinline__ void store_to_rank(const void *mine, int rank, float4
                  : "memory");
 }
 
-// Blocks that share a row: enough that every SM has two, no more than there
-// are steps for.
-inline int gated_cluster(int64_t chains, int64_t T)
+__host__ __device__ inline int64_t gated_marks(int64_t T) { return (T + RLSCAN_GATED_SCAN_CHECKPOINT - 1) / RLSCAN_GATED_SCAN_CHECKPOINT; }
+
+// Blocks of a cluster that share a row: as many as make the fewest steps one
+// after the other, counting the rounds in which clusters of that size become
+// resident.  A row split over blocks costs each step an exchange, taken as a
+// quarter of a step.
+template <class T, bool VEC, class K>
+inline int gated_cluster(K kernel, int64_t chains, int64_t tokens, int tile)
 {
-    const int64_t sms = sm_count() > 0 ? sm_count() : 152, tiles = ceil_div(T, kGatedTile);
-    int c = 1;
-    while (c < kGatedCluster && chains * c < 2 * sms && 2 * c <= tiles) c *= 2;
-    return c;
+    static PerDevice resident[kGatedCluster + 1];
+    const int64_t tiles = ceil_div(tokens, tile);
+    int best = 1;
+    double least = 0;
+    for (int c = 1; c <= kGatedCluster; ++c) {
+        if (c > 1 && c > tiles) break;
+        const int64_t fit = resident[c].get(current_device(), [&] {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(c));
+            cfg.blockDim = dim3(32 * kGatedWarps);
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            return ok(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) ? n : 0;
+        });
+        if (fit <= 0) continue;
+        const double time = static_cast<double>(ceil_div(chains, fit)) * static_cast<double>(ceil_div(tiles, c)) * (c > 1 ? 1.25 : 1.0);
+        if (c == 1 || time < least) best = c, least = time;
+    }
+    return best;
 }
 
 template <class K, class... Args>

@@ -27,7 +27,7 @@ __all__ = [
     "distill_loss", "distill_loss_backward", "distill_loss_and_grad",
 ]
 
-GATED_CHECKPOINT = 64   # tokens between two checkpoints of the gated scan (RLSCAN_GATED_SCAN_CHECKPOINT)
+GATED_CHECKPOINT = 32   # tokens between two checkpoints of the gated scan (RLSCAN_GATED_SCAN_CHECKPOINT)
 
 _GATED_ARGS = struct.Struct("=17q")
 _GATED_GRADS = struct.Struct("=5q")
@@ -117,7 +117,7 @@ def gated_scan(x, gate, input_gate, log_decay, initial_state=None, resets=None, 
     selective_scan (at a reset h_{t-1} counts 0, the input keeps its root).
     Returns (y, final_state): y like x, the states [N,channels] float32 after
     each row's last token.  With ``return_checkpoints`` a third value, what
-    gated_scan_backward needs: the states before every 64th token (these
+    gated_scan_backward needs: the states before every 32nd token (these
     carry no gradient)."""
     args = (x, gate, input_gate, log_decay, initial_state, resets, lengths)
     _refuse_tangents(*args[:5])
