@@ -829,11 +829,6 @@ rlscan_status rlscan_gated_projection_backward(const rlscan_gated_projection_arg
                                                int64_t grad_h_stride, void *grad_x, void *grad_gate, void *grad_up,
                                                void *ws, size_t ws_bytes, rlscan_stream_t stream);
 
-/* Synchronises the stream; RLSCAN_ERR_TIMEOUT once after a wait inside a
- * projection on the current device ran out (4 s; what that call wrote is
- * incomplete). */
-rlscan_status rlscan_gated_projection_status(rlscan_stream_t stream);
-
 /* ---------------------------------------------------------------------------
  * Distillation from a teacher's top logits.  For each token, with the
  * teacher's logits over K tokens of the vocabulary and the student's over all:
@@ -886,6 +881,12 @@ rlscan_status rlscan_distill_loss_backward(const rlscan_distill_args *args, cons
  * (while a row of V logits has at most 512 KB; longer rows are read twice). */
 rlscan_status rlscan_distill_loss_and_grad(const rlscan_distill_args *args, const float *grad_loss, float *loss,
                                            float *normalizers, void *grad_logits, rlscan_stream_t stream);
+
+/* Synchronises the stream; RLSCAN_ERR_TIMEOUT once after a wait inside a gated
+ * scan or a gated projection (of a block for its copies, or for a block that
+ * shares its work) ran out on the current device: after 4 s such a kernel ends,
+ * and what its call wrote is void. */
+rlscan_status rlscan_wait_status(rlscan_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -89,7 +89,7 @@ SIGNATURES = {
     "rlscan_gated_projection": ([_P] * 3 + [_SZ, _P], _I),
     "rlscan_gated_projection_backward_workspace_bytes": ([_P], _SZ),
     "rlscan_gated_projection_backward": ([_P, _P, _I64] + [_P] * 4 + [_SZ, _P], _I),
-    "rlscan_gated_projection_status": ([_P], _I),
+    "rlscan_wait_status": ([_P], _I),
     # the distillation loss
     "rlscan_distill_loss": ([_P] * 4, _I),
     "rlscan_distill_loss_backward": ([_P] * 5, _I),

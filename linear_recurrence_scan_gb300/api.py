@@ -224,12 +224,12 @@ def _ws_for(c):
 
 def workspace_status(device=None):
     """Synchronise the current stream and raise if a kernel recorded an
-    error (a cross-block wait that timed out) in its workspace, or a matrix
-    product one on the device."""
+    error (a cross-block wait that timed out) in its workspace, or one of the
+    token policy's kernels one on the device."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     s = _stream_handle(device)
     with torch.cuda.device(device):
-        _native.check(_native.lib().rlscan_gated_projection_status(s), "rlscan_gated_projection_status")
+        _native.check(_native.lib().rlscan_wait_status(s), "rlscan_wait_status")
     ws = _ws_cache.get((device.index, s))
     if ws is None:
         torch.cuda.current_stream(device).synchronize()

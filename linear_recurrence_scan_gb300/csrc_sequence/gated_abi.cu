@@ -1,6 +1,7 @@
 // gated_abi.cu -- the extern "C" entry points of the gated recurrence: argument
 // validation, then the launchers of k_gated_scan*.cu.
 #include "abi_checks.cuh"
+#include "gated_projection.cuh"
 
 using namespace rlscan;
 using namespace rlscan::seq;
@@ -94,6 +95,13 @@ RLSCAN_API rlscan_status rlscan_gated_scan_step(const rlscan_gated_scan_args *ar
     if (conflict(a, {y, state}, {slots})) return RLSCAN_ERR_ARG_CONFLICT;
     if (!gated_reachable(a) || !reachable({state, slots, y})) return RLSCAN_ERR_MEMORY;
     return launch_gated_scan_step(a, state, P, slots, y, cs(stream));
+}
+
+RLSCAN_API rlscan_status rlscan_wait_status(rlscan_stream_t stream)
+{
+    const rlscan_status all[] = {gated_scan_status(cs(stream)), gated_scan_backward_status(cs(stream)), gated_projection_status(cs(stream))};
+    for (const rlscan_status st : all) RLSCAN_TRY(st);
+    return RLSCAN_OK;
 }
 
 }  // extern "C"

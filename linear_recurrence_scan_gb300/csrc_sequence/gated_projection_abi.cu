@@ -73,6 +73,4 @@ RLSCAN_API rlscan_status rlscan_gated_projection_backward(const rlscan_gated_pro
     return launch_gated_projection_backward(a, grad_h, grad_h_stride, grad_x, grad_gate, grad_up, ws, cs(stream));
 }
 
-RLSCAN_API rlscan_status rlscan_gated_projection_status(rlscan_stream_t stream) { return gated_projection_status(cs(stream)); }
-
 }  // extern "C"

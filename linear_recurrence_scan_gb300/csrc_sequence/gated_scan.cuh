@@ -3,7 +3,7 @@
 // blocks of a cluster that walk one row together.
 #pragma once
 
-#include "sequence.cuh"
+#include "async_copy.cuh"
 
 namespace rlscan {
 namespace seq {
@@ -68,38 +68,66 @@ struct Two {
     }
 };
 
-// A lane's two channels: the first one, whether both are the array's, and the
-// ones it reads (a lane past the last channel reads the last ones, and writes
-// nothing).
+// A lane's two channels of a block of 64: the block's first, the lane's first
+// in it, whether both are the array's, and the one it reads from (a lane past
+// the last channel reads the last ones, and writes nothing).
 template <bool VEC>
 struct Lane {
-    int64_t d, from;
+    int64_t block;
+    uint32_t d, from;
     bool on0, on1;
     int apart;
-    __device__ __forceinline__ Lane(int64_t block, int lane, int64_t D)
+    __device__ __forceinline__ Lane(int64_t number, int lane, int64_t D) : block(number * kGatedWidth)
     {
-        d = block * kGatedWidth + (VEC ? 2 * lane : lane);
-        on0 = d < D;
-        on1 = VEC ? on0 : d + 32 < D;
-        from = on0 ? d : D - (VEC ? 2 : 1);
+        const uint32_t left = D - block < kGatedWidth ? static_cast<uint32_t>(D - block) : kGatedWidth;
+        d = VEC ? 2 * lane : lane;
+        on0 = d < left;
+        on1 = VEC ? on0 : d + 32 < left;
+        from = on0 ? d : left - (VEC ? 2 : 1);
         apart = on1 ? 32 : 0;
     }
 };
+
+// The warp's number, the same for all lanes to the compiler too: addresses are
+// then a uniform base and the lane's 32-bit offset.
+__device__ __forceinline__ int warp_number() { return static_cast<int>(__reduce_max_sync(0xffffffffu, threadIdx.x >> 5)); }
+
+// A block's row, its rank among those that share it, and their steps.
+struct Walk {
+    int lane, w, rank;
+    int64_t n, len, tiles, span, steps;
+};
+template <int TILE, bool CLUSTER>
+__device__ __forceinline__ Walk walk(const rlscan_gated_scan_args &a, int ranks, int64_t &block)
+{
+    Walk k;
+    k.lane = threadIdx.x & 31;
+    k.w = warp_number();
+    k.rank = CLUSTER ? static_cast<int>(blockIdx.x % static_cast<unsigned>(ranks)) : 0;
+    const Division at = divide(CLUSTER ? blockIdx.x / static_cast<unsigned>(ranks) : blockIdx.x, (a.D + kGatedWidth - 1) / kGatedWidth);
+    k.n = at.q;
+    block = at.r;
+    k.len = row_length(a.lengths, k.n, a.T);
+    k.tiles = (a.T + TILE - 1) / TILE;
+    k.span = static_cast<int64_t>(ranks) * TILE;
+    k.steps = (k.len + k.span - 1) / k.span;
+    return k;
+}
 
 // TOK tokens from t0 on of one array; past `len` (the row's tokens) zeros
 template <class T, bool VEC, int TOK>
 __device__ __forceinline__ void fetch_tokens(Two<T, VEC> (&v)[TOK], const rlscan_array3 &a, int64_t n, int64_t t0, int64_t len, const Lane<VEC> &l)
 {
-    const T *p = static_cast<const T *>(a.data) + n * a.row_stride + t0 * a.token_stride + l.from;
+    const T *p = static_cast<const T *>(a.data) + n * a.row_stride + t0 * a.token_stride + l.block;
     const int64_t step = a.token_stride;
     if (t0 + TOK <= len) {
 #pragma unroll
-        for (int k = 0; k < TOK; ++k, p += step) v[k].load(p, l.apart);
+        for (int k = 0; k < TOK; ++k, p += step) v[k].load(p + l.from, l.apart);
     } else {
 #pragma unroll
-        for (int k = 0; k < TOK; ++k) {
+        for (int k = 0; k < TOK; ++k, p += step) {
             v[k].zero();
-            if (t0 + k < len) v[k].load(p + k * step, l.apart);
+            if (t0 + k < len) v[k].load(p + l.from, l.apart);
         }
     }
 }
@@ -133,6 +161,24 @@ __device__ __forceinline__ void store_two(T *p, f2 v, bool on0, bool on1)
     }
 }
 
+// Two neighbouring channels in shared memory
+template <class T>
+__device__ __forceinline__ f2 read_two(const char *p)
+{
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+        return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    } else {
+        const float2 h = *reinterpret_cast<const float2 *>(p);
+        return pair(h.x, h.y);
+    }
+}
+template <class T>
+__device__ __forceinline__ void write_two(char *p, f2 v)
+{
+    store_two<T, true>(reinterpret_cast<T *>(p), v, true, true);
+}
+
 // The lane's two channels of a [D] array of float32
 template <bool VEC>
 __device__ __forceinline__ f2 load_two(const float *p, bool on0, bool on1)
@@ -140,35 +186,41 @@ __device__ __forceinline__ f2 load_two(const float *p, bool on0, bool on1)
     return pair(on0 ? p[0] : 0.f, on1 ? p[VEC ? 1 : 32] : 0.f);
 }
 
-__device__ __forceinline__ f2 neg2(f2 v) { return v ^ 0x8000000080000000ull; }
+// reciprocals
+__device__ __forceinline__ f2 rcp2(f2 v)
+{
+    const float2 h = halves(v);
+    return pair(rcp_fast(h.x), rcp_fast(h.y));
+}
 
-// What a token's gates give.  a = exp(L) with L = log_decay r; the square of
-// the root, 1 - a^2 = -expm1(2 L), is its power series up to the sixth term
-// where |2 L| < 1/4 (the first omitted is below 5e-8 of the sum) and 1 - a a
-// beyond, where a's own rounding is below 5e-7 of it.  The square stays above
-// 2^-100, so that a closed gate (a = 1) gives a finite gradient: the slope of
-// the root grows without bound there, but the gate's slope vanishes faster.
+// What a channel's tokens share: log_decay times log2 e, and times -2.
+struct Decay {
+    f2 log2, twice;
+    __device__ __forceinline__ explicit Decay(f2 log_decay) : log2(mul2(log_decay, both(kLog2e))), twice(mul2(log_decay, both(-2.f))) {}
+};
+
+// What a token's gates give.  a = exp(L) with L = log_decay r.  The square of
+// the root is 1 - a^2 = -2 a sinh(L) = a Y (1 + Y^2 / 24 + Y^4 / 1920 + ...)
+// with Y = -2 L: where Y < 1/2 the first omitted term is below 5e-8 of the sum,
+// and beyond, where a^2 < 0.61, 1 - a a is right to 5e-7 by a's own rounding.
+// The square stays above 2^-100, so that a closed gate (a = 1) gives a finite
+// gradient: the slope of the root grows without bound there, but the gate's
+// slope vanishes faster.
 struct Gates {
     f2 r, i, a, root;
 };
-__device__ __forceinline__ Gates gates(f2 gate, f2 input_gate, f2 log_decay, f2 log2_decay, f2 *inverse_root = nullptr)
+__device__ __forceinline__ Gates gates(f2 gate, f2 input_gate, const Decay &d)
 {
     Gates g;
     g.r = sigmoid(gate);
     g.i = sigmoid(input_gate);
-    g.a = decay(g.r, log2_decay);
-    const f2 y = mul2(mul2(g.r, log_decay), both(2.f));
-    f2 p = fma2(y, both(1.f / 720.f), both(1.f / 120.f));
-    p = fma2(p, y, both(1.f / 24.f));
-    p = fma2(p, y, both(1.f / 6.f));
-    p = fma2(p, y, both(0.5f));
-    p = fma2(p, y, both(1.f));
-    const float2 near = halves(mul2(p, neg2(y))), far = halves(fma2(neg2(g.a), g.a, both(1.f))), yy = halves(y);
-    const float s0 = max_nan(yy.x > -0.25f ? near.x : far.x, kSquareFloor);
-    const float s1 = max_nan(yy.y > -0.25f ? near.y : far.y, kSquareFloor);
-    const f2 inv = pair(rsqrt_fast(s0), rsqrt_fast(s1));
-    g.root = mul2(pair(s0, s1), inv);
-    if (inverse_root != nullptr) *inverse_root = inv;
+    g.a = decay(g.r, d.log2);
+    const f2 y = mul2(g.r, d.twice), q = mul2(y, y);
+    const f2 p = fma2(fma2(q, both(1.f / 1920.f), both(1.f / 24.f)), q, both(1.f));
+    const float2 near = halves(mul2(mul2(g.a, y), p)), a = halves(g.a), yy = halves(y);
+    const float s0 = max_nan(yy.x < 0.5f ? near.x : fmaf(-a.x, a.x, 1.f), kSquareFloor);
+    const float s1 = max_nan(yy.y < 0.5f ? near.y : fmaf(-a.y, a.y, 1.f), kSquareFloor);
+    g.root = mul2(pair(s0, s1), pair(rsqrt_fast(s0), rsqrt_fast(s1)));
     return g;
 }
 
@@ -185,14 +237,99 @@ __device__ __forceinline__ void store_to_rank(const void *mine, int rank, float4
                  : "memory");
 }
 
+// The maps of a cluster's blocks, handed round once a step: every block sends
+// its own to all (stores that count on the receiver's barrier, so nobody waits
+// for more than the values) and waits for all.  Two buffers take turns: who
+// has all maps of a step knows that all have read those of the step before.
+struct Exchange {
+    float4 map[2][kGatedCluster][32];
+    uint64_t bar[2];
+
+    __device__ __forceinline__ void init()  // one thread; the blocks meet before the first send
+    {
+        ptx::mbar_init(&bar[0], 1);
+        ptx::mbar_init(&bar[1], 1);
+    }
+    __device__ __forceinline__ void send(int p, int mine, int to, int lane, f2 factor, f2 rest)
+    {
+        const float2 a = halves(factor), b = halves(rest);
+        uint32_t at, signal;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(&map[p][mine][lane])), "r"(to));
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(signal) : "r"(ptx::smem_u32(&bar[p])), "r"(to));
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
+                     "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "r"(signal)
+                     : "memory");
+    }
+    __device__ __forceinline__ void expect(int p, int ranks)  // one thread, once a step
+    {
+        ptx::mbar_arrive_expect_tx(&bar[p], static_cast<uint32_t>(ranks) * sizeof map[0][0]);
+    }
+    __device__ __forceinline__ void receive(int p, uint32_t parity, int *gave_up) { wait(ptx::smem_u32(&bar[p]), parity, gave_up); }
+};
+
+__device__ __forceinline__ f2 apply(f2 h, const float4 &m) { return fma2(pair(m.x, m.y), h, pair(m.z, m.w)); }
+
+// What a step's warps share of one chain (states forwards, messages backwards).
+template <bool CLUSTER>
+struct Chain {
+    float4 map[2][kGatedWarps][32];  // (factor, rest) of each warp's tokens
+    float2 last[2][32];              // the value behind a step, of a block that walks alone
+    __device__ __forceinline__ void put(int p, int w, int lane, f2 factor, f2 rest)
+    {
+        const float2 a = halves(factor), b = halves(rest);
+        map[p][w][lane] = make_float4(a.x, a.y, b.x, b.y);
+    }
+};
+
+// Behind the barrier that follows `put`: the value in front of the warp's
+// tokens, from the one in front of the step, `carry` (kept current by every
+// warp in a cluster, by the last warp alone otherwise).  turn: steps done.
+template <bool CLUSTER, bool FORWARD>
+__device__ __forceinline__ f2 in_front(Chain<CLUSTER> &c, Exchange *ex, int64_t turn, int w, int lane, int rank, int ranks, f2 &carry,
+                                       int *gave_up)
+{
+    const int p = static_cast<int>(turn & 1);
+    f2 h = carry;
+    if constexpr (CLUSTER) {
+        f2 factor = both(1.f), rest = both(0.f);  // the block's map
+#pragma unroll
+        for (int i = 0; i < kGatedWarps; ++i) {
+            const float4 m = c.map[p][FORWARD ? i : kGatedWarps - 1 - i][lane];
+            factor = mul2(factor, pair(m.x, m.y));
+            rest = apply(rest, m);
+        }
+        if (w < ranks) ex->send(p, rank, w, lane, factor, rest);
+        if (threadIdx.x == 0) ex->expect(p, ranks);
+        ex->receive(p, static_cast<uint32_t>(turn >> 1) & 1u, gave_up);
+#pragma unroll 1
+        for (int i = 0; i < ranks; ++i) {
+            const int q = FORWARD ? i : ranks - 1 - i;
+            if (q == rank) h = carry;
+            carry = apply(carry, ex->map[p][q][lane]);
+        }
+    } else if (turn > 0) {
+        const float2 f = c.last[p ^ 1][lane];
+        h = pair(f.x, f.y);
+    }
+    if constexpr (FORWARD) {
+#pragma unroll 1
+        for (int q = 0; q < w; ++q) h = apply(h, c.map[p][q][lane]);
+    } else {
+#pragma unroll 1
+        for (int q = kGatedWarps - 1; q > w; --q) h = apply(h, c.map[p][q][lane]);
+    }
+    return h;
+}
+static_assert(kGatedWarps >= kGatedCluster);  // a warp sends to one block
+
 __host__ __device__ inline int64_t gated_marks(int64_t T) { return (T + RLSCAN_GATED_SCAN_CHECKPOINT - 1) / RLSCAN_GATED_SCAN_CHECKPOINT; }
 
 // Blocks of a cluster that share a row: as many as make the fewest steps one
 // after the other, counting the rounds in which clusters of that size become
 // resident.  A row split over blocks costs each step an exchange, taken as a
 // quarter of a step.
-template <class T, bool VEC, class K>
-inline int gated_cluster(K kernel, int64_t chains, int64_t tokens, int tile)
+template <class T, int KIND, class K>
+inline int gated_cluster(K kernel, int64_t chains, int64_t tokens, int tile, size_t smem)
 {
     static PerDevice resident[kGatedCluster + 1];
     const int64_t tiles = ceil_div(tokens, tile);
@@ -204,6 +341,7 @@ inline int gated_cluster(K kernel, int64_t chains, int64_t tokens, int tile)
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>(c));
             cfg.blockDim = dim3(32 * kGatedWarps);
+            cfg.dynamicSmemBytes = smem;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
             attr[0].val.clusterDim.x = static_cast<unsigned>(c);
@@ -221,12 +359,13 @@ inline int gated_cluster(K kernel, int64_t chains, int64_t tokens, int tile)
 }
 
 template <class K, class... Args>
-inline rlscan_status launch_cluster(K kernel, int64_t grid, int threads, int cluster, cudaStream_t stream, Args... args)
+inline rlscan_status launch_cluster(K kernel, int64_t grid, int threads, size_t smem, int cluster, cudaStream_t stream, Args... args)
 {
     if (grid > 0x7fffffff) return RLSCAN_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -243,11 +382,36 @@ inline rlscan_status launch_cluster(K kernel, int64_t grid, int threads, int clu
     return RLSCAN_OK;
 }
 
-// Whether pairs of channels are aligned in every array added to the chunk
+// The kernel for arrays whose addresses and strides are `bits`: Tiles where
+// all are multiples of 16 bytes (tensor maps), Pairs where two channels are,
+// else Values.
+enum class Access { Values, Pairs, Tiles };
 template <class T>
-inline bool gated_pairs(const Chunk &c, int64_t D)
+inline Access gated_access(std::initializer_list<const rlscan_array3 *> in, std::initializer_list<const void *> out,
+                           std::initializer_list<const void *> floats, int64_t N, int64_t T_, int64_t D)
 {
-    return D % 2 == 0 && c.bits % (2 * sizeof(T)) == 0;
+    uint64_t bits = 0, wide = 0;
+    bool plain = T_ < 0x7fffffff - 1024 && N < 0x7fffffff;  // coordinates are 32-bit
+    for (const rlscan_array3 *a : in) {
+        const int64_t row = N > 1 ? a->row_stride : 0, token = T_ > 1 ? a->token_stride : 0;
+        bits |= reinterpret_cast<uintptr_t>(a->data) | static_cast<uint64_t>(row * sizeof(T)) | static_cast<uint64_t>(token * sizeof(T));
+        plain = plain && (N <= 1 || (row > 0 && row < (int64_t{1} << 36))) && (T_ <= 1 || (token > 0 && token < (int64_t{1} << 36)));
+    }
+    for (const void *p : out) bits |= reinterpret_cast<uintptr_t>(p);
+    for (const void *p : floats) wide |= reinterpret_cast<uintptr_t>(p);
+    if (D % 2 != 0 || bits % (2 * sizeof(T)) != 0 || wide % 8 != 0) return Access::Values;
+    return plain && bits % 16 == 0 && D * sizeof(T) % 16 == 0 ? Access::Tiles : Access::Pairs;
+}
+
+// A map of [N,T,D] for boxes of 64 channels x `tokens`
+template <class T>
+inline bool gated_map(CUtensorMap *m, const void *p, int64_t row_stride, int64_t token_stride, int64_t N, int64_t T_, int64_t D, uint32_t tokens)
+{
+    constexpr int64_t e = sizeof(T);
+    const int64_t token = T_ > 1 ? token_stride * e : D * e, row = N > 1 ? row_stride * e : token * T_;
+    const int64_t extents[3] = {D, T_, N}, strides[2] = {token, row};
+    const uint32_t box[3] = {kGatedWidth, tokens, 1};
+    return encode_map(m, p, sizeof(T) == 2, 3, extents, strides, box, false);
 }
 
 }  // namespace seq

@@ -355,7 +355,7 @@ rlscan_status run(const rlscan_distill_args &a, const DistillOut &o, Plan p, cud
         return launch_overlapped(distill_kernel<T, 512, kUnits, PART, false>, rows * p.ranks, 512, 0, s, a, o, p.ranks);
     } else {
         if (p.ranks > 1)
-            return launch_cluster(distill_kernel<T, 512, kUnits, PART, true>, rows * p.ranks, 512, p.ranks, s, a, o, p.ranks);
+            return launch_cluster(distill_kernel<T, 512, kUnits, PART, true>, rows * p.ranks, 512, 0, p.ranks, s, a, o, p.ranks);
         return launch_overlapped(distill_kernel<T, 512, kUnits, PART, false>, rows, 512, 0, s, a, o, 1);
     }
 }

@@ -140,7 +140,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int64_t tm, tn;
             place(tile, tm, tn);
             for (int64_t s = 0; s < k.steps; ++s) {
-                if (!umma::wait(ptx::smem_u32(&empty[stage]), phase, &gave_up)) break;
+                if (!wait(ptx::smem_u32(&empty[stage]), phase, &gave_up)) break;
                 const uint32_t bar = umma::of_rank(ptx::smem_u32(&full[stage]), 0);
                 const uint32_t a = smem + stage * kStageBytes, b = a + kTileBytes;
                 if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
@@ -167,16 +167,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // The block stays until the products have taken its last copies.
         for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-            if (!umma::wait(ptx::smem_u32(&empty[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u, &gave_up)) break;
+            if (!wait(ptx::smem_u32(&empty[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u, &gave_up)) break;
     } else if (warp == 1 && lane == 0 && rank == 0) {  // products
         constexpr uint32_t kInstruction = umma::instruction(kAMn, kBMn, 256, 256);
         uint32_t stage = 0, phase = 0, buffer = 0, buffer_phase = 1;
         for (int64_t tile = pair; tile < tiles; tile += pairs) {
-            if (!umma::wait(ptx::smem_u32(&sums_empty[buffer]), buffer_phase, &gave_up)) break;
+            if (!wait(ptx::smem_u32(&sums_empty[buffer]), buffer_phase, &gave_up)) break;
             umma::fence_after();
             bool fine = true;
             for (int64_t s = 0; s < k.steps && fine; ++s) {
-                fine = umma::wait(ptx::smem_u32(&full[stage]), phase, &gave_up);
+                fine = wait(ptx::smem_u32(&full[stage]), phase, &gave_up);
                 if (!fine) break;
                 umma::fence_after();
                 const uint32_t a = smem + stage * kStageBytes, b = a + kTileBytes;
@@ -202,7 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int which = JOB == Job::Weights && tm >= half ? 1 : 0;
             const int64_t row = (tm - which * half) * 256 + rank * 128 + part * 32 + lane;
             const int64_t rows = JOB == Job::Weights ? k.F : k.M;
-            if (!umma::wait(ptx::smem_u32(&sums_full[buffer]), phase, &gave_up)) break;
+            if (!wait(ptx::smem_u32(&sums_full[buffer]), phase, &gave_up)) break;
             umma::fence_after();
             const uint32_t at = tmem + buffer * 256 + (static_cast<uint32_t>(part * 32) << 16);
             if constexpr (kGates) {
@@ -255,12 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     umma::fence_before();
     __syncthreads();
-    if (gave_up != 0) {  // copies and products in flight take microseconds: they end before the block does
-        if (threadIdx.x == 0) atomicExch(&g_timed_out, 1u);
-        const uint64_t start = ptx::globaltimer_ns();
-        while (ptx::globaltimer_ns() - start < 1'000'000) {
-        }
-    }
+    leave(&gave_up, &g_timed_out);
     __syncwarp();
     cluster_arrive();
     cluster_wait();  // neither block leaves while the other may still reach it
@@ -442,17 +437,7 @@ rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_arg
     return st;
 }
 
-rlscan_status gated_projection_status(cudaStream_t s)
-{
-    unsigned int seen = 0;
-    if (!ok(cudaMemcpyFromSymbolAsync(&seen, g_timed_out, sizeof seen, 0, cudaMemcpyDeviceToHost, s)) || !ok(cudaStreamSynchronize(s)))
-        return RLSCAN_ERR_CUDA;
-    if (seen == 0) return RLSCAN_OK;
-    const unsigned int none = 0;
-    if (!ok(cudaMemcpyToSymbolAsync(g_timed_out, &none, sizeof none, 0, cudaMemcpyHostToDevice, s)) || !ok(cudaStreamSynchronize(s)))
-        return RLSCAN_ERR_CUDA;
-    return RLSCAN_ERR_TIMEOUT;
-}
+rlscan_status gated_projection_status(cudaStream_t s) { return take_flag(g_timed_out, s); }
 
 }  // namespace seq
 }  // namespace rlscan

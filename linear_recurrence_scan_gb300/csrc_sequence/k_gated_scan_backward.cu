@@ -10,6 +10,8 @@ namespace rlscan {
 namespace seq {
 namespace {
 
+__device__ unsigned int g_timed_out;  // a wait ran out on this device
+
 struct BackwardArgs {
     rlscan_array3 grad_y;
     const float *grad_final, *checkpoints;
@@ -17,207 +19,372 @@ struct BackwardArgs {
     float *parts;  // [N * ranks][D]: each block's share of dlog_decay
 };
 
-constexpr int kBackTile = RLSCAN_GATED_SCAN_CHECKPOINT;  // tokens of a step
+constexpr int kBackTile = RLSCAN_GATED_SCAN_CHECKPOINT;  // tokens of a step of the untiled kernel
 
-// The forward kernel's walk from the last step to the first, in steps of 32
-// tokens, four of a warp, with two affine maps of a warp's tokens: of the
-// state before them and of the message behind them (both have the same factor,
-// the product of the decays).  The states start again from the checkpoint in
-// front of the step, so only the messages are handed between steps.
+// The forward kernel's walk from the last step to the first, with two affine
+// maps of a warp's tokens: of the state before them and of the message behind
+// them (both have the same factor, the product of the decays).  The states
+// start again from the checkpoint in front of the step, so only the messages
+// are handed between steps.
+// What a token adds: dx, the gates' gradients, log_decay's share; and the
+// message to the token in front of it.
+struct TokenGrads {
+    f2 x, gate, input_gate, share;
+};
+__device__ __forceinline__ TokenGrads token_grads(const Gates &v, f2 keep, f2 x, f2 gy, f2 before, f2 log_decay, f2 &m)
+{
+    const f2 one = both(1.f), minus = both(-1.f), G = add2(gy, m);
+    m = mul2(keep, G);
+    // i x a^2 / root: what the decay takes from the input
+    const f2 taken = mul2(mul2(mul2(v.i, x), rcp2(v.root)), mul2(v.a, v.a));
+    TokenGrads t;
+    t.share = mul2(mul2(G, v.r), fma2(taken, minus, mul2(keep, before)));
+    t.x = mul2(G, mul2(v.root, v.i));
+    t.gate = mul2(mul2(t.share, log_decay), fma2(v.r, minus, one));
+    t.input_gate = mul2(mul2(t.x, x), fma2(v.i, minus, one));
+    return t;
+}
+
+// Behind the last step: zeros for tiles of padding, the initial state's
+// gradient, the block's share of dlog_decay (its warps' in order).
+template <class T, bool VEC, int TILE, bool CLUSTER>
+__device__ __forceinline__ void finish(const rlscan_gated_scan_args &a, const BackwardArgs &o, const Walk &k, int ranks, const Lane<VEC> &l,
+                                       f2 carry, f2 sum, Chain<CLUSTER> &chain)
+{
+    constexpr int TOK = TILE / kGatedWarps;
+    for (int64_t tile = k.steps * ranks + k.rank; tile < k.tiles; tile += ranks) {
+        const int64_t t0 = tile * TILE + k.w * TOK;
+        for (int i = 0; i < TOK; ++i) {
+            if (t0 + i >= a.T) break;
+            const int64_t at_token = (k.n * a.T + t0 + i) * a.D + l.block + l.d;
+            store_two<T, VEC>(static_cast<T *>(o.g.x) + at_token, both(0.f), l.on0, l.on1);
+            store_two<T, VEC>(static_cast<T *>(o.g.gate) + at_token, both(0.f), l.on0, l.on1);
+            store_two<T, VEC>(static_cast<T *>(o.g.input_gate) + at_token, both(0.f), l.on0, l.on1);
+        }
+    }
+    if (k.rank == 0 && k.w == 0 && o.g.initial_state != nullptr)
+        store_two<float, VEC>(o.g.initial_state + k.n * a.D + l.block + l.d, carry, l.on0, l.on1);
+    if (o.parts == nullptr) return;
+    __syncthreads();
+    chain.put(0, k.w, k.lane, sum, sum);
+    __syncthreads();
+    if (k.w == 0) {
+        f2 all = both(0.f);
+#pragma unroll
+        for (int q = 0; q < kGatedWarps; ++q) all = add2(all, pair(chain.map[0][q][k.lane].x, chain.map[0][q][k.lane].y));
+        store_two<float, VEC>(o.parts + (k.n * ranks + k.rank) * a.D + l.block + l.d, all, l.on0, l.on1);
+    }
+}
+
+// Arrays of any alignment: the next step's values are loaded into registers
+// while this one's are worked on.
 template <class T, bool VEC, bool CLUSTER>
 __global__ void __launch_bounds__(32 * kGatedWarps, 2)
     backward_kernel(const __grid_constant__ rlscan_gated_scan_args a, const __grid_constant__ BackwardArgs o, int ranks)
 {
-    constexpr int TOK = kBackTile / kGatedWarps;
-    __shared__ float4 state_map[2][kGatedWarps][32], message_map[2][kGatedWarps][32];
-    __shared__ float4 of_rank[2][CLUSTER ? kGatedCluster : 1][32];
-    __shared__ float2 last[2][32];  // the message out of the step
+    constexpr int TILE = kBackTile, TOK = TILE / kGatedWarps;
+    __shared__ float4 state_map[2][kGatedWarps][32];
+    __shared__ Chain<CLUSTER> chain;
+    __shared__ std::conditional_t<CLUSTER, Exchange, char> exchange;
+    __shared__ int gave_up;
     ptx::pdl_trigger_dependents();
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        if constexpr (CLUSTER) exchange.init(), ptx::fence_mbar_init();
+    }
+    __syncthreads();
     if constexpr (CLUSTER) cluster_arrive();
     ptx::pdl_wait_prerequisites();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int rank = CLUSTER ? static_cast<int>(blockIdx.x % static_cast<unsigned>(ranks)) : 0;
-    const Division at = divide(CLUSTER ? blockIdx.x / static_cast<unsigned>(ranks) : blockIdx.x, (a.D + kGatedWidth - 1) / kGatedWidth);
-    const int64_t n = at.q;
-    const Lane<VEC> l(at.r, lane, a.D);
-    const int64_t len = row_length(a.lengths, n, a.T), tiles = gated_marks(a.T);
-    const int64_t span = static_cast<int64_t>(ranks) * kBackTile, steps = (len + span - 1) / span;
-    const f2 log_decay = load_two<VEC>(a.log_decay + l.d, l.on0, l.on1), log2_decay = mul2(log_decay, both(kLog2e));
-    f2 carry = o.grad_final != nullptr ? load_two<VEC>(o.grad_final + n * a.D + l.d, l.on0, l.on1) : both(0.f);
+    int64_t block;
+    const Walk k = walk<TILE, CLUSTER>(a, ranks, block);
+    const Lane<VEC> l(block, k.lane, a.D);
+    const f2 log_decay = load_two<VEC>(a.log_decay + l.block + l.d, l.on0, l.on1);
+    const Decay decays(log_decay);
+    f2 carry = o.grad_final != nullptr ? load_two<VEC>(o.grad_final + k.n * a.D + l.block + l.d, l.on0, l.on1) : both(0.f);
     f2 sum = both(0.f);  // the lane's share of dlog_decay
     Two<T, VEC> x[TOK], g[TOK], ig[TOK], gy[TOK];
     Two<float, VEC> mark;
     uint32_t reset = 0;
     auto fetch = [&](int64_t tile) {
-        const int64_t t0 = tile * kBackTile + w * TOK;
-        fetch_tokens(g, a.gate, n, t0, len, l);
-        fetch_tokens(ig, a.input_gate, n, t0, len, l);
-        fetch_tokens(x, a.x, n, t0, len, l);
-        fetch_tokens(gy, o.grad_y, n, t0, len, l);
-        reset = fetch_resets<TOK>(a.resets, n * a.T, t0, len, lane);
+        const int64_t t0 = tile * TILE + k.w * TOK;
+        fetch_tokens(g, a.gate, k.n, t0, k.len, l);
+        fetch_tokens(ig, a.input_gate, k.n, t0, k.len, l);
+        fetch_tokens(x, a.x, k.n, t0, k.len, l);
+        fetch_tokens(gy, o.grad_y, k.n, t0, k.len, l);
+        reset = fetch_resets<TOK>(a.resets, k.n * a.T, t0, k.len, k.lane);
         mark.zero();
-        if (tile < tiles) mark.load(o.checkpoints + (n * tiles + tile) * a.D + l.from, l.apart);
+        if (tile < k.tiles) mark.load(o.checkpoints + (k.n * k.tiles + tile) * a.D + l.block + l.from, l.apart);
     };
-    if (steps > 0) fetch((steps - 1) * ranks + rank);
+    if (k.steps > 0) fetch((k.steps - 1) * ranks + k.rank);
     if constexpr (CLUSTER) cluster_wait();
-    auto factor = [](const float4 &m) { return pair(m.x, m.y); };
-    auto apply = [](f2 h, const float4 &m) { return fma2(pair(m.x, m.y), h, pair(m.z, m.w)); };
-    T *gx = static_cast<T *>(o.g.x), *gg = static_cast<T *>(o.g.gate), *gi = static_cast<T *>(o.g.input_gate);
-    for (int64_t s = steps - 1; s >= 0; --s) {
-        const int p = static_cast<int>(s & 1);
-        const int64_t tile = s * ranks + rank, t0 = tile * kBackTile + w * TOK;
+    for (int64_t s = k.steps - 1; s >= 0; --s) {
+        const int64_t turn = k.steps - 1 - s, tile = s * ranks + k.rank, t0 = tile * TILE + k.w * TOK;
+        const int p = static_cast<int>(turn & 1);
         Gates v[TOK];
         f2 xs[TOK], gs[TOK], keep[TOK], b[TOK];
         const uint32_t cut = reset;
         f2 state = mark.get();
 #pragma unroll
-        for (int k = 0; k < TOK; ++k) {
-            v[k] = gates(g[k].get(), ig[k].get(), log_decay, log2_decay);
-            xs[k] = x[k].get();
-            gs[k] = gy[k].get();
-            b[k] = mul2(mul2(v[k].root, v[k].i), xs[k]);
-            keep[k] = v[k].a;
+        for (int i = 0; i < TOK; ++i) {
+            v[i] = gates(g[i].get(), ig[i].get(), decays);
+            xs[i] = x[i].get();
+            gs[i] = gy[i].get();
+            b[i] = mul2(mul2(v[i].root, v[i].i), xs[i]);
+            keep[i] = v[i].a;
         }
         if (cut != 0) {
 #pragma unroll
-            for (int k = 0; k < TOK; ++k)
-                if ((cut >> k & 1u) != 0u) keep[k] = both(0.f);
+            for (int i = 0; i < TOK; ++i)
+                if ((cut >> i & 1u) != 0u) keep[i] = both(0.f);
         }
-        const bool pad = t0 + TOK > len;
+        const bool pad = t0 + TOK > k.len;
         if (pad) {  // padding hands state and message on
 #pragma unroll
-            for (int k = 0; k < TOK; ++k)
-                if (t0 + k >= len) keep[k] = both(1.f), b[k] = gs[k] = xs[k] = both(0.f);
+            for (int i = 0; i < TOK; ++i)
+                if (t0 + i >= k.len) keep[i] = both(1.f), b[i] = gs[i] = xs[i] = both(0.f);
         }
         if (s > 0) fetch(tile - ranks);
         f2 A = keep[0], B = b[0], M = mul2(keep[TOK - 1], gs[TOK - 1]);
 #pragma unroll
-        for (int k = 1; k < TOK; ++k) {
-            A = mul2(A, keep[k]);
-            B = fma2(keep[k], B, b[k]);
-            M = mul2(keep[TOK - 1 - k], add2(gs[TOK - 1 - k], M));
+        for (int i = 1; i < TOK; ++i) {
+            A = mul2(A, keep[i]);
+            B = fma2(keep[i], B, b[i]);
+            M = mul2(keep[TOK - 1 - i], add2(gs[TOK - 1 - i], M));
         }
         {
-            const float2 fa = halves(A), fb = halves(B), fm = halves(M);
-            state_map[p][w][lane] = make_float4(fa.x, fa.y, fb.x, fb.y);
-            message_map[p][w][lane] = make_float4(fa.x, fa.y, fm.x, fm.y);
+            const float2 fa = halves(A), fb = halves(B);
+            state_map[p][k.w][k.lane] = make_float4(fa.x, fa.y, fb.x, fb.y);
         }
+        chain.put(p, k.w, k.lane, A, M);
         __syncthreads();
-        f2 m = carry;
-        if constexpr (CLUSTER) {
-            f2 BA = both(1.f), BM = both(0.f);
-#pragma unroll
-            for (int q = kGatedWarps - 1; q >= 0; --q) {
-                const float4 f = message_map[p][q][lane];
-                BA = mul2(BA, factor(f));
-                BM = apply(BM, f);
-            }
-            const float2 fa = halves(BA), fm = halves(BM);
-            for (int q = w; q < ranks; q += kGatedWarps)
-                store_to_rank(&of_rank[p][rank][lane], q, make_float4(fa.x, fa.y, fm.x, fm.y));
-            cluster_arrive();
-            cluster_wait();
-            for (int q = ranks - 1; q >= 0; --q) {
-                if (q == rank) m = carry;
-                carry = apply(carry, of_rank[p][q][lane]);
-            }
-        } else if (s + 1 < steps) {
-            const float2 f = last[p ^ 1][lane];
-            m = pair(f.x, f.y);
-        }
+        Exchange *ex = nullptr;
+        if constexpr (CLUSTER) ex = &exchange;
+        f2 m = in_front<CLUSTER, false>(chain, ex, turn, k.w, k.lane, k.rank, ranks, carry, &gave_up);
 #pragma unroll 1
-        for (int q = kGatedWarps - 1; q > w; --q) m = apply(m, message_map[p][q][lane]);
-#pragma unroll 1
-        for (int q = 0; q < w; ++q) state = apply(state, state_map[p][q][lane]);
+        for (int q = 0; q < k.w; ++q) state = apply(state, state_map[p][q][k.lane]);
         f2 before[TOK];  // the state before each token
 #pragma unroll
-        for (int k = 0; k < TOK; ++k) {
-            before[k] = state;
-            state = fma2(keep[k], state, b[k]);
+        for (int i = 0; i < TOK; ++i) {
+            before[i] = state;
+            state = fma2(keep[i], state, b[i]);
         }
-        const int64_t at_last = (n * a.T + t0 + TOK - 1) * a.D + l.d;
-        T *px = gx + at_last, *pg = gg + at_last, *pi = gi + at_last;
+        const int64_t at_last = (k.n * a.T + t0 + TOK - 1) * a.D + l.block;
+        T *px = static_cast<T *>(o.g.x) + at_last, *pg = static_cast<T *>(o.g.gate) + at_last, *pi = static_cast<T *>(o.g.input_gate) + at_last;
 #pragma unroll
-        for (int k = TOK - 1; k >= 0; --k, px -= a.D, pg -= a.D, pi -= a.D) {
-            const f2 G = add2(gs[k], m), one = both(1.f);
-            m = mul2(keep[k], G);
-            const f2 moved = mul2(v[k].i, xs[k]);
-            const float2 rt = halves(v[k].root);
-            const f2 slope = mul2(mul2(v[k].a, v[k].a), pair(rcp_fast(rt.x), rcp_fast(rt.y)));  // of the root, negated
-            f2 dL = mul2(mul2(G, fma2(keep[k], before[k], neg2(mul2(moved, slope)))), v[k].r);  // times r: log_decay's share
-            f2 dx = mul2(G, mul2(v[k].root, v[k].i));
-            f2 dg = mul2(mul2(dL, log_decay), fma2(neg2(v[k].r), one, one));
-            f2 di = mul2(mul2(dx, xs[k]), fma2(neg2(v[k].i), one, one));
+        for (int i = TOK - 1; i >= 0; --i, px -= a.D, pg -= a.D, pi -= a.D) {
+            TokenGrads t = token_grads(v[i], keep[i], xs[i], gs[i], before[i], log_decay, m);
             bool on0 = l.on0, on1 = l.on1;
             if (pad) {
-                if (t0 + k >= len) dL = dx = dg = di = both(0.f);
-                on0 = on0 && t0 + k < a.T, on1 = on1 && t0 + k < a.T;
+                if (t0 + i >= k.len) t.x = t.gate = t.input_gate = t.share = both(0.f);
+                on0 = on0 && t0 + i < a.T, on1 = on1 && t0 + i < a.T;
             }
-            sum = add2(sum, dL);
-            store_two<T, VEC>(px, dx, on0, on1);
-            store_two<T, VEC>(pg, dg, on0, on1);
-            store_two<T, VEC>(pi, di, on0, on1);
+            sum = add2(sum, t.share);
+            store_two<T, VEC>(px + l.d, t.x, on0, on1);
+            store_two<T, VEC>(pg + l.d, t.gate, on0, on1);
+            store_two<T, VEC>(pi + l.d, t.input_gate, on0, on1);
         }
         if constexpr (!CLUSTER) {
-            if (w == 0) {
-                last[p][lane] = halves(m);
+            if (k.w == 0) {
+                chain.last[p][k.lane] = halves(m);
                 carry = m;
             }
         }
     }
-    for (int64_t tile = steps * ranks + rank; tile < tiles; tile += ranks) {  // padding alone
-        const int64_t t0 = tile * kBackTile + w * TOK;
-        for (int k = 0; k < TOK; ++k) {
-            if (t0 + k >= a.T) break;
-            const int64_t at_token = (n * a.T + t0 + k) * a.D + l.d;
-            store_two<T, VEC>(gx + at_token, both(0.f), l.on0, l.on1);
-            store_two<T, VEC>(gg + at_token, both(0.f), l.on0, l.on1);
-            store_two<T, VEC>(gi + at_token, both(0.f), l.on0, l.on1);
-        }
+    finish<T, VEC, TILE, CLUSTER>(a, o, k, ranks, l, carry, sum, chain);
+    leave(&gave_up, &g_timed_out);
+}
+
+// Arrays that tensor maps take: the inputs of a step come into shared memory
+// while the step behind it is worked on, and what the gradients need again (x,
+// grad_y) is read again from there.  The gradients leave through shared memory.
+struct BackwardMaps {
+    CUtensorMap x, gate, input_gate, grad_y, dx, dgate, dinput_gate;
+};
+template <class T>
+struct BackwardTile {
+    static constexpr int TOK = 16 / static_cast<int>(sizeof(T)), TOKENS = TOK * kGatedWarps;
+    static constexpr uint32_t BYTES = TOKENS * kGatedWidth * sizeof(T);  // of one array
+    static constexpr size_t SMEM = 2 * 4 * BYTES + 3 * BYTES + 128;      // two stages, three gradients
+};
+
+template <class T, bool CLUSTER>
+__global__ void __launch_bounds__(32 * kGatedWarps, 2)
+    tiled_backward_kernel(const __grid_constant__ rlscan_gated_scan_args a, const __grid_constant__ BackwardArgs o,
+                          const __grid_constant__ BackwardMaps maps, int ranks)
+{
+    constexpr int TOK = BackwardTile<T>::TOK, TILE = BackwardTile<T>::TOKENS, STEP = kGatedWidth * sizeof(T);
+    constexpr uint32_t BYTES = BackwardTile<T>::BYTES;
+    extern __shared__ char raw[];
+    __shared__ float4 state_map[2][kGatedWarps][32];
+    __shared__ Chain<CLUSTER> chain;
+    __shared__ std::conditional_t<CLUSTER, Exchange, char> exchange;
+    __shared__ uint64_t full[2];
+    __shared__ int gave_up;
+    ptx::pdl_trigger_dependents();
+    char *stages = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 127) & ~static_cast<uintptr_t>(127));
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        ptx::mbar_init(&full[0], 1);
+        ptx::mbar_init(&full[1], 1);
+        if constexpr (CLUSTER) exchange.init();
+        ptx::fence_mbar_init();
     }
-    if (rank == 0 && w == 0 && o.g.initial_state != nullptr)
-        store_two<float, VEC>(o.g.initial_state + n * a.D + l.d, carry, l.on0, l.on1);
-    if (o.parts != nullptr) {  // the warps' shares in order
-        __syncthreads();
-        state_map[0][w][lane].x = halves(sum).x;
-        state_map[0][w][lane].y = halves(sum).y;
-        __syncthreads();
-        if (w == 0) {
-            f2 all = both(0.f);
+    __syncthreads();
+    if constexpr (CLUSTER) cluster_arrive();
+    ptx::pdl_wait_prerequisites();
+    int64_t block;
+    const Walk k = walk<TILE, CLUSTER>(a, ranks, block);
+    const Lane<true> l(block, k.lane, a.D);
+    const int x0 = static_cast<int>(l.block), row = static_cast<int>(k.n);
+    auto fetch = [&](int64_t turn) {  // by one thread
+        const int st = static_cast<int>(turn & 1), t = static_cast<int>(((k.steps - 1 - turn) * ranks + k.rank) * TILE);
+        const uint32_t at = ptx::smem_u32(stages) + st * 4 * BYTES, bar = ptx::smem_u32(&full[st]);
+        ptx::mbar_arrive_expect_tx(&full[st], 4 * BYTES);
+        load_box3(at, &maps.gate, x0, t, row, bar);
+        load_box3(at + BYTES, &maps.input_gate, x0, t, row, bar);
+        load_box3(at + 2 * BYTES, &maps.x, x0, t, row, bar);
+        load_box3(at + 3 * BYTES, &maps.grad_y, x0, t, row, bar);
+    };
+    const int64_t marks = gated_marks(a.T);
+    f2 mark = both(0.f);
+    uint32_t reset = 0;
+    auto look = [&](int64_t turn) {  // the step's checkpoint and resets
+        const int64_t t = ((k.steps - 1 - turn) * ranks + k.rank) * TILE;
+        reset = fetch_resets<TOK>(a.resets, k.n * a.T, t + k.w * TOK, k.len, k.lane);
+        const int64_t i = t / RLSCAN_GATED_SCAN_CHECKPOINT;
+        mark = load_two<true>(o.checkpoints + (k.n * marks + i) * a.D + l.block + l.d, i < marks && l.on0, i < marks && l.on1);
+    };
+    const f2 log_decay = load_two<true>(a.log_decay + l.block + l.d, l.on0, l.on1);
+    const Decay decays(log_decay);
+    f2 carry = o.grad_final != nullptr ? load_two<true>(o.grad_final + k.n * a.D + l.block + l.d, l.on0, l.on1) : both(0.f);
+    f2 sum = both(0.f);  // the lane's share of dlog_decay
+    if (k.steps > 0) {
+        if (threadIdx.x == 0) fetch(0);
+        look(0);
+    }
+    if constexpr (CLUSTER) cluster_wait();
+    const uint32_t mine = k.w * TOK * STEP + l.d * sizeof(T);  // of the lane, in a tile
+    char *out = stages + 2 * 4 * BYTES;
+    for (int64_t turn = 0; turn < k.steps; ++turn) {
+        const int64_t t0 = ((k.steps - 1 - turn) * ranks + k.rank) * TILE + k.w * TOK;
+        const int p = static_cast<int>(turn & 1);
+        wait(ptx::smem_u32(&full[p]), static_cast<uint32_t>(turn >> 1) & 1u, &gave_up);
+        char *in = stages + p * 4 * BYTES + mine;
+        const bool pad = t0 + TOK > k.len;
+        if (pad) {  // x and grad_y of padding count 0
+#pragma unroll 1
+            for (int i = 0; i < TOK; ++i)
+                if (t0 + i >= k.len) {
+                    write_two<T>(in + 2 * BYTES + i * STEP, both(0.f));
+                    write_two<T>(in + 3 * BYTES + i * STEP, both(0.f));
+                }
+            fence_async();  // in front of the copy that takes the stage next
+        }
+        Gates v[TOK];
+        const uint32_t cut = reset;
+        f2 state = mark, A = both(1.f), B = both(0.f), M = both(0.f);
 #pragma unroll
-            for (int q = 0; q < kGatedWarps; ++q) all = add2(all, factor(state_map[0][q][lane]));
-            store_two<float, VEC>(o.parts + (n * ranks + rank) * a.D + l.d, all, l.on0, l.on1);
+        for (int i = 0; i < TOK; ++i) v[i] = gates(read_two<T>(in + i * STEP), read_two<T>(in + BYTES + i * STEP), decays);
+        auto keep = [&](int i) { return (cut >> i & 1u) != 0u ? both(0.f) : v[i].a; };
+        if (pad) {  // and hands state and message on
+#pragma unroll
+            for (int i = 0; i < TOK; ++i)
+                if (t0 + i >= k.len) v[i].a = both(1.f), v[i].root = both(0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < TOK; ++i) {
+            A = mul2(A, keep(i));
+            B = fma2(keep(i), B, mul2(mul2(v[i].root, v[i].i), read_two<T>(in + 2 * BYTES + i * STEP)));
+        }
+#pragma unroll
+        for (int i = TOK - 1; i >= 0; --i) M = mul2(keep(i), add2(read_two<T>(in + 3 * BYTES + i * STEP), M));
+        {
+            const float2 fa = halves(A), fb = halves(B);
+            state_map[p][k.w][k.lane] = make_float4(fa.x, fa.y, fb.x, fb.y);
+        }
+        chain.put(p, k.w, k.lane, A, M);
+        __syncthreads();  // the step behind has been worked on: its stage takes the step in front
+        if (turn + 1 < k.steps) {
+            if (threadIdx.x == 0) fetch(turn + 1);
+            look(turn + 1);
+        }
+        Exchange *ex = nullptr;
+        if constexpr (CLUSTER) ex = &exchange;
+        f2 m = in_front<CLUSTER, false>(chain, ex, turn, k.w, k.lane, k.rank, ranks, carry, &gave_up);
+#pragma unroll 1
+        for (int q = 0; q < k.w; ++q) state = apply(state, state_map[p][q][k.lane]);
+        f2 before[TOK];  // the state before each token
+#pragma unroll
+        for (int i = 0; i < TOK; ++i) {
+            before[i] = state;
+            state = fma2(keep(i), state, mul2(mul2(v[i].root, v[i].i), read_two<T>(in + 2 * BYTES + i * STEP)));
+        }
+        if (k.lane == 0) stores_read();  // the step behind has left the warp's part
+        __syncwarp();
+#pragma unroll
+        for (int i = TOK - 1; i >= 0; --i) {
+            TokenGrads t = token_grads(v[i], keep(i), read_two<T>(in + 2 * BYTES + i * STEP), read_two<T>(in + 3 * BYTES + i * STEP),
+                                       before[i], log_decay, m);
+            if (pad && t0 + i >= k.len) t.x = t.gate = t.input_gate = t.share = both(0.f);
+            sum = add2(sum, t.share);
+            write_two<T>(out + mine + i * STEP, t.x);
+            write_two<T>(out + BYTES + mine + i * STEP, t.gate);
+            write_two<T>(out + 2 * BYTES + mine + i * STEP, t.input_gate);
+        }
+        fence_async();
+        __syncwarp();
+        if (k.lane == 0 && t0 < a.T) {
+            const uint32_t from = ptx::smem_u32(out) + k.w * TOK * STEP;
+            store_box3(&maps.dx, x0, static_cast<int>(t0), row, from);
+            store_box3(&maps.dgate, x0, static_cast<int>(t0), row, from + BYTES);
+            store_box3(&maps.dinput_gate, x0, static_cast<int>(t0), row, from + 2 * BYTES);
+            stores_commit();
+        }
+        if constexpr (!CLUSTER) {
+            if (k.w == 0) {
+                chain.last[p][k.lane] = halves(m);
+                carry = m;
+            }
         }
     }
-}
-
-template <class T, bool VEC>
-int back_ranks(const rlscan_gated_scan_args &a)
-{
-    return gated_cluster<T, VEC>(backward_kernel<T, VEC, true>, a.N * ceil_div(a.D, kGatedWidth), a.T, kBackTile);
-}
-
-template <class T, bool VEC>
-rlscan_status backward_as(const rlscan_gated_scan_args &a, const BackwardArgs &o, int ranks, cudaStream_t s)
-{
-    const int64_t chains = a.N * ceil_div(a.D, kGatedWidth);
-    const int threads = 32 * kGatedWarps;
-    return ranks > 1 ? launch_cluster(backward_kernel<T, VEC, true>, chains * ranks, threads, ranks, s, a, o, ranks)
-                     : launch_cluster(backward_kernel<T, VEC, false>, chains, threads, 1, s, a, o, 1);
+    finish<T, true, TILE, CLUSTER>(a, o, k, ranks, l, carry, sum, chain);
+    if (k.lane == 0) stores_read();
+    leave(&gave_up, &g_timed_out);
 }
 
 template <class T>
-rlscan_status backward_typed(const rlscan_gated_scan_args &a, BackwardArgs &o, int64_t &parts, cudaStream_t s)
+rlscan_status backward_typed(const rlscan_gated_scan_args &a, const BackwardArgs &o, int64_t &parts, cudaStream_t s)
 {
-    const rlscan_array3 &grad_y = o.grad_y;
-    Chunk c;
-    for (const rlscan_array3 *v : {&a.x, &a.gate, &a.input_gate, &grad_y}) c.add(v->data, v->row_stride, v->token_stride, sizeof(T));
-    for (void *p : {o.g.x, o.g.gate, o.g.input_gate}) c.add(p, 0, 0, sizeof(T));
-    const bool vec = gated_pairs<T>(c, a.D) && ((reinterpret_cast<uintptr_t>(o.g.initial_state) | reinterpret_cast<uintptr_t>(o.parts) |
-                                                 reinterpret_cast<uintptr_t>(o.checkpoints)) & 7u) == 0;
-    const int ranks = vec ? back_ranks<T, true>(a) : back_ranks<T, false>(a);
-    parts = a.N * ranks;
-    return vec ? backward_as<T, true>(a, o, ranks, s) : backward_as<T, false>(a, o, ranks, s);
+    const int64_t chains = a.N * ceil_div(a.D, kGatedWidth);
+    const int threads = 32 * kGatedWarps;
+    const Access access = gated_access<T>({&a.x, &a.gate, &a.input_gate, &o.grad_y}, {o.g.x, o.g.gate, o.g.input_gate},
+                                          {o.g.initial_state, o.parts, o.checkpoints}, a.N, a.T, a.D);
+    if (access == Access::Tiles && a.T > 0) {
+        using Tile = BackwardTile<T>;
+        static PerDevice alone, shared;
+        if (!raise_smem(alone, tiled_backward_kernel<T, false>, Tile::SMEM) || !raise_smem(shared, tiled_backward_kernel<T, true>, Tile::SMEM))
+            return RLSCAN_ERR_CUDA;
+        BackwardMaps m;
+        auto in = [&](CUtensorMap *map, const rlscan_array3 &v) {
+            return gated_map<T>(map, v.data, v.row_stride, v.token_stride, a.N, a.T, a.D, Tile::TOKENS);
+        };
+        auto out = [&](CUtensorMap *map, void *p) { return gated_map<T>(map, p, a.T * a.D, a.D, a.N, a.T, a.D, Tile::TOK); };
+        if (!in(&m.x, a.x) || !in(&m.gate, a.gate) || !in(&m.input_gate, a.input_gate) || !in(&m.grad_y, o.grad_y) ||
+            !out(&m.dx, o.g.x) || !out(&m.dgate, o.g.gate) || !out(&m.dinput_gate, o.g.input_gate))
+            return RLSCAN_ERR_CUDA;
+        const int ranks = gated_cluster<T, 2>(tiled_backward_kernel<T, true>, chains, a.T, Tile::TOKENS, Tile::SMEM);
+        parts = a.N * ranks;
+        return ranks > 1 ? launch_cluster(tiled_backward_kernel<T, true>, chains * ranks, threads, Tile::SMEM, ranks, s, a, o, m, ranks)
+                         : launch_cluster(tiled_backward_kernel<T, false>, chains, threads, Tile::SMEM, 1, s, a, o, m, 1);
+    }
+    auto go = [&](auto pairs) {
+        constexpr bool VEC = decltype(pairs)::value;
+        const int ranks = gated_cluster<T, VEC>(backward_kernel<T, VEC, true>, chains, a.T, kBackTile, 0);
+        parts = a.N * ranks;
+        return ranks > 1 ? launch_cluster(backward_kernel<T, VEC, true>, chains * ranks, threads, 0, ranks, s, a, o, ranks)
+                         : launch_cluster(backward_kernel<T, VEC, false>, chains, threads, 0, 1, s, a, o, 1);
+    };
+    return access != Access::Values ? go(std::true_type()) : go(std::false_type());
 }
 
 }  // namespace
@@ -237,7 +404,7 @@ rlscan_status launch_gated_scan_backward(const rlscan_gated_scan_args &a, const 
     float *shares = g.log_decay != nullptr ? static_cast<float *>(ws) : nullptr;
     int64_t parts = 0;
     if (a.N > 0) {
-        BackwardArgs o{grad_y, grad_final_state, checkpoints, g, shares};
+        const BackwardArgs o{grad_y, grad_final_state, checkpoints, g, shares};
         const rlscan_status st = a.dtype == RLSCAN_BF16 ? backward_typed<bf16>(a, o, parts, s) : backward_typed<float>(a, o, parts, s);
         if (st != RLSCAN_OK) return st;
     }
@@ -246,6 +413,8 @@ rlscan_status launch_gated_scan_backward(const rlscan_gated_scan_args &a, const 
     jobs.add(shares, parts, a.D, a.D, g.log_decay, false);
     return launch_sums(jobs, s);
 }
+
+rlscan_status gated_scan_backward_status(cudaStream_t s) { return take_flag(g_timed_out, s); }
 
 }  // namespace seq
 }  // namespace rlscan

@@ -569,6 +569,8 @@ rlscan_status launch_gated_scan_backward(const rlscan_gated_scan_args &a, const 
                                          const float *grad_final_state, const float *checkpoints,
                                          const rlscan_gated_scan_grads &g, void *ws, cudaStream_t s);
 size_t gated_scan_backward_workspace(const rlscan_gated_scan_args &a);
+rlscan_status gated_scan_status(cudaStream_t s);           // whether a wait ran out
+rlscan_status gated_scan_backward_status(cudaStream_t s);
 
 // Sums over parts, several in one launch:
 // out[i] = sum over w < parts of part[w * pitch + i], i < m, in a fixed order.

@@ -3,9 +3,7 @@
 // blocks), and descriptors of operands in shared memory.
 #pragma once
 
-#include "sequence.cuh"
-
-#include <cuda.h>
+#include "async_copy.cuh"
 
 namespace rlscan {
 namespace umma {
@@ -28,37 +26,6 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-constexpr uint64_t kWaitNs = 4'000'000'000ull;
-
-// Waits for phase `parity`, at most kWaitNs; then, or once another thread of
-// the block has given up, false.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *gave_up)
-{
-    if (try_wait_cluster(bar, parity)) return true;
-    const uint64_t start = ptx::globaltimer_ns();
-    while (!try_wait_cluster(bar, parity)) {
-        if (*gave_up != 0) return false;
-        if (ptx::globaltimer_ns() - start > kWaitNs) {
-            *gave_up = 1;
-            return false;
-        }
-    }
-    return true;
-}
-
 // ---- copies ---------------------------------------------------------------------
 // A box of a tensor map into this block's shared memory; its bytes count on a
 // barrier of any block of the pair.
@@ -147,24 +114,9 @@ __device__ __forceinline__ void commit(uint32_t bar)
 // lies outside the array reads 0.
 inline bool encode(CUtensorMap *map, const void *p, int64_t rows, int64_t columns, int64_t pitch, uint32_t box)
 {
-    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                                const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static const Encode call = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (!seq::ok(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found)) ||
-            found != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<Encode>(f);
-    }();
-    if (call == nullptr) return false;
-    const cuuint64_t size[2] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(pitch) * 2};
-    const cuuint32_t boxes[2] = {64, box}, step[2] = {1, 1};
-    return call(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), size, stride, boxes, step,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const int64_t extents[2] = {columns, rows}, strides[1] = {pitch * 2};
+    const uint32_t boxes[2] = {64, box};
+    return seq::encode_map(map, p, true, 2, extents, strides, boxes, true);
 }
 
 }  // namespace umma
