@@ -878,12 +878,12 @@ rlscan_status rlscan_distill_loss_backward(const rlscan_distill_args *args, cons
                                            const float *normalizers, void *grad_logits, rlscan_stream_t stream);
 
 /* Both, for a caller who knows grad_loss beforehand: the logits are read once
- * (while a row of V logits has at most 512 KB; longer rows are read twice). */
+ * (while a row of V logits has at most 800 KB; longer rows are read twice). */
 rlscan_status rlscan_distill_loss_and_grad(const rlscan_distill_args *args, const float *grad_loss, float *loss,
                                            float *normalizers, void *grad_logits, rlscan_stream_t stream);
 
 /* Synchronises the stream; RLSCAN_ERR_TIMEOUT once after a wait inside a gated
- * scan or a gated projection (of a block for its copies, or for a block that
+ * scan, a gated projection or a distillation loss (of a block for its copies, or for a block that
  * shares its work) ran out on the current device: after 4 s such a kernel ends,
  * and what its call wrote is void. */
 rlscan_status rlscan_wait_status(rlscan_stream_t stream);

@@ -19,6 +19,7 @@ rlscan_status launch_distill(const rlscan_distill_args &a, const DistillOut &o, 
 rlscan_status launch_distill_backward(const rlscan_distill_args &a, const DistillOut &o, cudaStream_t s);
 // Loss and gradient; false: the rows do not fit on chip (the two calls above do the same).
 bool distill_fits(const rlscan_distill_args &a);
+rlscan_status distill_status(cudaStream_t s);  // whether a wait ran out
 rlscan_status launch_distill_both(const rlscan_distill_args &a, const DistillOut &o, cudaStream_t s);
 
 }  // namespace seq

@@ -1,6 +1,7 @@
 // gated_abi.cu -- the extern "C" entry points of the gated recurrence: argument
 // validation, then the launchers of k_gated_scan*.cu.
 #include "abi_checks.cuh"
+#include "distill.cuh"
 #include "gated_projection.cuh"
 
 using namespace rlscan;
@@ -99,7 +100,8 @@ RLSCAN_API rlscan_status rlscan_gated_scan_step(const rlscan_gated_scan_args *ar
 
 RLSCAN_API rlscan_status rlscan_wait_status(rlscan_stream_t stream)
 {
-    const rlscan_status all[] = {gated_scan_status(cs(stream)), gated_scan_backward_status(cs(stream)), gated_projection_status(cs(stream))};
+    const rlscan_status all[] = {gated_scan_status(cs(stream)), gated_scan_backward_status(cs(stream)), gated_projection_status(cs(stream)),
+                                 distill_status(cs(stream))};
     for (const rlscan_status st : all) RLSCAN_TRY(st);
     return RLSCAN_OK;
 }

@@ -132,15 +132,16 @@ __device__ __forceinline__ void fetch_tokens(Two<T, VEC> (&v)[TOK], const rlscan
     }
 }
 
-// bit k: a new episode starts at token t0 + k
+// The lane's flag of a warp's TOK tokens from t0 on.  The load stays in flight
+// until `starts` looks at it: bit k, a new episode starts at token k.
 template <int TOK>
-__device__ __forceinline__ uint32_t fetch_resets(const uint8_t *resets, int64_t row, int64_t t0, int64_t len, int lane)
+__device__ __forceinline__ uint32_t fetch_flag(const uint8_t *resets, int64_t row, int64_t t0, int64_t len, int lane)
 {
-    if (resets == nullptr) return 0u;
     uint32_t flag = 0;
-    if (lane < TOK && t0 + lane < len) flag = resets[row + t0 + lane];
-    return __ballot_sync(0xffffffffu, flag != 0);
+    if (resets != nullptr && lane < TOK && t0 + lane < len) flag = load_byte(resets + row + t0 + lane);
+    return flag;
 }
+__device__ __forceinline__ uint32_t starts(uint32_t flag) { return __ballot_sync(0xffffffffu, flag != 0); }
 
 template <class T, bool VEC>
 __device__ __forceinline__ void store_two(T *p, f2 v, bool on0, bool on1)
@@ -225,24 +226,18 @@ __device__ __forceinline__ Gates gates(f2 gate, f2 input_gate, const Decay &d)
 }
 
 // ---- the blocks of a cluster -------------------------------------------------
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// (what the blocks tell each other so is that they have begun: what they write
+// for each other has barriers of its own, and a release would wait for it)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
-// a value into the same place of block `rank`'s shared memory
-__device__ __forceinline__ void store_to_rank(const void *mine, int rank, float4 v)
-{
-    uint32_t at;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(mine)), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
-}
 
 // The maps of a cluster's blocks, handed round once a step: every block sends
 // its own to all (stores that count on the receiver's barrier, so nobody waits
 // for more than the values) and waits for all.  Two buffers take turns: who
 // has all maps of a step knows that all have read those of the step before.
+template <int RANKS>
 struct Exchange {
-    float4 map[2][kGatedCluster][32];
+    float4 map[2][RANKS][32];
     uint64_t bar[2];
 
     __device__ __forceinline__ void init()  // one thread; the blocks meet before the first send
@@ -270,7 +265,6 @@ struct Exchange {
 __device__ __forceinline__ f2 apply(f2 h, const float4 &m) { return fma2(pair(m.x, m.y), h, pair(m.z, m.w)); }
 
 // What a step's warps share of one chain (states forwards, messages backwards).
-template <bool CLUSTER>
 struct Chain {
     float4 map[2][kGatedWarps][32];  // (factor, rest) of each warp's tokens
     float2 last[2][32];              // the value behind a step, of a block that walks alone
@@ -279,13 +273,31 @@ struct Chain {
         const float2 a = halves(factor), b = halves(rest);
         map[p][w][lane] = make_float4(a.x, a.y, b.x, b.y);
     }
+    __device__ __forceinline__ float4 get(int p, int w, int lane) const { return map[p][w][lane]; }
+};
+
+// The same of states and messages together, whose maps share the factor.
+struct TwoChains {
+    float4 map[2][kGatedWarps][32];     // (factor, rest of the states)
+    float2 message[2][kGatedWarps][32], last[2][32];
+    __device__ __forceinline__ void put(int p, int w, int lane, f2 factor, f2 state, f2 m)
+    {
+        const float2 a = halves(factor), b = halves(state);
+        map[p][w][lane] = make_float4(a.x, a.y, b.x, b.y);
+        message[p][w][lane] = halves(m);
+    }
+    __device__ __forceinline__ float4 get(int p, int w, int lane) const
+    {
+        const float2 f = *reinterpret_cast<const float2 *>(&map[p][w][lane]), m = message[p][w][lane];
+        return make_float4(f.x, f.y, m.x, m.y);
+    }
 };
 
 // Behind the barrier that follows `put`: the value in front of the warp's
 // tokens, from the one in front of the step, `carry` (kept current by every
 // warp in a cluster, by the last warp alone otherwise).  turn: steps done.
-template <bool CLUSTER, bool FORWARD>
-__device__ __forceinline__ f2 in_front(Chain<CLUSTER> &c, Exchange *ex, int64_t turn, int w, int lane, int rank, int ranks, f2 &carry,
+template <bool CLUSTER, bool FORWARD, class C, class E>
+__device__ __forceinline__ f2 in_front(C &c, E *ex, int64_t turn, int w, int lane, int rank, int ranks, f2 &carry,
                                        int *gave_up)
 {
     const int p = static_cast<int>(turn & 1);
@@ -294,7 +306,7 @@ __device__ __forceinline__ f2 in_front(Chain<CLUSTER> &c, Exchange *ex, int64_t 
         f2 factor = both(1.f), rest = both(0.f);  // the block's map
 #pragma unroll
         for (int i = 0; i < kGatedWarps; ++i) {
-            const float4 m = c.map[p][FORWARD ? i : kGatedWarps - 1 - i][lane];
+            const float4 m = c.get(p, FORWARD ? i : kGatedWarps - 1 - i, lane);
             factor = mul2(factor, pair(m.x, m.y));
             rest = apply(rest, m);
         }
@@ -313,10 +325,10 @@ __device__ __forceinline__ f2 in_front(Chain<CLUSTER> &c, Exchange *ex, int64_t 
     }
     if constexpr (FORWARD) {
 #pragma unroll 1
-        for (int q = 0; q < w; ++q) h = apply(h, c.map[p][q][lane]);
+        for (int q = 0; q < w; ++q) h = apply(h, c.get(p, q, lane));
     } else {
 #pragma unroll 1
-        for (int q = kGatedWarps - 1; q > w; --q) h = apply(h, c.map[p][q][lane]);
+        for (int q = kGatedWarps - 1; q > w; --q) h = apply(h, c.get(p, q, lane));
     }
     return h;
 }
@@ -326,16 +338,18 @@ __host__ __device__ inline int64_t gated_marks(int64_t T) { return (T + RLSCAN_G
 
 // Blocks of a cluster that share a row: as many as make the fewest steps one
 // after the other, counting the rounds in which clusters of that size become
-// resident.  A row split over blocks costs each step an exchange, taken as a
-// quarter of a step.
+// resident.  A row split over blocks costs each step an exchange, taken as
+// three quarters of a step (measured: 16 x 1024 x 2048, 512 chains, alone 60
+// us, in fours 69; 2 x 16384 x 2048, 64 chains, alone 354, in fours 195, in
+// sixes 144, in eights, which no longer fit at once, 184).
 template <class T, int KIND, class K>
-inline int gated_cluster(K kernel, int64_t chains, int64_t tokens, int tile, size_t smem)
+inline int gated_cluster(K kernel, int64_t chains, int64_t tokens, int tile, size_t smem, int most = kGatedCluster)
 {
     static PerDevice resident[kGatedCluster + 1];
     const int64_t tiles = ceil_div(tokens, tile);
     int best = 1;
     double least = 0;
-    for (int c = 1; c <= kGatedCluster; ++c) {
+    for (int c = 1; c <= most; ++c) {
         if (c > 1 && c > tiles) break;
         const int64_t fit = resident[c].get(current_device(), [&] {
             cudaLaunchConfig_t cfg = {};
@@ -352,14 +366,20 @@ inline int gated_cluster(K kernel, int64_t chains, int64_t tokens, int tile, siz
             return ok(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) ? n : 0;
         });
         if (fit <= 0) continue;
-        const double time = static_cast<double>(ceil_div(chains, fit)) * static_cast<double>(ceil_div(tiles, c)) * (c > 1 ? 1.25 : 1.0);
+        const double time = static_cast<double>(ceil_div(chains, fit)) * static_cast<double>(ceil_div(tiles, c)) * (c > 1 ? 1.75 : 1.0);
         if (c == 1 || time < least) best = c, least = time;
     }
     return best;
 }
 
+// `overlapped`: whether the grid may start while the kernel before it still
+// runs.  A grid of several blocks an SM would then go to the SMs that are done
+// first, several at once, and end unevenly (4 x 4096 x 4096 float32 forward
+// 189 us, started behind 169; loss and gradient of 4 x 1024 x 50304 logits 279
+// and 192), so only grids of a block an SM do.
 template <class K, class... Args>
-inline rlscan_status launch_cluster(K kernel, int64_t grid, int threads, size_t smem, int cluster, cudaStream_t stream, Args... args)
+inline rlscan_status launch_cluster(bool overlapped, K kernel, int64_t grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                                    Args... args)
 {
     if (grid > 0x7fffffff) return RLSCAN_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
@@ -369,7 +389,7 @@ inline rlscan_status launch_cluster(K kernel, int64_t grid, int threads, size_t 
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    attr[0].val.programmaticStreamSerializationAllowed = overlapped && pdl_enabled() ? 1 : 0;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;

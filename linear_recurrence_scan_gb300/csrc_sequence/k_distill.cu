@@ -10,6 +10,8 @@ namespace rlscan {
 namespace seq {
 namespace {
 
+__device__ unsigned int g_timed_out;  // a wait ran out on this device
+
 enum class Part { Loss, Grad, Both };
 
 // 16 bytes of a row of logits
@@ -40,45 +42,32 @@ struct Unit {
     }
 };
 
-// A row of V values as units of 16 bytes of memory: the first and the last
-// may hold others' values, and are then taken value by value.
+// A row of V values: `units` whole units of 16 bytes of memory from `p + head`
+// on, and the values in front of and behind them (`head` and `tail`, at most
+// PER - 1 each), which are taken one by one.
 template <class T>
 struct Row {
-    const T *aligned;  // start of the first unit
-    int64_t off, V;    // values of the first unit in front of the row
-    __device__ __forceinline__ Row(const T *p, int64_t n)
-        : aligned(reinterpret_cast<const T *>(reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(15))),
-          off(p - aligned), V(n)
+    const T *p;
+    int V, head, units, tail;
+    __device__ __forceinline__ Row(const T *row, int64_t n) : p(row), V(static_cast<int>(n))
     {
+        constexpr int PER = Unit<T>::PER;
+        head = (PER - static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T))) % PER;
+        head = head < V ? head : V;
+        units = (V - head) / PER;
+        tail = V - head - units * PER;
     }
-    __device__ __forceinline__ int64_t units() const { return (off + V + Unit<T>::PER - 1) / Unit<T>::PER; }
-    __device__ __forceinline__ int64_t first(int64_t u) const { return u * Unit<T>::PER - off; }
-    __device__ __forceinline__ bool whole(int64_t u) const { return first(u) >= 0 && first(u) + Unit<T>::PER <= V; }
-    // unit u; -infinity where it lies outside the row
-    __device__ __forceinline__ Unit<T> load(int64_t u, int64_t end) const
+    __device__ __forceinline__ int64_t first(int u) const { return head + static_cast<int64_t>(u) * Unit<T>::PER; }
+    __device__ __forceinline__ Unit<T> load(int u) const
     {
         Unit<T> r;
-        const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-        r.v = make_uint4(none, none, none, none);
-        if (u >= end) return r;
-        if (whole(u)) {
-            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(r.v.x), "=r"(r.v.y), "=r"(r.v.z), "=r"(r.v.w)
-                         : "l"(aligned + u * Unit<T>::PER));
-            return r;
-        }
-        float f[Unit<T>::PER];
-#pragma unroll
-        for (int i = 0; i < Unit<T>::PER; ++i) {
-            const int64_t e = first(u) + i;
-            f[i] = e >= 0 && e < V ? to_f(aligned[u * Unit<T>::PER + i]) : -INFINITY;
-        }
-        Words<T, Unit<T>::PER> w;
-#pragma unroll
-        for (int i = 0; i < Unit<T>::PAIRS; ++i) w.set(i, f[2 * i], f[2 * i + 1]);
-        r.v = make_uint4(w.w[0], w.w[1], w.w[2], w.w[3]);
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.v.x), "=r"(r.v.y), "=r"(r.v.z), "=r"(r.v.w)
+                     : "l"(p + first(u)));
         return r;
     }
+    // the t-th value outside the units: its place, or -1
+    __device__ __forceinline__ int edge(int t) const { return t < head ? t : t < head + tail ? V - tail + (t - head) : -1; }
 };
 
 struct Stats {
@@ -97,295 +86,487 @@ __device__ __forceinline__ float warp_sum(float v)
     for (int i = 16; i > 0; i /= 2) v += __shfl_xor_sync(0xffffffffu, v, i);
     return v;
 }
-__device__ __forceinline__ Stats join(Stats a, Stats b, float c)
-{
-    const float m = fmaxf(a.m, b.m);
-    return {m, a.s * exp2_fast((a.m - m) * c) + b.s * exp2_fast((b.m - m) * c)};
-}
-
-// A row belongs to a warp (THREADS = 32: four rows a block), to a block, or,
-// CLUSTER, to the blocks of a cluster, each with a slice.  A thread holds
-// UNITS units of 16 bytes in registers, all in flight together.  Part::Both
-// reads the logits once: largest value and sum from the registers, joined
-// over lanes, warps and blocks, then the gradient from the same registers.
-// Loss walks longer rows in several rounds with a running maximum and sum;
-// Grad starts from the kept maximum and sum, its blocks share nothing.  The
-// maximum starts at the lowest finite number, not at -infinity, so that rows
-// and parts of rows without a finite value need no case of their own (their
-// sum is 0), and values enter as (z - m) / tau, which is 0 for the largest
-// whatever its size.
-template <class T, int THREADS, int UNITS, Part PART, bool CLUSTER>
-__global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS == 512 ? 2 : 6)
-    distill_kernel(const __grid_constant__ rlscan_distill_args a, const __grid_constant__ DistillOut o, int ranks)
-{
-    constexpr bool WARP = THREADS == 32;
-    constexpr int GROUPS = WARP ? 4 : 1, WARPS = WARP ? 1 : THREADS / 32, PER = Unit<T>::PER;
-    struct Teacher {
-        float q[kMostTeacher], z[kMostTeacher];
-        int32_t token[kMostTeacher];
-    };
-    __shared__ Teacher teachers[GROUPS];
-    __shared__ Stats of_warp[WARPS];
-    __shared__ float4 of_rank[CLUSTER ? kGatedCluster : 1];
-    __shared__ float logs[GROUPS];  // sum of q log q
-    __shared__ int taught[GROUPS];  // whether a teacher's token is left
-    ptx::pdl_trigger_dependents();
-    ptx::pdl_wait_prerequisites();
-    const int g = WARP ? threadIdx.x / 32 : 0, t = WARP ? threadIdx.x % 32 : threadIdx.x, lane = threadIdx.x & 31;
-    const int rank = WARP ? 0 : static_cast<int>(blockIdx.x % static_cast<unsigned>(ranks));
-    const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * GROUPS + g : blockIdx.x / static_cast<unsigned>(ranks);
-    if (row >= a.N * a.T) return;  // a whole warp
-    auto sync = [] {
-        if constexpr (WARP) __syncwarp();
-        else __syncthreads();
-    };
-    const Division at = divide(row, a.T);
-    const Row<T> in(static_cast<const T *>(a.logits.data) + at.q * a.logits.row_stride + at.r * a.logits.token_stride, a.V);
-    // the slice of this rank, in whole rounds of the block
-    const int64_t all = in.units(), share = (all + ranks - 1) / ranks, u0 = rank * share, end = u0 + share < all ? u0 + share : all;
-    T *out = static_cast<T *>(o.grad) + row * a.V;
-    const bool same = PART != Part::Loss && (reinterpret_cast<uintptr_t>(out) & 15u) == static_cast<uintptr_t>(in.off) * sizeof(T);
-    // a unit of the gradient, from fp32 values that `value` gives
-    auto put = [&](int64_t u, auto value) {
-        if (same && in.whole(u)) {
-            Words<T, PER> w;
-#pragma unroll
-            for (int i = 0; i < PER / 2; ++i) {
-                const float2 h = halves(value(i));
-                w.set(i, h.x, h.y);
-            }
-            *reinterpret_cast<uint4 *>(out + in.first(u)) = make_uint4(w.w[0], w.w[1], w.w[2], w.w[3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER / 2; ++i) {
-                const float2 h = halves(value(i));
-                const int64_t e = in.first(u) + 2 * i;
-                if (e >= 0 && e < a.V) out[e] = from_f<T>(h.x);
-                if (e + 1 >= 0 && e + 1 < a.V) out[e + 1] = from_f<T>(h.y);
-            }
-        }
-    };
-    if (a.mask != nullptr && a.mask[row] == 0) {  // neither its logits nor its teacher are read
-        if (PART != Part::Grad && rank == 0 && t == 0) {
-            o.loss[row] = 0.f;
-            if (o.normalizers != nullptr) reinterpret_cast<float2 *>(o.normalizers)[row] = make_float2(0.f, 1.f);
-        }
-        if constexpr (PART != Part::Loss)
-            for (int64_t u = u0 + t; u < end; u += THREADS) put(u, [](int) { return both(0.f); });
-        return;
+// exp((z - m) / tau) of a pair, for a logit z and its row's largest m: one
+// multiply-add in front of the exponential, z c - m c with c = log2 e / tau.
+// m c is rounded, by the same `rest` for every logit, which `exact` takes back
+// from a sum or a factor.  Where m c is too large for that (|m| of the size of
+// a type's lowest value, as masks have it) values are taken one by one, the
+// difference z - m first.
+struct Shift {
+    f2 c, mc;
+    float rest;
+    bool wide;
+    __device__ __forceinline__ Shift(float m, float c1)
+    {
+        const float product = m * c1;
+        c = both(c1);
+        mc = both(-product);
+        wide = !(fabsf(product) < 1e30f);
+        rest = wide ? 0.f : fmaf(m, c1, -product);
     }
-    const float c = kLog2e / static_cast<float>(a.temperature), rtau = 1.f / static_cast<float>(a.temperature);
-    Unit<T> v[UNITS];
-    auto load = [&](int64_t first) {
-#pragma unroll
-        for (int i = 0; i < UNITS; ++i) v[i] = in.load(first + i * THREADS + t, end);
-    };
-    load(u0);
-    if constexpr (CLUSTER && PART != Part::Grad) cluster_arrive();
-    Teacher &teach = teachers[g];
-    const int K = static_cast<int>(a.K);
-    if (t < 32) {  // the teacher's probabilities, by one warp
-        float largest = -INFINITY, sum = 0.f;
-        for (int k = lane; k < K; k += 32) {
-            const int64_t i = row * a.K + k;
-            const int64_t token = a.token_bytes == 8 ? static_cast<const int64_t *>(a.teacher_tokens)[i]
-                                                     : static_cast<const int32_t *>(a.teacher_tokens)[i];
-            const bool valid = token >= 0 && token < a.V;
-            teach.token[k] = valid ? static_cast<int32_t>(token) : -1;
-            const float x = a.teacher_dtype == RLSCAN_BF16 ? to_f(static_cast<const bf16 *>(a.teacher_logits)[i])
-                                                           : static_cast<const float *>(a.teacher_logits)[i];
-            teach.q[k] = valid ? x : -INFINITY;
-            teach.z[k] = valid ? to_f(in.aligned[in.off + token]) : 0.f;
-            if (valid) largest = x > largest || x != x ? x : largest;  // a NaN stays
-        }
-        const bool nan = __any_sync(0xffffffffu, largest != largest);
-        largest = nan ? NAN : warp_max(largest);
-        if (lane == 0) taught[g] = largest != -INFINITY;
-        if (largest != -INFINITY) {
-            for (int k = lane; k < K; k += 32) sum += exp2_fast((teach.q[k] - largest) * c);
-            sum = warp_sum(sum);
-            const float log_sum = logf(sum);
-            float entropy = 0.f;  // sum of q log q
-            for (int k = lane; k < K; k += 32) {
-                const float lq = (teach.q[k] - largest) * rtau - log_sum, q = exp2_fast((teach.q[k] - largest) * c) / sum;
-                if (!(q == 0.f)) entropy += q * lq;
-                teach.q[k] = q;
-            }
-            entropy = warp_sum(entropy);
-            if (lane == 0) logs[g] = entropy;
-        }
-    }
-    Stats st{-FLT_MAX, 0.f};
-    if constexpr (PART == Part::Grad) {
-        const float2 kept = reinterpret_cast<const float2 *>(o.normalizers)[row];
-        st = {kept.x, kept.y};
-        sync();
-    } else {
-        for (int64_t first = u0;;) {
-            float m = st.m;
-#pragma unroll
-            for (int i = 0; i < UNITS; ++i) m = fmaxf(m, v[i].max());
-            const f2 low = both(-m), scale = both(c);
-            f2 s0 = both(0.f), s1 = both(0.f);
-#pragma unroll
-            for (int i = 0; i < UNITS; ++i)
-#pragma unroll
-                for (int j = 0; j < Unit<T>::PAIRS; ++j) {
-                    f2 &s = j % 2 == 0 ? s0 : s1;
-                    s = add2(s, exp2_fast(mul2(add2(v[i].get(j), low), scale)));
-                }
-            const float2 h = halves(add2(s0, s1));
-            st = {m, st.s * exp2_fast((st.m - m) * c) + (h.x + h.y)};
-            first += THREADS * UNITS;
-            if (PART == Part::Both || first >= end) break;
-            load(first);
-        }
-        const float m = warp_max(st.m);
-        st = {m, warp_sum(st.s * exp2_fast((st.m - m) * c))};
-        if constexpr (!WARP) {
-            if (lane == 0) of_warp[threadIdx.x / 32] = st;
-            __syncthreads();
-            st = of_warp[0];
-#pragma unroll
-            for (int i = 1; i < WARPS; ++i) st = join(st, of_warp[i], c);
-        } else {
-            __syncwarp();
-        }
-        if constexpr (CLUSTER) {
-            cluster_wait();
-            if (t < ranks) store_to_rank(&of_rank[rank], t, make_float4(st.m, st.s, 0.f, 0.f));
-            cluster_arrive();
-            cluster_wait();
-            st = {of_rank[0].x, of_rank[0].y};
-            for (int i = 1; i < ranks; ++i) st = join(st, Stats{of_rank[i].x, of_rank[i].y}, c);
-        }
-        if (rank == 0 && t < 32) {
-            float cross = 0.f;
-            for (int k = lane; k < K; k += 32) {
-                const float q = teach.q[k];
-                if (!(q == 0.f)) cross += q * ((teach.z[k] - st.m) * rtau);
-            }
-            cross = warp_sum(cross);
-            if (lane == 0) {
-                o.loss[row] = taught[g] ? logs[g] - cross + logf(st.s) : 0.f;
-                if (o.normalizers != nullptr) reinterpret_cast<float2 *>(o.normalizers)[row] = make_float2(st.m, st.s);
-            }
-        }
-    }
-    if constexpr (PART != Part::Loss) {
-        const bool some = taught[g] != 0;
-        const float weight = some ? o.grad_loss[row] * rtau : 0.f, scale = weight / st.s;
-        const f2 low = both(-st.m), c2 = both(c), scale2 = both(scale);
-        // The registers keep the logits as they were read: without this the
-        // compiler keeps the widened values from the first pass to this one.
-        if constexpr (PART == Part::Both) {
-#pragma unroll
-            for (int i = 0; i < UNITS; ++i) asm volatile("" : "+r"(v[i].v.x), "+r"(v[i].v.y), "+r"(v[i].v.z), "+r"(v[i].v.w));
-        }
-        for (int64_t first = u0;;) {
-#pragma unroll
-            for (int i = 0; i < UNITS; ++i) {
-                const int64_t u = first + i * THREADS + t;
-                if (u < end)
-                    put(u, [&](int j) {
-                        const f2 e = mul2(exp2_fast(mul2(add2(v[i].get(j), low), c2)), scale2);
-                        return some ? e : both(0.f);
-                    });
-            }
-            first += THREADS * UNITS;
-            if (PART == Part::Both || first >= end) break;
-            load(first);
-        }
-        sync();  // the teacher's tokens over what has been written
-        if (some)
-            for (int k = t; k < K; k += THREADS) {
-                const int32_t token = teach.token[k];
-                const int64_t u = (in.off + token) / PER;
-                if (token < 0 || u < u0 || u >= end) continue;
-                float q = 0.f;
-                bool first = true;  // a token that comes twice counts twice, and is written once
-                for (int j = 0; j < K; ++j)
-                    if (teach.token[j] == token) {
-                        first = first && j >= k;
-                        q += teach.q[j];
-                    }
-                if (first) out[token] = from_f<T>(exp2_fast((teach.z[k] - st.m) * c) * scale - q * weight);
-            }
-    }
-}
-
-// Loss, or loss and gradient: threads and blocks of a row.
-struct Plan {
-    int threads, ranks;
+    __device__ __forceinline__ f2 exp(f2 z) const { return exp2_fast(fma2(z, c, mc)); }
+    __device__ __forceinline__ float exact() const { return exp2_fast(-rest); }
 };
 
-constexpr int kUnits = 8;  // of a thread
+// The maxima and sums of a row's warps, of all the blocks that share it.  Two
+// buffers take turns: who has all of a row's knows that all have read those of
+// the row before.
+template <int WARPS, bool CLUSTER>
+struct Meeting {
+    float2 of_warp[2][CLUSTER ? kGatedCluster * WARPS : WARPS];
+    uint64_t bar[2];
+};
 
-// Units that a row may touch: one more than its own where it starts inside one
-int64_t most_units(const rlscan_distill_args &a)
+// What comes with a row's last part in shared memory: the teacher's
+// probabilities, the logits at its tokens, the tokens (K each, behind the
+// stages), and the row's values outside units.
+struct Head {
+    float edge[16];
+    float entropy;     // sum of q log q
+    float m, s;        // Part::Grad: the kept maximum and sum
+    float weight;      // grad_loss / tau
+    int taught, masked;
+};
+
+constexpr int kStages = 2;
+
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
-    const int64_t per = a.dtype == RLSCAN_BF16 ? 8 : 4;
-    return ceil_div(a.V + per - 1, per);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+                 "r"(bar)
+                 : "memory");
 }
 
-// Rows of up to a warp's or a small block's registers stay there; longer ones
-// are split while they do not fit a block of 512 threads (`hold`), or while
-// there are too few rows to give every SM two blocks.
-Plan plan(const rlscan_distill_args &a, bool hold)
+// Blocks that stay for many rows.  The last warp runs ahead: it brings the
+// next part of the row's logits into shared memory (one copy a stage) and works
+// out the teacher's probabilities there; CONSUMERS threads take a part's sums
+// and write its gradient.  So copies are in flight while sums, the exchange
+// between blocks and the stores of the row before take their time: with blocks
+// that came and went with their row, held in registers, half of a row's time
+// was spent without a byte in flight (4 x 1023 x 50257, loss and gradient 197
+// us).  Part::Both reads the logits once: a block's slice of a row is one part,
+// CLUSTER: a row is several blocks' slices, whose maxima and sums meet.  Loss
+// and Grad walk a row in several parts.  The maximum starts at the lowest
+// finite number, not at -infinity, so that rows and parts of rows without a
+// finite value need no case of their own (their sum is 0).
+template <class T, int CONSUMERS, Part PART, bool CLUSTER>
+__global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 16 : CONSUMERS == 64 ? 8 : CONSUMERS == 128 ? 4 : 2)
+    distill_kernel(const __grid_constant__ rlscan_distill_args a, const __grid_constant__ DistillOut o, int ranks, int stage_units)
+{
+    constexpr int WARPS = CONSUMERS / 32, PER = Unit<T>::PER, ROUND = 4;
+    extern __shared__ __align__(16) char buffers[];
+    __shared__ Head heads[kStages];
+    __shared__ Meeting<WARPS, CLUSTER> meeting;
+    __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ int gave_up;
+    ptx::pdl_trigger_dependents();
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        for (int i = 0; i < kStages; ++i) {
+            ptx::mbar_init(&full[i], 2);  // the copy has been asked for; the head is there
+            ptx::mbar_init(&empty[i], WARPS);
+        }
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&meeting.bar[i], 1);
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    if constexpr (CLUSTER) {
+        cluster_arrive();
+        cluster_wait();  // all can be written to
+    }
+    ptx::pdl_wait_prerequisites();
+    const int lane = threadIdx.x & 31, rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(ranks)), K = static_cast<int>(a.K);
+    const int padded = (K + 3) / 4 * 4;  // of the teacher's arrays: the tokens are looked through by fours
+    auto teacher = [&](int st) { return reinterpret_cast<float *>(buffers + static_cast<size_t>(kStages) * stage_units * 16) + st * 3 * padded; };
+    const int64_t rows = a.N * a.T, stride = gridDim.x / static_cast<unsigned>(ranks), row0 = blockIdx.x / static_cast<unsigned>(ranks);
+    const float c = kLog2e / static_cast<float>(a.temperature), rtau = 1.f / static_cast<float>(a.temperature);
+    auto row_of = [&](int64_t row) {
+        const Division at = divide(row, a.T);
+        return Row<T>(static_cast<const T *>(a.logits.data) + at.q * a.logits.row_stride + at.r * a.logits.token_stride, a.V);
+    };
+    // the rank's units of a row: from `u0` to `end`
+    auto slice = [&](const Row<T> &in, int &u0, int &end) {
+        const int share = (in.units + ranks - 1) / ranks;
+        u0 = rank * share < in.units ? rank * share : in.units;
+        end = u0 + share < in.units ? u0 + share : in.units;
+    };
+    int stage = 0;
+    uint32_t parity = 0;
+    auto next = [&] {
+        if (++stage == kStages) stage = 0, parity ^= 1u;
+    };
+    // The head of a row, by the warp that brings it: the teacher's tokens (-1:
+    // none), q = softmax of its logits over them, the row's logits there.
+    auto teach = [&](Head &h, float *q_of, const Row<T> &in, int64_t row) {
+        float *z_of = q_of + padded;
+        int32_t *token_of = reinterpret_cast<int32_t *>(q_of + 2 * padded);
+        if (lane < padded - K) token_of[K + lane] = -1;
+        if (rank == 0 && in.edge(lane) >= 0) h.edge[lane] = to_f(in.p[in.edge(lane)]);
+        float largest = -INFINITY, sum = 0.f, entropy = 0.f;
+        for (int k = lane; k < K; k += 32) {
+            const int64_t i = row * K + k;
+            const int64_t token = a.token_bytes == 8 ? static_cast<const int64_t *>(a.teacher_tokens)[i]
+                                                     : static_cast<const int32_t *>(a.teacher_tokens)[i];
+            const float x = a.teacher_dtype == RLSCAN_BF16 ? to_f(static_cast<const bf16 *>(a.teacher_logits)[i])
+                                                           : static_cast<const float *>(a.teacher_logits)[i];
+            const bool valid = token >= 0 && token < a.V;
+            token_of[k] = valid ? static_cast<int32_t>(token) : -1;
+            q_of[k] = valid ? x : -INFINITY;
+            z_of[k] = valid ? to_f(in.p[token]) : 0.f;
+            if (valid) largest = x > largest || x != x ? x : largest;  // a NaN stays
+        }
+        largest = __any_sync(0xffffffffu, largest != largest) ? NAN : warp_max(largest);
+        if (largest != -INFINITY) {
+            for (int k = lane; k < K; k += 32) sum += exp2_fast((q_of[k] - largest) * c);
+            sum = warp_sum(sum);
+            const float log_sum = logf(sum);
+            for (int k = lane; k < K; k += 32) {
+                const float lq = (q_of[k] - largest) * rtau - log_sum, q = exp2_fast((q_of[k] - largest) * c) / sum;
+                if (!(q == 0.f)) entropy += q * lq;
+                q_of[k] = q;
+            }
+            entropy = warp_sum(entropy);
+        }
+        if (lane == 0) h.taught = largest != -INFINITY, h.entropy = entropy;
+    };
+    if (threadIdx.x >= CONSUMERS) {  // ---- brings rows
+        uint32_t mask = a.mask != nullptr && row0 < rows ? load_byte(a.mask + row0) : 1u;
+        for (int64_t row = row0; row < rows; row += stride) {
+            const Row<T> in = row_of(row);
+            int u0, end;
+            slice(in, u0, end);
+            const bool masked = mask == 0u;
+            if (a.mask != nullptr && row + stride < rows) mask = load_byte(a.mask + row + stride);
+            for (int u = u0;;) {  // a masked row is one part without logits
+                const int n = masked ? 0 : end - u < stage_units ? end - u : stage_units;
+                const bool last = masked || u + n >= end;
+                wait(ptx::smem_u32(&empty[stage]), parity ^ 1u, &gave_up);
+                if (lane == 0) {
+                    if (n > 0) {
+                        ptx::mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(n) * 16);
+                        copy_bulk(ptx::smem_u32(buffers) + stage * stage_units * 16, in.p + in.first(u), static_cast<uint32_t>(n) * 16,
+                                  ptx::smem_u32(&full[stage]));
+                    } else {
+                        ptx::mbar_arrive(&full[stage]);
+                    }
+                }
+                Head &h = heads[stage];
+                if (lane == 0) {
+                    h.masked = masked;
+                    if (PART != Part::Loss && !masked) h.weight = o.grad_loss[row] * rtau;
+                    if (PART == Part::Grad && !masked) {
+                        const float2 kept = reinterpret_cast<const float2 *>(o.normalizers)[row];
+                        h.m = kept.x, h.s = kept.y;
+                    }
+                }
+                if (last && !masked) teach(h, teacher(stage), in, row);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&full[stage]);
+                next();
+                if (last) break;
+                u += n;
+            }
+        }
+    } else {  // ---- sums and gradients
+        const int t = threadIdx.x;
+        auto sync = [] {
+            if constexpr (CONSUMERS == 32) __syncwarp();
+            else ptx::named_barrier(1, CONSUMERS);
+        };
+        auto release = [&] {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&empty[stage]);
+            next();
+        };
+        int turn = 0;
+        for (int64_t row = row0; row < rows; row += stride) {
+            const Row<T> in = row_of(row);
+            int u0, end;
+            slice(in, u0, end);
+            T *out = static_cast<T *>(o.grad) + row * a.V;
+            const bool aligned = (reinterpret_cast<uintptr_t>(out + in.head) & 15u) == 0;  // units of the gradient as of the logits
+            const int edge = rank == 0 ? in.edge(t) : -1;                                // the thread's value outside the units
+            auto clear = [&] {
+                if (edge >= 0) out[edge] = from_f<T>(0.f);
+                if (aligned) {
+                    for (int u = u0 + t; u < end; u += CONSUMERS) *reinterpret_cast<uint4 *>(out + in.first(u)) = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    for (int64_t e = in.first(u0) + t; e < in.first(end); e += CONSUMERS) out[e] = from_f<T>(0.f);
+                }
+            };
+            Stats st{-FLT_MAX, 0.f};
+            for (int u = u0;;) {
+                wait(ptx::smem_u32(&full[stage]), parity, &gave_up);
+                const Head &h = heads[stage];
+                const float *q_of = teacher(stage), *z_of = q_of + padded;
+                const int32_t *token_of = reinterpret_cast<const int32_t *>(q_of + 2 * padded);
+                const uint4 *part = reinterpret_cast<const uint4 *>(buffers + static_cast<size_t>(stage) * stage_units * 16);
+                if (h.masked) {
+                    if (PART != Part::Grad && rank == 0 && t == 0) {
+                        o.loss[row] = 0.f;
+                        if (o.normalizers != nullptr) reinterpret_cast<float2 *>(o.normalizers)[row] = make_float2(0.f, 1.f);
+                    }
+                    if constexpr (PART != Part::Loss) clear();
+                    release();
+                    break;
+                }
+                const int n = end - u < stage_units ? end - u : stage_units;
+                const bool last = u + n >= end;
+                if constexpr (PART == Part::Grad) {
+                    st = {h.m, h.s};
+                } else {
+                    const float at_edge = last && edge >= 0 ? h.edge[t] : -INFINITY;
+                    if (last && edge >= 0) {
+                        const float m = fmaxf(st.m, at_edge);
+                        st = {m, st.s * exp2_fast((st.m - m) * c) + exp2_fast((at_edge - m) * c)};
+                    }
+                    auto round = [&](int i0, auto units) {  // as many units, from i0 on
+                        constexpr int UNITS = decltype(units)::value;
+                        Unit<T> v[UNITS];
+                        float m = st.m;
+#pragma unroll
+                        for (int i = 0; i < UNITS; ++i) {
+                            v[i].v = part[i0 + i * CONSUMERS];
+                            m = fmaxf(m, v[i].max());
+                        }
+                        const Shift shift(m, c);
+                        float more = 0.f;
+                        if (!shift.wide) {
+                            f2 s0 = both(0.f), s1 = both(0.f);
+#pragma unroll
+                            for (int i = 0; i < UNITS; ++i)
+#pragma unroll
+                                for (int j = 0; j < Unit<T>::PAIRS; j += 2) {
+                                    s0 = add2(s0, shift.exp(v[i].get(j)));
+                                    s1 = add2(s1, shift.exp(v[i].get(j + 1)));
+                                }
+                            const float2 f = halves(add2(s0, s1));
+                            more = (f.x + f.y) * shift.exact();
+                        } else {  // value by value
+                            for (int i = 0; i < UNITS; ++i) {
+                                const T *at = reinterpret_cast<const T *>(part + i0 + i * CONSUMERS);
+                                for (int j = 0; j < PER; ++j) more += exp2_fast((to_f(at[j]) - m) * c);
+                            }
+                        }
+                        st = {m, fmaf(st.s, exp2_fast((st.m - m) * c), more)};
+                    };
+                    int i0 = t;
+                    for (; i0 + (ROUND - 1) * CONSUMERS < n; i0 += ROUND * CONSUMERS) round(i0, std::integral_constant<int, ROUND>());
+                    for (; i0 < n; i0 += CONSUMERS) round(i0, std::integral_constant<int, 1>());
+                }
+                if (PART != Part::Grad && last) {
+                    // lanes, then the warps' results in every warp: the same sums in all
+                    const int p = turn & 1;
+                    const float m = warp_max(st.m);
+                    st = {m, warp_sum(st.s * exp2_fast((st.m - m) * c))};
+                    if constexpr (CLUSTER) {
+                        const int mine = rank * WARPS + t / 32;
+                        if (t == 0) ptx::mbar_arrive_expect_tx(&meeting.bar[p], static_cast<uint32_t>(ranks * WARPS) * sizeof(float2));
+                        if (lane < ranks) {
+                            uint32_t to, signal;
+                            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(ptx::smem_u32(&meeting.of_warp[p][mine])), "r"(lane));
+                            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(signal) : "r"(ptx::smem_u32(&meeting.bar[p])), "r"(lane));
+                            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
+                                         "f"(st.m), "f"(st.s), "r"(signal)
+                                         : "memory");
+                        }
+                        wait(ptx::smem_u32(&meeting.bar[p]), static_cast<uint32_t>(turn >> 1) & 1u, &gave_up);
+                    } else if constexpr (WARPS > 1) {
+                        if (lane == 0) meeting.of_warp[p][t / 32] = make_float2(st.m, st.s);
+                        sync();
+                    }
+                    if constexpr (WARPS > 1) {
+                        const int all = CLUSTER ? ranks * WARPS : WARPS;
+                        Stats some{-FLT_MAX, 0.f};
+                        for (int i = lane; i < all; i += 32) {
+                            const float2 one = meeting.of_warp[p][i];
+                            const float top = fmaxf(some.m, one.x);
+                            some = {top, some.s * exp2_fast((some.m - top) * c) + one.y * exp2_fast((one.x - top) * c)};
+                        }
+                        const float top = warp_max(some.m);
+                        st = {top, warp_sum(some.s * exp2_fast((some.m - top) * c))};
+                    }
+                    ++turn;
+                }
+                if constexpr (PART != Part::Loss) {
+                    const Shift shift(st.m, c);
+                    const float scale = h.weight / st.s;
+                    auto value = [&](float z) { return from_f<T>(exp2_fast((z - st.m) * c) * scale); };
+                    if (aligned && !shift.wide) {
+                        const f2 factor = both(scale * shift.exact());
+#pragma unroll 4
+                        for (int i = t; i < n; i += CONSUMERS) {
+                            Unit<T> v;
+                            v.v = part[i];
+                            Words<T, PER> w;
+#pragma unroll
+                            for (int j = 0; j < PER / 2; ++j) {
+                                const float2 f = halves(mul2(shift.exp(v.get(j)), factor));
+                                w.set(j, f.x, f.y);
+                            }
+                            *reinterpret_cast<uint4 *>(out + in.first(u + i)) = make_uint4(w.w[0], w.w[1], w.w[2], w.w[3]);
+                        }
+                    } else {
+                        const T *from = reinterpret_cast<const T *>(part);
+                        const int64_t first = in.first(u);
+                        for (int i = t; i < n * PER; i += CONSUMERS) out[first + i] = value(to_f(from[i]));
+                    }
+                    if (last) {
+                        if (edge >= 0) out[edge] = value(h.edge[t]);
+                        sync();  // over what has been written: the teacher's tokens,
+                        if (h.taught) {
+                            for (int k = CONSUMERS - 1 - t; k < K; k += CONSUMERS) {  // (the first warp has the loss to do)
+                                const int32_t token = token_of[k];
+                                // the rank that has written the token's place
+                                const bool outside = token < in.head || token >= in.V - in.tail;
+                                const int at = (token - in.head) / PER;
+                                if (token < 0 || (outside ? rank != 0 : at < u0 || at >= end)) continue;
+                                float q = 0.f;
+                                bool first = true;  // a token that comes twice counts twice, and is written once
+                                for (int j = 0; j < K; j += 4) {
+                                    const int4 four = *reinterpret_cast<const int4 *>(token_of + j);
+                                    const int same = (four.x == token ? 1 : 0) | (four.y == token ? 2 : 0) | (four.z == token ? 4 : 0) |
+                                                     (four.w == token ? 8 : 0);
+                                    if (same != 0)
+                                        for (int i = 0; i < 4; ++i)
+                                            if ((same >> i & 1) != 0) {
+                                                first = first && j + i >= k;
+                                                q += q_of[j + i];
+                                            }
+                                }
+                                if (first) out[token] = from_f<T>(exp2_fast((z_of[k] - st.m) * c) * scale - q * h.weight);
+                            }
+                        } else {
+                            clear();  // or, where there is nothing to learn from, zeros
+                        }
+                    }
+                }
+                if (PART != Part::Grad && last && rank == 0 && t < 32) {
+                    float cross = 0.f;
+                    if (h.taught)
+                        for (int k = lane; k < K; k += 32) {
+                            const float q = q_of[k];
+                            if (!(q == 0.f)) cross += q * ((z_of[k] - st.m) * rtau);
+                        }
+                    cross = warp_sum(cross);
+                    if (lane == 0) {
+                        o.loss[row] = h.taught ? h.entropy - cross + logf(st.s) : 0.f;
+                        if (o.normalizers != nullptr) reinterpret_cast<float2 *>(o.normalizers)[row] = make_float2(st.m, st.s);
+                    }
+                }
+                release();
+                if (last) break;
+                u += n;
+            }
+        }
+    }
+    __syncwarp();
+    leave(&gave_up, &g_timed_out);
+}
+
+// Threads that take a row's sums and the bytes of a stage: larger ones for
+// longer rows, so that what a row costs beside its bytes (the reduction, the
+// hand-over) stays in proportion, as many blocks an SM as fit beside each
+// other.  Both parts of a stage's pair hold a row, or a block's slice of one.
+struct Plan {
+    int consumers, stage_units, ranks;
+    bool cluster;
+};
+constexpr int kStageUnits[] = {256, 768, 1536, 3000};  // of 32, 64, 128 and 256 consumers: 4, 12, 24 and 47 KB
+constexpr int kWideUnits = 6400;                       // one block an SM: 100 KB
+constexpr int kMostConsumers = 256;
+
+// Units of 16 bytes that a row may have
+int64_t most_units(const rlscan_distill_args &a) { return a.V / (a.dtype == RLSCAN_BF16 ? 8 : 4); }
+
+// Part::Both keeps a block's slice of a row in one stage; the others split rows
+// while there are too few of them to give every SM two blocks.
+Plan plan(const rlscan_distill_args &a, Part part)
 {
     const int64_t units = most_units(a), rows = a.N * a.T, sms = sm_count() > 0 ? sm_count() : 152;
-    if (units <= 32 * kUnits) return {32, 1};
-    if (units <= 128 * kUnits) return {128, 1};
-    int ranks = 1;
-    while (ranks < kGatedCluster &&
-           ((hold && ceil_div(units, ranks) > 512 * kUnits) || (rows * ranks < 2 * sms && ceil_div(units, ranks) > 512)))
-        ranks *= 2;
-    return {512, ranks};
+    if (units <= kStageUnits[0]) return {32, kStageUnits[0], 1, false};
+    if (units <= kStageUnits[1]) return {64, kStageUnits[1], 1, false};
+    if (units <= kStageUnits[2]) return {128, kStageUnits[2], 1, false};
+    Plan p{kMostConsumers, kStageUnits[3], 1, false};
+    if (part == Part::Both) {
+        if (units > int64_t{kGatedCluster} * p.stage_units) p.stage_units = kWideUnits;
+        p.ranks = static_cast<int>(ceil_div(units, p.stage_units));
+    }
+    while (2 * p.ranks <= kGatedCluster && rows * p.ranks < 2 * sms && ceil_div(units, p.ranks) > 512) p.ranks *= 2;
+    p.cluster = p.ranks > 1 && part != Part::Grad;
+    return p;
+}
+
+template <class T, int CONSUMERS, Part PART, bool CLUSTER>
+rlscan_status launch_stream(const rlscan_distill_args &a, const DistillOut &o, Plan p, cudaStream_t s)
+{
+    auto kernel = distill_kernel<T, CONSUMERS, PART, CLUSTER>;
+    // as much shared memory as any call of this kernel takes, for the limit and for the blocks that fit
+    const bool wide = p.stage_units == kWideUnits;
+    const size_t stages = static_cast<size_t>(kStages) * p.stage_units * 16, smem = stages + kStages * 12 * ((a.K + 3) / 4 * 4);
+    const size_t limit = static_cast<size_t>(kStages) * (CONSUMERS == kMostConsumers ? kWideUnits : p.stage_units) * 16 + kStages * 12 * kMostTeacher;
+    static PerDevice raised, resident[2][kGatedCluster + 1];
+    const int device = current_device();
+    if (raised.get(device, [&] {
+            return ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(limit))) ? 1 : 0;
+        }) <= 0)
+        return RLSCAN_ERR_CUDA;
+    const int cluster = CLUSTER ? p.ranks : 1;
+    const int groups_fit = resident[wide ? 1 : 0][cluster].get(device, [&] {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+        cfg.blockDim = dim3(CONSUMERS + 32);
+        cfg.dynamicSmemBytes = stages + kStages * 12 * 64;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        return ok(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) ? n : 0;
+    });
+    const int64_t rows = a.N * a.T, fit = groups_fit > 0 ? groups_fit : 1;
+    int64_t groups = CLUSTER ? fit : fit / p.ranks;  // that share a row
+    groups = groups < 1 ? 1 : groups < rows ? groups : rows;
+    return launch_cluster(groups * p.ranks <= sm_count(), kernel, groups * p.ranks, CONSUMERS + 32, smem, cluster, s, a, o, p.ranks, p.stage_units);
 }
 
 template <class T, Part PART>
-rlscan_status run(const rlscan_distill_args &a, const DistillOut &o, Plan p, cudaStream_t s)
+rlscan_status run(const rlscan_distill_args &a, const DistillOut &o, cudaStream_t s)
 {
-    const int64_t rows = a.N * a.T;
-    if (p.threads == 32)
-        return launch_overlapped(distill_kernel<T, 32, kUnits, PART, false>, ceil_div(rows, 4), 128, 0, s, a, o, 1);
-    if (p.threads == 128)
-        return launch_overlapped(distill_kernel<T, 128, kUnits, PART, false>, rows * p.ranks, 128, 0, s, a, o, p.ranks);
-    if constexpr (PART == Part::Grad) {
-        return launch_overlapped(distill_kernel<T, 512, kUnits, PART, false>, rows * p.ranks, 512, 0, s, a, o, p.ranks);
-    } else {
-        if (p.ranks > 1)
-            return launch_cluster(distill_kernel<T, 512, kUnits, PART, true>, rows * p.ranks, 512, 0, p.ranks, s, a, o, p.ranks);
-        return launch_overlapped(distill_kernel<T, 512, kUnits, PART, false>, rows, 512, 0, s, a, o, 1);
+    const Plan p = plan(a, PART);
+    switch (p.consumers) {
+    case 32: return launch_stream<T, 32, PART, false>(a, o, p, s);
+    case 64: return launch_stream<T, 64, PART, false>(a, o, p, s);
+    case 128: return launch_stream<T, 128, PART, false>(a, o, p, s);
+    default:
+        if constexpr (PART != Part::Grad)
+            if (p.cluster) return launch_stream<T, kMostConsumers, PART, true>(a, o, p, s);
+        return launch_stream<T, kMostConsumers, PART, false>(a, o, p, s);
     }
 }
 
 template <Part PART>
-rlscan_status run_typed(const rlscan_distill_args &a, const DistillOut &o, Plan p, cudaStream_t s)
+rlscan_status run_typed(const rlscan_distill_args &a, const DistillOut &o, cudaStream_t s)
 {
-    return a.dtype == RLSCAN_BF16 ? run<bf16, PART>(a, o, p, s) : run<float, PART>(a, o, p, s);
+    return a.dtype == RLSCAN_BF16 ? run<bf16, PART>(a, o, s) : run<float, PART>(a, o, s);
 }
 
 }  // namespace
 
-rlscan_status launch_distill(const rlscan_distill_args &a, const DistillOut &o, cudaStream_t s)
-{
-    return run_typed<Part::Loss>(a, o, plan(a, false), s);
-}
+rlscan_status launch_distill(const rlscan_distill_args &a, const DistillOut &o, cudaStream_t s) { return run_typed<Part::Loss>(a, o, s); }
 
 rlscan_status launch_distill_backward(const rlscan_distill_args &a, const DistillOut &o, cudaStream_t s)
 {
-    Plan p = plan(a, false);
-    if (p.threads == 512) p.ranks = static_cast<int>(ceil_div(most_units(a), 512 * kUnits));
-    return run_typed<Part::Grad>(a, o, p, s);
+    return run_typed<Part::Grad>(a, o, s);
 }
 
-bool distill_fits(const rlscan_distill_args &a) { return most_units(a) <= static_cast<int64_t>(kGatedCluster) * 512 * kUnits; }
+bool distill_fits(const rlscan_distill_args &a) { return most_units(a) <= int64_t{kGatedCluster} * kWideUnits; }
 
-rlscan_status launch_distill_both(const rlscan_distill_args &a, const DistillOut &o, cudaStream_t s)
-{
-    return run_typed<Part::Both>(a, o, plan(a, true), s);
-}
+rlscan_status launch_distill_both(const rlscan_distill_args &a, const DistillOut &o, cudaStream_t s) { return run_typed<Part::Both>(a, o, s); }
+
+rlscan_status distill_status(cudaStream_t s) { return take_flag(g_timed_out, s); }
 
 }  // namespace seq
 }  // namespace rlscan

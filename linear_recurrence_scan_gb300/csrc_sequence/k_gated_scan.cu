@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(32 * kGatedWarps, sizeof(T) == 2 && VEC ? 3 : 
     forward_kernel(const __grid_constant__ rlscan_gated_scan_args a, const __grid_constant__ ForwardArgs o, int ranks)
 {
     constexpr int TILE = kGatedTile, TOK = TILE / kGatedWarps;
-    __shared__ Chain<CLUSTER> chain;
-    __shared__ std::conditional_t<CLUSTER, Exchange, char> exchange;
+    __shared__ Chain chain;
+    __shared__ std::conditional_t<CLUSTER, Exchange<kGatedCluster>, char> exchange;
     __shared__ int gave_up;
     ptx::pdl_trigger_dependents();
     if (threadIdx.x == 0) {
@@ -92,12 +92,12 @@ __global__ void __launch_bounds__(32 * kGatedWarps, sizeof(T) == 2 && VEC ? 3 : 
     const Decay decays(load_two<VEC>(a.log_decay + l.block + l.d, l.on0, l.on1));
     f2 carry = a.initial_state != nullptr ? load_two<VEC>(a.initial_state + k.n * a.D + l.block + l.d, l.on0, l.on1) : both(0.f);
     Two<T, VEC> x[TOK], g[TOK], ig[TOK];
-    uint32_t reset = 0;
+    uint32_t flag = 0;
     auto fetch = [&](int64_t t0) {
         fetch_tokens(g, a.gate, k.n, t0, k.len, l);
         fetch_tokens(ig, a.input_gate, k.n, t0, k.len, l);
         fetch_tokens(x, a.x, k.n, t0, k.len, l);
-        reset = fetch_resets<TOK>(a.resets, k.n * a.T, t0, k.len, k.lane);
+        flag = fetch_flag<TOK>(a.resets, k.n * a.T, t0, k.len, k.lane);
     };
     if (k.steps > 0) fetch(static_cast<int64_t>(k.rank) * TILE + k.w * TOK);
     if constexpr (CLUSTER) cluster_wait();
@@ -111,12 +111,12 @@ __global__ void __launch_bounds__(32 * kGatedWarps, sizeof(T) == 2 && VEC ? 3 : 
             keep[i] = v.a;
             b[i] = mul2(mul2(v.root, v.i), x[i].get());
         }
-        cut_and_pad(keep, b, reset, t0, k.len);
+        cut_and_pad(keep, b, starts(flag), t0, k.len);
         if (s + 1 < k.steps) fetch(t0 + k.span);
         fold(keep, b, A, B);
         chain.put(p, k.w, k.lane, A, B);
         __syncthreads();
-        Exchange *ex = nullptr;
+        Exchange<kGatedCluster> *ex = nullptr;
         if constexpr (CLUSTER) ex = &exchange;
         f2 h = in_front<CLUSTER, true>(chain, ex, s, k.w, k.lane, k.rank, ranks, carry, &gave_up);
         if (o.checkpoints != nullptr && k.w % (RLSCAN_GATED_SCAN_CHECKPOINT / TOK) == 0 && t0 < a.T) {
@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 3)
     constexpr int TOK = ForwardTile<T>::TOK, TILE = ForwardTile<T>::TOKENS;
     constexpr uint32_t BYTES = ForwardTile<T>::BYTES;
     extern __shared__ char raw[];
-    __shared__ Chain<CLUSTER> chain;
-    __shared__ std::conditional_t<CLUSTER, Exchange, char> exchange;
+    __shared__ Chain chain;
+    __shared__ std::conditional_t<CLUSTER, Exchange<kGatedCluster>, char> exchange;
     __shared__ uint64_t full[2];
     __shared__ int gave_up;
     ptx::pdl_trigger_dependents();
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 3)
     }
     const Decay decays(load_two<true>(a.log_decay + l.block + l.d, l.on0, l.on1));
     f2 carry = a.initial_state != nullptr ? load_two<true>(a.initial_state + k.n * a.D + l.block + l.d, l.on0, l.on1) : both(0.f);
-    uint32_t reset = fetch_resets<TOK>(a.resets, k.n * a.T, static_cast<int64_t>(k.rank) * TILE + k.w * TOK, k.len, k.lane);
+    uint32_t flag = fetch_flag<TOK>(a.resets, k.n * a.T, static_cast<int64_t>(k.rank) * TILE + k.w * TOK, k.len, k.lane);
     if constexpr (CLUSTER) cluster_wait();
     const uint32_t mine = k.w * TOK * kGatedWidth * sizeof(T) + l.d * sizeof(T);  // of the lane, in a tile
     char *out = stages + 2 * 3 * BYTES;
@@ -221,13 +221,13 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 3)
             keep[i] = v.a;
             b[i] = mul2(mul2(v.root, v.i), read_two<T>(in + 2 * BYTES + i * STEP));
         }
-        cut_and_pad(keep, b, reset, t0, k.len);
-        if (s + 1 < k.steps) reset = fetch_resets<TOK>(a.resets, k.n * a.T, t0 + k.span, k.len, k.lane);
+        cut_and_pad(keep, b, starts(flag), t0, k.len);
+        if (s + 1 < k.steps) flag = fetch_flag<TOK>(a.resets, k.n * a.T, t0 + k.span, k.len, k.lane);
         fold(keep, b, A, B);
         chain.put(p, k.w, k.lane, A, B);
         __syncthreads();  // all have taken the stage's values
         if (threadIdx.x == 0 && s + 2 < k.steps) fetch(s + 2);
-        Exchange *ex = nullptr;
+        Exchange<kGatedCluster> *ex = nullptr;
         if constexpr (CLUSTER) ex = &exchange;
         f2 h = in_front<CLUSTER, true>(chain, ex, s, k.w, k.lane, k.rank, ranks, carry, &gave_up);
         if (o.checkpoints != nullptr && k.w % (RLSCAN_GATED_SCAN_CHECKPOINT / TOK) == 0 && t0 < a.T) {
@@ -318,14 +318,14 @@ rlscan_status forward_typed(const rlscan_gated_scan_args &a, const ForwardArgs &
             !gated_map<T>(&m.y, o.y, a.T * a.D, a.D, a.N, a.T, a.D, Tile::TOK))
             return RLSCAN_ERR_CUDA;
         const int ranks = gated_cluster<T, 2>(tiled_forward_kernel<T, true>, chains, a.T, Tile::TOKENS, Tile::SMEM);
-        return ranks > 1 ? launch_cluster(tiled_forward_kernel<T, true>, chains * ranks, threads, Tile::SMEM, ranks, s, a, o, m, ranks)
-                         : launch_cluster(tiled_forward_kernel<T, false>, chains, threads, Tile::SMEM, 1, s, a, o, m, 1);
+        return ranks > 1 ? launch_cluster(chains * ranks <= sm_count(), tiled_forward_kernel<T, true>, chains * ranks, threads, Tile::SMEM, ranks, s, a, o, m, ranks)
+                         : launch_cluster(chains <= sm_count(), tiled_forward_kernel<T, false>, chains, threads, Tile::SMEM, 1, s, a, o, m, 1);
     }
     auto go = [&](auto pairs) {
         constexpr bool VEC = decltype(pairs)::value;
         const int ranks = gated_cluster<T, VEC>(forward_kernel<T, VEC, true>, chains, a.T, kGatedTile, 0);
-        return ranks > 1 ? launch_cluster(forward_kernel<T, VEC, true>, chains * ranks, threads, 0, ranks, s, a, o, ranks)
-                         : launch_cluster(forward_kernel<T, VEC, false>, chains, threads, 0, 1, s, a, o, 1);
+        return ranks > 1 ? launch_cluster(chains * ranks <= sm_count(), forward_kernel<T, VEC, true>, chains * ranks, threads, 0, ranks, s, a, o, ranks)
+                         : launch_cluster(chains <= sm_count(), forward_kernel<T, VEC, false>, chains, threads, 0, 1, s, a, o, 1);
     };
     return access != Access::Values ? go(std::true_type()) : go(std::false_type());
 }

@@ -49,7 +49,7 @@ __device__ __forceinline__ TokenGrads token_grads(const Gates &v, f2 keep, f2 x,
 // gradient, the block's share of dlog_decay (its warps' in order).
 template <class T, bool VEC, int TILE, bool CLUSTER>
 __device__ __forceinline__ void finish(const rlscan_gated_scan_args &a, const BackwardArgs &o, const Walk &k, int ranks, const Lane<VEC> &l,
-                                       f2 carry, f2 sum, Chain<CLUSTER> &chain)
+                                       f2 carry, f2 sum, TwoChains &chain)
 {
     constexpr int TOK = TILE / kGatedWarps;
     for (int64_t tile = k.steps * ranks + k.rank; tile < k.tiles; tile += ranks) {
@@ -66,7 +66,7 @@ __device__ __forceinline__ void finish(const rlscan_gated_scan_args &a, const Ba
         store_two<float, VEC>(o.g.initial_state + k.n * a.D + l.block + l.d, carry, l.on0, l.on1);
     if (o.parts == nullptr) return;
     __syncthreads();
-    chain.put(0, k.w, k.lane, sum, sum);
+    chain.put(0, k.w, k.lane, sum, sum, sum);
     __syncthreads();
     if (k.w == 0) {
         f2 all = both(0.f);
@@ -83,9 +83,8 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
     backward_kernel(const __grid_constant__ rlscan_gated_scan_args a, const __grid_constant__ BackwardArgs o, int ranks)
 {
     constexpr int TILE = kBackTile, TOK = TILE / kGatedWarps;
-    __shared__ float4 state_map[2][kGatedWarps][32];
-    __shared__ Chain<CLUSTER> chain;
-    __shared__ std::conditional_t<CLUSTER, Exchange, char> exchange;
+    __shared__ TwoChains chain;
+    __shared__ std::conditional_t<CLUSTER, Exchange<kGatedCluster>, char> exchange;
     __shared__ int gave_up;
     ptx::pdl_trigger_dependents();
     if (threadIdx.x == 0) {
@@ -104,14 +103,14 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
     f2 sum = both(0.f);  // the lane's share of dlog_decay
     Two<T, VEC> x[TOK], g[TOK], ig[TOK], gy[TOK];
     Two<float, VEC> mark;
-    uint32_t reset = 0;
+    uint32_t flag = 0;
     auto fetch = [&](int64_t tile) {
         const int64_t t0 = tile * TILE + k.w * TOK;
         fetch_tokens(g, a.gate, k.n, t0, k.len, l);
         fetch_tokens(ig, a.input_gate, k.n, t0, k.len, l);
         fetch_tokens(x, a.x, k.n, t0, k.len, l);
         fetch_tokens(gy, o.grad_y, k.n, t0, k.len, l);
-        reset = fetch_resets<TOK>(a.resets, k.n * a.T, t0, k.len, k.lane);
+        flag = fetch_flag<TOK>(a.resets, k.n * a.T, t0, k.len, k.lane);
         mark.zero();
         if (tile < k.tiles) mark.load(o.checkpoints + (k.n * k.tiles + tile) * a.D + l.block + l.from, l.apart);
     };
@@ -122,7 +121,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
         const int p = static_cast<int>(turn & 1);
         Gates v[TOK];
         f2 xs[TOK], gs[TOK], keep[TOK], b[TOK];
-        const uint32_t cut = reset;
+        const uint32_t cut = starts(flag);
         f2 state = mark.get();
 #pragma unroll
         for (int i = 0; i < TOK; ++i) {
@@ -151,17 +150,13 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
             B = fma2(keep[i], B, b[i]);
             M = mul2(keep[TOK - 1 - i], add2(gs[TOK - 1 - i], M));
         }
-        {
-            const float2 fa = halves(A), fb = halves(B);
-            state_map[p][k.w][k.lane] = make_float4(fa.x, fa.y, fb.x, fb.y);
-        }
-        chain.put(p, k.w, k.lane, A, M);
+        chain.put(p, k.w, k.lane, A, B, M);
         __syncthreads();
-        Exchange *ex = nullptr;
+        Exchange<kGatedCluster> *ex = nullptr;
         if constexpr (CLUSTER) ex = &exchange;
         f2 m = in_front<CLUSTER, false>(chain, ex, turn, k.w, k.lane, k.rank, ranks, carry, &gave_up);
 #pragma unroll 1
-        for (int q = 0; q < k.w; ++q) state = apply(state, state_map[p][q][k.lane]);
+        for (int q = 0; q < k.w; ++q) state = apply(state, chain.map[p][q][k.lane]);
         f2 before[TOK];  // the state before each token
 #pragma unroll
         for (int i = 0; i < TOK; ++i) {
@@ -194,9 +189,14 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
     leave(&gave_up, &g_timed_out);
 }
 
-// Arrays that tensor maps take: the inputs of a step come into shared memory
-// while the step behind it is worked on, and what the gradients need again (x,
-// grad_y) is read again from there.  The gradients leave through shared memory.
+// Arrays that tensor maps take: two steps' inputs are on their way into shared
+// memory while a third's are worked on; what the gradients need again (x,
+// grad_y) is read again from there, and each gradient leaves from its input's
+// place, which the same lane has read.  With two steps in shared memory, one of
+// them on its way, the bytes in flight bound the kernel (8 x 2048 x 4096: 226
+// to 253 us).  Two blocks an SM leave 17 KB for the maps, which is why at most
+// four blocks share a row here.
+constexpr int kBackCluster = 4, kBackStages = 3;
 struct BackwardMaps {
     CUtensorMap x, gate, input_gate, grad_y, dx, dgate, dinput_gate;
 };
@@ -204,7 +204,7 @@ template <class T>
 struct BackwardTile {
     static constexpr int TOK = 16 / static_cast<int>(sizeof(T)), TOKENS = TOK * kGatedWarps;
     static constexpr uint32_t BYTES = TOKENS * kGatedWidth * sizeof(T);  // of one array
-    static constexpr size_t SMEM = 2 * 4 * BYTES + 3 * BYTES + 128;      // two stages, three gradients
+    static constexpr size_t SMEM = kBackStages * 4 * BYTES + 128;
 };
 
 template <class T, bool CLUSTER>
@@ -215,17 +215,15 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
     constexpr int TOK = BackwardTile<T>::TOK, TILE = BackwardTile<T>::TOKENS, STEP = kGatedWidth * sizeof(T);
     constexpr uint32_t BYTES = BackwardTile<T>::BYTES;
     extern __shared__ char raw[];
-    __shared__ float4 state_map[2][kGatedWarps][32];
-    __shared__ Chain<CLUSTER> chain;
-    __shared__ std::conditional_t<CLUSTER, Exchange, char> exchange;
-    __shared__ uint64_t full[2];
+    __shared__ TwoChains chain;
+    __shared__ std::conditional_t<CLUSTER, Exchange<kBackCluster>, char> exchange;
+    __shared__ uint64_t full[kBackStages];
     __shared__ int gave_up;
     ptx::pdl_trigger_dependents();
     char *stages = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 127) & ~static_cast<uintptr_t>(127));
     if (threadIdx.x == 0) {
         gave_up = 0;
-        ptx::mbar_init(&full[0], 1);
-        ptx::mbar_init(&full[1], 1);
+        for (int i = 0; i < kBackStages; ++i) ptx::mbar_init(&full[i], 1);
         if constexpr (CLUSTER) exchange.init();
         ptx::fence_mbar_init();
     }
@@ -236,8 +234,8 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
     const Walk k = walk<TILE, CLUSTER>(a, ranks, block);
     const Lane<true> l(block, k.lane, a.D);
     const int x0 = static_cast<int>(l.block), row = static_cast<int>(k.n);
-    auto fetch = [&](int64_t turn) {  // by one thread
-        const int st = static_cast<int>(turn & 1), t = static_cast<int>(((k.steps - 1 - turn) * ranks + k.rank) * TILE);
+    auto fetch = [&](int64_t turn, int st) {  // by one thread
+        const int t = static_cast<int>(((k.steps - 1 - turn) * ranks + k.rank) * TILE);
         const uint32_t at = ptx::smem_u32(stages) + st * 4 * BYTES, bar = ptx::smem_u32(&full[st]);
         ptx::mbar_arrive_expect_tx(&full[st], 4 * BYTES);
         load_box3(at, &maps.gate, x0, t, row, bar);
@@ -247,10 +245,10 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
     };
     const int64_t marks = gated_marks(a.T);
     f2 mark = both(0.f);
-    uint32_t reset = 0;
+    uint32_t flag = 0;
     auto look = [&](int64_t turn) {  // the step's checkpoint and resets
         const int64_t t = ((k.steps - 1 - turn) * ranks + k.rank) * TILE;
-        reset = fetch_resets<TOK>(a.resets, k.n * a.T, t + k.w * TOK, k.len, k.lane);
+        flag = fetch_flag<TOK>(a.resets, k.n * a.T, t + k.w * TOK, k.len, k.lane);
         const int64_t i = t / RLSCAN_GATED_SCAN_CHECKPOINT;
         mark = load_two<true>(o.checkpoints + (k.n * marks + i) * a.D + l.block + l.d, i < marks && l.on0, i < marks && l.on1);
     };
@@ -259,17 +257,21 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
     f2 carry = o.grad_final != nullptr ? load_two<true>(o.grad_final + k.n * a.D + l.block + l.d, l.on0, l.on1) : both(0.f);
     f2 sum = both(0.f);  // the lane's share of dlog_decay
     if (k.steps > 0) {
-        if (threadIdx.x == 0) fetch(0);
+        if (threadIdx.x == 0) {
+            fetch(0, 0);
+            if (k.steps > 1) fetch(1, 1);
+        }
         look(0);
     }
     if constexpr (CLUSTER) cluster_wait();
     const uint32_t mine = k.w * TOK * STEP + l.d * sizeof(T);  // of the lane, in a tile
-    char *out = stages + 2 * 4 * BYTES;
+    int stage = 0;
+    uint32_t parity = 0;
     for (int64_t turn = 0; turn < k.steps; ++turn) {
         const int64_t t0 = ((k.steps - 1 - turn) * ranks + k.rank) * TILE + k.w * TOK;
         const int p = static_cast<int>(turn & 1);
-        wait(ptx::smem_u32(&full[p]), static_cast<uint32_t>(turn >> 1) & 1u, &gave_up);
-        char *in = stages + p * 4 * BYTES + mine;
+        wait(ptx::smem_u32(&full[stage]), parity, &gave_up);
+        char *in = stages + stage * 4 * BYTES + mine;
         const bool pad = t0 + TOK > k.len;
         if (pad) {  // x and grad_y of padding count 0
 #pragma unroll 1
@@ -281,63 +283,67 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
             fence_async();  // in front of the copy that takes the stage next
         }
         Gates v[TOK];
-        const uint32_t cut = reset;
-        f2 state = mark, A = both(1.f), B = both(0.f), M = both(0.f);
 #pragma unroll
         for (int i = 0; i < TOK; ++i) v[i] = gates(read_two<T>(in + i * STEP), read_two<T>(in + BYTES + i * STEP), decays);
-        auto keep = [&](int i) { return (cut >> i & 1u) != 0u ? both(0.f) : v[i].a; };
+        const uint32_t cut = starts(flag);
+        f2 state = mark, A = both(1.f), B = both(0.f), M = both(0.f);
         if (pad) {  // and hands state and message on
 #pragma unroll
             for (int i = 0; i < TOK; ++i)
                 if (t0 + i >= k.len) v[i].a = both(1.f), v[i].root = both(0.f);
         }
+        // Steps without a reset, which are most, take a path of their own: the
+        // decays that a reset cuts would otherwise be kept beside the others.
+        auto fold = [&](auto cutting) {
+            auto keep = [&](int i) { return decltype(cutting)::value && (cut >> i & 1u) != 0u ? both(0.f) : v[i].a; };
 #pragma unroll
-        for (int i = 0; i < TOK; ++i) {
-            A = mul2(A, keep(i));
-            B = fma2(keep(i), B, mul2(mul2(v[i].root, v[i].i), read_two<T>(in + 2 * BYTES + i * STEP)));
-        }
+            for (int i = 0; i < TOK; ++i) {
+                A = mul2(A, keep(i));
+                B = fma2(keep(i), B, mul2(mul2(v[i].root, v[i].i), read_two<T>(in + 2 * BYTES + i * STEP)));
+            }
 #pragma unroll
-        for (int i = TOK - 1; i >= 0; --i) M = mul2(keep(i), add2(read_two<T>(in + 3 * BYTES + i * STEP), M));
-        {
-            const float2 fa = halves(A), fb = halves(B);
-            state_map[p][k.w][k.lane] = make_float4(fa.x, fa.y, fb.x, fb.y);
-        }
-        chain.put(p, k.w, k.lane, A, M);
-        __syncthreads();  // the step behind has been worked on: its stage takes the step in front
-        if (turn + 1 < k.steps) {
-            if (threadIdx.x == 0) fetch(turn + 1);
-            look(turn + 1);
-        }
-        Exchange *ex = nullptr;
+            for (int i = TOK - 1; i >= 0; --i) M = mul2(keep(i), add2(read_two<T>(in + 3 * BYTES + i * STEP), M));
+        };
+        if (cut == 0) fold(std::false_type());
+        else fold(std::true_type());
+        chain.put(p, k.w, k.lane, A, B, M);
+        if (k.lane == 0) stores_read();  // the step behind has left its stage,
+        __syncthreads();                 // all of it: the stage takes the step after next
+        const int behind = stage == 0 ? kBackStages - 1 : stage - 1;
+        if (threadIdx.x == 0 && turn + 2 < k.steps) fetch(turn + 2, behind);
+        Exchange<kBackCluster> *ex = nullptr;
         if constexpr (CLUSTER) ex = &exchange;
         f2 m = in_front<CLUSTER, false>(chain, ex, turn, k.w, k.lane, k.rank, ranks, carry, &gave_up);
 #pragma unroll 1
-        for (int q = 0; q < k.w; ++q) state = apply(state, state_map[p][q][k.lane]);
-        f2 before[TOK];  // the state before each token
+        for (int q = 0; q < k.w; ++q) state = apply(state, chain.map[p][q][k.lane]);
+        auto gradients = [&](auto cutting) {
+            auto keep = [&](int i) { return decltype(cutting)::value && (cut >> i & 1u) != 0u ? both(0.f) : v[i].a; };
+            f2 before[TOK];  // the state before each token
 #pragma unroll
-        for (int i = 0; i < TOK; ++i) {
-            before[i] = state;
-            state = fma2(keep(i), state, mul2(mul2(v[i].root, v[i].i), read_two<T>(in + 2 * BYTES + i * STEP)));
-        }
-        if (k.lane == 0) stores_read();  // the step behind has left the warp's part
-        __syncwarp();
+            for (int i = 0; i < TOK; ++i) {
+                before[i] = state;
+                state = fma2(keep(i), state, mul2(mul2(v[i].root, v[i].i), read_two<T>(in + 2 * BYTES + i * STEP)));
+            }
 #pragma unroll
-        for (int i = TOK - 1; i >= 0; --i) {
-            TokenGrads t = token_grads(v[i], keep(i), read_two<T>(in + 2 * BYTES + i * STEP), read_two<T>(in + 3 * BYTES + i * STEP),
-                                       before[i], log_decay, m);
-            if (pad && t0 + i >= k.len) t.x = t.gate = t.input_gate = t.share = both(0.f);
-            sum = add2(sum, t.share);
-            write_two<T>(out + mine + i * STEP, t.x);
-            write_two<T>(out + BYTES + mine + i * STEP, t.gate);
-            write_two<T>(out + 2 * BYTES + mine + i * STEP, t.input_gate);
-        }
+            for (int i = TOK - 1; i >= 0; --i) {
+                TokenGrads t = token_grads(v[i], keep(i), read_two<T>(in + 2 * BYTES + i * STEP), read_two<T>(in + 3 * BYTES + i * STEP),
+                                           before[i], log_decay, m);
+                if (pad && t0 + i >= k.len) t.x = t.gate = t.input_gate = t.share = both(0.f);
+                sum = add2(sum, t.share);
+                write_two<T>(in + i * STEP, t.gate);
+                write_two<T>(in + BYTES + i * STEP, t.input_gate);
+                write_two<T>(in + 2 * BYTES + i * STEP, t.x);
+            }
+        };
+        if (cut == 0) gradients(std::false_type());
+        else gradients(std::true_type());
         fence_async();
         __syncwarp();
         if (k.lane == 0 && t0 < a.T) {
-            const uint32_t from = ptx::smem_u32(out) + k.w * TOK * STEP;
-            store_box3(&maps.dx, x0, static_cast<int>(t0), row, from);
-            store_box3(&maps.dgate, x0, static_cast<int>(t0), row, from + BYTES);
-            store_box3(&maps.dinput_gate, x0, static_cast<int>(t0), row, from + 2 * BYTES);
+            const uint32_t from = ptx::smem_u32(stages) + stage * 4 * BYTES + k.w * TOK * STEP;
+            store_box3(&maps.dgate, x0, static_cast<int>(t0), row, from);
+            store_box3(&maps.dinput_gate, x0, static_cast<int>(t0), row, from + BYTES);
+            store_box3(&maps.dx, x0, static_cast<int>(t0), row, from + 2 * BYTES);
             stores_commit();
         }
         if constexpr (!CLUSTER) {
@@ -346,6 +352,8 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
                 carry = m;
             }
         }
+        if (turn + 1 < k.steps) look(turn + 1);  // here, where registers are free; looked at behind the gates
+        if (++stage == kBackStages) stage = 0, parity ^= 1u;
     }
     finish<T, true, TILE, CLUSTER>(a, o, k, ranks, l, carry, sum, chain);
     if (k.lane == 0) stores_read();
@@ -372,17 +380,17 @@ rlscan_status backward_typed(const rlscan_gated_scan_args &a, const BackwardArgs
         if (!in(&m.x, a.x) || !in(&m.gate, a.gate) || !in(&m.input_gate, a.input_gate) || !in(&m.grad_y, o.grad_y) ||
             !out(&m.dx, o.g.x) || !out(&m.dgate, o.g.gate) || !out(&m.dinput_gate, o.g.input_gate))
             return RLSCAN_ERR_CUDA;
-        const int ranks = gated_cluster<T, 2>(tiled_backward_kernel<T, true>, chains, a.T, Tile::TOKENS, Tile::SMEM);
+        const int ranks = gated_cluster<T, 2>(tiled_backward_kernel<T, true>, chains, a.T, Tile::TOKENS, Tile::SMEM, kBackCluster);
         parts = a.N * ranks;
-        return ranks > 1 ? launch_cluster(tiled_backward_kernel<T, true>, chains * ranks, threads, Tile::SMEM, ranks, s, a, o, m, ranks)
-                         : launch_cluster(tiled_backward_kernel<T, false>, chains, threads, Tile::SMEM, 1, s, a, o, m, 1);
+        return ranks > 1 ? launch_cluster(chains * ranks <= sm_count(), tiled_backward_kernel<T, true>, chains * ranks, threads, Tile::SMEM, ranks, s, a, o, m, ranks)
+                         : launch_cluster(chains <= sm_count(), tiled_backward_kernel<T, false>, chains, threads, Tile::SMEM, 1, s, a, o, m, 1);
     }
     auto go = [&](auto pairs) {
         constexpr bool VEC = decltype(pairs)::value;
         const int ranks = gated_cluster<T, VEC>(backward_kernel<T, VEC, true>, chains, a.T, kBackTile, 0);
         parts = a.N * ranks;
-        return ranks > 1 ? launch_cluster(backward_kernel<T, VEC, true>, chains * ranks, threads, 0, ranks, s, a, o, ranks)
-                         : launch_cluster(backward_kernel<T, VEC, false>, chains, threads, 0, 1, s, a, o, 1);
+        return ranks > 1 ? launch_cluster(chains * ranks <= sm_count(), backward_kernel<T, VEC, true>, chains * ranks, threads, 0, ranks, s, a, o, ranks)
+                         : launch_cluster(chains <= sm_count(), backward_kernel<T, VEC, false>, chains, threads, 0, 1, s, a, o, 1);
     };
     return access != Access::Values ? go(std::true_type()) : go(std::false_type());
 }
