@@ -10,8 +10,10 @@ namespace rlscan {
 namespace seq {
 
 // ---- waits -----------------------------------------------------------------------
-// A wait that runs out sets the block's flag; the kernel then goes on without
-// waiting (its results are void), sets its file's device flag and ends.
+// A wait that runs out sets the block's flag.  The block then goes on to its end
+// through the same barriers of all its threads, but waits for nothing, asks for
+// no copy and arrives at no mbarrier, whose counts no longer fit; its results
+// are void, and it sets its file's device flag.
 constexpr uint64_t kWaitNs = 4'000'000'000ull;
 
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
@@ -43,11 +45,13 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
     return true;
 }
 
+__device__ __forceinline__ bool has_given_up(const int *gave_up) { return *const_cast<const volatile int *>(gave_up) != 0; }
+
 // At the end of a block, by all its threads: tells the host, and stays until
 // what is in flight (which takes microseconds) has ended.
 __device__ __forceinline__ void leave(const int *gave_up, unsigned int *device_flag)
 {
-    if (*const_cast<const volatile int *>(gave_up) == 0) return;
+    if (!has_given_up(gave_up)) return;
     if (threadIdx.x == 0) atomicExch(device_flag, 1u);
     const uint64_t start = ptx::globaltimer_ns();
     while (ptx::globaltimer_ns() - start < 1'000'000) {

@@ -310,8 +310,10 @@ __device__ __forceinline__ f2 in_front(C &c, E *ex, int64_t turn, int w, int lan
             factor = mul2(factor, pair(m.x, m.y));
             rest = apply(rest, m);
         }
-        if (w < ranks) ex->send(p, rank, w, lane, factor, rest);
-        if (threadIdx.x == 0) ex->expect(p, ranks);
+        if (!has_given_up(gave_up)) {
+            if (w < ranks) ex->send(p, rank, w, lane, factor, rest);
+            if (threadIdx.x == 0) ex->expect(p, ranks);
+        }
         ex->receive(p, static_cast<uint32_t>(turn >> 1) & 1u, gave_up);
 #pragma unroll 1
         for (int i = 0; i < ranks; ++i) {

@@ -125,10 +125,13 @@ struct Head {
     float entropy;     // sum of q log q
     float m, s;        // Part::Grad: the kept maximum and sum
     float weight;      // grad_loss / tau
-    int taught, masked;
+    int taught;
 };
 
 constexpr int kStages = 2;
+constexpr int kStageUnits[] = {256, 768, 1536, 3000};  // of 32, 64, 128 and 256 consumers: 4, 12, 24 and 47 KB
+constexpr int kWideUnits = 6400;                       // one block an SM: 100 KB
+constexpr int kMostConsumers = 256;
 
 __device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
@@ -140,17 +143,20 @@ __device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, uint32_
 // Blocks that stay for many rows.  The last warp runs ahead: it brings the
 // next part of the row's logits into shared memory (one copy a stage) and works
 // out the teacher's probabilities there; CONSUMERS threads take a part's sums
-// and write its gradient.  So copies are in flight while sums, the exchange
-// between blocks and the stores of the row before take their time: with blocks
-// that came and went with their row, held in registers, half of a row's time
-// was spent without a byte in flight (4 x 1023 x 50257, loss and gradient 197
-// us).  Part::Both reads the logits once: a block's slice of a row is one part,
-// CLUSTER: a row is several blocks' slices, whose maxima and sums meet.  Loss
-// and Grad walk a row in several parts.  The maximum starts at the lowest
-// finite number, not at -infinity, so that rows and parts of rows without a
-// finite value need no case of their own (their sum is 0).
+// and write its gradient.  So copies are in flight while sums, the meeting of
+// blocks and the stores of the row before take their time.  Part::Both reads
+// the logits once: a block's slice of a row is one part; CLUSTER: a row is
+// several blocks' slices, whose maxima and sums meet.  Loss and Grad walk
+// longer rows in several parts.  The maximum starts at the lowest finite
+// number, not at -infinity, so that rows and parts of rows without a finite
+// value need no case of their own (their sum is 0).
+// Bound by a row's chain of steps (sums, meeting, gradient), of which an SM has
+// two to fourteen side by side, and by instructions.  Measured, loss and
+// gradient of 4 x 1023 x 50257: blocks that held one row in registers and went
+// with it 197 us, these 165 us; with a row's gradient behind the next row's
+// sums, which takes a third stage and so shorter slices, 187 us.
 template <class T, int CONSUMERS, Part PART, bool CLUSTER>
-__global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 16 : CONSUMERS == 64 ? 8 : CONSUMERS == 128 ? 4 : 2)
+__global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 14 : CONSUMERS == 64 ? 8 : CONSUMERS == 128 ? 4 : 2)
     distill_kernel(const __grid_constant__ rlscan_distill_args a, const __grid_constant__ DistillOut o, int ranks, int stage_units)
 {
     constexpr int WARPS = CONSUMERS / 32, PER = Unit<T>::PER, ROUND = 4;
@@ -195,52 +201,85 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 16 : CONSUME
     auto next = [&] {
         if (++stage == kStages) stage = 0, parity ^= 1u;
     };
-    // The head of a row, by the warp that brings it: the teacher's tokens (-1:
-    // none), q = softmax of its logits over them, the row's logits there.
-    auto teach = [&](Head &h, float *q_of, const Row<T> &in, int64_t row) {
-        float *z_of = q_of + padded;
-        int32_t *token_of = reinterpret_cast<int32_t *>(q_of + 2 * padded);
-        if (lane < padded - K) token_of[K + lane] = -1;
-        if (rank == 0 && in.edge(lane) >= 0) h.edge[lane] = to_f(in.p[in.edge(lane)]);
-        float largest = -INFINITY, sum = 0.f, entropy = 0.f;
-        for (int k = lane; k < K; k += 32) {
+    // Brings rows, by the last warp.
+    auto bring = [&] {
+        // Of the loss of a row of many parts the warp has the next row's first 64
+        // teacher's tokens, their logits and the row's there before the row's
+        // last part: loaded behind that part's copy, one after the other, they
+        // held up the next row's first (8 x 1024 x 131072: 350 us, so 325).
+        // Shorter rows lose by it: theirs are held up in front of the copy.
+        constexpr int AHEAD = PART == Part::Loss && CONSUMERS == kMostConsumers ? 2 : 0;
+        int32_t next_token[AHEAD + 1];
+        float next_x[AHEAD + 1], next_z[AHEAD + 1];
+        auto token_at = [&](int64_t row, int k) -> int32_t {
             const int64_t i = row * K + k;
-            const int64_t token = a.token_bytes == 8 ? static_cast<const int64_t *>(a.teacher_tokens)[i]
-                                                     : static_cast<const int32_t *>(a.teacher_tokens)[i];
-            const float x = a.teacher_dtype == RLSCAN_BF16 ? to_f(static_cast<const bf16 *>(a.teacher_logits)[i])
-                                                           : static_cast<const float *>(a.teacher_logits)[i];
-            const bool valid = token >= 0 && token < a.V;
-            token_of[k] = valid ? static_cast<int32_t>(token) : -1;
-            q_of[k] = valid ? x : -INFINITY;
-            z_of[k] = valid ? to_f(in.p[token]) : 0.f;
-            if (valid) largest = x > largest || x != x ? x : largest;  // a NaN stays
-        }
-        largest = __any_sync(0xffffffffu, largest != largest) ? NAN : warp_max(largest);
-        if (largest != -INFINITY) {
-            for (int k = lane; k < K; k += 32) sum += exp2_fast((q_of[k] - largest) * c);
-            sum = warp_sum(sum);
-            const float log_sum = logf(sum);
-            for (int k = lane; k < K; k += 32) {
-                const float lq = (q_of[k] - largest) * rtau - log_sum, q = exp2_fast((q_of[k] - largest) * c) / sum;
-                if (!(q == 0.f)) entropy += q * lq;
-                q_of[k] = q;
+            const int64_t id = a.token_bytes == 8 ? static_cast<const int64_t *>(a.teacher_tokens)[i]
+                                                  : static_cast<const int32_t *>(a.teacher_tokens)[i];
+            return id >= 0 && id < a.V ? static_cast<int32_t>(id) : -1;
+        };
+        auto logit_at = [&](int64_t row, int k) {
+            const int64_t i = row * K + k;
+            return a.teacher_dtype == RLSCAN_BF16 ? to_f(static_cast<const bf16 *>(a.teacher_logits)[i])
+                                                  : static_cast<const float *>(a.teacher_logits)[i];
+        };
+        auto look = [&](const Row<T> &in, int64_t row) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int k = 32 * i + lane;
+                next_token[i] = k < K ? token_at(row, k) : -1;
+                next_x[i] = k < K ? logit_at(row, k) : 0.f;
             }
-            entropy = warp_sum(entropy);
-        }
-        if (lane == 0) h.taught = largest != -INFINITY, h.entropy = entropy;
-    };
-    if (threadIdx.x >= CONSUMERS) {  // ---- brings rows
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) next_z[i] = next_token[i] >= 0 ? to_f(in.p[next_token[i]]) : 0.f;
+        };
+        // The head of a row: the teacher's tokens (-1: none), q = softmax of its
+        // logits over them, the row's logits there.
+        auto teach = [&](Head &h, float *q_of, const Row<T> &in, int64_t row, bool looked) {
+            float *z_of = q_of + padded;
+            int32_t *token_of = reinterpret_cast<int32_t *>(q_of + 2 * padded);
+            if (lane < padded - K) token_of[K + lane] = -1;
+            if (rank == 0 && in.edge(lane) >= 0) h.edge[lane] = to_f(in.p[in.edge(lane)]);
+            float largest = -INFINITY, sum = 0.f, entropy = 0.f;
+            auto place = [&](int k, int32_t token, float x, float z) {
+                token_of[k] = token;
+                q_of[k] = token >= 0 ? x : -INFINITY;
+                z_of[k] = z;
+                if (token >= 0) largest = x > largest || x != x ? x : largest;  // a NaN stays
+            };
+            if (looked) {
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+                    if (32 * i + lane < K) place(32 * i + lane, next_token[i], next_x[i], next_z[i]);
+            }
+            for (int k = (looked ? 32 * AHEAD : 0) + lane; k < K; k += 32) {
+                const int32_t token = token_at(row, k);
+                place(k, token, logit_at(row, k), token >= 0 ? to_f(in.p[token]) : 0.f);
+            }
+            largest = __any_sync(0xffffffffu, largest != largest) ? NAN : warp_max(largest);
+            if (largest != -INFINITY) {
+                for (int k = lane; k < K; k += 32) sum += exp2_fast((q_of[k] - largest) * c);
+                sum = warp_sum(sum);
+                const float log_sum = logf(sum);
+                for (int k = lane; k < K; k += 32) {
+                    const float lq = (q_of[k] - largest) * rtau - log_sum, q = exp2_fast((q_of[k] - largest) * c) / sum;
+                    if (!(q == 0.f)) entropy += q * lq;
+                    q_of[k] = q;
+                }
+                entropy = warp_sum(entropy);
+            }
+            if (lane == 0) h.taught = largest != -INFINITY, h.entropy = entropy;
+        };
         uint32_t mask = a.mask != nullptr && row0 < rows ? load_byte(a.mask + row0) : 1u;
         for (int64_t row = row0; row < rows; row += stride) {
             const Row<T> in = row_of(row);
             int u0, end;
             slice(in, u0, end);
-            const bool masked = mask == 0u;
+            const bool masked = mask == 0u, ahead = AHEAD > 0 && !masked && end - u0 > 3 * stage_units;
             if (a.mask != nullptr && row + stride < rows) mask = load_byte(a.mask + row + stride);
             for (int u = u0;;) {  // a masked row is one part without logits
                 const int n = masked ? 0 : end - u < stage_units ? end - u : stage_units;
                 const bool last = masked || u + n >= end;
-                wait(ptx::smem_u32(&empty[stage]), parity ^ 1u, &gave_up);
+                if (!wait(ptx::smem_u32(&empty[stage]), parity ^ 1u, &gave_up)) return;
                 if (lane == 0) {
                     if (n > 0) {
                         ptx::mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(n) * 16);
@@ -252,21 +291,24 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 16 : CONSUME
                 }
                 Head &h = heads[stage];
                 if (lane == 0) {
-                    h.masked = masked;
                     if (PART != Part::Loss && !masked) h.weight = o.grad_loss[row] * rtau;
                     if (PART == Part::Grad && !masked) {
                         const float2 kept = reinterpret_cast<const float2 *>(o.normalizers)[row];
                         h.m = kept.x, h.s = kept.y;
                     }
                 }
-                if (last && !masked) teach(h, teacher(stage), in, row);
+                if (last && !masked) teach(h, teacher(stage), in, row, ahead);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&full[stage]);
+                if (ahead && u == u0) look(in, row);
                 next();
                 if (last) break;
                 u += n;
             }
         }
+    };
+    if (threadIdx.x >= CONSUMERS) {
+        bring();
     } else {  // ---- sums and gradients
         const int t = threadIdx.x;
         auto sync = [] {
@@ -275,14 +317,18 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 16 : CONSUME
         };
         auto release = [&] {
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&empty[stage]);
+            if (lane == 0 && !has_given_up(&gave_up)) ptx::mbar_arrive(&empty[stage]);
             next();
         };
         int turn = 0;
+        // What decides which barriers a row takes is read from memory by all.
+        uint32_t mask = a.mask != nullptr && row0 < rows ? load_byte(a.mask + row0) : 1u;
         for (int64_t row = row0; row < rows; row += stride) {
             const Row<T> in = row_of(row);
             int u0, end;
             slice(in, u0, end);
+            const bool masked = mask == 0u;
+            if (a.mask != nullptr && row + stride < rows) mask = load_byte(a.mask + row + stride);
             T *out = static_cast<T *>(o.grad) + row * a.V;
             const bool aligned = (reinterpret_cast<uintptr_t>(out + in.head) & 15u) == 0;  // units of the gradient as of the logits
             const int edge = rank == 0 ? in.edge(t) : -1;                                // the thread's value outside the units
@@ -301,7 +347,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 16 : CONSUME
                 const float *q_of = teacher(stage), *z_of = q_of + padded;
                 const int32_t *token_of = reinterpret_cast<const int32_t *>(q_of + 2 * padded);
                 const uint4 *part = reinterpret_cast<const uint4 *>(buffers + static_cast<size_t>(stage) * stage_units * 16);
-                if (h.masked) {
+                if (masked) {
                     if (PART != Part::Grad && rank == 0 && t == 0) {
                         o.loss[row] = 0.f;
                         if (o.normalizers != nullptr) reinterpret_cast<float2 *>(o.normalizers)[row] = make_float2(0.f, 1.f);
@@ -361,8 +407,9 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 16 : CONSUME
                     st = {m, warp_sum(st.s * exp2_fast((st.m - m) * c))};
                     if constexpr (CLUSTER) {
                         const int mine = rank * WARPS + t / 32;
-                        if (t == 0) ptx::mbar_arrive_expect_tx(&meeting.bar[p], static_cast<uint32_t>(ranks * WARPS) * sizeof(float2));
-                        if (lane < ranks) {
+                        const bool fine = !has_given_up(&gave_up);
+                        if (fine && t == 0) ptx::mbar_arrive_expect_tx(&meeting.bar[p], static_cast<uint32_t>(ranks * WARPS) * sizeof(float2));
+                        if (fine && lane < ranks) {
                             uint32_t to, signal;
                             asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(ptx::smem_u32(&meeting.of_warp[p][mine])), "r"(lane));
                             asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(signal) : "r"(ptx::smem_u32(&meeting.bar[p])), "r"(lane));
@@ -420,7 +467,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 16 : CONSUME
                                 // the rank that has written the token's place
                                 const bool outside = token < in.head || token >= in.V - in.tail;
                                 const int at = (token - in.head) / PER;
-                                if (token < 0 || (outside ? rank != 0 : at < u0 || at >= end)) continue;
+                                if (token < 0 || token >= in.V || (outside ? rank != 0 : at < u0 || at >= end)) continue;
                                 float q = 0.f;
                                 bool first = true;  // a token that comes twice counts twice, and is written once
                                 for (int j = 0; j < K; j += 4) {
@@ -472,10 +519,6 @@ struct Plan {
     int consumers, stage_units, ranks;
     bool cluster;
 };
-constexpr int kStageUnits[] = {256, 768, 1536, 3000};  // of 32, 64, 128 and 256 consumers: 4, 12, 24 and 47 KB
-constexpr int kWideUnits = 6400;                       // one block an SM: 100 KB
-constexpr int kMostConsumers = 256;
-
 // Units of 16 bytes that a row may have
 int64_t most_units(const rlscan_distill_args &a) { return a.V / (a.dtype == RLSCAN_BF16 ? 8 : 4); }
 

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 3)
         fold(keep, b, A, B);
         chain.put(p, k.w, k.lane, A, B);
         __syncthreads();  // all have taken the stage's values
-        if (threadIdx.x == 0 && s + 2 < k.steps) fetch(s + 2);
+        if (threadIdx.x == 0 && s + 2 < k.steps && !has_given_up(&gave_up)) fetch(s + 2);
         Exchange<kGatedCluster> *ex = nullptr;
         if constexpr (CLUSTER) ex = &exchange;
         f2 h = in_front<CLUSTER, true>(chain, ex, s, k.w, k.lane, k.rank, ranks, carry, &gave_up);

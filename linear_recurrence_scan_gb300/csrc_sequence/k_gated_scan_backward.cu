@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
         if (k.lane == 0) stores_read();  // the step behind has left its stage,
         __syncthreads();                 // all of it: the stage takes the step after next
         const int behind = stage == 0 ? kBackStages - 1 : stage - 1;
-        if (threadIdx.x == 0 && turn + 2 < k.steps) fetch(turn + 2, behind);
+        if (threadIdx.x == 0 && turn + 2 < k.steps && !has_given_up(&gave_up)) fetch(turn + 2, behind);
         Exchange<kBackCluster> *ex = nullptr;
         if constexpr (CLUSTER) ex = &exchange;
         f2 m = in_front<CLUSTER, false>(chain, ex, turn, k.w, k.lane, k.rank, ranks, carry, &gave_up);

@@ -65,9 +65,9 @@ def test_loss_and_gradient(N, T, V, K, dtype, tau):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
-@pytest.mark.parametrize("N,T,V,K", [(2, 400, 9000, 4), (1, 700, 300, 6), (3, 150, 5000, 3)])
+@pytest.mark.parametrize("N,T,V,K", [(2, 400, 9000, 4), (1, 7000, 300, 6), (3, 900, 5000, 3), (1, 650, 36001, 3), (1, 330, 140000, 2)])
 def test_many_rows(N, T, V, K, dtype):
-    """Rows that keep a block to themselves."""
+    """More rows than blocks: every block takes several, in one part each and in several."""
     logits, teacher, tokens, mask, grad, _ = distill_inputs(N, T, V, K, dtype, 3)
     check(logits, teacher, tokens, mask, grad)
 
