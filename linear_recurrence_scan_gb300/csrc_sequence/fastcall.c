@@ -1,9 +1,11 @@
-/* fastcall.c -- the state-space layer's latency-bound calls without the
- * interpreter between the tensors and the C entry points.
+/* fastcall.c -- the latency-bound calls of the state-space layer and of the
+ * token policy's other operators without the interpreter between the tensors
+ * and the C entry points.
  *
  * A single token's kernel takes a few microseconds; asking ten tensors for
  * their type, shape, strides and address from Python takes longer.  Each
- * function here does what its namesake in state_space.py does for arguments
+ * function here does what its namesake in state_space.py or token_policy.py
+ * does for arguments
  * in the usual form (plain CUDA tensors of the right type and shape, element
  * stride 1, no gradient wanted, outside forward-mode differentiation, on the
  * current device) and returns None for any others, which then take the
@@ -25,7 +27,7 @@ typedef struct Tensor {
 
 static PyObject *g_tensor, *g_parameter, *g_f32, *g_bf16, *g_i32, *g_u8, *g_bool, *g_fp8, *g_empty,
     *g_raw_stream, *g_grad_enabled, *g_norm_result, *g_current_device, *g_forward_ad,
-    *g_changed;
+    *g_changed, *g_i64, *g_gated_grads, *g_projection_grads;
 static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_requires_grad, *s_device, *s_level, *kw_empty;
 
 static size_t (*f_scan_ws)(const rlscan_selective_scan_args *);
@@ -418,6 +420,306 @@ static PyObject *add_rms_norm(PyObject *self, PyObject *const *args, Py_ssize_t 
     return result != NULL ? result : other_way();
 }
 
+/* ---- the token policy's other operators ------------------------------------- */
+
+static rlscan_status (*f_gated)(const rlscan_gated_scan_args *, void *, float *, float *, rlscan_stream_t);
+static size_t (*f_gated_back_ws)(const rlscan_gated_scan_args *);
+static rlscan_status (*f_gated_back)(const rlscan_gated_scan_args *, const rlscan_array3 *, const float *, const float *,
+                                     const rlscan_gated_scan_grads *, void *, size_t, rlscan_stream_t);
+static rlscan_status (*f_gated_step)(const rlscan_gated_scan_args *, float *, int64_t, const int32_t *, void *, rlscan_stream_t);
+static size_t (*f_projection_ws)(const rlscan_gated_projection_args *);
+static rlscan_status (*f_projection)(const rlscan_gated_projection_args *, void *, void *, size_t, rlscan_stream_t);
+static size_t (*f_projection_back_ws)(const rlscan_gated_projection_args *);
+static rlscan_status (*f_projection_back)(const rlscan_gated_projection_args *, const void *, int64_t, void *, void *, void *,
+                                          void *, size_t, rlscan_stream_t);
+static rlscan_status (*f_distill)(const rlscan_distill_args *, float *, float *, rlscan_stream_t);
+static rlscan_status (*f_distill_both)(const rlscan_distill_args *, const float *, float *, float *, void *, rlscan_stream_t);
+
+static int is_empty(const int64_t *sizes, int n)
+{
+    for (int i = 0; i < n; ++i)
+        if (sizes[i] == 0) return 1;
+    return 0;
+}
+
+/* x, gate, input_gate, log_decay at args[0..3] */
+static int gated_args(PyObject *const *args, rlscan_gated_scan_args *a, PyObject **dtype, int64_t *device, int step)
+{
+    Tensor x;
+    const void *p;
+    const int dims = step ? 2 : 3;
+    if (!io_type(args[0], dtype, &a->dtype) || !look(args[0], &x, *dtype, device) || x.dims != dims || x.stride[dims - 1] != 1 ||
+        is_empty(x.size, dims))
+        return 0;
+    a->N = x.size[0];
+    a->T = step ? 1 : x.size[1];
+    a->D = x.size[dims - 1];
+    a->x.data = x.data;
+    a->x.row_stride = x.stride[0];
+    a->x.token_stride = step ? 0 : x.stride[1];
+    const int64_t second = step ? a->D : a->T;
+    if (!act(args[1], &a->gate, *dtype, device, dims, a->N, second, a->D) ||
+        !act(args[2], &a->input_gate, *dtype, device, dims, a->N, second, a->D) || !array(args[3], &p, g_f32, device, 1, 1, a->D, 0, 0))
+        return 0;
+    a->log_decay = (const float *)p;
+    a->initial_state = NULL;
+    a->resets = NULL;
+    a->lengths = NULL;
+    return 1;
+}
+
+/* gated_scan(x, gate, input_gate, log_decay, initial_state, resets, lengths, return_checkpoints) */
+static PyObject *gated_scan(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    rlscan_gated_scan_args a;
+    PyObject *dtype;
+    int64_t device = -1;
+    const void *init, *resets, *lengths;
+    rlscan_stream_t s;
+    if (n != 8 || dual_level() || !gated_args(args, &a, &dtype, &device, 0) || (args[7] != Py_True && args[7] != Py_False) ||
+        !array(args[4], &init, g_f32, &device, 0, 2, a.N, a.D, 0) || !flags(args[5], &resets, &device, a.N, a.T) ||
+        !array(args[6], &lengths, g_i32, &device, 0, 1, a.N, 0, 0) || !stream_of(device, &s))
+        return other_way();
+    a.initial_state = (const float *)init;
+    a.resets = (const uint8_t *)resets;
+    a.lengths = (const int32_t *)lengths;
+    const int marks = args[7] == Py_True;
+    void *yp, *fp, *mp = NULL;
+    PyObject *y = new_tensor(args[0], 3, a.N, a.T, a.D, dtype, &yp);
+    PyObject *final = y != NULL ? new_tensor(args[0], 2, a.N, a.D, 0, g_f32, &fp) : NULL;
+    const int64_t count = (a.T + RLSCAN_GATED_SCAN_CHECKPOINT - 1) / RLSCAN_GATED_SCAN_CHECKPOINT;
+    PyObject *kept = final != NULL && marks ? new_tensor(args[0], 3, a.N, count, a.D, g_f32, &mp) : NULL;
+    PyObject *r = NULL;
+    if (final != NULL && (!marks || kept != NULL) && f_gated(&a, yp, (float *)fp, (float *)mp, s) == RLSCAN_OK)
+        r = marks ? PyTuple_Pack(3, y, final, kept) : PyTuple_Pack(2, y, final);
+    Py_XDECREF(y);
+    Py_XDECREF(final);
+    Py_XDECREF(kept);
+    return r != NULL ? r : other_way();
+}
+
+/* gated_scan_backward(grad_y, x, gate, input_gate, log_decay, checkpoints, resets, lengths, grad_final_state) */
+static PyObject *gated_scan_backward(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    rlscan_gated_scan_args a;
+    rlscan_array3 gy;
+    PyObject *dtype;
+    int64_t device = -1;
+    const void *marks, *final, *resets, *lengths;
+    rlscan_stream_t s;
+    if (n != 9 || dual_level() || !gated_args(args + 1, &a, &dtype, &device, 0)) return other_way();
+    const int64_t count = (a.T + RLSCAN_GATED_SCAN_CHECKPOINT - 1) / RLSCAN_GATED_SCAN_CHECKPOINT;
+    if (!act(args[0], &gy, dtype, &device, 3, a.N, a.T, a.D) || !array(args[5], &marks, g_f32, &device, 1, 3, a.N, count, a.D) ||
+        !flags(args[6], &resets, &device, a.N, a.T) || !array(args[7], &lengths, g_i32, &device, 0, 1, a.N, 0, 0) ||
+        !array(args[8], &final, g_f32, &device, 0, 2, a.N, a.D, 0) || !stream_of(device, &s))
+        return other_way();
+    a.resets = (const uint8_t *)resets;
+    a.lengths = (const int32_t *)lengths;
+    const size_t bytes = f_gated_back_ws(&a);
+    void *p[5], *wp = NULL;
+    PyObject *out[5] = {NULL, NULL, NULL, NULL, NULL}, *ws = NULL, *r = NULL;
+    int ok = 1;
+    for (int i = 0; i < 3 && ok; ++i) ok = (out[i] = new_tensor(args[1], 3, a.N, a.T, a.D, dtype, &p[i])) != NULL;
+    ok = ok && (out[3] = new_tensor(args[1], 1, a.D, 0, 0, g_f32, &p[3])) != NULL;
+    ok = ok && (out[4] = new_tensor(args[1], 2, a.N, a.D, 0, g_f32, &p[4])) != NULL;
+    if (ok && bytes > 0) ok = (ws = new_tensor(args[1], 1, (int64_t)bytes, 0, 0, g_u8, &wp)) != NULL;
+    if (ok) {
+        const rlscan_gated_scan_grads g = {p[0], p[1], p[2], (float *)p[3], (float *)p[4]};
+        if (f_gated_back(&a, &gy, (const float *)final, (const float *)marks, &g, wp, bytes, s) == RLSCAN_OK)
+            r = PyObject_Vectorcall(g_gated_grads, out, 5, NULL);
+    }
+    for (int i = 0; i < 5; ++i) Py_XDECREF(out[i]);
+    Py_XDECREF(ws);
+    return r != NULL ? r : other_way();
+}
+
+/* gated_scan_step(state, x, gate, input_gate, log_decay, slots) */
+static PyObject *gated_scan_step(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    rlscan_gated_scan_args a;
+    PyObject *dtype;
+    int64_t device = -1;
+    Tensor state;
+    const void *slots;
+    rlscan_stream_t s;
+    if (n != 6 || dual_level() || !gated_args(args + 1, &a, &dtype, &device, 1) || !look(args[0], &state, g_f32, &device) ||
+        !sized(&state, 2, state.size[0], a.D, 0) || !dense(&state) || !array(args[5], &slots, g_i32, &device, 0, 1, a.N, 0, 0) ||
+        !stream_of(device, &s))
+        return other_way();
+    void *yp;
+    PyObject *y = new_tensor(args[1], 2, a.N, a.D, 0, dtype, &yp);
+    if (y != NULL && f_gated_step(&a, (float *)state.data, state.size[0], (const int32_t *)slots, yp, s) == RLSCAN_OK)
+        return updated(args[0], y);
+    Py_XDECREF(y);
+    return other_way();
+}
+
+/* x, gate_weight, up_weight, activation at args[0..3], x of two dimensions */
+static int projection_args(PyObject *const *args, rlscan_gated_projection_args *a, int64_t *device)
+{
+    Tensor x, g, u;
+    if (!look(args[0], &x, g_bf16, device) || x.dims != 2 || x.stride[1] != 1 || !look(args[1], &g, g_bf16, device) || g.dims != 2 ||
+        g.stride[1] != 1 || !look(args[2], &u, g_bf16, device) || !sized(&u, 2, g.size[0], g.size[1], 0) || u.stride[1] != 1 ||
+        g.size[1] != x.size[1] || is_empty(x.size, 2) || is_empty(g.size, 2) || !PyUnicode_Check(args[3]))
+        return 0;
+    if (PyUnicode_CompareWithASCIIString(args[3], "silu") == 0)
+        a->activation = RLSCAN_SILU;
+    else if (PyUnicode_CompareWithASCIIString(args[3], "gelu") == 0)
+        a->activation = RLSCAN_GELU;
+    else
+        return 0;
+    a->M = x.size[0];
+    a->D = x.size[1];
+    a->F = g.size[0];
+    a->x = x.data;
+    a->x_stride = x.stride[0];
+    a->gate_weight = g.data;
+    a->gate_stride = g.stride[0];
+    a->up_weight = u.data;
+    a->up_stride = u.stride[0];
+    return 1;
+}
+
+/* gated_projection(x, gate_weight, up_weight, activation) */
+static PyObject *gated_projection(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    rlscan_gated_projection_args a;
+    int64_t device = -1;
+    rlscan_stream_t s;
+    if (n != 4 || dual_level() || !projection_args(args, &a, &device) || !stream_of(device, &s)) return other_way();
+    const size_t bytes = f_projection_ws(&a);
+    void *hp, *wp = NULL;
+    PyObject *h = new_tensor(args[0], 2, a.M, a.F, 0, g_bf16, &hp);
+    PyObject *ws = h != NULL && bytes > 0 ? new_tensor(args[0], 1, (int64_t)bytes, 0, 0, g_u8, &wp) : NULL;
+    const int ok = h != NULL && (bytes == 0 || ws != NULL) && f_projection(&a, hp, wp, bytes, s) == RLSCAN_OK;
+    Py_XDECREF(ws);
+    if (ok) return h;
+    Py_XDECREF(h);
+    return other_way();
+}
+
+/* gated_projection_backward(grad_h, x, gate_weight, up_weight, activation) */
+static PyObject *gated_projection_backward(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    rlscan_gated_projection_args a;
+    Tensor gh;
+    int64_t device = -1;
+    rlscan_stream_t s;
+    if (n != 5 || dual_level() || !projection_args(args + 1, &a, &device) || !look(args[0], &gh, g_bf16, &device) ||
+        !sized(&gh, 2, a.M, a.F, 0) || gh.stride[1] != 1 || !stream_of(device, &s))
+        return other_way();
+    const size_t bytes = f_projection_back_ws(&a);
+    void *p[3], *wp = NULL;
+    PyObject *out[3] = {NULL, NULL, NULL}, *ws = NULL, *r = NULL;
+    int ok = (out[0] = new_tensor(args[1], 2, a.M, a.D, 0, g_bf16, &p[0])) != NULL;
+    for (int i = 1; i < 3 && ok; ++i) ok = (out[i] = new_tensor(args[1], 2, a.F, a.D, 0, g_bf16, &p[i])) != NULL;
+    if (ok && bytes > 0) ok = (ws = new_tensor(args[1], 1, (int64_t)bytes, 0, 0, g_u8, &wp)) != NULL;
+    if (ok && f_projection_back(&a, gh.data, gh.stride[0], p[0], p[1], p[2], wp, bytes, s) == RLSCAN_OK)
+        r = PyObject_Vectorcall(g_projection_grads, out, 3, NULL);
+    for (int i = 0; i < 3; ++i) Py_XDECREF(out[i]);
+    Py_XDECREF(ws);
+    return r != NULL ? r : other_way();
+}
+
+/* logits, teacher_logits, teacher_tokens, temperature, mask at args[0..4] */
+static int distill_args(PyObject *const *args, rlscan_distill_args *a, PyObject **dtype, int64_t *device)
+{
+    Tensor z, t, k;
+    PyObject *ttype;
+    const void *mask;
+    if (!io_type(args[0], dtype, &a->dtype) || !look(args[0], &z, *dtype, device) || z.dims != 3 || z.stride[2] != 1 ||
+        is_empty(z.size, 3) || !io_type(args[1], &ttype, &a->teacher_dtype) || !look(args[1], &t, ttype, device) || t.dims != 3 ||
+        !sized(&t, 3, z.size[0], z.size[1], t.size[2]) || !dense(&t) || !look(args[2], &k, NULL, device) ||
+        !sized(&k, 3, t.size[0], t.size[1], t.size[2]) || !dense(&k) || !PyFloat_Check(args[3]) ||
+        !flags(args[4], &mask, device, z.size[0], z.size[1]))
+        return 0;
+    PyObject *v = PyObject_GetAttr(args[2], s_dtype);
+    if (v == NULL) return 0;
+    Py_DECREF(v);
+    if (v != g_i32 && v != g_i64) return 0;
+    a->token_bytes = v == g_i64 ? 8 : 4;
+    a->N = z.size[0];
+    a->T = z.size[1];
+    a->V = z.size[2];
+    a->K = t.size[2];
+    a->logits.data = z.data;
+    a->logits.row_stride = z.stride[0];
+    a->logits.token_stride = z.stride[1];
+    a->teacher_logits = t.data;
+    a->teacher_tokens = k.data;
+    a->mask = (const uint8_t *)mask;
+    a->temperature = PyFloat_AS_DOUBLE(args[3]);
+    return 1;
+}
+
+/* distill_loss(logits, teacher_logits, teacher_tokens, temperature, mask) */
+static PyObject *distill_loss(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    rlscan_distill_args a;
+    PyObject *dtype;
+    int64_t device = -1;
+    rlscan_stream_t s;
+    if (n != 5 || dual_level() || !distill_args(args, &a, &dtype, &device) || !stream_of(device, &s)) return other_way();
+    void *lp;
+    PyObject *loss = new_tensor(args[0], 2, a.N, a.T, 0, g_f32, &lp);
+    if (loss != NULL && f_distill(&a, (float *)lp, NULL, s) == RLSCAN_OK) return loss;
+    Py_XDECREF(loss);
+    return other_way();
+}
+
+/* distill_loss_and_grad(grad_loss, logits, teacher_logits, teacher_tokens, temperature, mask) */
+static PyObject *distill_loss_and_grad(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    rlscan_distill_args a;
+    PyObject *dtype;
+    int64_t device = -1;
+    const void *weight;
+    rlscan_stream_t s;
+    if (n != 6 || dual_level() || !distill_args(args + 1, &a, &dtype, &device) ||
+        !array(args[0], &weight, g_f32, &device, 1, 2, a.N, a.T, 0) || !stream_of(device, &s))
+        return other_way();
+    void *lp, *np, *gp;
+    PyObject *loss = new_tensor(args[1], 2, a.N, a.T, 0, g_f32, &lp), *r = NULL;
+    PyObject *norm = loss != NULL ? new_tensor(args[1], 3, a.N, a.T, 2, g_f32, &np) : NULL;
+    PyObject *grad = norm != NULL ? new_tensor(args[1], 3, a.N, a.T, a.V, dtype, &gp) : NULL;
+    if (grad != NULL && f_distill_both(&a, (const float *)weight, (float *)lp, (float *)np, gp, s) == RLSCAN_OK)
+        r = PyTuple_Pack(2, loss, grad);
+    Py_XDECREF(loss);
+    Py_XDECREF(norm);
+    Py_XDECREF(grad);
+    return r != NULL ? r : other_way();
+}
+
+/* setup_token_policy(torch, GatedScanGrads, GatedProjectionGrads, addresses of the ten entry points), behind setup */
+static PyObject *setup_token_policy(PyObject *self, PyObject *args)
+{
+    PyObject *torch, *gated, *projection;
+    unsigned long long f[10];
+    if (!PyArg_ParseTuple(args, "OOOKKKKKKKKKK", &torch, &gated, &projection, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6],
+                          &f[7], &f[8], &f[9]))
+        return NULL;
+    if ((g_i64 = PyObject_GetAttrString(torch, "int64")) == NULL) return NULL;
+    Py_INCREF(gated);
+    g_gated_grads = gated;
+    Py_INCREF(projection);
+    g_projection_grads = projection;
+    f_gated = (rlscan_status (*)(const rlscan_gated_scan_args *, void *, float *, float *, rlscan_stream_t))(uintptr_t)f[0];
+    f_gated_back_ws = (size_t (*)(const rlscan_gated_scan_args *))(uintptr_t)f[1];
+    f_gated_back = (rlscan_status (*)(const rlscan_gated_scan_args *, const rlscan_array3 *, const float *, const float *,
+                                      const rlscan_gated_scan_grads *, void *, size_t, rlscan_stream_t))(uintptr_t)f[2];
+    f_gated_step = (rlscan_status (*)(const rlscan_gated_scan_args *, float *, int64_t, const int32_t *, void *,
+                                      rlscan_stream_t))(uintptr_t)f[3];
+    f_projection_ws = (size_t (*)(const rlscan_gated_projection_args *))(uintptr_t)f[4];
+    f_projection = (rlscan_status (*)(const rlscan_gated_projection_args *, void *, void *, size_t, rlscan_stream_t))(uintptr_t)f[5];
+    f_projection_back_ws = (size_t (*)(const rlscan_gated_projection_args *))(uintptr_t)f[6];
+    f_projection_back = (rlscan_status (*)(const rlscan_gated_projection_args *, const void *, int64_t, void *, void *, void *,
+                                           void *, size_t, rlscan_stream_t))(uintptr_t)f[7];
+    f_distill = (rlscan_status (*)(const rlscan_distill_args *, float *, float *, rlscan_stream_t))(uintptr_t)f[8];
+    f_distill_both = (rlscan_status (*)(const rlscan_distill_args *, const float *, float *, float *, void *,
+                                        rlscan_stream_t))(uintptr_t)f[9];
+    Py_RETURN_NONE;
+}
+
 /* setup(torch, RmsNorm, raw stream function, current device function, torch.autograd.forward_ad, increment_version,
  * addresses of the six entry points) */
 static PyObject *setup(PyObject *self, PyObject *args)
@@ -476,7 +778,10 @@ static PyObject *setup(PyObject *self, PyObject *args)
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {{"setup", setup, METH_VARARGS, NULL}, FAST(selective_scan), FAST(selective_scan_step),
-                                FAST(causal_conv), FAST(causal_conv_step), FAST(add_rms_norm), {NULL, NULL, 0, NULL}};
+                                FAST(causal_conv), FAST(causal_conv_step), FAST(add_rms_norm),
+                                {"setup_token_policy", setup_token_policy, METH_VARARGS, NULL}, FAST(gated_scan),
+                                FAST(gated_scan_backward), FAST(gated_scan_step), FAST(gated_projection),
+                                FAST(gated_projection_backward), FAST(distill_loss), FAST(distill_loss_and_grad), {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -62,6 +62,9 @@ class _NoFastCall:
         return None
 
     selective_scan = selective_scan_step = causal_conv = causal_conv_step = add_rms_norm = _none
+    setup_token_policy = _none   # and the operators of token_policy.py
+    gated_scan = gated_scan_backward = gated_scan_step = gated_projection = gated_projection_backward = _none
+    distill_loss = distill_loss_and_grad = _none
 
 
 _fast = None

@@ -11,6 +11,7 @@ are refused.
 """
 from __future__ import annotations
 
+import ctypes
 import struct
 from typing import NamedTuple
 
@@ -18,7 +19,7 @@ import torch
 
 from . import _native
 from .api import _stream_handle
-from .state_space import (_ARRAY3, _TYPES, _act, _at, _changed, _check, _dense, _flags, _lead, _on,
+from .state_space import (_ARRAY3, _TYPES, _act, _at, _changed, _check, _dense, _flags, _lead, _load_fast, _on,
                           _refuse_tangents, _scratch, _wants_grad)
 
 __all__ = [
@@ -36,6 +37,24 @@ _ACTIVATIONS = {"silu": 0, "gelu": 1}
 _DISTILL_ARGS = struct.Struct("=13qd")
 
 MAX_TEACHER_TOKENS = 256   # RLSCAN_DISTILL_MOST
+
+
+_fast = None
+
+
+def _load():
+    """The native call layer (csrc_sequence/fastcall.c), or one that leaves all to Python."""
+    global _fast
+    if _fast is None:
+        fast = _load_fast()
+        lib = _native.lib()
+        fast.setup_token_policy(torch, GatedScanGrads, GatedProjectionGrads, *(
+            ctypes.cast(getattr(lib, "rlscan_" + name), ctypes.c_void_p).value for name in (
+                "gated_scan", "gated_scan_backward_workspace_bytes", "gated_scan_backward", "gated_scan_step",
+                "gated_projection_workspace_bytes", "gated_projection", "gated_projection_backward_workspace_bytes",
+                "gated_projection_backward", "distill_loss", "distill_loss_and_grad")))
+        _fast = fast
+    return _fast
 
 
 # ---------------------------------------------------------------------------
@@ -120,6 +139,9 @@ def gated_scan(x, gate, input_gate, log_decay, initial_state=None, resets=None, 
     gated_scan_backward needs: the states before every 32nd token (these
     carry no gradient)."""
     args = (x, gate, input_gate, log_decay, initial_state, resets, lengths)
+    out = (_fast or _load()).gated_scan(*args, return_checkpoints)
+    if out is not None:
+        return out
     _refuse_tangents(*args[:5])
     out = _GatedScan.apply(*args) if _wants_grad(*args[:5]) else _gated_forward(return_checkpoints, *args)
     return out if return_checkpoints else out[:2]
@@ -130,6 +152,10 @@ def gated_scan_backward(grad_y, x, gate, input_gate, log_decay, checkpoints, res
     """Gradients of gated_scan: ``grad_y`` like x, ``checkpoints`` from the
     forward call on the same inputs, ``grad_final_state`` [N,channels] float32
     or None.  Returns GatedScanGrads."""
+    g = (_fast or _load()).gated_scan_backward(grad_y, x, gate, input_gate, log_decay, checkpoints, resets, lengths,
+                                               grad_final_state)
+    if g is not None:
+        return g
     _refuse_tangents(grad_y, x, gate, input_gate, log_decay, checkpoints, grad_final_state)
     dev, (N, T, width), packed, kept = _gated_args(False, x, gate, input_gate, log_decay, None, resets, lengths)
     x = kept[0]
@@ -157,6 +183,9 @@ def gated_scan_step(state, x, gate, input_gate, log_decay, slots=None):
     """One token of each of N sequences: x, gate, input_gate [N,channels];
     ``state`` [P,channels] float32 (dense) is updated in place, with ``slots``
     as in selective_scan_step.  Returns y [N,channels].  Not differentiable."""
+    y = (_fast or _load()).gated_scan_step(state, x, gate, input_gate, log_decay, slots)
+    if y is not None:
+        return y
     _refuse_tangents(state, x, gate, input_gate, log_decay)
     dev, (N, _, width), packed, kept = _gated_args(True, x, gate, input_gate, log_decay, None, None, None)
     if not isinstance(state, torch.Tensor) or state.dim() != 2:
@@ -257,6 +286,9 @@ def gated_projection(x, gate_weight, up_weight, activation="silu"):
     float32, h [..., F] is rounded once.  ``activation`` is "silu" or "gelu"
     (z times the normal distribution up to z).  float32 is refused: the tensor
     cores would round its factors to 11 bits."""
+    h = (_fast or _load()).gated_projection(x, gate_weight, up_weight, activation)
+    if h is not None:
+        return h
     _refuse_tangents(x, gate_weight, up_weight)
     if _wants_grad(x, gate_weight, up_weight):
         return _GatedProjection.apply(x, gate_weight, up_weight, activation)
@@ -285,6 +317,9 @@ def gated_projection_backward(grad_h, x, gate_weight, up_weight, activation="sil
     """Gradients of gated_projection: ``grad_h`` [..., F] bfloat16.  z and u
     are made again from x, in 32 bits; the gradients at z and u are rounded to
     bfloat16 for the products that follow.  Returns GatedProjectionGrads."""
+    g = (_fast or _load()).gated_projection_backward(grad_h, x, gate_weight, up_weight, activation)
+    if g is not None:
+        return g
     _refuse_tangents(grad_h, x, gate_weight, up_weight)
     return _projection_backward(grad_h, x, gate_weight, up_weight, activation, True, True)
 
@@ -369,6 +404,10 @@ def distill_loss(logits, teacher_logits, teacher_tokens, temperature=1.0, mask=N
     [N,T,2] float32.  Differentiable in the logits; the teacher has no
     gradient (one that requires it is refused).  The factor temperature^2
     that some recipes have is left to the caller."""
+    if not return_normalizers:
+        loss = (_fast or _load()).distill_loss(logits, teacher_logits, teacher_tokens, temperature, mask)
+        if loss is not None:
+            return loss
     _refuse_tangents(logits, teacher_logits)
     args = (logits, teacher_logits, teacher_tokens, temperature, mask)
     if _wants_grad(teacher_logits):
@@ -407,6 +446,9 @@ def distill_loss_and_grad(grad_loss, logits, teacher_logits, teacher_tokens, tem
     knows each token's weight ``grad_loss`` [N,T] float32 before its loss (a
     mask over the number of tokens, say): the logits are read once.  Not
     followed by autograd."""
+    out = (_fast or _load()).distill_loss_and_grad(grad_loss, logits, teacher_logits, teacher_tokens, temperature, mask)
+    if out is not None:
+        return out
     _refuse_tangents(grad_loss, logits, teacher_logits)
     dev, packed, kept = _distill_args(logits, teacher_logits, teacher_tokens, temperature, mask)
     logits = kept[0]
