@@ -19,7 +19,7 @@ __device__ unsigned int g_timed_out;  // a wait ran out on this device
 enum class Job { Forward, Gates, Input, Weights };
 
 struct Maps {
-    CUtensorMap a[2], b[2];
+    CUtensorMap a[2], b[2], out[2];
 };
 
 struct Work {
@@ -28,42 +28,42 @@ struct Work {
     int act;
     const bf16 *grad_h;
     int64_t grad_h_stride;
-    bool grad_h_vec, out_vec;
+    bool grad_h_vec;
     bf16 *out[2];
     int64_t out_stride;
+    bool out_mapped;  // outputs leave through maps.out
 };
 
 constexpr int kBlockK = 64;  // values of K in a stage: a row of 128 bytes
-constexpr int kStages = 6, kThreads = 256;
+constexpr int kStages = 5, kThreads = 256;
 constexpr uint32_t kTileBytes = 128 * kBlockK * 2, kStageBytes = 2 * kTileBytes;
-constexpr size_t kSmem = kStages * kStageBytes + 1024;
+constexpr uint32_t kOutBytes = 32 * 128;  // 32 rows of 64 values, two of a warp that takes sums out
+constexpr size_t kSmem = kStages * kStageBytes + 4 * 2 * kOutBytes + 1024;
 
-__device__ __forceinline__ float2 act_slope(float z, int act)
+// 32 neighbouring values of a row, of which `n` are the row's, one by one
+__device__ __forceinline__ void store_row(bf16 *p, const float (&v)[32], int64_t n)
 {
-    if (act == RLSCAN_SILU) {
-        const float g = sigmoid(z), a = z * g;
-        return make_float2(a, fmaf(a, 1.f - g, g));
-    }
-    const float half = 0.5f * erfcf(-0.70710678118654752f * z);  // the normal distribution up to z
-    return make_float2(z * half, fmaf(z * 0.3989422804014327f, exp2_fast(-0.5f * kLog2e * z * z), half));
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (j < n) p[j] = from_f<bf16>(v[j]);
 }
-
-// 32 neighbouring values of a row, from column `c`, of which `n` are the row's
-__device__ __forceinline__ void store_row(bf16 *p, const float (&v)[32], int64_t n, bool vec)
+// ... into half `h` of the lane's row of an output box, with its swizzle: the
+// 16-byte units of a row change places by the row's number
+__device__ __forceinline__ void box_row(char *box, int lane, int h, const float (&v)[32])
 {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-        if (vec && i + 8 <= n) {
-            Words<bf16, 8> w;
+    for (int i = 0; i < 4; ++i) {
+        Words<bf16, 8> w;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w.set(j, v[i + 2 * j], v[i + 2 * j + 1]);
-            w.store(p + i);
-        } else {
-#pragma unroll
-            for (int j = i; j < i + 8; ++j)
-                if (j < n) p[j] = from_f<bf16>(v[j]);
-        }
+        for (int j = 0; j < 4; ++j) w.set(j, v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+        w.store(reinterpret_cast<bf16 *>(box + lane * 128 + (((4 * h + i) ^ (lane & 7)) * 16)));
     }
+}
+__device__ __forceinline__ void store_box2(const CUtensorMap *map, int64_t x, int64_t y, const char *box)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(static_cast<int>(x)),
+                 "r"(static_cast<int>(y)), "r"(ptx::smem_u32(box))
+                 : "memory");
 }
 __device__ __forceinline__ void load_row(Words<bf16, 8> (&w)[4], const bf16 *p, int64_t n, bool vec)
 {
@@ -100,7 +100,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_at;
     __shared__ int gave_up;
     ptx::pdl_trigger_dependents();
-    const uint32_t smem = (ptx::smem_u32(raw) + 1023u) & ~1023u, rank = umma::cluster_rank();
+    char *raw_aligned = reinterpret_cast<char *>(raw) + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);
+    const uint32_t smem = ptx::smem_u32(raw_aligned), rank = umma::cluster_rank();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         gave_up = 0;
@@ -195,6 +196,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp >= 4) {  // sums
         uint32_t buffer = 0, phase = 0;
         const int part = warp % 4;
+        char *boxes = raw_aligned + kStages * kStageBytes + part * 2 * kOutBytes;
+        // the box that comes next has been read: all of the warp's, or (two take turns) all but the last
+        auto free_box = [&](bool turns) {
+            if (lane == 0) {
+                if (turns) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            __syncwarp();
+        };
         for (int64_t tile = pair; tile < tiles; tile += pairs) {
             int64_t tm, tn;
             place(tile, tm, tn);
@@ -205,6 +215,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!wait(ptx::smem_u32(&sums_full[buffer]), phase, &gave_up)) break;
             umma::fence_after();
             const uint32_t at = tmem + buffer * 256 + (static_cast<uint32_t>(part * 32) << 16);
+            const int64_t row0 = row - lane;  // of the warp
             if constexpr (kGates) {
                 const int64_t f0 = tn * 128;
 #pragma unroll 1
@@ -229,8 +240,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             w[i] = g * as.x;
                         }
                     }
-                    store_row(k.out[0] + row * k.out_stride + f0 + c, v, n, k.out_vec);
-                    if constexpr (JOB == Job::Gates) store_row(k.out[1] + row * k.out_stride + f0 + c, w, n, k.out_vec);
+                    const int h = c / 32 % 2;
+                    if (k.out_mapped) {
+                        char *box = boxes + (JOB == Job::Forward ? c / 64 * kOutBytes : 0);
+                        if (h == 0) free_box(JOB == Job::Forward);
+                        box_row(box, lane, h, v);
+                        if constexpr (JOB == Job::Gates) box_row(boxes + kOutBytes, lane, h, w);
+                        if (h == 1) {
+                            fence_async();
+                            __syncwarp();
+                            if (lane == 0 && row0 < rows && f0 + c - 32 < k.F) {
+                                store_box2(&maps.out[0], f0 + c - 32, row0, box);
+                                if constexpr (JOB == Job::Gates) store_box2(&maps.out[1], f0 + c - 32, row0, boxes + kOutBytes);
+                            }
+                            if (lane == 0) stores_commit();
+                        }
+                    } else {
+                        store_row(k.out[0] + row * k.out_stride + f0 + c, v, n);
+                        if constexpr (JOB == Job::Gates) store_row(k.out[1] + row * k.out_stride + f0 + c, w, n);
+                    }
                 }
             } else {
                 const int64_t d0 = tn * 256;
@@ -242,7 +270,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     float f[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-                    store_row(k.out[which] + row * k.out_stride + d0 + c, f, row < rows ? k.D - d0 - c : 0, k.out_vec);
+                    if (k.out_mapped) {
+                        char *box = boxes + c / 64 % 2 * kOutBytes;
+                        const int h = c / 32 % 2;
+                        if (h == 0) free_box(true);
+                        box_row(box, lane, h, f);
+                        if (h == 1) {
+                            fence_async();
+                            __syncwarp();
+                            if (lane == 0 && row0 < rows && d0 + c - 32 < k.D) store_box2(&maps.out[which], d0 + c - 32, row0, box);
+                            if (lane == 0) stores_commit();
+                        }
+                    } else {
+                        store_row(k.out[which] + row * k.out_stride + d0 + c, f, row < rows ? k.D - d0 - c : 0);
+                    }
                 }
             }
             umma::fence_before();
@@ -251,6 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             buffer ^= 1;
             if (buffer == 0) phase ^= 1;
         }
+        if (lane == 0) stores_read();
     }
     __syncwarp();
     umma::fence_before();
@@ -361,18 +403,27 @@ rlscan_status launch_job(const Maps &maps, Work &w, cudaStream_t s)
     return launch(true, projection_kernel<JOB>, 2 * (tiles < pairs ? tiles : pairs), kThreads, kSmem, s, maps, w);
 }
 
+// An output [rows, columns] that leaves in boxes of 64 columns x 32 rows, where its alignment allows
+void map_out(Maps &m, int i, Work &w, void *p, int64_t rows, int64_t columns, int64_t pitch)
+{
+    w.out[i] = static_cast<bf16 *>(p);
+    w.out_stride = pitch;
+    w.out_mapped = (i == 0 || w.out_mapped) && fits_map(p, rows, columns, pitch) && umma::encode(&m.out[i], p, rows, columns, up8(pitch), 32);
+}
+
 bool vec_rows(const void *p, int64_t stride) { return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(stride * 2)) & 15u) == 0; }
 
 }  // namespace
 
 size_t gated_projection_workspace(const rlscan_gated_projection_args &a)
 {
-    return a.M == 0 || a.F == 0 || a.D == 0 ? 0 : layout(a).bytes;
+    return a.M == 0 || a.F == 0 || a.D == 0 || projection_is_few(a) ? 0 : layout(a).bytes;
 }
 
 rlscan_status launch_gated_projection(const rlscan_gated_projection_args &a, void *h, void *ws, cudaStream_t s)
 {
     if (a.D == 0) return ok(cudaMemsetAsync(h, 0, static_cast<size_t>(a.M) * a.F * 2, s)) ? RLSCAN_OK : RLSCAN_ERR_CUDA;
+    if (projection_is_few(a)) return launch_gated_projection_few(a, h, s);
     Layout l = layout(a);
     rlscan_status st = pack_all(a, l, static_cast<char *>(ws), s);
     if (st != RLSCAN_OK) return st;
@@ -381,7 +432,7 @@ rlscan_status launch_gated_projection(const rlscan_gated_projection_args &a, voi
     Work w = {};
     w.M = a.M, w.D = a.D, w.F = a.F, w.act = static_cast<int>(a.activation);
     w.tiles_m = ceil_div(a.M, 256), w.tiles_n = ceil_div(a.F, 128), w.steps = ceil_div(a.D, kBlockK);
-    w.out[0] = static_cast<bf16 *>(h), w.out_stride = a.F, w.out_vec = vec_rows(h, a.F);
+    map_out(m, 0, w, h, a.M, a.F, a.F);
     return launch_job<Job::Forward>(m, w, s);
 }
 
@@ -413,7 +464,8 @@ rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_arg
     w.M = a.M, w.D = a.D, w.F = a.F, w.act = static_cast<int>(a.activation);
     w.tiles_m = ceil_div(a.M, 256), w.tiles_n = ceil_div(a.F, 128), w.steps = ceil_div(a.D, kBlockK);
     w.grad_h = static_cast<const bf16 *>(grad_h), w.grad_h_stride = grad_h_stride, w.grad_h_vec = vec_rows(grad_h, grad_h_stride);
-    w.out[0] = g, w.out[1] = g + pitch, w.out_stride = 2 * pitch, w.out_vec = true;
+    map_out(m, 0, w, g, a.M, a.F, 2 * pitch);
+    map_out(m, 1, w, g + pitch, a.M, a.F, 2 * pitch);
     st = launch_job<Job::Gates>(m, w, s);
     if (st != RLSCAN_OK) return st;
     const Operand gz{g, a.M, a.F, 2 * pitch, false}, gu{g + pitch, a.M, a.F, 2 * pitch, false};
@@ -422,7 +474,7 @@ rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_arg
         if (!map_of(&mx.a[0], gz, 128) || !map_of(&mx.a[1], gu, 128) || !map_of(&mx.b[0], l.gate, 64) || !map_of(&mx.b[1], l.up, 64))
             return RLSCAN_ERR_CUDA;
         w.tiles_n = ceil_div(a.D, 256), w.steps = 2 * ceil_div(a.F, kBlockK);
-        w.out[0] = static_cast<bf16 *>(grad_x), w.out_stride = a.D, w.out_vec = vec_rows(grad_x, a.D);
+        map_out(mx, 0, w, grad_x, a.M, a.D, a.D);
         st = launch_job<Job::Input>(mx, w, s);
         if (st != RLSCAN_OK) return st;
     }
@@ -430,8 +482,8 @@ rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_arg
         Maps mw = {};
         if (!map_of(&mw.a[0], gz, 64) || !map_of(&mw.a[1], gu, 64) || !map_of(&mw.b[0], l.x, 64)) return RLSCAN_ERR_CUDA;
         w.tiles_m = 2 * ceil_div(a.F, 256), w.tiles_n = ceil_div(a.D, 256), w.steps = ceil_div(a.M, kBlockK);
-        w.out[0] = static_cast<bf16 *>(grad_gate), w.out[1] = static_cast<bf16 *>(grad_up), w.out_stride = a.D;
-        w.out_vec = vec_rows(grad_gate, a.D) && vec_rows(grad_up, a.D);
+        map_out(mw, 0, w, grad_gate, a.F, a.D, a.D);
+        map_out(mw, 1, w, grad_up, a.F, a.D, a.D);
         st = launch_job<Job::Weights>(mw, w, s);
     }
     return st;
