@@ -32,6 +32,8 @@ struct Work {
     bf16 *out[2];
     int64_t out_stride;
     bool out_mapped;  // outputs leave through maps.out
+    int64_t parts, part_steps;  // K in `parts` of `part_steps` steps (1: whole)
+    float *sums;                // of parts > 1: [parts][rows of all outputs][columns]
 };
 
 constexpr int kBlockK = 64;  // values of K in a stage: a row of 128 bytes
@@ -123,7 +125,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     umma::fence_after();
     const uint32_t tmem = tmem_at;
     ptx::pdl_wait_prerequisites();
-    const int64_t tiles = k.tiles_m * k.tiles_n, pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int64_t items = k.tiles_m * k.tiles_n * k.parts, pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     // Tiles in bands of eight rows of tiles, column after column: the pairs at
     // work share rows of A and columns of B in L2.
     auto place = [&](int64_t tile, int64_t &m, int64_t &n) {
@@ -133,14 +135,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         m = band * kBand + in % high;
         n = in / high;
     };
+    // An item is a tile, or a part of its K
+    auto first_step = [&](int64_t item) { return item % k.parts * k.part_steps; };
+    auto last_step = [&](int64_t item) {
+        const int64_t e = (item % k.parts + 1) * k.part_steps;
+        return e < k.steps ? e : k.steps;
+    };
     if (warp == 0 && lane == 0) {  // copies
         uint32_t stage = 0, phase = 1;  // the first wait on an empty stage passes
         int64_t issued = 0;
         const int64_t half = kGates ? 0 : JOB == Job::Input ? k.steps / 2 : k.tiles_m / 2;
-        for (int64_t tile = pair; tile < tiles && !*const_cast<volatile int *>(&gave_up); tile += pairs) {
+        for (int64_t item = pair; item < items && !has_given_up(&gave_up); item += pairs) {
             int64_t tm, tn;
-            place(tile, tm, tn);
-            for (int64_t s = 0; s < k.steps; ++s) {
+            place(item / k.parts, tm, tn);
+            for (int64_t s = first_step(item), e = last_step(item); s < e; ++s) {
                 if (!wait(ptx::smem_u32(&empty[stage]), phase, &gave_up)) break;
                 const uint32_t bar = umma::of_rank(ptx::smem_u32(&full[stage]), 0);
                 const uint32_t a = smem + stage * kStageBytes, b = a + kTileBytes;
@@ -172,11 +180,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 1 && lane == 0 && rank == 0) {  // products
         constexpr uint32_t kInstruction = umma::instruction(kAMn, kBMn, 256, 256);
         uint32_t stage = 0, phase = 0, buffer = 0, buffer_phase = 1;
-        for (int64_t tile = pair; tile < tiles; tile += pairs) {
+        for (int64_t item = pair; item < items; item += pairs) {
             if (!wait(ptx::smem_u32(&sums_empty[buffer]), buffer_phase, &gave_up)) break;
             umma::fence_after();
             bool fine = true;
-            for (int64_t s = 0; s < k.steps && fine; ++s) {
+            const int64_t begin = first_step(item), stop = last_step(item);
+            for (int64_t s = begin; s < stop && fine; ++s) {
                 fine = wait(ptx::smem_u32(&full[stage]), phase, &gave_up);
                 if (!fine) break;
                 umma::fence_after();
@@ -184,7 +193,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kBlockK / 16; ++j)
                     umma::multiply(tmem + buffer * 256, umma::descriptor(a + j * (kAMn ? 2048 : 32), kTileBytes / 2),
-                                   umma::descriptor(b + j * (kBMn ? 2048 : 32), kTileBytes / 2), kInstruction, s > 0 || j > 0);
+                                   umma::descriptor(b + j * (kBMn ? 2048 : 32), kTileBytes / 2), kInstruction, s > begin || j > 0);
                 umma::commit(ptx::smem_u32(&empty[stage]));
                 if (++stage == kStages) stage = 0, phase ^= 1;
             }
@@ -205,9 +214,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
-        for (int64_t tile = pair; tile < tiles; tile += pairs) {
+        for (int64_t item = pair; item < items; item += pairs) {
             int64_t tm, tn;
-            place(tile, tm, tn);
+            place(item / k.parts, tm, tn);
             const int64_t half = k.tiles_m / 2;
             const int which = JOB == Job::Weights && tm >= half ? 1 : 0;
             const int64_t row = (tm - which * half) * 256 + rank * 128 + part * 32 + lane;
@@ -270,7 +279,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     float f[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-                    if (k.out_mapped) {
+                    if (k.parts > 1) {
+                        const int64_t all = JOB == Job::Weights ? 2 * rows : rows, n = row < rows ? k.D - d0 - c : 0;
+                        float *to = k.sums + ((item % k.parts) * all + which * rows + row) * k.D + d0 + c;
+                        if (k.D % 4 == 0) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                if (i < n) *reinterpret_cast<float4 *>(to + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < n) to[i] = f[i];
+                        }
+                    } else if (k.out_mapped) {
                         char *box = boxes + c / 64 % 2 * kOutBytes;
                         const int h = c / 32 % 2;
                         if (h == 0) free_box(true);
@@ -303,6 +324,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_wait();  // neither block leaves while the other may still reach it
     umma::fence_after();
     if (warp == 2) umma::tmem_free(tmem, 512);
+}
+
+// Outputs from the sums of parts of K, `half` values of out[0], then out[1]'s
+__global__ void __launch_bounds__(256) join_kernel(const float *sums, int64_t parts, int64_t all, int64_t half, bf16 *out0, bf16 *out1)
+{
+    ptx::pdl_trigger_dependents();
+    ptx::pdl_wait_prerequisites();
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += static_cast<int64_t>(gridDim.x) * 256) {
+        float v = 0.f;
+#pragma unroll 4
+        for (int64_t p = 0; p < parts; ++p) v += sums[p * all + i];
+        (i < half ? out0[i] : out1[i - half]) = from_f<bf16>(v);
+    }
 }
 
 // Rows of `columns` values into rows `pitch` values apart
@@ -379,6 +413,42 @@ rlscan_status pack_all(const rlscan_gated_projection_args &a, Layout &l, char *w
 
 bool map_of(CUtensorMap *m, const Operand &o, uint32_t box) { return umma::encode(m, o.p, o.rows, o.columns, o.pitch, box); }
 
+// Few tiles of a long K leave pairs without work: K is then taken in parts, at
+// least four steps each, whose sums are joined in order by another kernel.
+// Measured, gradients of 8 x 4096 x 12288 (dx: 16 tiles of 384 steps) SPLIT_TIME.
+struct Split {
+    int64_t parts, steps;
+};
+Split split_of(int64_t tiles, int64_t steps)
+{
+    const int64_t pairs = (sm_count() > 0 ? sm_count() : 152) / 2;
+    int64_t parts = tiles > 0 ? pairs / tiles : 1;
+    if (parts > steps / 4) parts = steps / 4;
+    if (parts < 2) return {1, steps};
+    const int64_t each = ceil_div(steps, parts);
+    return {ceil_div(steps, each), each};
+}
+struct GradSplits {
+    Split input, weights;
+    size_t bytes;  // of the sums of either, which take turns
+};
+GradSplits splits_of(const rlscan_gated_projection_args &a)
+{
+    GradSplits g;
+    g.input = split_of(ceil_div(a.M, 256) * ceil_div(a.D, 256), 2 * ceil_div(a.F, kBlockK));
+    g.weights = split_of(2 * ceil_div(a.F, 256) * ceil_div(a.D, 256), ceil_div(a.M, kBlockK));
+    const int64_t x = g.input.parts > 1 ? g.input.parts * a.M * a.D : 0, w = g.weights.parts > 1 ? g.weights.parts * 2 * a.F * a.D : 0;
+    g.bytes = static_cast<size_t>(x > w ? x : w) * sizeof(float);
+    return g;
+}
+
+rlscan_status join(const Work &w, int64_t rows, cudaStream_t s)
+{
+    const int64_t half = rows * w.D, all = w.out[1] != nullptr ? 2 * half : half, most = 16 * (sm_count() > 0 ? sm_count() : 152);
+    const int64_t blocks = ceil_div(all, 256);
+    return launch_overlapped(join_kernel, blocks < most ? blocks : most, 256, 0, s, w.sums, w.parts, all, half, w.out[0], w.out[1]);
+}
+
 template <Job JOB>
 rlscan_status launch_job(const Maps &maps, Work &w, cudaStream_t s)
 {
@@ -398,7 +468,7 @@ rlscan_status launch_job(const Maps &maps, Work &w, cudaStream_t s)
         int n = 0;
         return ok(cudaOccupancyMaxActiveClusters(&n, projection_kernel<JOB>, &cfg)) ? n : 0;
     });
-    const int64_t tiles = w.tiles_m * w.tiles_n, pairs = most > 0 ? most : 1;
+    const int64_t tiles = w.tiles_m * w.tiles_n * w.parts, pairs = most > 0 ? most : 1;
     if (w.M > 0x7fffffff - 256 || w.F > 0x7fffffff - 256 || w.D > 0x7fffffff - 256) return RLSCAN_ERR_SHAPE;
     return launch(true, projection_kernel<JOB>, 2 * (tiles < pairs ? tiles : pairs), kThreads, kSmem, s, maps, w);
 }
@@ -432,6 +502,7 @@ rlscan_status launch_gated_projection(const rlscan_gated_projection_args &a, voi
     Work w = {};
     w.M = a.M, w.D = a.D, w.F = a.F, w.act = static_cast<int>(a.activation);
     w.tiles_m = ceil_div(a.M, 256), w.tiles_n = ceil_div(a.F, 128), w.steps = ceil_div(a.D, kBlockK);
+    w.parts = 1, w.part_steps = w.steps;
     map_out(m, 0, w, h, a.M, a.F, a.F);
     return launch_job<Job::Forward>(m, w, s);
 }
@@ -439,7 +510,7 @@ rlscan_status launch_gated_projection(const rlscan_gated_projection_args &a, voi
 size_t gated_projection_backward_workspace(const rlscan_gated_projection_args &a)
 {
     if (a.M == 0 || a.F == 0 || a.D == 0) return 0;
-    return layout(a).bytes + static_cast<size_t>(a.M) * 2 * up8(a.F) * 2;
+    return layout(a).bytes + up256(static_cast<size_t>(a.M) * 2 * up8(a.F) * 2) + splits_of(a).bytes;
 }
 
 rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_args &a, const void *grad_h,
@@ -464,18 +535,24 @@ rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_arg
     w.M = a.M, w.D = a.D, w.F = a.F, w.act = static_cast<int>(a.activation);
     w.tiles_m = ceil_div(a.M, 256), w.tiles_n = ceil_div(a.F, 128), w.steps = ceil_div(a.D, kBlockK);
     w.grad_h = static_cast<const bf16 *>(grad_h), w.grad_h_stride = grad_h_stride, w.grad_h_vec = vec_rows(grad_h, grad_h_stride);
+    w.parts = 1, w.part_steps = w.steps;
     map_out(m, 0, w, g, a.M, a.F, 2 * pitch);
     map_out(m, 1, w, g + pitch, a.M, a.F, 2 * pitch);
     st = launch_job<Job::Gates>(m, w, s);
     if (st != RLSCAN_OK) return st;
+    const GradSplits splits = splits_of(a);
+    w.sums = reinterpret_cast<float *>(reinterpret_cast<char *>(g) + up256(static_cast<size_t>(a.M) * 2 * pitch * 2));
     const Operand gz{g, a.M, a.F, 2 * pitch, false}, gu{g + pitch, a.M, a.F, 2 * pitch, false};
     if (grad_x != nullptr) {
         Maps mx = {};
         if (!map_of(&mx.a[0], gz, 128) || !map_of(&mx.a[1], gu, 128) || !map_of(&mx.b[0], l.gate, 64) || !map_of(&mx.b[1], l.up, 64))
             return RLSCAN_ERR_CUDA;
         w.tiles_n = ceil_div(a.D, 256), w.steps = 2 * ceil_div(a.F, kBlockK);
+        w.parts = splits.input.parts, w.part_steps = splits.input.steps;
         map_out(mx, 0, w, grad_x, a.M, a.D, a.D);
+        w.out[1] = nullptr;
         st = launch_job<Job::Input>(mx, w, s);
+        if (st == RLSCAN_OK && w.parts > 1) st = join(w, a.M, s);
         if (st != RLSCAN_OK) return st;
     }
     if (grad_gate != nullptr) {
@@ -484,7 +561,9 @@ rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_arg
         w.tiles_m = 2 * ceil_div(a.F, 256), w.tiles_n = ceil_div(a.D, 256), w.steps = ceil_div(a.M, kBlockK);
         map_out(mw, 0, w, grad_gate, a.F, a.D, a.D);
         map_out(mw, 1, w, grad_up, a.F, a.D, a.D);
+        w.parts = splits.weights.parts, w.part_steps = splits.weights.steps;
         st = launch_job<Job::Weights>(mw, w, s);
+        if (st == RLSCAN_OK && w.parts > 1) st = join(w, a.F, s);
     }
     return st;
 }
