@@ -42,15 +42,8 @@ constexpr uint32_t kTileBytes = 128 * kBlockK * 2, kStageBytes = 2 * kTileBytes;
 constexpr uint32_t kOutBytes = 32 * 128;  // 32 rows of 64 values, two of a warp that takes sums out
 constexpr size_t kSmem = kStages * kStageBytes + 4 * 2 * kOutBytes + 1024;
 
-// 32 neighbouring values of a row, of which `n` are the row's, one by one
-__device__ __forceinline__ void store_row(bf16 *p, const float (&v)[32], int64_t n)
-{
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (j < n) p[j] = from_f<bf16>(v[j]);
-}
-// ... into half `h` of the lane's row of an output box, with its swizzle: the
-// 16-byte units of a row change places by the row's number
+// 32 neighbouring values into half `h` of the lane's row of an output box, with
+// its swizzle: the 16-byte units of a row change places by the row's number
 __device__ __forceinline__ void box_row(char *box, int lane, int h, const float (&v)[32])
 {
 #pragma unroll
@@ -59,6 +52,17 @@ __device__ __forceinline__ void box_row(char *box, int lane, int h, const float 
 #pragma unroll
         for (int j = 0; j < 4; ++j) w.set(j, v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
         w.store(reinterpret_cast<bf16 *>(box + lane * 128 + (((4 * h + i) ^ (lane & 7)) * 16)));
+    }
+}
+// A box to rows of any alignment, row by row: neighbouring lanes write
+// neighbouring values (each lane its own row's: 32 sectors a store, all
+// gradients of 1 x 2047 x 8192 438 us, so 147)
+__device__ __forceinline__ void copy_box(bf16 *to, int64_t stride, const char *box, int lane, int64_t rows, int64_t columns)
+{
+    for (int r = 0; r < 32 && r < rows; ++r, to += stride) {
+#pragma unroll
+        for (int c = lane; c < 64; c += 32)
+            if (c < columns) to[c] = *reinterpret_cast<const bf16 *>(box + r * 128 + (((c / 8) ^ (r & 7)) * 16) + c % 8 * 2);
     }
 }
 __device__ __forceinline__ void store_box2(const CUtensorMap *map, int64_t x, int64_t y, const char *box)
@@ -214,6 +218,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
+        auto put_box = [&](int i, int64_t x, int64_t y, int64_t rows, int64_t columns, const char *box) {
+            const bool some = y < rows && x < columns;
+            if (k.out_mapped) {
+                fence_async();
+                __syncwarp();
+                if (lane == 0 && some) store_box2(&maps.out[i], x, y, box);
+                if (lane == 0) stores_commit();
+            } else {
+                __syncwarp();
+                if (some) copy_box(k.out[i] + y * k.out_stride + x, k.out_stride, box, lane, rows - y, columns - x);
+            }
+        };
         for (int64_t item = pair; item < items; item += pairs) {
             int64_t tm, tn;
             place(item / k.parts, tm, tn);
@@ -250,23 +266,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                     const int h = c / 32 % 2;
-                    if (k.out_mapped) {
-                        char *box = boxes + (JOB == Job::Forward ? c / 64 * kOutBytes : 0);
-                        if (h == 0) free_box(JOB == Job::Forward);
-                        box_row(box, lane, h, v);
-                        if constexpr (JOB == Job::Gates) box_row(boxes + kOutBytes, lane, h, w);
-                        if (h == 1) {
-                            fence_async();
-                            __syncwarp();
-                            if (lane == 0 && row0 < rows && f0 + c - 32 < k.F) {
-                                store_box2(&maps.out[0], f0 + c - 32, row0, box);
-                                if constexpr (JOB == Job::Gates) store_box2(&maps.out[1], f0 + c - 32, row0, boxes + kOutBytes);
-                            }
-                            if (lane == 0) stores_commit();
-                        }
-                    } else {
-                        store_row(k.out[0] + row * k.out_stride + f0 + c, v, n);
-                        if constexpr (JOB == Job::Gates) store_row(k.out[1] + row * k.out_stride + f0 + c, w, n);
+                    char *box = boxes + (JOB == Job::Forward ? c / 64 * kOutBytes : 0);
+                    if (h == 0) free_box(JOB == Job::Forward);
+                    box_row(box, lane, h, v);
+                    if constexpr (JOB == Job::Gates) box_row(boxes + kOutBytes, lane, h, w);
+                    if (h == 1) {
+                        const int64_t x = f0 + c - 32;
+                        put_box(0, x, row0, rows, k.F, box);
+                        if constexpr (JOB == Job::Gates) put_box(1, x, row0, rows, k.F, boxes + kOutBytes);
                     }
                 }
             } else {
@@ -291,19 +298,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             for (int i = 0; i < 32; ++i)
                                 if (i < n) to[i] = f[i];
                         }
-                    } else if (k.out_mapped) {
+                    } else {
                         char *box = boxes + c / 64 % 2 * kOutBytes;
                         const int h = c / 32 % 2;
                         if (h == 0) free_box(true);
                         box_row(box, lane, h, f);
-                        if (h == 1) {
-                            fence_async();
-                            __syncwarp();
-                            if (lane == 0 && row0 < rows && d0 + c - 32 < k.D) store_box2(&maps.out[which], d0 + c - 32, row0, box);
-                            if (lane == 0) stores_commit();
-                        }
-                    } else {
-                        store_row(k.out[which] + row * k.out_stride + d0 + c, f, row < rows ? k.D - d0 - c : 0);
+                        if (h == 1) put_box(which, d0 + c - 32, row0, rows, k.D, box);
                     }
                 }
             }
@@ -339,15 +339,25 @@ __global__ void __launch_bounds__(256) join_kernel(const float *sums, int64_t pa
     }
 }
 
-// Rows of `columns` values into rows `pitch` values apart
+// Rows of `columns` values into rows `pitch` values apart, a warp a row
 __global__ void __launch_bounds__(256) pack_kernel(const bf16 *from, int64_t stride, bf16 *to, int64_t pitch, int64_t rows, int64_t columns)
 {
+    constexpr int AHEAD = 8;
     ptx::pdl_trigger_dependents();
     ptx::pdl_wait_prerequisites();
-    const int64_t all = rows * columns, step = static_cast<int64_t>(gridDim.x) * 256;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += step) {
-        const Division at = divide(i, columns);
-        to[at.q * pitch + at.r] = from[at.q * stride + at.r];
+    const int lane = threadIdx.x & 31;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; r < rows; r += static_cast<int64_t>(gridDim.x) * 8) {
+        const uint16_t *in = reinterpret_cast<const uint16_t *>(from + r * stride);
+        uint16_t *out = reinterpret_cast<uint16_t *>(to + r * pitch);
+        for (int64_t c = lane; c < columns; c += 32 * AHEAD) {
+            uint32_t v[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (c + 32 * i < columns) asm volatile("ld.global.u16 %0, [%1];" : "=r"(v[i]) : "l"(in + c + 32 * i));
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (c + 32 * i < columns) out[c + 32 * i] = static_cast<uint16_t>(v[i]);
+        }
     }
 }
 
@@ -396,7 +406,7 @@ Layout layout(const rlscan_gated_projection_args &a)
 rlscan_status pack(Operand &o, int64_t stride, void *to, cudaStream_t s)
 {
     if (!o.packed) return RLSCAN_OK;
-    const int64_t blocks = ceil_div(o.rows * o.columns, 256), most = 16 * (sm_count() > 0 ? sm_count() : 152);
+    const int64_t blocks = ceil_div(o.rows, 8), most = 8 * (sm_count() > 0 ? sm_count() : 152);
     const rlscan_status st = launch_overlapped(pack_kernel, blocks < most ? blocks : most, 256, 0, s, static_cast<const bf16 *>(o.p),
                                                stride, static_cast<bf16 *>(to), o.pitch, o.rows, o.columns);
     o.p = to;
@@ -415,7 +425,9 @@ bool map_of(CUtensorMap *m, const Operand &o, uint32_t box) { return umma::encod
 
 // Few tiles of a long K leave pairs without work: K is then taken in parts, at
 // least four steps each, whose sums are joined in order by another kernel.
-// Measured, gradients of 8 x 4096 x 12288 (dx: 16 tiles of 384 steps) SPLIT_TIME.
+// Measured, gradients of 8 x 4096 x 12288 (dx: 16 tiles of 384 steps) 266 us
+// whole, 186 in four parts of 96 steps (and dW of 16384 x 512 x 512 in parts: all
+// gradients 211 and 129).
 struct Split {
     int64_t parts, steps;
 };
