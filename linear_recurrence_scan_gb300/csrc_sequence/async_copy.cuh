@@ -99,10 +99,17 @@ inline bool encode_map(CUtensorMap *map, const void *p, bool bf16_type, int dims
         boxes[i] = box[i];
         if (i > 0) stride[i - 1] = static_cast<cuuint64_t>(strides[i - 1]);
     }
-    return call(map, bf16_type ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dims, const_cast<void *>(p), size,
-                stride, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto encode = [&] {
+        return call(map, bf16_type ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dims, const_cast<void *>(p), size,
+                    stride, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (encode()) return true;
+    // A thread that has made no runtime call of its own yet (autograd's, say)
+    // has no context for the driver's: setting its device gives it one.
+    const int device = current_device();
+    return device >= 0 && ok(cudaSetDevice(device)) && encode();
 }
 
 // A box into this block's shared memory, its bytes counted on `bar`

@@ -264,6 +264,26 @@ struct Exchange {
 
 __device__ __forceinline__ f2 apply(f2 h, const float4 &m) { return fma2(pair(m.x, m.y), h, pair(m.z, m.w)); }
 
+// The same where the factor 0 of a map with a reset cuts off what is in front of
+// it whatever its value: 0 times infinity is no 0.  Values that are not finite
+// are rare, so the short form goes first and this one where it gave such.
+__device__ __forceinline__ f2 apply_cut(f2 h, const float4 &m)
+{
+    const float2 v = halves(apply(h, m));
+    return pair(m.x == 0.f ? m.z : v.x, m.y == 0.f ? m.w : v.y);
+}
+__device__ __forceinline__ f2 multiply_cut(f2 f, const float4 &m)
+{
+    const float2 v = halves(mul2(f, pair(m.x, m.y)));
+    return pair(m.x == 0.f ? 0.f : v.x, m.y == 0.f ? 0.f : v.y);
+}
+// whether all lanes' values are finite
+__device__ __forceinline__ bool all_finite(f2 v)
+{
+    const float2 h = halves(v);
+    return __all_sync(0xffffffffu, fabsf(h.x) <= 3.4028234e38f && fabsf(h.y) <= 3.4028234e38f) != 0;
+}
+
 // What a step's warps share of one chain (states forwards, messages backwards).
 struct Chain {
     float4 map[2][kGatedWarps][32];  // (factor, rest) of each warp's tokens
@@ -301,7 +321,7 @@ __device__ __forceinline__ f2 in_front(C &c, E *ex, int64_t turn, int w, int lan
                                        int *gave_up)
 {
     const int p = static_cast<int>(turn & 1);
-    f2 h = carry;
+    f2 from = carry;  // in front of the block's tokens
     if constexpr (CLUSTER) {
         f2 factor = both(1.f), rest = both(0.f);  // the block's map
 #pragma unroll
@@ -310,27 +330,48 @@ __device__ __forceinline__ f2 in_front(C &c, E *ex, int64_t turn, int w, int lan
             factor = mul2(factor, pair(m.x, m.y));
             rest = apply(rest, m);
         }
+        if (!all_finite(rest) || !all_finite(factor)) {
+            factor = both(1.f), rest = both(0.f);
+#pragma unroll 1
+            for (int i = 0; i < kGatedWarps; ++i) {
+                const float4 m = c.get(p, FORWARD ? i : kGatedWarps - 1 - i, lane);
+                factor = multiply_cut(factor, m);
+                rest = apply_cut(rest, m);
+            }
+        }
         if (!has_given_up(gave_up)) {
             if (w < ranks) ex->send(p, rank, w, lane, factor, rest);
             if (threadIdx.x == 0) ex->expect(p, ranks);
         }
         ex->receive(p, static_cast<uint32_t>(turn >> 1) & 1u, gave_up);
+        const f2 first = carry;
 #pragma unroll 1
         for (int i = 0; i < ranks; ++i) {
             const int q = FORWARD ? i : ranks - 1 - i;
-            if (q == rank) h = carry;
+            if (q == rank) from = carry;
             carry = apply(carry, ex->map[p][q][lane]);
+        }
+        if (!all_finite(carry) || !all_finite(from)) {
+            carry = first;
+#pragma unroll 1
+            for (int i = 0; i < ranks; ++i) {
+                const int q = FORWARD ? i : ranks - 1 - i;
+                if (q == rank) from = carry;
+                carry = apply_cut(carry, ex->map[p][q][lane]);
+            }
         }
     } else if (turn > 0) {
         const float2 f = c.last[p ^ 1][lane];
-        h = pair(f.x, f.y);
+        from = pair(f.x, f.y);
     }
-    if constexpr (FORWARD) {
+    f2 h = from;
+    const int earlier = FORWARD ? w : kGatedWarps - 1 - w;
 #pragma unroll 1
-        for (int q = 0; q < w; ++q) h = apply(h, c.get(p, q, lane));
-    } else {
+    for (int i = 0; i < earlier; ++i) h = apply(h, c.get(p, FORWARD ? i : kGatedWarps - 1 - i, lane));
+    if (!all_finite(h)) {
+        h = from;
 #pragma unroll 1
-        for (int q = kGatedWarps - 1; q > w; --q) h = apply(h, c.get(p, q, lane));
+        for (int i = 0; i < earlier; ++i) h = apply_cut(h, c.get(p, FORWARD ? i : kGatedWarps - 1 - i, lane));
     }
     return h;
 }

@@ -20,30 +20,34 @@ struct ForwardArgs {
 // in order, give its first state, and its tokens follow.  The coefficients are
 // made once and stay in registers, so the inputs are read once.  CLUSTER: the
 // blocks of a cluster take neighbouring steps and hand their maps round.
-// The coefficients of TOK tokens where an episode starts, and past the last token
+// Past the last token the state is handed on
 template <int TOK>
-__device__ __forceinline__ void cut_and_pad(f2 (&keep)[TOK], f2 (&b)[TOK], uint32_t reset, int64_t t0, int64_t len)
+__device__ __forceinline__ void pad(f2 (&keep)[TOK], f2 (&b)[TOK], int64_t t0, int64_t len)
 {
-    if (reset != 0) {
-#pragma unroll
-        for (int k = 0; k < TOK; ++k)
-            if ((reset >> k & 1u) != 0u) keep[k] = both(0.f);
-    }
-    if (t0 + TOK > len) {  // padding hands the state on
+    if (t0 + TOK > len) {
 #pragma unroll
         for (int k = 0; k < TOK; ++k)
             if (t0 + k >= len) keep[k] = both(1.f), b[k] = both(0.f);
     }
 }
 
-template <int TOK>
-__device__ __forceinline__ void fold(const f2 (&keep)[TOK], const f2 (&b)[TOK], f2 &A, f2 &B)
+// A step's state from the one before.  A reset (bit k of `cut`) is a select,
+// not a product with 0; steps without one, which are most, take no time for it.
+template <bool CUTTING>
+__device__ __forceinline__ f2 step_state(f2 h, f2 keep, f2 b, uint32_t cut, int k)
 {
-    A = keep[0], B = b[0];
+    const f2 v = fma2(keep, h, b);
+    return CUTTING && (cut >> k & 1u) != 0u ? b : v;
+}
+
+template <bool CUTTING, int TOK>
+__device__ __forceinline__ void fold(const f2 (&keep)[TOK], const f2 (&b)[TOK], uint32_t cut, f2 &A, f2 &B)
+{
+    A = CUTTING && (cut & 1u) != 0u ? both(0.f) : keep[0], B = b[0];
 #pragma unroll
     for (int k = 1; k < TOK; ++k) {
-        A = mul2(A, keep[k]);
-        B = fma2(keep[k], B, b[k]);
+        A = CUTTING && (cut >> k & 1u) != 0u ? both(0.f) : mul2(A, keep[k]);
+        B = step_state<CUTTING>(B, keep[k], b[k], cut, k);
     }
 }
 
@@ -111,9 +115,11 @@ __global__ void __launch_bounds__(32 * kGatedWarps, sizeof(T) == 2 && VEC ? 3 : 
             keep[i] = v.a;
             b[i] = mul2(mul2(v.root, v.i), x[i].get());
         }
-        cut_and_pad(keep, b, starts(flag), t0, k.len);
+        const uint32_t cut = starts(flag);
+        pad(keep, b, t0, k.len);
         if (s + 1 < k.steps) fetch(t0 + k.span);
-        fold(keep, b, A, B);
+        if (cut == 0) fold<false>(keep, b, cut, A, B);
+        else fold<true>(keep, b, cut, A, B);
         chain.put(p, k.w, k.lane, A, B);
         __syncthreads();
         Exchange<kGatedCluster> *ex = nullptr;
@@ -124,7 +130,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, sizeof(T) == 2 && VEC ? 3 : 
             store_two<float, VEC>(to + l.d, h, l.on0, l.on1);
         }
         T *to = static_cast<T *>(o.y) + (k.n * a.T + t0) * a.D + l.block;
-        if (t0 + TOK <= k.len) {
+        if (t0 + TOK <= k.len && cut == 0) {
 #pragma unroll
             for (int i = 0; i < TOK; ++i, to += a.D) {
                 h = fma2(keep[i], h, b[i]);
@@ -133,7 +139,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, sizeof(T) == 2 && VEC ? 3 : 
         } else {
 #pragma unroll
             for (int i = 0; i < TOK; ++i, to += a.D) {
-                h = fma2(keep[i], h, b[i]);
+                h = step_state<true>(h, keep[i], b[i], cut, i);
                 const bool in = t0 + i < a.T;
                 store_two<T, VEC>(to + l.d, t0 + i < k.len ? h : both(0.f), in && l.on0, in && l.on1);
             }
@@ -221,9 +227,11 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 3)
             keep[i] = v.a;
             b[i] = mul2(mul2(v.root, v.i), read_two<T>(in + 2 * BYTES + i * STEP));
         }
-        cut_and_pad(keep, b, starts(flag), t0, k.len);
+        const uint32_t cut = starts(flag);
+        pad(keep, b, t0, k.len);
         if (s + 1 < k.steps) flag = fetch_flag<TOK>(a.resets, k.n * a.T, t0 + k.span, k.len, k.lane);
-        fold(keep, b, A, B);
+        if (cut == 0) fold<false>(keep, b, cut, A, B);
+        else fold<true>(keep, b, cut, A, B);
         chain.put(p, k.w, k.lane, A, B);
         __syncthreads();  // all have taken the stage's values
         if (threadIdx.x == 0 && s + 2 < k.steps && !has_given_up(&gave_up)) fetch(s + 2);
@@ -236,10 +244,18 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 3)
         }
         if (k.lane == 0) stores_read();  // the step before has left the warp's part
         __syncwarp();
+        if (cut == 0) {
 #pragma unroll
-        for (int i = 0; i < TOK; ++i) {
-            h = fma2(keep[i], h, b[i]);
-            write_two<T>(out + mine + i * kGatedWidth * sizeof(T), h);
+            for (int i = 0; i < TOK; ++i) {
+                h = fma2(keep[i], h, b[i]);
+                write_two<T>(out + mine + i * kGatedWidth * sizeof(T), h);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < TOK; ++i) {
+                h = step_state<true>(h, keep[i], b[i], cut, i);
+                write_two<T>(out + mine + i * kGatedWidth * sizeof(T), h);
+            }
         }
         if (t0 + TOK > k.len) {  // y of padding is 0
 #pragma unroll

@@ -76,6 +76,20 @@ __device__ __forceinline__ void finish(const rlscan_gated_scan_args &a, const Ba
     }
 }
 
+// The state in front of the warp's tokens, from the step's checkpoint
+__device__ __forceinline__ f2 state_in_front(const TwoChains &c, int p, int w, int lane, f2 mark)
+{
+    f2 h = mark;
+#pragma unroll 1
+    for (int q = 0; q < w; ++q) h = apply(h, c.map[p][q][lane]);
+    if (!all_finite(h)) {
+        h = mark;
+#pragma unroll 1
+        for (int q = 0; q < w; ++q) h = apply_cut(h, c.map[p][q][lane]);
+    }
+    return h;
+}
+
 // Arrays of any alignment: the next step's values are loaded into registers
 // while this one's are worked on.
 template <class T, bool VEC, bool CLUSTER>
@@ -131,11 +145,6 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
             b[i] = mul2(mul2(v[i].root, v[i].i), xs[i]);
             keep[i] = v[i].a;
         }
-        if (cut != 0) {
-#pragma unroll
-            for (int i = 0; i < TOK; ++i)
-                if ((cut >> i & 1u) != 0u) keep[i] = both(0.f);
-        }
         const bool pad = t0 + TOK > k.len;
         if (pad) {  // padding hands state and message on
 #pragma unroll
@@ -143,31 +152,41 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
                 if (t0 + i >= k.len) keep[i] = both(1.f), b[i] = gs[i] = xs[i] = both(0.f);
         }
         if (s > 0) fetch(tile - ranks);
-        f2 A = keep[0], B = b[0], M = mul2(keep[TOK - 1], gs[TOK - 1]);
+        auto cuts = [&](int i) { return (cut >> i & 1u) != 0u; };
+        f2 A = both(1.f), B = both(0.f), M = both(0.f);
+        if (cut == 0) {
 #pragma unroll
-        for (int i = 1; i < TOK; ++i) {
-            A = mul2(A, keep[i]);
-            B = fma2(keep[i], B, b[i]);
-            M = mul2(keep[TOK - 1 - i], add2(gs[TOK - 1 - i], M));
+            for (int i = 0; i < TOK; ++i) {
+                A = mul2(A, keep[i]);
+                B = fma2(keep[i], B, b[i]);
+                M = mul2(keep[TOK - 1 - i], add2(gs[TOK - 1 - i], M));
+            }
+        } else {  // a reset is a select, not a product with 0
+#pragma unroll
+            for (int i = 0; i < TOK; ++i) {
+                A = cuts(i) ? both(0.f) : mul2(A, keep[i]);
+                B = cuts(i) ? b[i] : fma2(keep[i], B, b[i]);
+                M = cuts(TOK - 1 - i) ? both(0.f) : mul2(keep[TOK - 1 - i], add2(gs[TOK - 1 - i], M));
+            }
         }
         chain.put(p, k.w, k.lane, A, B, M);
         __syncthreads();
         Exchange<kGatedCluster> *ex = nullptr;
         if constexpr (CLUSTER) ex = &exchange;
         f2 m = in_front<CLUSTER, false>(chain, ex, turn, k.w, k.lane, k.rank, ranks, carry, &gave_up);
-#pragma unroll 1
-        for (int q = 0; q < k.w; ++q) state = apply(state, chain.map[p][q][k.lane]);
-        f2 before[TOK];  // the state before each token
+        state = state_in_front(chain, p, k.w, k.lane, state);
+        f2 before[TOK];  // the state before each token, 0 at a reset
 #pragma unroll
         for (int i = 0; i < TOK; ++i) {
-            before[i] = state;
-            state = fma2(keep[i], state, b[i]);
+            before[i] = cuts(i) ? both(0.f) : state;
+            state = fma2(keep[i], before[i], b[i]);
         }
         const int64_t at_last = (k.n * a.T + t0 + TOK - 1) * a.D + l.block;
         T *px = static_cast<T *>(o.g.x) + at_last, *pg = static_cast<T *>(o.g.gate) + at_last, *pi = static_cast<T *>(o.g.input_gate) + at_last;
 #pragma unroll
         for (int i = TOK - 1; i >= 0; --i, px -= a.D, pg -= a.D, pi -= a.D) {
             TokenGrads t = token_grads(v[i], keep[i], xs[i], gs[i], before[i], log_decay, m);
+            if (cuts(i)) m = both(0.f);
             bool on0 = l.on0, on1 = l.on1;
             if (pad) {
                 if (t0 + i >= k.len) t.x = t.gate = t.input_gate = t.share = both(0.f);
@@ -292,17 +311,18 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
             for (int i = 0; i < TOK; ++i)
                 if (t0 + i >= k.len) v[i].a = both(1.f), v[i].root = both(0.f);
         }
-        // Steps without a reset, which are most, take a path of their own: the
-        // decays that a reset cuts would otherwise be kept beside the others.
+        // A reset is a select, not a product with 0.  Steps without one, which are
+        // most, take a path of their own.
         auto fold = [&](auto cutting) {
-            auto keep = [&](int i) { return decltype(cutting)::value && (cut >> i & 1u) != 0u ? both(0.f) : v[i].a; };
+            auto cuts = [&](int i) { return decltype(cutting)::value && (cut >> i & 1u) != 0u; };
 #pragma unroll
             for (int i = 0; i < TOK; ++i) {
-                A = mul2(A, keep(i));
-                B = fma2(keep(i), B, mul2(mul2(v[i].root, v[i].i), read_two<T>(in + 2 * BYTES + i * STEP)));
+                const f2 b = mul2(mul2(v[i].root, v[i].i), read_two<T>(in + 2 * BYTES + i * STEP));
+                A = cuts(i) ? both(0.f) : mul2(A, v[i].a);
+                B = cuts(i) ? b : fma2(v[i].a, B, b);
             }
 #pragma unroll
-            for (int i = TOK - 1; i >= 0; --i) M = mul2(keep(i), add2(read_two<T>(in + 3 * BYTES + i * STEP), M));
+            for (int i = TOK - 1; i >= 0; --i) M = cuts(i) ? both(0.f) : mul2(v[i].a, add2(read_two<T>(in + 3 * BYTES + i * STEP), M));
         };
         if (cut == 0) fold(std::false_type());
         else fold(std::true_type());
@@ -314,20 +334,20 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
         Exchange<kBackCluster> *ex = nullptr;
         if constexpr (CLUSTER) ex = &exchange;
         f2 m = in_front<CLUSTER, false>(chain, ex, turn, k.w, k.lane, k.rank, ranks, carry, &gave_up);
-#pragma unroll 1
-        for (int q = 0; q < k.w; ++q) state = apply(state, chain.map[p][q][k.lane]);
+        state = state_in_front(chain, p, k.w, k.lane, state);
         auto gradients = [&](auto cutting) {
-            auto keep = [&](int i) { return decltype(cutting)::value && (cut >> i & 1u) != 0u ? both(0.f) : v[i].a; };
-            f2 before[TOK];  // the state before each token
+            auto cuts = [&](int i) { return decltype(cutting)::value && (cut >> i & 1u) != 0u; };
+            f2 before[TOK];  // the state before each token, 0 at a reset
 #pragma unroll
             for (int i = 0; i < TOK; ++i) {
-                before[i] = state;
-                state = fma2(keep(i), state, mul2(mul2(v[i].root, v[i].i), read_two<T>(in + 2 * BYTES + i * STEP)));
+                before[i] = cuts(i) ? both(0.f) : state;
+                state = fma2(v[i].a, before[i], mul2(mul2(v[i].root, v[i].i), read_two<T>(in + 2 * BYTES + i * STEP)));
             }
 #pragma unroll
             for (int i = TOK - 1; i >= 0; --i) {
-                TokenGrads t = token_grads(v[i], keep(i), read_two<T>(in + 2 * BYTES + i * STEP), read_two<T>(in + 3 * BYTES + i * STEP),
+                TokenGrads t = token_grads(v[i], v[i].a, read_two<T>(in + 2 * BYTES + i * STEP), read_two<T>(in + 3 * BYTES + i * STEP),
                                            before[i], log_decay, m);
+                if (cuts(i)) m = both(0.f);
                 if (pad && t0 + i >= k.len) t.x = t.gate = t.input_gate = t.share = both(0.f);
                 sum = add2(sum, t.share);
                 write_two<T>(in + i * STEP, t.gate);

@@ -84,3 +84,194 @@ def test_rows_longer_than_a_cluster_holds():
 def test_teacher_types(teacher_dtype, token_dtype):
     logits, teacher, tokens, mask, grad, _ = distill_inputs(2, 9, 300, 12, BF16, 4, teacher_dtype, token_dtype)
     check(logits, teacher, tokens, mask.bool(), grad)
+
+
+def test_masked_vocabulary():
+    """Logits of -infinity and of the type's lowest value: probability 0, or, where a row has nothing else, all alike."""
+    for dtype in (F32, BF16):
+        logits, teacher, tokens, _, grad, rng = distill_inputs(1, 4, 700, 5, dtype, 1)
+        tokens = tokens.clamp(0, 99)
+        low = torch.finfo(dtype).min
+        logits[0, 0, 100:] = -float("inf")
+        logits[0, 1, 100:] = low
+        loss, g = check(logits, teacher, tokens, None, grad)
+        assert not g[0, :2, 100:].any()
+        for k in range(5):   # tokens twice and all rows of one value
+            tokens[0, :, k] = k
+        logits[0, 2] = low
+        logits[0, 3] = 0
+        loss, g = check(logits[:, 2:], teacher[:, 2:], tokens[:, 2:], None, grad[:, 2:])
+        teacher[0, 3] = teacher[0, 2]
+        a, _ = L().distill_loss_and_grad(grad.to(DEV), logits.to(DEV), teacher.to(DEV), tokens.to(DEV))
+        assert torch.equal(a[0, 2], a[0, 3])
+        # the teacher learns of a token that the student rules out: an infinite loss, a finite gradient
+        logits[0, 0, tokens[0, 0, 0]] = -float("inf")
+        a, g = L().distill_loss_and_grad(grad.to(DEV), logits.to(DEV), teacher.to(DEV), tokens.to(DEV))
+        assert a[0, 0] == float("inf") and torch.isfinite(g[0, 0]).all()
+
+
+@pytest.mark.parametrize("V", [50, 3000, 40000])
+def test_rows_without_a_loss(V):
+    """Masked rows (NaN in them), rows without a teacher's token, teachers of -infinity: loss 0, gradient 0."""
+    for dtype in (F32, BF16):
+        logits, teacher, tokens, mask, grad, _ = distill_inputs(2, 6, V, 4, dtype, 2)
+        mask[:] = 1
+        mask[0, 2] = mask[1, 5] = 0
+        logits[0, 2] = float("nan")
+        teacher[1, 5] = float("nan")
+        tokens[0, 3] = -1
+        teacher[0, 4] = -float("inf")
+        teacher[0, 5, 0] = -float("inf")
+        tokens[0, 5] = torch.arange(4)
+        loss, g = check(logits, teacher, tokens, mask, grad)
+        for n, t in ((0, 2), (1, 5), (0, 3), (0, 4)):
+            assert loss[n, t] == 0 and not g[n, t].any()
+        none = torch.zeros_like(mask)
+        loss, g = check(logits, teacher, tokens, none, grad)
+        assert not loss.any() and not g.any()
+
+
+def test_values_that_are_not_numbers():
+    """A NaN or +infinity stays in its row; a row of -infinity alone has no distribution."""
+    logits, teacher, tokens, _, grad, _ = distill_inputs(1, 6, 900, 3, F32, 3)
+    logits[0, 0, 5] = float("nan")
+    logits[0, 1, 7] = float("inf")
+    logits[0, 2] = -float("inf")
+    teacher[0, 3, 0] = float("nan")
+    teacher[0, 4, 0] = float("inf")
+    for d in (F32, BF16):
+        loss, norm = L().distill_loss(logits.to(DEV).to(d), teacher.to(DEV), tokens.to(DEV), return_normalizers=True)
+        both, g = L().distill_loss_and_grad(grad.to(DEV), logits.to(DEV).to(d), teacher.to(DEV), tokens.to(DEV))
+        for v in (loss, both):
+            assert torch.isnan(v[0, :5]).all() and torch.isfinite(v[0, 5])
+        assert torch.isnan(g[0, :3]).all() and torch.isfinite(g[0, 5]).all()
+        assert torch.isnan(g[0, 3]).any() and torch.isnan(g[0, 4]).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [1, 9, 300, 1003, 5001, 33001])
+@pytest.mark.parametrize("pad,offset", [(8, 0), (5, 3), (16, 8), (1, 1)])
+def test_strides_and_alignments(pad, offset, V, dtype):
+    """Slices of wider arrays, whose units of 16 bytes lie otherwise than the dense gradient's; NaN around them."""
+    logits, teacher, tokens, mask, grad, _ = distill_inputs(2, 3, V, 5, dtype, V)
+    check(logits, teacher, tokens, mask, grad, on_gpu=strided(logits, pad, offset))
+    wide = torch.full((2, 7, V), float("nan"), dtype=dtype, device=DEV)   # every other token, the last one left out
+    wide[:, :6:2] = logits.to(DEV)
+    check(logits, teacher, tokens, mask, grad, on_gpu=wide[:, :6:2])
+
+
+def test_repeated_tokens():
+    """One token K times, and pairs of them over the chunks of a warp."""
+    logits, teacher, tokens, _, grad, _ = distill_inputs(1, 3, 500, 200, F32, 5)
+    tokens[0, 0] = 7
+    tokens[0, 1] = torch.arange(200) % 100
+    check(logits, teacher, tokens, None, grad)
+
+
+def test_expanded_arguments_and_empty_sizes():
+    logits, teacher, tokens, _, grad, _ = distill_inputs(2, 4, 60, 3, F32, 6)
+    one = teacher[:, :1].to(DEV).expand(2, 4, 3)
+    a = L().distill_loss(logits.to(DEV), one, tokens.to(DEV))
+    assert torch.equal(a, L().distill_loss(logits.to(DEV), one.contiguous(), tokens.to(DEV)))
+    w = torch.full((1, 1), 0.5, device=DEV).expand(2, 4)
+    assert torch.equal(L().distill_loss_and_grad(w, logits.to(DEV), one, tokens.to(DEV))[1],
+                       L().distill_loss_and_grad(w.contiguous(), logits.to(DEV), one, tokens.to(DEV))[1])
+    for N, T in ((0, 4), (2, 0)):
+        z, th, tok = torch.zeros(N, T, 9, device=DEV), torch.zeros(N, T, 3, device=DEV), torch.zeros(N, T, 3, dtype=torch.long, device=DEV)
+        loss, norm = L().distill_loss(z, th, tok, return_normalizers=True)
+        assert loss.shape == (N, T) and norm.shape == (N, T, 2)
+        assert L().distill_loss_backward(loss, z, th, tok, norm).shape == z.shape
+        assert L().distill_loss_and_grad(loss, z, th, tok)[1].shape == z.shape
+
+
+def test_autograd():
+    logits, teacher, tokens, mask, grad, _ = distill_inputs(2, 5, 400, 6, BF16, 7)
+    leaf = logits.to(DEV).requires_grad_()
+    loss = L().distill_loss(leaf, teacher.to(DEV), tokens.to(DEV), 2.0, mask.to(DEV))
+    want, g = L().distill_loss_and_grad(grad.to(DEV), logits.to(DEV), teacher.to(DEV), tokens.to(DEV), 2.0, mask.to(DEV))
+    assert torch.equal(loss, want)
+    (got,) = torch.autograd.grad((loss * grad.to(DEV)).sum(), leaf, create_graph=True)
+    torch.testing.assert_close(got, g, rtol=2 ** -7, atol=1e-30)
+    with pytest.raises(RuntimeError, match="once_differentiable|does not require grad"):
+        torch.autograd.grad(got.float().sum(), leaf)
+    with pytest.raises(ValueError, match="detach"):
+        L().distill_loss(leaf, teacher.to(DEV).requires_grad_(), tokens.to(DEV))
+
+
+def test_streams_and_graphs():
+    args = [distill_inputs(2, 40, V, 6, BF16, V)[:5] for V in (300, 9000, 50000)]
+    for logits, teacher, tokens, mask, grad in args:
+        dev = [t.to(DEV) for t in (logits, teacher, tokens)]
+        w, m = grad.to(DEV), mask.to(DEV)
+        want = L().distill_loss_and_grad(w, *dev, mask=m)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got = L().distill_loss_and_grad(w, *dev, mask=m)
+        side.synchronize()
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+        graphs = []
+        for _ in range(2):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                loss, norm = L().distill_loss(*dev, mask=m, return_normalizers=True)
+                g = L().distill_loss_backward(w, *dev, norm, mask=m)
+                both = L().distill_loss_and_grad(w, *dev, mask=m)
+            graphs.append((graph, loss, g, *both))
+        dev[0].copy_(-dev[0])
+        for graph, *_ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        want = L().distill_loss_and_grad(w, *dev, mask=m)
+        for _, loss, g, a, b in graphs:
+            assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+            torch.testing.assert_close(loss, want[0], rtol=1e-5, atol=1e-5)
+            torch.testing.assert_close(g, want[1], rtol=2 ** -7, atol=1e-7)
+    L().workspace_status()
+
+
+def test_offsets_past_32_bits():
+    """2^31 logits and more: the last rows against the same rows alone."""
+    N, T, V, K = 1, 17000, 131072, 4
+    logits = torch.empty(N, T, V, dtype=BF16, device=DEV)
+    some, teacher, tokens, _, grad, _ = distill_inputs(1, 3, V, K, BF16, 8)
+    logits[:] = 0
+    logits[0, -3:] = some[0].to(DEV)
+    th, tok = torch.zeros(N, T, K, device=DEV), torch.zeros(N, T, K, dtype=torch.int32, device=DEV)
+    w = torch.zeros(N, T, device=DEV)
+    th[0, -3:], tok[0, -3:], w[0, -3:] = teacher[0].to(DEV), tokens[0].to(DEV, torch.int32), grad[0].to(DEV)
+    loss, g = L().distill_loss_and_grad(w, logits, th, tok)
+    want, gw = L().distill_loss_and_grad(w[:, -3:].contiguous(), logits[:, -3:], th[:, -3:], tok[:, -3:])
+    torch.testing.assert_close(loss[:, -3:], want, rtol=1e-5, atol=1e-5)
+    torch.testing.assert_close(g[:, -3:], gw, rtol=2 ** -7, atol=1e-7)
+    torch.testing.assert_close(L().distill_loss(logits, th, tok), loss, rtol=1e-5, atol=1e-5)
+
+
+def test_refusals():
+    z, th = torch.zeros(2, 3, 9, device=DEV), torch.zeros(2, 3, 4, device=DEV)
+    tok, w = torch.zeros(2, 3, 4, dtype=torch.long, device=DEV), torch.zeros(2, 3, device=DEV)
+    f = L().distill_loss
+    with pytest.raises(TypeError, match="teacher_tokens"):
+        f(z, th, tok.float())
+    with pytest.raises(TypeError, match="teacher_logits"):
+        f(z, th.half(), tok)
+    with pytest.raises(ValueError, match="teacher_tokens shape"):
+        f(z, th, tok[..., :3])
+    with pytest.raises(ValueError, match="256"):
+        f(z, torch.zeros(2, 3, 257, device=DEV), tok)
+    with pytest.raises(ValueError, match="256"):
+        f(z, th[..., :0], tok[..., :0])
+    for tau in (0.0, -1.0, float("nan"), float("inf"), 0):
+        with pytest.raises(ValueError, match="temperature"):
+            f(z, th, tok, tau)
+    with pytest.raises(ValueError, match="vocabulary"):
+        f(z[..., :0], th, tok)
+    with pytest.raises(ValueError, match="mask shape"):
+        f(z, th, tok, mask=torch.ones(2, 4, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError, match="normalizers"):
+        L().distill_loss_backward(w, z, th, tok, None)
+    with pytest.raises(TypeError, match="grad_loss"):
+        L().distill_loss_backward(w.double(), z, th, tok, torch.zeros(2, 3, 2, device=DEV))
+    with pytest.raises(TypeError, match="grad_loss"):
+        L().distill_loss_and_grad(None, z, th, tok)
+    assert torch.equal(f(z, th, tok, 1), f(z, th, tok, 1.0))

@@ -58,3 +58,174 @@ def test_odd_sizes(M, D, F):
 
 def test_more_tiles_than_pairs():
     check(2100, 128, 3000)
+
+
+@pytest.mark.parametrize("M", [1, 7, 8, 9, 16, 17, 31, 32, 33])
+@pytest.mark.parametrize("D,F", [(64, 48), (40, 17), (33, 70), (8, 300), (520, 16)])
+def test_few_rows(M, D, F):
+    check(M, D, F, "gelu" if M % 2 else "silu")
+
+
+@pytest.mark.parametrize("M", [5, 70])
+@pytest.mark.parametrize("pad,offset", [(8, 0), (16, 8), (1, 1), (3, 0), (8, 4)])
+def test_strides_and_alignments(pad, offset, M):
+    """Slices of wider arrays with NaN around them."""
+    def place(t):
+        wide = torch.full((t.shape[0], t.shape[1] + pad), float("nan"), dtype=t.dtype, device=DEV)
+        wide[:, offset:offset + t.shape[1]] = t.to(DEV)
+        return wide[:, offset:offset + t.shape[1]]
+    check(M, 72, 136, place=place)
+
+
+def test_halves_of_one_weight_and_leading_dimensions():
+    x, wg, wu, gh, _ = projection_inputs(60, 64, 96, 5)
+    both = torch.cat([wg, wu]).to(DEV)
+    want = L().gated_projection(x.to(DEV), wg.to(DEV), wu.to(DEV))
+    got = L().gated_projection(x.to(DEV).view(3, 20, 64), both[:96], both[96:])
+    assert got.shape == (3, 20, 96) and torch.equal(got.view(60, 96), want)
+    g = L().gated_projection_backward(gh.to(DEV), x.to(DEV), wg.to(DEV), wu.to(DEV))
+    h = L().gated_projection_backward(gh.to(DEV).view(3, 20, 96), x.to(DEV).view(3, 20, 64), both[:96], both[96:])
+    assert h.x.shape == (3, 20, 64)
+    assert torch.equal(h.x.view(60, 64), g.x) and torch.equal(h.gate_weight, g.gate_weight) and torch.equal(h.up_weight, g.up_weight)
+    # one row for all, a column-major weight, the same weight twice
+    row = x[:1].to(DEV).expand(60, 64)
+    assert torch.equal(L().gated_projection(row, both[:96], both[96:]), L().gated_projection(row.contiguous(), both[:96], both[96:]))
+    turned = wg.to(DEV).t().contiguous().t()
+    assert torch.equal(L().gated_projection(x.to(DEV), turned, wu.to(DEV)), want)
+    assert torch.equal(L().gated_projection(x.to(DEV), wg.to(DEV), wg.to(DEV)), L().gated_projection(x.to(DEV), wg.to(DEV), wg.to(DEV).clone()))
+
+
+def test_sums_in_parts():
+    """Few tiles of a long K (dx of few rows, dW of few columns) join parts."""
+    check(20, 256, 3000)
+    check(3000, 64, 72)
+    check(2500, 130, 65, "gelu")
+    check(33, 70, 4001)
+
+
+def test_large_values():
+    """Activations far out: gates of hundreds, both signs."""
+    x, wg, wu, gh, _ = projection_inputs(40, 64, 64, 3, scale=100.0)
+    for act in ("silu", "gelu"):
+        h = L().gated_projection(x.to(DEV), wg.to(DEV), wu.to(DEV), act)
+        g = L().gated_projection_backward(gh.to(DEV), x.to(DEV), wg.to(DEV), wu.to(DEV), act)
+        want = projection_oracle(x, wg, wu, gh, act)
+        assert all(torch.isfinite(t).all() for t in (h, *g))
+        got = h.double().cpu().numpy()
+        assert (np.abs(got - want["h"][0]) <= 2.0 ** -7 * np.abs(want["h"][0]) + 0.02).all()
+
+
+def test_empty_sizes():
+    w = torch.ones(6, 8, dtype=BF16, device=DEV)
+    x = torch.ones(0, 8, dtype=BF16, device=DEV)
+    assert L().gated_projection(x, w, w).shape == (0, 6)
+    g = L().gated_projection_backward(torch.ones(0, 6, dtype=BF16, device=DEV), x, w, w)
+    assert g.x.shape == (0, 8) and not g.gate_weight.any() and not g.up_weight.any()
+    x = torch.ones(5, 8, dtype=BF16, device=DEV)
+    assert L().gated_projection(x, w[:0], w[:0]).shape == (5, 0)
+    g = L().gated_projection_backward(torch.ones(5, 0, dtype=BF16, device=DEV), x, w[:0], w[:0])
+    assert not g.x.any() and g.gate_weight.shape == (0, 8)
+
+
+def test_autograd():
+    x, wg, wu, gh, _ = (t.to(DEV) if isinstance(t, torch.Tensor) else t for t in projection_inputs(70, 64, 96, 9))
+    want = L().gated_projection_backward(gh, x, wg, wu, "gelu")
+    leaves = [t.clone().requires_grad_() for t in (x, wg, wu)]
+    h = L().gated_projection(*leaves, "gelu")
+    assert torch.equal(h, L().gated_projection(x, wg, wu, "gelu"))
+    got = torch.autograd.grad(h, leaves, gh, create_graph=True)
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+    with pytest.raises(RuntimeError, match="once_differentiable|does not require grad"):
+        torch.autograd.grad(got[0].float().sum(), leaves[1])
+    for i in range(3):   # one of them alone
+        some = [t.clone().requires_grad_(j == i) for j, t in enumerate((x, wg, wu))]
+        (one,) = torch.autograd.grad(L().gated_projection(*some, "gelu"), [some[i]], gh)
+        assert torch.equal(one, want[i])
+
+
+def test_streams_and_graphs():
+    for M in (3, 90):
+        x, wg, wu, gh, _ = (t.to(DEV) if isinstance(t, torch.Tensor) else t for t in projection_inputs(M, 72, 129, M))
+        want = (L().gated_projection(x, wg, wu), *L().gated_projection_backward(gh, x, wg, wu))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got = (L().gated_projection(x, wg, wu), *L().gated_projection_backward(gh, x, wg, wu))
+        side.synchronize()
+        for p, q in zip(want, got):
+            assert torch.equal(p, q)
+        graphs = []
+        for _ in range(2):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                out = (L().gated_projection(x, wg, wu), *L().gated_projection_backward(gh, x, wg, wu))
+            graphs.append((graph, out))
+        x.copy_(-x)
+        for graph, _ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        want = (L().gated_projection(x, wg, wu), *L().gated_projection_backward(gh, x, wg, wu))
+        for _, out in graphs:
+            for p, q in zip(want, out):
+                assert torch.equal(p, q)
+    L().workspace_status()
+
+
+def test_two_streams_at_once():
+    """Projections and gated scans that share the SMs."""
+    x, wg, wu, gh, _ = (t.to(DEV) if isinstance(t, torch.Tensor) else t for t in projection_inputs(1500, 512, 1000, 4))
+    s = torch.randn(4, 900, 256, device=DEV).to(BF16)
+    ld = -torch.rand(256, device=DEV) - 0.01
+    want = (*L().gated_projection_backward(gh, x, wg, wu), *L().gated_scan(s, s, s, ld))
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        with torch.cuda.stream(one):
+            a = L().gated_projection_backward(gh, x, wg, wu)
+        with torch.cuda.stream(two):
+            b = L().gated_scan(s, s, s, ld)
+            c = L().gated_projection_backward(gh, x, wg, wu)
+    torch.cuda.synchronize()
+    for p, q in zip(want, (*a, *b)):
+        assert torch.equal(p, q)
+    for p, q in zip(a, c):
+        assert torch.equal(p, q)
+    L().workspace_status()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 outputs: rows of the end against the same rows alone."""
+    M, D, F = 70000, 64, 33000
+    torch.manual_seed(0)
+    x, wg, wu = (torch.randn(n, D, device=DEV).to(BF16) for n in (M, F, F))
+    h = L().gated_projection(x, wg, wu)
+    tail = L().gated_projection(x[-300:], wg, wu)
+    torch.testing.assert_close(h[-300:], tail, rtol=2 ** -7, atol=1e-6)
+    gh = torch.zeros(M, F, dtype=BF16, device=DEV)
+    gh[-300:] = torch.randn(300, F, device=DEV).to(BF16)
+    g, t = L().gated_projection_backward(gh, x, wg, wu), L().gated_projection_backward(gh[-300:], x[-300:], wg, wu)
+    torch.testing.assert_close(g.x[-300:], t.x, rtol=2 ** -6, atol=2.0)
+    torch.testing.assert_close(g.gate_weight, t.gate_weight, rtol=2 ** -6, atol=0.5)
+    assert not g.x[:-300].any()
+
+
+def test_refusals():
+    x, w = torch.zeros(4, 8, dtype=BF16, device=DEV), torch.zeros(6, 8, dtype=BF16, device=DEV)
+    f = L().gated_projection
+    with pytest.raises(TypeError, match="bfloat16"):
+        f(x.float(), w, w)
+    with pytest.raises(TypeError, match="gate_weight"):
+        f(x, w.float(), w)
+    with pytest.raises(ValueError, match="up_weight shape"):
+        f(x, w, w[:5])
+    with pytest.raises(ValueError, match="gate_weight shape"):
+        f(x, w[:, :7], w)
+    with pytest.raises(ValueError, match="activation"):
+        f(x, w, w, "relu")
+    with pytest.raises(ValueError, match="2 dimensions"):
+        f(x[0], w, w)
+    with pytest.raises(ValueError, match="values"):
+        f(x[:, :0], w[:, :0], w[:, :0])
+    with pytest.raises(ValueError, match="grad_h shape"):
+        L().gated_projection_backward(torch.zeros(4, 5, dtype=BF16, device=DEV), x, w, w)
