@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import token_policy as ref
-from state_space_cases import DEV, close, np64, to_dev
+from state_space_cases import DEV, close, np64, strided, to_dev
 from token_policy_cases import distill_factor, distill_inputs
 
 pytestmark = pytest.mark.gpu
