@@ -37,10 +37,10 @@ struct Work {
 };
 
 constexpr int kBlockK = 64;  // values of K in a stage: a row of 128 bytes
-constexpr int kStages = 5, kThreads = 256;
+constexpr int kStages = 5, kThreads = 384, kSumWarps = 8;
 constexpr uint32_t kTileBytes = 128 * kBlockK * 2, kStageBytes = 2 * kTileBytes;
 constexpr uint32_t kOutBytes = 32 * 128;  // 32 rows of 64 values, two of a warp that takes sums out
-constexpr size_t kSmem = kStages * kStageBytes + 4 * 2 * kOutBytes + 1024;
+constexpr size_t kSmem = kStages * kStageBytes + kSumWarps * 2 * kOutBytes + 1024;
 
 // 32 neighbouring values into half `h` of the lane's row of an output box, with
 // its swizzle: the 16-byte units of a row change places by the row's number
@@ -93,7 +93,7 @@ __device__ __forceinline__ void load_row(Words<bf16, 8> (&w)[4], const bf16 *p, 
 // one thread of the pair's first block multiplies for both.  For z and u the
 // halves are 128 columns of z and the same 128 of u, so that the epilogue
 // finds both of a value in its own tensor memory.  Warps: 0 copies, 1
-// multiplies (the first block's), 2 holds the tensor memory, 4 to 7 take the
+// multiplies (the first block's), 2 holds the tensor memory, 4 to 11 take the
 // sums out while the next tile's are made in the other half of the 512 columns.
 template <Job JOB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -117,7 +117,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&sums_full[i], 1);
-            ptx::mbar_init(&sums_empty[i], 8);  // a warp's arrival each, of both blocks
+            ptx::mbar_init(&sums_empty[i], 2 * kSumWarps);  // a warp's arrival each, of both blocks
         }
         ptx::fence_mbar_init();
     }
@@ -208,8 +208,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 4) {  // sums
         uint32_t buffer = 0, phase = 0;
-        const int part = warp % 4;
-        char *boxes = raw_aligned + kStages * kStageBytes + part * 2 * kOutBytes;
+        // a warp reaches a quarter of the tensor memory's rows; two warps share it, half of the columns each
+        const int part = warp % 4, side = (warp - 4) / 4;
+        char *boxes = raw_aligned + kStages * kStageBytes + (warp - 4) * 2 * kOutBytes;
         // the box that comes next has been read: all of the warp's, or (two take turns) all but the last
         auto free_box = [&](bool turns) {
             if (lane == 0) {
@@ -218,6 +219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
+        int turn = 0;  // of Forward's two boxes
         auto put_box = [&](int i, int64_t x, int64_t y, int64_t rows, int64_t columns, const char *box) {
             const bool some = y < rows && x < columns;
             if (k.out_mapped) {
@@ -244,7 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if constexpr (kGates) {
                 const int64_t f0 = tn * 128;
 #pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = side * 64; c < side * 64 + 64; c += 32) {
                     const int64_t n = row < rows ? k.F - f0 - c : 0;
                     uint32_t z[32], u[32];
                     Words<bf16, 8> gh[4];
@@ -266,20 +268,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                     const int h = c / 32 % 2;
-                    char *box = boxes + (JOB == Job::Forward ? c / 64 * kOutBytes : 0);
+                    char *box = boxes + (JOB == Job::Forward ? turn * kOutBytes : 0);
                     if (h == 0) free_box(JOB == Job::Forward);
                     box_row(box, lane, h, v);
                     if constexpr (JOB == Job::Gates) box_row(boxes + kOutBytes, lane, h, w);
                     if (h == 1) {
                         const int64_t x = f0 + c - 32;
                         put_box(0, x, row0, rows, k.F, box);
+                        turn ^= 1;
                         if constexpr (JOB == Job::Gates) put_box(1, x, row0, rows, k.F, boxes + kOutBytes);
                     }
                 }
             } else {
                 const int64_t d0 = tn * 256;
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 32) {
+                for (int c = side * 128; c < side * 128 + 128; c += 32) {
                     uint32_t v[32];
                     umma::tmem_load(v, at + c);
                     umma::tmem_loaded();
