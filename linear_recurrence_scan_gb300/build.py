@@ -16,7 +16,7 @@ import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")                    # the estimators' scan kernels
-CSRC_SEQUENCE = os.path.join(HERE, "csrc_sequence")  # the state-space layer
+CSRC_SEQUENCE = os.path.join(HERE, "csrc_sequence")  # the state-space layer and the token policy's other operators
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "librlscan.so")
