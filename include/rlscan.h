@@ -867,8 +867,8 @@ typedef struct rlscan_distill_args {
 /* loss [N,T] float32; normalizers [N,T,2] float32, nullable: the row's largest
  * logit m and sum exp((logit - m) / temperature), which the gradient needs.
  * Errors: RLSCAN_ERR_NULL, RLSCAN_ERR_SHAPE, RLSCAN_ERR_ARG_VALUE (K, a type or
- * the temperature out of range), RLSCAN_ERR_ARG_CONFLICT, RLSCAN_ERR_MEMORY,
- * RLSCAN_ERR_CUDA. */
+ * the temperature out of range), RLSCAN_ERR_ARG_CONFLICT, RLSCAN_ERR_MEMORY
+ * (also: logits that are not device memory), RLSCAN_ERR_CUDA. */
 rlscan_status rlscan_distill_loss(const rlscan_distill_args *args, float *loss, float *normalizers,
                                   rlscan_stream_t stream);
 

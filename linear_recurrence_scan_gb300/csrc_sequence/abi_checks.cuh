@@ -19,12 +19,20 @@ inline bool equals_any(const void *out, std::initializer_list<const void *> othe
     return false;
 }
 
-inline bool reachable(std::initializer_list<const void *> ptrs)
+// the residency of all of them together: the one that allows least
+inline Residency residency_of(std::initializer_list<const void *> ptrs)
 {
-    for (const void *p : ptrs)
-        if (p != nullptr && residency(p) == Residency::Unreachable) return false;
-    return true;
+    Residency all = Residency::Device;
+    for (const void *p : ptrs) {
+        const Residency one = p != nullptr ? residency(p) : Residency::Device;
+        if (one == Residency::Unreachable) return one;
+        if (one == Residency::Host) all = one;
+    }
+    return all;
 }
+inline bool reachable(std::initializer_list<const void *> ptrs) { return residency_of(ptrs) != Residency::Unreachable; }
+// Copies into shared memory are for device memory alone.
+inline bool on_device(std::initializer_list<const void *> ptrs) { return residency_of(ptrs) == Residency::Device; }
 
 inline bool workspace_ok(const void *ws, size_t have, size_t need)
 {

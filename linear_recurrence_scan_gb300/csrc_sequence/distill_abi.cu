@@ -29,7 +29,7 @@ rlscan_status check_distill_call(const rlscan_distill_args &a, std::initializer_
         for (auto j = outs.begin(); j != i; ++j)
             if (*j == *i) return RLSCAN_ERR_ARG_CONFLICT;
     }
-    return reachable({a.logits.data, a.teacher_logits, a.teacher_tokens, a.mask}) && reachable(outs) && reachable(more)
+    return on_device({a.logits.data}) && reachable({a.teacher_logits, a.teacher_tokens, a.mask}) && reachable(outs) && reachable(more)
                ? RLSCAN_OK
                : RLSCAN_ERR_MEMORY;
 }

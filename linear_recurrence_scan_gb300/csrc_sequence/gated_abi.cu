@@ -28,7 +28,7 @@ bool is_gated_input(const void *out, const rlscan_gated_scan_args &a)
 
 bool gated_reachable(const rlscan_gated_scan_args &a)
 {
-    return reachable({a.x.data, a.gate.data, a.input_gate.data, a.log_decay, a.initial_state, a.resets, a.lengths});
+    return reachable({a.log_decay, a.initial_state, a.resets, a.lengths});
 }
 
 // outputs that are one another or an input
@@ -55,8 +55,9 @@ RLSCAN_API rlscan_status rlscan_gated_scan(const rlscan_gated_scan_args *args, v
     if (a.N == 0 || a.D == 0) return RLSCAN_OK;
     if (!inputs_given(a) || (a.T > 0 && y == nullptr)) return RLSCAN_ERR_NULL;
     if (conflict(a, {y, final_state, checkpoints}, {})) return RLSCAN_ERR_ARG_CONFLICT;
-    if (!gated_reachable(a) || !reachable({y, final_state, checkpoints})) return RLSCAN_ERR_MEMORY;
-    return launch_gated_scan(a, y, final_state, checkpoints, cs(stream));
+    const Residency tokens = residency_of({a.x.data, a.gate.data, a.input_gate.data, y});
+    if (tokens == Residency::Unreachable || !gated_reachable(a) || !reachable({final_state, checkpoints})) return RLSCAN_ERR_MEMORY;
+    return launch_gated_scan(a, y, final_state, checkpoints, tokens == Residency::Device, cs(stream));
 }
 
 RLSCAN_API size_t rlscan_gated_scan_backward_workspace_bytes(const rlscan_gated_scan_args *args)
@@ -79,10 +80,10 @@ RLSCAN_API rlscan_status rlscan_gated_scan_backward(const rlscan_gated_scan_args
     if (conflict(a, {g.x, g.gate, g.input_gate, g.log_decay, g.initial_state}, {grad_y->data, grad_final_state, checkpoints}))
         return RLSCAN_ERR_ARG_CONFLICT;
     if (g.log_decay && !workspace_ok(ws, ws_bytes, gated_scan_backward_workspace(a))) return RLSCAN_ERR_WORKSPACE;
-    if (!gated_reachable(a) || !reachable({grad_y->data, grad_final_state, checkpoints, g.x, g.gate, g.input_gate,
-                                           g.log_decay, g.initial_state}))
+    const Residency tokens = residency_of({a.x.data, a.gate.data, a.input_gate.data, grad_y->data, g.x, g.gate, g.input_gate});
+    if (tokens == Residency::Unreachable || !gated_reachable(a) || !reachable({grad_final_state, checkpoints, g.log_decay, g.initial_state}))
         return RLSCAN_ERR_MEMORY;
-    return launch_gated_scan_backward(a, *grad_y, grad_final_state, checkpoints, g, ws, cs(stream));
+    return launch_gated_scan_backward(a, *grad_y, grad_final_state, checkpoints, g, ws, tokens == Residency::Device, cs(stream));
 }
 
 RLSCAN_API rlscan_status rlscan_gated_scan_step(const rlscan_gated_scan_args *args, float *state, int64_t P,
@@ -94,7 +95,7 @@ RLSCAN_API rlscan_status rlscan_gated_scan_step(const rlscan_gated_scan_args *ar
     if (a.N == 0 || a.D == 0) return RLSCAN_OK;
     if (!inputs_given(a) || (P > 0 && state == nullptr) || y == nullptr) return RLSCAN_ERR_NULL;
     if (conflict(a, {y, state}, {slots})) return RLSCAN_ERR_ARG_CONFLICT;
-    if (!gated_reachable(a) || !reachable({state, slots, y})) return RLSCAN_ERR_MEMORY;
+    if (!gated_reachable(a) || !reachable({a.x.data, a.gate.data, a.input_gate.data, state, slots, y})) return RLSCAN_ERR_MEMORY;
     return launch_gated_scan_step(a, state, P, slots, y, cs(stream));
 }
 

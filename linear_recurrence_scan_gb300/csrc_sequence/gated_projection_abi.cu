@@ -22,14 +22,6 @@ bool inputs_given(const rlscan_gated_projection_args &a)
     return a.D == 0 || ((a.M == 0 || a.x) && (a.F == 0 || (a.gate_weight && a.up_weight)));
 }
 
-// The copies into shared memory read device memory alone.
-bool on_device(std::initializer_list<const void *> ptrs)
-{
-    for (const void *p : ptrs)
-        if (p != nullptr && residency(p) != Residency::Device) return false;
-    return true;
-}
-
 }  // namespace
 
 extern "C" {

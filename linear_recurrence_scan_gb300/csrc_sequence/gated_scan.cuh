@@ -445,16 +445,16 @@ inline rlscan_status launch_cluster(bool overlapped, K kernel, int64_t grid, int
     return RLSCAN_OK;
 }
 
-// The kernel for arrays whose addresses and strides are `bits`: Tiles where
-// all are multiples of 16 bytes (tensor maps), Pairs where two channels are,
-// else Values.
+// The kernel for a call's arrays: Tiles where all are device memory (`tiles`)
+// and addresses and strides multiples of 16 bytes (tensor maps), Pairs where
+// they are multiples of two channels, else Values.
 enum class Access { Values, Pairs, Tiles };
 template <class T>
 inline Access gated_access(std::initializer_list<const rlscan_array3 *> in, std::initializer_list<const void *> out,
-                           std::initializer_list<const void *> floats, int64_t N, int64_t T_, int64_t D)
+                           std::initializer_list<const void *> floats, int64_t N, int64_t T_, int64_t D, bool tiles)
 {
     uint64_t bits = 0, wide = 0;
-    bool plain = T_ < 0x7fffffff - 1024 && N < 0x7fffffff;  // coordinates are 32-bit
+    bool plain = tiles && T_ > 0 && T_ < 0x7fffffff - 1024 && N < 0x7fffffff;  // coordinates are 32-bit
     for (const rlscan_array3 *a : in) {
         const int64_t row = N > 1 ? a->row_stride : 0, token = T_ > 1 ? a->token_stride : 0;
         bits |= reinterpret_cast<uintptr_t>(a->data) | static_cast<uint64_t>(row * sizeof(T)) | static_cast<uint64_t>(token * sizeof(T));

@@ -20,7 +20,8 @@ struct ForwardArgs {
 // in order, give its first state, and its tokens follow.  The coefficients are
 // made once and stay in registers, so the inputs are read once.  CLUSTER: the
 // blocks of a cluster take neighbouring steps and hand their maps round.
-// Past the last token the state is handed on
+
+// Past the last token the state is handed on.
 template <int TOK>
 __device__ __forceinline__ void pad(f2 (&keep)[TOK], f2 (&b)[TOK], int64_t t0, int64_t len)
 {
@@ -73,7 +74,8 @@ __device__ __forceinline__ void finish(const rlscan_gated_scan_args &a, const Fo
 }
 
 // Arrays of any alignment: the next step's values are loaded into registers
-// while this one's are worked on.
+// while this one's are worked on.  Measured, 3 x 1001 x 1111 float32 (13 MB a
+// tensor, one value a load): 15 us, its bytes' time 8.
 template <class T, bool VEC, bool CLUSTER>
 __global__ void __launch_bounds__(32 * kGatedWarps, sizeof(T) == 2 && VEC ? 3 : 2)
     forward_kernel(const __grid_constant__ rlscan_gated_scan_args a, const __grid_constant__ ForwardArgs o, int ranks)
@@ -157,7 +159,13 @@ __global__ void __launch_bounds__(32 * kGatedWarps, sizeof(T) == 2 && VEC ? 3 : 
 
 // Arrays that tensor maps take: two steps' inputs are on their way into shared
 // memory, so registers hold coefficients alone and a warp takes twice the
-// tokens of 16-bit values; y leaves through shared memory too.
+// tokens of 16-bit values; y leaves through shared memory too.  Three blocks an
+// SM are what 78 registers and 57 KB allow.  Measured: 8 x 2048 x 4096 bfloat16
+// 120 us (its bytes' time 79), 4 x 4096 x 4096 float32 170 us (158), 2 x 16384 x
+// 2048 bfloat16 in clusters of six 144 us (79).  Float32 is bound by its bytes;
+// bfloat16 by instructions and by the steps' chain of waits: issue slots 63%
+// busy, exponential units (three exponentials, two reciprocals and a reciprocal
+// root a value) 42%, and of 512 blocks' work 456 at once leave a second round.
 struct ForwardMaps {
     CUtensorMap x, gate, input_gate, y;
 };
@@ -317,12 +325,12 @@ __global__ void __launch_bounds__(32 * kStepWarps)
 }
 
 template <class T>
-rlscan_status forward_typed(const rlscan_gated_scan_args &a, const ForwardArgs &o, cudaStream_t s)
+rlscan_status forward_typed(const rlscan_gated_scan_args &a, const ForwardArgs &o, bool on_device, cudaStream_t s)
 {
     const int64_t chains = a.N * ceil_div(a.D, kGatedWidth);
     const int threads = 32 * kGatedWarps;
-    const Access access = gated_access<T>({&a.x, &a.gate, &a.input_gate}, {o.y}, {o.final_state, o.checkpoints}, a.N, a.T, a.D);
-    if (access == Access::Tiles && a.T > 0) {
+    const Access access = gated_access<T>({&a.x, &a.gate, &a.input_gate}, {o.y}, {o.final_state, o.checkpoints}, a.N, a.T, a.D, on_device);
+    if (access == Access::Tiles) {
         using Tile = ForwardTile<T>;
         static PerDevice alone, shared;
         if (!raise_smem(alone, tiled_forward_kernel<T, false>, Tile::SMEM) || !raise_smem(shared, tiled_forward_kernel<T, true>, Tile::SMEM))
@@ -349,7 +357,7 @@ rlscan_status forward_typed(const rlscan_gated_scan_args &a, const ForwardArgs &
 template <class T>
 rlscan_status step_typed(const rlscan_gated_scan_args &a, const StepArgs &q, cudaStream_t s)
 {
-    const bool pairs = gated_access<T>({&a.x, &a.gate, &a.input_gate}, {q.y}, {q.state}, a.N, 1, a.D) != Access::Values;
+    const bool pairs = gated_access<T>({&a.x, &a.gate, &a.input_gate}, {q.y}, {q.state}, a.N, 1, a.D, false) != Access::Values;
     const int64_t grid = ceil_div(a.N * ceil_div(a.D, kGatedWidth), kStepWarps);
     return pairs ? launch_overlapped(step_kernel<T, true>, grid, 32 * kStepWarps, 0, s, a, q)
                  : launch_overlapped(step_kernel<T, false>, grid, 32 * kStepWarps, 0, s, a, q);
@@ -358,10 +366,10 @@ rlscan_status step_typed(const rlscan_gated_scan_args &a, const StepArgs &q, cud
 }  // namespace
 
 rlscan_status launch_gated_scan(const rlscan_gated_scan_args &a, void *y, float *final_state, float *checkpoints,
-                                cudaStream_t s)
+                                bool on_device, cudaStream_t s)
 {
     const ForwardArgs o{y, final_state, checkpoints};
-    return a.dtype == RLSCAN_BF16 ? forward_typed<bf16>(a, o, s) : forward_typed<float>(a, o, s);
+    return a.dtype == RLSCAN_BF16 ? forward_typed<bf16>(a, o, on_device, s) : forward_typed<float>(a, o, on_device, s);
 }
 
 rlscan_status launch_gated_scan_step(const rlscan_gated_scan_args &a, float *state, int64_t P, const int32_t *slots,

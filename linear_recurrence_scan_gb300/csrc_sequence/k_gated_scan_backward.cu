@@ -26,6 +26,7 @@ constexpr int kBackTile = RLSCAN_GATED_SCAN_CHECKPOINT;  // tokens of a step of 
 // them (both have the same factor, the product of the decays).  The states
 // start again from the checkpoint in front of the step, so only the messages
 // are handed between steps.
+
 // What a token adds: dx, the gates' gradients, log_decay's share; and the
 // message to the token in front of it.
 struct TokenGrads {
@@ -378,13 +379,13 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
 }
 
 template <class T>
-rlscan_status backward_typed(const rlscan_gated_scan_args &a, const BackwardArgs &o, int64_t &parts, cudaStream_t s)
+rlscan_status backward_typed(const rlscan_gated_scan_args &a, const BackwardArgs &o, int64_t &parts, bool on_device, cudaStream_t s)
 {
     const int64_t chains = a.N * ceil_div(a.D, kGatedWidth);
     const int threads = 32 * kGatedWarps;
     const Access access = gated_access<T>({&a.x, &a.gate, &a.input_gate, &o.grad_y}, {o.g.x, o.g.gate, o.g.input_gate},
-                                          {o.g.initial_state, o.parts, o.checkpoints}, a.N, a.T, a.D);
-    if (access == Access::Tiles && a.T > 0) {
+                                          {o.g.initial_state, o.parts, o.checkpoints}, a.N, a.T, a.D, on_device);
+    if (access == Access::Tiles) {
         using Tile = BackwardTile<T>;
         static PerDevice alone, shared;
         if (!raise_smem(alone, tiled_backward_kernel<T, false>, Tile::SMEM) || !raise_smem(shared, tiled_backward_kernel<T, true>, Tile::SMEM))
@@ -424,13 +425,14 @@ size_t gated_scan_backward_workspace(const rlscan_gated_scan_args &a)
 
 rlscan_status launch_gated_scan_backward(const rlscan_gated_scan_args &a, const rlscan_array3 &grad_y,
                                          const float *grad_final_state, const float *checkpoints,
-                                         const rlscan_gated_scan_grads &g, void *ws, cudaStream_t s)
+                                         const rlscan_gated_scan_grads &g, void *ws, bool on_device, cudaStream_t s)
 {
     float *shares = g.log_decay != nullptr ? static_cast<float *>(ws) : nullptr;
     int64_t parts = 0;
     if (a.N > 0) {
         const BackwardArgs o{grad_y, grad_final_state, checkpoints, g, shares};
-        const rlscan_status st = a.dtype == RLSCAN_BF16 ? backward_typed<bf16>(a, o, parts, s) : backward_typed<float>(a, o, parts, s);
+        const rlscan_status st = a.dtype == RLSCAN_BF16 ? backward_typed<bf16>(a, o, parts, on_device, s)
+                                                        : backward_typed<float>(a, o, parts, on_device, s);
         if (st != RLSCAN_OK) return st;
     }
     if (g.log_decay == nullptr) return RLSCAN_OK;

@@ -561,13 +561,14 @@ struct NormGradArgs {
 rlscan_status launch_add_rms_norm_backward(const NormGradArgs &a, bool bf16_io, bool bf16_h, void *ws, cudaStream_t s);
 size_t add_rms_norm_backward_workspace(int64_t M, int64_t D);
 
+// (`on_device`: whether all [N,T,D] arrays are device memory, which bulk copies are for)
 rlscan_status launch_gated_scan(const rlscan_gated_scan_args &a, void *y, float *final_state, float *checkpoints,
-                                cudaStream_t s);
+                                bool on_device, cudaStream_t s);
 rlscan_status launch_gated_scan_step(const rlscan_gated_scan_args &a, float *state, int64_t P, const int32_t *slots,
                                      void *y, cudaStream_t s);
 rlscan_status launch_gated_scan_backward(const rlscan_gated_scan_args &a, const rlscan_array3 &grad_y,
                                          const float *grad_final_state, const float *checkpoints,
-                                         const rlscan_gated_scan_grads &g, void *ws, cudaStream_t s);
+                                         const rlscan_gated_scan_grads &g, void *ws, bool on_device, cudaStream_t s);
 size_t gated_scan_backward_workspace(const rlscan_gated_scan_args &a);
 rlscan_status gated_scan_status(cudaStream_t s);           // whether a wait ran out
 rlscan_status gated_scan_backward_status(cudaStream_t s);

@@ -275,3 +275,18 @@ def test_refusals():
     with pytest.raises(TypeError, match="grad_loss"):
         L().distill_loss_and_grad(None, z, th, tok)
     assert torch.equal(f(z, th, tok, 1), f(z, th, tok, 1.0))
+
+
+def test_logits_on_the_host_are_refused():
+    """Rows of logits come by bulk copies, which are for device memory: others end with an error in front of any launch."""
+    from linear_recurrence_scan_gb300 import _native, token_policy as tp
+    z, th = torch.zeros(2, 3, 16).pin_memory(), torch.zeros(2, 3, 4, device=DEV)
+    tok, loss, w = torch.zeros(2, 3, 4, dtype=torch.long, device=DEV), torch.full((2, 3), 7.0, device=DEV), torch.ones(2, 3, device=DEV)
+    norm, grad = torch.zeros(2, 3, 2, device=DEV), torch.zeros(2, 3, 16, device=DEV)
+    args = tp._DISTILL_ARGS.pack(2, 3, 16, 4, 0, 0, 8, z.data_ptr(), 48, 16, th.data_ptr(), tok.data_ptr(), 0, 1.0)
+    lib, memory = _native.lib(), 10
+    assert lib.rlscan_distill_loss(args, loss.data_ptr(), None, None) == memory
+    assert lib.rlscan_distill_loss_backward(args, w.data_ptr(), norm.data_ptr(), grad.data_ptr(), None) == memory
+    assert lib.rlscan_distill_loss_and_grad(args, w.data_ptr(), loss.data_ptr(), norm.data_ptr(), grad.data_ptr(), None) == memory
+    torch.cuda.synchronize()
+    assert (loss == 7).all()

@@ -370,3 +370,24 @@ def test_refusals():
         s(torch.zeros(2, 8, dtype=BF16, device=DEV), one, one, one, d)
     with pytest.raises(ValueError, match="state"):
         s(torch.zeros(2, 1, 8, device=DEV), one, one, one, d)
+
+
+@pytest.mark.parametrize("which", ["x", "y", "all"])
+def test_page_locked_memory(which):
+    """Page-locked host arrays, which bulk copies are not for, are read and written in place."""
+    from linear_recurrence_scan_gb300 import _native, token_policy as tp
+    N, T, D = 2, 100, 64
+    rng = np.random.default_rng(7)
+    x, gate, ig = (torch.from_numpy(rng.standard_normal((N, T, D)).astype(np.float32)) for _ in range(3))
+    ld = torch.from_numpy(-rng.uniform(0.1, 2, D).astype(np.float32))
+    want = L().gated_scan(x.to(DEV), gate.to(DEV), ig.to(DEV), ld.to(DEV))[0]
+    at = {k: v.pin_memory() if which in (k, "all") else v.to(DEV)
+          for k, v in dict(x=x, gate=gate, ig=ig, ld=ld, y=torch.empty(N, T, D)).items()}
+    args = tp._GATED_ARGS.pack(N, T, D, 0, *(v for k in ("x", "gate", "ig") for v in (at[k].data_ptr(), T * D, D)),
+                               at["ld"].data_ptr(), 0, 0, 0)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert _native.lib().rlscan_gated_scan(args, at["y"].data_ptr(), None, None, stream) == 0
+    torch.cuda.synchronize()
+    # the same sums in another order: T products and sums of terms below 5 (|x| < 5), each rounded to 2^-24
+    torch.testing.assert_close(at["y"].cpu(), want.cpu(), rtol=0, atol=5 * 3 * T * 2 ** -24)
+    L().workspace_status()
