@@ -15,6 +15,12 @@ struct DistillOut {
     void *grad;                // [N,T,V]
 };
 
+enum class Part { Loss, Grad, Both };
+
+// Rows of at most kShortUnits units of 16 bytes
+constexpr int64_t kShortUnits = 256;
+rlscan_status launch_distill_short(const rlscan_distill_args &a, Part part, const DistillOut &o, cudaStream_t s);
+
 rlscan_status launch_distill(const rlscan_distill_args &a, const DistillOut &o, cudaStream_t s);
 rlscan_status launch_distill_backward(const rlscan_distill_args &a, const DistillOut &o, cudaStream_t s);
 // Loss and gradient; false: the rows do not fit on chip (the two calls above do the same).

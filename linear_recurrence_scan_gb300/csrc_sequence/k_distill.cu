@@ -4,6 +4,7 @@
 #include <cfloat>
 
 #include "distill.cuh"
+#include "distill_rows.cuh"
 #include "gated_scan.cuh"
 
 namespace rlscan {
@@ -11,102 +12,6 @@ namespace seq {
 namespace {
 
 __device__ unsigned int g_timed_out;  // a wait ran out on this device
-
-enum class Part { Loss, Grad, Both };
-
-// 16 bytes of a row of logits
-template <class T>
-struct Unit {
-    static constexpr int PER = 16 / static_cast<int>(sizeof(T)), PAIRS = PER / 2;
-    uint4 v;
-    __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-    __device__ __forceinline__ f2 get(int j) const
-    {
-        if constexpr (sizeof(T) == 2) return pair(__uint_as_float(word(j) << 16), __uint_as_float(word(j) & 0xffff0000u));
-        return pair(__uint_as_float(word(2 * j)), __uint_as_float(word(2 * j + 1)));
-    }
-    __device__ __forceinline__ float value(int i) const
-    {
-        const float2 h = halves(get(i / 2));
-        return i % 2 == 0 ? h.x : h.y;
-    }
-    __device__ __forceinline__ float max() const
-    {
-        if constexpr (sizeof(T) == 2) {
-            auto as2 = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
-            const __nv_bfloat162 m = __hmax2(__hmax2(as2(v.x), as2(v.y)), __hmax2(as2(v.z), as2(v.w)));
-            return fmaxf(__low2float(m), __high2float(m));
-        } else {
-            return fmaxf(fmaxf(value(0), value(1)), fmaxf(value(2), value(3)));
-        }
-    }
-};
-
-// A row of V values: `units` whole units of 16 bytes of memory from `p + head`
-// on, and the values in front of and behind them (`head` and `tail`, at most
-// PER - 1 each), which are taken one by one.
-template <class T>
-struct Row {
-    const T *p;
-    int V, head, units, tail;
-    __device__ __forceinline__ Row(const T *row, int64_t n) : p(row), V(static_cast<int>(n))
-    {
-        constexpr int PER = Unit<T>::PER;
-        head = (PER - static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T))) % PER;
-        head = head < V ? head : V;
-        units = (V - head) / PER;
-        tail = V - head - units * PER;
-    }
-    __device__ __forceinline__ int64_t first(int u) const { return head + static_cast<int64_t>(u) * Unit<T>::PER; }
-    __device__ __forceinline__ Unit<T> load(int u) const
-    {
-        Unit<T> r;
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(r.v.x), "=r"(r.v.y), "=r"(r.v.z), "=r"(r.v.w)
-                     : "l"(p + first(u)));
-        return r;
-    }
-    // the t-th value outside the units: its place, or -1
-    __device__ __forceinline__ int edge(int t) const { return t < head ? t : t < head + tail ? V - tail + (t - head) : -1; }
-};
-
-struct Stats {
-    float m, s;  // the largest logit and sum exp((z - m) / tau)
-};
-
-__device__ __forceinline__ float warp_max(float v)
-{
-#pragma unroll
-    for (int i = 16; i > 0; i /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, i));
-    return v;
-}
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int i = 16; i > 0; i /= 2) v += __shfl_xor_sync(0xffffffffu, v, i);
-    return v;
-}
-// exp((z - m) / tau) of a pair, for a logit z and its row's largest m: one
-// multiply-add in front of the exponential, z c - m c with c = log2 e / tau.
-// m c is rounded, by the same `rest` for every logit, which `exact` takes back
-// from a sum or a factor.  Where m c is too large for that (|m| of the size of
-// a type's lowest value, as masks have it) values are taken one by one, the
-// difference z - m first.
-struct Shift {
-    f2 c, mc;
-    float rest;
-    bool wide;
-    __device__ __forceinline__ Shift(float m, float c1)
-    {
-        const float product = m * c1;
-        c = both(c1);
-        mc = both(-product);
-        wide = !(fabsf(product) < 1e30f);
-        rest = wide ? 0.f : fmaf(m, c1, -product);
-    }
-    __device__ __forceinline__ f2 exp(f2 z) const { return exp2_fast(fma2(z, c, mc)); }
-    __device__ __forceinline__ float exact() const { return exp2_fast(-rest); }
-};
 
 // The maxima and sums of a row's warps, of all the blocks that share it.  Two
 // buffers take turns: who has all of a row's knows that all have read those of
@@ -129,7 +34,7 @@ struct Head {
 };
 
 constexpr int kStages = 2;
-constexpr int kStageUnits[] = {256, 768, 1536, 3000};  // of 32, 64, 128 and 256 consumers: 4, 12, 24 and 47 KB
+constexpr int kStageUnits[] = {768, 1600, 3000};  // of 64, 128 and 256 consumers: 12, 25 and 47 KB
 constexpr int kWideUnits = 6400;                       // one block an SM: 100 KB
 constexpr int kMostConsumers = 256;
 
@@ -150,13 +55,15 @@ __device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, uint32_
 // longer rows in several parts.  The maximum starts at the lowest finite
 // number, not at -infinity, so that rows and parts of rows without a finite
 // value need no case of their own (their sum is 0).
-// Bound by a row's chain of steps (sums, meeting, gradient), of which an SM has
-// two to fourteen side by side, and by instructions.  Measured, loss and
-// gradient of 4 x 1023 x 50257: blocks that held one row in registers and went
-// with it 197 us, these 165 us; with a row's gradient behind the next row's
-// sums, which takes a third stage and so shorter slices, 187 us.
+// The loss of long rows is bound by its bytes (8 x 1024 x 131072 bfloat16 302
+// us, 7.1 TB/s); loss and gradient by a row's chain of steps (sums, meeting,
+// gradient), of which an SM has two to eight side by side, and by
+// instructions: 4 x 1023 x 50257 134 us, its bytes' time 106 (blocks that held
+// one row in registers and went with it 197 us; a row's gradient behind the
+// next row's sums, which takes a third stage, 187 us against 169 then), 16 x
+// 2048 x 6000 176 us, its bytes' time 118.
 template <class T, int CONSUMERS, Part PART, bool CLUSTER>
-__global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 14 : CONSUMERS == 64 ? 8 : CONSUMERS == 128 ? 4 : 2)
+__global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 64 ? 8 : CONSUMERS == 128 ? 4 : 2)
     distill_kernel(const __grid_constant__ rlscan_distill_args a, const __grid_constant__ DistillOut o, int ranks, int stage_units)
 {
     constexpr int WARPS = CONSUMERS / 32, PER = Unit<T>::PER, ROUND = 4;
@@ -208,26 +115,15 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 14 : CONSUME
         // last part: loaded behind that part's copy, one after the other, they
         // held up the next row's first (8 x 1024 x 131072: 350 us, so 325).
         // Shorter rows lose by it: theirs are held up in front of the copy.
-        constexpr int AHEAD = PART == Part::Loss && CONSUMERS == kMostConsumers ? 2 : 0;
+        constexpr int AHEAD = PART == Part::Loss && CONSUMERS == 128 ? 2 : 0;
         int32_t next_token[AHEAD + 1];
         float next_x[AHEAD + 1], next_z[AHEAD + 1];
-        auto token_at = [&](int64_t row, int k) -> int32_t {
-            const int64_t i = row * K + k;
-            const int64_t id = a.token_bytes == 8 ? static_cast<const int64_t *>(a.teacher_tokens)[i]
-                                                  : static_cast<const int32_t *>(a.teacher_tokens)[i];
-            return id >= 0 && id < a.V ? static_cast<int32_t>(id) : -1;
-        };
-        auto logit_at = [&](int64_t row, int k) {
-            const int64_t i = row * K + k;
-            return a.teacher_dtype == RLSCAN_BF16 ? to_f(static_cast<const bf16 *>(a.teacher_logits)[i])
-                                                  : static_cast<const float *>(a.teacher_logits)[i];
-        };
         auto look = [&](const Row<T> &in, int64_t row) {
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 const int k = 32 * i + lane;
-                next_token[i] = k < K ? token_at(row, k) : -1;
-                next_x[i] = k < K ? logit_at(row, k) : 0.f;
+                next_token[i] = k < K ? token_at(a, row, k) : -1;
+                next_x[i] = k < K ? logit_at(a, row, k) : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) next_z[i] = next_token[i] >= 0 ? to_f(in.p[next_token[i]]) : 0.f;
@@ -235,39 +131,17 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 14 : CONSUME
         // The head of a row: the teacher's tokens (-1: none), q = softmax of its
         // logits over them, the row's logits there.
         auto teach = [&](Head &h, float *q_of, const Row<T> &in, int64_t row, bool looked) {
-            float *z_of = q_of + padded;
-            int32_t *token_of = reinterpret_cast<int32_t *>(q_of + 2 * padded);
-            if (lane < padded - K) token_of[K + lane] = -1;
+            if (lane < padded - K) reinterpret_cast<int32_t *>(q_of + 2 * padded)[K + lane] = -1;
             if (rank == 0 && in.edge(lane) >= 0) h.edge[lane] = to_f(in.p[in.edge(lane)]);
-            float largest = -INFINITY, sum = 0.f, entropy = 0.f;
-            auto place = [&](int k, int32_t token, float x, float z) {
-                token_of[k] = token;
-                q_of[k] = token >= 0 ? x : -INFINITY;
-                z_of[k] = z;
-                if (token >= 0) largest = x > largest || x != x ? x : largest;  // a NaN stays
-            };
+            Teacher of(q_of, padded);
             if (looked) {
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i)
-                    if (32 * i + lane < K) place(32 * i + lane, next_token[i], next_x[i], next_z[i]);
+                    if (32 * i + lane < K) of.place(32 * i + lane, next_token[i], next_x[i], next_z[i]);
             }
-            for (int k = (looked ? 32 * AHEAD : 0) + lane; k < K; k += 32) {
-                const int32_t token = token_at(row, k);
-                place(k, token, logit_at(row, k), token >= 0 ? to_f(in.p[token]) : 0.f);
-            }
-            largest = __any_sync(0xffffffffu, largest != largest) ? NAN : warp_max(largest);
-            if (largest != -INFINITY) {
-                for (int k = lane; k < K; k += 32) sum += exp2_fast((q_of[k] - largest) * c);
-                sum = warp_sum(sum);
-                const float log_sum = logf(sum);
-                for (int k = lane; k < K; k += 32) {
-                    const float lq = (q_of[k] - largest) * rtau - log_sum, q = exp2_fast((q_of[k] - largest) * c) / sum;
-                    if (!(q == 0.f)) entropy += q * lq;
-                    q_of[k] = q;
-                }
-                entropy = warp_sum(entropy);
-            }
-            if (lane == 0) h.taught = largest != -INFINITY, h.entropy = entropy;
+            of.template gather<2>(a, in, row, looked ? 32 * AHEAD : 0, K, lane);
+            const bool taught = of.softmax(K, lane, c, rtau);
+            if (lane == 0) h.taught = taught, h.entropy = of.entropy;
         };
         uint32_t mask = a.mask != nullptr && row0 < rows ? load_byte(a.mask + row0) : 1u;
         for (int64_t row = row0; row < rows; row += stride) {
@@ -311,10 +185,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 14 : CONSUME
         bring();
     } else {  // ---- sums and gradients
         const int t = threadIdx.x;
-        auto sync = [] {
-            if constexpr (CONSUMERS == 32) __syncwarp();
-            else ptx::named_barrier(1, CONSUMERS);
-        };
+        auto sync = [] { ptx::named_barrier(1, CONSUMERS); };
         auto release = [&] {
             __syncwarp();
             if (lane == 0 && !has_given_up(&gave_up)) ptx::mbar_arrive(&empty[stage]);
@@ -418,21 +289,19 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 14 : CONSUME
                                          : "memory");
                         }
                         wait(ptx::smem_u32(&meeting.bar[p]), static_cast<uint32_t>(turn >> 1) & 1u, &gave_up);
-                    } else if constexpr (WARPS > 1) {
+                    } else {
                         if (lane == 0) meeting.of_warp[p][t / 32] = make_float2(st.m, st.s);
                         sync();
                     }
-                    if constexpr (WARPS > 1) {
-                        const int all = CLUSTER ? ranks * WARPS : WARPS;
-                        Stats some{-FLT_MAX, 0.f};
-                        for (int i = lane; i < all; i += 32) {
-                            const float2 one = meeting.of_warp[p][i];
-                            const float top = fmaxf(some.m, one.x);
-                            some = {top, some.s * exp2_fast((some.m - top) * c) + one.y * exp2_fast((one.x - top) * c)};
-                        }
-                        const float top = warp_max(some.m);
-                        st = {top, warp_sum(some.s * exp2_fast((some.m - top) * c))};
+                    const int all = CLUSTER ? ranks * WARPS : WARPS;
+                    Stats some{-FLT_MAX, 0.f};
+                    for (int i = lane; i < all; i += 32) {
+                        const float2 one = meeting.of_warp[p][i];
+                        const float top = fmaxf(some.m, one.x);
+                        some = {top, some.s * exp2_fast((some.m - top) * c) + one.y * exp2_fast((one.x - top) * c)};
                     }
+                    const float top = warp_max(some.m);
+                    st = {top, warp_sum(some.s * exp2_fast((some.m - top) * c))};
                     ++turn;
                 }
                 if constexpr (PART != Part::Loss) {
@@ -468,20 +337,9 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 14 : CONSUME
                                 const bool outside = token < in.head || token >= in.V - in.tail;
                                 const int at = (token - in.head) / PER;
                                 if (token < 0 || token >= in.V || (outside ? rank != 0 : at < u0 || at >= end)) continue;
-                                float q = 0.f;
-                                bool first = true;  // a token that comes twice counts twice, and is written once
-                                for (int j = 0; j < K; j += 4) {
-                                    const int4 four = *reinterpret_cast<const int4 *>(token_of + j);
-                                    const int same = (four.x == token ? 1 : 0) | (four.y == token ? 2 : 0) | (four.z == token ? 4 : 0) |
-                                                     (four.w == token ? 8 : 0);
-                                    if (same != 0)
-                                        for (int i = 0; i < 4; ++i)
-                                            if ((same >> i & 1) != 0) {
-                                                first = first && j + i >= k;
-                                                q += q_of[j + i];
-                                            }
-                                }
-                                if (first) out[token] = from_f<T>(exp2_fast((z_of[k] - st.m) * c) * scale - q * h.weight);
+                                float q;
+                                if (taught_at(q_of, token_of, k, padded, q))
+                                    out[token] = from_f<T>(exp2_fast((z_of[k] - st.m) * c) * scale - q * h.weight);
                             }
                         } else {
                             clear();  // or, where there is nothing to learn from, zeros
@@ -489,13 +347,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 14 : CONSUME
                     }
                 }
                 if (PART != Part::Grad && last && rank == 0 && t < 32) {
-                    float cross = 0.f;
-                    if (h.taught)
-                        for (int k = lane; k < K; k += 32) {
-                            const float q = q_of[k];
-                            if (!(q == 0.f)) cross += q * ((z_of[k] - st.m) * rtau);
-                        }
-                    cross = warp_sum(cross);
+                    const float cross = h.taught ? cross_of(q_of, z_of, K, lane, st.m, rtau) : 0.f;
                     if (lane == 0) {
                         o.loss[row] = h.taught ? h.entropy - cross + logf(st.s) : 0.f;
                         if (o.normalizers != nullptr) reinterpret_cast<float2 *>(o.normalizers)[row] = make_float2(st.m, st.s);
@@ -514,7 +366,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 32 ? 14 : CONSUME
 // Threads that take a row's sums and the bytes of a stage: larger ones for
 // longer rows, so that what a row costs beside its bytes (the reduction, the
 // hand-over) stays in proportion, as many blocks an SM as fit beside each
-// other.  Both parts of a stage's pair hold a row, or a block's slice of one.
+// other.
 struct Plan {
     int consumers, stage_units, ranks;
     bool cluster;
@@ -522,15 +374,21 @@ struct Plan {
 // Units of 16 bytes that a row may have
 int64_t most_units(const rlscan_distill_args &a) { return a.V / (a.dtype == RLSCAN_BF16 ? 8 : 4); }
 
-// Part::Both keeps a block's slice of a row in one stage; the others split rows
-// while there are too few of them to give every SM two blocks.
+// Part::Both keeps a block's slice of a row in one stage: of 25 KB where up to
+// eight blocks hold a row so (4 x 1023 x 50257 bfloat16 134 us; of 47 KB, two
+// blocks an SM instead of four, 169), of 47 KB and then of 100 KB for longer
+// ones.  The others take longer rows in several parts, the loss in the smaller
+// ones (8 x 1024 x 131072 302 us, in the larger 318), the gradient, which has no
+// sums to wait for, in the larger (4 x 1023 x 50257 121 us, in ones of 34 KB
+// 128).  Rows are split further while there are too few of them to give every
+// SM two blocks (four, where as many fit: 1 x 64 x 50257 both 19 us, so 14).
 Plan plan(const rlscan_distill_args &a, Part part)
 {
     const int64_t units = most_units(a), rows = a.N * a.T, sms = sm_count() > 0 ? sm_count() : 152;
-    if (units <= kStageUnits[0]) return {32, kStageUnits[0], 1, false};
-    if (units <= kStageUnits[1]) return {64, kStageUnits[1], 1, false};
-    if (units <= kStageUnits[2]) return {128, kStageUnits[2], 1, false};
-    Plan p{kMostConsumers, kStageUnits[3], 1, false};
+    if (units <= kStageUnits[0]) return {64, kStageUnits[0], 1, false};
+    if (units <= kStageUnits[1]) return {128, kStageUnits[1], 1, false};
+    Plan p{kMostConsumers, kStageUnits[2], 1, false};
+    if (part == Part::Loss || (part == Part::Both && units <= kGatedCluster * kStageUnits[1])) p = {128, kStageUnits[1], 1, false};
     if (part == Part::Both) {
         if (units > int64_t{kGatedCluster} * p.stage_units) p.stage_units = kWideUnits;
         p.ranks = static_cast<int>(ceil_div(units, p.stage_units));
@@ -578,15 +436,19 @@ rlscan_status launch_stream(const rlscan_distill_args &a, const DistillOut &o, P
 template <class T, Part PART>
 rlscan_status run(const rlscan_distill_args &a, const DistillOut &o, cudaStream_t s)
 {
+    if (most_units(a) <= kShortUnits) return launch_distill_short(a, PART, o, s);
     const Plan p = plan(a, PART);
     switch (p.consumers) {
-    case 32: return launch_stream<T, 32, PART, false>(a, o, p, s);
     case 64: return launch_stream<T, 64, PART, false>(a, o, p, s);
-    case 128: return launch_stream<T, 128, PART, false>(a, o, p, s);
-    default:
+    case 128:
         if constexpr (PART != Part::Grad)
+            if (p.cluster) return launch_stream<T, 128, PART, true>(a, o, p, s);
+        return launch_stream<T, 128, PART, false>(a, o, p, s);
+    default:  // (the loss takes long rows with 128)
+        if constexpr (PART == Part::Both)
             if (p.cluster) return launch_stream<T, kMostConsumers, PART, true>(a, o, p, s);
-        return launch_stream<T, kMostConsumers, PART, false>(a, o, p, s);
+        if constexpr (PART != Part::Loss) return launch_stream<T, kMostConsumers, PART, false>(a, o, p, s);
+        return RLSCAN_ERR_SHAPE;
     }
 }
 

@@ -290,3 +290,16 @@ def test_logits_on_the_host_are_refused():
     assert lib.rlscan_distill_loss_and_grad(args, w.data_ptr(), loss.data_ptr(), norm.data_ptr(), grad.data_ptr(), None) == memory
     torch.cuda.synchronize()
     assert (loss == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [7, 8, 127, 135, 255, 256, 263, 264, 511, 519, 1023, 1031, 1032, 2047, 2055, 2056, 3079, 6151, 12807])
+def test_rows_at_the_ends_of_each_kind(V, dtype):
+    """One value less and more than lanes, warps and stages hold, rows that start anywhere in 16 bytes; the teacher has
+    the first and the last token, the last one twice."""
+    K = min(V, 40)
+    logits, teacher, tokens, mask, grad, rng = distill_inputs(3, 5, V, K, dtype, V)
+    tokens[..., 0], tokens[..., -1] = 0, V - 1
+    if K > 2:
+        tokens[:, ::2, K // 2] = V - 1
+    check(logits, teacher, tokens, mask, grad)
