@@ -345,7 +345,7 @@ __device__ __forceinline__ f2 in_front(C &c, E *ex, int64_t turn, int w, int lan
         }
         ex->receive(p, static_cast<uint32_t>(turn >> 1) & 1u, gave_up);
         const f2 first = carry;
-#pragma unroll 1
+#pragma unroll 2
         for (int i = 0; i < ranks; ++i) {
             const int q = FORWARD ? i : ranks - 1 - i;
             if (q == rank) from = carry;

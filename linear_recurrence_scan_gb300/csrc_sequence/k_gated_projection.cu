@@ -129,7 +129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     umma::fence_after();
     const uint32_t tmem = tmem_at;
     ptx::pdl_wait_prerequisites();
-    const int64_t items = k.tiles_m * k.tiles_n * k.parts, pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int64_t items = k.tiles_m * k.tiles_n * k.parts, first_item = blockIdx.x / 2, pairs = gridDim.x / 2;
     // Tiles in bands of eight rows of tiles, column after column: the pairs at
     // work share rows of A and columns of B in L2.
     auto place = [&](int64_t tile, int64_t &m, int64_t &n) {
@@ -149,7 +149,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t stage = 0, phase = 1;  // the first wait on an empty stage passes
         int64_t issued = 0;
         const int64_t half = kGates ? 0 : JOB == Job::Input ? k.steps / 2 : k.tiles_m / 2;
-        for (int64_t item = pair; item < items && !has_given_up(&gave_up); item += pairs) {
+        for (int64_t item = first_item; item < items && !has_given_up(&gave_up); item += pairs) {
             int64_t tm, tn;
             place(item / k.parts, tm, tn);
             for (int64_t s = first_step(item), e = last_step(item); s < e; ++s) {
@@ -184,7 +184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 1 && lane == 0 && rank == 0) {  // products
         constexpr uint32_t kInstruction = umma::instruction(kAMn, kBMn, 256, 256);
         uint32_t stage = 0, phase = 0, buffer = 0, buffer_phase = 1;
-        for (int64_t item = pair; item < items; item += pairs) {
+        for (int64_t item = first_item; item < items; item += pairs) {
             if (!wait(ptx::smem_u32(&sums_empty[buffer]), buffer_phase, &gave_up)) break;
             umma::fence_after();
             bool fine = true;
@@ -232,7 +232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (some) copy_box(k.out[i] + y * k.out_stride + x, k.out_stride, box, lane, rows - y, columns - x);
             }
         };
-        for (int64_t item = pair; item < items; item += pairs) {
+        for (int64_t item = first_item; item < items; item += pairs) {
             int64_t tm, tn;
             place(item / k.parts, tm, tn);
             const int64_t half = k.tiles_m / 2;
@@ -255,18 +255,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     umma::tmem_load(u, at + 128 + c);
                     umma::tmem_loaded();
                     float v[32], w[32];
+                    auto outputs = [&](auto act) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float uu = __uint_as_float(u[i]);
-                        const float2 as = act_slope(__uint_as_float(z[i]), k.act);
-                        if constexpr (JOB == Job::Forward) {
-                            v[i] = as.x * uu;
-                        } else {
-                            const float g = gh[i / 8][i % 8];
-                            v[i] = g * uu * as.y;
-                            w[i] = g * as.x;
+                        for (int i = 0; i < 32; i += 2) {
+                            const f2 uu = pair(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+                            const Activated of = act(pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1])));
+                            if constexpr (JOB == Job::Forward) {
+                                const float2 h = halves(mul2(of.value, uu));
+                                v[i] = h.x, v[i + 1] = h.y;
+                            } else {
+                                const f2 g = pair(gh[i / 8][i % 8], gh[i / 8][i % 8 + 1]);
+                                const float2 gz = halves(mul2(mul2(g, uu), of.slope)), gu = halves(mul2(g, of.value));
+                                v[i] = gz.x, v[i + 1] = gz.y, w[i] = gu.x, w[i + 1] = gu.y;
+                            }
                         }
-                    }
+                    };
+                    if (k.act == RLSCAN_SILU) outputs([](f2 x) { return silu(x); });
+                    else outputs([](f2 x) { return gelu(x); });
                     const int h = c / 32 % 2;
                     char *box = boxes + (JOB == Job::Forward ? turn * kOutBytes : 0);
                     if (h == 0) free_box(JOB == Job::Forward);

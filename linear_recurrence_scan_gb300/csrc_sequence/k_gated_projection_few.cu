@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 4 ? 2 : 3)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) zz += part[w][0][n][i][l], uu += part[w][1][n][i][l];
         const int64_t f = f0 + 8 * (i / 2) + l / 4, m = 8 * n + 2 * (l % 4) + i % 2;
-        if (f < a.F && m < a.M) h[m * a.F + f] = from_f<bf16>(act_slope(zz, static_cast<int>(a.activation)).x * uu);
+        if (f < a.F && m < a.M) h[m * a.F + f] = from_f<bf16>(halves((a.activation == RLSCAN_SILU ? silu(both(zz)) : gelu(both(zz))).value).x * uu);
     }
 }
 
