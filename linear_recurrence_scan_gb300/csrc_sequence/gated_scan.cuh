@@ -382,9 +382,9 @@ __host__ __device__ inline int64_t gated_marks(int64_t T) { return (T + RLSCAN_G
 // Blocks of a cluster that share a row: as many as make the fewest steps one
 // after the other, counting the rounds in which clusters of that size become
 // resident.  A row split over blocks costs each step an exchange, taken as
-// three quarters of a step (measured: 16 x 1024 x 2048, 512 chains, alone 60
-// us, in fours 69; 2 x 16384 x 2048, 64 chains, alone 354, in fours 195, in
-// sixes 144, in eights, which no longer fit at once, 184).
+// three quarters of a step (measured: 16 x 1024 x 2048, 512 chains, alone 66
+// us, in fours 76; 2 x 16384 x 2048, 64 chains, alone 349, in fours 169, in
+// sixes 154, in eights, which no longer fit at once, 185).
 template <class T, int KIND, class K>
 inline int gated_cluster(K kernel, int64_t chains, int64_t tokens, int tile, size_t smem, int most = kGatedCluster)
 {
@@ -417,9 +417,8 @@ inline int gated_cluster(K kernel, int64_t chains, int64_t tokens, int tile, siz
 
 // `overlapped`: whether the grid may start while the kernel before it still
 // runs.  A grid of several blocks an SM would then go to the SMs that are done
-// first, several at once, and end unevenly (4 x 4096 x 4096 float32 forward
-// 189 us, started behind 169; loss and gradient of 4 x 1024 x 50304 logits 279
-// and 192), so only grids of a block an SM do.
+// first, several at once, and end unevenly (4 x 4096 x 4096 float32 forward 194
+// us back to back, started behind 170), so only grids of a block an SM do.
 template <class K, class... Args>
 inline rlscan_status launch_cluster(bool overlapped, K kernel, int64_t grid, int threads, size_t smem, int cluster, cudaStream_t stream,
                                     Args... args)

@@ -55,8 +55,8 @@ __device__ __forceinline__ void box_row(char *box, int lane, int h, const float 
     }
 }
 // A box to rows of any alignment, row by row: neighbouring lanes write
-// neighbouring values (each lane its own row's: 32 sectors a store, all
-// gradients of 1 x 2047 x 8192 438 us, so 147)
+// neighbouring values (each lane its own row's: 32 sectors a store, which
+// made all gradients of 1 x 2047 x 8192 three times as long)
 __device__ __forceinline__ void copy_box(bf16 *to, int64_t stride, const char *box, int lane, int64_t rows, int64_t columns)
 {
     for (int r = 0; r < 32 && r < rows; ++r, to += stride) {
@@ -95,6 +95,11 @@ __device__ __forceinline__ void load_row(Words<bf16, 8> (&w)[4], const bf16 *p, 
 // finds both of a value in its own tensor memory.  Warps: 0 copies, 1
 // multiplies (the first block's), 2 holds the tensor memory, 4 to 11 take the
 // sums out while the next tile's are made in the other half of the 512 columns.
+// Bound by the products where K is long (forward 16384 x 4096 x 12288 1838 us,
+// 1.79 PFLOP/s of the 1.89 that the library's plain product reaches), by the
+// epilogue and the outputs' bytes where it is short (3636 x 64 x 4016 26 us).
+// Four warps for the sums held the products up: gradients of 16384 x 512 x 512
+// 130 us, with eight 107.
 template <Job JOB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     projection_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Work k)
@@ -433,9 +438,9 @@ bool map_of(CUtensorMap *m, const Operand &o, uint32_t box) { return umma::encod
 
 // Few tiles of a long K leave pairs without work: K is then taken in parts, at
 // least four steps each, whose sums are joined in order by another kernel.
-// Measured, gradients of 8 x 4096 x 12288 (dx: 16 tiles of 384 steps) 266 us
-// whole, 186 in four parts of 96 steps (and dW of 16384 x 512 x 512 in parts: all
-// gradients 211 and 129).
+// Measured, gradients of 8 x 4096 x 12288 (dx: 16 tiles of 384 steps) 250 us
+// whole, 166 in four parts of 96 steps (and dW of 16384 x 512 x 512 in parts: all
+// gradients 132 and 70).
 struct Split {
     int64_t parts, steps;
 };

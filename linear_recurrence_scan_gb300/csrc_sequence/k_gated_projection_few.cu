@@ -38,8 +38,8 @@ __device__ __forceinline__ Words<bf16, 8> eight(const bf16 *row, int64_t k, int6
 // weights' bytes bound it, not the products, so the tensor cores' older warp
 // form, which takes its operands from registers, is the one that fits.
 // Measured: 1 x 2048 x 8192 16 us, by the tiles of 256 rows 24 (the call on the
-// host 7); 8 x 4096 x 12288 34 us, 5.9 TB/s, 16 rows 42, 32 rows 62, by the
-// tiles 54 for any of them; 32 x 2047 x 8192, read value by value, 48 us, by the
+// host 7); 8 x 4096 x 12288 34 us, 5.9 TB/s, 16 rows 43, 32 rows 62, by the
+// tiles 54 for any of them; 32 x 2047 x 8192, read value by value, 46 us, by the
 // tiles, which need copies of such weights, 100.
 template <int NT, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps, NT == 4 ? 2 : 3)

@@ -75,7 +75,7 @@ __device__ __forceinline__ void finish(const rlscan_gated_scan_args &a, const Fo
 
 // Arrays of any alignment: the next step's values are loaded into registers
 // while this one's are worked on.  Measured, 3 x 1001 x 1111 float32 (13 MB a
-// tensor, one value a load): 15 us, its bytes' time 8.
+// tensor, one value a load): 23 us, its bytes' time 8.
 template <class T, bool VEC, bool CLUSTER>
 __global__ void __launch_bounds__(32 * kGatedWarps, sizeof(T) == 2 && VEC ? 3 : 2)
     forward_kernel(const __grid_constant__ rlscan_gated_scan_args a, const __grid_constant__ ForwardArgs o, int ranks)
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, sizeof(T) == 2 && VEC ? 3 : 
 // tokens of 16-bit values; y leaves through shared memory too.  Three blocks an
 // SM are what 78 registers and 57 KB allow.  Measured: 8 x 2048 x 4096 bfloat16
 // 120 us (its bytes' time 79), 4 x 4096 x 4096 float32 170 us (158), 2 x 16384 x
-// 2048 bfloat16 in clusters of six 144 us (79).  Float32 is bound by its bytes;
+// 2048 bfloat16 in clusters of six 152 us (79).  Float32 is bound by its bytes;
 // bfloat16 by instructions and by the steps' chain of waits: issue slots 63%
 // busy, exponential units (three exponentials, two reciprocals and a reciprocal
 // root a value) 42%, and of 512 blocks' work 456 at once leave a second round.

@@ -209,9 +209,13 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
 // memory while a third's are worked on; what the gradients need again (x,
 // grad_y) is read again from there, and each gradient leaves from its input's
 // place, which the same lane has read.  With two steps in shared memory, one of
-// them on its way, the bytes in flight bound the kernel (8 x 2048 x 4096: 226
-// to 253 us).  Two blocks an SM leave 17 KB for the maps, which is why at most
-// four blocks share a row here.
+// them on its way, the bytes in flight bound the kernel (a tenth slower).  Two
+// blocks an SM leave 17 KB for the maps, which is why at most four blocks share
+// a row here.  Measured: 8 x 2048 x 4096 bfloat16 238 us (its bytes' time 139), 4
+// x 4096 x 4096 float32 297 us (277), 2 x 16384 x 2048 bfloat16 in clusters of
+// four 299 us (139).  Float32 is bound by its bytes; bfloat16 by instructions (issue
+// slots 58% busy at two blocks an SM; 8 x 2048 x 4096 has 512 blocks' work for
+// 304 places).
 constexpr int kBackCluster = 4, kBackStages = 3;
 struct BackwardMaps {
     CUtensorMap x, gate, input_gate, grad_y, dx, dgate, dinput_gate;
