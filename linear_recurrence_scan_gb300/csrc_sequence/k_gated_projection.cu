@@ -14,27 +14,55 @@ namespace {
 
 __device__ unsigned int g_timed_out;  // a wait ran out on this device
 
-// Forward: z and u, then h.  Gates: z and u, then gz and gu.  Input: dx, the
-// sum over both gates' columns.  Weights: dWg and dWu.
-enum class Job { Forward, Gates, Input, Weights };
+// Forward: z and u, then h.  Gates: z and u, then gz and gu.  Grads: dx, the sum
+// over both gates' columns, and dWg and dWu.
+enum class Job { Forward, Gates, Grads };
 
 struct Maps {
-    CUtensorMap a[2], b[2], out[2];
+    CUtensorMap a[4], b[3], out[3];  // Grads: dx's, then the weights'
+};
+
+// A product: its tiles, each in `parts` of `part_steps` steps (blocks of 64
+// values of K; 1: whole), which are the items of work.
+struct Product {
+    bool weights;
+    int64_t tiles_m, tiles_n, steps, parts, part_steps;
+    float *sums;  // of parts > 1: [parts][rows of all outputs][columns]
+    __host__ __device__ int64_t items() const { return tiles_m * tiles_n * parts; }
 };
 
 struct Work {
     int64_t M, D, F;
-    int64_t tiles_m, tiles_n, steps;  // steps: blocks of 64 values of K
     int act;
     const bf16 *grad_h;
     int64_t grad_h_stride;
     bool grad_h_vec;
-    bf16 *out[2];
+    Product product[2];  // the one of longer items first; the second may have none
+    int64_t extra;       // see item_of
+    bf16 *out[3];
     int64_t out_stride;
-    bool out_mapped;  // outputs leave through maps.out
-    int64_t parts, part_steps;  // K in `parts` of `part_steps` steps (1: whole)
-    float *sums;                // of parts > 1: [parts][rows of all outputs][columns]
+    bool out_mapped[3];  // the output leaves through maps.out
 };
+
+// The i-th item of a pair of blocks, -1 behind its last: the first product's in
+// turn; then the pairs that had one less of them take `extra` of the second's,
+// which last as long, and all take the rest in turn.
+__device__ __forceinline__ int64_t item_of(const Work &k, int64_t at, int64_t pairs, int64_t i)
+{
+    const int64_t a = k.product[0].items(), b = k.product[1].items(), high = a % pairs, mine = a / pairs + (at < high ? 1 : 0);
+    if (i < mine) return at + i * pairs;
+    int64_t j = i - mine;
+    const int64_t low = high > 0 ? pairs - high : 0;
+    if (low > 0 && at >= high) {
+        if (j < k.extra) {
+            const int64_t first = at - high + j * low;
+            return first < b ? a + first : -1;
+        }
+        j -= k.extra;
+    }
+    const int64_t rest = k.extra * low + (at >= high ? at - high : at - high + pairs) + j * pairs;
+    return rest < b ? a + rest : -1;
+}
 
 constexpr int kBlockK = 64;  // values of K in a stage: a row of 128 bytes
 constexpr int kStages = 5, kThreads = 384, kSumWarps = 8;
@@ -105,7 +133,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     projection_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Work k)
 {
     constexpr bool kGates = JOB == Job::Forward || JOB == Job::Gates;
-    constexpr bool kAMn = JOB == Job::Weights, kBMn = !kGates;
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t full[kStages], empty[kStages], sums_full[2], sums_empty[2];
     __shared__ uint32_t tmem_at;
@@ -134,30 +161,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     umma::fence_after();
     const uint32_t tmem = tmem_at;
     ptx::pdl_wait_prerequisites();
-    const int64_t items = k.tiles_m * k.tiles_n * k.parts, first_item = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int64_t at_pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     // Tiles in bands of eight rows of tiles, column after column: the pairs at
     // work share rows of A and columns of B in L2.
-    auto place = [&](int64_t tile, int64_t &m, int64_t &n) {
+    auto place = [&](const Product &of, int64_t tile, int64_t &m, int64_t &n) {
         constexpr int64_t kBand = 8;
-        const int64_t band = tile / (kBand * k.tiles_n), in = tile - band * kBand * k.tiles_n;
-        const int64_t high = k.tiles_m - band * kBand < kBand ? k.tiles_m - band * kBand : kBand;
+        const int64_t band = tile / (kBand * of.tiles_n), in = tile - band * kBand * of.tiles_n;
+        const int64_t high = of.tiles_m - band * kBand < kBand ? of.tiles_m - band * kBand : kBand;
         m = band * kBand + in % high;
         n = in / high;
     };
+    // The item's product, and the item's number among the product's
+    auto product_of = [&](int64_t &item) -> const Product & {
+        const int64_t first = k.product[0].items();
+        if (item < first) return k.product[0];
+        item -= first;
+        return k.product[1];
+    };
     // An item is a tile, or a part of its K
-    auto first_step = [&](int64_t item) { return item % k.parts * k.part_steps; };
-    auto last_step = [&](int64_t item) {
-        const int64_t e = (item % k.parts + 1) * k.part_steps;
-        return e < k.steps ? e : k.steps;
+    auto first_step = [](const Product &of, int64_t item) { return item % of.parts * of.part_steps; };
+    auto last_step = [](const Product &of, int64_t item) {
+        const int64_t e = (item % of.parts + 1) * of.part_steps;
+        return e < of.steps ? e : of.steps;
     };
     if (warp == 0 && lane == 0) {  // copies
         uint32_t stage = 0, phase = 1;  // the first wait on an empty stage passes
         int64_t issued = 0;
-        const int64_t half = kGates ? 0 : JOB == Job::Input ? k.steps / 2 : k.tiles_m / 2;
-        for (int64_t item = first_item; item < items && !has_given_up(&gave_up); item += pairs) {
+        for (int64_t i = 0, item; !has_given_up(&gave_up) && (item = item_of(k, at_pair, pairs, i)) >= 0; ++i) {
+            const Product &of = product_of(item);
             int64_t tm, tn;
-            place(item / k.parts, tm, tn);
-            for (int64_t s = first_step(item), e = last_step(item); s < e; ++s) {
+            place(of, item / of.parts, tm, tn);
+            for (int64_t s = first_step(of, item), e = last_step(of, item); s < e; ++s) {
                 if (!wait(ptx::smem_u32(&empty[stage]), phase, &gave_up)) break;
                 const uint32_t bar = umma::of_rank(ptx::smem_u32(&full[stage]), 0);
                 const uint32_t a = smem + stage * kStageBytes, b = a + kTileBytes;
@@ -166,17 +200,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int k0 = static_cast<int>(s) * kBlockK;
                     umma::load_box(a, &maps.a[0], k0, static_cast<int>(tm * 256 + rank * 128), bar);
                     umma::load_box(b, &maps.b[rank], k0, static_cast<int>(tn * 128), bar);
-                } else if constexpr (JOB == Job::Input) {
+                } else if (!of.weights) {
+                    const int64_t half = of.steps / 2;
                     const int part = s >= half ? 1 : 0, k0 = static_cast<int>(s - part * half) * kBlockK;
                     umma::load_box(a, &maps.a[part], k0, static_cast<int>(tm * 256 + rank * 128), bar);
                     for (int i = 0; i < 2; ++i)
                         umma::load_box(b + i * (kTileBytes / 2), &maps.b[part], static_cast<int>(tn * 256 + rank * 128 + 64 * i), k0, bar);
                 } else {
+                    const int64_t half = of.tiles_m / 2;
                     const int part = tm >= half ? 1 : 0, k0 = static_cast<int>(s) * kBlockK;
                     const int f0 = static_cast<int>((tm - part * half) * 256 + rank * 128);
                     for (int i = 0; i < 2; ++i) {
-                        umma::load_box(a + i * (kTileBytes / 2), &maps.a[part], f0 + 64 * i, k0, bar);
-                        umma::load_box(b + i * (kTileBytes / 2), &maps.b[0], static_cast<int>(tn * 256 + rank * 128 + 64 * i), k0, bar);
+                        umma::load_box(a + i * (kTileBytes / 2), &maps.a[2 + part], f0 + 64 * i, k0, bar);
+                        umma::load_box(b + i * (kTileBytes / 2), &maps.b[2], static_cast<int>(tn * 256 + rank * 128 + 64 * i), k0, bar);
                     }
                 }
                 ++issued;
@@ -187,13 +223,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
             if (!wait(ptx::smem_u32(&empty[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u, &gave_up)) break;
     } else if (warp == 1 && lane == 0 && rank == 0) {  // products
-        constexpr uint32_t kInstruction = umma::instruction(kAMn, kBMn, 256, 256);
         uint32_t stage = 0, phase = 0, buffer = 0, buffer_phase = 1;
-        for (int64_t item = first_item; item < items; item += pairs) {
+        for (int64_t i = 0, item; (item = item_of(k, at_pair, pairs, i)) >= 0; ++i) {
+            const Product &of = product_of(item);
+            // rows of A and columns of B lie along K (Forward, Gates; dx's A) or across it
+            const bool a_across = !kGates && of.weights;
+            const uint32_t instruction = kGates ? umma::instruction(false, false, 256, 256)
+                                         : a_across ? umma::instruction(true, true, 256, 256) : umma::instruction(false, true, 256, 256);
             if (!wait(ptx::smem_u32(&sums_empty[buffer]), buffer_phase, &gave_up)) break;
             umma::fence_after();
             bool fine = true;
-            const int64_t begin = first_step(item), stop = last_step(item);
+            const int64_t begin = first_step(of, item), stop = last_step(of, item);
             for (int64_t s = begin; s < stop && fine; ++s) {
                 fine = wait(ptx::smem_u32(&full[stage]), phase, &gave_up);
                 if (!fine) break;
@@ -201,8 +241,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t a = smem + stage * kStageBytes, b = a + kTileBytes;
 #pragma unroll
                 for (int j = 0; j < kBlockK / 16; ++j)
-                    umma::multiply(tmem + buffer * 256, umma::descriptor(a + j * (kAMn ? 2048 : 32), kTileBytes / 2),
-                                   umma::descriptor(b + j * (kBMn ? 2048 : 32), kTileBytes / 2), kInstruction, s > begin || j > 0);
+                    umma::multiply(tmem + buffer * 256, umma::descriptor(a + j * (a_across ? 2048 : 32), kTileBytes / 2),
+                                   umma::descriptor(b + j * (kGates ? 32 : 2048), kTileBytes / 2), instruction, s > begin || j > 0);
                 umma::commit(ptx::smem_u32(&empty[stage]));
                 if (++stage == kStages) stage = 0, phase ^= 1;
             }
@@ -227,7 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int turn = 0;  // of Forward's two boxes
         auto put_box = [&](int i, int64_t x, int64_t y, int64_t rows, int64_t columns, const char *box) {
             const bool some = y < rows && x < columns;
-            if (k.out_mapped) {
+            if (k.out_mapped[i]) {
                 fence_async();
                 __syncwarp();
                 if (lane == 0 && some) store_box2(&maps.out[i], x, y, box);
@@ -237,13 +277,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (some) copy_box(k.out[i] + y * k.out_stride + x, k.out_stride, box, lane, rows - y, columns - x);
             }
         };
-        for (int64_t item = first_item; item < items; item += pairs) {
+        for (int64_t i = 0, item; (item = item_of(k, at_pair, pairs, i)) >= 0; ++i) {
+            const Product &of = product_of(item);
             int64_t tm, tn;
-            place(item / k.parts, tm, tn);
-            const int64_t half = k.tiles_m / 2;
-            const int which = JOB == Job::Weights && tm >= half ? 1 : 0;
+            place(of, item / of.parts, tm, tn);
+            const int64_t half = of.tiles_m / 2;
+            const int which = of.weights && tm >= half ? 1 : 0;
             const int64_t row = (tm - which * half) * 256 + rank * 128 + part * 32 + lane;
-            const int64_t rows = JOB == Job::Weights ? k.F : k.M;
+            const int64_t rows = of.weights ? k.F : k.M;
             if (!wait(ptx::smem_u32(&sums_full[buffer]), phase, &gave_up)) break;
             umma::fence_after();
             const uint32_t at = tmem + buffer * 256 + (static_cast<uint32_t>(part * 32) << 16);
@@ -299,9 +340,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     float f[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-                    if (k.parts > 1) {
-                        const int64_t all = JOB == Job::Weights ? 2 * rows : rows, n = row < rows ? k.D - d0 - c : 0;
-                        float *to = k.sums + ((item % k.parts) * all + which * rows + row) * k.D + d0 + c;
+                    if (of.parts > 1) {
+                        const int64_t all = of.weights ? 2 * rows : rows, n = row < rows ? k.D - d0 - c : 0;
+                        float *to = of.sums + ((item % of.parts) * all + which * rows + row) * k.D + d0 + c;
                         if (k.D % 4 == 0) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 4)
@@ -316,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int h = c / 32 % 2;
                         if (h == 0) free_box(true);
                         box_row(box, lane, h, f);
-                        if (h == 1) put_box(which, d0 + c - 32, row0, rows, k.D, box);
+                        if (h == 1) put_box(of.weights ? 1 + which : 0, d0 + c - 32, row0, rows, k.D, box);
                     }
                 }
             }
@@ -436,42 +477,45 @@ rlscan_status pack_all(const rlscan_gated_projection_args &a, Layout &l, char *w
 
 bool map_of(CUtensorMap *m, const Operand &o, uint32_t box) { return umma::encode(m, o.p, o.rows, o.columns, o.pitch, box); }
 
-// Few tiles of a long K leave pairs without work: K is then taken in parts, at
-// least four steps each, whose sums are joined in order by another kernel.
-// Measured, gradients of 8 x 4096 x 12288 (dx: 16 tiles of 384 steps) 250 us
-// whole, 166 in four parts of 96 steps (and dW of 16384 x 512 x 512 in parts: all
-// gradients 132 and 70).
-struct Split {
-    int64_t parts, steps;
+// The gradients' two products share one launch, the longer items first.  Few
+// tiles of a long K leave pairs without work: a tile of more steps than a pair's
+// average load is taken in parts, of at least four steps each, whose sums are
+// joined in order by another kernel.  Taking a tile's sums out counts as eight
+// steps.  Measured, gradients of 8 x 4096 x 12288 (dx: 16 tiles of 384 steps) @C@
+// us whole, @D@ in parts (and dW of 16384 x 512 x 512 in parts: all gradients @E@
+// and @F@); 5000 x 2560 x 6912, whose products fill 2.6 and 7.1 rounds of pairs,
+// 683 us in launches of their own, 661 in one.
+struct GradPlan {
+    Product input, weights;
+    size_t at_weights, bytes;  // of the sums of parts
 };
-Split split_of(int64_t tiles, int64_t steps)
+GradPlan plan_of(const rlscan_gated_projection_args &a, bool want_x, bool want_weights)
 {
+    constexpr int64_t kEnd = 8;
+    GradPlan g = {};
+    g.input = {false, want_x ? ceil_div(a.M, 256) : 0, ceil_div(a.D, 256), 2 * ceil_div(a.F, kBlockK), 1, 0, nullptr};
+    g.weights = {true, want_weights ? 2 * ceil_div(a.F, 256) : 0, ceil_div(a.D, 256), ceil_div(a.M, kBlockK), 1, 0, nullptr};
     const int64_t pairs = (sm_count() > 0 ? sm_count() : 152) / 2;
-    int64_t parts = tiles > 0 ? pairs / tiles : 1;
-    if (parts > steps / 4) parts = steps / 4;
-    if (parts < 2) return {1, steps};
-    const int64_t each = ceil_div(steps, parts);
-    return {ceil_div(steps, each), each};
-}
-struct GradSplits {
-    Split input, weights;
-    size_t bytes;  // of the sums of either, which take turns
-};
-GradSplits splits_of(const rlscan_gated_projection_args &a)
-{
-    GradSplits g;
-    g.input = split_of(ceil_div(a.M, 256) * ceil_div(a.D, 256), 2 * ceil_div(a.F, kBlockK));
-    g.weights = split_of(2 * ceil_div(a.F, 256) * ceil_div(a.D, 256), ceil_div(a.M, kBlockK));
-    const int64_t x = g.input.parts > 1 ? g.input.parts * a.M * a.D : 0, w = g.weights.parts > 1 ? g.weights.parts * 2 * a.F * a.D : 0;
-    g.bytes = static_cast<size_t>(x > w ? x : w) * sizeof(float);
+    const int64_t load = (g.input.items() * (g.input.steps + kEnd) + g.weights.items() * (g.weights.steps + kEnd)) / pairs;
+    size_t at = 0;
+    for (Product *p : {&g.input, &g.weights}) {
+        const int64_t each = load > 4 ? load : 4;
+        p->parts = p->items() > 0 && p->steps > each ? ceil_div(p->steps, each) : 1;
+        if (p->parts > p->steps / 4) p->parts = p->steps / 4 > 1 ? p->steps / 4 : 1;
+        p->part_steps = ceil_div(p->steps, p->parts);
+        p->parts = ceil_div(p->steps, p->part_steps);
+        if (p == &g.weights) g.at_weights = at;
+        if (p->parts > 1) at += up256(static_cast<size_t>(p->parts) * (p->weights ? 2 * a.F : a.M) * a.D * sizeof(float));
+    }
+    g.bytes = at;
     return g;
 }
 
-rlscan_status join(const Work &w, int64_t rows, cudaStream_t s)
+rlscan_status join(const Product &p, int64_t rows, int64_t columns, bf16 *out0, bf16 *out1, cudaStream_t s)
 {
-    const int64_t half = rows * w.D, all = w.out[1] != nullptr ? 2 * half : half, most = 16 * (sm_count() > 0 ? sm_count() : 152);
+    const int64_t half = rows * columns, all = out1 != nullptr ? 2 * half : half, most = 16 * (sm_count() > 0 ? sm_count() : 152);
     const int64_t blocks = ceil_div(all, 256);
-    return launch_overlapped(join_kernel, blocks < most ? blocks : most, 256, 0, s, w.sums, w.parts, all, half, w.out[0], w.out[1]);
+    return launch_overlapped(join_kernel, blocks < most ? blocks : most, 256, 0, s, p.sums, p.parts, all, half, out0, out1);
 }
 
 template <Job JOB>
@@ -493,9 +537,9 @@ rlscan_status launch_job(const Maps &maps, Work &w, cudaStream_t s)
         int n = 0;
         return ok(cudaOccupancyMaxActiveClusters(&n, projection_kernel<JOB>, &cfg)) ? n : 0;
     });
-    const int64_t tiles = w.tiles_m * w.tiles_n * w.parts, pairs = most > 0 ? most : 1;
+    const int64_t items = w.product[0].items() + w.product[1].items(), pairs = most > 0 ? most : 1;
     if (w.M > 0x7fffffff - 256 || w.F > 0x7fffffff - 256 || w.D > 0x7fffffff - 256) return RLSCAN_ERR_SHAPE;
-    return launch(true, projection_kernel<JOB>, 2 * (tiles < pairs ? tiles : pairs), kThreads, kSmem, s, maps, w);
+    return launch(true, projection_kernel<JOB>, 2 * (items < pairs ? items : pairs), kThreads, kSmem, s, maps, w);
 }
 
 // An output [rows, columns] that leaves in boxes of 64 columns x 32 rows, where its alignment allows
@@ -503,7 +547,7 @@ void map_out(Maps &m, int i, Work &w, void *p, int64_t rows, int64_t columns, in
 {
     w.out[i] = static_cast<bf16 *>(p);
     w.out_stride = pitch;
-    w.out_mapped = (i == 0 || w.out_mapped) && fits_map(p, rows, columns, pitch) && umma::encode(&m.out[i], p, rows, columns, up8(pitch), 32);
+    w.out_mapped[i] = fits_map(p, rows, columns, pitch) && umma::encode(&m.out[i], p, rows, columns, up8(pitch), 32);
 }
 
 bool vec_rows(const void *p, int64_t stride) { return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(stride * 2)) & 15u) == 0; }
@@ -526,8 +570,7 @@ rlscan_status launch_gated_projection(const rlscan_gated_projection_args &a, voi
     if (!map_of(&m.a[0], l.x, 128) || !map_of(&m.b[0], l.gate, 128) || !map_of(&m.b[1], l.up, 128)) return RLSCAN_ERR_CUDA;
     Work w = {};
     w.M = a.M, w.D = a.D, w.F = a.F, w.act = static_cast<int>(a.activation);
-    w.tiles_m = ceil_div(a.M, 256), w.tiles_n = ceil_div(a.F, 128), w.steps = ceil_div(a.D, kBlockK);
-    w.parts = 1, w.part_steps = w.steps;
+    w.product[0] = {false, ceil_div(a.M, 256), ceil_div(a.F, 128), ceil_div(a.D, kBlockK), 1, ceil_div(a.D, kBlockK), nullptr};
     map_out(m, 0, w, h, a.M, a.F, a.F);
     return launch_job<Job::Forward>(m, w, s);
 }
@@ -535,7 +578,13 @@ rlscan_status launch_gated_projection(const rlscan_gated_projection_args &a, voi
 size_t gated_projection_backward_workspace(const rlscan_gated_projection_args &a)
 {
     if (a.M == 0 || a.F == 0 || a.D == 0) return 0;
-    return layout(a).bytes + up256(static_cast<size_t>(a.M) * 2 * up8(a.F) * 2) + splits_of(a).bytes;
+    size_t sums = 0;  // of whichever gradients are asked for: one alone may be in more parts
+    for (const bool x : {true, false})
+        for (const bool weights : {true, false}) {
+            const size_t n = plan_of(a, x, weights).bytes;
+            sums = n > sums ? n : sums;
+        }
+    return layout(a).bytes + up256(static_cast<size_t>(a.M) * 2 * up8(a.F) * 2) + sums;
 }
 
 rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_args &a, const void *grad_h,
@@ -558,38 +607,37 @@ rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_arg
     if (!map_of(&m.a[0], l.x, 128) || !map_of(&m.b[0], l.gate, 128) || !map_of(&m.b[1], l.up, 128)) return RLSCAN_ERR_CUDA;
     Work w = {};
     w.M = a.M, w.D = a.D, w.F = a.F, w.act = static_cast<int>(a.activation);
-    w.tiles_m = ceil_div(a.M, 256), w.tiles_n = ceil_div(a.F, 128), w.steps = ceil_div(a.D, kBlockK);
+    w.product[0] = {false, ceil_div(a.M, 256), ceil_div(a.F, 128), ceil_div(a.D, kBlockK), 1, ceil_div(a.D, kBlockK), nullptr};
     w.grad_h = static_cast<const bf16 *>(grad_h), w.grad_h_stride = grad_h_stride, w.grad_h_vec = vec_rows(grad_h, grad_h_stride);
-    w.parts = 1, w.part_steps = w.steps;
     map_out(m, 0, w, g, a.M, a.F, 2 * pitch);
     map_out(m, 1, w, g + pitch, a.M, a.F, 2 * pitch);
     st = launch_job<Job::Gates>(m, w, s);
-    if (st != RLSCAN_OK) return st;
-    const GradSplits splits = splits_of(a);
-    w.sums = reinterpret_cast<float *>(reinterpret_cast<char *>(g) + up256(static_cast<size_t>(a.M) * 2 * pitch * 2));
+    if (st != RLSCAN_OK || (grad_x == nullptr && grad_gate == nullptr)) return st;
+    GradPlan p = plan_of(a, grad_x != nullptr, grad_gate != nullptr);
+    char *sums = reinterpret_cast<char *>(g) + up256(static_cast<size_t>(a.M) * 2 * pitch * 2);
+    p.input.sums = reinterpret_cast<float *>(sums);
+    p.weights.sums = reinterpret_cast<float *>(sums + p.at_weights);
     const Operand gz{g, a.M, a.F, 2 * pitch, false}, gu{g + pitch, a.M, a.F, 2 * pitch, false};
+    Maps mg = {};
     if (grad_x != nullptr) {
-        Maps mx = {};
-        if (!map_of(&mx.a[0], gz, 128) || !map_of(&mx.a[1], gu, 128) || !map_of(&mx.b[0], l.gate, 64) || !map_of(&mx.b[1], l.up, 64))
+        if (!map_of(&mg.a[0], gz, 128) || !map_of(&mg.a[1], gu, 128) || !map_of(&mg.b[0], l.gate, 64) || !map_of(&mg.b[1], l.up, 64))
             return RLSCAN_ERR_CUDA;
-        w.tiles_n = ceil_div(a.D, 256), w.steps = 2 * ceil_div(a.F, kBlockK);
-        w.parts = splits.input.parts, w.part_steps = splits.input.steps;
-        map_out(mx, 0, w, grad_x, a.M, a.D, a.D);
-        w.out[1] = nullptr;
-        st = launch_job<Job::Input>(mx, w, s);
-        if (st == RLSCAN_OK && w.parts > 1) st = join(w, a.M, s);
-        if (st != RLSCAN_OK) return st;
+        map_out(mg, 0, w, grad_x, a.M, a.D, a.D);
     }
     if (grad_gate != nullptr) {
-        Maps mw = {};
-        if (!map_of(&mw.a[0], gz, 64) || !map_of(&mw.a[1], gu, 64) || !map_of(&mw.b[0], l.x, 64)) return RLSCAN_ERR_CUDA;
-        w.tiles_m = 2 * ceil_div(a.F, 256), w.tiles_n = ceil_div(a.D, 256), w.steps = ceil_div(a.M, kBlockK);
-        map_out(mw, 0, w, grad_gate, a.F, a.D, a.D);
-        map_out(mw, 1, w, grad_up, a.F, a.D, a.D);
-        w.parts = splits.weights.parts, w.part_steps = splits.weights.steps;
-        st = launch_job<Job::Weights>(mw, w, s);
-        if (st == RLSCAN_OK && w.parts > 1) st = join(w, a.F, s);
+        if (!map_of(&mg.a[2], gz, 64) || !map_of(&mg.a[3], gu, 64) || !map_of(&mg.b[2], l.x, 64)) return RLSCAN_ERR_CUDA;
+        map_out(mg, 1, w, grad_gate, a.F, a.D, a.D);
+        map_out(mg, 2, w, grad_up, a.F, a.D, a.D);
     }
+    const bool input_first = p.weights.items() == 0 || (p.input.items() > 0 && p.input.part_steps >= p.weights.part_steps);
+    w.product[0] = input_first ? p.input : p.weights;
+    w.product[1] = input_first ? p.weights : p.input;
+    const int64_t each = w.product[1].part_steps + 1;  // (an item takes a little time beside its steps)
+    w.extra = (w.product[0].part_steps + each / 2) / each;
+    st = launch_job<Job::Grads>(mg, w, s);
+    if (st == RLSCAN_OK && p.input.parts > 1) st = join(p.input, a.M, a.D, static_cast<bf16 *>(grad_x), nullptr, s);
+    if (st == RLSCAN_OK && p.weights.parts > 1)
+        st = join(p.weights, a.F, a.D, static_cast<bf16 *>(grad_gate), static_cast<bf16 *>(grad_up), s);
     return st;
 }
 
