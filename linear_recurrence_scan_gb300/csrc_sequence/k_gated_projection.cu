@@ -38,7 +38,7 @@ struct Work {
     int64_t grad_h_stride;
     bool grad_h_vec;
     Product product[2];  // the one of longer items first; the second may have none
-    int64_t extra;       // see item_of
+    int64_t items[2], whole, high, extra;  // see item_of: items of both, whole rounds of the first's, pairs with one more
     bf16 *out[3];
     int64_t out_stride;
     bool out_mapped[3];  // the output leaves through maps.out
@@ -49,7 +49,7 @@ struct Work {
 // which last as long, and all take the rest in turn.
 __device__ __forceinline__ int64_t item_of(const Work &k, int64_t at, int64_t pairs, int64_t i)
 {
-    const int64_t a = k.product[0].items(), b = k.product[1].items(), high = a % pairs, mine = a / pairs + (at < high ? 1 : 0);
+    const int64_t a = k.items[0], b = k.items[1], high = k.high, mine = k.whole + (at < high ? 1 : 0);
     if (i < mine) return at + i * pairs;
     int64_t j = i - mine;
     const int64_t low = high > 0 ? pairs - high : 0;
@@ -173,9 +173,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     // The item's product, and the item's number among the product's
     auto product_of = [&](int64_t &item) -> const Product & {
-        const int64_t first = k.product[0].items();
-        if (item < first) return k.product[0];
-        item -= first;
+        if (item < k.items[0]) return k.product[0];
+        item -= k.items[0];
         return k.product[1];
     };
     // An item is a tile, or a part of its K
@@ -477,16 +476,16 @@ rlscan_status pack_all(const rlscan_gated_projection_args &a, Layout &l, char *w
 
 bool map_of(CUtensorMap *m, const Operand &o, uint32_t box) { return umma::encode(m, o.p, o.rows, o.columns, o.pitch, box); }
 
-// The gradients' two products share one launch, the longer items first.  Few
+// The gradients' two products share a launch, the longer items first.  Few
 // tiles of a long K leave pairs without work: a tile of more steps than a pair's
 // average load is taken in parts, of at least four steps each, whose sums are
 // joined in order by another kernel.  Taking a tile's sums out counts as eight
-// steps.  Measured, gradients of 8 x 4096 x 12288 (dx: 16 tiles of 384 steps) @C@
-// us whole, @D@ in parts (and dW of 16384 x 512 x 512 in parts: all gradients @E@
-// and @F@); 5000 x 2560 x 6912, whose products fill 2.6 and 7.1 rounds of pairs,
-// 683 us in launches of their own, 661 in one.
+// steps.  Measured, gradients of 8 x 4096 x 12288 (dx: 16 tiles of 384 steps) 209
+// us whole, 168 in parts (and dW of 16384 x 512 x 512 in parts: all gradients 125
+// and 66).
 struct GradPlan {
     Product input, weights;
+    int64_t load;              // steps of a pair, on average
     size_t at_weights, bytes;  // of the sums of parts
 };
 GradPlan plan_of(const rlscan_gated_projection_args &a, bool want_x, bool want_weights)
@@ -496,10 +495,10 @@ GradPlan plan_of(const rlscan_gated_projection_args &a, bool want_x, bool want_w
     g.input = {false, want_x ? ceil_div(a.M, 256) : 0, ceil_div(a.D, 256), 2 * ceil_div(a.F, kBlockK), 1, 0, nullptr};
     g.weights = {true, want_weights ? 2 * ceil_div(a.F, 256) : 0, ceil_div(a.D, 256), ceil_div(a.M, kBlockK), 1, 0, nullptr};
     const int64_t pairs = (sm_count() > 0 ? sm_count() : 152) / 2;
-    const int64_t load = (g.input.items() * (g.input.steps + kEnd) + g.weights.items() * (g.weights.steps + kEnd)) / pairs;
+    g.load = (g.input.items() * (g.input.steps + kEnd) + g.weights.items() * (g.weights.steps + kEnd)) / pairs;
     size_t at = 0;
     for (Product *p : {&g.input, &g.weights}) {
-        const int64_t each = load > 4 ? load : 4;
+        const int64_t each = g.load > 4 ? g.load : 4;
         p->parts = p->items() > 0 && p->steps > each ? ceil_div(p->steps, each) : 1;
         if (p->parts > p->steps / 4) p->parts = p->steps / 4 > 1 ? p->steps / 4 : 1;
         p->part_steps = ceil_div(p->steps, p->parts);
@@ -537,9 +536,13 @@ rlscan_status launch_job(const Maps &maps, Work &w, cudaStream_t s)
         int n = 0;
         return ok(cudaOccupancyMaxActiveClusters(&n, projection_kernel<JOB>, &cfg)) ? n : 0;
     });
-    const int64_t items = w.product[0].items() + w.product[1].items(), pairs = most > 0 ? most : 1;
+    for (int i = 0; i < 2; ++i) w.items[i] = w.product[i].items();
+    const int64_t items = w.items[0] + w.items[1], pairs = most > 0 && most < items ? most : most > 0 ? items : 1;
+    w.whole = w.items[0] / pairs, w.high = w.items[0] % pairs;
+    const int64_t each = w.product[1].part_steps + 1;  // (an item takes a little time beside its steps)
+    w.extra = (w.product[0].part_steps + each / 2) / each;
     if (w.M > 0x7fffffff - 256 || w.F > 0x7fffffff - 256 || w.D > 0x7fffffff - 256) return RLSCAN_ERR_SHAPE;
-    return launch(true, projection_kernel<JOB>, 2 * (items < pairs ? items : pairs), kThreads, kSmem, s, maps, w);
+    return launch(true, projection_kernel<JOB>, 2 * pairs, kThreads, kSmem, s, maps, w);
 }
 
 // An output [rows, columns] that leaves in boxes of 64 columns x 32 rows, where its alignment allows
@@ -632,9 +635,17 @@ rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_arg
     const bool input_first = p.weights.items() == 0 || (p.input.items() > 0 && p.input.part_steps >= p.weights.part_steps);
     w.product[0] = input_first ? p.input : p.weights;
     w.product[1] = input_first ? p.weights : p.input;
-    const int64_t each = w.product[1].part_steps + 1;  // (an item takes a little time beside its steps)
-    w.extra = (w.product[0].part_steps + each / 2) / each;
-    st = launch_job<Job::Grads>(mg, w, s);
+    // Much work gains little by sharing a launch, and loses by it: the pairs, no
+    // longer at the same steps of K, find less of their operands in L2 (16384 x
+    // 4096 x 12288, 10600 steps a pair: one launch 6400 us, two 6200; 5000 x 2560 x
+    // 6912, 1200 steps: 670 and 683; 375 x 2912 x 368, 15 steps: 40 and 56).
+    if (p.load > 4096) {
+        const Product second = w.product[1];
+        w.product[1] = {};
+        st = launch_job<Job::Grads>(mg, w, s);
+        w.product[0] = second;
+    }
+    if (st == RLSCAN_OK && w.product[0].items() > 0) st = launch_job<Job::Grads>(mg, w, s);
     if (st == RLSCAN_OK && p.input.parts > 1) st = join(p.input, a.M, a.D, static_cast<bf16 *>(grad_x), nullptr, s);
     if (st == RLSCAN_OK && p.weights.parts > 1)
         st = join(p.weights, a.F, a.D, static_cast<bf16 *>(grad_gate), static_cast<bf16 *>(grad_up), s);
