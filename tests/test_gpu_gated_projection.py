@@ -229,3 +229,56 @@ def test_refusals():
         f(x[:, :0], w[:, :0], w[:, :0])
     with pytest.raises(ValueError, match="grad_h shape"):
         L().gated_projection_backward(torch.zeros(4, 5, dtype=BF16, device=DEV), x, w, w)
+
+
+@pytest.mark.parametrize("M,D,F", [(8, 512, 3000), (3000, 128, 128), (300, 640, 320), (40, 111, 333)])
+def test_one_gradient_alone(M, D, F):
+    """The gradient of x or of the weights alone: other items, other parts of K, than both together."""
+    x, wg, wu, gh, _ = projection_inputs(M, D, F, M + D)
+    want = projection_oracle(x, wg, wu, gh, "silu")
+    for names in (("x",), ("gate_weight", "up_weight")):
+        t = dict(x=x.to(DEV), gate_weight=wg.to(DEV), up_weight=wu.to(DEV))
+        for k in names:
+            t[k].requires_grad_()
+        L().gated_projection(**t).backward(gh.to(DEV))
+        for k, v in t.items():
+            assert (v.grad is not None) == (k in names)
+            if k in names:
+                close(v.grad, *want[k], 1.0, "gradient of " + k)
+    L().workspace_status()
+
+
+def test_much_work():
+    """Gradients of so many steps that their products take a launch each; some rows and some features against float64."""
+    M, D, F = 16384, 4096, 6144
+    gen = torch.Generator(DEV).manual_seed(3)
+    x, wg, wu, gh = (torch.randn(s, generator=gen, device=DEV, dtype=BF16) * f
+                     for s, f in (((M, D), 1.0), ((F, D), D ** -0.5), ((F, D), D ** -0.5), ((M, F), 1.0)))
+    h = L().gated_projection(x, wg, wu)
+    g = L().gated_projection_backward(gh, x, wg, wu)
+    rows, features = [0, 255, 256, 5000, M - 1], [0, 127, 128, 3333, F - 1]
+    want = projection_oracle(x[rows].cpu(), wg.cpu(), wu.cpu(), gh[rows].cpu(), "silu")
+    close(h[rows], *want["h"], 1.0, "h")
+    close(g.x[rows], *want["x"], 1.0, "gradient of x")
+    want = projection_oracle(x.cpu(), wg[features].cpu(), wu[features].cpu(), gh[:, features].cpu(), "silu")
+    for k in ("gate_weight", "up_weight"):
+        close(getattr(g, k)[features], *want[k], 1.0, "gradient of " + k)
+    L().workspace_status()
+
+
+@pytest.mark.parametrize("rows", [5, 700])
+def test_gelu_far_from_zero(rows):
+    """One value a row, weights 1: h = gelu(z) itself, to its own size.  The exponential's argument z^2 / 2 is rounded
+    twice (2^-24 of itself each, times log 2 in the result, below z^2 2^-24 in all), the rest adds less than 20 steps of
+    2^-24, and the result is rounded by 2^-8 of itself at most."""
+    from scipy.special import ndtr
+    z = torch.linspace(-12, 12, rows).to(BF16)
+    z[rows // 2] = 0
+    x, w = torch.zeros(rows, 8, dtype=BF16), torch.zeros(16, 8, dtype=BF16)
+    x[:, 0], x[:, 1] = z, 1
+    up = w.clone()
+    w[:, 0], up[:, 1] = 1, 1
+    h = L().gated_projection(x.to(DEV), w.to(DEV), up.to(DEV), "gelu").double().cpu().numpy()
+    v = z.double().numpy()
+    want = (v * ndtr(v))[:, None]
+    assert (np.abs(h - want) <= np.abs(want) * (2.0 ** -8 + (v[:, None] ** 2 + 20) * 2.0 ** -24)).all()
