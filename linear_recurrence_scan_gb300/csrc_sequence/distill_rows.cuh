@@ -85,9 +85,10 @@ __device__ __forceinline__ float warp_sum(float v)
 // exp((z - m) / tau) of a pair, for a logit z and its row's largest m: one
 // multiply-add in front of the exponential, z c - m c with c = log2 e / tau.
 // m c is rounded, by the same `rest` for every logit, which `exact` takes back
-// from a sum or a factor.  Where m c is too large for that (|m| of the size of
-// a type's lowest value, as masks have it) values are taken one by one, the
-// difference z - m first.
+// from a sum or a factor.  Below 2^24 `rest` is at most 1/2; it grows with m c,
+// and from 2^32 on 2^rest and 2^-rest leave the type's range.  So from 2^24 on
+// (logits far from 0 or low temperatures, rows masked throughout with -1e10,
+// say) values are taken one by one, the difference z - m first.
 struct Shift {
     f2 c, mc;
     float rest;
@@ -97,7 +98,7 @@ struct Shift {
         const float product = m * c1;
         c = both(c1);
         mc = both(-product);
-        wide = !(fabsf(product) < 1e30f);
+        wide = !(fabsf(product) < 0x1p24f);  // (NaN too)
         rest = wide ? 0.f : fmaf(m, c1, -product);
     }
     __device__ __forceinline__ f2 exp(f2 z) const { return exp2_fast(fma2(z, c, mc)); }

@@ -303,3 +303,52 @@ def test_rows_at_the_ends_of_each_kind(V, dtype):
     if K > 2:
         tokens[:, ::2, K // 2] = V - 1
     check(logits, teacher, tokens, mask, grad)
+
+
+LEVELS = [1e6, -1e7, 1.2e7, 1e8, -1e8, 5e9, -5e9, 1e10, -1e10, 1e12, -1e20, 1e20, -1e29, 1e29]
+
+
+def far_rows(V, K, dtype, level, rng):
+    """Logits around `level` (from 1e10 on, and for bfloat16 sooner, all the same value), one in three -infinity, one in
+    seven the type's lowest; the teacher knows the others alone."""
+    z = torch.from_numpy((level + 2 * rng.standard_normal((1, 1, V))).astype(np.float32)).to(dtype)
+    places = np.arange(V)
+    some = np.flatnonzero((places % 3 != 1) & (places % 7 != 2))
+    z[..., places % 7 == 2] = torch.finfo(dtype).min
+    z[..., places % 3 == 1] = -float("inf")
+    return z, torch.from_numpy(rng.choice(some, (1, 1, K)))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [5, 300, 2047, 5000, 9001, 50257, 131075])
+def test_logits_far_from_zero(V, dtype):
+    """Rows whose largest logit lies anywhere between 0 and the type's ends, as a row masked with -1e10 throughout: finite
+    losses and gradients, by each kernel (a warp's rows, blocks', clusters').  The exponent (z - m) / tau has the error
+    that token_policy_cases.py derives: logits of one row differ by little."""
+    K, rng = 5, np.random.default_rng(V)
+    rows = []
+    for level in LEVELS:
+        z, tokens = far_rows(V, K, dtype, level, rng)
+        teacher = torch.from_numpy((2 * rng.standard_normal((1, 1, K))).astype(np.float32))
+        grad = torch.from_numpy(rng.standard_normal((1, 1)).astype(np.float32))
+        loss, g = check(z, teacher, tokens, None, grad)
+        assert torch.isfinite(loss).all() and torch.isfinite(g).all(), level
+        rows.append((z, teacher, tokens, grad))
+    z, teacher, tokens, grad = (torch.cat(t, 1).to(DEV) for t in zip(*rows))   # one behind the other
+    loss, g = L().distill_loss_and_grad(grad, z, teacher, tokens)
+    assert torch.isfinite(loss).all() and torch.isfinite(g).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [40, 3001, 50257])
+@pytest.mark.parametrize("level,tau", [(1e4, 1e-6), (-5e3, 1e-6), (-3e9, 0.5), (7.0, 1e-6), (1e30, 1e6)])
+def test_far_logits_at_low_and_high_temperatures(level, tau, V, dtype):
+    """What counts is the logit over the temperature; the teacher's differ by a few temperatures."""
+    K, rng = 6, np.random.default_rng(1)
+    z = torch.full((1, 2, V), level).to(dtype)
+    z[0, 1, V // 2:] = -float("inf")
+    teacher = torch.from_numpy((rng.integers(0, 5, (1, 2, K)) * tau).astype(np.float32))
+    tokens = torch.from_numpy(rng.integers(0, V // 2, (1, 2, K)))
+    grad = torch.from_numpy(rng.standard_normal((1, 2)).astype(np.float32))
+    loss, g = check(z, teacher, tokens, None, grad, tau)
+    assert torch.isfinite(loss).all() and torch.isfinite(g).all()
