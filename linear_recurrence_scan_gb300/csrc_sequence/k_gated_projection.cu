@@ -270,11 +270,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 fence_async();
                 __syncwarp();
                 if (lane == 0 && some) store_box2(&maps.out[i], x, y, box);
-                if (lane == 0) stores_commit();
             } else {
                 __syncwarp();
                 if (some) copy_box(k.out[i] + y * k.out_stride + x, k.out_stride, box, lane, rows - y, columns - x);
             }
+            // (one group a box, an empty one too: free_box counts them, and Grads' outputs may leave either way)
+            if (lane == 0) stores_commit();
         };
         for (int64_t i = 0, item; (item = item_of(k, at_pair, pairs, i)) >= 0; ++i) {
             const Product &of = product_of(item);

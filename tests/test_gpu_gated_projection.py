@@ -282,3 +282,31 @@ def test_gelu_far_from_zero(rows):
     v = z.double().numpy()
     want = (v * ndtr(v))[:, None]
     assert (np.abs(h - want) <= np.abs(want) * (2.0 ** -8 + (v[:, None] ** 2 + 20) * 2.0 ** -24)).all()
+
+
+@pytest.mark.parametrize("M,D,F", [(1, 20001, 64), (1, 50257, 128), (600, 9001, 1)])
+def test_outputs_that_leave_in_different_ways(M, D, F):
+    """A single row leaves by a tensor map whatever its length, rows of an odd length beside it value by value: pairs of
+    blocks that take tiles of both."""
+    check(M, D, F)
+
+
+@pytest.mark.parametrize("M,D,F", [(64, 4096, 2048), (2000, 2048, 300), (300, 8192, 520)])
+def test_outputs_of_different_alignment(M, D, F):
+    """Through the C entry point: gradients on 16 bytes and off them in one call, the same bits as dense ones."""
+    from linear_recurrence_scan_gb300 import _native, token_policy as tp
+    from linear_recurrence_scan_gb300.api import _stream_handle
+    lib = _native.lib()
+    x, wg, wu, gh, _ = (t.to(DEV) if isinstance(t, torch.Tensor) else t for t in projection_inputs(M, D, F, 2))
+    want = L().gated_projection_backward(gh, x, wg, wu)
+    args = tp._PROJECTION_ARGS.pack(M, D, F, 0, x.data_ptr(), D, wg.data_ptr(), D, wu.data_ptr(), D)
+    ws = torch.empty(lib.rlscan_gated_projection_backward_workspace_bytes(args), dtype=torch.uint8, device=DEV)
+    for offsets in ((0, 1, 0), (0, 0, 3), (5, 0, 0), (0, 7, 1), (1, 2, 3)):
+        flat = [torch.full((t.numel() + 8,), 7.0, dtype=BF16, device=DEV) for t in want]
+        outs = [f[o:o + t.numel()] for f, o, t in zip(flat, offsets, want)]
+        assert lib.rlscan_gated_projection_backward(args, gh.data_ptr(), F, *(o.data_ptr() for o in outs), ws.data_ptr(),
+                                                    ws.numel(), _stream_handle(x.device)) == 0
+        for f, o, out, t in zip(flat, offsets, outs, want):
+            assert torch.equal(out.view(t.shape), t)
+            assert (f[:o] == 7).all() and (f[o + t.numel():] == 7).all()
+    L().workspace_status()
