@@ -70,6 +70,12 @@ struct Stats {
     float m, s;  // the largest logit and sum exp((z - m) / tau)
 };
 
+// A row's two normalizers, each by itself: the array is aligned as floats are.
+__device__ __forceinline__ void keep_normalizers(float *normalizers, int64_t row, float m, float s)
+{
+    if (normalizers != nullptr) normalizers[2 * row] = m, normalizers[2 * row + 1] = s;
+}
+
 __device__ __forceinline__ float warp_max(float v)
 {
 #pragma unroll

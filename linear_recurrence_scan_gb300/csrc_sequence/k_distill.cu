@@ -167,8 +167,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 64 ? 8 : CONSUMER
                 if (lane == 0) {
                     if (PART != Part::Loss && !masked) h.weight = o.grad_loss[row] * rtau;
                     if (PART == Part::Grad && !masked) {
-                        const float2 kept = reinterpret_cast<const float2 *>(o.normalizers)[row];
-                        h.m = kept.x, h.s = kept.y;
+                        h.m = o.normalizers[2 * row], h.s = o.normalizers[2 * row + 1];
                     }
                 }
                 if (last && !masked) teach(h, teacher(stage), in, row, ahead);
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 64 ? 8 : CONSUMER
                 if (masked) {
                     if (PART != Part::Grad && rank == 0 && t == 0) {
                         o.loss[row] = 0.f;
-                        if (o.normalizers != nullptr) reinterpret_cast<float2 *>(o.normalizers)[row] = make_float2(0.f, 1.f);
+                        keep_normalizers(o.normalizers, row, 0.f, 1.f);
                     }
                     if constexpr (PART != Part::Loss) clear();
                     release();
@@ -350,7 +349,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 64 ? 8 : CONSUMER
                     const float cross = h.taught ? cross_of(q_of, z_of, K, lane, st.m, rtau) : 0.f;
                     if (lane == 0) {
                         o.loss[row] = h.taught ? h.entropy - cross + logf(st.s) : 0.f;
-                        if (o.normalizers != nullptr) reinterpret_cast<float2 *>(o.normalizers)[row] = make_float2(st.m, st.s);
+                        keep_normalizers(o.normalizers, row, st.m, st.s);
                     }
                 }
                 release();

@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(32 * kRows, UNITS == 8 ? 3 : UNITS == 4 ? 4 : 
     if (a.mask != nullptr && load_byte(a.mask + row) == 0u) {
         if (PART != Part::Grad && lane == 0) {
             o.loss[row] = 0.f;
-            if (o.normalizers != nullptr) reinterpret_cast<float2 *>(o.normalizers)[row] = make_float2(0.f, 1.f);
+            keep_normalizers(o.normalizers, row, 0.f, 1.f);
         }
         if constexpr (PART != Part::Loss) clear();
         return;
@@ -76,8 +76,7 @@ __global__ void __launch_bounds__(32 * kRows, UNITS == 8 ? 3 : UNITS == 4 ? 4 : 
     }
     float m = fmaxf(-FLT_MAX, at_edge), s = 0.f;
     if constexpr (PART == Part::Grad) {
-        const float2 kept = reinterpret_cast<const float2 *>(o.normalizers)[row];
-        m = kept.x, s = kept.y;
+        m = o.normalizers[2 * row], s = o.normalizers[2 * row + 1];
     } else {
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) m = fmaxf(m, v[i].max());
@@ -141,7 +140,7 @@ __global__ void __launch_bounds__(32 * kRows, UNITS == 8 ? 3 : UNITS == 4 ? 4 : 
         const float cross = taught ? cross_of(of.q, of.z, K, lane, m, rtau) : 0.f;
         if (lane == 0) {
             o.loss[row] = taught ? of.entropy - cross + logf(s) : 0.f;
-            if (o.normalizers != nullptr) reinterpret_cast<float2 *>(o.normalizers)[row] = make_float2(m, s);
+            keep_normalizers(o.normalizers, row, m, s);
         }
     }
 }

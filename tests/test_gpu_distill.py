@@ -352,3 +352,34 @@ def test_far_logits_at_low_and_high_temperatures(level, tau, V, dtype):
     grad = torch.from_numpy(rng.standard_normal((1, 2)).astype(np.float32))
     loss, g = check(z, teacher, tokens, None, grad, tau)
     assert torch.isfinite(loss).all() and torch.isfinite(g).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [50, 2000, 5000, 50257, 140001])
+def test_normalizers_of_any_alignment(V, dtype):
+    """A [N,T,2] view one float behind a 16-byte boundary, read by the gradient's call and written through the C entry
+    points: the same bits as a dense tensor's."""
+    from linear_recurrence_scan_gb300 import _native, token_policy as tp
+    from linear_recurrence_scan_gb300.api import _stream_handle
+    N, T, K = 2, 3, 4
+    logits, teacher, tokens, mask, grad, _ = distill_inputs(N, T, V, K, dtype, V)
+    dev = [t.to(DEV) for t in (logits, teacher, tokens)]
+    m, w = mask.to(DEV), grad.to(DEV)
+    loss, norm = L().distill_loss(*dev, 2.0, m, return_normalizers=True)
+    g = L().distill_loss_backward(w, *dev, norm, 2.0, m)
+    flat = torch.full((2 * N * T + 2,), 7.0, device=DEV)
+    view = flat[1:-1].view(N, T, 2)
+    view.copy_(norm)
+    assert view.data_ptr() % 8 == 4
+    assert torch.equal(L().distill_loss_backward(w, *dev, view, 2.0, m), g)
+    lib, s = _native.lib(), _stream_handle(flat.device)
+    args = tp._DISTILL_ARGS.pack(N, T, V, K, tp._TYPES[dtype], 0, 8, dev[0].data_ptr(), T * V, V, dev[1].data_ptr(), dev[2].data_ptr(),
+                                 m.data_ptr(), 2.0)
+    both_loss, both_norm, both_grad = torch.empty_like(loss), torch.empty_like(norm), torch.empty_like(g)
+    assert lib.rlscan_distill_loss_and_grad(args, w.data_ptr(), both_loss.data_ptr(), both_norm.data_ptr(), both_grad.data_ptr(), s) == 0
+    for call, want in ((lambda: lib.rlscan_distill_loss(args, loss.data_ptr(), view.data_ptr(), s), norm),
+                       (lambda: lib.rlscan_distill_loss_and_grad(args, w.data_ptr(), both_loss.data_ptr(), view.data_ptr(),
+                                                                 both_grad.data_ptr(), s), both_norm)):
+        view.zero_()
+        assert call() == 0 and torch.equal(view, want)
+        assert flat[0] == 7 and flat[-1] == 7
