@@ -453,7 +453,8 @@ inline Access gated_access(std::initializer_list<const rlscan_array3 *> in, std:
                            std::initializer_list<const void *> floats, int64_t N, int64_t T_, int64_t D, bool tiles)
 {
     uint64_t bits = 0, wide = 0;
-    bool plain = tiles && T_ > 0 && T_ < 0x7fffffff - 1024 && N < 0x7fffffff;  // coordinates are 32-bit
+    // coordinates are 32-bit, those of a last block's end too (a negative one would read 0 and write nothing)
+    bool plain = tiles && T_ > 0 && T_ < 0x7fffffff - 1024 && N < 0x7fffffff && D < 0x7fffffff - kGatedWidth;
     for (const rlscan_array3 *a : in) {
         const int64_t row = N > 1 ? a->row_stride : 0, token = T_ > 1 ? a->token_stride : 0;
         bits |= reinterpret_cast<uintptr_t>(a->data) | static_cast<uint64_t>(row * sizeof(T)) | static_cast<uint64_t>(token * sizeof(T));

@@ -391,3 +391,36 @@ def test_page_locked_memory(which):
     # the same sums in another order: T products and sums of terms below 5 (|x| < 5), each rounded to 2^-24
     torch.testing.assert_close(at["y"].cpu(), want.cpu(), rtol=0, atol=5 * 3 * T * 2 ** -24)
     L().workspace_status()
+
+
+def test_channels_past_32_bits():
+    """More than 2^31 channels, whose blocks tensor maps cannot address: the first, the last and those around 2^31 against
+    the oracle, forward, gradients and a single token."""
+    D = 2 ** 31 + 136
+    gen = torch.Generator(DEV).manual_seed(1)
+
+    def normal():
+        return torch.empty(1, 1, D, dtype=BF16, device=DEV).normal_(generator=gen)
+
+    a = dict(x=normal(), gate=normal(), input_gate=normal(),
+             log_decay=torch.empty(D, dtype=F32, device=DEV).uniform_(-3, -0.01, generator=gen))
+    init = torch.empty(1, D, dtype=F32, device=DEV).normal_(generator=gen)
+    gy = normal()
+    y, final, marks = L().gated_scan(**a, initial_state=init, return_checkpoints=True)
+    g = L().gated_scan_backward(gy, **a, checkpoints=marks)
+    L().workspace_status()
+    step = init.clone()
+    ys = L().gated_scan_step(step, *(a[k][:, 0] for k in ("x", "gate", "input_gate")), a["log_decay"])
+    for at in (slice(0, 300), slice(2 ** 31 - 200, 2 ** 31 + 136)):
+        r64 = {k: np64(v[..., at]) for k, v in a.items()}
+        h0, gy64 = np64(init[..., at]), np64(gy[..., at])
+        ry, rf, _ = ref.gated_scan(**r64, initial_state=h0)
+        my, mf, _ = ref.gated_scan(**r64, initial_state=h0, bound=True)
+        close(y[..., at], ry, my, gated_factor(1), "y")
+        close(final[..., at], rf, mf, gated_factor(1), "final state")
+        close(step[..., at], rf, mf, gated_factor(1), "state of one token")
+        close(ys[..., at], ry[:, 0], my[:, 0], gated_factor(1), "y of one token")
+        want = ref.gated_scan_backward(gy64, **r64, initial_state=h0)
+        mag = ref.gated_scan_backward(gy64, **r64, initial_state=h0, bound=True)
+        for k in want:
+            close(getattr(g, k)[..., at], want[k], mag[k], gated_grad_factor(1, 1), "gradient of " + k)
