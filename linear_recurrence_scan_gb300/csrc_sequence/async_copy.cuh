@@ -11,9 +11,10 @@ namespace seq {
 
 // ---- waits -----------------------------------------------------------------------
 // A wait that runs out sets the block's flag.  The block then goes on to its end
-// through the same barriers of all its threads, but waits for nothing, asks for
-// no copy and arrives at no mbarrier, whose counts no longer fit; its results
-// are void, and it sets its file's device flag.
+// through the same barriers of all its threads, but a thread that has seen the
+// flag waits for nothing, asks for no copy and arrives at no mbarrier, whose
+// counts no longer fit; the block's results are void, and it sets its file's
+// device flag.
 constexpr uint64_t kWaitNs = 4'000'000'000ull;
 
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
@@ -29,15 +30,15 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// Waits for phase `parity`, at most kWaitNs; then, or once another thread of
+// Waits for phase `parity`, at most `limit`; then, or once another thread of
 // the block has given up, false.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *gave_up)
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *gave_up, uint64_t limit = kWaitNs)
 {
     if (try_wait(bar, parity)) return true;
     const uint64_t start = ptx::globaltimer_ns();
     while (!try_wait(bar, parity)) {
         if (*gave_up != 0) return false;
-        if (ptx::globaltimer_ns() - start > kWaitNs) {
+        if (ptx::globaltimer_ns() - start > limit) {
             *gave_up = 1;
             return false;
         }
@@ -47,12 +48,21 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
 
 __device__ __forceinline__ bool has_given_up(const int *gave_up) { return *const_cast<const volatile int *>(gave_up) != 0; }
 
-// At the end of a block, by all its threads: tells the host, and stays until
-// what is in flight (which takes microseconds) has ended.
+// The same by a warp, in front of what its lanes do together (votes, exchanges,
+// loads of tensor memory) or of copies: one answer for all of them, false too
+// where the phase has come but another thread has given up.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int *gave_up, uint64_t limit = kWaitNs)
+{
+    const bool fine = wait(bar, parity, gave_up, limit) && !has_given_up(gave_up);
+    return __all_sync(0xffffffffu, fine) != 0;
+}
+
+// At the end of a block, by all its threads: any that has seen the flag tells
+// the host, and stays until what is in flight (which takes microseconds) has ended.
 __device__ __forceinline__ void leave(const int *gave_up, unsigned int *device_flag)
 {
     if (!has_given_up(gave_up)) return;
-    if (threadIdx.x == 0) atomicExch(device_flag, 1u);
+    atomicExch(device_flag, 1u);
     const uint64_t start = ptx::globaltimer_ns();
     while (ptx::globaltimer_ns() - start < 1'000'000) {
     }

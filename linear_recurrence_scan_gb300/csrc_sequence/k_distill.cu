@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32, CONSUMERS == 64 ? 8 : CONSUMER
             for (int u = u0;;) {  // a masked row is one part without logits
                 const int n = masked ? 0 : end - u < stage_units ? end - u : stage_units;
                 const bool last = masked || u + n >= end;
-                if (!wait(ptx::smem_u32(&empty[stage]), parity ^ 1u, &gave_up)) return;
+                if (!wait_warp(ptx::smem_u32(&empty[stage]), parity ^ 1u, &gave_up)) return;
                 if (lane == 0) {
                     if (n > 0) {
                         ptx::mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(n) * 16);

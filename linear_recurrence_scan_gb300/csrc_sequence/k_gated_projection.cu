@@ -191,7 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int64_t tm, tn;
             place(of, item / of.parts, tm, tn);
             for (int64_t s = first_step(of, item), e = last_step(of, item); s < e; ++s) {
-                if (!wait(ptx::smem_u32(&empty[stage]), phase, &gave_up)) break;
+                if (!wait(ptx::smem_u32(&empty[stage]), phase, &gave_up) || has_given_up(&gave_up)) break;
                 const uint32_t bar = umma::of_rank(ptx::smem_u32(&full[stage]), 0);
                 const uint32_t a = smem + stage * kStageBytes, b = a + kTileBytes;
                 if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
@@ -285,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int which = of.weights && tm >= half ? 1 : 0;
             const int64_t row = (tm - which * half) * 256 + rank * 128 + part * 32 + lane;
             const int64_t rows = of.weights ? k.F : k.M;
-            if (!wait(ptx::smem_u32(&sums_full[buffer]), phase, &gave_up)) break;
+            if (!wait_warp(ptx::smem_u32(&sums_full[buffer]), phase, &gave_up)) break;
             umma::fence_after();
             const uint32_t at = tmem + buffer * 256 + (static_cast<uint32_t>(part * 32) << 16);
             const int64_t row0 = row - lane;  // of the warp
