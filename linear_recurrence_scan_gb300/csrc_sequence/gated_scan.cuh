@@ -264,18 +264,22 @@ struct Exchange {
 
 __device__ __forceinline__ f2 apply(f2 h, const float4 &m) { return fma2(pair(m.x, m.y), h, pair(m.z, m.w)); }
 
-// The same where the factor 0 of a map with a reset cuts off what is in front of
-// it whatever its value: 0 times infinity is no 0.  Values that are not finite
-// are rare, so the short form goes first and this one where it gave such.
+// A map with a reset cuts off what is in front of it whatever its value, which
+// 0 times infinity would not: its factor is -0, which stays -0 in products with
+// decays.  (A product of decays that is too small for 32 bits is +0, and cuts
+// nothing off: a NaN stays, an infinity becomes one.)  Values that are not
+// finite are rare, so the short form goes first and this one where it gave such.
+constexpr float kCut = -0.f;
+__device__ __forceinline__ bool is_cut(float factor) { return __float_as_uint(factor) == 0x80000000u; }
 __device__ __forceinline__ f2 apply_cut(f2 h, const float4 &m)
 {
     const float2 v = halves(apply(h, m));
-    return pair(m.x == 0.f ? m.z : v.x, m.y == 0.f ? m.w : v.y);
+    return pair(is_cut(m.x) ? m.z : v.x, is_cut(m.y) ? m.w : v.y);
 }
 __device__ __forceinline__ f2 multiply_cut(f2 f, const float4 &m)
 {
-    const float2 v = halves(mul2(f, pair(m.x, m.y)));
-    return pair(m.x == 0.f ? 0.f : v.x, m.y == 0.f ? 0.f : v.y);
+    const float2 v = halves(mul2(f, pair(m.x, m.y))), g = halves(f);
+    return pair(is_cut(m.x) || is_cut(g.x) ? kCut : v.x, is_cut(m.y) || is_cut(g.y) ? kCut : v.y);
 }
 // whether all lanes' values are finite
 __device__ __forceinline__ bool all_finite(f2 v)
@@ -323,13 +327,15 @@ __device__ __forceinline__ f2 in_front(C &c, E *ex, int64_t turn, int w, int lan
     const int p = static_cast<int>(turn & 1);
     f2 from = carry;  // in front of the block's tokens
     if constexpr (CLUSTER) {
-        f2 factor = both(1.f), rest = both(0.f);  // the block's map
+        f2 factor = both(1.f), rest = both(0.f), signs = 0;  // the block's map
 #pragma unroll
         for (int i = 0; i < kGatedWarps; ++i) {
             const float4 m = c.get(p, FORWARD ? i : kGatedWarps - 1 - i, lane);
             factor = mul2(factor, pair(m.x, m.y));
+            signs |= pair(m.x, m.y);
             rest = apply(rest, m);
         }
+        factor |= signs & both(kCut);  // -0 also where an even number of them are
         if (!all_finite(rest) || !all_finite(factor)) {
             factor = both(1.f), rest = both(0.f);
 #pragma unroll 1

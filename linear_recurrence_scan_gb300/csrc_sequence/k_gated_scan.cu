@@ -44,10 +44,10 @@ __device__ __forceinline__ f2 step_state(f2 h, f2 keep, f2 b, uint32_t cut, int 
 template <bool CUTTING, int TOK>
 __device__ __forceinline__ void fold(const f2 (&keep)[TOK], const f2 (&b)[TOK], uint32_t cut, f2 &A, f2 &B)
 {
-    A = CUTTING && (cut & 1u) != 0u ? both(0.f) : keep[0], B = b[0];
+    A = CUTTING && (cut & 1u) != 0u ? both(kCut) : keep[0], B = b[0];
 #pragma unroll
     for (int k = 1; k < TOK; ++k) {
-        A = CUTTING && (cut >> k & 1u) != 0u ? both(0.f) : mul2(A, keep[k]);
+        A = CUTTING && (cut >> k & 1u) != 0u ? both(kCut) : mul2(A, keep[k]);
         B = step_state<CUTTING>(B, keep[k], b[k], cut, k);
     }
 }

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
         } else {  // a reset is a select, not a product with 0
 #pragma unroll
             for (int i = 0; i < TOK; ++i) {
-                A = cuts(i) ? both(0.f) : mul2(A, keep[i]);
+                A = cuts(i) ? both(kCut) : mul2(A, keep[i]);
                 B = cuts(i) ? b[i] : fma2(keep[i], B, b[i]);
                 M = cuts(TOK - 1 - i) ? both(0.f) : mul2(keep[TOK - 1 - i], add2(gs[TOK - 1 - i], M));
             }
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, 2)
 #pragma unroll
             for (int i = 0; i < TOK; ++i) {
                 const f2 b = mul2(mul2(v[i].root, v[i].i), read_two<T>(in + 2 * BYTES + i * STEP));
-                A = cuts(i) ? both(0.f) : mul2(A, v[i].a);
+                A = cuts(i) ? both(kCut) : mul2(A, v[i].a);
                 B = cuts(i) ? b : fma2(v[i].a, B, b);
             }
 #pragma unroll

@@ -424,3 +424,41 @@ def test_channels_past_32_bits():
         mag = ref.gated_scan_backward(gy64, **r64, initial_state=h0, bound=True)
         for k in want:
             close(getattr(g, k)[..., at], want[k], mag[k], gated_grad_factor(1, 1), "gradient of " + k)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("N,T,D", [(2, 200, 64), (2, 200, 66), (2, 200, 65), (2, 200, 20480), (2, 700, 130), (1, 3000, 64)])
+def test_values_that_are_not_numbers(N, T, D, dtype):
+    """A NaN or an infinity stays in its row's states (and gradients' messages) up to the next reset and no further, also
+    where the product of a few decays is 0 in 32 bits (here exp(-40) each)."""
+    first, second, cut, last = T // 20, T // 5, 3 * T // 4, T - 5
+    for strong in (True, False):
+        x, gate, ig, gy = (torch.randn(N, T, D, device=DEV).clamp(-3, 3).to(dtype) for _ in range(4))
+        if strong:
+            gate[:] = 10
+        ld = torch.full((D,), -40.0 if strong else -0.1, device=DEV)
+        for bad in (float("nan"), float("inf")):
+            resets = torch.zeros(N, T, dtype=torch.uint8, device=DEV)
+            resets[:, first], resets[:, cut], resets[:, cut + 2], resets[:, cut - 30] = 1, 1, 1, 1
+            resets[:, second - 1] = 1
+            xb, gb, init = x.clone(), gy.clone(), torch.full((N, D), bad, device=DEV)
+            xb[:, second], gb[:, last] = bad, bad
+            y, final, marks = L().gated_scan(xb, gate, ig, ld, initial_state=init, resets=resets, return_checkpoints=True)
+            want = torch.zeros(T, dtype=torch.bool, device=DEV)
+            want[:first] = want[second:cut - 30] = True
+            assert torch.equal(~torch.isfinite(y), want[None, :, None].expand(N, T, D))
+            assert torch.isfinite(final).all()
+            g = L().gated_scan_backward(gb, xb, gate, ig, ld, marks, resets=resets)
+            back = torch.zeros(T, dtype=torch.bool, device=DEV)
+            back[cut + 2:last + 1] = True
+            assert torch.equal(~torch.isfinite(g.x), back[None, :, None].expand(N, T, D))
+            assert torch.isfinite(g.initial_state).all()
+            # without the resets all that follows (or, of the gradients, is in front)
+            y, final, marks = L().gated_scan(xb, gate, ig, ld, return_checkpoints=True)
+            want[:] = False
+            want[second:] = True
+            assert torch.equal(~torch.isfinite(y), want[None, :, None].expand(N, T, D))
+            assert not torch.isfinite(final).any()
+            g = L().gated_scan_backward(gb, xb, gate, ig, ld, marks)
+            assert not torch.isfinite(g.x[:, :last + 1]).any() and torch.isfinite(g.x[:, last + 1:]).all()
+            assert not torch.isfinite(g.initial_state).any()
