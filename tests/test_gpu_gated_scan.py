@@ -462,3 +462,10 @@ def test_values_that_are_not_numbers(N, T, D, dtype):
             g = L().gated_scan_backward(gb, xb, gate, ig, ld, marks)
             assert not torch.isfinite(g.x[:, :last + 1]).any() and torch.isfinite(g.x[:, last + 1:]).all()
             assert not torch.isfinite(g.initial_state).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("N,T,D", [(10, 150, 4096), (11, 70, 4098), (9, 90, 4161), (19, 260, 2048)])
+def test_more_chains_than_places(N, T, D, dtype):
+    """640 chains of blocks and about as many, where the GPU holds 456 or 304 at once: a second round of them."""
+    check(N, T, D, dtype, "both")
