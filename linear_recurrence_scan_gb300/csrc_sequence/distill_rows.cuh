@@ -183,12 +183,12 @@ struct Teacher {
     }
 };
 
-// sum of q (z - m) / tau, by a warp
+// sum of q (z - m) / tau, by a warp (q / tau first: a type's lowest value over a low temperature is past float32)
 __device__ __forceinline__ float cross_of(const float *q, const float *z, int K, int lane, float m, float rtau)
 {
     float cross = 0.f;
     for (int k = lane; k < K; k += 32)
-        if (!(q[k] == 0.f)) cross += q[k] * ((z[k] - m) * rtau);
+        if (!(q[k] == 0.f)) cross += q[k] * rtau * (z[k] - m);
     return warp_sum(cross);
 }
 

@@ -383,3 +383,18 @@ def test_normalizers_of_any_alignment(V, dtype):
         view.zero_()
         assert call() == 0 and torch.equal(view, want)
         assert flat[0] == 7 and flat[-1] == 7
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [30, 5000, 60000])
+@pytest.mark.parametrize("tau", [0.7, 0.01])
+def test_tokens_that_the_student_masks(tau, V, dtype):
+    """The teacher knows a token whose logit is the type's lowest value: the loss is large, but a float32 as long as the
+    token's probability over the temperature times that value is one."""
+    logits, teacher, tokens, _, grad, _ = distill_inputs(1, 3, V, 4, dtype, 3)
+    tokens[0] = torch.arange(4)
+    logits[0, :, 3] = torch.finfo(dtype).min
+    teacher = 0.1 * teacher * tau
+    teacher[0, :, 3] = teacher[0, :, :3].amax(-1) - 8 * tau   # exp(-8) / 0.01 is about 1/30
+    loss, g = check(logits, teacher, tokens, None, grad, tau)
+    assert (loss > 1e34).all() and torch.isfinite(loss).all() and torch.isfinite(g).all()
