@@ -840,7 +840,8 @@ rlscan_status rlscan_gated_projection_backward(const rlscan_gated_projection_arg
  * 2015, Sec. 2, with the teacher cut to its K tokens and renormalised; the
  * factor temperature^2 is left to the caller).
  *  - A teacher token outside 0..V-1 (-1, say) is an empty place; a token that
- *    comes twice counts twice; a teacher logit of -infinity counts q = 0.  A
+ *    comes twice counts twice; a teacher logit of -infinity, or so far below the
+ *    largest that q is below 2^-126, counts q = 0.  A
  *    row with nothing left has loss 0 and gradient 0.
  *  - mask [N,T] uint8, nullable: tokens where it is 0 have loss and gradient 0;
  *    their logits and teacher are not read.
@@ -861,7 +862,7 @@ typedef struct rlscan_distill_args {
     const void *teacher_logits;   /* [N,T,K] */
     const void *teacher_tokens;   /* [N,T,K] int32 or int64 */
     const uint8_t *mask;          /* [N,T], nullable */
-    double temperature;           /* above 0 */
+    double temperature;           /* 1e-6 to 1e6 */
 } rlscan_distill_args;
 
 /* loss [N,T] float32; normalizers [N,T,2] float32, nullable: the row's largest
