@@ -388,9 +388,15 @@ __host__ __device__ inline int64_t gated_marks(int64_t T) { return (T + RLSCAN_G
 // Blocks of a cluster that share a row: as many as make the fewest steps one
 // after the other, counting the rounds in which clusters of that size become
 // resident.  A row split over blocks costs each step an exchange, taken as
-// three quarters of a step (measured: 16 x 1024 x 2048, 512 chains, alone 66
-// us, in fours 76; 2 x 16384 x 2048, 64 chains, alone 349, in fours 169, in
-// sixes 154, in eights, which no longer fit at once, 185).
+// three quarters of a step.  Measured, bfloat16, forward / gradients, us, alone and
+// in twos, threes, fours, sixes, eights (gradients at most fours), the rule's in
+// brackets:
+//   2 x 16384 x 2048, 64 chains    353/874  348/429  216/396  165/[301]  [150]  180
+//   2 x 4096 x 4096, 128 chains    148/230  82/[152]  [78]/175  82/157  81  85
+//   8 x 2048 x 2048, 256 chains    [67]/[125]  80/153  78/162  72/146  83  83
+//   16 x 1024 x 2048, 512 chains   [64]/[126]  68/142  81/167  73/149  85  89
+// and of 14 such calls in both types, with 16 to 512 chains, by tiles and by value,
+// the rule's size was the fastest or, within 3 us, next to it.
 template <class T, int KIND, class K>
 inline int gated_cluster(K kernel, int64_t chains, int64_t tokens, int tile, size_t smem, int most = kGatedCluster)
 {

@@ -15,7 +15,11 @@ namespace {
 __device__ unsigned int g_timed_out;  // a wait ran out on this device
 
 // Forward: z and u, then h.  Gates: z and u, then gz and gu.  Grads: dx, the sum
-// over both gates' columns, and dWg and dWu.
+// over both gates' columns, and dWg and dWu.  gz and gu are rounded to bfloat16,
+// the type of the last products' operands: the gradients are 0.0023 of their size
+// off, which with 32 bits there would be 0.0017, the outputs' own rounding.  A
+// second bfloat16 part of each would keep those bits, and make the last products,
+// two thirds of all operations, twice as many.
 enum class Job { Forward, Gates, Grads };
 
 struct Maps {
@@ -123,9 +127,10 @@ __device__ __forceinline__ void load_row(Words<bf16, 8> (&w)[4], const bf16 *p, 
 // finds both of a value in its own tensor memory.  Warps: 0 copies, 1
 // multiplies (the first block's), 2 holds the tensor memory, 4 to 11 take the
 // sums out while the next tile's are made in the other half of the 512 columns.
-// Bound by the products where K is long (forward 16384 x 4096 x 12288 1838 us,
-// 1.79 PFLOP/s of the 1.89 that the library's plain product reaches), by the
-// epilogue and the outputs' bytes where it is short (3636 x 64 x 4016 26 us).
+// Bound by the products where K is long (forward 16384 x 4096 x 12288 back to
+// back 1840 us, 1.79 PFLOP/s of the 1.89 that the library's plain product reaches
+// in a burst; a pass of its own, inputs cold, 1960 to 2060), by the epilogue and
+// the outputs' bytes where it is short (3636 x 64 x 4016, gelu, 26 us).
 // Four warps for the sums held the products up: gradients of 16384 x 512 x 512
 // 130 us, with eight 107.
 template <Job JOB>

@@ -397,9 +397,9 @@ def distill_loss(logits, teacher_logits, teacher_tokens, temperature=1.0, mask=N
     logits [N,T,vocabulary] float32 or bfloat16 (any strides over rows and
     tokens); teacher_logits [N,T,K] float32 or bfloat16 and teacher_tokens
     [N,T,K] int32 or int64, K up to 256 (a token outside the vocabulary, -1
-    say, is an empty place; one that comes twice counts twice); ``mask`` [N,T]
-    (uint8 or bool) is 0 where a token has no loss, and its logits are not
-    read.  Returns the loss [N,T] float32, 0 where nothing is left to learn
+    say, is an empty place; one that comes twice counts twice); ``temperature``
+    1e-6 to 1e6; ``mask`` [N,T] (uint8 or bool) is 0 where a token has no loss,
+    and its logits are not read.  Returns the loss [N,T] float32, 0 where nothing is left to learn
     from; with ``return_normalizers`` also what distill_loss_backward needs,
     [N,T,2] float32.  Differentiable in the logits; the teacher has no
     gradient (one that requires it is refused).  The factor temperature^2
