@@ -644,14 +644,11 @@ rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_arg
     const bool input_first = p.weights.items() == 0 || (p.input.items() > 0 && p.input.part_steps >= p.weights.part_steps);
     w.product[0] = input_first ? p.input : p.weights;
     w.product[1] = input_first ? p.weights : p.input;
-    // Sharing a launch saves the first product's last round of items and an end,
-    // which is much of little work; of very much it is nothing, and the pairs, no
-    // longer at the same steps of K, find less of their operands in L2.  Measured,
-    // all gradients, one launch and two: 375 x 2912 x 368 (15 steps a pair) 35 and
-    // 44 us, 5000 x 2560 x 6912 (1207) 703 and 753, 16384 x 2560 x 6912 (3762) 2235
-    // and 2308, 16384 x 4096 x 8192 (7114) 4176 and 4257, 16384 x 4096 x 12288
-    // (10617) 6483 and 6490, 30000 x 4096 x 12288 (19378) 11924 and 11749.
-    if (p.load > 16384) {
+    // Much work gains little by sharing a launch, and loses by it: the pairs, no
+    // longer at the same steps of K, find less of their operands in L2 (16384 x
+    // 4096 x 12288, 10600 steps a pair: one launch 6400 us, two 6200; 5000 x 2560 x
+    // 6912, 1200 steps: 670 and 683; 375 x 2912 x 368, 15 steps: 40 and 56).
+    if (p.load > 4096) {
         const Product second = w.product[1];
         w.product[1] = {};
         st = launch_job<Job::Grads>(mg, w, s);
