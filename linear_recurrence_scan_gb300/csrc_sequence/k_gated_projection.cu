@@ -128,8 +128,8 @@ __device__ __forceinline__ void load_row(Words<bf16, 8> (&w)[4], const bf16 *p, 
 // multiplies (the first block's), 2 holds the tensor memory, 4 to 11 take the
 // sums out while the next tile's are made in the other half of the 512 columns.
 // Bound by the products where K is long (forward 16384 x 4096 x 12288 back to
-// back 1840 us, 1.79 PFLOP/s of the 1.89 that the library's plain product reaches
-// in a burst; a pass of its own, inputs cold, 1960 to 2060), by the epilogue and
+// back 1810 to 1900 us, 1.74 to 1.82 PFLOP/s of the 1.89 that the library's plain
+// product reaches in a burst; a pass, inputs cold, 1940 to 2060), by the epilogue and
 // the outputs' bytes where it is short (3636 x 64 x 4016, gelu, 26 us).
 // Four warps for the sums held the products up: gradients of 16384 x 512 x 512
 // 130 us, with eight 107.
@@ -644,10 +644,12 @@ rlscan_status launch_gated_projection_backward(const rlscan_gated_projection_arg
     const bool input_first = p.weights.items() == 0 || (p.input.items() > 0 && p.input.part_steps >= p.weights.part_steps);
     w.product[0] = input_first ? p.input : p.weights;
     w.product[1] = input_first ? p.weights : p.input;
-    // Much work gains little by sharing a launch, and loses by it: the pairs, no
-    // longer at the same steps of K, find less of their operands in L2 (16384 x
-    // 4096 x 12288, 10600 steps a pair: one launch 6400 us, two 6200; 5000 x 2560 x
-    // 6912, 1200 steps: 670 and 683; 375 x 2912 x 368, 15 steps: 40 and 56).
+    // Much work gains nothing by sharing a launch, and the most loses by it: the
+    // pairs, no longer at the same steps of K, find less of their operands in L2.
+    // Measured, all gradients, one launch and two: 375 x 2912 x 368 (15 steps a
+    // pair) 36 and 45 us, 5000 x 2560 x 6912 (1207) 665 and 708, 8192 x 4096 x 8192
+    // (3610) 2059 and 2065, 16384 x 4096 x 6144 (5362) 3121 and 3130, 16384 x 4096
+    // x 12288 (10617) 6420 and 6370, 30000 x 4096 x 12288 (19378) 11829 and 11627.
     if (p.load > 4096) {
         const Product second = w.product[1];
         w.product[1] = {};

@@ -310,3 +310,21 @@ def test_outputs_of_different_alignment(M, D, F):
             assert torch.equal(out.view(t.shape), t)
             assert (f[:o] == 7).all() and (f[o + t.numel():] == 7).all()
     L().workspace_status()
+
+
+def test_more_work_than_one_launch_takes():
+    """So many steps a pair of blocks that both products of the gradients have a launch of their own: the same bits as
+    each gradient alone, and some rows against float64."""
+    M, D, F = 30000, 4096, 12288
+    gen = torch.Generator(DEV).manual_seed(4)
+    x, wg, wu, gh = (torch.randn(s, generator=gen, device=DEV, dtype=BF16) * f
+                     for s, f in (((M, D), 1.0), ((F, D), D ** -0.5), ((F, D), D ** -0.5), ((M, F), 1.0)))
+    g = L().gated_projection_backward(gh, x, wg, wu)
+    for i, k in enumerate(("x", "gate_weight", "up_weight")):
+        leaves = [t.clone().requires_grad_(j == i) for j, t in enumerate((x, wg, wu))]
+        (one,) = torch.autograd.grad(L().gated_projection(*leaves), [leaves[i]], gh)
+        assert torch.equal(one, getattr(g, k)), k
+    rows = [0, 255, 256, 29999]
+    want = projection_oracle(x[rows].cpu(), wg.cpu(), wu.cpu(), gh[rows].cpu(), "silu")
+    close(g.x[rows], *want["x"], 1.0, "gradient of x")
+    L().workspace_status()
