@@ -11,10 +11,11 @@ namespace seq {
 
 // ---- waits -----------------------------------------------------------------------
 // A wait that runs out sets the block's flag.  The block then goes on to its end
-// through the same barriers of all its threads, but a thread that has seen the
-// flag waits for nothing, asks for no copy and arrives at no mbarrier, whose
-// counts no longer fit; the block's results are void, and it sets its file's
-// device flag.
+// through the same barriers of all its threads, but a thread whose wait was in
+// vain asks for no copy and arrives at no mbarrier, whose counts no longer fit.
+// One whose waits pass goes on meanwhile, on phases that others completed before
+// they gave up, until one does not.  The block's results are void, and it sets its
+// file's device flag.
 constexpr uint64_t kWaitNs = 4'000'000'000ull;
 
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
@@ -49,12 +50,10 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
 __device__ __forceinline__ bool has_given_up(const int *gave_up) { return *const_cast<const volatile int *>(gave_up) != 0; }
 
 // The same by a warp, in front of what its lanes do together (votes, exchanges,
-// loads of tensor memory) or of copies: one answer for all of them, false too
-// where the phase has come but another thread has given up.
+// loads of tensor memory): one answer for all of them.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int *gave_up, uint64_t limit = kWaitNs)
 {
-    const bool fine = wait(bar, parity, gave_up, limit) && !has_given_up(gave_up);
-    return __all_sync(0xffffffffu, fine) != 0;
+    return __all_sync(0xffffffffu, wait(bar, parity, gave_up, limit)) != 0;
 }
 
 // At the end of a block, by all its threads: any that has seen the flag tells

@@ -196,9 +196,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int64_t tm, tn;
             place(of, item / of.parts, tm, tn);
             for (int64_t s = first_step(of, item), e = last_step(of, item); s < e; ++s) {
-                // (the flag is looked at an item at a time: at each stage, behind a wait
-                // that has passed, the look made the gradients of 5000 x 2560 x 6912 701
-                // us long, so 660; a stage asked for in vain lands in blocks that stay)
+                // (a look at the flag here, behind a wait that has passed, made the
+                // gradients of 5000 x 2560 x 6912 701 us long, so 660)
                 if (!wait(ptx::smem_u32(&empty[stage]), phase, &gave_up)) break;
                 const uint32_t bar = umma::of_rank(ptx::smem_u32(&full[stage]), 0);
                 const uint32_t a = smem + stage * kStageBytes, b = a + kTileBytes;

@@ -24,7 +24,7 @@ def lib(tmp_path_factory):
 
 
 # kind of wait_limit.cu -> the threads' answers, the warps', the status (None: not asked)
-CASES = {0: (0, 0, TIMEOUT), 1: (1, 1, OK), 2: (1, 0, TIMEOUT), 3: (0, 0, TIMEOUT)}
+CASES = {0: (0, 0, TIMEOUT), 1: (1, 1, OK), 2: (1, 1, TIMEOUT), 3: (0, 0, TIMEOUT), 4: (None, 0, TIMEOUT)}
 
 
 @pytest.mark.parametrize("kind", CASES)
@@ -38,6 +38,8 @@ def test_waits(lib, kind):
     each, together, want = CASES[kind]
     assert (status, again.value) == (want, OK)
     asked = slice(32, 64) if kind == 3 else slice(0, 64)
+    if each is None:
+        each = (torch.arange(64, device="cuda") + 1) % 2   # the phase has come for even lanes
     assert (threads[asked] == each).all() and (warps[asked] == together).all()
     if kind == 3:
         assert (threads[:32] == 7).all() and (warps[:32] == 7).all()

@@ -7,8 +7,9 @@ namespace ptx = rlscan::ptx;
 
 __device__ unsigned int g_timed_out;
 
-// 0: the phase never comes; 1: it has come; 2: it has come, but a thread has
-// given up; 3: as 0, and the first warp is gone before the second gives up.
+// 0: the phase never comes; 1: it has come; 2: it has come, and a thread has given
+// up elsewhere; 3: as 0, and the first warp is gone before the second gives up;
+// 4: it has come for every other lane alone.
 __global__ void __launch_bounds__(64) wait_kernel(int kind, int *threads, int *warps)
 {
     constexpr uint64_t kLimitNs = 2'000'000;
@@ -18,12 +19,13 @@ __global__ void __launch_bounds__(64) wait_kernel(int kind, int *threads, int *w
         gave_up = kind == 2;
         ptx::mbar_init(&bar, 1);
         ptx::fence_mbar_init();
-        if (kind == 1 || kind == 2) ptx::mbar_arrive(&bar);
+        if (kind == 1 || kind == 2 || kind == 4) ptx::mbar_arrive(&bar);
     }
     __syncthreads();
     if (kind != 3 || threadIdx.x >= 32) {
-        threads[threadIdx.x] = wait(ptx::smem_u32(&bar), 0, &gave_up, kLimitNs);
-        warps[threadIdx.x] = wait_warp(ptx::smem_u32(&bar), 0, &gave_up, kLimitNs);
+        const uint32_t parity = kind == 4 ? threadIdx.x & 1u : 0u;
+        threads[threadIdx.x] = wait(ptx::smem_u32(&bar), parity, &gave_up, kLimitNs);
+        warps[threadIdx.x] = wait_warp(ptx::smem_u32(&bar), parity, &gave_up, kLimitNs);
     }
     leave(&gave_up, &g_timed_out);
 }
