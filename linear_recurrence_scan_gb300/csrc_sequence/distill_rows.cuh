@@ -183,13 +183,17 @@ struct Teacher {
     }
 };
 
-// sum of q (z - m) / tau, by a warp (q / tau first: a type's lowest value over a low temperature is past float32)
+// sum of q (z - m) / tau, by a warp.  The temperature comes last: a type's lowest
+// value over a low one is past float32 where its part of the sum is not, and q
+// over a high one may be 0, which would hide a z of -infinity.  Halves are summed,
+// which stay finite where z - m, or q that sum to a little over 1, would not.
 __device__ __forceinline__ float cross_of(const float *q, const float *z, int K, int lane, float m, float rtau)
 {
+    const float half = 0.5f * m;
     float cross = 0.f;
     for (int k = lane; k < K; k += 32)
-        if (!(q[k] == 0.f)) cross += q[k] * rtau * (z[k] - m);
-    return warp_sum(cross);
+        if (!(q[k] == 0.f)) cross += q[k] * fmaf(0.5f, z[k], -half);
+    return warp_sum(cross) * (2.f * rtau);
 }
 
 // The probability of the k-th place's token: one that comes twice counts twice,

@@ -398,3 +398,30 @@ def test_tokens_that_the_student_masks(tau, V, dtype):
     teacher[0, :, 3] = teacher[0, :, :3].amax(-1) - 8 * tau   # exp(-8) / 0.01 is about 1/30
     loss, g = check(logits, teacher, tokens, None, grad, tau)
     assert (loss > 1e34).all() and torch.isfinite(loss).all() and torch.isfinite(g).all()
+
+
+@pytest.mark.parametrize("V", [300, 5000, 60000])
+def test_the_smallest_probability_of_a_token_ruled_out(V):
+    """The student rules out a token to which a hot teacher gives exp(-87.2) / 200, next to float32's end: an infinite
+    loss, no NaN."""
+    K, tau = 200, 1e6
+    z = torch.zeros(1, 2, V, device=DEV)
+    z[..., K - 1] = -float("inf")
+    teacher = torch.zeros(1, 2, K, device=DEV)
+    teacher[..., K - 1] = -87.2 * tau
+    tokens = torch.arange(K, device=DEV).expand(1, 2, K)
+    loss, g = L().distill_loss_and_grad(torch.ones(1, 2, device=DEV), z, teacher, tokens, tau)
+    assert (loss == float("inf")).all() and torch.isfinite(g).all()
+    assert torch.equal(L().distill_loss(z, teacher, tokens, tau), loss)
+
+
+@pytest.mark.parametrize("V", [30, 5000, 60000])
+def test_tokens_at_both_ends_at_a_high_temperature(V):
+    """Every teacher's token has the type's lowest value, the others 0 or 3e38: a difference past float32, but not over
+    the temperature of 10."""
+    logits, teacher, tokens, _, grad, _ = distill_inputs(1, 3, V, 4, F32, 4)
+    tokens[0] = torch.arange(4)
+    logits[0, :2], logits[0, 2] = 0, 3e38
+    logits[..., :4] = torch.finfo(F32).min
+    loss, g = check(logits, teacher, tokens, None, grad, 10.0)
+    assert (loss > 3e37).all() and torch.isfinite(loss).all() and torch.isfinite(g).all()
